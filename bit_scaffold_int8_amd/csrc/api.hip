@@ -56,6 +56,25 @@ hipError_t launch_gemm_prefill(const int8_t* x_q, const float* s_x, int64_t M, i
                                const int8_t* w_b, const float* s_b, const int32_t* t, int32_t* t_out, int rank,
                                float* y, int32_t* acc_dbg, int64_t batch, int force_cfg, int force_tail,
                                hipStream_t stream);
+hipError_t launch_int8_gemm(const int8_t* x_q, int64_t ldx, const float* s_x, int64_t M, int64_t N, int64_t K,
+                            const int8_t* w, int64_t ldw, const float* s_w, void* y, int64_t ldy, bool bf16,
+                            hipStream_t stream);
+size_t cross_entropy_workspace_bytes(int64_t M, int64_t V);
+hipError_t launch_cross_entropy(const int8_t* x_q, const float* s_x, int64_t M, int64_t V, int64_t K, const int8_t* e,
+                                const float* s_e, const int32_t* targets, float* loss, float* lse, void* workspace,
+                                hipStream_t stream);
+size_t cross_entropy_backward_workspace_bytes(int64_t M, int64_t V, int64_t K, bool bf16, bool want_dx, bool want_de);
+hipError_t launch_cross_entropy_backward(const int8_t* x_q, const float* s_x, int64_t M, int64_t V, int64_t K,
+                                         const int8_t* e, const float* s_e, const int32_t* targets, const float* lse,
+                                         const float* dloss, void* dx, void* de, bool bf16, bool accumulate,
+                                         void* workspace, hipStream_t stream);
+hipError_t launch_embedding_lookup_scaled(const int32_t* tokens, int64_t T, const int8_t* e, const float* s_e,
+                                          int64_t V, int64_t K, float scale, void* out, int64_t ldo, bool bf16,
+                                          hipStream_t stream);
+size_t embedding_backward_workspace_bytes(int64_t T, int64_t V, int64_t K);
+hipError_t launch_embedding_backward(const int32_t* tokens, int64_t T, const void* dout, int64_t ldd, bool dout_bf16,
+                                     int64_t V, int64_t K, float scale, void* de, bool de_bf16, bool accumulate,
+                                     void* workspace, hipStream_t stream);
 }  // namespace dfssm
 
 #include "decode_args.h"
@@ -278,6 +297,28 @@ dfssm_status decode_layers_impl(const dfssm_decode_layer_weights* w, int64_t n_l
     return e == hipSuccess ? DFSSM_OK : DFSSM_ERR_HIP;
 }
 
+// ---- the operators over an int8 matrix with fp32 or bf16 results
+constexpr int64_t kMaxStride = (int64_t)1 << 22;     // row strides of the int8 operands: a tile's 256 rows stay below 2^30
+constexpr int64_t kMaxTiles = ((int64_t)1 << 31) / 2;  // workgroups of one launch
+constexpr int64_t kMaxLossTokens = (int64_t)1 << 18;   // tokens of one backward call
+constexpr int64_t kMaxGradTokens = (int64_t)1 << 24;   // tokens of one embedding gradient
+
+bool type_ok(int32_t t) { return t == DFSSM_F32 || t == DFSSM_BF16; }
+bool aligned_type(const void* p, int32_t t) { return ((uintptr_t)p & (t == DFSSM_BF16 ? 1u : 3u)) == 0; }
+
+// Sizes of the cross entropy over [V][K] for M tokens.
+dfssm_status loss_sizes(int64_t M, int64_t V, int64_t K) {
+    if (M <= 0 || V <= 0 || K <= 0 || M >= kMaxRows || V >= kMaxRows || K % 16 != 0) return DFSSM_ERR_INVALID_ARG;
+    if (K > kMaxK || ((V + 127) / 128) * ((M + 31) / 32) > kMaxTiles) return DFSSM_ERR_UNSUPPORTED;
+    return DFSSM_OK;
+}
+
+dfssm_status embedding_sizes(int64_t T, int64_t V, int64_t K) {
+    if (T <= 0 || V <= 0 || K <= 0 || T >= kMaxRows || V >= kMaxRows) return DFSSM_ERR_INVALID_ARG;
+    if (K > kMaxK) return DFSSM_ERR_UNSUPPORTED;
+    return DFSSM_OK;
+}
+
 dfssm_status density_checks(int64_t rows, int64_t d_state) {
     if (rows <= 0 || d_state <= 0) return DFSSM_ERR_INVALID_ARG;
     if (!dfssm::density_field_supported(d_state)) return DFSSM_ERR_UNSUPPORTED;
@@ -299,7 +340,7 @@ const char* dfssm_status_string(dfssm_status status) {
     return "DFSSM_ERR_UNKNOWN";
 }
 
-int32_t dfssm_version(void) { return 400; }
+int32_t dfssm_version(void) { return 401; }
 
 dfssm_status dfssm_prefill_plan(int64_t M, int64_t N, int64_t K, int64_t batch, int32_t* main_cfg,
                                 int32_t* tail_cfg, int64_t* n_split) {
@@ -511,6 +552,104 @@ dfssm_status dfssm_mamba2_decode_step(const float* zxbcdt, int64_t S, int64_t nh
         return DFSSM_ERR_INVALID_ARG;
     return dfssm::launch_mamba2_step(zxbcdt, S, (int)nheads, conv_state_in, conv_state_out, ssm_state, conv_w, conv_b,
                                      dt_bias, A_log, D, norm_w, eps, out, stream) == hipSuccess
+               ? DFSSM_OK
+               : DFSSM_ERR_HIP;
+}
+
+dfssm_status dfssm_int8_gemm(const int8_t* x_q, int64_t ldx, const float* s_x, int64_t M, int64_t N, int64_t K,
+                             const int8_t* w, int64_t ldw, const float* s_w, void* y, int64_t ldy, int32_t y_type,
+                             hipStream_t stream) {
+    if (!x_q || !s_x || !w || !s_w || !y) return DFSSM_ERR_INVALID_ARG;
+    if (M <= 0 || N <= 0 || K <= 0 || M >= kMaxRows || N >= kMaxRows) return DFSSM_ERR_INVALID_ARG;
+    if (ldx < K || ldw < K || ldy < N || !type_ok(y_type)) return DFSSM_ERR_INVALID_ARG;
+    if (!aligned4(s_x) || !aligned4(s_w) || !aligned_type(y, y_type)) return DFSSM_ERR_INVALID_ARG;
+    if (K > kMaxK || ldx > kMaxStride || ldw > kMaxStride || ldy >= ((int64_t)1 << 40) ||
+        ((N + 31) / 32) * ((M + 31) / 32) > kMaxTiles)
+        return DFSSM_ERR_UNSUPPORTED;
+    return dfssm::launch_int8_gemm(x_q, ldx, s_x, M, N, K, w, ldw, s_w, y, ldy, y_type == DFSSM_BF16, stream) ==
+                   hipSuccess
+               ? DFSSM_OK
+               : DFSSM_ERR_HIP;
+}
+
+size_t dfssm_cross_entropy_workspace_bytes(int64_t M, int64_t V, int64_t K) {
+    return loss_sizes(M, V, K) == DFSSM_OK ? dfssm::cross_entropy_workspace_bytes(M, V) : 0;
+}
+
+dfssm_status dfssm_cross_entropy(const int8_t* x_q, const float* s_x, int64_t M, int64_t V, int64_t K,
+                                 const int8_t* e, const float* s_e, const int32_t* targets, float* loss, float* lse,
+                                 void* workspace, size_t workspace_bytes, hipStream_t stream) {
+    if (!x_q || !s_x || !e || !s_e || !targets || !loss || !lse || !workspace) return DFSSM_ERR_INVALID_ARG;
+    if (dfssm_status st = loss_sizes(M, V, K)) return st;
+    if (!aligned16(x_q) || !aligned16(e) || !aligned16(workspace) || !aligned4(s_x) || !aligned4(s_e) ||
+        !aligned4(targets) || !aligned4(loss) || !aligned4(lse))
+        return DFSSM_ERR_INVALID_ARG;
+    if (workspace_bytes < dfssm::cross_entropy_workspace_bytes(M, V)) return DFSSM_ERR_INVALID_ARG;
+    return dfssm::launch_cross_entropy(x_q, s_x, M, V, K, e, s_e, targets, loss, lse, workspace, stream) == hipSuccess
+               ? DFSSM_OK
+               : DFSSM_ERR_HIP;
+}
+
+size_t dfssm_cross_entropy_backward_workspace_bytes(int64_t M, int64_t V, int64_t K, int32_t grad_type,
+                                                    int32_t want_dx, int32_t want_de) {
+    if (loss_sizes(M, V, K) != DFSSM_OK || M > kMaxLossTokens || !type_ok(grad_type) || (!want_dx && !want_de)) return 0;
+    return dfssm::cross_entropy_backward_workspace_bytes(M, V, K, grad_type == DFSSM_BF16, want_dx != 0, want_de != 0);
+}
+
+dfssm_status dfssm_cross_entropy_backward(const int8_t* x_q, const float* s_x, int64_t M, int64_t V, int64_t K,
+                                          const int8_t* e, const float* s_e, const int32_t* targets, const float* lse,
+                                          const float* dloss, void* dx, void* de, int32_t grad_type,
+                                          int32_t accumulate_de, void* workspace, size_t workspace_bytes,
+                                          hipStream_t stream) {
+    if (!x_q || !s_x || !e || !s_e || !targets || !lse || !dloss || (!dx && !de) || !workspace)
+        return DFSSM_ERR_INVALID_ARG;
+    if (!type_ok(grad_type) || (accumulate_de != 0 && accumulate_de != 1)) return DFSSM_ERR_INVALID_ARG;
+    if (dfssm_status st = loss_sizes(M, V, K)) return st;
+    if (!aligned16(x_q) || !aligned16(e) || !aligned16(workspace) || !aligned16(dx) || !aligned16(de) ||
+        !aligned4(s_x) || !aligned4(s_e) || !aligned4(targets) || !aligned4(lse) || !aligned4(dloss))
+        return DFSSM_ERR_INVALID_ARG;
+    if (M > kMaxLossTokens) return DFSSM_ERR_UNSUPPORTED;
+    const bool bf16 = grad_type == DFSSM_BF16;
+    if (workspace_bytes < dfssm::cross_entropy_backward_workspace_bytes(M, V, K, bf16, dx != nullptr, de != nullptr))
+        return DFSSM_ERR_INVALID_ARG;
+    return dfssm::launch_cross_entropy_backward(x_q, s_x, M, V, K, e, s_e, targets, lse, dloss, dx, de, bf16,
+                                                accumulate_de != 0, workspace, stream) == hipSuccess
+               ? DFSSM_OK
+               : DFSSM_ERR_HIP;
+}
+
+dfssm_status dfssm_embedding_lookup_scaled(const int32_t* tokens, int64_t T, const int8_t* e, const float* s_e,
+                                           int64_t V, int64_t K, float scale, void* out, int64_t ldo,
+                                           int32_t out_type, hipStream_t stream) {
+    if (!tokens || !e || !s_e || !out || !type_ok(out_type)) return DFSSM_ERR_INVALID_ARG;
+    if (dfssm_status st = embedding_sizes(T, V, K)) return st;
+    if (!aligned4(tokens) || !aligned4(s_e) || !aligned_type(out, out_type) || ldo < K) return DFSSM_ERR_INVALID_ARG;
+    if (ldo >= ((int64_t)1 << 31)) return DFSSM_ERR_UNSUPPORTED;
+    return dfssm::launch_embedding_lookup_scaled(tokens, T, e, s_e, V, K, scale, out, ldo, out_type == DFSSM_BF16,
+                                                 stream) == hipSuccess
+               ? DFSSM_OK
+               : DFSSM_ERR_HIP;
+}
+
+size_t dfssm_embedding_backward_workspace_bytes(int64_t T, int64_t V, int64_t K) {
+    if (embedding_sizes(T, V, K) != DFSSM_OK || T > kMaxGradTokens) return 0;
+    return dfssm::embedding_backward_workspace_bytes(T, V, K);
+}
+
+dfssm_status dfssm_embedding_backward(const int32_t* tokens, int64_t T, const void* dout, int64_t ldd,
+                                      int32_t dout_type, int64_t V, int64_t K, float scale, void* de,
+                                      int32_t de_type, int32_t accumulate, void* workspace, size_t workspace_bytes,
+                                      hipStream_t stream) {
+    if (!tokens || !dout || !de || !workspace || !type_ok(dout_type) || !type_ok(de_type)) return DFSSM_ERR_INVALID_ARG;
+    if (accumulate != 0 && accumulate != 1) return DFSSM_ERR_INVALID_ARG;
+    if (dfssm_status st = embedding_sizes(T, V, K)) return st;
+    if (!aligned4(tokens) || !aligned_type(dout, dout_type) || !aligned_type(de, de_type) || !aligned16(workspace) ||
+        ldd < K)
+        return DFSSM_ERR_INVALID_ARG;
+    if (T > kMaxGradTokens || ldd >= ((int64_t)1 << 31)) return DFSSM_ERR_UNSUPPORTED;
+    if (workspace_bytes < dfssm::embedding_backward_workspace_bytes(T, V, K)) return DFSSM_ERR_INVALID_ARG;
+    return dfssm::launch_embedding_backward(tokens, T, dout, ldd, dout_type == DFSSM_BF16, V, K, scale, de,
+                                            de_type == DFSSM_BF16, accumulate != 0, workspace, stream) == hipSuccess
                ? DFSSM_OK
                : DFSSM_ERR_HIP;
 }

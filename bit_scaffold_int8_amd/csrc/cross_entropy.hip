@@ -1,0 +1,386 @@
+// cross_entropy.hip -- softmax cross entropy over the int8 vocabulary matrix, and its gradients
+// (gfx950), without the M x V logits in memory:
+//
+//   z[m][v] = s_x[m] (s_e[v] sum_k e[v][k] x_q[m][k])      lse[m] = log sum_v exp z[m][v]
+//   loss[m] = lse[m] - z[m][target]                          (0 where the target is no row of e)
+//   d[m][v] = dloss[m] (exp(z[m][v] - lse[m]) - [v = target])
+//   dx[m]   = sum_v d[m][v] s_e[v] e[v]        de[v] = sum_m d[m][v] s_x[m] x_q[m]
+//
+// Forward: each workgroup forms a tile of logits (tile_i8.h: exact int32 accumulators, a token per
+// lane, the vocabulary along its registers), takes each token's maximum and sum of exponentials over
+// the tile's rows, and writes that pair; a second kernel joins a token's pairs in tile order and
+// forms the target's logit by itself.  Exponents are base 2: z log2 e.
+//
+// Backward, one piece of the vocabulary at a time: a tile kernel forms the piece's logits again and
+// from them d, twice: d s_e with the vocabulary contiguous (for dx) and d s_x with the tokens contiguous
+// (for de), as bf16 pieces (grad_gemm.h); two products with the codes then give the piece's rows of de
+// and its share of dx.  The gradient's type sets the pieces: fp32 takes two (relative error at most
+// 2^-16 of each d), bf16 one (2^-8, the size of the final rounding).  Recomputing the logits costs one
+// int8 product; keeping them would cost 4 M V bytes written and read.
+#include <math.h>
+
+#include "grad_gemm.h"
+#include "tile_i8.h"
+
+namespace dfssm {
+
+namespace {
+
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLn2 = 0.69314718055994530942f;
+
+struct LossArgs {
+    const int8_t* x_q;
+    const float* s_x;
+    int64_t M, V;
+    int K, ntw, ntt;
+    const int8_t* e;
+    const float* s_e;
+    float2* part;   // [ntw][M]: a tile's maximum (of z log2 e) and sum of 2^(z log2 e - maximum)
+};
+
+// ---------------------------------------------------------------- forward
+template <class C>
+__global__ __launch_bounds__(C::NT, C::NT / 256) void loss_tile_kernel(LossArgs a) {
+    __shared__ __attribute__((aligned(16))) uint8_t lds[C::kLdsBytes];
+    const TilePos pos = tile_pos(blockIdx.x, a.ntw, a.ntt);
+    const int64_t n0 = (int64_t)pos.w * C::BW, m0 = (int64_t)pos.t * C::BT;
+    const int wrows = (int)(a.V - n0 < C::BW ? a.V - n0 : C::BW);
+    const int trows = (int)(a.M - m0 < C::BT ? a.M - m0 : C::BT);
+    v16i acc[C::WB][C::TB];
+    tile_i8<C, true>(a.e + n0 * a.K, a.K, wrows, a.x_q + m0 * a.K, a.K, trows, a.K, lds, acc);
+
+    const int lane = threadIdx.x & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x / kWave));
+    const int ww = wave % C::WW, tw = wave / C::WW;
+    const int l32 = lane & 31, g = lane >> 5;
+    const int wn = ww * C::WB * 32;
+    float se[C::WB][16];
+#pragma unroll
+    for (int b = 0; b < C::WB; ++b)
+#pragma unroll
+        for (int v = 0; v < 16; ++v) {
+            const int r = wn + b * 32 + 8 * (v >> 2) + 4 * g + (v & 3);
+            se[b][v] = a.s_e[n0 + (r < wrows ? r : wrows - 1)];
+        }
+    lds_barrier();
+    float2* const red = reinterpret_cast<float2*>(lds);  // [WW][BT]
+    const float neg = -__builtin_inff();
+#pragma unroll
+    for (int tb = 0; tb < C::TB; ++tb) {
+        const int t = (tw * C::TB + tb) * 32 + l32;
+        const float sx2 = a.s_x[m0 + (t < trows ? t : trows - 1)] * kLog2e;
+        float z[C::WB][16], top = neg;
+#pragma unroll
+        for (int b = 0; b < C::WB; ++b)
+#pragma unroll
+            for (int v = 0; v < 16; ++v) {
+                z[b][v] = sx2 * (se[b][v] * (float)acc[b][tb][v]);
+                if (wrows < C::BW && wn + b * 32 + 8 * (v >> 2) + 4 * g + (v & 3) >= wrows) z[b][v] = neg;
+                top = fmaxf(top, z[b][v]);
+            }
+        const float base = top == neg ? 0.0f : top;  // (no row of the wave's range exists)
+        float sum = 0.0f;
+#pragma unroll
+        for (int b = 0; b < C::WB; ++b)
+#pragma unroll
+            for (int v = 0; v < 16; ++v) sum += __builtin_amdgcn_exp2f(z[b][v] - base);
+        // the two halves of the wave hold the same tokens
+        const float otop = __shfl_xor(top, 32), osum = __shfl_xor(sum, 32);
+        const float both = fmaxf(top, otop), b2 = both == neg ? 0.0f : both;
+        sum = g == 0 ? sum * __builtin_amdgcn_exp2f(top - b2) + osum * __builtin_amdgcn_exp2f(otop - b2) : 0.0f;
+        if (g == 0) red[ww * C::BT + t] = make_float2(both, sum);
+    }
+    lds_barrier();
+    for (int t = threadIdx.x; t < trows; t += C::NT) {
+        float top = neg;
+#pragma unroll
+        for (int w = 0; w < C::WW; ++w) top = fmaxf(top, red[w * C::BT + t].x);
+        float sum = 0.0f;
+#pragma unroll
+        for (int w = 0; w < C::WW; ++w) sum += red[w * C::BT + t].y * __builtin_amdgcn_exp2f(red[w * C::BT + t].x - top);
+        a.part[(int64_t)pos.w * a.M + m0 + t] = make_float2(top, sum);
+    }
+}
+
+// Joins the tiles' pairs in tile order and forms the target's logit: 16 tokens to a workgroup of
+// 1024 threads, 64 threads to a token (one wave).
+__global__ __launch_bounds__(1024) void loss_join_kernel(LossArgs a, const int32_t* __restrict__ targets,
+                                                         float* __restrict__ loss, float* __restrict__ lse) {
+    // pairs[wave][token]: a wave reads 16 tokens x 4 tiles, consecutive tokens side by side
+    __shared__ float2 pairs[16][64];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t m0 = (int64_t)blockIdx.x * 16;
+    const float neg = -__builtin_inff();
+    float top = neg, sum = 0.0f;
+    if (m0 + (lane & 15) < a.M)
+        for (int w = wave * 4 + (lane >> 4); w < a.ntw; w += 64) {
+            const float2 p = a.part[(int64_t)w * a.M + m0 + (lane & 15)];
+            const float t = fmaxf(top, p.x);
+            sum = sum * __builtin_amdgcn_exp2f(top - t) + p.y * __builtin_amdgcn_exp2f(p.x - t);
+            top = t;
+        }
+    pairs[wave][lane] = make_float2(top, sum);
+    __syncthreads();
+    const int64_t m = m0 + wave;
+    if (m >= a.M) return;
+    // lane i holds pair i of the wave's token: waves i / 4, tile classes i % 4
+    const float2 p = pairs[lane >> 2][(lane & 3) * 16 + wave];
+    const float all = wave_max(p.x);
+    float s = p.y == 0.0f ? 0.0f : p.y * __builtin_amdgcn_exp2f(p.x - all);
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) s += __shfl_xor(s, d);
+    const float l = (all + __log2f(s)) * kLn2;
+
+    const int32_t target = targets[m];
+    float out = 0.0f;
+    if (target >= 0 && target < a.V) {
+        const int8_t* x = a.x_q + m * a.K;
+        const int8_t* e = a.e + (int64_t)target * a.K;
+        int32_t dot = 0;
+        for (int k = lane * 16; k < a.K; k += 64 * 16) {
+            const v4i xv = *reinterpret_cast<const v4i*>(x + k), ev = *reinterpret_cast<const v4i*>(e + k);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) dot = __builtin_amdgcn_sdot4(xv[j], ev[j], dot, false);
+        }
+        dot = wave_sum(dot);
+        out = l - a.s_x[m] * (a.s_e[target] * (float)dot);
+    }
+    if (lane == 0) {
+        lse[m] = l;
+        loss[m] = out;
+    }
+}
+
+// ---------------------------------------------------------------- backward
+struct GradArgs {
+    const int8_t* x_q;
+    const float* s_x;
+    int64_t M, V;    // V: rows of the piece (a piece starts at v0)
+    int64_t v0, vocab;
+    int K, ntw, ntt;
+    const int8_t* e;     // the piece's rows and scales
+    const float* s_e;
+    const int32_t* targets;
+    const float* lse;
+    const float* dloss;
+    uint16_t* gx;        // [tokens][Vp P]: d s_e, or NULL
+    uint16_t* gw;        // [Vp][Mp P]: d s_x, or NULL
+    int64_t ldgx, ldgw;  // elements
+};
+
+template <class C, int P>
+__global__ __launch_bounds__(C::NT, C::NT / 256) void grad_tile_kernel(GradArgs a) {
+    __shared__ __attribute__((aligned(16))) uint8_t lds[C::kLdsBytes];
+    const TilePos pos = tile_pos(blockIdx.x, a.ntw, a.ntt);
+    const int64_t n0 = (int64_t)pos.w * C::BW, m0 = (int64_t)pos.t * C::BT;
+    const int wrows = (int)(a.V - n0 < C::BW ? a.V - n0 : C::BW);
+    const int trows = (int)(a.M - m0 < C::BT ? a.M - m0 : C::BT);
+    v16i acc[C::WB][C::TB];
+    tile_i8<C, true>(a.e + n0 * a.K, a.K, wrows, a.x_q + m0 * a.K, a.K, trows, a.K, lds, acc);
+
+    const int lane = threadIdx.x & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x / kWave));
+    const int ww = wave % C::WW, tw = wave / C::WW;
+    const int l32 = lane & 31, g = lane >> 5;
+    const int wn = ww * C::WB * 32;
+    float se[C::WB][16];
+#pragma unroll
+    for (int b = 0; b < C::WB; ++b)
+#pragma unroll
+        for (int v = 0; v < 16; ++v) {
+            const int r = wn + b * 32 + 8 * (v >> 2) + 4 * g + (v & 3);
+            se[b][v] = a.s_e[n0 + (r < wrows ? r : wrows - 1)];
+        }
+#pragma unroll
+    for (int tb = 0; tb < C::TB; ++tb) {
+        const int t = (tw * C::TB + tb) * 32 + l32;
+        const int64_t m = m0 + (t < trows ? t : trows - 1);
+        const float sx = a.s_x[m], sx2 = sx * kLog2e, l2 = a.lse[m] * kLog2e;
+        const int64_t target = a.targets[m];
+        const bool counts = t < trows && target >= 0 && target < a.vocab;
+        const float dl = counts ? a.dloss[m] : 0.0f;
+        const int tl = (int)(target - a.v0 - n0 - wn);  // the target's row in the wave's range
+#pragma unroll
+        for (int b = 0; b < C::WB; ++b)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                float d[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int r = b * 32 + 8 * q + 4 * g + j;
+                    const float z = sx2 * (se[b][4 * q + j] * (float)acc[b][tb][4 * q + j]);
+                    float p = __builtin_amdgcn_exp2f(z - l2);
+                    if (r == tl) p -= 1.0f;
+                    d[j] = counts && wn + r < wrows ? dl * p : 0.0f;
+                }
+                const int64_t nb = n0 + wn + b * 32;  // first vocabulary row of the block
+                if (a.gx) {
+                    uint32_t h[4], l[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float x = d[j] * se[b][4 * q + j];
+                        h[j] = bf16_bits(x);
+                        l[j] = P == 2 ? bf16_bits(x - __uint_as_float(h[j] << 16)) : 0u;
+                    }
+                    uint16_t* dst = a.gx + (m0 + t) * a.ldgx + nb * P + 8 * q + 4 * g;
+                    *reinterpret_cast<uint2*>(dst) = make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
+                    if constexpr (P == 2)
+                        *reinterpret_cast<uint2*>(dst + 32) = make_uint2(l[0] | (l[1] << 16), l[2] | (l[3] << 16));
+                }
+                if (a.gw) {
+                    const int64_t mb = m0 + (tw * C::TB + tb) * 32;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float x = d[j] * sx;
+                        const uint32_t h = bf16_bits(x);
+                        uint16_t* dst = a.gw + (nb + 8 * q + 4 * g + j) * a.ldgw + mb * P + l32;
+                        dst[0] = (uint16_t)h;
+                        if constexpr (P == 2) dst[32] = (uint16_t)bf16_bits(x - __uint_as_float(h << 16));
+                    }
+                }
+            }
+    }
+}
+
+// dx = the sum of its splits' slabs, rounded to its type.
+template <bool kBf16>
+__global__ __launch_bounds__(256) void slab_sum_kernel(const float* __restrict__ slabs, int splits, int64_t n,
+                                                       void* __restrict__ out) {
+    for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4; i < n; i += (int64_t)gridDim.x * 1024) {
+        v4f s = *reinterpret_cast<const v4f*>(slabs + i);
+        for (int k = 1; k < splits; ++k) s += *reinterpret_cast<const v4f*>(slabs + k * n + i);
+        if constexpr (kBf16) {
+            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(out) + i) =
+                make_uint2(bf16_bits(s.x) | (bf16_bits(s.y) << 16), bf16_bits(s.z) | (bf16_bits(s.w) << 16));
+        } else {
+            *reinterpret_cast<v4f*>(static_cast<float*>(out) + i) = s;
+        }
+    }
+}
+
+using Tile256 = TileI8<2, 4, 4, 2>;  // 256 rows x 256 tokens, 8 waves
+using Tile128 = TileI8<2, 2, 2, 2>;  // 128 x 128, 4 waves
+using Tile64 = TileI8<1, 2, 4, 1>;   // 128 x 64, 4 waves
+using Tile32 = TileI8<1, 1, 4, 1>;   // 128 x 32, 4 waves
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// How a backward call is cut and where its workspace lies; the size query and the call agree on it.
+struct Plan {
+    int64_t Mp;      // tokens padded to the tile
+    int64_t piece;   // vocabulary rows per piece, a multiple of 256
+    int splits;      // of dx's sum over a piece
+    bool slabs;      // dx is summed in fp32 in the workspace
+    size_t gx, gw, dx, bytes;
+};
+
+int64_t token_tile(int64_t M) { return M <= 64 ? 64 : M <= 128 ? 128 : 256; }
+
+Plan make_plan(int64_t M, int64_t V, int64_t K, bool bf16, bool want_dx, bool want_de) {
+    const int64_t P = bf16 ? 1 : 2;
+    Plan p{};
+    p.Mp = ceil_div(M, token_tile(M)) * token_tile(M);
+    // pieces whose d stays in the 256 MB cache behind the L2s, but no fewer than 2048 rows
+    const int64_t per_row = p.Mp * P * 2 * ((want_dx ? 1 : 0) + (want_de ? 1 : 0));
+    int64_t piece = ((int64_t)256 << 20) / per_row;
+    if (piece < 2048) piece = 2048;
+    const int64_t n = ceil_div(V, piece);
+    p.piece = ceil_div(ceil_div(V, n), 256) * 256;
+    size_t at = 0;
+    auto take = [&](size_t b) {
+        const size_t was = at;
+        at += (b + 255) / 256 * 256;
+        return was;
+    };
+    if (want_dx) {
+        const int64_t tiles = grad_gemm_tiles(M, K);
+        int64_t s = 256 / tiles;
+        if (s > p.piece / 512) s = p.piece / 512;
+        p.splits = (int)(s < 1 ? 1 : s > 64 ? 64 : s);
+        p.slabs = bf16 || p.splits > 1;
+        p.gx = take((size_t)(p.Mp * p.piece * P * 2));
+        if (p.slabs) p.dx = take((size_t)p.splits * M * K * 4);
+    }
+    if (want_de) p.gw = take((size_t)(p.piece * p.Mp * P * 2));
+    p.bytes = at;
+    return p;
+}
+
+template <int P>
+hipError_t launch_grad_tiles(GradArgs a, hipStream_t stream) {
+    const int64_t bt = token_tile(a.M);
+    a.ntt = (int)ceil_div(a.M, bt);
+    a.ntw = (int)ceil_div(a.V, bt == 256 ? 256 : 128);
+    const dim3 grid((unsigned)(a.ntw * a.ntt));
+    if (bt == 256) grad_tile_kernel<Tile256, P><<<grid, Tile256::NT, 0, stream>>>(a);
+    else if (bt == 128) grad_tile_kernel<Tile128, P><<<grid, Tile128::NT, 0, stream>>>(a);
+    else grad_tile_kernel<Tile64, P><<<grid, Tile64::NT, 0, stream>>>(a);
+    return hipGetLastError();
+}
+
+int64_t loss_row_tile(int64_t M) { return M <= 256 ? 128 : 256; }
+
+}  // namespace
+
+size_t cross_entropy_workspace_bytes(int64_t M, int64_t V) {
+    return (size_t)(ceil_div(V, loss_row_tile(M)) * M) * sizeof(float2);
+}
+
+hipError_t launch_cross_entropy(const int8_t* x_q, const float* s_x, int64_t M, int64_t V, int64_t K, const int8_t* e,
+                                const float* s_e, const int32_t* targets, float* loss, float* lse, void* workspace,
+                                hipStream_t stream) {
+    LossArgs a{x_q, s_x, M, V, (int)K, 0, 0, e, s_e, static_cast<float2*>(workspace)};
+    a.ntw = (int)ceil_div(V, loss_row_tile(M));
+    const int64_t bt = M <= 32 ? 32 : M <= 256 ? 128 : 256;
+    a.ntt = (int)ceil_div(M, bt);
+    const dim3 grid((unsigned)((int64_t)a.ntw * a.ntt));
+    if (bt == 32) loss_tile_kernel<Tile32><<<grid, Tile32::NT, 0, stream>>>(a);
+    else if (bt == 128) loss_tile_kernel<Tile128><<<grid, Tile128::NT, 0, stream>>>(a);
+    else loss_tile_kernel<Tile256><<<grid, Tile256::NT, 0, stream>>>(a);
+    if (hipError_t err = hipGetLastError()) return err;
+    loss_join_kernel<<<dim3((unsigned)ceil_div(M, 16)), 1024, 0, stream>>>(a, targets, loss, lse);
+    return hipGetLastError();
+}
+
+size_t cross_entropy_backward_workspace_bytes(int64_t M, int64_t V, int64_t K, bool bf16, bool want_dx, bool want_de) {
+    return make_plan(M, V, K, bf16, want_dx, want_de).bytes;
+}
+
+hipError_t launch_cross_entropy_backward(const int8_t* x_q, const float* s_x, int64_t M, int64_t V, int64_t K,
+                                         const int8_t* e, const float* s_e, const int32_t* targets, const float* lse,
+                                         const float* dloss, void* dx, void* de, bool bf16, bool accumulate,
+                                         void* workspace, hipStream_t stream) {
+    const Plan p = make_plan(M, V, K, bf16, dx != nullptr, de != nullptr);
+    const int P = bf16 ? 1 : 2;
+    uint8_t* const ws = static_cast<uint8_t*>(workspace);
+    for (int64_t v0 = 0; v0 < V; v0 += p.piece) {
+        const int64_t rows = V - v0 < p.piece ? V - v0 : p.piece;
+        GradArgs g{x_q, s_x, M, rows, v0, V, (int)K, 0, 0, e + v0 * K, s_e + v0, targets, lse, dloss,
+                   dx ? reinterpret_cast<uint16_t*>(ws + p.gx) : nullptr,
+                   de ? reinterpret_cast<uint16_t*>(ws + p.gw) : nullptr, p.piece * P, p.Mp * P};
+        if (hipError_t err = P == 1 ? launch_grad_tiles<1>(g, stream) : launch_grad_tiles<2>(g, stream)) return err;
+        if (dx) {
+            const GradGemmArgs a{ws + p.gx, p.piece * P * 2, g.e, K, M, K, rows,
+                                 p.slabs ? static_cast<void*>(ws + p.dx) : dx, K, M * K, p.splits, v0 > 0, false};
+            if (hipError_t err = launch_grad_gemm(a, P, stream)) return err;
+        }
+        if (de) {
+            const GradGemmArgs a{ws + p.gw, p.Mp * P * 2, x_q, K, rows, K, M,
+                                 static_cast<uint8_t*>(de) + v0 * K * (bf16 ? 2 : 4), K, 0, 1, accumulate, bf16};
+            if (hipError_t err = launch_grad_gemm(a, P, stream)) return err;
+        }
+    }
+    if (dx && p.slabs) {
+        const int64_t n = M * K;
+        int64_t blocks = ceil_div(n, 1024);
+        if (blocks > 2048) blocks = 2048;
+        const float* slabs = reinterpret_cast<const float*>(ws + p.dx);
+        if (bf16) slab_sum_kernel<true><<<dim3((unsigned)blocks), 256, 0, stream>>>(slabs, p.splits, n, dx);
+        else slab_sum_kernel<false><<<dim3((unsigned)blocks), 256, 0, stream>>>(slabs, p.splits, n, dx);
+        return hipGetLastError();
+    }
+    return hipSuccess;
+}
+
+}  // namespace dfssm

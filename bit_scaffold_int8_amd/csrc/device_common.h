@@ -99,6 +99,17 @@ __device__ __forceinline__ void lds_barrier() {
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
+// Orders a wave's LDS accesses among its own lanes (they complete in program order; this
+// keeps the compiler from moving them across).
+__device__ __forceinline__ void wave_lds_order() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
+}
+
+// fp32 to bf16, round to nearest even, as its 16 bits.
+__device__ __forceinline__ uint32_t bf16_bits(float v) { return __builtin_bit_cast(uint16_t, (__bf16)v); }
+
 // Raw buffer resource over [base, base + bytes).  A buffer access past `bytes` is
 // dropped (store) or reads zero (load) by the hardware range check, so an offset of
 // kOffDead predicates a store without a branch -- and without the control flow that

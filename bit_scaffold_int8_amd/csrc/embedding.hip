@@ -1,0 +1,512 @@
+// embedding.hip -- scaled rows of the int8 embedding matrix, and the embedding's gradient (gfx950).
+//
+//   lookup:    out[t] = (scale s_e[id]) e[id],  id = tokens[t]         (zeros outside [0, V))
+//   backward:  de[v] (+)= scale sum over the t with tokens[t] = v of dout[t]
+//
+// The gradient is a scatter of T rows into V, with rows hit any number of times.  Float atomics
+// would add in an order that changes from run to run, so the tokens are sorted (stable radix sort by 8 bits a
+// pass; equal tokens stay in their order) and each row's sum runs over its tokens in order.  The sorted list
+// is cut into pieces of equal length, so that a token that fills half the batch is summed by many
+// workgroups: a piece writes the rows that lie wholly in it, and the sums of a row that crosses its
+// ends go to the workspace, from where a second kernel joins them in order.
+#include "device_common.h"
+
+namespace dfssm {
+
+namespace {
+
+// ---------------------------------------------------------------- lookup
+constexpr int kLookTokens = 4;  // tokens per thread: independent loads in flight
+
+template <bool kBf16, int VEC>
+__global__ __launch_bounds__(256) void lookup_scaled_kernel(const int32_t* __restrict__ tokens, int64_t T,
+                                                            const int8_t* __restrict__ e,
+                                                            const float* __restrict__ s_e, int64_t V, int64_t K,
+                                                            float scale, void* __restrict__ out, int64_t ldo) {
+    const int64_t k = ((int64_t)blockIdx.y * 256 + threadIdx.x) * VEC;
+    if (k >= K) return;
+    const int64_t t0 = (int64_t)blockIdx.x * kLookTokens;
+    int64_t id[kLookTokens];
+    float s[kLookTokens];
+    int8_t c[kLookTokens][VEC];
+#pragma unroll
+    for (int j = 0; j < kLookTokens; ++j) id[j] = tokens[t0 + j < T ? t0 + j : T - 1];
+#pragma unroll
+    for (int j = 0; j < kLookTokens; ++j) {
+        const bool in = id[j] >= 0 && id[j] < V;
+        const int64_t row = in ? id[j] : 0;
+        s[j] = in ? scale * s_e[row] : 0.0f;
+        __builtin_memcpy(c[j], __builtin_assume_aligned(e + row * K + k, VEC), VEC);
+        if (!in)
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) c[j][i] = 0;
+    }
+#pragma unroll
+    for (int j = 0; j < kLookTokens; ++j) {
+        if (t0 + j >= T) break;
+        const int64_t at = (t0 + j) * ldo + k;
+        if constexpr (kBf16) {
+            uint16_t o[VEC];
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) o[i] = (uint16_t)bf16_bits(s[j] * (float)c[j][i]);
+            __builtin_memcpy(__builtin_assume_aligned(static_cast<uint16_t*>(out) + at, VEC * 2), o, VEC * 2);
+        } else {
+            float o[VEC];
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) o[i] = s[j] * (float)c[j][i];
+            __builtin_memcpy(__builtin_assume_aligned(static_cast<float*>(out) + at, VEC * 4), o, VEC * 4);
+        }
+    }
+}
+
+// ---------------------------------------------------------------- sort
+// Blocks of 4096 items, 8 waves; wave w owns items [512 w, 512 w + 512) in 8 rounds of 64, so
+// (wave, round, lane) is the items' order.
+constexpr int kSortThreads = 512, kSortWaves = 8, kSortRounds = 8;
+constexpr int kSortBlock = kSortWaves * kSortRounds * kWave;
+
+// Lanes of the wave whose digit equals this lane's (live lanes only; dead lanes share digit 256).
+__device__ __forceinline__ uint64_t same_digit(int digit) {
+    uint64_t m = ~0ull;
+#pragma unroll
+    for (int b = 0; b < 9; ++b) {
+        const uint64_t set = __ballot((digit >> b) & 1);
+        m &= (digit >> b) & 1 ? set : ~set;
+    }
+    return m;
+}
+
+struct SortShared {
+    int32_t count[kSortWaves][256];  // per wave and digit; then the wave's first rank within the block
+    int32_t total[256];              // the block's items of a digit
+    int32_t start[256];              // where the block's items of a digit go
+};
+
+// Ranks of a block's items by digit: rank[r] counts the block's earlier items with the same digit.
+// sh.total is complete after the call (a barrier ends it).
+__device__ __forceinline__ void block_ranks(const uint32_t (&key)[kSortRounds], const bool (&live)[kSortRounds],
+                                            int shift, SortShared& sh, int (&digit)[kSortRounds],
+                                            int (&rank)[kSortRounds]) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    for (int d = lane; d < 256; d += 64) sh.count[wave][d] = 0;
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < kSortRounds; ++r) {
+        digit[r] = live[r] ? (int)((key[r] >> shift) & 255u) : 256;
+        const uint64_t same = same_digit(digit[r]);
+        const int before = __popcll(same & ((1ull << lane) - 1));
+        rank[r] = 0;
+        if (live[r]) rank[r] = sh.count[wave][digit[r]] + before;
+        wave_lds_order();  // every lane's read comes before the adds, and they before the next round's reads
+        if (live[r] && before == 0) sh.count[wave][digit[r]] += __popcll(same);
+        wave_lds_order();
+    }
+    __syncthreads();
+    if (threadIdx.x < 256) {
+        int sum = 0;
+        for (int w = 0; w < kSortWaves; ++w) {
+            const int c = sh.count[w][threadIdx.x];
+            sh.count[w][threadIdx.x] = sum;
+            sum += c;
+        }
+        sh.total[threadIdx.x] = sum;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < kSortRounds; ++r)
+        if (live[r]) rank[r] += sh.count[wave][digit[r]];
+}
+
+// Exclusive scan of 256 values, one per thread of the first four waves; all threads call it.
+__device__ __forceinline__ int scan256(int v, int32_t* part) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    int inc = v;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const int o = __shfl_up(inc, d);
+        if (lane >= d) inc += o;
+    }
+    if (lane == 63 && wave < 4) part[wave] = inc;
+    __syncthreads();
+    int base = 0;
+    for (int w = 0; w < wave && w < 4; ++w) base += part[w];
+    __syncthreads();
+    return base + inc - v;
+}
+
+// A token's sort key: tokens outside the vocabulary sort behind all others.
+__device__ __forceinline__ uint32_t token_key(int32_t id, uint32_t V) { return id >= 0 && (uint32_t)id < V ? (uint32_t)id : V; }
+
+// T <= kSortBlock: every pass in one workgroup.
+__global__ __launch_bounds__(kSortThreads) void sort_one_kernel(const int32_t* __restrict__ tokens, int T, uint32_t V,
+                                                                int passes, uint32_t* __restrict__ keys,
+                                                                int32_t* __restrict__ order) {
+    __shared__ SortShared sh;
+    __shared__ uint32_t skey[kSortBlock];
+    __shared__ int32_t sidx[kSortBlock];
+    __shared__ int32_t part[4];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    uint32_t key[kSortRounds];
+    int32_t idx[kSortRounds];
+    bool live[kSortRounds];
+    int digit[kSortRounds], rank[kSortRounds];
+    const int i0 = wave * kSortRounds * 64 + lane;
+#pragma unroll
+    for (int r = 0; r < kSortRounds; ++r) {
+        const int i = i0 + r * 64;
+        live[r] = i < T;
+        idx[r] = i;
+        key[r] = live[r] ? token_key(tokens[i], V) : 0u;
+    }
+    for (int p = 0; p < passes; ++p) {
+        block_ranks(key, live, 8 * p, sh, digit, rank);
+        const int start = scan256(threadIdx.x < 256 ? sh.total[threadIdx.x] : 0, part);
+        if (threadIdx.x < 256) sh.start[threadIdx.x] = start;
+        __syncthreads();
+#pragma unroll
+        for (int r = 0; r < kSortRounds; ++r)
+            if (live[r]) {
+                const int at = sh.start[digit[r]] + rank[r];
+                skey[at] = key[r];
+                sidx[at] = idx[r];
+            }
+        __syncthreads();
+#pragma unroll
+        for (int r = 0; r < kSortRounds; ++r)
+            if (live[r]) {
+                key[r] = skey[i0 + r * 64];
+                idx[r] = sidx[i0 + r * 64];
+            }
+        __syncthreads();
+    }
+#pragma unroll
+    for (int r = 0; r < kSortRounds; ++r)
+        if (live[r]) {
+            keys[i0 + r * 64] = key[r];
+            order[i0 + r * 64] = idx[r];
+        }
+}
+
+// A pass over many blocks: how often each digit occurs in each block ...
+__global__ __launch_bounds__(kSortThreads) void sort_count_kernel(const int32_t* __restrict__ tokens,
+                                                                  const uint32_t* __restrict__ keys, int64_t T,
+                                                                  uint32_t V, int shift, int32_t* __restrict__ hist) {
+    __shared__ int32_t count[256];
+    if (threadIdx.x < 256) count[threadIdx.x] = 0;
+    __syncthreads();
+    const int64_t b0 = (int64_t)blockIdx.x * kSortBlock;
+#pragma unroll
+    for (int r = 0; r < kSortBlock / kSortThreads; ++r) {
+        const int64_t i = b0 + r * kSortThreads + threadIdx.x;
+        if (i < T) atomicAdd(&count[((keys ? keys[i] : token_key(tokens[i], V)) >> shift) & 255u], 1);
+    }
+    __syncthreads();
+    if (threadIdx.x < 256) hist[(int64_t)blockIdx.x * 256 + threadIdx.x] = count[threadIdx.x];
+}
+
+// ... and each block's items to their places: behind all smaller digits and the digit's items of
+// the blocks before.  `tokens` on the first pass, (keys, order) afterwards.
+__global__ __launch_bounds__(kSortThreads) void sort_scatter_kernel(const int32_t* __restrict__ tokens,
+                                                                    const uint32_t* __restrict__ keys,
+                                                                    const int32_t* __restrict__ order, int64_t T,
+                                                                    uint32_t V, int shift,
+                                                                    const int32_t* __restrict__ hist,
+                                                                    uint32_t* __restrict__ keys_out,
+                                                                    int32_t* __restrict__ order_out) {
+    __shared__ SortShared sh;
+    __shared__ int32_t part[4];
+    __shared__ int32_t halves[2][256][2];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    // digit d's count in the blocks before this one and in all (two halves of the threads share the blocks)
+    {
+        const int d = threadIdx.x & 255, h = threadIdx.x >> 8;
+        int before = 0, all = 0;
+        for (int b = h; b < (int)gridDim.x; b += 2) {
+            const int c = hist[(int64_t)b * 256 + d];
+            all += c;
+            before += b < (int)blockIdx.x ? c : 0;
+        }
+        halves[h][d][0] = before;
+        halves[h][d][1] = all;
+    }
+    __syncthreads();
+    const int d = threadIdx.x & 255;
+    const int total = halves[0][d][1] + halves[1][d][1];
+    const int start = scan256(threadIdx.x < 256 ? total : 0, part);
+    if (threadIdx.x < 256) sh.start[d] = start + halves[0][d][0] + halves[1][d][0];
+
+    uint32_t key[kSortRounds];
+    int32_t idx[kSortRounds];
+    bool live[kSortRounds];
+    int digit[kSortRounds], rank[kSortRounds];
+    const int64_t i0 = (int64_t)blockIdx.x * kSortBlock + wave * kSortRounds * 64 + lane;
+#pragma unroll
+    for (int r = 0; r < kSortRounds; ++r) {
+        const int64_t i = i0 + r * 64;
+        live[r] = i < T;
+        idx[r] = live[r] ? (order ? order[i] : (int32_t)i) : 0;
+        key[r] = live[r] ? (keys ? keys[i] : token_key(tokens[i], V)) : 0u;
+    }
+    block_ranks(key, live, shift, sh, digit, rank);
+#pragma unroll
+    for (int r = 0; r < kSortRounds; ++r)
+        if (live[r]) {
+            const int at = sh.start[digit[r]] + rank[r];
+            keys_out[at] = key[r];
+            order_out[at] = idx[r];
+        }
+}
+
+// ---------------------------------------------------------------- sums
+struct SumArgs {
+    const uint32_t* keys;   // sorted
+    const int32_t* order;
+    int64_t T;
+    const void* dout;
+    int64_t ldd;
+    uint32_t V;
+    int64_t K;
+    float scale;
+    void* de;
+    float* head;            // [pieces][K]: a piece's part of the row that began before it
+    float* tail;            // [pieces][K]: its part of a row that begins in it and goes on behind it
+    int64_t piece;          // sorted tokens per piece
+    int pieces, col_blocks;
+};
+
+template <bool kBf16, int VEC>
+__device__ __forceinline__ void load_vec(const void* base, int64_t at, float (&v)[VEC]) {
+    if constexpr (kBf16) {
+        uint16_t b[VEC];
+        __builtin_memcpy(b, __builtin_assume_aligned(static_cast<const uint16_t*>(base) + at, VEC * 2), VEC * 2);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) v[i] = __uint_as_float((uint32_t)b[i] << 16);
+    } else {
+        __builtin_memcpy(v, __builtin_assume_aligned(static_cast<const float*>(base) + at, VEC * 4), VEC * 4);
+    }
+}
+
+template <bool kBf16, int VEC>
+__device__ __forceinline__ void store_vec(void* base, int64_t at, const float (&v)[VEC]) {
+    if constexpr (kBf16) {
+        uint16_t b[VEC];
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) b[i] = (uint16_t)bf16_bits(v[i]);
+        __builtin_memcpy(__builtin_assume_aligned(static_cast<uint16_t*>(base) + at, VEC * 2), b, VEC * 2);
+    } else {
+        __builtin_memcpy(__builtin_assume_aligned(static_cast<float*>(base) + at, VEC * 4), v, VEC * 4);
+    }
+}
+
+template <bool kOutBf16, bool kAdd, int VEC>
+__device__ __forceinline__ void write_row(const SumArgs& a, uint32_t row, int64_t k, const float (&sum)[VEC]) {
+    float o[VEC];
+    const int64_t at = (int64_t)row * a.K + k;
+    if constexpr (kAdd) {
+        load_vec<kOutBf16, VEC>(a.de, at, o);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) o[i] += a.scale * sum[i];
+    } else {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) o[i] = a.scale * sum[i];
+    }
+    store_vec<kOutBf16, VEC>(a.de, at, o);
+}
+
+constexpr int kFillRows = 32;  // rows per workgroup that fills the rows without tokens
+
+// Workgroups [0, pieces * col_blocks) sum pieces; the ones behind them (none when adding to de) write zeros
+// to the rows that no token names.
+template <bool kInBf16, bool kOutBf16, bool kAdd, int VEC>
+__global__ __launch_bounds__(256) void piece_sum_kernel(SumArgs a) {
+    const int nsum = a.pieces * a.col_blocks;
+    if ((int)blockIdx.x >= nsum) {
+        if constexpr (!kAdd) {
+            __shared__ int32_t named[kFillRows];
+            const int64_t r0 = (int64_t)((int)blockIdx.x - nsum) * kFillRows;
+            if (threadIdx.x < kFillRows) {
+                const uint32_t row = (uint32_t)(r0 + threadIdx.x);
+                int64_t lo = 0, hi = a.T;  // first sorted token >= row
+                while (lo < hi) {
+                    const int64_t mid = (lo + hi) >> 1;
+                    if (a.keys[mid] < row) lo = mid + 1;
+                    else hi = mid;
+                }
+                named[threadIdx.x] = lo < a.T && a.keys[lo] == row;
+            }
+            __syncthreads();
+            const float zero[VEC] = {};
+            for (int r = 0; r < kFillRows && r0 + r < a.V; ++r)
+                if (!named[r])
+                    for (int64_t k = threadIdx.x * VEC; k < a.K; k += 256 * VEC)
+                        store_vec<kOutBf16, VEC>(a.de, (r0 + r) * a.K + k, zero);
+        }
+        return;
+    }
+    const int piece = (int)blockIdx.x / a.col_blocks, cb = (int)blockIdx.x - piece * a.col_blocks;
+    const int64_t k = ((int64_t)cb * 256 + threadIdx.x) * VEC;
+    const int64_t p0 = piece * a.piece, p1 = p0 + a.piece < a.T ? p0 + a.piece : a.T;
+    if (k >= a.K) return;
+    const bool from_before = p0 > 0 && a.keys[p0 - 1] == a.keys[p0];
+    const bool goes_on = p1 < a.T && a.keys[p1] == a.keys[p1 - 1];
+    float sum[VEC] = {};
+    bool first = true;  // still in the piece's first row
+    constexpr int U = 8;  // rows in flight
+    for (int64_t p = p0; p < p1; p += U) {
+        float v[U][VEC];
+        uint32_t key[U + 1];
+#pragma unroll
+        for (int j = 0; j < U; ++j) {
+            const int64_t q = p + j < p1 ? p + j : p1 - 1;
+            key[j] = a.keys[q];
+            load_vec<kInBf16, VEC>(a.dout, a.order[q] * a.ldd + k, v[j]);
+        }
+        key[U] = p + U < p1 ? a.keys[p + U] : 0xffffffffu;
+#pragma unroll
+        for (int j = 0; j < U; ++j) {
+            if (p + j >= p1) break;
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) sum[i] += v[j][i];
+            const bool last = p + j + 1 == p1;
+            if (last || key[j + 1] != key[j]) {
+                if (key[j] < a.V) {
+                    if (first && from_before) store_vec<false, VEC>(a.head, piece * a.K + k, sum);
+                    else if (last && goes_on) store_vec<false, VEC>(a.tail, piece * a.K + k, sum);
+                    else write_row<kOutBf16, kAdd, VEC>(a, key[j], k, sum);
+                }
+                first = false;
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) sum[i] = 0.0f;
+            }
+        }
+    }
+}
+
+// Rows that cross pieces: the piece where a row begins adds the following pieces' parts in order.
+template <bool kOutBf16, bool kAdd, int VEC>
+__global__ __launch_bounds__(256) void piece_join_kernel(SumArgs a) {
+    const int piece = (int)blockIdx.x / a.col_blocks, cb = (int)blockIdx.x - piece * a.col_blocks;
+    const int64_t k = ((int64_t)cb * 256 + threadIdx.x) * VEC;
+    const int64_t p0 = piece * a.piece, p1 = p0 + a.piece;
+    if (k >= a.K || p1 >= a.T) return;
+    const uint32_t row = a.keys[p1 - 1];
+    if (row >= a.V || a.keys[p1] != row) return;                    // nothing goes on
+    if (p0 > 0 && a.keys[p0] == row && a.keys[p0 - 1] == row) return;  // it began before this piece
+    float sum[VEC];
+    load_vec<false, VEC>(a.tail, piece * a.K + k, sum);
+    for (int q = piece + 1; q < a.pieces && a.keys[q * a.piece] == row; ++q) {
+        float v[VEC];
+        load_vec<false, VEC>(a.head, q * a.K + k, v);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) sum[i] += v[i];
+    }
+    write_row<kOutBf16, kAdd, VEC>(a, row, k, sum);
+}
+
+// How a backward call's workspace lies.
+struct Plan {
+    int64_t piece;
+    int pieces, sort_blocks, passes;
+    size_t keys[2], order[2], hist, head, tail, bytes;
+};
+
+Plan make_plan(int64_t T, int64_t V, int64_t K) {
+    Plan p{};
+    // pieces of 32 tokens, longer ones past 32768 tokens (1024 pieces fill the GPU)
+    p.piece = ((T + 1023) / 1024 + 31) / 32 * 32;
+    p.pieces = (int)((T + p.piece - 1) / p.piece);
+    p.sort_blocks = (int)((T + kSortBlock - 1) / kSortBlock);
+    p.passes = 1;
+    while (p.passes < 4 && ((uint64_t)V >> (8 * p.passes)) != 0) ++p.passes;  // keys 0 .. V
+    size_t at = 0;
+    auto take = [&](int64_t b) {
+        const size_t was = at;
+        at += ((size_t)b + 255) / 256 * 256;
+        return was;
+    };
+    for (int i = 0; i < 2; ++i) {
+        p.keys[i] = take(T * 4);
+        p.order[i] = take(T * 4);
+    }
+    p.hist = take((int64_t)p.sort_blocks * 256 * 4);
+    p.head = take(p.pieces * K * 4);
+    p.tail = take(p.pieces * K * 4);
+    p.bytes = at;
+    return p;
+}
+
+template <bool kInBf16, bool kOutBf16, bool kAdd, int VEC>
+hipError_t launch_sums(SumArgs a, hipStream_t stream) {
+    a.col_blocks = (int)((a.K + 256 * VEC - 1) / (256 * VEC));
+    const int64_t fills = kAdd ? 0 : ((int64_t)a.V + kFillRows - 1) / kFillRows;
+    piece_sum_kernel<kInBf16, kOutBf16, kAdd, VEC>
+        <<<dim3((unsigned)((int64_t)a.pieces * a.col_blocks + fills)), 256, 0, stream>>>(a);
+    if (hipError_t err = hipGetLastError()) return err;
+    if (a.pieces > 1)
+        piece_join_kernel<kOutBf16, kAdd, VEC><<<dim3((unsigned)(a.pieces * a.col_blocks)), 256, 0, stream>>>(a);
+    return hipGetLastError();
+}
+
+template <bool kInBf16, bool kOutBf16>
+hipError_t launch_sums_t(const SumArgs& a, bool add, bool vec, hipStream_t stream) {
+    if (add) return vec ? launch_sums<kInBf16, kOutBf16, true, 4>(a, stream) : launch_sums<kInBf16, kOutBf16, true, 1>(a, stream);
+    return vec ? launch_sums<kInBf16, kOutBf16, false, 4>(a, stream) : launch_sums<kInBf16, kOutBf16, false, 1>(a, stream);
+}
+
+bool aligned(const void* p, uintptr_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
+
+template <bool kBf16>
+hipError_t launch_lookup_t(const int32_t* tokens, int64_t T, const int8_t* e, const float* s_e, int64_t V, int64_t K,
+                           float scale, void* out, int64_t ldo, hipStream_t stream) {
+    constexpr int VEC = kBf16 ? 8 : 4;  // 16 bytes of output a thread
+    const bool vec = K % VEC == 0 && ldo % VEC == 0 && aligned(e, VEC) && aligned(out, 16);
+    const int64_t per = 256 * (vec ? VEC : 1);
+    const dim3 grid((unsigned)((T + kLookTokens - 1) / kLookTokens), (unsigned)((K + per - 1) / per));
+    if (vec) lookup_scaled_kernel<kBf16, VEC><<<grid, 256, 0, stream>>>(tokens, T, e, s_e, V, K, scale, out, ldo);
+    else lookup_scaled_kernel<kBf16, 1><<<grid, 256, 0, stream>>>(tokens, T, e, s_e, V, K, scale, out, ldo);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_embedding_lookup_scaled(const int32_t* tokens, int64_t T, const int8_t* e, const float* s_e,
+                                          int64_t V, int64_t K, float scale, void* out, int64_t ldo, bool bf16,
+                                          hipStream_t stream) {
+    return bf16 ? launch_lookup_t<true>(tokens, T, e, s_e, V, K, scale, out, ldo, stream)
+                : launch_lookup_t<false>(tokens, T, e, s_e, V, K, scale, out, ldo, stream);
+}
+
+size_t embedding_backward_workspace_bytes(int64_t T, int64_t V, int64_t K) { return make_plan(T, V, K).bytes; }
+
+hipError_t launch_embedding_backward(const int32_t* tokens, int64_t T, const void* dout, int64_t ldd, bool dout_bf16,
+                                     int64_t V, int64_t K, float scale, void* de, bool de_bf16, bool accumulate,
+                                     void* workspace, hipStream_t stream) {
+    const Plan p = make_plan(T, V, K);
+    uint8_t* const ws = static_cast<uint8_t*>(workspace);
+    uint32_t* keys[2] = {reinterpret_cast<uint32_t*>(ws + p.keys[0]), reinterpret_cast<uint32_t*>(ws + p.keys[1])};
+    int32_t* order[2] = {reinterpret_cast<int32_t*>(ws + p.order[0]), reinterpret_cast<int32_t*>(ws + p.order[1])};
+    int32_t* hist = reinterpret_cast<int32_t*>(ws + p.hist);
+    int at = 0;
+    if (p.sort_blocks == 1) {
+        sort_one_kernel<<<1, kSortThreads, 0, stream>>>(tokens, (int)T, (uint32_t)V, p.passes, keys[0], order[0]);
+    } else {
+        for (int i = 0; i < p.passes; ++i) {
+            const uint32_t* kin = i ? keys[at] : nullptr;
+            const int32_t* oin = i ? order[at] : nullptr;
+            const int to = i ? at ^ 1 : 0;
+            sort_count_kernel<<<dim3((unsigned)p.sort_blocks), kSortThreads, 0, stream>>>(tokens, kin, T, (uint32_t)V,
+                                                                                          8 * i, hist);
+            sort_scatter_kernel<<<dim3((unsigned)p.sort_blocks), kSortThreads, 0, stream>>>(
+                tokens, kin, oin, T, (uint32_t)V, 8 * i, hist, keys[to], order[to]);
+            at = to;
+        }
+    }
+    if (hipError_t err = hipGetLastError()) return err;
+    const SumArgs a{keys[at], order[at], T, dout, ldd, (uint32_t)V, K, scale, de,
+                    reinterpret_cast<float*>(ws + p.head), reinterpret_cast<float*>(ws + p.tail), p.piece, p.pieces, 0};
+    const bool vec = K % 4 == 0 && ldd % 4 == 0 && aligned(dout, dout_bf16 ? 8 : 16) && aligned(de, de_bf16 ? 8 : 16);
+    if (dout_bf16) return de_bf16 ? launch_sums_t<true, true>(a, accumulate, vec, stream) : launch_sums_t<true, false>(a, accumulate, vec, stream);
+    return de_bf16 ? launch_sums_t<false, true>(a, accumulate, vec, stream) : launch_sums_t<false, false>(a, accumulate, vec, stream);
+}
+
+}  // namespace dfssm

@@ -1,0 +1,204 @@
+// grad_gemm.hip -- C (+)= A B for bf16 pieces A and int8 codes B (gfx950; see grad_gemm.h).
+//
+// v_mfma_f32_32x32x16_bf16 with A's rows from LDS as they lie in memory (128-byte chunks, pieces
+// swizzled as in tile_i8.h) and B's codes in LDS as bytes, row by row.  B's fragment needs 8
+// consecutive r of one column: ds_read_b64_tr_b8 transposes 8 rows x 16 columns of bytes on the
+// way to the registers, where the codes become bf16 (exact).  Keeping B as bytes in memory and
+// LDS halves its traffic and needs no transposed copy.  With two pieces each B fragment
+// serves two products.  C's columns run along the lanes, so stores are runs of a row.
+#include "device_common.h"
+#include "grad_gemm.h"
+
+namespace dfssm {
+
+namespace {
+
+typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
+typedef int v2i __attribute__((ext_vector_type(2)));
+typedef uint32_t v4u __attribute__((ext_vector_type(4)));
+
+constexpr int kLoadDead = 0x7ff00000;  // a load offset past every resource used here: reads zero
+
+template <int MB_, int NB_, int MW_, int NW_>
+struct GradTile {
+    static constexpr int MB = MB_, NB = NB_, MW = MW_, NW = NW_;
+    static constexpr int BM = 32 * MB * MW, BN = 32 * NB * NW, NT = kWave * MW * NW;
+};
+
+// Four codes (bytes of w) as bf16, in two words.  An integer of 8 bits leaves the low half of
+// its fp32 form zero, so the high half is its bf16 form.
+__device__ __forceinline__ void codes4_bf16(int w, uint32_t& lo, uint32_t& hi) {
+    const float f0 = (float)(int8_t)w, f1 = (float)(int8_t)(w >> 8), f2 = (float)(int8_t)(w >> 16),
+                f3 = (float)(w >> 24);
+    lo = perm(__float_as_uint(f1), __float_as_uint(f0), 0x07060302u);
+    hi = perm(__float_as_uint(f3), __float_as_uint(f2), 0x07060302u);
+}
+
+template <class C, int P, bool kBf16, bool kAdd>
+__global__ __launch_bounds__(C::NT, C::NT / 256) void grad_gemm_kernel(GradGemmArgs a, int nti, int ntj,
+                                                                      int chunks_per_split) {
+    constexpr int kR = 64 / P;              // r per chunk: 128 bytes of an A row
+    constexpr int kLdB = C::BN + 16;        // 8 rows x 16 bytes read together hit distinct banks
+    constexpr int kA = C::BM * 128, kBuf = kA + kR * kLdB;
+    constexpr int PA = C::BM * 8 / C::NT;   // 16-byte pieces per thread per chunk
+    constexpr int PB = kR * C::BN / 16 / C::NT;
+    constexpr int TB = C::BN / 16;          // threads per B row
+    static_assert(PA * C::NT == C::BM * 8 && PB * C::NT * 16 == kR * C::BN && PB >= 1, "pieces split evenly");
+    static_assert(2 * kBuf <= 160 * 1024, "LDS");
+    __shared__ __attribute__((aligned(16))) uint8_t lds[2 * kBuf];
+
+    const int tid = threadIdx.x, lane = tid & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+    const int wm = wave % C::MW, wn = wave / C::MW;
+    const int l32 = lane & 31, g = lane >> 5, l16 = lane & 15;
+
+    // tiles of one XCD run along i within a column of tiles: they share B's columns
+    const int nt = nti * ntj;
+    const int per = nt >> 3, rem = nt & 7, xcd = blockIdx.x & 7;
+    const int tile = xcd * per + (xcd < rem ? xcd : rem) + (int)(blockIdx.x >> 3);
+    const int ti = tile / ntj, tj = tile - ti * ntj;
+    const int64_t i0 = (int64_t)ti * C::BM, j0 = (int64_t)tj * C::BN;
+    const int rows = (int)(a.I - i0 < C::BM ? a.I - i0 : C::BM);
+    const int cols = (int)(a.J - j0 < C::BN ? a.J - j0 : C::BN);
+    const int nchunks = (int)((a.R + kR - 1) / kR);
+    const int c0 = blockIdx.y * chunks_per_split;
+    const int c1 = c0 + chunks_per_split < nchunks ? c0 + chunks_per_split : nchunks;
+
+    const __amdgpu_buffer_rsrc_t ar = make_rsrc(a.a + i0 * a.lda, (uint32_t)((rows - 1) * a.lda + (int64_t)nchunks * 128));
+    const int arow = tid >> 3, apiece = tid & 7;
+    const int aoff = (int)(arow * a.lda) + apiece * 16, astep = (int)((C::NT / 8) * a.lda);
+    const int brow = tid / TB, bcol = (tid % TB) * 16;
+    const int boff = bcol < cols ? (int)(brow * a.ldb) + bcol : kLoadDead;
+    const int bstep = bcol < cols ? (int)((C::NT / TB) * a.ldb) : 0;
+    v4i va[PA], vb[PB];
+    auto load = [&](int c) {
+        const bool live = c < c1;
+        const int ao = aoff + c * 128;
+#pragma unroll
+        for (int j = 0; j < PA; ++j)
+            va[j] = __builtin_amdgcn_raw_buffer_load_b128(ar, live ? ao + j * astep : kLoadDead, 0, 0);
+        const int64_t left = live ? a.R - (int64_t)c * kR : 0;
+        const int br = (int)(left < kR ? left : kR);
+        const __amdgpu_buffer_rsrc_t rb =
+            make_rsrc(a.b + (live ? (int64_t)c * kR * a.ldb : 0) + j0, br > 0 ? (uint32_t)((br - 1) * a.ldb + cols) : 0u);
+#pragma unroll
+        for (int j = 0; j < PB; ++j) vb[j] = __builtin_amdgcn_raw_buffer_load_b128(rb, boff + j * bstep, 0, 0);
+    };
+    auto store = [&](uint8_t* buf) {
+#pragma unroll
+        for (int j = 0; j < PA; ++j)
+            *reinterpret_cast<v4i*>(buf + (arow + j * (C::NT / 8)) * 128 + ((apiece ^ (arow & 7)) << 4)) = va[j];
+#pragma unroll
+        for (int j = 0; j < PB; ++j)
+            *reinterpret_cast<v4i*>(buf + kA + (brow + j * (C::NT / TB)) * kLdB + bcol) = vb[j];
+    };
+
+    v16f acc[C::MB][C::NB];
+#pragma unroll
+    for (int x = 0; x < C::MB; ++x)
+#pragma unroll
+        for (int y = 0; y < C::NB; ++y)
+#pragma unroll
+            for (int v = 0; v < 16; ++v) acc[x][y][v] = 0.0f;
+
+    const int sw7 = l32 & 7;
+    const uint8_t* const afrag = lds + (wm * C::MB * 32 + l32) * 128;
+    // lane's source chunk of the transposing read: row 8 g + l16 / 2, columns 16 (group & 1) + 8 (l16 & 1)
+    uint8_t* const bfrag =
+        lds + kA + (8 * g + (l16 >> 1)) * kLdB + wn * C::NB * 32 + ((lane >> 4) & 1) * 16 + (l16 & 1) * 8;
+
+    load(c0);
+    store(lds);
+    load(c0 + 1);
+    for (int c = c0; c < c1; ++c) {
+        lds_barrier();
+        const int cur = ((c - c0) & 1) * kBuf, nxt = kBuf - cur;
+        store(lds + nxt);
+        load(c + 2);
+#pragma unroll
+        for (int s = 0; s < kR / 16; ++s) {
+            v8bf fb[C::NB];
+#pragma unroll
+            for (int y = 0; y < C::NB; ++y) {
+                const v2i w = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
+                    (__attribute__((address_space(3))) v2i*)(bfrag + cur + s * 16 * kLdB + y * 32));
+                v4u p;
+                uint32_t lo, hi;
+                codes4_bf16(w.x, lo, hi);
+                p.x = lo;
+                p.y = hi;
+                codes4_bf16(w.y, lo, hi);
+                p.z = lo;
+                p.w = hi;
+                fb[y] = __builtin_bit_cast(v8bf, p);
+            }
+#pragma unroll
+            for (int p = 0; p < P; ++p)
+#pragma unroll
+                for (int x = 0; x < C::MB; ++x) {
+                    const int piece = P == 1 ? 2 * s + g : 4 * p + 2 * s + g;
+                    const v8bf fa = *reinterpret_cast<const v8bf*>(afrag + cur + x * 32 * 128 + ((piece ^ sw7) << 4));
+#pragma unroll
+                    for (int y = 0; y < C::NB; ++y)
+                        acc[x][y] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa, fb[y], acc[x][y], 0, 0, 0);
+                }
+        }
+    }
+
+#pragma unroll
+    for (int y = 0; y < C::NB; ++y) {
+        const int col = wn * C::NB * 32 + y * 32 + l32;
+        if (col >= cols) continue;
+#pragma unroll
+        for (int x = 0; x < C::MB; ++x)
+#pragma unroll
+            for (int v = 0; v < 16; ++v) {
+                const int row = wm * C::MB * 32 + x * 32 + 8 * (v >> 2) + 4 * g + (v & 3);
+                if (row >= rows) continue;
+                const int64_t at = blockIdx.y * a.slab + (i0 + row) * a.ldc + j0 + col;
+                if constexpr (kBf16) {
+                    __bf16* p = static_cast<__bf16*>(a.c) + at;
+                    *p = (__bf16)(kAdd ? (float)*p + acc[x][y][v] : acc[x][y][v]);
+                } else {
+                    float* p = static_cast<float*>(a.c) + at;
+                    *p = kAdd ? *p + acc[x][y][v] : acc[x][y][v];
+                }
+            }
+    }
+}
+
+using Wide = GradTile<4, 2, 2, 4>;   // 256 x 256, 8 waves
+using Short = GradTile<2, 2, 1, 4>;  // 64 x 256, 4 waves: few rows of A
+
+template <class C, int P>
+hipError_t launch_c(const GradGemmArgs& a, hipStream_t stream) {
+    const int nti = (int)((a.I + C::BM - 1) / C::BM), ntj = (int)((a.J + C::BN - 1) / C::BN);
+    constexpr int kR = 64 / P;
+    const int64_t nchunks = (a.R + kR - 1) / kR;
+    const int per = (int)((nchunks + a.splits - 1) / a.splits);
+    const dim3 grid((unsigned)(nti * ntj), (unsigned)a.splits);
+    if (a.bf16_out) {
+        if (a.accumulate) grad_gemm_kernel<C, P, true, true><<<grid, C::NT, 0, stream>>>(a, nti, ntj, per);
+        else grad_gemm_kernel<C, P, true, false><<<grid, C::NT, 0, stream>>>(a, nti, ntj, per);
+    } else {
+        if (a.accumulate) grad_gemm_kernel<C, P, false, true><<<grid, C::NT, 0, stream>>>(a, nti, ntj, per);
+        else grad_gemm_kernel<C, P, false, false><<<grid, C::NT, 0, stream>>>(a, nti, ntj, per);
+    }
+    return hipGetLastError();
+}
+
+bool use_short(int64_t I) { return I <= 128; }
+
+}  // namespace
+
+int64_t grad_gemm_tiles(int64_t I, int64_t J) {
+    const int64_t bm = use_short(I) ? Short::BM : Wide::BM;
+    return ((I + bm - 1) / bm) * ((J + Wide::BN - 1) / Wide::BN);
+}
+
+hipError_t launch_grad_gemm(const GradGemmArgs& a, int pieces, hipStream_t stream) {
+    if (use_short(a.I)) return pieces == 1 ? launch_c<Short, 1>(a, stream) : launch_c<Short, 2>(a, stream);
+    return pieces == 1 ? launch_c<Wide, 1>(a, stream) : launch_c<Wide, 2>(a, stream);
+}
+
+}  // namespace dfssm

@@ -1,0 +1,135 @@
+// int8_gemm.hip -- the int8 product with one scale per token and one per channel (gfx950):
+//
+//   acc[m][n] = sum_k W[n][k] x_q[m][k]             (exact int32)
+//   y[m][n]   = s_x[m] * (s_w[n] * acc[m][n])       (fp32, two roundings; rounded once more to bf16)
+//
+// for any number of tokens: the LM head over a whole prompt, or an int8 layer.  The tile
+// product is tile_i8.h's.  The epilogue turns each 32-token block of a wave through LDS, so
+// that lanes write runs of a token's row instead of 16-byte pieces of 32 rows.
+#include "tile_i8.h"
+
+namespace dfssm {
+
+namespace {
+
+struct GemmArgs {
+    const int8_t* x_q;
+    int64_t ldx;
+    const float* s_x;
+    const int8_t* w;
+    int64_t ldw;
+    const float* s_w;
+    void* y;
+    int64_t ldy;
+    int64_t M, N;
+    int K, ntw, ntt;
+};
+
+// kVec: y and its rows are 16-byte aligned, so four outputs go out together.
+template <class C, bool kFast, bool kBf16, bool kVec>
+__global__ __launch_bounds__(C::NT, C::NT / 256 > 0 ? C::NT / 256 : 1) void int8_gemm_kernel(GemmArgs a) {
+    constexpr int kLd = C::WB * 32 + 4;  // floats per token row of a wave's LDS block
+    constexpr int kEpi = C::WW * C::TW * 32 * kLd * 4;
+    __shared__ __attribute__((aligned(16))) uint8_t lds[C::kLdsBytes > kEpi ? C::kLdsBytes : kEpi];
+    const TilePos pos = tile_pos(blockIdx.x, a.ntw, a.ntt);
+    const int64_t n0 = (int64_t)pos.w * C::BW, m0 = (int64_t)pos.t * C::BT;
+    const int wrows = (int)(a.N - n0 < C::BW ? a.N - n0 : C::BW);
+    const int trows = (int)(a.M - m0 < C::BT ? a.M - m0 : C::BT);
+    v16i acc[C::WB][C::TB];
+    tile_i8<C, kFast>(a.w + n0 * a.ldw, a.ldw, wrows, a.x_q + m0 * a.ldx, a.ldx, trows, a.K, lds, acc);
+
+    const int lane = threadIdx.x & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x / kWave));
+    const int ww = wave % C::WW, tw = wave / C::WW;
+    const int l32 = lane & 31, g = lane >> 5;
+    const int wn = ww * C::WB * 32;            // the wave's first weight row in the tile
+    const int live_n = wrows - wn;             // outputs of a token that exist in the wave's range
+    lds_barrier();
+    float* const blk = reinterpret_cast<float*>(lds) + wave * 32 * kLd;
+    // the lane's row scales: rows past N are clamped (their outputs are not stored)
+    float sw[C::WB][16];
+#pragma unroll
+    for (int b = 0; b < C::WB; ++b)
+#pragma unroll
+        for (int v = 0; v < 16; ++v) {
+            const int r = wn + b * 32 + 8 * (v >> 2) + 4 * g + (v & 3);
+            sw[b][v] = a.s_w[n0 + (r < wrows ? r : wrows - 1)];
+        }
+#pragma unroll
+    for (int tb = 0; tb < C::TB; ++tb) {
+        const int t0 = (tw * C::TB + tb) * 32;
+        const float sx = a.s_x[m0 + (t0 + l32 < trows ? t0 + l32 : trows - 1)];
+#pragma unroll
+        for (int b = 0; b < C::WB; ++b)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                v4f o;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[e] = sx * (sw[b][4 * q + e] * (float)acc[b][tb][4 * q + e]);
+                *reinterpret_cast<v4f*>(blk + l32 * kLd + b * 32 + 8 * q + 4 * g) = o;
+            }
+        // (the block is the wave's own)
+        wave_lds_order();
+        constexpr int L = C::WB * 8;  // lanes per token row, four outputs each
+        const int c = (lane % L) * 4;
+#pragma unroll
+        for (int r = 0; r < 32; r += kWave / L) {
+            const int tr = r + lane / L;
+            const v4f o = *reinterpret_cast<const v4f*>(blk + tr * kLd + c);
+            if (t0 + tr < trows && c < live_n) {
+                const int64_t at = (m0 + t0 + tr) * a.ldy + n0 + wn + c;
+                if (kVec && c + 4 <= live_n) {
+                    if constexpr (kBf16) {
+                        uint2 p;
+                        p.x = bf16_bits(o.x) | (bf16_bits(o.y) << 16);
+                        p.y = bf16_bits(o.z) | (bf16_bits(o.w) << 16);
+                        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.y) + at) = p;
+                    } else {
+                        *reinterpret_cast<v4f*>(static_cast<float*>(a.y) + at) = o;
+                    }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (c + e < live_n) {
+                            if constexpr (kBf16) static_cast<uint16_t*>(a.y)[at + e] = (uint16_t)bf16_bits(o[e]);
+                            else static_cast<float*>(a.y)[at + e] = o[e];
+                        }
+                }
+            }
+        }
+        wave_lds_order();
+    }
+}
+
+template <class C, bool kFast, bool kBf16>
+hipError_t launch_c(GemmArgs a, bool vec, hipStream_t stream) {
+    a.ntw = (int)((a.N + C::BW - 1) / C::BW);
+    a.ntt = (int)((a.M + C::BT - 1) / C::BT);
+    const dim3 grid((unsigned)((int64_t)a.ntw * a.ntt));
+    if (vec) int8_gemm_kernel<C, kFast, kBf16, true><<<grid, C::NT, 0, stream>>>(a);
+    else int8_gemm_kernel<C, kFast, kBf16, false><<<grid, C::NT, 0, stream>>>(a);
+    return hipGetLastError();
+}
+
+template <bool kFast, bool kBf16>
+hipError_t launch_f(const GemmArgs& a, bool vec, hipStream_t stream) {
+    const int64_t big = ((a.N + 255) / 256) * ((a.M + 255) / 256);
+    if (a.M <= 32) return launch_c<TileI8<1, 1, 4, 1>, kFast, kBf16>(a, vec, stream);
+    if (big >= 256) return launch_c<TileI8<2, 4, 4, 2>, kFast, kBf16>(a, vec, stream);
+    return launch_c<TileI8<2, 2, 2, 2>, kFast, kBf16>(a, vec, stream);
+}
+
+}  // namespace
+
+hipError_t launch_int8_gemm(const int8_t* x_q, int64_t ldx, const float* s_x, int64_t M, int64_t N, int64_t K,
+                            const int8_t* w, int64_t ldw, const float* s_w, void* y, int64_t ldy, bool bf16,
+                            hipStream_t stream) {
+    const GemmArgs a{x_q, ldx, s_x, w, ldw, s_w, y, ldy, M, N, (int)K, 0, 0};
+    auto al16 = [](const void* p) { return ((uintptr_t)p & 15u) == 0; };
+    const bool fast = al16(x_q) && al16(w) && ldx % 16 == 0 && ldw % 16 == 0 && K % 16 == 0;
+    const bool vec = al16(y) && ldy % (bf16 ? 8 : 4) == 0;
+    if (fast) return bf16 ? launch_f<true, true>(a, vec, stream) : launch_f<true, false>(a, vec, stream);
+    return bf16 ? launch_f<false, true>(a, vec, stream) : launch_f<false, false>(a, vec, stream);
+}
+
+}  // namespace dfssm

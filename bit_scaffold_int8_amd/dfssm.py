@@ -27,7 +27,14 @@ EXPORTED = ("dfssm_status_string", "dfssm_version", "dfssm_quantize_act", "dfssm
             "dfssm_int8_rowscale_gemm_strided_batched", "dfssm_embedding_lookup", "dfssm_mamba2_decode_step",
             "dfssm_prefill_plan", "dfssm_decode_layers_workspace_bytes", "dfssm_decode_layers_trace_words",
             "dfssm_decode_layers", "dfssm_decode_layers_noalloc", "dfssm_density_field_encode",
-            "dfssm_density_field_decode", "dfssm_density_field_requantize")
+            "dfssm_density_field_decode", "dfssm_density_field_requantize", "dfssm_int8_gemm",
+            "dfssm_cross_entropy_workspace_bytes", "dfssm_cross_entropy",
+            "dfssm_cross_entropy_backward_workspace_bytes", "dfssm_cross_entropy_backward",
+            "dfssm_embedding_lookup_scaled", "dfssm_embedding_backward_workspace_bytes", "dfssm_embedding_backward")
+
+# dfssm_type: the element type of a result or a gradient
+DFSSM_F32 = 0
+DFSSM_BF16 = 1
 
 DFSSM_DECODE_STATUS_TIMEOUT = 1
 DFSSM_DECODE_STATUS_GAVE_UP = 2
@@ -95,7 +102,18 @@ def _load():
         "dfssm_density_field_encode": [P, i64, i64, P, P, P],
         "dfssm_density_field_decode": [P, P, i64, i64, P, P],
         "dfssm_density_field_requantize": [P, i64, i64, P, P, P],
+        "dfssm_int8_gemm": [P, i64, P, i64, i64, i64, P, i64, P, P, i64, i32, P],
+        "dfssm_cross_entropy": [P, P, i64, i64, i64, P, P, P, P, P, P, ctypes.c_size_t, P],
+        "dfssm_cross_entropy_backward": [P, P, i64, i64, i64, P, P, P, P, P, P, P, i32, i32, P, ctypes.c_size_t, P],
+        "dfssm_embedding_lookup_scaled": [P, i64, P, P, i64, i64, ctypes.c_float, P, i64, i32, P],
+        "dfssm_embedding_backward": [P, i64, P, i64, i32, i64, i64, ctypes.c_float, P, i32, i32, P, ctypes.c_size_t,
+                                     P],
     }
+    for name, argtypes in (("dfssm_cross_entropy_workspace_bytes", [i64, i64, i64]),
+                           ("dfssm_cross_entropy_backward_workspace_bytes", [i64, i64, i64, i32, i32, i32]),
+                           ("dfssm_embedding_backward_workspace_bytes", [i64, i64, i64])):
+        getattr(lib, name).argtypes = argtypes
+        getattr(lib, name).restype = ctypes.c_size_t
     for name, argtypes in sigs.items():
         f = getattr(lib, name)
         f.argtypes = argtypes
@@ -336,3 +354,167 @@ def dfssm_density_field_requantize(state, field=None, scale=None, stream=None) -
     R, d = state.shape
     _call("dfssm_density_field_requantize", _ptr(state), R, d, _ptr(field), _ptr(scale), _stream(stream))
 
+
+
+# ---- operators with fp32 or bf16 results: these functions also check what the C ABI cannot see
+# (element types, shapes, strides, devices; ValueError) and run on the tensors' own device.
+
+def _type(what, t) -> int:
+    """dfssm_type of a tensor."""
+    import torch
+    if t.dtype is torch.float32:
+        return DFSSM_F32
+    if t.dtype is torch.bfloat16:
+        return DFSSM_BF16
+    raise ValueError(f"{what}: fp32 or bf16 expected, got {t.dtype}")
+
+
+def _rows(what, t, shape, dtype=None) -> int:
+    """Checks a matrix with contiguous rows; its row stride in elements."""
+    if t.shape != shape:
+        raise ValueError(f"{what}: shape {tuple(shape)} expected, got {tuple(t.shape)}")
+    if dtype is not None and t.dtype is not dtype:
+        raise ValueError(f"{what}: {dtype} expected, got {t.dtype}")
+    M, K = shape
+    sm, sk = t.stride()
+    if (sk != 1 and K > 1) or (sm < K and M > 1):
+        raise ValueError(f"{what}: rows must be contiguous and must not overlap, got strides {t.stride()}")
+    return sm if M > 1 else K
+
+
+def _dense(what, t, shape, dtype) -> None:
+    if t.shape != shape or t.dtype is not dtype or not t.is_contiguous():
+        raise ValueError(f"{what}: contiguous {dtype} {tuple(shape)} expected, got {t.dtype} {tuple(t.shape)} "
+                         f"with strides {t.stride()}")
+
+
+def _matrix(what, t) -> tuple:
+    if t.dim() != 2:
+        raise ValueError(f"{what}: a matrix expected, got shape {tuple(t.shape)}")
+    return t.shape
+
+
+def _run_on(name, tensors, stream, *args) -> None:
+    """Calls an entry point on the device that holds the tensors (and on its current stream)."""
+    import torch
+    dev = tensors[0].device
+    for t in tensors:
+        if t.device != dev or dev.type != "cuda":
+            raise ValueError(f"{name}: all tensors must be on one GPU, got {[str(t.device) for t in tensors]}")
+    if dev.index == torch.cuda.current_device():
+        _call(name, *args, _stream(stream))
+        return
+    with torch.cuda.device(dev):
+        _call(name, *args, _stream(stream))
+
+
+def _bytes(t) -> int:
+    if not t.is_contiguous():
+        raise ValueError("workspace: a contiguous tensor expected")
+    return t.numel() * t.element_size()
+
+
+def dfssm_int8_gemm(x_q, s_x, w, s_w, y, stream=None) -> None:
+    """y [M, N] (fp32 or bf16) = s_x (s_w (W x_q)) from x_q int8 [M, K], s_x [M], w int8 [N, K], s_w [N]; the rows
+    of x_q, w and y may be strided."""
+    import torch
+    M, K = _matrix("x_q", x_q)
+    N = _matrix("w", w)[0]
+    ldx, ldw = _rows("x_q", x_q, (M, K), torch.int8), _rows("w", w, (N, K), torch.int8)
+    ldy = _rows("y", y, (M, N))
+    _dense("s_x", s_x, (M,), torch.float32)
+    _dense("s_w", s_w, (N,), torch.float32)
+    _run_on("dfssm_int8_gemm", (x_q, s_x, w, s_w, y), stream, x_q.data_ptr(), ldx, s_x.data_ptr(), M, N, K,
+            w.data_ptr(), ldw, s_w.data_ptr(), y.data_ptr(), ldy, _type("y", y))
+
+
+def _head(x_q, s_x, e, s_e, targets) -> tuple:
+    """Checks the head's operands; (M, V, K)."""
+    import torch
+    M, K = _matrix("x_q", x_q)
+    V = _matrix("e", e)[0]
+    _dense("x_q", x_q, (M, K), torch.int8)
+    _dense("s_x", s_x, (M,), torch.float32)
+    _dense("e", e, (V, K), torch.int8)
+    _dense("s_e", s_e, (V,), torch.float32)
+    _dense("targets", targets, (M,), torch.int32)
+    return M, V, K
+
+
+def dfssm_cross_entropy_workspace_bytes(M: int, V: int, K: int) -> int:
+    return int(lib.dfssm_cross_entropy_workspace_bytes(M, V, K))
+
+
+def dfssm_cross_entropy(x_q, s_x, e, s_e, targets, loss, lse, workspace, stream=None) -> None:
+    """loss, lse fp32 [M] of the head's logits (x_q int8 [M, K], s_x [M], e int8 [V, K], s_e [V]) for the
+    int32 targets [M] (outside [0, V): the position does not count); workspace: a tensor of
+    dfssm_cross_entropy_workspace_bytes(M, V, K) bytes."""
+    import torch
+    M, V, K = _head(x_q, s_x, e, s_e, targets)
+    _dense("loss", loss, (M,), torch.float32)
+    _dense("lse", lse, (M,), torch.float32)
+    _run_on("dfssm_cross_entropy", (x_q, s_x, e, s_e, targets, loss, lse, workspace), stream, x_q.data_ptr(),
+            s_x.data_ptr(), M, V, K, e.data_ptr(), s_e.data_ptr(), targets.data_ptr(), loss.data_ptr(),
+            lse.data_ptr(), workspace.data_ptr(), _bytes(workspace))
+
+
+def dfssm_cross_entropy_backward_workspace_bytes(M: int, V: int, K: int, dx, de) -> int:
+    """For the gradients dx and de (tensors, or None for one that is not wanted)."""
+    t = _type("dx, de", de if dx is None else dx)
+    return int(lib.dfssm_cross_entropy_backward_workspace_bytes(M, V, K, t, dx is not None, de is not None))
+
+
+def dfssm_cross_entropy_backward(x_q, s_x, e, s_e, targets, lse, dloss, dx, de, workspace, accumulate: bool = False,
+                                 stream=None) -> None:
+    """dx [M, K] and de [V, K] (both fp32 or both bf16; None for one that is not wanted) from the forward
+    call's operands, its lse, and dloss fp32 [M]; accumulate adds to de.  workspace: a tensor of
+    dfssm_cross_entropy_backward_workspace_bytes(M, V, K, dx, de) bytes."""
+    import torch
+    M, V, K = _head(x_q, s_x, e, s_e, targets)
+    _dense("lse", lse, (M,), torch.float32)
+    _dense("dloss", dloss, (M,), torch.float32)
+    outs = [t for t in (dx, de) if t is not None]
+    if not outs:
+        raise ValueError("dfssm_cross_entropy_backward: dx or de expected")
+    t = _type("dx, de", outs[0])
+    if dx is not None:
+        _dense("dx", dx, (M, K), outs[0].dtype)
+    if de is not None:
+        _dense("de", de, (V, K), outs[0].dtype)
+    _run_on("dfssm_cross_entropy_backward", (x_q, s_x, e, s_e, targets, lse, dloss, workspace, *outs), stream,
+            x_q.data_ptr(), s_x.data_ptr(), M, V, K, e.data_ptr(), s_e.data_ptr(), targets.data_ptr(),
+            lse.data_ptr(), dloss.data_ptr(), _ptr(dx), _ptr(de), t, int(bool(accumulate)), workspace.data_ptr(),
+            _bytes(workspace))
+
+
+def dfssm_embedding_lookup_scaled(tokens, e, s_e, scale, out, stream=None) -> None:
+    """out [T, K] (fp32 or bf16, rows may be strided) = scale s_e[id] E[id] for the int32 ids `tokens` [T]
+    (ids outside [0, V): zeros)."""
+    import torch
+    V, K = _matrix("e", e)
+    T = tokens.numel()
+    _dense("tokens", tokens, (T,), torch.int32)
+    _dense("e", e, (V, K), torch.int8)
+    _dense("s_e", s_e, (V,), torch.float32)
+    ldo = _rows("out", out, (T, K))
+    _run_on("dfssm_embedding_lookup_scaled", (tokens, e, s_e, out), stream, tokens.data_ptr(), T, e.data_ptr(),
+            s_e.data_ptr(), V, K, float(scale), out.data_ptr(), ldo, _type("out", out))
+
+
+def dfssm_embedding_backward_workspace_bytes(T: int, V: int, K: int) -> int:
+    return int(lib.dfssm_embedding_backward_workspace_bytes(T, V, K))
+
+
+def dfssm_embedding_backward(tokens, dout, scale, de, workspace, accumulate: bool = False, stream=None) -> None:
+    """de [V, K] = scale times the sum of dout's rows (fp32 or bf16 [T, K], rows may be strided) of each id
+    of the int32 `tokens` [T]; accumulate adds to de instead (rows without tokens stay as they are).
+    workspace: a tensor of dfssm_embedding_backward_workspace_bytes(T, V, K) bytes."""
+    import torch
+    V, K = _matrix("de", de)
+    T = tokens.numel()
+    _dense("tokens", tokens, (T,), torch.int32)
+    ldd = _rows("dout", dout, (T, K))
+    _dense("de", de, (V, K), de.dtype)
+    _run_on("dfssm_embedding_backward", (tokens, dout, de, workspace), stream, tokens.data_ptr(), T, dout.data_ptr(),
+            ldd, _type("dout", dout), V, K, float(scale), de.data_ptr(), _type("de", de), int(bool(accumulate)),
+            workspace.data_ptr(), _bytes(workspace))

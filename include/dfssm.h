@@ -444,6 +444,115 @@ dfssm_status dfssm_density_field_decode(const uint32_t* field, const float* scal
 dfssm_status dfssm_density_field_requantize(float* state, int64_t rows, int64_t d_state, uint32_t* field,
                                             float* scale, hipStream_t stream);
 
+/* Element type of a result or a gradient. */
+typedef enum {
+    DFSSM_F32 = 0,
+    DFSSM_BF16 = 1               /* round to nearest even of the fp32 result */
+} dfssm_type;
+
+/*
+ * The int8 product of dfssm_int8_rowscale_gemm for any number of tokens, with row strides
+ * and an fp32 or bf16 result (the LM head over a whole prompt, or an int8 layer):
+ *   acc[m][n] = sum_k W[n][k] * x_q[m][k]        (exact int32)
+ *   y[m][n]   = s_x[m] * (s_w[n] * acc[m][n])    (fp32, then rounded to y_type)
+ *   x_q  int8 [M][K], row m at x_q + m*ldx;   s_x fp32 [M]
+ *   w    int8 [N][K], row n at w + n*ldw;     s_w fp32 [N]
+ *   y    y_type [M][N], row m at element m*ldy, written; elements past N of a row are left
+ * Any alignment of x_q and w, any K; rows whose start and stride are multiples of 16 bytes, with
+ * K % 16 == 0, are read fastest.  y needs its element's alignment (16 bytes and a row stride of 16
+ * bytes' multiple store fastest).  y must not overlap an input.
+ * Errors: DFSSM_ERR_INVALID_ARG for a NULL pointer, sizes <= 0 or >= 2^31, ldx or ldw < K, ldy < N,
+ * a type that is none, misaligned scales or y; DFSSM_ERR_UNSUPPORTED for K > 131072, ldx or ldw >
+ * 2^22, ldy >= 2^40, or more than 2^30 blocks of 32 x 32 outputs.
+ */
+dfssm_status dfssm_int8_gemm(const int8_t* x_q, int64_t ldx, const float* s_x, int64_t M, int64_t N, int64_t K,
+                             const int8_t* w, int64_t ldw, const float* s_w, void* y, int64_t ldy, int32_t y_type,
+                             hipStream_t stream);
+
+/*
+ * Softmax cross entropy of the int8 LM head, without the M x V logits in memory:
+ *   z[m][v] = s_x[m] * (s_e[v] * sum_k e[v][k] x_q[m][k])     (the head's logits)
+ *   lse[m]  = log sum_v exp(z[m][v])
+ *   loss[m] = lse[m] - z[m][targets[m]];  0 where targets[m] is outside [0, V) (a position that
+ *             does not count, such as -100; its lse is still written)
+ *   x_q int8 [M][K], s_x fp32 [M], e int8 [V][K], s_e fp32 [V], targets int32 [M] (read)
+ *   loss, lse fp32 [M] (written)
+ *   workspace  at least dfssm_cross_entropy_workspace_bytes(M, V, K) bytes, 16-byte aligned; its
+ *              contents need no preparation and mean nothing afterwards.  Calls that share one
+ *              must not overlap in time; graphs captured with one may be replayed in turn.
+ * x_q and e 16-byte aligned.  Scales must be finite.  Requires K % 16 == 0.  Sums are formed in fp32 in a
+ * fixed order: equal inputs give equal bits.
+ * Errors: DFSSM_ERR_INVALID_ARG for a NULL or misaligned pointer, sizes <= 0 or >= 2^31, K % 16 != 0, a
+ * short workspace; DFSSM_ERR_UNSUPPORTED for K > 131072 or more than 2^30 blocks of 32 tokens x 128 rows.
+ * The size query returns 0 for sizes that the call refuses.
+ */
+size_t dfssm_cross_entropy_workspace_bytes(int64_t M, int64_t V, int64_t K);
+dfssm_status dfssm_cross_entropy(const int8_t* x_q, const float* s_x, int64_t M, int64_t V, int64_t K,
+                                 const int8_t* e, const float* s_e, const int32_t* targets, float* loss, float* lse,
+                                 void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * Gradients of dfssm_cross_entropy for the dequantized values x = s_x x_q and E = s_e e (straight
+ * through the quantizers):
+ *   d[m][v]  = dloss[m] * (exp(z[m][v] - lse[m]) - [v == targets[m]]);  0 for positions that do not
+ *              count, whatever dloss holds there
+ *   dx[m][k] = sum_v d[m][v] * s_e[v] * e[v][k]
+ *   de[v][k] = sum_m d[m][v] * s_x[m] * x_q[m][k]     (added to what de holds if accumulate_de)
+ *   x_q, s_x, e, s_e, targets as in the forward call, lse [M] from it, dloss fp32 [M] (read)
+ *   dx  grad_type [M][K], or NULL;  de  grad_type [V][K], or NULL (a frozen matrix); not both NULL;
+ *       16-byte aligned, written (every row), overlapping nothing
+ *   workspace  at least dfssm_cross_entropy_backward_workspace_bytes(M, V, K, grad_type, dx != NULL,
+ *              de != NULL) bytes, 16-byte aligned, under the forward call's rules
+ * d enters the two products as bf16: for DFSSM_F32 gradients as two pieces (the rounded value and the
+ * rounded remainder, together within 2^-16 of d), for DFSSM_BF16 as one (2^-8); the codes are
+ * exact in bf16 and sums run in fp32 in a fixed order.
+ * Errors: as the forward call's; DFSSM_ERR_INVALID_ARG also for accumulate_de other than 0 and 1 or a
+ * type that is none, DFSSM_ERR_UNSUPPORTED also for M > 262144.
+ */
+size_t dfssm_cross_entropy_backward_workspace_bytes(int64_t M, int64_t V, int64_t K, int32_t grad_type,
+                                                    int32_t want_dx, int32_t want_de);
+dfssm_status dfssm_cross_entropy_backward(const int8_t* x_q, const float* s_x, int64_t M, int64_t V, int64_t K,
+                                          const int8_t* e, const float* s_e, const int32_t* targets, const float* lse,
+                                          const float* dloss, void* dx, void* de, int32_t grad_type,
+                                          int32_t accumulate_de, void* workspace, size_t workspace_bytes,
+                                          hipStream_t stream);
+
+/*
+ * dfssm_embedding_lookup with a factor, a row stride and an fp32 or bf16 result:
+ *   out[t][k] = (scale * s_e[id]) * E[id][k], id = tokens[t]   (fp32, then rounded to out_type);
+ *   zeros for an id outside [0, V)
+ *   tokens int32 [T], e int8 [V][K], s_e fp32 [V]; row t of out at element t*ldo (written; elements
+ *   past K are left)
+ * Errors: DFSSM_ERR_INVALID_ARG for a NULL or misaligned pointer, sizes <= 0 or >= 2^31, ldo < K, a type
+ * that is none; DFSSM_ERR_UNSUPPORTED for K > 131072 or ldo >= 2^31.
+ */
+dfssm_status dfssm_embedding_lookup_scaled(const int32_t* tokens, int64_t T, const int8_t* e, const float* s_e,
+                                           int64_t V, int64_t K, float scale, void* out, int64_t ldo,
+                                           int32_t out_type, hipStream_t stream);
+
+/*
+ * The embedding's gradient, for the dequantized matrix E = s_e e (straight through the quantizer):
+ *   de[v][k] = scale * sum over t with tokens[t] == v of dout[t][k]
+ * accumulate 0: every row of de is written (zeros where no token names it); 1: the sums are added
+ * to what de holds, and rows that no token names are left untouched.  So the tied matrix's gradient is
+ * dfssm_cross_entropy_backward into de, then this call with accumulate 1.
+ *   tokens int32 [T]; ids outside [0, V) take no part
+ *   dout dout_type [T][K], row t at element t*ldd;  de de_type [V][K] (16 bytes' alignment and K % 4 ==
+ *   0 are fastest)
+ *   workspace  at least dfssm_embedding_backward_workspace_bytes(T, V, K) bytes, 16-byte aligned,
+ *              under dfssm_cross_entropy's rules
+ * The tokens are sorted; a row's sum runs over its tokens in order, in fp32: equal inputs give
+ * equal bits.
+ * Errors: DFSSM_ERR_INVALID_ARG for a NULL or misaligned pointer, sizes <= 0 or >= 2^31, ldd < K, a type
+ * that is none, accumulate other than 0 and 1, a short workspace; DFSSM_ERR_UNSUPPORTED for T > 2^24,
+ * K > 131072 or ldd >= 2^31.  The size query returns 0 for sizes that the call refuses.
+ */
+size_t dfssm_embedding_backward_workspace_bytes(int64_t T, int64_t V, int64_t K);
+dfssm_status dfssm_embedding_backward(const int32_t* tokens, int64_t T, const void* dout, int64_t ldd,
+                                      int32_t dout_type, int64_t V, int64_t K, float scale, void* de,
+                                      int32_t de_type, int32_t accumulate, void* workspace, size_t workspace_bytes,
+                                      hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -71,26 +71,31 @@ __global__ __launch_bounds__(C::NT, C::NT / 256) void grad_gemm_kernel(GradGemmA
     const int boff = bcol < cols ? (int)(brow * a.ldb) + bcol : kLoadDead;
     const int bstep = bcol < cols ? (int)((C::NT / TB) * a.ldb) : 0;
     v4i va[PA], vb[PB];
-    auto load = [&](int c) {
-        const bool live = c < c1;
-        const int ao = aoff + c * 128;
-#pragma unroll
-        for (int j = 0; j < PA; ++j)
-            va[j] = __builtin_amdgcn_raw_buffer_load_b128(ar, live ? ao + j * astep : kLoadDead, 0, 0);
-        const int64_t left = live ? a.R - (int64_t)c * kR : 0;
+    // Chunk c's source, past the split's end nothing: piece by piece, A's pieces first.
+    auto a_offset = [&](int c) { return c < c1 ? aoff + c * 128 : kLoadDead; };
+    auto b_rows = [&](int c) {
+        const int64_t left = c < c1 ? a.R - (int64_t)c * kR : 0;
         const int br = (int)(left < kR ? left : kR);
-        const __amdgpu_buffer_rsrc_t rb =
-            make_rsrc(a.b + (live ? (int64_t)c * kR * a.ldb : 0) + j0, br > 0 ? (uint32_t)((br - 1) * a.ldb + cols) : 0u);
-#pragma unroll
-        for (int j = 0; j < PB; ++j) vb[j] = __builtin_amdgcn_raw_buffer_load_b128(rb, boff + j * bstep, 0, 0);
+        return make_rsrc(a.b + (c < c1 ? (int64_t)c * kR * a.ldb : 0) + j0, br > 0 ? (uint32_t)((br - 1) * a.ldb + cols) : 0u);
     };
-    auto store = [&](uint8_t* buf) {
+    auto load_a = [&](int j, int off) { va[j] = __builtin_amdgcn_raw_buffer_load_b128(ar, off + j * astep, 0, 0); };
+    auto load_b = [&](int j, __amdgpu_buffer_rsrc_t rb) {
+        vb[j] = __builtin_amdgcn_raw_buffer_load_b128(rb, boff + j * bstep, 0, 0);
+    };
+    auto store_a = [&](int j, uint8_t* buf) {
+        *reinterpret_cast<v4i*>(buf + (arow + j * (C::NT / 8)) * 128 + ((apiece ^ ((arow >> 1) & 7)) << 4)) = va[j];
+    };
+    auto store_b = [&](int j, uint8_t* buf) {
+        *reinterpret_cast<v4i*>(buf + kA + (brow + j * (C::NT / TB)) * kLdB + bcol) = vb[j];
+    };
+    // the pieces that step s of a chunk stages
+    auto for_pieces = [&](int s, auto fa, auto fb) {
 #pragma unroll
         for (int j = 0; j < PA; ++j)
-            *reinterpret_cast<v4i*>(buf + (arow + j * (C::NT / 8)) * 128 + ((apiece ^ (arow & 7)) << 4)) = va[j];
+            if (j * 4 / PA == s) fa(j);
 #pragma unroll
         for (int j = 0; j < PB; ++j)
-            *reinterpret_cast<v4i*>(buf + kA + (brow + j * (C::NT / TB)) * kLdB + bcol) = vb[j];
+            if (j * 4 / PB == s) fb(j);
     };
 
     v16f acc[C::MB][C::NB];
@@ -101,47 +106,143 @@ __global__ __launch_bounds__(C::NT, C::NT / 256) void grad_gemm_kernel(GradGemmA
 #pragma unroll
             for (int v = 0; v < 16; ++v) acc[x][y][v] = 0.0f;
 
-    const int sw7 = l32 & 7;
+    const int sw7 = (l32 >> 1) & 7;
     const uint8_t* const afrag = lds + (wm * C::MB * 32 + l32) * 128;
     // lane's source chunk of the transposing read: row 8 g + l16 / 2, columns 16 (group & 1) + 8 (l16 & 1)
     uint8_t* const bfrag =
         lds + kA + (8 * g + (l16 >> 1)) * kLdB + wn * C::NB * 32 + ((lane >> 4) & 1) * 16 + (l16 & 1) * 8;
 
-    load(c0);
-    store(lds);
-    load(c0 + 1);
+    // step s of a chunk: 16 r of one piece of A with the fragments of B it needs
+    struct Frags {
+        v8bf a[C::MB];
+    };
+    auto read_a = [&](int cur, int p, int s, Frags& f) {
+        const int piece = (P == 1 ? 0 : 4 * p) + 2 * s + g;
+#pragma unroll
+        for (int x = 0; x < C::MB; ++x)
+            f.a[x] = *reinterpret_cast<const v8bf*>(afrag + cur + x * 32 * 128 + ((piece ^ sw7) << 4));
+    };
+    auto read_b = [&](int cur, int s, v2i (&w)[C::NB]) {
+#pragma unroll
+        for (int y = 0; y < C::NB; ++y)
+            w[y] = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
+                (__attribute__((address_space(3))) v2i*)(bfrag + cur + s * 16 * kLdB + y * 32));
+    };
+    auto convert = [&](const v2i (&w)[C::NB], v8bf (&fb)[C::NB]) {
+#pragma unroll
+        for (int y = 0; y < C::NB; ++y) {
+            uint32_t p0, p1, p2, p3;
+            codes4_bf16(w[y].x, p0, p1);
+            codes4_bf16(w[y].y, p2, p3);
+            fb[y] = __builtin_bit_cast(v8bf, (v4u){p0, p1, p2, p3});
+        }
+    };
+    auto multiply = [&](const Frags& f, const v8bf (&fb)[C::NB]) {
+#pragma unroll
+        for (int x = 0; x < C::MB; ++x)
+#pragma unroll
+            for (int y = 0; y < C::NB; ++y)
+                acc[x][y] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f.a[x], fb[y], acc[x][y], 0, 0, 0);
+    };
+
+    for (int c = c0; c < c0 + 2; ++c) {
+        const int ao = a_offset(c);
+        const __amdgpu_buffer_rsrc_t rb = b_rows(c);
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {  // in the order of the loop's steps, so that its waits count right
+            for_pieces(s, [&](int j) { load_a(j, ao); }, [&](int j) { load_b(j, rb); });
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        if (c == c0)
+#pragma unroll
+            for (int s = 0; s < 4; ++s) for_pieces(s, [&](int j) { store_a(j, lds); }, [&](int j) { store_b(j, lds); });
+    }
+    // Four steps of MB x NB products a chunk: (s, piece) in the order 00 01 10 11, or four s with one piece.
+    // Between a step's products the next step's fragments are read and a quarter of the staging runs, one
+    // instruction at a time (a wave issues in order: a burst would hold back the products behind it).
+    Frags f0, f1;
+    v2i w0[C::NB], w1[C::NB];
+    v8bf fb[C::NB];
     for (int c = c0; c < c1; ++c) {
         lds_barrier();
         const int cur = ((c - c0) & 1) * kBuf, nxt = kBuf - cur;
-        store(lds + nxt);
-        load(c + 2);
+        const int ao = a_offset(c + 2);
+        const __amdgpu_buffer_rsrc_t rb = b_rows(c + 2);
+        auto at = [&](int i, Frags& f) {
+            if constexpr (P == 1) read_a(cur, 0, i, f);
+            else read_a(cur, i & 1, i >> 1, f);
+        };
+        auto stage = [&](int s) {
+            for_pieces(
+                s,
+                [&](int j) {
+                    store_a(j, lds + nxt);
+                    load_a(j, ao);
+                },
+                [&](int j) {
+                    store_b(j, lds + nxt);
+                    load_b(j, rb);
+                });
+        };
+        auto spread = [&]() {
 #pragma unroll
-        for (int s = 0; s < kR / 16; ++s) {
-            v8bf fb[C::NB];
-#pragma unroll
-            for (int y = 0; y < C::NB; ++y) {
-                const v2i w = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
-                    (__attribute__((address_space(3))) v2i*)(bfrag + cur + s * 16 * kLdB + y * 32));
-                v4u p;
-                uint32_t lo, hi;
-                codes4_bf16(w.x, lo, hi);
-                p.x = lo;
-                p.y = hi;
-                codes4_bf16(w.y, lo, hi);
-                p.z = lo;
-                p.w = hi;
-                fb[y] = __builtin_bit_cast(v8bf, p);
+            for (int i = 0; i < C::MB * C::NB; ++i) {
+                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // a product
+                __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);  // an LDS read
+                __builtin_amdgcn_sched_group_barrier(0x200, 1, 0);  // an LDS write
+                __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);  // a load
+                __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);  // conversions
             }
-#pragma unroll
-            for (int p = 0; p < P; ++p)
-#pragma unroll
-                for (int x = 0; x < C::MB; ++x) {
-                    const int piece = P == 1 ? 2 * s + g : 4 * p + 2 * s + g;
-                    const v8bf fa = *reinterpret_cast<const v8bf*>(afrag + cur + x * 32 * 128 + ((piece ^ sw7) << 4));
-#pragma unroll
-                    for (int y = 0; y < C::NB; ++y)
-                        acc[x][y] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa, fb[y], acc[x][y], 0, 0, 0);
-                }
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        read_b(cur, 0, w0);
+        at(0, f0);
+        if constexpr (P == 1) {
+            read_b(cur, 1, w1);
+            __builtin_amdgcn_sched_barrier(0);
+            convert(w0, fb);
+            v8bf fn[C::NB];
+            at(1, f1);
+            stage(0);
+            multiply(f0, fb);
+            convert(w1, fn);
+            read_b(cur, 2, w0);
+            spread();
+            at(2, f0);
+            stage(1);
+            multiply(f1, fn);
+            convert(w0, fb);
+            read_b(cur, 3, w1);
+            spread();
+            at(3, f1);
+            stage(2);
+            multiply(f0, fb);
+            convert(w1, fn);
+            spread();
+            stage(3);
+            multiply(f1, fn);
+            spread();
+        } else {
+            __builtin_amdgcn_sched_barrier(0);
+            convert(w0, fb);
+            at(1, f1);
+            read_b(cur, 1, w1);
+            stage(0);
+            multiply(f0, fb);
+            spread();
+            v8bf fn[C::NB];
+            at(2, f0);
+            stage(1);
+            multiply(f1, fb);
+            convert(w1, fn);
+            spread();
+            at(3, f1);
+            stage(2);
+            multiply(f0, fn);
+            spread();
+            stage(3);
+            multiply(f1, fn);
+            spread();
         }
     }
 

@@ -59,34 +59,39 @@ struct Stager {
             off0 = (int)(row0 * ld_);
         }
     }
-    __device__ __forceinline__ void load(int chunk, int K) {
+    // Piece j of a chunk: off = offset(chunk) first.
+    __device__ __forceinline__ int offset(int chunk, int K) const {
         const int k = chunk * kTileChunk + piece * 16;
+        if constexpr (kFast) return off0 + (k < K ? k : kTileDead);
+        return k;
+    }
+    __device__ __forceinline__ void load(int j, int off, int K) {
         if constexpr (kFast) {
-            const int off = off0 + (k < K ? k : kTileDead);
-            const int step = (int)(kRowStep * ld);
-#pragma unroll
-            for (int j = 0; j < P; ++j) {
-                const v4i r = __builtin_amdgcn_raw_buffer_load_b128(rsrc, off + j * step, 0, 0);
-                v[j] = make_uint4((uint32_t)r.x, (uint32_t)r.y, (uint32_t)r.z, (uint32_t)r.w);
-            }
+            const v4i r = __builtin_amdgcn_raw_buffer_load_b128(rsrc, off + j * (int)(kRowStep * ld), 0, 0);
+            v[j] = make_uint4((uint32_t)r.x, (uint32_t)r.y, (uint32_t)r.z, (uint32_t)r.w);
         } else {
-#pragma unroll
-            for (int j = 0; j < P; ++j) {
-                const int row = row0 + j * kRowStep;
-                uint4 r = make_uint4(0u, 0u, 0u, 0u);
-                if (row < rows && k < K) {
-                    const uint8_t* src = reinterpret_cast<const uint8_t*>(base) + row * ld + k;
-                    if (k + 16 <= K) __builtin_memcpy(&r, src, 16);
-                    else r = load16_guarded<false>(src, 0, K - k);
-                }
-                v[j] = r;
+            const int row = row0 + j * kRowStep;
+            uint4 r = make_uint4(0u, 0u, 0u, 0u);
+            if (row < rows && off < K) {
+                const uint8_t* src = reinterpret_cast<const uint8_t*>(base) + row * ld + off;
+                if (off + 16 <= K) __builtin_memcpy(&r, src, 16);
+                else r = load16_guarded<false>(src, 0, K - off);
             }
+            v[j] = r;
         }
     }
-    __device__ __forceinline__ void store(uint8_t* lds) const {
-        uint8_t* dst = lds + row0 * kTileChunk + ((piece ^ (row0 & 7)) << 4);
+    __device__ __forceinline__ void store(int j, uint8_t* lds) const {
+        *reinterpret_cast<uint4*>(lds + (row0 + j * kRowStep) * kTileChunk + ((piece ^ ((row0 >> 1) & 7)) << 4)) = v[j];
+    }
+    // All pieces of a chunk.
+    __device__ __forceinline__ void load_all(int chunk, int K) {
+        const int off = offset(chunk, K);
 #pragma unroll
-        for (int j = 0; j < P; ++j) *reinterpret_cast<uint4*>(dst + j * kRowStep * kTileChunk) = v[j];
+        for (int j = 0; j < P; ++j) load(j, off, K);
+    }
+    __device__ __forceinline__ void store_all(uint8_t* lds) const {
+#pragma unroll
+        for (int j = 0; j < P; ++j) store(j, lds);
     }
 };
 
@@ -116,36 +121,84 @@ __device__ __forceinline__ void tile_i8(const int8_t* __restrict__ w, int64_t ld
     constexpr int kXOff = C::BW * kTileChunk;
     const uint8_t* const wfrag = lds + (ww * C::WB * 32 + l32) * kTileChunk;
     const uint8_t* const xfrag = lds + kXOff + (tw * C::TB * 32 + l32) * kTileChunk;
-    const int sw7 = l32 & 7;
+    const int sw7 = (l32 >> 1) & 7;
 
-    sw.load(0, K);
-    st.load(0, K);
-    sw.store(lds);
-    st.store(lds + kXOff);
-    sw.load(1, K);
-    st.load(1, K);
+    sw.load_all(0, K);
+    st.load_all(0, K);
+    sw.store_all(lds);
+    st.store_all(lds + kXOff);
+    // in the order of the loop's steps: the waits for them then count only what lies between
+    const int ow1 = sw.offset(1, K), ot1 = st.offset(1, K);
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+#pragma unroll
+        for (int j = 0; j < C::PW; ++j)
+            if (j * 4 / C::PW == s) sw.load(j, ow1, K);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int j = 0; j < C::PT; ++j)
+            if (j * 4 / C::PT == s) st.load(j, ot1, K);
+        __builtin_amdgcn_sched_barrier(0);
+    }
+    struct Frags {
+        v4i w[C::WB], x[C::TB];
+    };
+    auto read = [&](int cur, int s, Frags& f) {
+        const int off = cur + (((2 * s + g) ^ sw7) << 4);
+#pragma unroll
+        for (int a = 0; a < C::WB; ++a) f.w[a] = *reinterpret_cast<const v4i*>(wfrag + off + a * 32 * kTileChunk);
+#pragma unroll
+        for (int b = 0; b < C::TB; ++b) f.x[b] = *reinterpret_cast<const v4i*>(xfrag + off + b * 32 * kTileChunk);
+    };
+    auto multiply = [&](const Frags& f) {
+#pragma unroll
+        for (int a = 0; a < C::WB; ++a)
+#pragma unroll
+            for (int b = 0; b < C::TB; ++b)
+                acc[a][b] = __builtin_amdgcn_mfma_i32_32x32x32_i8(f.w[a], f.x[b], acc[a][b], 0, 0, 0);
+    };
+    // One of a chunk's four steps: the products of `f`, and between them the reads of the next step's
+    // fragments and a quarter of the staging (registers to the other buffer, then the loads that refill
+    // them).  A wave issues in order, so a burst of LDS or memory instructions would hold back the
+    // products behind it; the pattern spreads them one by one over the products.
+    auto step = [&](int s, int cur, int nxt, int ow, int ot, const Frags& f, Frags* next) {
+        if (next) read(cur, s + 1, *next);
+#pragma unroll
+        for (int j = 0; j < C::PW; ++j)
+            if (j * 4 / C::PW == s) {
+                sw.store(j, lds + nxt);
+                sw.load(j, ow, K);
+            }
+#pragma unroll
+        for (int j = 0; j < C::PT; ++j)
+            if (j * 4 / C::PT == s) {
+                st.store(j, lds + nxt + kXOff);
+                st.load(j, ot, K);
+            }
+        multiply(f);
+        if constexpr (kFast) {
+#pragma unroll
+            for (int i = 0; i < C::WB * C::TB; ++i) {
+                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // a product
+                __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);  // an LDS read
+                __builtin_amdgcn_sched_group_barrier(0x200, 1, 0);  // an LDS write
+                __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);  // a load
+            }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    Frags f0, f1;
     for (int c = 0; c < nch; ++c) {
         lds_barrier();
         const int cur = (c & 1) * C::kBufBytes, nxt = C::kBufBytes - cur;
-        // (past the last chunk these are zeros that nothing reads)
-        sw.store(lds + nxt);
-        st.store(lds + nxt + kXOff);
-        sw.load(c + 2, K);
-        st.load(c + 2, K);
-#pragma unroll
-        for (int s = 0; s < 4; ++s) {
-            const int off = cur + (((2 * s + g) ^ sw7) << 4);
-            v4i fw[C::WB], fx[C::TB];
-#pragma unroll
-            for (int a = 0; a < C::WB; ++a) fw[a] = *reinterpret_cast<const v4i*>(wfrag + off + a * 32 * kTileChunk);
-#pragma unroll
-            for (int b = 0; b < C::TB; ++b) fx[b] = *reinterpret_cast<const v4i*>(xfrag + off + b * 32 * kTileChunk);
-#pragma unroll
-            for (int a = 0; a < C::WB; ++a)
-#pragma unroll
-                for (int b = 0; b < C::TB; ++b)
-                    acc[a][b] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fw[a], fx[b], acc[a][b], 0, 0, 0);
-        }
+        // (past the last chunk zeros are staged that nothing reads)
+        const int ow = sw.offset(c + 2, K), ot = st.offset(c + 2, K);
+        read(cur, 0, f0);
+        __builtin_amdgcn_sched_barrier(0);
+        step(0, cur, nxt, ow, ot, f0, &f1);
+        step(1, cur, nxt, ow, ot, f1, &f0);
+        step(2, cur, nxt, ow, ot, f0, &f1);
+        step(3, cur, nxt, ow, ot, f1, nullptr);
     }
 }
 

@@ -169,8 +169,41 @@ struct GradArgs {
     int64_t ldgx, ldgw;  // elements
 };
 
+// Two values rounded to bf16, the first in the low half.
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+    typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, (v2bf){(__bf16)a, (__bf16)b});
+}
+
+// Four values as bf16: the rounded values and, with two pieces, the rounded remainders.
+template <int P>
+__device__ __forceinline__ void split4(const float (&x)[4], uint2& hi, uint2& lo) {
+    hi = make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
+    if constexpr (P == 2)
+        lo = make_uint2(pack_bf16(x[0] - __uint_as_float(hi.x << 16), x[1] - __uint_as_float(hi.x & 0xFFFF0000u)),
+                        pack_bf16(x[2] - __uint_as_float(hi.y << 16), x[3] - __uint_as_float(hi.y & 0xFFFF0000u)));
+}
+
+// A 32 x 32 block of pieces from a wave's LDS block to memory: 16 bytes a lane, whole rows of 64 P bytes.
+template <int P>
+__device__ __forceinline__ void store_block(const uint8_t* blk, int ld_blk, uint16_t* dst, int64_t ld, int lane) {
+    constexpr int L = 4 * P;  // lanes per row
+#pragma unroll
+    for (int r = 0; r < 32; r += kWave / L) {
+        const int row = r + lane / L;
+        const v4i v = *reinterpret_cast<const v4i*>(blk + row * ld_blk + (lane % L) * 16);
+        *reinterpret_cast<v4i*>(dst + row * ld + (lane % L) * 8) = v;
+    }
+}
+
+// What lies past the vocabulary or the tokens inside the padded buffers is finite and meets zero codes
+// (or is not read) in the products.  Both forms of d go through LDS, so that memory is written in whole
+// rows of a block (64 P bytes): written from the registers, d s_x would go out in 2-byte stores.
 template <class C, int P>
 __global__ __launch_bounds__(C::NT, C::NT / 256) void grad_tile_kernel(GradArgs a) {
+    constexpr int kLd = 64 * P + 16;            // a block row in LDS
+    constexpr int kBlk = 2 * 32 * kLd;          // a wave's two blocks
+    static_assert(C::WW * C::TW * kBlk <= C::kLdsBytes, "the epilogue's blocks fit the tile's buffers");
     __shared__ __attribute__((aligned(16))) uint8_t lds[C::kLdsBytes];
     const TilePos pos = tile_pos(blockIdx.x, a.ntw, a.ntt);
     const int64_t n0 = (int64_t)pos.w * C::BW, m0 = (int64_t)pos.t * C::BT;
@@ -192,58 +225,65 @@ __global__ __launch_bounds__(C::NT, C::NT / 256) void grad_tile_kernel(GradArgs 
             const int r = wn + b * 32 + 8 * (v >> 2) + 4 * g + (v & 3);
             se[b][v] = a.s_e[n0 + (r < wrows ? r : wrows - 1)];
         }
+    lds_barrier();
+    uint8_t* const bx = lds + wave * kBlk;      // [token][vocabulary row]
+    uint8_t* const bw = bx + 32 * kLd;          // [vocabulary row][token]
 #pragma unroll
     for (int tb = 0; tb < C::TB; ++tb) {
         const int t = (tw * C::TB + tb) * 32 + l32;
         const int64_t m = m0 + (t < trows ? t : trows - 1);
-        const float sx = a.s_x[m], sx2 = sx * kLog2e, l2 = a.lse[m] * kLog2e;
         const int64_t target = a.targets[m];
         const bool counts = t < trows && target >= 0 && target < a.vocab;
-        const float dl = counts ? a.dloss[m] : 0.0f;
-        const int tl = (int)(target - a.v0 - n0 - wn);  // the target's row in the wave's range
+        const float sx2 = a.s_x[m] * kLog2e;
+        const float l2 = counts ? a.lse[m] * kLog2e : __builtin_inff();  // (exp 0 where the token does not count)
+        const float dl = counts ? a.dloss[m] : 0.0f, dlx = dl * a.s_x[m];
+        const int tl = counts ? (int)(target - a.v0 - n0 - wn) : -1;     // the target's row in the wave's range
 #pragma unroll
-        for (int b = 0; b < C::WB; ++b)
+        for (int b = 0; b < C::WB; ++b) {
+            float p[16];
+#pragma unroll
+            for (int v = 0; v < 16; ++v)
+                p[v] = __builtin_amdgcn_exp2f(__builtin_fmaf(se[b][v] * (float)acc[b][tb][v], sx2, -l2));
+            if (__ballot(tl >= b * 32 && tl < b * 32 + 32)) {
+#pragma unroll
+                for (int v = 0; v < 16; ++v)
+                    if (tl == b * 32 + 8 * (v >> 2) + 4 * g + (v & 3)) p[v] -= 1.0f;
+            }
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                float d[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int r = b * 32 + 8 * q + 4 * g + j;
-                    const float z = sx2 * (se[b][4 * q + j] * (float)acc[b][tb][4 * q + j]);
-                    float p = __builtin_amdgcn_exp2f(z - l2);
-                    if (r == tl) p -= 1.0f;
-                    d[j] = counts && wn + r < wrows ? dl * p : 0.0f;
-                }
-                const int64_t nb = n0 + wn + b * 32;  // first vocabulary row of the block
+                uint2 hi, lo;
+                float x[4];
                 if (a.gx) {
-                    uint32_t h[4], l[4];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float x = d[j] * se[b][4 * q + j];
-                        h[j] = bf16_bits(x);
-                        l[j] = P == 2 ? bf16_bits(x - __uint_as_float(h[j] << 16)) : 0u;
-                    }
-                    uint16_t* dst = a.gx + (m0 + t) * a.ldgx + nb * P + 8 * q + 4 * g;
-                    *reinterpret_cast<uint2*>(dst) = make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
-                    if constexpr (P == 2)
-                        *reinterpret_cast<uint2*>(dst + 32) = make_uint2(l[0] | (l[1] << 16), l[2] | (l[3] << 16));
+                    for (int j = 0; j < 4; ++j) x[j] = p[4 * q + j] * dl * se[b][4 * q + j];
+                    split4<P>(x, hi, lo);
+                    *reinterpret_cast<uint2*>(bx + l32 * kLd + (8 * q + 4 * g) * 2) = hi;
+                    if constexpr (P == 2) *reinterpret_cast<uint2*>(bx + l32 * kLd + 64 + (8 * q + 4 * g) * 2) = lo;
                 }
                 if (a.gw) {
-                    const int64_t mb = m0 + (tw * C::TB + tb) * 32;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) x[j] = p[4 * q + j] * dlx;
+                    split4<P>(x, hi, lo);
+                    uint8_t* const dst = bw + (8 * q + 4 * g) * kLd + l32 * 2;
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        const float x = d[j] * sx;
-                        const uint32_t h = bf16_bits(x);
-                        uint16_t* dst = a.gw + (nb + 8 * q + 4 * g + j) * a.ldgw + mb * P + l32;
-                        dst[0] = (uint16_t)h;
-                        if constexpr (P == 2) dst[32] = (uint16_t)bf16_bits(x - __uint_as_float(h << 16));
+                        *reinterpret_cast<uint16_t*>(dst + j * kLd) = (uint16_t)((j < 2 ? hi.x : hi.y) >> (16 * (j & 1)));
+                        if constexpr (P == 2)
+                            *reinterpret_cast<uint16_t*>(dst + j * kLd + 64) =
+                                (uint16_t)((j < 2 ? lo.x : lo.y) >> (16 * (j & 1)));
                     }
                 }
             }
+            wave_lds_order();
+            const int64_t nb = n0 + wn + b * 32, mb = m0 + (tw * C::TB + tb) * 32;  // the block's first row and token
+            if (a.gx) store_block<P>(bx, kLd, a.gx + mb * a.ldgx + nb * P, a.ldgx, lane);
+            if (a.gw) store_block<P>(bw, kLd, a.gw + nb * a.ldgw + mb * P, a.ldgw, lane);
+            wave_lds_order();
+        }
     }
 }
 
-// dx = the sum of its splits' slabs, rounded to its type.
+// dx = the sum of its slabs (one for each piece and split), rounded to its type.
 template <bool kBf16>
 __global__ __launch_bounds__(256) void slab_sum_kernel(const float* __restrict__ slabs, int splits, int64_t n,
                                                        void* __restrict__ out) {
@@ -271,7 +311,8 @@ struct Plan {
     int64_t Mp;      // tokens padded to the tile
     int64_t piece;   // vocabulary rows per piece, a multiple of 256
     int splits;      // of dx's sum over a piece
-    bool slabs;      // dx is summed in fp32 in the workspace
+    int slabs;       // fp32 slabs of dx in the workspace; 0: dx itself is the only one
+    bool add;        // the pieces add to the same slabs
     size_t gx, gw, dx, bytes;
 };
 
@@ -298,9 +339,14 @@ Plan make_plan(int64_t M, int64_t V, int64_t K, bool bf16, bool want_dx, bool wa
         int64_t s = 256 / tiles;
         if (s > p.piece / 512) s = p.piece / 512;
         p.splits = (int)(s < 1 ? 1 : s > 64 ? 64 : s);
-        p.slabs = bf16 || p.splits > 1;
+        // Each piece has slabs of its own, summed at the end: adding to a slab at the end of every piece's
+        // product costs more (all workgroups read and write at once, and nothing else runs).  Not past 512 MB.
+        const int64_t pieces = ceil_div(V, p.piece);
+        p.add = pieces > 1 && pieces * p.splits * M * K * 4 > ((int64_t)512 << 20);
+        p.slabs = (int)(p.add ? p.splits : pieces * p.splits);
+        if (p.slabs == 1 && !bf16) p.slabs = 0;
         p.gx = take((size_t)(p.Mp * p.piece * P * 2));
-        if (p.slabs) p.dx = take((size_t)p.splits * M * K * 4);
+        p.dx = take((size_t)p.slabs * M * K * 4);
     }
     if (want_de) p.gw = take((size_t)(p.piece * p.Mp * P * 2));
     p.bytes = at;
@@ -361,8 +407,9 @@ hipError_t launch_cross_entropy_backward(const int8_t* x_q, const float* s_x, in
                    de ? reinterpret_cast<uint16_t*>(ws + p.gw) : nullptr, p.piece * P, p.Mp * P};
         if (hipError_t err = P == 1 ? launch_grad_tiles<1>(g, stream) : launch_grad_tiles<2>(g, stream)) return err;
         if (dx) {
-            const GradGemmArgs a{ws + p.gx, p.piece * P * 2, g.e, K, M, K, rows,
-                                 p.slabs ? static_cast<void*>(ws + p.dx) : dx, K, M * K, p.splits, v0 > 0, false};
+            float* const slab = reinterpret_cast<float*>(ws + p.dx) + (p.add ? 0 : v0 / p.piece * p.splits * M * K);
+            const GradGemmArgs a{ws + p.gx, p.piece * P * 2, g.e, K, M, K, rows, p.slabs ? slab : dx, K, M * K, p.splits,
+                                 p.add && v0 > 0, false};
             if (hipError_t err = launch_grad_gemm(a, P, stream)) return err;
         }
         if (de) {
@@ -376,8 +423,8 @@ hipError_t launch_cross_entropy_backward(const int8_t* x_q, const float* s_x, in
         int64_t blocks = ceil_div(n, 1024);
         if (blocks > 2048) blocks = 2048;
         const float* slabs = reinterpret_cast<const float*>(ws + p.dx);
-        if (bf16) slab_sum_kernel<true><<<dim3((unsigned)blocks), 256, 0, stream>>>(slabs, p.splits, n, dx);
-        else slab_sum_kernel<false><<<dim3((unsigned)blocks), 256, 0, stream>>>(slabs, p.splits, n, dx);
+        if (bf16) slab_sum_kernel<true><<<dim3((unsigned)blocks), 256, 0, stream>>>(slabs, p.slabs, n, dx);
+        else slab_sum_kernel<false><<<dim3((unsigned)blocks), 256, 0, stream>>>(slabs, p.slabs, n, dx);
         return hipGetLastError();
     }
     return hipSuccess;

@@ -44,8 +44,8 @@ __global__ __launch_bounds__(C::NT, C::NT / 256) void grad_gemm_kernel(GradGemmA
     constexpr int PB = kR * C::BN / 16 / C::NT;
     constexpr int TB = C::BN / 16;          // threads per B row
     static_assert(PA * C::NT == C::BM * 8 && PB * C::NT * 16 == kR * C::BN && PB >= 1, "pieces split evenly");
-    static_assert(2 * kBuf <= 160 * 1024, "LDS");
-    __shared__ __attribute__((aligned(16))) uint8_t lds[2 * kBuf];
+    static_assert(3 * kBuf <= 160 * 1024, "LDS");
+    __shared__ __attribute__((aligned(16))) uint8_t lds[3 * kBuf];
 
     const int tid = threadIdx.x, lane = tid & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
@@ -145,7 +145,9 @@ __global__ __launch_bounds__(C::NT, C::NT / 256) void grad_gemm_kernel(GradGemmA
                 acc[x][y] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f.a[x], fb[y], acc[x][y], 0, 0, 0);
     };
 
-    for (int c = c0; c < c0 + 2; ++c) {
+    #pragma unroll
+    for (int i = 0; i < 3; ++i) {
+        const int c = c0 + i;
         const int ao = a_offset(c);
         const __amdgpu_buffer_rsrc_t rb = b_rows(c);
 #pragma unroll
@@ -153,34 +155,41 @@ __global__ __launch_bounds__(C::NT, C::NT / 256) void grad_gemm_kernel(GradGemmA
             for_pieces(s, [&](int j) { load_a(j, ao); }, [&](int j) { load_b(j, rb); });
             __builtin_amdgcn_sched_barrier(0);
         }
-        if (c == c0)
+        if (i < 2)
 #pragma unroll
-            for (int s = 0; s < 4; ++s) for_pieces(s, [&](int j) { store_a(j, lds); }, [&](int j) { store_b(j, lds); });
+            for (int s = 0; s < 4; ++s) for_pieces(s, [&](int j) { store_a(j, lds + i * kBuf); }, [&](int j) { store_b(j, lds + i * kBuf); });
     }
     // Four steps of MB x NB products a chunk: (s, piece) in the order 00 01 10 11, or four s with one piece.
     // Between a step's products the next step's fragments are read and a quarter of the staging runs, one
     // instruction at a time (a wave issues in order: a burst would hold back the products behind it).
+    // Three LDS buffers: one is computed from, the next is complete (its first fragments are read before the
+    // barrier, so the products go on right behind it), the third is written from the registers.
     Frags f0, f1;
     v2i w0[C::NB], w1[C::NB];
     v8bf fb[C::NB];
+    lds_barrier();
+    int cur = 0, nxt = kBuf, far = 2 * kBuf;
+    auto at = [&](int buf, int i, Frags& f) {
+        if constexpr (P == 1) read_a(buf, 0, i, f);
+        else read_a(buf, i & 1, i >> 1, f);
+    };
+    v8bf fn[C::NB];
+    at(0, 0, f0);
+    read_b(0, 0, w0);
+    if constexpr (P == 1) read_b(0, 1, w1);
+    convert(w0, fb);
     for (int c = c0; c < c1; ++c) {
-        lds_barrier();
-        const int cur = ((c - c0) & 1) * kBuf, nxt = kBuf - cur;
-        const int ao = a_offset(c + 2);
-        const __amdgpu_buffer_rsrc_t rb = b_rows(c + 2);
-        auto at = [&](int i, Frags& f) {
-            if constexpr (P == 1) read_a(cur, 0, i, f);
-            else read_a(cur, i & 1, i >> 1, f);
-        };
+        const int ao = a_offset(c + 3);
+        const __amdgpu_buffer_rsrc_t rb = b_rows(c + 3);
         auto stage = [&](int s) {
             for_pieces(
                 s,
                 [&](int j) {
-                    store_a(j, lds + nxt);
+                    store_a(j, lds + far);
                     load_a(j, ao);
                 },
                 [&](int j) {
-                    store_b(j, lds + nxt);
+                    store_b(j, lds + far);
                     load_b(j, rb);
                 });
         };
@@ -195,55 +204,59 @@ __global__ __launch_bounds__(C::NT, C::NT / 256) void grad_gemm_kernel(GradGemmA
             }
             __builtin_amdgcn_sched_barrier(0);
         };
-        read_b(cur, 0, w0);
-        at(0, f0);
+        __builtin_amdgcn_sched_barrier(0);
         if constexpr (P == 1) {
-            read_b(cur, 1, w1);
-            __builtin_amdgcn_sched_barrier(0);
-            convert(w0, fb);
-            v8bf fn[C::NB];
-            at(1, f1);
+            at(cur, 1, f1);
             stage(0);
             multiply(f0, fb);
             convert(w1, fn);
             read_b(cur, 2, w0);
             spread();
-            at(2, f0);
+            at(cur, 2, f0);
             stage(1);
             multiply(f1, fn);
             convert(w0, fb);
             read_b(cur, 3, w1);
             spread();
-            at(3, f1);
+            at(cur, 3, f1);
             stage(2);
             multiply(f0, fb);
             convert(w1, fn);
+            read_b(nxt, 0, w0);
             spread();
+            at(nxt, 0, f0);
             stage(3);
             multiply(f1, fn);
+            convert(w0, fb);
+            read_b(nxt, 1, w1);
             spread();
         } else {
-            __builtin_amdgcn_sched_barrier(0);
-            convert(w0, fb);
-            at(1, f1);
+            at(cur, 1, f1);
             read_b(cur, 1, w1);
             stage(0);
             multiply(f0, fb);
             spread();
-            v8bf fn[C::NB];
-            at(2, f0);
+            at(cur, 2, f0);
             stage(1);
             multiply(f1, fb);
             convert(w1, fn);
             spread();
-            at(3, f1);
+            at(cur, 3, f1);
             stage(2);
             multiply(f0, fn);
+            read_b(nxt, 0, w0);
             spread();
+            at(nxt, 0, f0);
             stage(3);
             multiply(f1, fn);
+            convert(w0, fb);
             spread();
         }
+        const int was = cur;
+        cur = nxt;
+        nxt = far;
+        far = was;
+        lds_barrier();
     }
 
 #pragma unroll

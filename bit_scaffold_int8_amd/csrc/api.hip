@@ -59,7 +59,7 @@ hipError_t launch_gemm_prefill(const int8_t* x_q, const float* s_x, int64_t M, i
 hipError_t launch_int8_gemm(const int8_t* x_q, int64_t ldx, const float* s_x, int64_t M, int64_t N, int64_t K,
                             const int8_t* w, int64_t ldw, const float* s_w, void* y, int64_t ldy, bool bf16,
                             hipStream_t stream);
-size_t cross_entropy_workspace_bytes(int64_t M, int64_t V);
+size_t cross_entropy_workspace_bytes(int64_t M, int64_t V, int64_t K);
 hipError_t launch_cross_entropy(const int8_t* x_q, const float* s_x, int64_t M, int64_t V, int64_t K, const int8_t* e,
                                 const float* s_e, const int32_t* targets, float* loss, float* lse, void* workspace,
                                 hipStream_t stream);
@@ -573,7 +573,7 @@ dfssm_status dfssm_int8_gemm(const int8_t* x_q, int64_t ldx, const float* s_x, i
 }
 
 size_t dfssm_cross_entropy_workspace_bytes(int64_t M, int64_t V, int64_t K) {
-    return loss_sizes(M, V, K) == DFSSM_OK ? dfssm::cross_entropy_workspace_bytes(M, V) : 0;
+    return loss_sizes(M, V, K) == DFSSM_OK ? dfssm::cross_entropy_workspace_bytes(M, V, K) : 0;
 }
 
 dfssm_status dfssm_cross_entropy(const int8_t* x_q, const float* s_x, int64_t M, int64_t V, int64_t K,
@@ -584,7 +584,7 @@ dfssm_status dfssm_cross_entropy(const int8_t* x_q, const float* s_x, int64_t M,
     if (!aligned16(x_q) || !aligned16(e) || !aligned16(workspace) || !aligned4(s_x) || !aligned4(s_e) ||
         !aligned4(targets) || !aligned4(loss) || !aligned4(lse))
         return DFSSM_ERR_INVALID_ARG;
-    if (workspace_bytes < dfssm::cross_entropy_workspace_bytes(M, V)) return DFSSM_ERR_INVALID_ARG;
+    if (workspace_bytes < dfssm::cross_entropy_workspace_bytes(M, V, K)) return DFSSM_ERR_INVALID_ARG;
     return dfssm::launch_cross_entropy(x_q, s_x, M, V, K, e, s_e, targets, loss, lse, workspace, stream) == hipSuccess
                ? DFSSM_OK
                : DFSSM_ERR_HIP;

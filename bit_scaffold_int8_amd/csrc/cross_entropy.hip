@@ -41,14 +41,14 @@ struct LossArgs {
 
 // ---------------------------------------------------------------- forward
 template <class C>
-__global__ __launch_bounds__(C::NT, C::NT / 256) void loss_tile_kernel(LossArgs a) {
+__global__ __launch_bounds__(C::NT, C::kMinWaves) void loss_tile_kernel(LossArgs a) {
     __shared__ __attribute__((aligned(16))) uint8_t lds[C::kLdsBytes];
     const TilePos pos = tile_pos(blockIdx.x, a.ntw, a.ntt);
     const int64_t n0 = (int64_t)pos.w * C::BW, m0 = (int64_t)pos.t * C::BT;
     const int wrows = (int)(a.V - n0 < C::BW ? a.V - n0 : C::BW);
     const int trows = (int)(a.M - m0 < C::BT ? a.M - m0 : C::BT);
     v16i acc[C::WB][C::TB];
-    tile_i8<C, true>(a.e + n0 * a.K, a.K, wrows, a.x_q + m0 * a.K, a.K, trows, a.K, lds, acc);
+    const bool holds = tile_i8<C, true>(a.e + n0 * a.K, a.K, wrows, a.x_q + m0 * a.K, a.K, trows, a.K, lds, acc);
 
     const int lane = threadIdx.x & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x / kWave));
@@ -67,7 +67,7 @@ __global__ __launch_bounds__(C::NT, C::NT / 256) void loss_tile_kernel(LossArgs 
     float2* const red = reinterpret_cast<float2*>(lds);  // [WW][BT]
     const float neg = -__builtin_inff();
 #pragma unroll
-    for (int tb = 0; tb < C::TB; ++tb) {
+    for (int tb = 0; tb < C::TB && holds; ++tb) {
         const int t = (tw * C::TB + tb) * 32 + l32;
         const float sx2 = a.s_x[m0 + (t < trows ? t : trows - 1)] * kLog2e;
         float z[C::WB][16], top = neg;
@@ -200,7 +200,8 @@ __device__ __forceinline__ void store_block(const uint8_t* blk, int ld_blk, uint
 // (or is not read) in the products.  Both forms of d go through LDS, so that memory is written in whole
 // rows of a block (64 P bytes): written from the registers, d s_x would go out in 2-byte stores.
 template <class C, int P>
-__global__ __launch_bounds__(C::NT, C::NT / 256) void grad_tile_kernel(GradArgs a) {
+__global__ __launch_bounds__(C::NT, C::kMinWaves) void grad_tile_kernel(GradArgs a) {
+    static_assert(C::KS == 1, "every wave holds its sums");
     constexpr int kLd = 64 * P + 16;            // a block row in LDS
     constexpr int kBlk = 2 * 32 * kLd;          // a wave's two blocks
     static_assert(C::WW * C::TW * kBlk <= C::kLdsBytes, "the epilogue's blocks fit the tile's buffers");
@@ -299,11 +300,6 @@ __global__ __launch_bounds__(256) void slab_sum_kernel(const float* __restrict__
     }
 }
 
-using Tile256 = TileI8<2, 4, 4, 2>;  // 256 rows x 256 tokens, 8 waves
-using Tile128 = TileI8<2, 2, 2, 2>;  // 128 x 128, 4 waves
-using Tile64 = TileI8<1, 2, 4, 1>;   // 128 x 64, 4 waves
-using Tile32 = TileI8<1, 1, 4, 1>;   // 128 x 32, 4 waves
-
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // How a backward call is cut and where its workspace lies; the size query and the call agree on it.
@@ -316,12 +312,14 @@ struct Plan {
     size_t gx, gw, dx, bytes;
 };
 
-int64_t token_tile(int64_t M) { return M <= 64 ? 64 : M <= 128 ? 128 : 256; }
+// The tile of the gradient kernel for a piece's rows: one of those with 64 tokens or more, so that the padded
+// tokens of d s_x fill whole chunks of the product (64 tokens) and are all written.
+int grad_tile(int64_t M, int64_t rows, int64_t K) { return pick_tile(rows, M, K, kTileKindsNoSplit); }
 
 Plan make_plan(int64_t M, int64_t V, int64_t K, bool bf16, bool want_dx, bool want_de) {
     const int64_t P = bf16 ? 1 : 2;
     Plan p{};
-    p.Mp = ceil_div(M, token_tile(M)) * token_tile(M);
+    p.Mp = ceil_div(M, 256) * 256;
     // pieces whose d stays in the 256 MB cache behind the L2s, but no fewer than 2048 rows
     const int64_t per_row = p.Mp * P * 2 * ((want_dx ? 1 : 0) + (want_de ? 1 : 0));
     int64_t piece = ((int64_t)256 << 20) / per_row;
@@ -355,36 +353,37 @@ Plan make_plan(int64_t M, int64_t V, int64_t K, bool bf16, bool want_dx, bool wa
 
 template <int P>
 hipError_t launch_grad_tiles(GradArgs a, hipStream_t stream) {
-    const int64_t bt = token_tile(a.M);
-    a.ntt = (int)ceil_div(a.M, bt);
-    a.ntw = (int)ceil_div(a.V, bt == 256 ? 256 : 128);
-    const dim3 grid((unsigned)(a.ntw * a.ntt));
-    if (bt == 256) grad_tile_kernel<Tile256, P><<<grid, Tile256::NT, 0, stream>>>(a);
-    else if (bt == 128) grad_tile_kernel<Tile128, P><<<grid, Tile128::NT, 0, stream>>>(a);
-    else grad_tile_kernel<Tile64, P><<<grid, Tile64::NT, 0, stream>>>(a);
-    return hipGetLastError();
+    return with_tile(grad_tile(a.M, a.V, a.K), [&](auto tile) {
+        using C = decltype(tile);
+        if constexpr (C::BT >= 64 && C::KS == 1) {
+            a.ntt = (int)ceil_div(a.M, C::BT);
+            a.ntw = (int)ceil_div(a.V, C::BW);
+            grad_tile_kernel<C, P><<<dim3((unsigned)(a.ntw * a.ntt)), C::NT, 0, stream>>>(a);
+            return hipGetLastError();
+        } else {
+            return hipErrorInvalidValue;
+        }
+    });
 }
-
-int64_t loss_row_tile(int64_t M) { return M <= 256 ? 128 : 256; }
 
 }  // namespace
 
-size_t cross_entropy_workspace_bytes(int64_t M, int64_t V) {
-    return (size_t)(ceil_div(V, loss_row_tile(M)) * M) * sizeof(float2);
+size_t cross_entropy_workspace_bytes(int64_t M, int64_t V, int64_t K) {
+    return (size_t)(ceil_div(V, tile_shape(pick_tile(V, M, K)).rows) * M) * sizeof(float2);
 }
 
 hipError_t launch_cross_entropy(const int8_t* x_q, const float* s_x, int64_t M, int64_t V, int64_t K, const int8_t* e,
                                 const float* s_e, const int32_t* targets, float* loss, float* lse, void* workspace,
                                 hipStream_t stream) {
     LossArgs a{x_q, s_x, M, V, (int)K, 0, 0, e, s_e, static_cast<float2*>(workspace)};
-    a.ntw = (int)ceil_div(V, loss_row_tile(M));
-    const int64_t bt = M <= 32 ? 32 : M <= 256 ? 128 : 256;
-    a.ntt = (int)ceil_div(M, bt);
-    const dim3 grid((unsigned)((int64_t)a.ntw * a.ntt));
-    if (bt == 32) loss_tile_kernel<Tile32><<<grid, Tile32::NT, 0, stream>>>(a);
-    else if (bt == 128) loss_tile_kernel<Tile128><<<grid, Tile128::NT, 0, stream>>>(a);
-    else loss_tile_kernel<Tile256><<<grid, Tile256::NT, 0, stream>>>(a);
-    if (hipError_t err = hipGetLastError()) return err;
+    const hipError_t err = with_tile(pick_tile(V, M, K), [&](auto tile) {
+        using C = decltype(tile);
+        a.ntw = (int)ceil_div(V, C::BW);
+        a.ntt = (int)ceil_div(M, C::BT);
+        loss_tile_kernel<C><<<dim3((unsigned)((int64_t)a.ntw * a.ntt)), C::NT, 0, stream>>>(a);
+        return hipGetLastError();
+    });
+    if (err) return err;
     loss_join_kernel<<<dim3((unsigned)ceil_div(M, 16)), 1024, 0, stream>>>(a, targets, loss, lse);
     return hipGetLastError();
 }

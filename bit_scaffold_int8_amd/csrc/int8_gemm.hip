@@ -23,11 +23,12 @@ struct GemmArgs {
     int64_t ldy;
     int64_t M, N;
     int K, ntw, ntt;
+    bool vec;
 };
 
-// kVec: y and its rows are 16-byte aligned, so four outputs go out together.
-template <class C, bool kFast, bool kBf16, bool kVec>
-__global__ __launch_bounds__(C::NT, C::NT / 256 > 0 ? C::NT / 256 : 1) void int8_gemm_kernel(GemmArgs a) {
+// vec: y and its rows are 16-byte aligned, so four outputs go out together.
+template <class C, bool kFast, bool kBf16>
+__global__ __launch_bounds__(C::NT, C::kMinWaves) void int8_gemm_kernel(GemmArgs a) {
     constexpr int kLd = C::WB * 32 + 4;  // floats per token row of a wave's LDS block
     constexpr int kEpi = C::WW * C::TW * 32 * kLd * 4;
     __shared__ __attribute__((aligned(16))) uint8_t lds[C::kLdsBytes > kEpi ? C::kLdsBytes : kEpi];
@@ -36,7 +37,7 @@ __global__ __launch_bounds__(C::NT, C::NT / 256 > 0 ? C::NT / 256 : 1) void int8
     const int wrows = (int)(a.N - n0 < C::BW ? a.N - n0 : C::BW);
     const int trows = (int)(a.M - m0 < C::BT ? a.M - m0 : C::BT);
     v16i acc[C::WB][C::TB];
-    tile_i8<C, kFast>(a.w + n0 * a.ldw, a.ldw, wrows, a.x_q + m0 * a.ldx, a.ldx, trows, a.K, lds, acc);
+    const bool holds = tile_i8<C, kFast>(a.w + n0 * a.ldw, a.ldw, wrows, a.x_q + m0 * a.ldx, a.ldx, trows, a.K, lds, acc);
 
     const int lane = threadIdx.x & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x / kWave));
@@ -45,6 +46,7 @@ __global__ __launch_bounds__(C::NT, C::NT / 256 > 0 ? C::NT / 256 : 1) void int8
     const int wn = ww * C::WB * 32;            // the wave's first weight row in the tile
     const int live_n = wrows - wn;             // outputs of a token that exist in the wave's range
     lds_barrier();
+    if (!holds) return;  // (no barrier follows)
     float* const blk = reinterpret_cast<float*>(lds) + wave * 32 * kLd;
     // the lane's row scales: rows past N are clamped (their outputs are not stored)
     float sw[C::WB][16];
@@ -78,7 +80,7 @@ __global__ __launch_bounds__(C::NT, C::NT / 256 > 0 ? C::NT / 256 : 1) void int8
             const v4f o = *reinterpret_cast<const v4f*>(blk + tr * kLd + c);
             if (t0 + tr < trows && c < live_n) {
                 const int64_t at = (m0 + t0 + tr) * a.ldy + n0 + wn + c;
-                if (kVec && c + 4 <= live_n) {
+                if (a.vec && c + 4 <= live_n) {
                     if constexpr (kBf16) {
                         uint2 p;
                         p.x = bf16_bits(o.x) | (bf16_bits(o.y) << 16);
@@ -101,22 +103,16 @@ __global__ __launch_bounds__(C::NT, C::NT / 256 > 0 ? C::NT / 256 : 1) void int8
     }
 }
 
-template <class C, bool kFast, bool kBf16>
-hipError_t launch_c(GemmArgs a, bool vec, hipStream_t stream) {
-    a.ntw = (int)((a.N + C::BW - 1) / C::BW);
-    a.ntt = (int)((a.M + C::BT - 1) / C::BT);
-    const dim3 grid((unsigned)((int64_t)a.ntw * a.ntt));
-    if (vec) int8_gemm_kernel<C, kFast, kBf16, true><<<grid, C::NT, 0, stream>>>(a);
-    else int8_gemm_kernel<C, kFast, kBf16, false><<<grid, C::NT, 0, stream>>>(a);
-    return hipGetLastError();
-}
-
 template <bool kFast, bool kBf16>
-hipError_t launch_f(const GemmArgs& a, bool vec, hipStream_t stream) {
-    const int64_t big = ((a.N + 255) / 256) * ((a.M + 255) / 256);
-    if (a.M <= 32) return launch_c<TileI8<1, 1, 4, 1>, kFast, kBf16>(a, vec, stream);
-    if (big >= 256) return launch_c<TileI8<2, 4, 4, 2>, kFast, kBf16>(a, vec, stream);
-    return launch_c<TileI8<2, 2, 2, 2>, kFast, kBf16>(a, vec, stream);
+hipError_t launch_tiles(GemmArgs a, hipStream_t stream) {
+    return with_tile(pick_tile(a.N, a.M, a.K), [&](auto tile) {
+        using C = decltype(tile);
+        a.ntw = (int)((a.N + C::BW - 1) / C::BW);
+        a.ntt = (int)((a.M + C::BT - 1) / C::BT);
+        const dim3 grid((unsigned)((int64_t)a.ntw * a.ntt));
+        int8_gemm_kernel<C, kFast, kBf16><<<grid, C::NT, 0, stream>>>(a);
+        return hipGetLastError();
+    });
 }
 
 }  // namespace
@@ -124,12 +120,11 @@ hipError_t launch_f(const GemmArgs& a, bool vec, hipStream_t stream) {
 hipError_t launch_int8_gemm(const int8_t* x_q, int64_t ldx, const float* s_x, int64_t M, int64_t N, int64_t K,
                             const int8_t* w, int64_t ldw, const float* s_w, void* y, int64_t ldy, bool bf16,
                             hipStream_t stream) {
-    const GemmArgs a{x_q, ldx, s_x, w, ldw, s_w, y, ldy, M, N, (int)K, 0, 0};
     auto al16 = [](const void* p) { return ((uintptr_t)p & 15u) == 0; };
     const bool fast = al16(x_q) && al16(w) && ldx % 16 == 0 && ldw % 16 == 0 && K % 16 == 0;
-    const bool vec = al16(y) && ldy % (bf16 ? 8 : 4) == 0;
-    if (fast) return bf16 ? launch_f<true, true>(a, vec, stream) : launch_f<true, false>(a, vec, stream);
-    return bf16 ? launch_f<false, true>(a, vec, stream) : launch_f<false, false>(a, vec, stream);
+    const GemmArgs a{x_q, ldx, s_x, w, ldw, s_w, y, ldy, M, N, (int)K, 0, 0, al16(y) && ldy % (bf16 ? 8 : 4) == 0};
+    if (fast) return bf16 ? launch_tiles<true, true>(a, stream) : launch_tiles<true, false>(a, stream);
+    return bf16 ? launch_tiles<false, true>(a, stream) : launch_tiles<false, false>(a, stream);
 }
 
 }  // namespace dfssm

@@ -23,17 +23,20 @@ constexpr int kTileChunk = 128;               // k bytes per chunk
 constexpr int kTileDead = 0x40000000;         // a load offset past every tile's resource: reads zero
 constexpr int64_t kTileMaxLd = (int64_t)1 << 22;  // row stride limit: 256 rows stay below kTileDead
 
-// WW x TW waves; each owns WB x TB blocks of 32 x 32.
-template <int WB_, int TB_, int WW_, int TW_>
+// WW x TW waves, each with WB x TB blocks of 32 x 32; KS such groups of waves take every KS-th chunk of K each and
+// add up their sums through LDS (small tiles: they are used where there are few, and K's length is the time).
+template <int WB_, int TB_, int WW_, int TW_, int KS_ = 1>
 struct TileI8 {
-    static constexpr int WB = WB_, TB = TB_, WW = WW_, TW = TW_;
+    static constexpr int WB = WB_, TB = TB_, WW = WW_, TW = TW_, KS = KS_;
     static constexpr int BW = 32 * WB * WW, BT = 32 * TB * TW;
-    static constexpr int NT = kWave * WW * TW;
-    static constexpr int PW = BW * 8 / NT, PT = BT * 8 / NT;  // 16-byte pieces per thread per chunk
+    static constexpr int NG = kWave * WW * TW, NT = NG * KS;  // threads of a K group, of the workgroup
+    static constexpr int PW = BW * 8 / NG, PT = BT * 8 / NG;  // 16-byte pieces per thread per chunk
     static constexpr int kBufBytes = (BW + BT) * kTileChunk;
-    static constexpr int kLdsBytes = 2 * kBufBytes;
-    static_assert(PW * NT == BW * 8 && PT * NT == BT * 8, "pieces split evenly over the threads");
-    static_assert(NT % 64 == 0 && BW <= 256 && BT <= 256, "tile sizes");
+    static constexpr int kLdsBytes = 2 * kBufBytes * KS;
+    static constexpr int kMinWaves = NT >= 256 ? NT / 256 : 1;  // per SIMD, for one workgroup on a CU
+    static_assert(PW * NG == BW * 8 && PT * NG == BT * 8, "pieces split evenly over the threads");
+    static_assert(NT <= 512 && BW <= 256 && BT <= 256, "tile sizes");
+    static_assert((KS - 1) * WB * TB * 16 * NG * 4 <= kLdsBytes, "the K groups' sums fit the buffers");
 };
 
 // Pieces of one operand's chunk for one thread.  kFast: base and row stride are multiples of 16
@@ -42,6 +45,7 @@ struct TileI8 {
 // where a piece crosses the row's end.
 template <bool kFast, int P, int kRowStep>
 struct Stager {
+    static_assert(kRowStep % 2 == 0, "the rows of a thread's pieces differ by whole pairs");
     __amdgpu_buffer_rsrc_t rsrc;
     const int8_t* base;
     int64_t ld;
@@ -81,7 +85,7 @@ struct Stager {
         }
     }
     __device__ __forceinline__ void store(int j, uint8_t* lds) const {
-        *reinterpret_cast<uint4*>(lds + (row0 + j * kRowStep) * kTileChunk + ((piece ^ ((row0 >> 1) & 7)) << 4)) = v[j];
+        *reinterpret_cast<uint4*>(lds + (row0 + j * kRowStep) * kTileChunk + ((piece ^ (((row0 >> 1) + j * kRowStep / 2 % 8) & 7)) << 4)) = v[j];
     }
     // All pieces of a chunk.
     __device__ __forceinline__ void load_all(int chunk, int K) {
@@ -97,19 +101,22 @@ struct Stager {
 
 // The tile's accumulators.  w, x: the tile's first rows; wrows, trows: rows of them that exist
 // (the others read zero).  Every thread of the group calls it; LDS is free again after the
-// caller's next barrier.
+// caller's next barrier.  Returns whether this wave holds the sums (the first K group's do).
 template <class C, bool kFast>
-__device__ __forceinline__ void tile_i8(const int8_t* __restrict__ w, int64_t ldw, int wrows,
+__device__ __forceinline__ bool tile_i8(const int8_t* __restrict__ w, int64_t ldw, int wrows,
                                         const int8_t* __restrict__ x, int64_t ldx, int trows, int K,
                                         uint8_t* __restrict__ lds, v16i (&acc)[C::WB][C::TB]) {
-    const int tid = threadIdx.x;
-    const int lane = tid & (kWave - 1);
-    const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+    const int lane = threadIdx.x & (kWave - 1);
+    const int wave_wg = __builtin_amdgcn_readfirstlane((int)(threadIdx.x / kWave));
+    const int kg = wave_wg / (C::WW * C::TW), wave = wave_wg % (C::WW * C::TW);
+    const int tid = wave * kWave + lane;  // thread within the K group
     const int ww = wave % C::WW, tw = wave / C::WW;
     const int l32 = lane & 31, g = lane >> 5;
+    uint8_t* const all_lds = lds;
+    lds += kg * 2 * C::kBufBytes;
 
-    Stager<kFast, C::PW, C::NT / 8> sw;
-    Stager<kFast, C::PT, C::NT / 8> st;
+    Stager<kFast, C::PW, C::NG / 8> sw;
+    Stager<kFast, C::PT, C::NG / 8> st;
     sw.init(w, ldw, wrows, K, tid);
     st.init(x, ldx, trows, K, tid);
 #pragma unroll
@@ -117,18 +124,19 @@ __device__ __forceinline__ void tile_i8(const int8_t* __restrict__ w, int64_t ld
 #pragma unroll
         for (int b = 0; b < C::TB; ++b) acc[a][b] = (v16i){0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
 
-    const int nch = (K + kTileChunk - 1) / kTileChunk;
+    // chunk i of this K group is chunk i KS + kg of K; every group takes the same number (past K: zeros)
+    const int nch = ((K + kTileChunk - 1) / kTileChunk + C::KS - 1) / C::KS;
     constexpr int kXOff = C::BW * kTileChunk;
     const uint8_t* const wfrag = lds + (ww * C::WB * 32 + l32) * kTileChunk;
     const uint8_t* const xfrag = lds + kXOff + (tw * C::TB * 32 + l32) * kTileChunk;
     const int sw7 = (l32 >> 1) & 7;
 
-    sw.load_all(0, K);
-    st.load_all(0, K);
+    sw.load_all(kg, K);
+    st.load_all(kg, K);
     sw.store_all(lds);
     st.store_all(lds + kXOff);
     // in the order of the loop's steps: the waits for them then count only what lies between
-    const int ow1 = sw.offset(1, K), ot1 = st.offset(1, K);
+    const int ow1 = sw.offset(C::KS + kg, K), ot1 = st.offset(C::KS + kg, K);
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
 #pragma unroll
@@ -192,13 +200,85 @@ __device__ __forceinline__ void tile_i8(const int8_t* __restrict__ w, int64_t ld
         lds_barrier();
         const int cur = (c & 1) * C::kBufBytes, nxt = C::kBufBytes - cur;
         // (past the last chunk zeros are staged that nothing reads)
-        const int ow = sw.offset(c + 2, K), ot = st.offset(c + 2, K);
+        const int ow = sw.offset((c + 2) * C::KS + kg, K), ot = st.offset((c + 2) * C::KS + kg, K);
         read(cur, 0, f0);
         __builtin_amdgcn_sched_barrier(0);
         step(0, cur, nxt, ow, ot, f0, &f1);
         step(1, cur, nxt, ow, ot, f1, &f0);
         step(2, cur, nxt, ow, ot, f0, &f1);
         step(3, cur, nxt, ow, ot, f1, nullptr);
+    }
+    if constexpr (C::KS > 1) {
+        int32_t* const sums = reinterpret_cast<int32_t*>(all_lds) + tid;
+        lds_barrier();
+#pragma unroll
+        for (int a = 0; a < C::WB; ++a)
+#pragma unroll
+            for (int b = 0; b < C::TB; ++b)
+#pragma unroll
+                for (int v = 0; v < 16; ++v)
+                    if (kg) sums[(((kg - 1) * C::WB * C::TB + a * C::TB + b) * 16 + v) * C::NG] = acc[a][b][v];
+        lds_barrier();
+#pragma unroll
+        for (int q = 0; q < C::KS - 1; ++q)
+#pragma unroll
+            for (int a = 0; a < C::WB; ++a)
+#pragma unroll
+                for (int b = 0; b < C::TB; ++b)
+#pragma unroll
+                    for (int v = 0; v < 16; ++v)
+                        if (!kg) acc[a][b][v] += sums[((q * C::WB * C::TB + a * C::TB + b) * 16 + v) * C::NG];
+    }
+    return kg == 0;
+}
+
+// ---- which tile a shape takes (host)
+
+enum TileKind { kTile256, kTile128, kTile128x64, kTile128x32, kTile64x64, kTile64x32, kTile32x32, kTileKinds };
+constexpr int kTileKindsNoSplit = kTile128x64 + 1;  // the first ones: 64 tokens or more, K not split
+
+struct TileShape {
+    int rows, tokens;
+    float fixed;        // us that do not grow with K
+    float first, more;  // us for up to 256 tiles, and for each further 256, at K = 2048
+};
+// Measured on 512 to 50280 rows x 1 to 2048 tokens, K 512 to 8192.  Large tiles reread least and win
+// when they fill the GPU (50280 rows x 512 tokens, K 2048: 61 us for the first, then 65, 74, 103); small ones win
+// when they do not (2048 rows x 1 token, K 4096, in this order: 39, 17, 12, 11, 9.5, 7.2, 6.1 us), or when the
+// large ones' last round would be nearly empty (8512 rows x 2048 tokens: 58 against 48 us for 128 x 128).
+inline const TileShape& tile_shape(int kind) {
+    static const TileShape t[kTileKinds] = {
+        {256, 256, 7.0f, 24.0f, 34.0f}, {128, 128, 4.1f, 10.7f, 9.0f}, {128, 64, 3.3f, 7.9f, 5.5f},
+        {128, 32, 2.9f, 6.8f, 4.0f},    {64, 64, 3.4f, 6.3f, 3.4f},    {64, 32, 3.6f, 5.4f, 2.35f},
+        {32, 32, 3.95f, 5.0f, 4.0f}};
+    return t[kind];
+}
+
+inline float tile_cost(int kind, int64_t rows, int64_t tokens, int64_t K) {
+    const TileShape& t = tile_shape(kind);
+    const int64_t n = ((rows + t.rows - 1) / t.rows) * ((tokens + t.tokens - 1) / t.tokens);
+    return t.fixed + (t.first - t.fixed + (float)((n - 1) / 256) * t.more) * ((float)K / 2048.0f);
+}
+
+// The cheapest of the first `kinds` tiles.
+inline int pick_tile(int64_t rows, int64_t tokens, int64_t K, int kinds = kTileKinds) {
+    int best = 0;
+    for (int k = 1; k < kinds; ++k)
+        if (tile_cost(k, rows, tokens, K) < tile_cost(best, rows, tokens, K)) best = k;
+    return best;
+}
+
+// f(Tile{}) for the tile of a kind.
+template <class F>
+auto with_tile(int kind, F f) {
+    switch (kind) {
+        case kTile256: return f(TileI8<2, 4, 4, 2>{});
+        case kTile128: return f(TileI8<2, 2, 2, 2>{});
+        case kTile128x64: return f(TileI8<1, 2, 4, 1>{});
+        case kTile128x32: return f(TileI8<1, 1, 4, 1>{});
+        case kTile64x64: return f(TileI8<1, 1, 2, 2, 2>{});
+        case kTile64x32: return f(TileI8<1, 1, 2, 1, 4>{});
+        default: return f(TileI8<1, 1, 1, 1, 8>{});
     }
 }
 

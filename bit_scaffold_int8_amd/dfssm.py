@@ -397,15 +397,20 @@ def _matrix(what, t) -> tuple:
 def _run_on(name, tensors, stream, *args) -> None:
     """Calls an entry point on the device that holds the tensors (and on its current stream)."""
     import torch
-    dev = tensors[0].device
+    dev = tensors[0].get_device()
     for t in tensors:
-        if t.device != dev or dev.type != "cuda":
+        if t.get_device() != dev or dev < 0:
             raise ValueError(f"{name}: all tensors must be on one GPU, got {[str(t.device) for t in tensors]}")
-    if dev.index == torch.cuda.current_device():
-        _call(name, *args, _stream(stream))
+    if stream is None:
+        # the current stream's handle without the Stream object, whose making takes longer than a launch
+        stream = torch._C._cuda_getCurrentRawStream(dev)
+    elif not isinstance(stream, int):
+        stream = stream.cuda_stream
+    if dev == torch.cuda.current_device():
+        _call(name, *args, stream)
         return
     with torch.cuda.device(dev):
-        _call(name, *args, _stream(stream))
+        _call(name, *args, stream)
 
 
 def _bytes(t) -> int:

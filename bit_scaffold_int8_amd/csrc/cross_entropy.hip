@@ -302,9 +302,13 @@ __global__ __launch_bounds__(256) void slab_sum_kernel(const float* __restrict__
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
+// The tile of the gradient kernel for a piece's rows: one of those with 64 tokens or more, so that the padded
+// tokens of d s_x fill whole chunks of the product (64 tokens) and are all written.
+int grad_tile(int64_t M, int64_t rows, int64_t K) { return pick_tile(rows, M, K, 0, kTileKindsNoSplit); }
+
 // How a backward call is cut and where its workspace lies; the size query and the call agree on it.
 struct Plan {
-    int64_t Mp;      // tokens padded to the tile
+    int64_t Mp;      // tokens padded to the largest tile
     int64_t piece;   // vocabulary rows per piece, a multiple of 256
     int splits;      // of dx's sum over a piece
     int slabs;       // fp32 slabs of dx in the workspace; 0: dx itself is the only one
@@ -312,20 +316,41 @@ struct Plan {
     size_t gx, gw, dx, bytes;
 };
 
-// The tile of the gradient kernel for a piece's rows: one of those with 64 tokens or more, so that the padded
-// tokens of d s_x fill whole chunks of the product (64 tokens) and are all written.
-int grad_tile(int64_t M, int64_t rows, int64_t K) { return pick_tile(rows, M, K, kTileKindsNoSplit); }
+constexpr int64_t kMaxSlabBytes = (int64_t)512 << 20, kMaxPieceBytes = (int64_t)512 << 20;
+
+// About how long a piece takes: its gradient tiles and its products (dx with the slabs it adds), and the launches.
+float piece_cost(int64_t M, int64_t rows, int64_t K, int P, bool want_dx, bool want_de) {
+    const float tiles = 1.35f * tile_cost(grad_tile(M, rows, K), rows, M, K);  // (the epilogue is the heavier one)
+    return tiles + (want_dx ? grad_shape(M, K, rows, P, 1, 64).cost : 0.0f) +
+           (want_de ? grad_shape(rows, K, M, P, 1, 1).cost : 0.0f) + 4.0f;
+}
 
 Plan make_plan(int64_t M, int64_t V, int64_t K, bool bf16, bool want_dx, bool want_de) {
-    const int64_t P = bf16 ? 1 : 2;
+    const int P = bf16 ? 1 : 2;
     Plan p{};
     p.Mp = ceil_div(M, 256) * 256;
-    // pieces whose d stays in the 256 MB cache behind the L2s, but no fewer than 2048 rows
+    // The longest piece whose d takes at most 512 MB (2048 rows at the least); among pieces up to it, the one that
+    // wastes least: pieces of equal length, and pieces whose tiles of de fill whole rounds of the 256 CUs, with
+    // a short last one (4096 tokens x 50280 rows: 6 rounds of 8192 rows and a rest instead of 7 of 7424).
     const int64_t per_row = p.Mp * P * 2 * ((want_dx ? 1 : 0) + (want_de ? 1 : 0));
-    int64_t piece = ((int64_t)256 << 20) / per_row;
-    if (piece < 2048) piece = 2048;
-    const int64_t n = ceil_div(V, piece);
-    p.piece = ceil_div(ceil_div(V, n), 256) * 256;
+    const int64_t all = ceil_div(V, 256);
+    int64_t most = kMaxPieceBytes / per_row / 256;
+    if (most < 8) most = 8;
+    if (most > all) most = all;
+    float best = 3.0e38f;
+    auto consider = [&](int64_t k) {
+        if (k < 1 || k > most || k < most / 4) return;
+        const int64_t rows = k * 256, full = V / rows, rest = V - full * rows;
+        const float cost = (float)full * piece_cost(M, rows, K, P, want_dx, want_de) +
+                           (rest ? piece_cost(M, rest, K, P, want_dx, want_de) : 0.0f);
+        if (cost < best) {
+            best = cost;
+            p.piece = rows;
+        }
+    };
+    const int64_t fewest = ceil_div(all, most), tj = ceil_div(K, 256);
+    for (int64_t n = fewest; n < fewest + 6; ++n) consider(ceil_div(all, n));
+    for (int64_t r = 1; r <= 4; ++r) consider(256 * r / tj);
     size_t at = 0;
     auto take = [&](size_t b) {
         const size_t was = at;
@@ -333,18 +358,16 @@ Plan make_plan(int64_t M, int64_t V, int64_t K, bool bf16, bool want_dx, bool wa
         return was;
     };
     if (want_dx) {
-        const int64_t tiles = grad_gemm_tiles(M, K);
-        int64_t s = 256 / tiles;
-        if (s > p.piece / 512) s = p.piece / 512;
-        p.splits = (int)(s < 1 ? 1 : s > 64 ? 64 : s);
         // Each piece has slabs of its own, summed at the end: adding to a slab at the end of every piece's
         // product costs more (all workgroups read and write at once, and nothing else runs).  Not past 512 MB.
-        const int64_t pieces = ceil_div(V, p.piece);
-        p.add = pieces > 1 && pieces * p.splits * M * K * 4 > ((int64_t)512 << 20);
+        const int64_t pieces = ceil_div(V, p.piece), slab = M * K * 4;
+        const int64_t room = kMaxSlabBytes / (slab * pieces);
+        p.add = pieces > 1 && room < 1;
+        p.splits = grad_shape(M, K, p.piece < V ? p.piece : V, P, 1, (int)(p.add || room < 1 ? 1 : room > 64 ? 64 : room)).splits;
         p.slabs = (int)(p.add ? p.splits : pieces * p.splits);
         if (p.slabs == 1 && !bf16) p.slabs = 0;
         p.gx = take((size_t)(p.Mp * p.piece * P * 2));
-        p.dx = take((size_t)p.slabs * M * K * 4);
+        p.dx = take((size_t)(p.slabs * slab));
     }
     if (want_de) p.gw = take((size_t)(p.piece * p.Mp * P * 2));
     p.bytes = at;
@@ -407,13 +430,14 @@ hipError_t launch_cross_entropy_backward(const int8_t* x_q, const float* s_x, in
         if (hipError_t err = P == 1 ? launch_grad_tiles<1>(g, stream) : launch_grad_tiles<2>(g, stream)) return err;
         if (dx) {
             float* const slab = reinterpret_cast<float*>(ws + p.dx) + (p.add ? 0 : v0 / p.piece * p.splits * M * K);
-            const GradGemmArgs a{ws + p.gx, p.piece * P * 2, g.e, K, M, K, rows, p.slabs ? slab : dx, K, M * K, p.splits,
-                                 p.add && v0 > 0, false};
+            const GradGemmArgs a{ws + p.gx, p.piece * P * 2, g.e, K, M, K, rows, p.slabs ? slab : dx, K, M * K,
+                                 grad_shape(M, K, rows, P, p.splits, p.splits).wide, p.splits, p.add && v0 > 0, false};
             if (hipError_t err = launch_grad_gemm(a, P, stream)) return err;
         }
         if (de) {
             const GradGemmArgs a{ws + p.gw, p.Mp * P * 2, x_q, K, rows, K, M,
-                                 static_cast<uint8_t*>(de) + v0 * K * (bf16 ? 2 : 4), K, 0, 1, accumulate, bf16};
+                                 static_cast<uint8_t*>(de) + v0 * K * (bf16 ? 2 : 4), K, 0,
+                                 grad_shape(rows, K, M, P, 1, 1).wide, 1, accumulate, bf16};
             if (hipError_t err = launch_grad_gemm(a, P, stream)) return err;
         }
     }

@@ -23,6 +23,7 @@ struct GradGemmArgs {
     void* c;               // fp32 or bf16 [I][ldc]
     int64_t ldc;
     int64_t slab;          // elements between the outputs of two splits of R (fp32)
+    bool wide;             // 256 x 256 tiles, else 64 x 256 (grad_shape)
     int splits;
     bool accumulate;       // add to what C holds
     bool bf16_out;
@@ -30,7 +31,13 @@ struct GradGemmArgs {
 
 hipError_t launch_grad_gemm(const GradGemmArgs& a, int pieces, hipStream_t stream);
 
-// Output tiles of a launch before R is split.
-int64_t grad_gemm_tiles(int64_t I, int64_t J);
+// The tile and the splits of R (at most max_splits; each writes a slab that is summed later) that a product
+// takes, and about how long it runs, in us.
+struct GradShape {
+    bool wide;
+    int splits;
+    float cost;
+};
+GradShape grad_shape(int64_t I, int64_t J, int64_t R, int pieces, int min_splits, int max_splits);
 
 }  // namespace dfssm

@@ -301,17 +301,37 @@ hipError_t launch_c(const GradGemmArgs& a, hipStream_t stream) {
     return hipGetLastError();
 }
 
-bool use_short(int64_t I) { return I <= 128; }
+float grad_cost(bool wide, int64_t I, int64_t J, int64_t R, int P, int splits) {
+    const int64_t bm = wide ? Wide::BM : Short::BM;
+    const int64_t n = ((I + bm - 1) / bm) * ((J + Wide::BN - 1) / Wide::BN) * splits;
+    float per_r;
+    if (wide) per_r = (P == 2 ? 0.0434f : 0.0264f) * (float)((n + 255) / 256);
+    else per_r = P == 2 ? 0.0160f + 0.0000448f * (float)(n > 256 ? n - 256 : 0) : 0.0104f + 0.0000397f * (float)(n > 256 ? n - 256 : 0);
+    return 8.0f + per_r * (float)R / (float)splits;
+}
 
 }  // namespace
 
-int64_t grad_gemm_tiles(int64_t I, int64_t J) {
-    const int64_t bm = use_short(I) ? Short::BM : Wide::BM;
-    return ((I + bm - 1) / bm) * ((J + Wide::BN - 1) / Wide::BN);
+// Costs measured with J = 2048: wide tiles run one to a CU, 178 us (two pieces; one: 110) a round of 256 at
+// R = 4096; short ones 65 us (43) up to 256 of them and 207 (165) for 1024.  So short ones take what wide
+// ones would fill badly: I = 1128 101 against 179 us with the gradient tiles, I = 300 (R 50280) 195 against 221,
+// I = 512 (R 50280) 276 against 234.
+GradShape grad_shape(int64_t I, int64_t J, int64_t R, int pieces, int min_splits, int max_splits) {
+    static const int kSplits[] = {1, 2, 3, 4, 6, 8, 12, 16, 24, 32, 48, 64};
+    GradShape best{true, min_splits, 3.0e38f};
+    for (int s : kSplits) {
+        if (s < min_splits || s > max_splits || (s > min_splits && R / s < 256)) continue;
+        const float slabs = (float)(I * J) * (float)s * 4.0f / 4.0e6f;  // read once more
+        for (int w = 0; w < 2; ++w) {
+            const float c = grad_cost(w != 0, I, J, R, pieces, s) + (max_splits > min_splits ? slabs : 0.0f);
+            if (c < best.cost) best = GradShape{w != 0, s, c};
+        }
+    }
+    return best;
 }
 
 hipError_t launch_grad_gemm(const GradGemmArgs& a, int pieces, hipStream_t stream) {
-    if (use_short(a.I)) return pieces == 1 ? launch_c<Short, 1>(a, stream) : launch_c<Short, 2>(a, stream);
+    if (!a.wide) return pieces == 1 ? launch_c<Short, 1>(a, stream) : launch_c<Short, 2>(a, stream);
     return pieces == 1 ? launch_c<Wide, 1>(a, stream) : launch_c<Wide, 2>(a, stream);
 }
 

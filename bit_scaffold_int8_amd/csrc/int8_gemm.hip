@@ -6,6 +6,8 @@
 // for any number of tokens: the LM head over a whole prompt, or an int8 layer.  The tile
 // product is tile_i8.h's.  The epilogue turns each 32-token block of a wave through LDS, so
 // that lanes write runs of a token's row instead of 16-byte pieces of 32 rows.
+#include <type_traits>
+
 #include "tile_i8.h"
 
 namespace dfssm {
@@ -23,8 +25,17 @@ struct GemmArgs {
     int64_t ldy;
     int64_t M, N;
     int K, ntw, ntt;
-    bool vec;
+    bool vec, stream;
 };
+
+typedef uint32_t v2u __attribute__((ext_vector_type(2)));
+
+// stream: past the caches, which an output of this size would only sweep.
+template <class T>
+__device__ __forceinline__ void store_out(T* p, T v, bool stream) {
+    if (stream) __builtin_nontemporal_store(v, p);
+    else *p = v;
+}
 
 // vec: y and its rows are 16-byte aligned, so four outputs go out together.
 template <class C, bool kFast, bool kBf16>
@@ -82,12 +93,12 @@ __global__ __launch_bounds__(C::NT, C::kMinWaves) void int8_gemm_kernel(GemmArgs
                 const int64_t at = (m0 + t0 + tr) * a.ldy + n0 + wn + c;
                 if (a.vec && c + 4 <= live_n) {
                     if constexpr (kBf16) {
-                        uint2 p;
+                        v2u p;
                         p.x = bf16_bits(o.x) | (bf16_bits(o.y) << 16);
                         p.y = bf16_bits(o.z) | (bf16_bits(o.w) << 16);
-                        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.y) + at) = p;
+                        store_out(reinterpret_cast<v2u*>(static_cast<uint16_t*>(a.y) + at), p, a.stream);
                     } else {
-                        *reinterpret_cast<v4f*>(static_cast<float*>(a.y) + at) = o;
+                        store_out(reinterpret_cast<v4f*>(static_cast<float*>(a.y) + at), o, a.stream);
                     }
                 } else {
 #pragma unroll
@@ -105,8 +116,11 @@ __global__ __launch_bounds__(C::NT, C::kMinWaves) void int8_gemm_kernel(GemmArgs
 
 template <bool kFast, bool kBf16>
 hipError_t launch_tiles(GemmArgs a, hipStream_t stream) {
-    return with_tile(pick_tile(a.N, a.M, a.K), [&](auto tile) {
-        using C = decltype(tile);
+    // Not the largest tile where rows are unaligned (they take more registers to stage) or the output streams
+    // (with two groups on a CU one's stores overlap the other's products: 2048 x 50280 fp32 257 us against
+    // 268; without streaming 333 and 276).
+    return with_tile(pick_tile(a.N, a.M, a.K, kFast && !a.stream ? 0 : 1), [&](auto tile) {
+        using C = std::conditional_t<kFast || decltype(tile)::BW * decltype(tile)::BT < 65536, decltype(tile), TileI8<2, 2, 2, 2>>;
         a.ntw = (int)((a.N + C::BW - 1) / C::BW);
         a.ntt = (int)((a.M + C::BT - 1) / C::BT);
         const dim3 grid((unsigned)((int64_t)a.ntw * a.ntt));
@@ -122,7 +136,11 @@ hipError_t launch_int8_gemm(const int8_t* x_q, int64_t ldx, const float* s_x, in
                             hipStream_t stream) {
     auto al16 = [](const void* p) { return ((uintptr_t)p & 15u) == 0; };
     const bool fast = al16(x_q) && al16(w) && ldx % 16 == 0 && ldw % 16 == 0 && K % 16 == 0;
-    const GemmArgs a{x_q, ldx, s_x, w, ldw, s_w, y, ldy, M, N, (int)K, 0, 0, al16(y) && ldy % (bf16 ? 8 : 4) == 0};
+    // Outputs past 160 MB go past the caches (1024 x 50280 fp32, 206 MB: 134 us against 146; but 512 x 50280,
+    // 103 MB, 74 against 68, and a reader finds the smaller ones in the 256 MB cache).
+    const bool streams = M * N * (bf16 ? 2 : 4) > (int64_t)160 << 20;
+    const GemmArgs a{x_q, ldx, s_x, w, ldw, s_w, y, ldy, M, N, (int)K, 0, 0, al16(y) && ldy % (bf16 ? 8 : 4) == 0,
+                     streams};
     if (fast) return bf16 ? launch_tiles<true, true>(a, stream) : launch_tiles<true, false>(a, stream);
     return bf16 ? launch_tiles<false, true>(a, stream) : launch_tiles<false, false>(a, stream);
 }

@@ -10,9 +10,15 @@
 // consecutive registers are four consecutive outputs of a token.
 //
 // Both operands go through LDS in chunks of 128 k: 8 threads stage a row's 128 bytes (a whole
-// cache line), and the 16-byte pieces of row r are stored at piece ^ (r & 7), so that the 8
-// lanes that read together (8 rows, one piece) hit all banks.  Two LDS buffers, one barrier per
-// chunk; loads run two chunks ahead (registers hold the chunk after the one in LDS).
+// cache line).  LDS has 64 banks, so two rows of a chunk span them once; the 16-byte pieces of row r are
+// stored at piece ^ (r / 2 & 7), so that the 16 lanes that read together (16 rows, one piece) meet
+// different banks (with r & 7 a third of the LDS cycles were conflicts).  Two LDS buffers, one barrier per chunk;
+// loads run two chunks ahead (registers hold the chunk after the one in LDS).  Chunks of 64 k,
+// with three buffers or with two smaller tiles per CU, measured 8 % slower: half-line loads.
+//
+// What bounds it: 2048 tokens x 50280 rows x 2048 run 239 us as logits' statistics (1.8 POPS); without
+// staging 207 us, so most of it is the products under the power limit (the GPU clocks down to 2.0 GHz at 45 %
+// matrix-core occupancy) and each tile's epilogue (about 5 of 33 us), which nothing overlaps.
 #pragma once
 
 #include "device_common.h"
@@ -39,28 +45,46 @@ struct TileI8 {
     static_assert((KS - 1) * WB * TB * 16 * NG * 4 <= kLdsBytes, "the K groups' sums fit the buffers");
 };
 
+// A 16-byte value shifted down by s bytes (zeros from 16 on).
+__device__ __forceinline__ uint4 shift_bytes(uint4 v, int s) {
+    uint64_t lo = v.x | (uint64_t)v.y << 32, hi = v.z | (uint64_t)v.w << 32;
+    if (s >= 8) {
+        lo = s < 16 ? hi : 0;
+        hi = 0;
+        s -= 8;
+    }
+    const int bits = 8 * (s & 7);
+    lo = lo >> bits | (hi << 1) << (63 - bits);
+    hi >>= bits;
+    return make_uint4((uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32));
+}
+
 // Pieces of one operand's chunk for one thread.  kFast: base and row stride are multiples of 16
 // and so is K; a piece is then wholly inside or outside its row, and the buffer resource's range
-// check zeroes rows past the last.  Otherwise 16-byte loads at any address, gathered by bytes
-// where a piece crosses the row's end.
+// check zeroes rows past the last.  Otherwise 16-byte loads at any address that never leave the row: a piece
+// that would is loaded from the row's last 16 bytes and shifted on its way to LDS (rows of less than
+// 16 bytes are gathered by bytes); rows past the last repeat it, and their outputs are not used.
 template <bool kFast, int P, int kRowStep>
 struct Stager {
     static_assert(kRowStep % 2 == 0, "the rows of a thread's pieces differ by whole pairs");
     __amdgpu_buffer_rsrc_t rsrc;
     const int8_t* base;
     int64_t ld;
-    int row0, rows, piece, off0;
+    int row0, piece, off0;
+    int row_off[P];
     uint4 v[P];
 
-    __device__ __forceinline__ void init(const int8_t* p, int64_t ld_, int rows_, int K, int tid) {
+    __device__ __forceinline__ void init(const int8_t* p, int64_t ld_, int rows, int K, int tid) {
         base = p;
         ld = ld_;
-        rows = rows_;
         row0 = tid >> 3;
         piece = tid & 7;
         if constexpr (kFast) {
-            rsrc = make_rsrc(p, rows_ > 0 ? (uint32_t)((rows_ - 1) * ld_ + K) : 0u);
+            rsrc = make_rsrc(p, rows > 0 ? (uint32_t)((rows - 1) * ld_ + K) : 0u);
             off0 = (int)(row0 * ld_);
+        } else {
+#pragma unroll
+            for (int j = 0; j < P; ++j) row_off[j] = (int)(min(row0 + j * kRowStep, rows - 1) * ld_);
         }
     }
     // Piece j of a chunk: off = offset(chunk) first.
@@ -73,19 +97,21 @@ struct Stager {
         if constexpr (kFast) {
             const v4i r = __builtin_amdgcn_raw_buffer_load_b128(rsrc, off + j * (int)(kRowStep * ld), 0, 0);
             v[j] = make_uint4((uint32_t)r.x, (uint32_t)r.y, (uint32_t)r.z, (uint32_t)r.w);
+        } else if (K >= 16) {
+            __builtin_memcpy(&v[j], base + (uint32_t)(row_off[j] + min(off, K - 16)), 16);
         } else {
-            const int row = row0 + j * kRowStep;
-            uint4 r = make_uint4(0u, 0u, 0u, 0u);
-            if (row < rows && off < K) {
-                const uint8_t* src = reinterpret_cast<const uint8_t*>(base) + row * ld + off;
-                if (off + 16 <= K) __builtin_memcpy(&r, src, 16);
-                else r = load16_guarded<false>(src, 0, K - off);
-            }
-            v[j] = r;
+            v[j] = load16_guarded<false>(reinterpret_cast<const uint8_t*>(base) + row_off[j], off, K);
         }
     }
-    __device__ __forceinline__ void store(int j, uint8_t* lds) const {
-        *reinterpret_cast<uint4*>(lds + (row0 + j * kRowStep) * kTileChunk + ((piece ^ (((row0 >> 1) + j * kRowStep / 2 % 8) & 7)) << 4)) = v[j];
+    // off: the offset that piece j was loaded with.
+    __device__ __forceinline__ void store(int j, uint8_t* lds, int off, int K) const {
+        uint4 r = v[j];
+        if constexpr (!kFast) {
+            // only a row's last chunk (and what follows it) holds pieces that leave the row
+            if (off - piece * 16 + kTileChunk > K && K >= 16) r = shift_bytes(r, max(off - (K - 16), 0));
+        }
+        *reinterpret_cast<uint4*>(lds + (row0 + j * kRowStep) * kTileChunk +
+                                  ((piece ^ (((row0 >> 1) + j * kRowStep / 2 % 8) & 7)) << 4)) = r;
     }
     // All pieces of a chunk.
     __device__ __forceinline__ void load_all(int chunk, int K) {
@@ -93,9 +119,10 @@ struct Stager {
 #pragma unroll
         for (int j = 0; j < P; ++j) load(j, off, K);
     }
-    __device__ __forceinline__ void store_all(uint8_t* lds) const {
+    __device__ __forceinline__ void store_all(int chunk, uint8_t* lds, int K) const {
+        const int off = offset(chunk, K);
 #pragma unroll
-        for (int j = 0; j < P; ++j) store(j, lds);
+        for (int j = 0; j < P; ++j) store(j, lds, off, K);
     }
 };
 
@@ -133,8 +160,8 @@ __device__ __forceinline__ bool tile_i8(const int8_t* __restrict__ w, int64_t ld
 
     sw.load_all(kg, K);
     st.load_all(kg, K);
-    sw.store_all(lds);
-    st.store_all(lds + kXOff);
+    sw.store_all(kg, lds, K);
+    st.store_all(kg, lds + kXOff, K);
     // in the order of the loop's steps: the waits for them then count only what lies between
     const int ow1 = sw.offset(C::KS + kg, K), ot1 = st.offset(C::KS + kg, K);
 #pragma unroll
@@ -169,18 +196,18 @@ __device__ __forceinline__ bool tile_i8(const int8_t* __restrict__ w, int64_t ld
     // fragments and a quarter of the staging (registers to the other buffer, then the loads that refill
     // them).  A wave issues in order, so a burst of LDS or memory instructions would hold back the
     // products behind it; the pattern spreads them one by one over the products.
-    auto step = [&](int s, int cur, int nxt, int ow, int ot, const Frags& f, Frags* next) {
+    auto step = [&](int s, int cur, int nxt, int ow, int ot, int held, const Frags& f, Frags* next) {
         if (next) read(cur, s + 1, *next);
 #pragma unroll
         for (int j = 0; j < C::PW; ++j)
             if (j * 4 / C::PW == s) {
-                sw.store(j, lds + nxt);
+                sw.store(j, lds + nxt, held, K);
                 sw.load(j, ow, K);
             }
 #pragma unroll
         for (int j = 0; j < C::PT; ++j)
             if (j * 4 / C::PT == s) {
-                st.store(j, lds + nxt + kXOff);
+                st.store(j, lds + nxt + kXOff, held, K);
                 st.load(j, ot, K);
             }
         multiply(f);
@@ -201,12 +228,14 @@ __device__ __forceinline__ bool tile_i8(const int8_t* __restrict__ w, int64_t ld
         const int cur = (c & 1) * C::kBufBytes, nxt = C::kBufBytes - cur;
         // (past the last chunk zeros are staged that nothing reads)
         const int ow = sw.offset((c + 2) * C::KS + kg, K), ot = st.offset((c + 2) * C::KS + kg, K);
+        // (the offset of the chunk that the registers hold; used where rows are not aligned, and there it is the same for both)
+        const int held = st.offset((c + 1) * C::KS + kg, K);
         read(cur, 0, f0);
         __builtin_amdgcn_sched_barrier(0);
-        step(0, cur, nxt, ow, ot, f0, &f1);
-        step(1, cur, nxt, ow, ot, f1, &f0);
-        step(2, cur, nxt, ow, ot, f0, &f1);
-        step(3, cur, nxt, ow, ot, f1, nullptr);
+        step(0, cur, nxt, ow, ot, held, f0, &f1);
+        step(1, cur, nxt, ow, ot, held, f1, &f0);
+        step(2, cur, nxt, ow, ot, held, f0, &f1);
+        step(3, cur, nxt, ow, ot, held, f1, nullptr);
     }
     if constexpr (C::KS > 1) {
         int32_t* const sums = reinterpret_cast<int32_t*>(all_lds) + tid;
@@ -260,10 +289,10 @@ inline float tile_cost(int kind, int64_t rows, int64_t tokens, int64_t K) {
     return t.fixed + (t.first - t.fixed + (float)((n - 1) / 256) * t.more) * ((float)K / 2048.0f);
 }
 
-// The cheapest of the first `kinds` tiles.
-inline int pick_tile(int64_t rows, int64_t tokens, int64_t K, int kinds = kTileKinds) {
-    int best = 0;
-    for (int k = 1; k < kinds; ++k)
+// The cheapest of the tiles [from, to).
+inline int pick_tile(int64_t rows, int64_t tokens, int64_t K, int from = 0, int to = kTileKinds) {
+    int best = from;
+    for (int k = from + 1; k < to; ++k)
         if (tile_cost(k, rows, tokens, K) < tile_cost(best, rows, tokens, K)) best = k;
     return best;
 }

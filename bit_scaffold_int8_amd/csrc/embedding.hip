@@ -60,12 +60,10 @@ __global__ __launch_bounds__(256) void lookup_scaled_kernel(const int32_t* __res
 }
 
 // ---------------------------------------------------------------- sort
-// Blocks of 4096 items, 8 waves; wave w owns items [512 w, 512 w + 512) in 8 rounds of 64, so
+// A workgroup of W waves sorts blocks of W * R * 64 items: wave w owns R rounds of 64 in a row, so
 // (wave, round, lane) is the items' order.
-constexpr int kSortThreads = 512, kSortWaves = 8, kSortRounds = 8;
-constexpr int kSortBlock = kSortWaves * kSortRounds * kWave;
 
-// Lanes of the wave whose digit equals this lane's (live lanes only; dead lanes share digit 256).
+// Lanes of the wave whose digit equals this lane's (dead lanes share digit 256).
 __device__ __forceinline__ uint64_t same_digit(int digit) {
     uint64_t m = ~0ull;
 #pragma unroll
@@ -76,22 +74,23 @@ __device__ __forceinline__ uint64_t same_digit(int digit) {
     return m;
 }
 
+template <int W>
 struct SortShared {
-    int32_t count[kSortWaves][256];  // per wave and digit; then the wave's first rank within the block
-    int32_t total[256];              // the block's items of a digit
-    int32_t start[256];              // where the block's items of a digit go
+    int32_t count[W][256];  // per wave and digit; then the wave's first rank within the block
+    int32_t total[256];     // the block's items of a digit
+    int32_t start[256];     // where the block's items of a digit go
 };
 
 // Ranks of a block's items by digit: rank[r] counts the block's earlier items with the same digit.
 // sh.total is complete after the call (a barrier ends it).
-__device__ __forceinline__ void block_ranks(const uint32_t (&key)[kSortRounds], const bool (&live)[kSortRounds],
-                                            int shift, SortShared& sh, int (&digit)[kSortRounds],
-                                            int (&rank)[kSortRounds]) {
+template <int W, int R>
+__device__ __forceinline__ void block_ranks(const uint32_t (&key)[R], const bool (&live)[R], int shift,
+                                            SortShared<W>& sh, int (&digit)[R], int (&rank)[R]) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     for (int d = lane; d < 256; d += 64) sh.count[wave][d] = 0;
     __syncthreads();
 #pragma unroll
-    for (int r = 0; r < kSortRounds; ++r) {
+    for (int r = 0; r < R; ++r) {
         digit[r] = live[r] ? (int)((key[r] >> shift) & 255u) : 256;
         const uint64_t same = same_digit(digit[r]);
         const int before = __popcll(same & ((1ull << lane) - 1));
@@ -104,7 +103,8 @@ __device__ __forceinline__ void block_ranks(const uint32_t (&key)[kSortRounds], 
     __syncthreads();
     if (threadIdx.x < 256) {
         int sum = 0;
-        for (int w = 0; w < kSortWaves; ++w) {
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
             const int c = sh.count[w][threadIdx.x];
             sh.count[w][threadIdx.x] = sum;
             sum += c;
@@ -113,7 +113,7 @@ __device__ __forceinline__ void block_ranks(const uint32_t (&key)[kSortRounds], 
     }
     __syncthreads();
 #pragma unroll
-    for (int r = 0; r < kSortRounds; ++r)
+    for (int r = 0; r < R; ++r)
         if (live[r]) rank[r] += sh.count[wave][digit[r]];
 }
 
@@ -137,34 +137,37 @@ __device__ __forceinline__ int scan256(int v, int32_t* part) {
 // A token's sort key: tokens outside the vocabulary sort behind all others.
 __device__ __forceinline__ uint32_t token_key(int32_t id, uint32_t V) { return id >= 0 && (uint32_t)id < V ? (uint32_t)id : V; }
 
-// T <= kSortBlock: every pass in one workgroup.
-__global__ __launch_bounds__(kSortThreads) void sort_one_kernel(const int32_t* __restrict__ tokens, int T, uint32_t V,
-                                                                int passes, uint32_t* __restrict__ keys,
-                                                                int32_t* __restrict__ order) {
-    __shared__ SortShared sh;
-    __shared__ uint32_t skey[kSortBlock];
-    __shared__ int32_t sidx[kSortBlock];
+// Few tokens (1024 R at the most): every pass in one workgroup.
+constexpr int kOneWaves = 16;
+
+template <int R>
+__global__ __launch_bounds__(kOneWaves * 64) void sort_one_kernel(const int32_t* __restrict__ tokens, int T, uint32_t V,
+                                                                  int passes, uint32_t* __restrict__ keys,
+                                                                  int32_t* __restrict__ order) {
+    __shared__ SortShared<kOneWaves> sh;
+    __shared__ uint32_t skey[kOneWaves * R * 64];
+    __shared__ int32_t sidx[kOneWaves * R * 64];
     __shared__ int32_t part[4];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    uint32_t key[kSortRounds];
-    int32_t idx[kSortRounds];
-    bool live[kSortRounds];
-    int digit[kSortRounds], rank[kSortRounds];
-    const int i0 = wave * kSortRounds * 64 + lane;
+    uint32_t key[R];
+    int32_t idx[R];
+    bool live[R];
+    int digit[R], rank[R];
+    const int i0 = wave * R * 64 + lane;
 #pragma unroll
-    for (int r = 0; r < kSortRounds; ++r) {
+    for (int r = 0; r < R; ++r) {
         const int i = i0 + r * 64;
         live[r] = i < T;
         idx[r] = i;
         key[r] = live[r] ? token_key(tokens[i], V) : 0u;
     }
     for (int p = 0; p < passes; ++p) {
-        block_ranks(key, live, 8 * p, sh, digit, rank);
+        block_ranks<kOneWaves, R>(key, live, 8 * p, sh, digit, rank);
         const int start = scan256(threadIdx.x < 256 ? sh.total[threadIdx.x] : 0, part);
         if (threadIdx.x < 256) sh.start[threadIdx.x] = start;
         __syncthreads();
 #pragma unroll
-        for (int r = 0; r < kSortRounds; ++r)
+        for (int r = 0; r < R; ++r)
             if (live[r]) {
                 const int at = sh.start[digit[r]] + rank[r];
                 skey[at] = key[r];
@@ -172,7 +175,7 @@ __global__ __launch_bounds__(kSortThreads) void sort_one_kernel(const int32_t* _
             }
         __syncthreads();
 #pragma unroll
-        for (int r = 0; r < kSortRounds; ++r)
+        for (int r = 0; r < R; ++r)
             if (live[r]) {
                 key[r] = skey[i0 + r * 64];
                 idx[r] = sidx[i0 + r * 64];
@@ -180,76 +183,85 @@ __global__ __launch_bounds__(kSortThreads) void sort_one_kernel(const int32_t* _
         __syncthreads();
     }
 #pragma unroll
-    for (int r = 0; r < kSortRounds; ++r)
+    for (int r = 0; r < R; ++r)
         if (live[r]) {
             keys[i0 + r * 64] = key[r];
             order[i0 + r * 64] = idx[r];
         }
 }
 
-// A pass over many blocks: how often each digit occurs in each block ...
-__global__ __launch_bounds__(kSortThreads) void sort_count_kernel(const int32_t* __restrict__ tokens,
+// Many tokens, blocks of 512 R items.  A pass is two kernels: how often each digit occurs in each block ...
+// (`tokens` on the first pass, (keys, order) afterwards.  Counting for the next pass inside the scatter saves a
+// launch, but a token that fills much of the batch sends that many atomics to one count: 15.7 us against 5 + 4.6.)
+constexpr int kManyWaves = 8, kManyThreads = kManyWaves * 64;
+
+__global__ __launch_bounds__(kManyThreads) void sort_count_kernel(const int32_t* __restrict__ tokens,
                                                                   const uint32_t* __restrict__ keys, int64_t T,
-                                                                  uint32_t V, int shift, int32_t* __restrict__ hist) {
+                                                                  uint32_t V, int block, int shift,
+                                                                  int32_t* __restrict__ hist) {
     __shared__ int32_t count[256];
     if (threadIdx.x < 256) count[threadIdx.x] = 0;
     __syncthreads();
-    const int64_t b0 = (int64_t)blockIdx.x * kSortBlock;
-#pragma unroll
-    for (int r = 0; r < kSortBlock / kSortThreads; ++r) {
-        const int64_t i = b0 + r * kSortThreads + threadIdx.x;
+    const int64_t b0 = (int64_t)blockIdx.x * block;
+    for (int r = 0; r < block; r += kManyThreads) {
+        const int64_t i = b0 + r + threadIdx.x;
         if (i < T) atomicAdd(&count[((keys ? keys[i] : token_key(tokens[i], V)) >> shift) & 255u], 1);
     }
     __syncthreads();
     if (threadIdx.x < 256) hist[(int64_t)blockIdx.x * 256 + threadIdx.x] = count[threadIdx.x];
 }
 
-// ... and each block's items to their places: behind all smaller digits and the digit's items of
-// the blocks before.  `tokens` on the first pass, (keys, order) afterwards.
-__global__ __launch_bounds__(kSortThreads) void sort_scatter_kernel(const int32_t* __restrict__ tokens,
+// ... and the block's items to their places, behind all smaller digits and the digit's items of the blocks before.
+template <int R>
+__global__ __launch_bounds__(kManyThreads) void sort_scatter_kernel(const int32_t* __restrict__ tokens,
                                                                     const uint32_t* __restrict__ keys,
                                                                     const int32_t* __restrict__ order, int64_t T,
                                                                     uint32_t V, int shift,
                                                                     const int32_t* __restrict__ hist,
                                                                     uint32_t* __restrict__ keys_out,
                                                                     int32_t* __restrict__ order_out) {
-    __shared__ SortShared sh;
+    constexpr int kBlock = kManyThreads * R;
+    __shared__ SortShared<kManyWaves> sh;
     __shared__ int32_t part[4];
     __shared__ int32_t halves[2][256][2];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    // digit d's count in the blocks before this one and in all (two halves of the threads share the blocks)
-    {
-        const int d = threadIdx.x & 255, h = threadIdx.x >> 8;
-        int before = 0, all = 0;
-        for (int b = h; b < (int)gridDim.x; b += 2) {
-            const int c = hist[(int64_t)b * 256 + d];
-            all += c;
-            before += b < (int)blockIdx.x ? c : 0;
-        }
-        halves[h][d][0] = before;
-        halves[h][d][1] = all;
-    }
-    __syncthreads();
-    const int d = threadIdx.x & 255;
-    const int total = halves[0][d][1] + halves[1][d][1];
-    const int start = scan256(threadIdx.x < 256 ? total : 0, part);
-    if (threadIdx.x < 256) sh.start[d] = start + halves[0][d][0] + halves[1][d][0];
-
-    uint32_t key[kSortRounds];
-    int32_t idx[kSortRounds];
-    bool live[kSortRounds];
-    int digit[kSortRounds], rank[kSortRounds];
-    const int64_t i0 = (int64_t)blockIdx.x * kSortBlock + wave * kSortRounds * 64 + lane;
+    uint32_t key[R];
+    int32_t idx[R];
+    bool live[R];
+    int digit[R], rank[R];
+    const int64_t i0 = (int64_t)blockIdx.x * kBlock + wave * R * 64 + lane;
 #pragma unroll
-    for (int r = 0; r < kSortRounds; ++r) {
+    for (int r = 0; r < R; ++r) {
         const int64_t i = i0 + r * 64;
         live[r] = i < T;
         idx[r] = live[r] ? (order ? order[i] : (int32_t)i) : 0;
         key[r] = live[r] ? (keys ? keys[i] : token_key(tokens[i], V)) : 0u;
     }
-    block_ranks(key, live, shift, sh, digit, rank);
+    // digit d's count in the blocks before this one and in all (two halves of the threads share the blocks)
+    const int d = threadIdx.x & 255;
+    {
+        const int h = threadIdx.x >> 8, n = (int)gridDim.x;
+        int before = 0, all = 0;
+        for (int b0 = h; b0 < n; b0 += 16) {
+            int c[8];
 #pragma unroll
-    for (int r = 0; r < kSortRounds; ++r)
+            for (int j = 0; j < 8; ++j) c[j] = b0 + 2 * j < n ? hist[(int64_t)(b0 + 2 * j) * 256 + d] : 0;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                all += c[j];
+                before += b0 + 2 * j < (int)blockIdx.x ? c[j] : 0;
+            }
+        }
+        halves[h][d][0] = before;
+        halves[h][d][1] = all;
+    }
+    __syncthreads();
+    const int total = halves[0][d][1] + halves[1][d][1];
+    const int start = scan256(threadIdx.x < 256 ? total : 0, part);
+    if (threadIdx.x < 256) sh.start[d] = start + halves[0][d][0] + halves[1][d][0];
+    block_ranks<kManyWaves, R>(key, live, shift, sh, digit, rank);
+#pragma unroll
+    for (int r = 0; r < R; ++r)
         if (live[r]) {
             const int at = sh.start[digit[r]] + rank[r];
             keys_out[at] = key[r];
@@ -298,6 +310,21 @@ __device__ __forceinline__ void store_vec(void* base, int64_t at, const float (&
     }
 }
 
+// Zeros; past the caches where de is larger than they are (412 MB: the sums and zeros of 16384 tokens 89 against
+// 93 us, and the parts of crossing rows stay cached: their join 7.4 against 9.3).
+template <bool kBf16, int VEC, bool kStream>
+__device__ __forceinline__ void store_zeros(void* base, int64_t at) {
+    if constexpr (kStream) {
+        static_assert(VEC == 4, "streamed in vectors");
+        typedef uint32_t v2u __attribute__((ext_vector_type(2)));
+        if constexpr (kBf16) __builtin_nontemporal_store((v2u){0, 0}, reinterpret_cast<v2u*>(static_cast<uint16_t*>(base) + at));
+        else __builtin_nontemporal_store((v4f){0, 0, 0, 0}, reinterpret_cast<v4f*>(static_cast<float*>(base) + at));
+    } else {
+        const float zero[VEC] = {};
+        store_vec<kBf16, VEC>(base, at, zero);
+    }
+}
+
 template <bool kOutBf16, bool kAdd, int VEC>
 __device__ __forceinline__ void write_row(const SumArgs& a, uint32_t row, int64_t k, const float (&sum)[VEC]) {
     float o[VEC];
@@ -317,29 +344,34 @@ constexpr int kFillRows = 32;  // rows per workgroup that fills the rows without
 
 // Workgroups [0, pieces * col_blocks) sum pieces; the ones behind them (none when adding to de) write zeros
 // to the rows that no token names.
-template <bool kInBf16, bool kOutBf16, bool kAdd, int VEC>
+template <bool kInBf16, bool kOutBf16, bool kAdd, int VEC, bool kStream>
 __global__ __launch_bounds__(256) void piece_sum_kernel(SumArgs a) {
     const int nsum = a.pieces * a.col_blocks;
     if ((int)blockIdx.x >= nsum) {
         if constexpr (!kAdd) {
+            static_assert(kFillRows * 8 == 256, "8 lanes search a row");
             __shared__ int32_t named[kFillRows];
             const int64_t r0 = (int64_t)((int)blockIdx.x - nsum) * kFillRows;
-            if (threadIdx.x < kFillRows) {
-                const uint32_t row = (uint32_t)(r0 + threadIdx.x);
-                int64_t lo = 0, hi = a.T;  // first sorted token >= row
-                while (lo < hi) {
-                    const int64_t mid = (lo + hi) >> 1;
-                    if (a.keys[mid] < row) lo = mid + 1;
-                    else hi = mid;
+            // the first sorted token >= row, 8 probes a step
+            const int j = threadIdx.x & 7, group = threadIdx.x & 56;
+            const uint32_t row = (uint32_t)(r0 + (threadIdx.x >> 3));
+            int lo = 0, hi = (int)a.T;
+            while (__any(lo < hi)) {
+                const int len = hi - lo, p = lo + (int)((int64_t)len * (j + 1) / 9);
+                const bool less = len > 0 && a.keys[p] < row;
+                const int n = __popcll((__ballot(less) >> group) & 255);  // the probes below the row: the first n
+                const int below = lo + (int)((int64_t)len * n / 9), above = lo + (int)((int64_t)len * (n + 1) / 9);
+                if (len > 0) {
+                    if (n < 8) hi = above;
+                    if (n > 0) lo = below + 1;
                 }
-                named[threadIdx.x] = lo < a.T && a.keys[lo] == row;
             }
+            if (j == 0) named[threadIdx.x >> 3] = lo < a.T && a.keys[lo] == row;
             __syncthreads();
-            const float zero[VEC] = {};
             for (int r = 0; r < kFillRows && r0 + r < a.V; ++r)
                 if (!named[r])
                     for (int64_t k = threadIdx.x * VEC; k < a.K; k += 256 * VEC)
-                        store_vec<kOutBf16, VEC>(a.de, (r0 + r) * a.K + k, zero);
+                        store_zeros<kOutBf16, VEC, kStream>(a.de, (r0 + r) * a.K + k);
         }
         return;
     }
@@ -394,11 +426,25 @@ __global__ __launch_bounds__(256) void piece_join_kernel(SumArgs a) {
     if (p0 > 0 && a.keys[p0] == row && a.keys[p0 - 1] == row) return;  // it began before this piece
     float sum[VEC];
     load_vec<false, VEC>(a.tail, piece * a.K + k, sum);
-    for (int q = piece + 1; q < a.pieces && a.keys[q * a.piece] == row; ++q) {
-        float v[VEC];
-        load_vec<false, VEC>(a.head, q * a.K + k, v);
+    constexpr int U = 8;  // parts in flight
+    for (int q = piece + 1; q < a.pieces; q += U) {
+        uint32_t key[U];
+        float v[U][VEC];
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) sum[i] += v[i];
+        for (int j = 0; j < U; ++j) {
+            const int64_t p = q + j < a.pieces ? q + j : a.pieces - 1;
+            key[j] = a.keys[p * a.piece];
+            load_vec<false, VEC>(a.head, p * a.K + k, v[j]);  // (may be no part of the row: not added then)
+        }
+        int n = 0;  // parts of the row: the first ones, since the keys are sorted
+#pragma unroll
+        for (int j = 0; j < U; ++j) n += q + j < a.pieces && key[j] == row ? 1 : 0;
+#pragma unroll
+        for (int j = 0; j < U; ++j)
+            if (j < n)
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) sum[i] += v[j][i];
+        if (n < U) break;
     }
     write_row<kOutBf16, kAdd, VEC>(a, row, k, sum);
 }
@@ -406,7 +452,7 @@ __global__ __launch_bounds__(256) void piece_join_kernel(SumArgs a) {
 // How a backward call's workspace lies.
 struct Plan {
     int64_t piece;
-    int pieces, sort_blocks, passes;
+    int pieces, sort_block, sort_blocks, passes;
     size_t keys[2], order[2], hist, head, tail, bytes;
 };
 
@@ -415,7 +461,10 @@ Plan make_plan(int64_t T, int64_t V, int64_t K) {
     // pieces of 32 tokens, longer ones past 32768 tokens (1024 pieces fill the GPU)
     p.piece = ((T + 1023) / 1024 + 31) / 32 * 32;
     p.pieces = (int)((T + p.piece - 1) / p.piece);
-    p.sort_blocks = (int)((T + kSortBlock - 1) / kSortBlock);
+    // sorted by one workgroup, or in blocks of 1024 tokens; of 4096 where so many blocks' counts would take long to
+    // add up (each block reads all)
+    p.sort_block = T <= 4096 ? 4096 : T <= 65536 ? kManyThreads * 2 : kManyThreads * 8;
+    p.sort_blocks = (int)((T + p.sort_block - 1) / p.sort_block);
     p.passes = 1;
     while (p.passes < 4 && ((uint64_t)V >> (8 * p.passes)) != 0) ++p.passes;  // keys 0 .. V
     size_t at = 0;
@@ -439,8 +488,12 @@ template <bool kInBf16, bool kOutBf16, bool kAdd, int VEC>
 hipError_t launch_sums(SumArgs a, hipStream_t stream) {
     a.col_blocks = (int)((a.K + 256 * VEC - 1) / (256 * VEC));
     const int64_t fills = kAdd ? 0 : ((int64_t)a.V + kFillRows - 1) / kFillRows;
-    piece_sum_kernel<kInBf16, kOutBf16, kAdd, VEC>
-        <<<dim3((unsigned)((int64_t)a.pieces * a.col_blocks + fills)), 256, 0, stream>>>(a);
+    const dim3 grid((unsigned)((int64_t)a.pieces * a.col_blocks + fills));
+    constexpr bool kMayStream = !kAdd && VEC == 4;
+    if (kMayStream && (int64_t)a.V * a.K * (kOutBf16 ? 2 : 4) > (int64_t)160 << 20)
+        piece_sum_kernel<kInBf16, kOutBf16, kAdd, VEC, kMayStream><<<grid, 256, 0, stream>>>(a);
+    else
+        piece_sum_kernel<kInBf16, kOutBf16, kAdd, VEC, false><<<grid, 256, 0, stream>>>(a);
     if (hipError_t err = hipGetLastError()) return err;
     if (a.pieces > 1)
         piece_join_kernel<kOutBf16, kAdd, VEC><<<dim3((unsigned)(a.pieces * a.col_blocks)), 256, 0, stream>>>(a);
@@ -488,16 +541,19 @@ hipError_t launch_embedding_backward(const int32_t* tokens, int64_t T, const voi
     int32_t* hist = reinterpret_cast<int32_t*>(ws + p.hist);
     int at = 0;
     if (p.sort_blocks == 1) {
-        sort_one_kernel<<<1, kSortThreads, 0, stream>>>(tokens, (int)T, (uint32_t)V, p.passes, keys[0], order[0]);
+        if (T <= 1024) sort_one_kernel<1><<<1, kOneWaves * 64, 0, stream>>>(tokens, (int)T, (uint32_t)V, p.passes, keys[0], order[0]);
+        else sort_one_kernel<4><<<1, kOneWaves * 64, 0, stream>>>(tokens, (int)T, (uint32_t)V, p.passes, keys[0], order[0]);
     } else {
+        const dim3 grid((unsigned)p.sort_blocks);
         for (int i = 0; i < p.passes; ++i) {
             const uint32_t* kin = i ? keys[at] : nullptr;
             const int32_t* oin = i ? order[at] : nullptr;
             const int to = i ? at ^ 1 : 0;
-            sort_count_kernel<<<dim3((unsigned)p.sort_blocks), kSortThreads, 0, stream>>>(tokens, kin, T, (uint32_t)V,
-                                                                                          8 * i, hist);
-            sort_scatter_kernel<<<dim3((unsigned)p.sort_blocks), kSortThreads, 0, stream>>>(
-                tokens, kin, oin, T, (uint32_t)V, 8 * i, hist, keys[to], order[to]);
+            sort_count_kernel<<<grid, kManyThreads, 0, stream>>>(tokens, kin, T, (uint32_t)V, p.sort_block, 8 * i, hist);
+            if (p.sort_block == kManyThreads * 2)
+                sort_scatter_kernel<2><<<grid, kManyThreads, 0, stream>>>(tokens, kin, oin, T, (uint32_t)V, 8 * i, hist, keys[to], order[to]);
+            else
+                sort_scatter_kernel<8><<<grid, kManyThreads, 0, stream>>>(tokens, kin, oin, T, (uint32_t)V, 8 * i, hist, keys[to], order[to]);
             at = to;
         }
     }

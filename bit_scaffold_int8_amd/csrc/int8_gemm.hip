@@ -25,20 +25,21 @@ struct GemmArgs {
     int64_t ldy;
     int64_t M, N;
     int K, ntw, ntt;
-    bool vec, stream;
+    bool vec;
 };
 
 typedef uint32_t v2u __attribute__((ext_vector_type(2)));
 
-// stream: past the caches, which an output of this size would only sweep.
-template <class T>
-__device__ __forceinline__ void store_out(T* p, T v, bool stream) {
-    if (stream) __builtin_nontemporal_store(v, p);
+// kStream: past the caches, which an output of such a size would only sweep.  (A template parameter: behind a
+// flag the two stores become one plain store.)
+template <bool kStream, class T>
+__device__ __forceinline__ void store_out(T* p, T v) {
+    if constexpr (kStream) __builtin_nontemporal_store(v, p);
     else *p = v;
 }
 
 // vec: y and its rows are 16-byte aligned, so four outputs go out together.
-template <class C, bool kFast, bool kBf16>
+template <class C, bool kFast, bool kBf16, bool kStream>
 __global__ __launch_bounds__(C::NT, C::kMinWaves) void int8_gemm_kernel(GemmArgs a) {
     constexpr int kLd = C::WB * 32 + 4;  // floats per token row of a wave's LDS block
     constexpr int kEpi = C::WW * C::TW * 32 * kLd * 4;
@@ -96,9 +97,9 @@ __global__ __launch_bounds__(C::NT, C::kMinWaves) void int8_gemm_kernel(GemmArgs
                         v2u p;
                         p.x = bf16_bits(o.x) | (bf16_bits(o.y) << 16);
                         p.y = bf16_bits(o.z) | (bf16_bits(o.w) << 16);
-                        store_out(reinterpret_cast<v2u*>(static_cast<uint16_t*>(a.y) + at), p, a.stream);
+                        store_out<kStream>(reinterpret_cast<v2u*>(static_cast<uint16_t*>(a.y) + at), p);
                     } else {
-                        store_out(reinterpret_cast<v4f*>(static_cast<float*>(a.y) + at), o, a.stream);
+                        store_out<kStream>(reinterpret_cast<v4f*>(static_cast<float*>(a.y) + at), o);
                     }
                 } else {
 #pragma unroll
@@ -114,18 +115,29 @@ __global__ __launch_bounds__(C::NT, C::kMinWaves) void int8_gemm_kernel(GemmArgs
     }
 }
 
+template <class C, bool kFast, bool kBf16, bool kStream>
+hipError_t launch_tile(GemmArgs a, hipStream_t stream) {
+    a.ntw = (int)((a.N + C::BW - 1) / C::BW);
+    a.ntt = (int)((a.M + C::BT - 1) / C::BT);
+    const dim3 grid((unsigned)((int64_t)a.ntw * a.ntt));
+    int8_gemm_kernel<C, kFast, kBf16, kStream><<<grid, C::NT, 0, stream>>>(a);
+    return hipGetLastError();
+}
+
 template <bool kFast, bool kBf16>
-hipError_t launch_tiles(GemmArgs a, hipStream_t stream) {
-    // Not the largest tile where rows are unaligned (they take more registers to stage) or the output streams
-    // (with two groups on a CU one's stores overlap the other's products: 2048 x 50280 fp32 257 us against
-    // 268; without streaming 333 and 276).
-    return with_tile(pick_tile(a.N, a.M, a.K, kFast && !a.stream ? 0 : 1), [&](auto tile) {
-        using C = std::conditional_t<kFast || decltype(tile)::BW * decltype(tile)::BT < 65536, decltype(tile), TileI8<2, 2, 2, 2>>;
-        a.ntw = (int)((a.N + C::BW - 1) / C::BW);
-        a.ntt = (int)((a.M + C::BT - 1) / C::BT);
-        const dim3 grid((unsigned)((int64_t)a.ntw * a.ntt));
-        int8_gemm_kernel<C, kFast, kBf16><<<grid, C::NT, 0, stream>>>(a);
-        return hipGetLastError();
+hipError_t launch_tiles(const GemmArgs& a, hipStream_t stream) {
+    if constexpr (kFast) {
+        // Outputs past 160 MB go past the caches, from 128 x 128 tiles: with two groups on a CU one's stores overlap
+        // the other's products (2048 x 50280 fp32, 412 MB: 257 us; 268 from 256 x 256; 333 and 276 without
+        // streaming.  512 x 50280, 103 MB: 74 against 68, and a reader finds it in the 256 MB cache).
+        if (a.vec && a.M >= 128 && a.M * a.N * (kBf16 ? 2 : 4) > (int64_t)160 << 20)
+            return launch_tile<TileI8<2, 2, 2, 2>, true, kBf16, true>(a, stream);
+    }
+    // (unaligned rows take more registers to stage: not with the largest tile)
+    return with_tile(pick_tile(a.N, a.M, a.K, kFast ? 0 : 1), [&](auto tile) {
+        using T = decltype(tile);
+        using C = std::conditional_t<kFast || T::BW * T::BT < 65536, T, TileI8<2, 2, 2, 2>>;
+        return launch_tile<C, kFast, kBf16, false>(a, stream);
     });
 }
 
@@ -136,11 +148,7 @@ hipError_t launch_int8_gemm(const int8_t* x_q, int64_t ldx, const float* s_x, in
                             hipStream_t stream) {
     auto al16 = [](const void* p) { return ((uintptr_t)p & 15u) == 0; };
     const bool fast = al16(x_q) && al16(w) && ldx % 16 == 0 && ldw % 16 == 0 && K % 16 == 0;
-    // Outputs past 160 MB go past the caches (1024 x 50280 fp32, 206 MB: 134 us against 146; but 512 x 50280,
-    // 103 MB, 74 against 68, and a reader finds the smaller ones in the 256 MB cache).
-    const bool streams = M * N * (bf16 ? 2 : 4) > (int64_t)160 << 20;
-    const GemmArgs a{x_q, ldx, s_x, w, ldw, s_w, y, ldy, M, N, (int)K, 0, 0, al16(y) && ldy % (bf16 ? 8 : 4) == 0,
-                     streams};
+    const GemmArgs a{x_q, ldx, s_x, w, ldw, s_w, y, ldy, M, N, (int)K, 0, 0, al16(y) && ldy % (bf16 ? 8 : 4) == 0};
     if (fast) return bf16 ? launch_tiles<true, true>(a, stream) : launch_tiles<true, false>(a, stream);
     return bf16 ? launch_tiles<false, true>(a, stream) : launch_tiles<false, false>(a, stream);
 }

@@ -6,6 +6,13 @@
 // for any number of tokens: the LM head over a whole prompt, or an int8 layer.  The tile
 // product is tile_i8.h's.  The epilogue turns each 32-token block of a wave through LDS, so
 // that lanes write runs of a token's row instead of 16-byte pieces of 32 rows.
+//
+// What bounds it: many tokens, the products under the power limit and, in bursts that nothing overlaps, the stores
+// (2048 x 50280 x 2048: 275 us for fp32, 249 for bf16; the loss over the same logits 235); few tokens, reading w once
+// (50280 x 2048, 1 to 64 tokens: 17 to 19 us, 5.5 to 6 TB/s); few rows, the latency of K's chunks (1 x 2048 x
+// 4096: 6.1 us, of which 4 do not grow with K).
+// Measured and not kept: stores past the caches (275 against 276 us for 412 MB, 545 against 517 for 824), device-scope
+// stores (333), two smaller tiles to a CU so that stores overlap products (310 streamed, 337 not).
 #include <type_traits>
 
 #include "tile_i8.h"
@@ -30,16 +37,8 @@ struct GemmArgs {
 
 typedef uint32_t v2u __attribute__((ext_vector_type(2)));
 
-// kStream: past the caches, which an output of such a size would only sweep.  (A template parameter: behind a
-// flag the two stores become one plain store.)
-template <bool kStream, class T>
-__device__ __forceinline__ void store_out(T* p, T v) {
-    if constexpr (kStream) __builtin_nontemporal_store(v, p);
-    else *p = v;
-}
-
 // vec: y and its rows are 16-byte aligned, so four outputs go out together.
-template <class C, bool kFast, bool kBf16, bool kStream>
+template <class C, bool kFast, bool kBf16>
 __global__ __launch_bounds__(C::NT, C::kMinWaves) void int8_gemm_kernel(GemmArgs a) {
     constexpr int kLd = C::WB * 32 + 4;  // floats per token row of a wave's LDS block
     constexpr int kEpi = C::WW * C::TW * 32 * kLd * 4;
@@ -97,9 +96,9 @@ __global__ __launch_bounds__(C::NT, C::kMinWaves) void int8_gemm_kernel(GemmArgs
                         v2u p;
                         p.x = bf16_bits(o.x) | (bf16_bits(o.y) << 16);
                         p.y = bf16_bits(o.z) | (bf16_bits(o.w) << 16);
-                        store_out<kStream>(reinterpret_cast<v2u*>(static_cast<uint16_t*>(a.y) + at), p);
+                        *reinterpret_cast<v2u*>(static_cast<uint16_t*>(a.y) + at) = p;
                     } else {
-                        store_out<kStream>(reinterpret_cast<v4f*>(static_cast<float*>(a.y) + at), o);
+                        *reinterpret_cast<v4f*>(static_cast<float*>(a.y) + at) = o;
                     }
                 } else {
 #pragma unroll
@@ -115,29 +114,17 @@ __global__ __launch_bounds__(C::NT, C::kMinWaves) void int8_gemm_kernel(GemmArgs
     }
 }
 
-template <class C, bool kFast, bool kBf16, bool kStream>
-hipError_t launch_tile(GemmArgs a, hipStream_t stream) {
-    a.ntw = (int)((a.N + C::BW - 1) / C::BW);
-    a.ntt = (int)((a.M + C::BT - 1) / C::BT);
-    const dim3 grid((unsigned)((int64_t)a.ntw * a.ntt));
-    int8_gemm_kernel<C, kFast, kBf16, kStream><<<grid, C::NT, 0, stream>>>(a);
-    return hipGetLastError();
-}
-
 template <bool kFast, bool kBf16>
-hipError_t launch_tiles(const GemmArgs& a, hipStream_t stream) {
-    if constexpr (kFast) {
-        // Outputs past 160 MB go past the caches, from 128 x 128 tiles: with two groups on a CU one's stores overlap
-        // the other's products (2048 x 50280 fp32, 412 MB: 257 us; 268 from 256 x 256; 333 and 276 without
-        // streaming.  512 x 50280, 103 MB: 74 against 68, and a reader finds it in the 256 MB cache).
-        if (a.vec && a.M >= 128 && a.M * a.N * (kBf16 ? 2 : 4) > (int64_t)160 << 20)
-            return launch_tile<TileI8<2, 2, 2, 2>, true, kBf16, true>(a, stream);
-    }
+hipError_t launch_tiles(GemmArgs a, hipStream_t stream) {
     // (unaligned rows take more registers to stage: not with the largest tile)
     return with_tile(pick_tile(a.N, a.M, a.K, kFast ? 0 : 1), [&](auto tile) {
         using T = decltype(tile);
         using C = std::conditional_t<kFast || T::BW * T::BT < 65536, T, TileI8<2, 2, 2, 2>>;
-        return launch_tile<C, kFast, kBf16, false>(a, stream);
+        a.ntw = (int)((a.N + C::BW - 1) / C::BW);
+        a.ntt = (int)((a.M + C::BT - 1) / C::BT);
+        const dim3 grid((unsigned)((int64_t)a.ntw * a.ntt));
+        int8_gemm_kernel<C, kFast, kBf16><<<grid, C::NT, 0, stream>>>(a);
+        return hipGetLastError();
     });
 }
 

@@ -272,12 +272,13 @@ struct TileShape {
     float first, more;  // us for up to 256 tiles, and for each further 256, at K = 2048
 };
 // Measured on 512 to 50280 rows x 1 to 2048 tokens, K 512 to 8192.  Large tiles reread least and win
-// when they fill the GPU (50280 rows x 512 tokens, K 2048: 61 us for the first, then 65, 74, 103); small ones win
+// when they fill the GPU (50280 rows x 512 tokens, K 2048: 61 us for the first, then 65, 74, 103; long runs under
+// the power limit set them further apart: x 2048 tokens 249 and 277); small ones win
 // when they do not (2048 rows x 1 token, K 4096, in this order: 39, 17, 12, 11, 9.5, 7.2, 6.1 us), or when the
 // large ones' last round would be nearly empty (8512 rows x 2048 tokens: 58 against 48 us for 128 x 128).
 inline const TileShape& tile_shape(int kind) {
     static const TileShape t[kTileKinds] = {
-        {256, 256, 7.0f, 24.0f, 34.0f}, {128, 128, 4.1f, 10.7f, 9.0f}, {128, 64, 3.3f, 7.9f, 5.5f},
+        {256, 256, 7.0f, 24.0f, 34.0f}, {128, 128, 4.1f, 10.7f, 10.5f}, {128, 64, 3.3f, 7.9f, 5.5f},
         {128, 32, 2.9f, 6.8f, 4.0f},    {64, 64, 3.4f, 6.3f, 3.4f},    {64, 32, 3.6f, 5.4f, 2.35f},
         {32, 32, 3.95f, 5.0f, 4.0f}};
     return t[kind];

@@ -302,9 +302,9 @@ __global__ __launch_bounds__(256) void slab_sum_kernel(const float* __restrict__
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// The tile of the gradient kernel for a piece's rows: one of those with 64 tokens or more, so that the padded
+// The tiles of the gradient kernel for a piece's rows: of those with 64 tokens or more, so that the padded
 // tokens of d s_x fill whole chunks of the product (64 tokens) and are all written.
-int grad_tile(int64_t M, int64_t rows, int64_t K) { return pick_tile(rows, M, K, 0, kTileKindsNoSplit); }
+TileSplit grad_tiles(int64_t M, int64_t rows, int64_t K) { return split_rows(rows, M, K, kTile256, kTileKindsNoSplit); }
 
 // How a backward call is cut and where its workspace lies; the size query and the call agree on it.
 struct Plan {
@@ -320,7 +320,7 @@ constexpr int64_t kMaxSlabBytes = (int64_t)512 << 20, kMaxPieceBytes = (int64_t)
 
 // About how long a piece takes: its gradient tiles and its products (dx with the slabs it adds), and the launches.
 float piece_cost(int64_t M, int64_t rows, int64_t K, int P, bool want_dx, bool want_de) {
-    const float tiles = 1.35f * tile_cost(grad_tile(M, rows, K), rows, M, K);  // (the epilogue is the heavier one)
+    const float tiles = 1.35f * grad_tiles(M, rows, K).cost;  // (the epilogue is the heavier one)
     return tiles + (want_dx ? grad_shape(M, K, rows, P, 1, 64).cost : 0.0f) +
            (want_de ? grad_shape(rows, K, M, P, 1, 1).cost : 0.0f) + 4.0f;
 }
@@ -375,8 +375,8 @@ Plan make_plan(int64_t M, int64_t V, int64_t K, bool bf16, bool want_dx, bool wa
 }
 
 template <int P>
-hipError_t launch_grad_tiles(GradArgs a, hipStream_t stream) {
-    return with_tile(grad_tile(a.M, a.V, a.K), [&](auto tile) {
+hipError_t launch_grad_kind(GradArgs a, int kind, hipStream_t stream) {
+    return with_tile(kind, [&](auto tile) {
         using C = decltype(tile);
         if constexpr (C::BT >= 64 && C::KS == 1) {
             a.ntt = (int)ceil_div(a.M, C::BT);
@@ -389,24 +389,61 @@ hipError_t launch_grad_tiles(GradArgs a, hipStream_t stream) {
     });
 }
 
+template <int P>
+hipError_t launch_grad_tiles(const GradArgs& a, hipStream_t stream) {
+    const TileSplit split = grad_tiles(a.M, a.V, a.K);
+    GradArgs part = a;
+    part.V = split.main;
+    if (hipError_t err = launch_grad_kind<P>(part, split.kind, stream)) return err;
+    if (split.main == a.V) return hipSuccess;
+    part.V = a.V - split.main;
+    part.v0 = a.v0 + split.main;
+    part.e = a.e + split.main * a.K;
+    part.s_e = a.s_e + split.main;
+    if (a.gx) part.gx = a.gx + split.main * P;
+    if (a.gw) part.gw = a.gw + split.main * a.ldgw;
+    return launch_grad_kind<P>(part, split.tail, stream);
+}
+
+hipError_t launch_loss_kind(LossArgs a, int kind, hipStream_t stream) {
+    return with_tile(kind, [&](auto tile) {
+        using C = decltype(tile);
+        a.ntw = (int)ceil_div(a.V, C::BW);
+        a.ntt = (int)ceil_div(a.M, C::BT);
+        loss_tile_kernel<C><<<dim3((unsigned)((int64_t)a.ntw * a.ntt)), C::NT, 0, stream>>>(a);
+        return hipGetLastError();
+    });
+}
+
+// Row tiles of the forward pass: of the main rows, and of all.
+int64_t main_row_tiles(const TileSplit& s) { return ceil_div(s.main, tile_shape(s.kind).rows); }
+int64_t row_tiles(const TileSplit& s, int64_t V) {
+    return main_row_tiles(s) + (s.main < V ? ceil_div(V - s.main, tile_shape(s.tail).rows) : 0);
+}
+
 }  // namespace
 
 size_t cross_entropy_workspace_bytes(int64_t M, int64_t V, int64_t K) {
-    return (size_t)(ceil_div(V, tile_shape(pick_tile(V, M, K)).rows) * M) * sizeof(float2);
+    return (size_t)(row_tiles(split_rows(V, M, K), V) * M) * sizeof(float2);
 }
 
 hipError_t launch_cross_entropy(const int8_t* x_q, const float* s_x, int64_t M, int64_t V, int64_t K, const int8_t* e,
                                 const float* s_e, const int32_t* targets, float* loss, float* lse, void* workspace,
                                 hipStream_t stream) {
     LossArgs a{x_q, s_x, M, V, (int)K, 0, 0, e, s_e, static_cast<float2*>(workspace)};
-    const hipError_t err = with_tile(pick_tile(V, M, K), [&](auto tile) {
-        using C = decltype(tile);
-        a.ntw = (int)ceil_div(V, C::BW);
-        a.ntt = (int)ceil_div(M, C::BT);
-        loss_tile_kernel<C><<<dim3((unsigned)((int64_t)a.ntw * a.ntt)), C::NT, 0, stream>>>(a);
-        return hipGetLastError();
-    });
-    if (err) return err;
+    const TileSplit split = split_rows(V, M, K);
+    a.V = split.main;
+    if (hipError_t err = launch_loss_kind(a, split.kind, stream)) return err;
+    if (split.main < V) {
+        LossArgs rest = a;
+        rest.V = V - split.main;
+        rest.e = e + split.main * K;
+        rest.s_e = s_e + split.main;
+        rest.part = a.part + main_row_tiles(split) * M;
+        if (hipError_t err = launch_loss_kind(rest, split.tail, stream)) return err;
+    }
+    a.V = V;
+    a.ntw = (int)row_tiles(split, V);
     loss_join_kernel<<<dim3((unsigned)ceil_div(M, 16)), 1024, 0, stream>>>(a, targets, loss, lse);
     return hipGetLastError();
 }
@@ -431,13 +468,13 @@ hipError_t launch_cross_entropy_backward(const int8_t* x_q, const float* s_x, in
         if (dx) {
             float* const slab = reinterpret_cast<float*>(ws + p.dx) + (p.add ? 0 : v0 / p.piece * p.splits * M * K);
             const GradGemmArgs a{ws + p.gx, p.piece * P * 2, g.e, K, M, K, rows, p.slabs ? slab : dx, K, M * K,
-                                 grad_shape(M, K, rows, P, p.splits, p.splits).wide, p.splits, p.add && v0 > 0, false};
+                                 grad_shape(M, K, rows, P, p.splits, p.splits).wide_rows, p.splits, p.add && v0 > 0, false};
             if (hipError_t err = launch_grad_gemm(a, P, stream)) return err;
         }
         if (de) {
             const GradGemmArgs a{ws + p.gw, p.Mp * P * 2, x_q, K, rows, K, M,
                                  static_cast<uint8_t*>(de) + v0 * K * (bf16 ? 2 : 4), K, 0,
-                                 grad_shape(rows, K, M, P, 1, 1).wide, 1, accumulate, bf16};
+                                 grad_shape(rows, K, M, P, 1, 1).wide_rows, 1, accumulate, bf16};
             if (hipError_t err = launch_grad_gemm(a, P, stream)) return err;
         }
     }

@@ -23,7 +23,7 @@ struct GradGemmArgs {
     void* c;               // fp32 or bf16 [I][ldc]
     int64_t ldc;
     int64_t slab;          // elements between the outputs of two splits of R (fp32)
-    bool wide;             // 256 x 256 tiles, else 64 x 256 (grad_shape)
+    int64_t wide_rows;     // the first rows of C by 256 x 256 tiles (a multiple of 256, or all), the rest by 64 x 256
     int splits;
     bool accumulate;       // add to what C holds
     bool bf16_out;
@@ -31,10 +31,10 @@ struct GradGemmArgs {
 
 hipError_t launch_grad_gemm(const GradGemmArgs& a, int pieces, hipStream_t stream);
 
-// The tile and the splits of R (at most max_splits; each writes a slab that is summed later) that a product
-// takes, and about how long it runs, in us.
+// The rows that 256 x 256 tiles take and the splits of R (at most max_splits; each writes a slab that is summed
+// later) that a product takes, and about how long it runs, in us.
 struct GradShape {
-    bool wide;
+    int64_t wide_rows;
     int splits;
     float cost;
 };

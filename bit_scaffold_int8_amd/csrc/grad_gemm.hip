@@ -318,21 +318,35 @@ float grad_cost(bool wide, int64_t I, int64_t J, int64_t R, int P, int splits) {
 // I = 512 (R 50280) 276 against 234.
 GradShape grad_shape(int64_t I, int64_t J, int64_t R, int pieces, int min_splits, int max_splits) {
     static const int kSplits[] = {1, 2, 3, 4, 6, 8, 12, 16, 24, 32, 48, 64};
-    GradShape best{true, min_splits, 3.0e38f};
+    GradShape best{0, min_splits, 3.0e38f};
+    const int64_t ti = (I + Wide::BM - 1) / Wide::BM, tj = (J + Wide::BN - 1) / Wide::BN;
     for (int s : kSplits) {
         if (s < min_splits || s > max_splits || (s > min_splits && R / s < 256)) continue;
-        const float slabs = (float)(I * J) * (float)s * 4.0f / 4.0e6f;  // read once more
-        for (int w = 0; w < 2; ++w) {
-            const float c = grad_cost(w != 0, I, J, R, pieces, s) + (max_splits > min_splits ? slabs : 0.0f);
-            if (c < best.cost) best = GradShape{w != 0, s, c};
-        }
+        const float slabs = max_splits > min_splits ? (float)(I * J) * (float)s * 4.0f / 4.0e6f : 0.0f;  // read once more
+        auto consider = [&](int64_t rows, float cost) {
+            if (cost + slabs < best.cost) best = GradShape{rows, s, cost + slabs};
+        };
+        consider(0, grad_cost(false, I, J, R, pieces, s));
+        consider(I, grad_cost(true, I, J, R, pieces, s));
+        // wide tiles for whole rounds, short ones for the rest (50280 rows: 6 rounds and 144 short tiles, not 7 rounds)
+        const int64_t main = ti * tj * s / 256 * 256 / (tj * s) * Wide::BM;
+        if (main > 0 && main < I)
+            consider(main, grad_cost(true, main, J, R, pieces, s) + grad_cost(false, I - main, J, R, pieces, s));
     }
     return best;
 }
 
 hipError_t launch_grad_gemm(const GradGemmArgs& a, int pieces, hipStream_t stream) {
-    if (!a.wide) return pieces == 1 ? launch_c<Short, 1>(a, stream) : launch_c<Short, 2>(a, stream);
-    return pieces == 1 ? launch_c<Wide, 1>(a, stream) : launch_c<Wide, 2>(a, stream);
+    GradGemmArgs part = a;
+    if (a.wide_rows > 0) {
+        part.I = a.wide_rows;
+        if (hipError_t err = pieces == 1 ? launch_c<Wide, 1>(part, stream) : launch_c<Wide, 2>(part, stream)) return err;
+    }
+    if (a.wide_rows == a.I) return hipSuccess;
+    part.I = a.I - a.wide_rows;
+    part.a = a.a + a.wide_rows * a.lda;
+    part.c = static_cast<uint8_t*>(a.c) + a.wide_rows * a.ldc * (a.bf16_out ? 2 : 4);
+    return pieces == 1 ? launch_c<Short, 1>(part, stream) : launch_c<Short, 2>(part, stream);
 }
 
 }  // namespace dfssm

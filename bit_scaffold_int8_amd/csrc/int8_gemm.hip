@@ -115,9 +115,8 @@ __global__ __launch_bounds__(C::NT, C::kMinWaves) void int8_gemm_kernel(GemmArgs
 }
 
 template <bool kFast, bool kBf16>
-hipError_t launch_tiles(GemmArgs a, hipStream_t stream) {
-    // (unaligned rows take more registers to stage: not with the largest tile)
-    return with_tile(pick_tile(a.N, a.M, a.K, kFast ? 0 : 1), [&](auto tile) {
+hipError_t launch_kind(GemmArgs a, int kind, hipStream_t stream) {
+    return with_tile(kind, [&](auto tile) {
         using T = decltype(tile);
         using C = std::conditional_t<kFast || T::BW * T::BT < 65536, T, TileI8<2, 2, 2, 2>>;
         a.ntw = (int)((a.N + C::BW - 1) / C::BW);
@@ -126,6 +125,21 @@ hipError_t launch_tiles(GemmArgs a, hipStream_t stream) {
         int8_gemm_kernel<C, kFast, kBf16><<<grid, C::NT, 0, stream>>>(a);
         return hipGetLastError();
     });
+}
+
+template <bool kFast, bool kBf16>
+hipError_t launch_tiles(const GemmArgs& a, hipStream_t stream) {
+    // (unaligned rows take more registers to stage: not with the largest tile)
+    const TileSplit split = split_rows(a.N, a.M, a.K, kFast ? kTile256 : kTile128);
+    GemmArgs part = a;
+    part.N = split.main;
+    if (hipError_t err = launch_kind<kFast, kBf16>(part, split.kind, stream)) return err;
+    if (split.main == a.N) return hipSuccess;
+    part.N = a.N - split.main;
+    part.w = a.w + split.main * a.ldw;
+    part.s_w = a.s_w + split.main;
+    part.y = static_cast<uint8_t*>(a.y) + split.main * (kBf16 ? 2 : 4);
+    return launch_kind<kFast, kBf16>(part, split.tail, stream);
 }
 
 }  // namespace

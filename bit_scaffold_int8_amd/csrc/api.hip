@@ -299,9 +299,12 @@ dfssm_status decode_layers_impl(const dfssm_decode_layer_weights* w, int64_t n_l
 
 // ---- the operators over an int8 matrix with fp32 or bf16 results
 constexpr int64_t kMaxStride = (int64_t)1 << 22;     // row strides of the int8 operands: a tile's 256 rows stay below 2^30
-constexpr int64_t kMaxTiles = ((int64_t)1 << 31) / 2;  // workgroups of one launch
-constexpr int64_t kMaxLossTokens = (int64_t)1 << 18;   // tokens of one backward call
-constexpr int64_t kMaxGradTokens = (int64_t)1 << 24;   // tokens of one embedding gradient
+constexpr int64_t kMaxBlocks = (int64_t)1 << 30;       // 32 x 32 blocks of one product's output
+// (a launch holds fewer than 2^32 threads)
+constexpr int64_t kMaxLossTokens = (int64_t)1 << 25, kMaxLossRows = (int64_t)1 << 28;  // of one forward call
+constexpr int64_t kMaxLossLogits = (int64_t)1 << 38;
+constexpr int64_t kMaxLossGradTokens = (int64_t)1 << 18;  // of one backward call
+constexpr int64_t kMaxGradTokens = (int64_t)1 << 24, kMaxGradRows = (int64_t)1 << 28;  // of one embedding gradient
 
 bool type_ok(int32_t t) { return t == DFSSM_F32 || t == DFSSM_BF16; }
 bool aligned_type(const void* p, int32_t t) { return ((uintptr_t)p & (t == DFSSM_BF16 ? 1u : 3u)) == 0; }
@@ -309,7 +312,7 @@ bool aligned_type(const void* p, int32_t t) { return ((uintptr_t)p & (t == DFSSM
 // Sizes of the cross entropy over [V][K] for M tokens.
 dfssm_status loss_sizes(int64_t M, int64_t V, int64_t K) {
     if (M <= 0 || V <= 0 || K <= 0 || M >= kMaxRows || V >= kMaxRows || K % 16 != 0) return DFSSM_ERR_INVALID_ARG;
-    if (K > kMaxK || ((V + 127) / 128) * ((M + 31) / 32) > kMaxTiles) return DFSSM_ERR_UNSUPPORTED;
+    if (K > kMaxK || M > kMaxLossTokens || V > kMaxLossRows || M * V > kMaxLossLogits) return DFSSM_ERR_UNSUPPORTED;
     return DFSSM_OK;
 }
 
@@ -564,7 +567,7 @@ dfssm_status dfssm_int8_gemm(const int8_t* x_q, int64_t ldx, const float* s_x, i
     if (ldx < K || ldw < K || ldy < N || !type_ok(y_type)) return DFSSM_ERR_INVALID_ARG;
     if (!aligned4(s_x) || !aligned4(s_w) || !aligned_type(y, y_type)) return DFSSM_ERR_INVALID_ARG;
     if (K > kMaxK || ldx > kMaxStride || ldw > kMaxStride || ldy >= ((int64_t)1 << 40) ||
-        ((N + 31) / 32) * ((M + 31) / 32) > kMaxTiles)
+        ((N + 31) / 32) * ((M + 31) / 32) > kMaxBlocks)
         return DFSSM_ERR_UNSUPPORTED;
     return dfssm::launch_int8_gemm(x_q, ldx, s_x, M, N, K, w, ldw, s_w, y, ldy, y_type == DFSSM_BF16, stream) ==
                    hipSuccess
@@ -592,7 +595,7 @@ dfssm_status dfssm_cross_entropy(const int8_t* x_q, const float* s_x, int64_t M,
 
 size_t dfssm_cross_entropy_backward_workspace_bytes(int64_t M, int64_t V, int64_t K, int32_t grad_type,
                                                     int32_t want_dx, int32_t want_de) {
-    if (loss_sizes(M, V, K) != DFSSM_OK || M > kMaxLossTokens || !type_ok(grad_type) || (!want_dx && !want_de)) return 0;
+    if (loss_sizes(M, V, K) != DFSSM_OK || M > kMaxLossGradTokens || !type_ok(grad_type) || (!want_dx && !want_de)) return 0;
     return dfssm::cross_entropy_backward_workspace_bytes(M, V, K, grad_type == DFSSM_BF16, want_dx != 0, want_de != 0);
 }
 
@@ -608,7 +611,7 @@ dfssm_status dfssm_cross_entropy_backward(const int8_t* x_q, const float* s_x, i
     if (!aligned16(x_q) || !aligned16(e) || !aligned16(workspace) || !aligned16(dx) || !aligned16(de) ||
         !aligned4(s_x) || !aligned4(s_e) || !aligned4(targets) || !aligned4(lse) || !aligned4(dloss))
         return DFSSM_ERR_INVALID_ARG;
-    if (M > kMaxLossTokens) return DFSSM_ERR_UNSUPPORTED;
+    if (M > kMaxLossGradTokens) return DFSSM_ERR_UNSUPPORTED;
     const bool bf16 = grad_type == DFSSM_BF16;
     if (workspace_bytes < dfssm::cross_entropy_backward_workspace_bytes(M, V, K, bf16, dx != nullptr, de != nullptr))
         return DFSSM_ERR_INVALID_ARG;
@@ -632,7 +635,7 @@ dfssm_status dfssm_embedding_lookup_scaled(const int32_t* tokens, int64_t T, con
 }
 
 size_t dfssm_embedding_backward_workspace_bytes(int64_t T, int64_t V, int64_t K) {
-    if (embedding_sizes(T, V, K) != DFSSM_OK || T > kMaxGradTokens) return 0;
+    if (embedding_sizes(T, V, K) != DFSSM_OK || T > kMaxGradTokens || V > kMaxGradRows) return 0;
     return dfssm::embedding_backward_workspace_bytes(T, V, K);
 }
 
@@ -646,7 +649,7 @@ dfssm_status dfssm_embedding_backward(const int32_t* tokens, int64_t T, const vo
     if (!aligned4(tokens) || !aligned_type(dout, dout_type) || !aligned_type(de, de_type) || !aligned16(workspace) ||
         ldd < K)
         return DFSSM_ERR_INVALID_ARG;
-    if (T > kMaxGradTokens || ldd >= ((int64_t)1 << 31)) return DFSSM_ERR_UNSUPPORTED;
+    if (T > kMaxGradTokens || V > kMaxGradRows || ldd >= ((int64_t)1 << 31)) return DFSSM_ERR_UNSUPPORTED;
     if (workspace_bytes < dfssm::embedding_backward_workspace_bytes(T, V, K)) return DFSSM_ERR_INVALID_ARG;
     return dfssm::launch_embedding_backward(tokens, T, dout, ldd, dout_type == DFSSM_BF16, V, K, scale, de,
                                             de_type == DFSSM_BF16, accumulate != 0, workspace, stream) == hipSuccess

@@ -308,7 +308,7 @@ TileSplit grad_tiles(int64_t M, int64_t rows, int64_t K) { return split_rows(row
 
 // How a backward call is cut and where its workspace lies; the size query and the call agree on it.
 struct Plan {
-    int64_t Mp;      // tokens padded to the largest tile
+    int64_t Mp;      // tokens padded for every tile: ceil(M / t) t for t = 64, 128, 192 and 256
     int64_t piece;   // vocabulary rows per piece, a multiple of 256
     int splits;      // of dx's sum over a piece
     int slabs;       // fp32 slabs of dx in the workspace; 0: dx itself is the only one
@@ -328,7 +328,7 @@ float piece_cost(int64_t M, int64_t rows, int64_t K, int P, bool want_dx, bool w
 Plan make_plan(int64_t M, int64_t V, int64_t K, bool bf16, bool want_dx, bool want_de) {
     const int P = bf16 ? 1 : 2;
     Plan p{};
-    p.Mp = ceil_div(M, 256) * 256;
+    p.Mp = (M + 255) / 64 * 64;
     // The longest piece whose d takes at most 512 MB (2048 rows at the least); among pieces up to it, the one that
     // wastes least: pieces of equal length, and pieces whose tiles of de fill whole rounds of the 256 CUs, with
     // a short last one (4096 tokens x 50280 rows: 6 rounds of 8192 rows and a rest instead of 7 of 7424).

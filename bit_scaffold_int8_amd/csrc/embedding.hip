@@ -514,10 +514,16 @@ hipError_t launch_lookup_t(const int32_t* tokens, int64_t T, const int8_t* e, co
     constexpr int VEC = kBf16 ? 8 : 4;  // 16 bytes of output a thread
     const bool vec = K % VEC == 0 && ldo % VEC == 0 && aligned(e, VEC) && aligned(out, 16);
     const int64_t per = 256 * (vec ? VEC : 1);
-    const dim3 grid((unsigned)((T + kLookTokens - 1) / kLookTokens), (unsigned)((K + per - 1) / per));
-    if (vec) lookup_scaled_kernel<kBf16, VEC><<<grid, 256, 0, stream>>>(tokens, T, e, s_e, V, K, scale, out, ldo);
-    else lookup_scaled_kernel<kBf16, 1><<<grid, 256, 0, stream>>>(tokens, T, e, s_e, V, K, scale, out, ldo);
-    return hipGetLastError();
+    constexpr int64_t kSlice = (int64_t)1 << 24;  // tokens per launch: its threads stay below 2^32
+    for (int64_t t0 = 0; t0 < T; t0 += kSlice) {
+        const int64_t n = T - t0 < kSlice ? T - t0 : kSlice;
+        void* const o = static_cast<uint8_t*>(out) + t0 * ldo * (kBf16 ? 2 : 4);
+        const dim3 grid((unsigned)((n + kLookTokens - 1) / kLookTokens), (unsigned)((K + per - 1) / per));
+        if (vec) lookup_scaled_kernel<kBf16, VEC><<<grid, 256, 0, stream>>>(tokens + t0, n, e, s_e, V, K, scale, o, ldo);
+        else lookup_scaled_kernel<kBf16, 1><<<grid, 256, 0, stream>>>(tokens + t0, n, e, s_e, V, K, scale, o, ldo);
+        if (hipError_t err = hipGetLastError()) return err;
+    }
+    return hipSuccess;
 }
 
 }  // namespace

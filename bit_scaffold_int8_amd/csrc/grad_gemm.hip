@@ -17,7 +17,7 @@ typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 typedef int v2i __attribute__((ext_vector_type(2)));
 typedef uint32_t v4u __attribute__((ext_vector_type(4)));
 
-constexpr int kLoadDead = 0x7ff00000;  // a load offset past every resource used here: reads zero
+constexpr int kLoadDead = 0x40000000;  // a load offset past every resource used here (below 2^30): reads zero
 
 template <int MB_, int NB_, int MW_, int NW_>
 struct GradTile {

@@ -130,7 +130,7 @@ hipError_t launch_kind(GemmArgs a, int kind, hipStream_t stream) {
 template <bool kFast, bool kBf16>
 hipError_t launch_tiles(const GemmArgs& a, hipStream_t stream) {
     // (unaligned rows take more registers to stage: not with the largest tile)
-    const TileSplit split = split_rows(a.N, a.M, a.K, kFast ? kTile256 : kTile128);
+    const TileSplit split = split_rows(a.N, a.M, a.K, kFast ? kTile256 : kTile256x192);
     GemmArgs part = a;
     part.N = split.main;
     if (hipError_t err = launch_kind<kFast, kBf16>(part, split.kind, stream)) return err;
@@ -149,9 +149,19 @@ hipError_t launch_int8_gemm(const int8_t* x_q, int64_t ldx, const float* s_x, in
                             hipStream_t stream) {
     auto al16 = [](const void* p) { return ((uintptr_t)p & 15u) == 0; };
     const bool fast = al16(x_q) && al16(w) && ldx % 16 == 0 && ldw % 16 == 0 && K % 16 == 0;
-    const GemmArgs a{x_q, ldx, s_x, w, ldw, s_w, y, ldy, M, N, (int)K, 0, 0, al16(y) && ldy % (bf16 ? 8 : 4) == 0};
-    if (fast) return bf16 ? launch_tiles<true, true>(a, stream) : launch_tiles<true, false>(a, stream);
-    return bf16 ? launch_tiles<false, true>(a, stream) : launch_tiles<false, false>(a, stream);
+    const bool vec = al16(y) && ldy % (bf16 ? 8 : 4) == 0;
+    // A launch holds at most 2^32 threads: larger products go slice by slice.
+    constexpr int64_t kRows = (int64_t)1 << 20, kTokens = (int64_t)1 << 17;
+    for (int64_t n0 = 0; n0 < N; n0 += kRows)
+        for (int64_t m0 = 0; m0 < M; m0 += kTokens) {
+            const GemmArgs a{x_q + m0 * ldx, ldx, s_x + m0, w + n0 * ldw, ldw, s_w + n0,
+                             static_cast<uint8_t*>(y) + (m0 * ldy + n0) * (bf16 ? 2 : 4), ldy,
+                             M - m0 < kTokens ? M - m0 : kTokens, N - n0 < kRows ? N - n0 : kRows, (int)K, 0, 0, vec};
+            const hipError_t err = fast ? (bf16 ? launch_tiles<true, true>(a, stream) : launch_tiles<true, false>(a, stream))
+                                        : (bf16 ? launch_tiles<false, true>(a, stream) : launch_tiles<false, false>(a, stream));
+            if (err) return err;
+        }
+    return hipSuccess;
 }
 
 }  // namespace dfssm

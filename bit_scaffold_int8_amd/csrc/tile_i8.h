@@ -263,7 +263,7 @@ __device__ __forceinline__ bool tile_i8(const int8_t* __restrict__ w, int64_t ld
 
 // ---- which tile a shape takes (host)
 
-enum TileKind { kTile256, kTile128, kTile128x64, kTile128x32, kTile64x64, kTile64x32, kTile32x32, kTileKinds };
+enum TileKind { kTile256, kTile256x192, kTile128, kTile128x64, kTile128x32, kTile64x64, kTile64x32, kTile32x32, kTileKinds };
 constexpr int kTileKindsNoSplit = kTile128x64 + 1;  // the first ones: 64 tokens or more, K not split
 
 struct TileShape {
@@ -271,14 +271,15 @@ struct TileShape {
     float fixed;        // us that do not grow with K
     float first, more;  // us for up to 256 tiles, and for each further 256, at K = 2048
 };
-// Measured on 512 to 50280 rows x 1 to 2048 tokens, K 512 to 8192.  Large tiles reread least and win
-// when they fill the GPU (50280 rows x 512 tokens, K 2048: 61 us for the first, then 65, 74, 103; long runs under
-// the power limit set them further apart: x 2048 tokens 249 and 277); small ones win
-// when they do not (2048 rows x 1 token, K 4096, in this order: 39, 17, 12, 11, 9.5, 7.2, 6.1 us), or when the
-// large ones' last round would be nearly empty (8512 rows x 2048 tokens: 58 against 48 us for 128 x 128).
+// Measured on 512 to 50280 rows x 1 to 2048 tokens, K 512 to 8192, large ones in long runs under the power limit.
+// Large tiles reread least and win when they fill the GPU (50280 rows x 1500 tokens, K 2048, in this order:
+// 183, 199, 207, 235 us; x 300 tokens, of which the second wastes least: 59, 53, 60, 62); small ones win when they do
+// not (2048 rows x 1 token, K 4096: 39 us for the first, then 17, 12, 11, 9.5, 7.2, 6.1 from the third on), or when
+// the large ones' last round would be nearly empty (8512 rows x 300 tokens: 26, 22, 13, 13 us).
 inline const TileShape& tile_shape(int kind) {
     static const TileShape t[kTileKinds] = {
-        {256, 256, 7.0f, 24.0f, 34.0f}, {128, 128, 4.1f, 10.7f, 10.5f}, {128, 64, 3.3f, 7.9f, 5.5f},
+        {256, 256, 7.0f, 24.0f, 34.0f}, {256, 192, 6.5f, 21.0f, 30.0f}, {128, 128, 4.1f, 10.7f, 11.5f},
+        {128, 64, 3.3f, 7.9f, 7.8f},
         {128, 32, 2.9f, 6.8f, 4.0f},    {64, 64, 3.4f, 6.3f, 3.4f},    {64, 32, 3.6f, 5.4f, 2.35f},
         {32, 32, 3.95f, 5.0f, 4.0f}};
     return t[kind];
@@ -327,6 +328,7 @@ template <class F>
 auto with_tile(int kind, F f) {
     switch (kind) {
         case kTile256: return f(TileI8<2, 4, 4, 2>{});
+        case kTile256x192: return f(TileI8<2, 3, 4, 2>{});
         case kTile128: return f(TileI8<2, 2, 2, 2>{});
         case kTile128x64: return f(TileI8<1, 2, 4, 1>{});
         case kTile128x32: return f(TileI8<1, 1, 4, 1>{});

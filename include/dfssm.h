@@ -483,7 +483,7 @@ dfssm_status dfssm_int8_gemm(const int8_t* x_q, int64_t ldx, const float* s_x, i
  * x_q and e 16-byte aligned.  Scales must be finite.  Requires K % 16 == 0.  Sums are formed in fp32 in a
  * fixed order: equal inputs give equal bits.
  * Errors: DFSSM_ERR_INVALID_ARG for a NULL or misaligned pointer, sizes <= 0 or >= 2^31, K % 16 != 0, a
- * short workspace; DFSSM_ERR_UNSUPPORTED for K > 131072 or more than 2^30 blocks of 32 tokens x 128 rows.
+ * short workspace; DFSSM_ERR_UNSUPPORTED for K > 131072, M > 2^25, V > 2^28 or M * V > 2^38.
  * The size query returns 0 for sizes that the call refuses.
  */
 size_t dfssm_cross_entropy_workspace_bytes(int64_t M, int64_t V, int64_t K);
@@ -545,7 +545,7 @@ dfssm_status dfssm_embedding_lookup_scaled(const int32_t* tokens, int64_t T, con
  * equal bits.
  * Errors: DFSSM_ERR_INVALID_ARG for a NULL or misaligned pointer, sizes <= 0 or >= 2^31, ldd < K, a type
  * that is none, accumulate other than 0 and 1, a short workspace; DFSSM_ERR_UNSUPPORTED for T > 2^24,
- * K > 131072 or ldd >= 2^31.  The size query returns 0 for sizes that the call refuses.
+ * V > 2^28, K > 131072 or ldd >= 2^31.  The size query returns 0 for sizes that the call refuses.
  */
 size_t dfssm_embedding_backward_workspace_bytes(int64_t T, int64_t V, int64_t K);
 dfssm_status dfssm_embedding_backward(const int32_t* tokens, int64_t T, const void* dout, int64_t ldd,

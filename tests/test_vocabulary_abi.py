@@ -49,7 +49,8 @@ _COMMON = [
     (dict(lse=None), 1), (dict(ws=None), 1), (dict(M=0), 1), (dict(V=0), 1), (dict(K=0), 1), (dict(K=24), 1),
     (dict(M=1 << 31), 1), (dict(V=1 << 31), 1), (dict(x_q=A + 8), 1), (dict(e=A + 4), 1), (dict(ws=A + 8), 1),
     (dict(s_x=A + 2), 1), (dict(s_e=A + 1), 1), (dict(targets=A + 2), 1), (dict(lse=A + 2), 1), (dict(n=0), 1),
-    (dict(K=131072 + 16), 2), (dict(M=(1 << 31) - 1, V=(1 << 31) - 1), 2),
+    (dict(K=131072 + 16), 2), (dict(M=(1 << 31) - 1, V=(1 << 31) - 1), 2), (dict(M=(1 << 25) + 1), 2),
+    (dict(V=(1 << 28) + 1), 2), (dict(M=1 << 24, V=(1 << 14) + 1), 2),
 ]
 
 
@@ -95,7 +96,7 @@ def test_embedding_lookup_scaled_rejects(kw, want):
 @pytest.mark.parametrize("kw,want", _EMB + [
     (dict(dout=None), 1), (dict(de=None), 1), (dict(ws=None), 1), (dict(ws=A + 4), 1), (dict(dout=A + 2), 1),
     (dict(dout=A + 1, td=1), 1), (dict(de=A + 2), 1), (dict(ldd=63), 1), (dict(td=2), 1), (dict(te=-1), 1),
-    (dict(acc=-1), 1), (dict(n=0), 1), (dict(T=(1 << 24) + 1), 2), (dict(K=131073, ldd=131073), 2), (dict(ldd=1 << 31), 2),
+    (dict(acc=-1), 1), (dict(n=0), 1), (dict(T=(1 << 24) + 1), 2), (dict(V=(1 << 28) + 1), 2), (dict(K=131073, ldd=131073), 2), (dict(ldd=1 << 31), 2),
 ])
 def test_embedding_backward_rejects(kw, want):
     assert _embgrad(**kw) == want

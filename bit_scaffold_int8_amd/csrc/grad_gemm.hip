@@ -317,7 +317,9 @@ float grad_cost(bool wide, int64_t I, int64_t J, int64_t R, int P, int splits) {
 // ones would fill badly: I = 1128 101 against 179 us with the gradient tiles, I = 300 (R 50280) 195 against 221,
 // I = 512 (R 50280) 276 against 234.
 GradShape grad_shape(int64_t I, int64_t J, int64_t R, int pieces, int min_splits, int max_splits) {
-    static const int kSplits[] = {1, 2, 3, 4, 6, 8, 12, 16, 24, 32, 48, 64};
+    // (the last: as many short tiles as the CUs hold at once, 3 a CU with two pieces, 2 with one)
+    const int64_t short_tiles = (I + Short::BM - 1) / Short::BM * ((J + Wide::BN - 1) / Wide::BN);
+    const int kSplits[] = {1, 2, 3, 4, 6, 8, 12, 16, 24, 32, 48, 64, (int)((pieces == 2 ? 768 : 512) / short_tiles)};
     GradShape best{0, min_splits, 3.0e38f};
     const int64_t ti = (I + Wide::BM - 1) / Wide::BM, tj = (J + Wide::BN - 1) / Wide::BN;
     for (int s : kSplits) {

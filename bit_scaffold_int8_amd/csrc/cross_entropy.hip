@@ -13,10 +13,14 @@
 //
 // Backward, one piece of the vocabulary at a time: a tile kernel forms the piece's logits again and
 // from them d, twice: d s_e with the vocabulary contiguous (for dx) and d s_x with the tokens contiguous
-// (for de), as bf16 pieces (grad_gemm.h); two products with the codes then give the piece's rows of de
+// (for de), in 16-bit pieces (grad_gemm.h); two products with the codes then give the piece's rows of de
 // and its share of dx.  The gradient's type sets the pieces: fp32 takes two (relative error at most
-// 2^-16 of each d), bf16 one (2^-8, the size of the final rounding).  Recomputing the logits costs one
+// 2^-19 of each d), bf16 one (2^-11, an eighth of the final rounding).  Recomputing the logits costs one
 // int8 product; keeping them would cost 4 M V bytes written and read.
+//
+// What bounds it: forward, the int8 products under the power limit (tile_i8.h); backward, 4096 tokens x 50280 rows x
+// 2048 fp32 in 2.9 ms: the products for dx and de 1.25 and 1.3 ms (grad_gemm.h), the gradient tiles 0.65 ms, of which
+// about 0.25 are their 8 bytes a logit (1.6 GB), written in bursts between the products.
 #include <math.h>
 
 #include "grad_gemm.h"
@@ -164,24 +168,65 @@ struct GradArgs {
     const int32_t* targets;
     const float* lse;
     const float* dloss;
+    const float* maxima; // [3][kMaximaBlocks]: of |s_e|, |dloss|, |dloss s_x| (tokens that count)
     uint16_t* gx;        // [tokens][Vp P]: d s_e, or NULL
     uint16_t* gw;        // [Vp][Mp P]: d s_x, or NULL
     int64_t ldgx, ldgw;  // elements
 };
 
-// Two values rounded to bf16, the first in the low half.
+// Partial maxima of what bounds d s_e and d s_x (|p - [v = target]| <= 1): they scale d into fp16's range.
+__global__ __launch_bounds__(256) void grad_maxima_kernel(const float* __restrict__ s_e, int64_t V,
+                                                          const float* __restrict__ s_x,
+                                                          const float* __restrict__ dloss,
+                                                          const int32_t* __restrict__ targets, int64_t M,
+                                                          float* __restrict__ maxima) {
+    __shared__ float part[3][4];
+    const int64_t first = (int64_t)blockIdx.x * 256 + threadIdx.x, step = (int64_t)kMaximaBlocks * 256;
+    float e = 0.0f, d = 0.0f, dx = 0.0f;
+    for (int64_t i = first; i < V; i += step) e = fmaxf(e, fabsf(s_e[i]));
+    for (int64_t i = first; i < M; i += step) {
+        const int64_t target = targets[i];
+        if (target >= 0 && target < V) {
+            d = fmaxf(d, fabsf(dloss[i]));
+            dx = fmaxf(dx, fabsf(dloss[i] * s_x[i]));
+        }
+    }
+    e = wave_max(e);
+    d = wave_max(d);
+    dx = wave_max(dx);
+    if ((threadIdx.x & 63) == 0) {
+        part[0][threadIdx.x >> 6] = e;
+        part[1][threadIdx.x >> 6] = d;
+        part[2][threadIdx.x >> 6] = dx;
+    }
+    __syncthreads();
+    if (threadIdx.x < 3) {
+        const float* p = part[threadIdx.x];
+        maxima[threadIdx.x * kMaximaBlocks + blockIdx.x] = fmaxf(fmaxf(p[0], p[1]), fmaxf(p[2], p[3]));
+    }
+}
+
+// Two values rounded to bf16 or fp16, the first in the low half.
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
     typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
     return __builtin_bit_cast(uint32_t, (v2bf){(__bf16)a, (__bf16)b});
 }
+__device__ __forceinline__ uint32_t pack_fp16(float a, float b) {
+    typedef _Float16 v2h __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, (v2h){(_Float16)a, (_Float16)b});
+}
 
-// Four values as bf16: the rounded values and, with two pieces, the rounded remainders.
+// Four values in pieces: with two, rounded to bf16 and the remainders to fp16; with one, rounded to fp16.
 template <int P>
-__device__ __forceinline__ void split4(const float (&x)[4], uint2& hi, uint2& lo) {
-    hi = make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
-    if constexpr (P == 2)
-        lo = make_uint2(pack_bf16(x[0] - __uint_as_float(hi.x << 16), x[1] - __uint_as_float(hi.x & 0xFFFF0000u)),
-                        pack_bf16(x[2] - __uint_as_float(hi.y << 16), x[3] - __uint_as_float(hi.y & 0xFFFF0000u)));
+__device__ __forceinline__ void split4(const float (&x)[4], uint2& first, uint2& second) {
+    if constexpr (P == 2) {
+        first = make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
+        second = make_uint2(
+            pack_fp16(x[0] - __uint_as_float(first.x << 16), x[1] - __uint_as_float(first.x & 0xFFFF0000u)),
+            pack_fp16(x[2] - __uint_as_float(first.y << 16), x[3] - __uint_as_float(first.y & 0xFFFF0000u)));
+    } else {
+        first = make_uint2(pack_fp16(x[0], x[1]), pack_fp16(x[2], x[3]));
+    }
 }
 
 // A 32 x 32 block of pieces from a wave's LDS block to memory: 16 bytes a lane, whole rows of 64 P bytes.
@@ -210,10 +255,12 @@ __global__ __launch_bounds__(C::NT, C::kMinWaves) void grad_tile_kernel(GradArgs
     const int64_t n0 = (int64_t)pos.w * C::BW, m0 = (int64_t)pos.t * C::BT;
     const int wrows = (int)(a.V - n0 < C::BW ? a.V - n0 : C::BW);
     const int trows = (int)(a.M - m0 < C::BT ? a.M - m0 : C::BT);
+    const int lane = threadIdx.x & (kWave - 1);
+    const float max_e = a.maxima[lane], max_d = a.maxima[kMaximaBlocks + lane], max_dx = a.maxima[2 * kMaximaBlocks + lane];
     v16i acc[C::WB][C::TB];
     tile_i8<C, true>(a.e + n0 * a.K, a.K, wrows, a.x_q + m0 * a.K, a.K, trows, a.K, lds, acc);
 
-    const int lane = threadIdx.x & (kWave - 1);
+    const float up_x = grad_scale<P>(max_d, max_e, true).up, up_w = grad_scale<P>(max_dx, 0.0f, false).up;
     const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x / kWave));
     const int ww = wave % C::WW, tw = wave / C::WW;
     const int l32 = lane & 31, g = lane >> 5;
@@ -237,7 +284,8 @@ __global__ __launch_bounds__(C::NT, C::kMinWaves) void grad_tile_kernel(GradArgs
         const bool counts = t < trows && target >= 0 && target < a.vocab;
         const float sx2 = a.s_x[m] * kLog2e;
         const float l2 = counts ? a.lse[m] * kLog2e : __builtin_inff();  // (exp 0 where the token does not count)
-        const float dl = counts ? a.dloss[m] : 0.0f, dlx = dl * a.s_x[m];
+        const float dloss = counts ? a.dloss[m] : 0.0f;
+        const float dl = dloss * up_x, dlx = dloss * a.s_x[m] * up_w;
         const int tl = counts ? (int)(target - a.v0 - n0 - wn) : -1;     // the target's row in the wave's range
 #pragma unroll
         for (int b = 0; b < C::WB; ++b) {
@@ -252,26 +300,26 @@ __global__ __launch_bounds__(C::NT, C::kMinWaves) void grad_tile_kernel(GradArgs
             }
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                uint2 hi, lo;
+                uint2 first, second;
                 float x[4];
                 if (a.gx) {
 #pragma unroll
                     for (int j = 0; j < 4; ++j) x[j] = p[4 * q + j] * dl * se[b][4 * q + j];
-                    split4<P>(x, hi, lo);
-                    *reinterpret_cast<uint2*>(bx + l32 * kLd + (8 * q + 4 * g) * 2) = hi;
-                    if constexpr (P == 2) *reinterpret_cast<uint2*>(bx + l32 * kLd + 64 + (8 * q + 4 * g) * 2) = lo;
+                    split4<P>(x, first, second);
+                    *reinterpret_cast<uint2*>(bx + l32 * kLd + (8 * q + 4 * g) * 2) = first;
+                    if constexpr (P == 2) *reinterpret_cast<uint2*>(bx + l32 * kLd + 64 + (8 * q + 4 * g) * 2) = second;
                 }
                 if (a.gw) {
 #pragma unroll
                     for (int j = 0; j < 4; ++j) x[j] = p[4 * q + j] * dlx;
-                    split4<P>(x, hi, lo);
+                    split4<P>(x, first, second);
                     uint8_t* const dst = bw + (8 * q + 4 * g) * kLd + l32 * 2;
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        *reinterpret_cast<uint16_t*>(dst + j * kLd) = (uint16_t)((j < 2 ? hi.x : hi.y) >> (16 * (j & 1)));
+                        *reinterpret_cast<uint16_t*>(dst + j * kLd) = (uint16_t)((j < 2 ? first.x : first.y) >> (16 * (j & 1)));
                         if constexpr (P == 2)
                             *reinterpret_cast<uint16_t*>(dst + j * kLd + 64) =
-                                (uint16_t)((j < 2 ? lo.x : lo.y) >> (16 * (j & 1)));
+                                (uint16_t)((j < 2 ? second.x : second.y) >> (16 * (j & 1)));
                     }
                 }
             }
@@ -313,7 +361,7 @@ struct Plan {
     int splits;      // of dx's sum over a piece
     int slabs;       // fp32 slabs of dx in the workspace; 0: dx itself is the only one
     bool add;        // the pieces add to the same slabs
-    size_t gx, gw, dx, bytes;
+    size_t maxima, gx, gw, dx, bytes;
 };
 
 constexpr int64_t kMaxSlabBytes = (int64_t)512 << 20, kMaxPieceBytes = (int64_t)512 << 20;
@@ -357,6 +405,7 @@ Plan make_plan(int64_t M, int64_t V, int64_t K, bool bf16, bool want_dx, bool wa
         at += (b + 255) / 256 * 256;
         return was;
     };
+    p.maxima = take(3 * kMaximaBlocks * sizeof(float));
     if (want_dx) {
         // Each piece has slabs of its own, summed at the end: adding to a slab at the end of every piece's
         // product costs more (all workgroups read and write at once, and nothing else runs).  Not past 512 MB.
@@ -459,20 +508,24 @@ hipError_t launch_cross_entropy_backward(const int8_t* x_q, const float* s_x, in
     const Plan p = make_plan(M, V, K, bf16, dx != nullptr, de != nullptr);
     const int P = bf16 ? 1 : 2;
     uint8_t* const ws = static_cast<uint8_t*>(workspace);
+    float* const maxima = reinterpret_cast<float*>(ws + p.maxima);
+    const float *max_e = maxima, *max_d = maxima + kMaximaBlocks, *max_dx = maxima + 2 * kMaximaBlocks;
+    grad_maxima_kernel<<<kMaximaBlocks, 256, 0, stream>>>(s_e, V, s_x, dloss, targets, M, maxima);
+    if (hipError_t err = hipGetLastError()) return err;
     for (int64_t v0 = 0; v0 < V; v0 += p.piece) {
         const int64_t rows = V - v0 < p.piece ? V - v0 : p.piece;
-        GradArgs g{x_q, s_x, M, rows, v0, V, (int)K, 0, 0, e + v0 * K, s_e + v0, targets, lse, dloss,
+        GradArgs g{x_q, s_x, M, rows, v0, V, (int)K, 0, 0, e + v0 * K, s_e + v0, targets, lse, dloss, maxima,
                    dx ? reinterpret_cast<uint16_t*>(ws + p.gx) : nullptr,
                    de ? reinterpret_cast<uint16_t*>(ws + p.gw) : nullptr, p.piece * P, p.Mp * P};
         if (hipError_t err = P == 1 ? launch_grad_tiles<1>(g, stream) : launch_grad_tiles<2>(g, stream)) return err;
         if (dx) {
             float* const slab = reinterpret_cast<float*>(ws + p.dx) + (p.add ? 0 : v0 / p.piece * p.splits * M * K);
-            const GradGemmArgs a{ws + p.gx, p.piece * P * 2, g.e, K, M, K, rows, p.slabs ? slab : dx, K, M * K,
+            const GradGemmArgs a{ws + p.gx, p.piece * P * 2, g.e, K, M, K, rows, {max_d, max_e}, p.slabs ? slab : dx, K, M * K,
                                  grad_shape(M, K, rows, P, p.splits, p.splits).wide_rows, p.splits, p.add && v0 > 0, false};
             if (hipError_t err = launch_grad_gemm(a, P, stream)) return err;
         }
         if (de) {
-            const GradGemmArgs a{ws + p.gw, p.Mp * P * 2, x_q, K, rows, K, M,
+            const GradGemmArgs a{ws + p.gw, p.Mp * P * 2, x_q, K, rows, K, M, {max_dx, nullptr},
                                  static_cast<uint8_t*>(de) + v0 * K * (bf16 ? 2 : 4), K, 0,
                                  grad_shape(rows, K, M, P, 1, 1).wide_rows, 1, accumulate, bf16};
             if (hipError_t err = launch_grad_gemm(a, P, stream)) return err;

@@ -1,11 +1,15 @@
-// grad_gemm.hip -- C (+)= A B for bf16 pieces A and int8 codes B (gfx950; see grad_gemm.h).
+// grad_gemm.hip -- C (+)= A B for gradients A in bf16 and fp16 pieces and int8 codes B (gfx950; see grad_gemm.h).
 //
-// v_mfma_f32_32x32x16_bf16 with A's rows from LDS as they lie in memory (128-byte chunks, pieces
+// v_mfma_f32_32x32x16_{bf16,f16} with A's rows from LDS as they lie in memory (128-byte chunks, pieces
 // swizzled as in tile_i8.h) and B's codes in LDS as bytes, row by row.  B's fragment needs 8
 // consecutive r of one column: ds_read_b64_tr_b8 transposes 8 rows x 16 columns of bytes on the
-// way to the registers, where the codes become bf16 (exact).  Keeping B as bytes in memory and
-// LDS halves its traffic and needs no transposed copy.  With two pieces each B fragment
-// serves two products.  C's columns run along the lanes, so stores are runs of a row.
+// way to the registers, where the codes become bf16 and fp16 (exact).  Keeping B as bytes in memory and
+// LDS halves its traffic and needs no transposed copy.  C's columns run along the lanes, so stores are runs of a row.
+//
+// What bounds it: the matrix cores under the power limit.  7424 x 2048 x 4096 with two pieces ran 187 us (1.33 PFLOP/s of
+// products; the large bf16 product of the library reaches 1.41 on this GPU), at 2.0 GHz and 58 % of the matrix cores' cycles.
+// On the way: 214 us with the loads sunk to a chunk's end and LDS conflicts, 203 with both mended, 197 with the
+// staging spread between the products, 187 with the third LDS buffer.
 #include "device_common.h"
 #include "grad_gemm.h"
 
@@ -14,6 +18,8 @@ namespace dfssm {
 namespace {
 
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
+typedef _Float16 v8h __attribute__((ext_vector_type(8)));
+typedef _Float16 v2h __attribute__((ext_vector_type(2)));
 typedef int v2i __attribute__((ext_vector_type(2)));
 typedef uint32_t v4u __attribute__((ext_vector_type(4)));
 
@@ -25,13 +31,24 @@ struct GradTile {
     static constexpr int BM = 32 * MB * MW, BN = 32 * NB * NW, NT = kWave * MW * NW;
 };
 
-// Four codes (bytes of w) as bf16, in two words.  An integer of 8 bits leaves the low half of
+// Four codes (bytes of w) as bf16 and as fp16, two words each.  An integer of 8 bits leaves the low half of
 // its fp32 form zero, so the high half is its bf16 form.
-__device__ __forceinline__ void codes4_bf16(int w, uint32_t& lo, uint32_t& hi) {
+__device__ __forceinline__ void codes4_both(int w, uint32_t& b0, uint32_t& b1, uint32_t& h0, uint32_t& h1) {
     const float f0 = (float)(int8_t)w, f1 = (float)(int8_t)(w >> 8), f2 = (float)(int8_t)(w >> 16),
                 f3 = (float)(w >> 24);
-    lo = perm(__float_as_uint(f1), __float_as_uint(f0), 0x07060302u);
-    hi = perm(__float_as_uint(f3), __float_as_uint(f2), 0x07060302u);
+    b0 = perm(__float_as_uint(f1), __float_as_uint(f0), 0x07060302u);
+    b1 = perm(__float_as_uint(f3), __float_as_uint(f2), 0x07060302u);
+    h0 = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(f0, f1));
+    h1 = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(f2, f3));
+}
+
+// As fp16 alone: a byte u = code + 128 under the high byte 0x64 is the fp16 number 1024 + u; subtracting
+// 1152 leaves the code.
+__device__ __forceinline__ void codes4_fp16(int w, uint32_t& h0, uint32_t& h1) {
+    const uint32_t u = (uint32_t)w ^ 0x80808080u;
+    const v2h off = {(_Float16)1152.0f, (_Float16)1152.0f};
+    h0 = __builtin_bit_cast(uint32_t, __builtin_bit_cast(v2h, perm(0x64646464u, u, 0x04010400u)) - off);
+    h1 = __builtin_bit_cast(uint32_t, __builtin_bit_cast(v2h, perm(0x64646464u, u, 0x04030402u)) - off);
 }
 
 template <class C, int P, bool kBf16, bool kAdd>
@@ -52,7 +69,7 @@ __global__ __launch_bounds__(C::NT, C::NT / 256) void grad_gemm_kernel(GradGemmA
     const int wm = wave % C::MW, wn = wave / C::MW;
     const int l32 = lane & 31, g = lane >> 5, l16 = lane & 15;
 
-    // tiles of one XCD run along i within a column of tiles: they share B's columns
+    // tiles of one XCD run along j within a row of tiles: they share A's rows
     const int nt = nti * ntj;
     const int per = nt >> 3, rem = nt & 7, xcd = blockIdx.x & 7;
     const int tile = xcd * per + (xcd < rem ? xcd : rem) + (int)(blockIdx.x >> 3);
@@ -63,6 +80,7 @@ __global__ __launch_bounds__(C::NT, C::NT / 256) void grad_gemm_kernel(GradGemmA
     const int nchunks = (int)((a.R + kR - 1) / kR);
     const int c0 = blockIdx.y * chunks_per_split;
     const int c1 = c0 + chunks_per_split < nchunks ? c0 + chunks_per_split : nchunks;
+    const float max_a = a.maxima.a[lane], max_b = a.maxima.b ? a.maxima.b[lane] : 0.0f;
 
     const __amdgpu_buffer_rsrc_t ar = make_rsrc(a.a + i0 * a.lda, (uint32_t)((rows - 1) * a.lda + (int64_t)nchunks * 128));
     const int arow = tid >> 3, apiece = tid & 7;
@@ -114,13 +132,16 @@ __global__ __launch_bounds__(C::NT, C::NT / 256) void grad_gemm_kernel(GradGemmA
 
     // step s of a chunk: 16 r of one piece of A with the fragments of B it needs
     struct Frags {
-        v8bf a[C::MB];
+        v4u a[C::MB];
+    };
+    struct Codes {
+        v4u bf[P == 2 ? C::NB : 1], h[C::NB];
     };
     auto read_a = [&](int cur, int p, int s, Frags& f) {
         const int piece = (P == 1 ? 0 : 4 * p) + 2 * s + g;
 #pragma unroll
         for (int x = 0; x < C::MB; ++x)
-            f.a[x] = *reinterpret_cast<const v8bf*>(afrag + cur + x * 32 * 128 + ((piece ^ sw7) << 4));
+            f.a[x] = *reinterpret_cast<const v4u*>(afrag + cur + x * 32 * 128 + ((piece ^ sw7) << 4));
     };
     auto read_b = [&](int cur, int s, v2i (&w)[C::NB]) {
 #pragma unroll
@@ -128,24 +149,38 @@ __global__ __launch_bounds__(C::NT, C::NT / 256) void grad_gemm_kernel(GradGemmA
             w[y] = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
                 (__attribute__((address_space(3))) v2i*)(bfrag + cur + s * 16 * kLdB + y * 32));
     };
-    auto convert = [&](const v2i (&w)[C::NB], v8bf (&fb)[C::NB]) {
+    auto convert = [&](const v2i (&w)[C::NB], Codes& f) {
 #pragma unroll
         for (int y = 0; y < C::NB; ++y) {
-            uint32_t p0, p1, p2, p3;
-            codes4_bf16(w[y].x, p0, p1);
-            codes4_bf16(w[y].y, p2, p3);
-            fb[y] = __builtin_bit_cast(v8bf, (v4u){p0, p1, p2, p3});
+            uint32_t h0, h1, h2, h3;
+            if constexpr (P == 2) {
+                uint32_t b0, b1, b2, b3;
+                codes4_both(w[y].x, b0, b1, h0, h1);
+                codes4_both(w[y].y, b2, b3, h2, h3);
+                f.bf[y] = (v4u){b0, b1, b2, b3};
+            } else {
+                codes4_fp16(w[y].x, h0, h1);
+                codes4_fp16(w[y].y, h2, h3);
+            }
+            f.h[y] = (v4u){h0, h1, h2, h3};
         }
     };
-    auto multiply = [&](const Frags& f, const v8bf (&fb)[C::NB]) {
+    // first: the piece is the bf16 one
+    auto multiply = [&](const Frags& f, const Codes& b, bool first) {
 #pragma unroll
         for (int x = 0; x < C::MB; ++x)
 #pragma unroll
-            for (int y = 0; y < C::NB; ++y)
-                acc[x][y] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f.a[x], fb[y], acc[x][y], 0, 0, 0);
+            for (int y = 0; y < C::NB; ++y) {
+                if (P == 2 && first)
+                    acc[x][y] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                        __builtin_bit_cast(v8bf, f.a[x]), __builtin_bit_cast(v8bf, b.bf[P == 2 ? y : 0]), acc[x][y], 0, 0, 0);
+                else
+                    acc[x][y] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(v8h, f.a[x]),
+                                                                       __builtin_bit_cast(v8h, b.h[y]), acc[x][y], 0, 0, 0);
+            }
     };
 
-    #pragma unroll
+#pragma unroll
     for (int i = 0; i < 3; ++i) {
         const int c = c0 + i;
         const int ao = a_offset(c);
@@ -166,14 +201,13 @@ __global__ __launch_bounds__(C::NT, C::NT / 256) void grad_gemm_kernel(GradGemmA
     // barrier, so the products go on right behind it), the third is written from the registers.
     Frags f0, f1;
     v2i w0[C::NB], w1[C::NB];
-    v8bf fb[C::NB];
+    Codes fb, fn;
     lds_barrier();
     int cur = 0, nxt = kBuf, far = 2 * kBuf;
     auto at = [&](int buf, int i, Frags& f) {
         if constexpr (P == 1) read_a(buf, 0, i, f);
         else read_a(buf, i & 1, i >> 1, f);
     };
-    v8bf fn[C::NB];
     at(0, 0, f0);
     read_b(0, 0, w0);
     if constexpr (P == 1) read_b(0, 1, w1);
@@ -208,25 +242,25 @@ __global__ __launch_bounds__(C::NT, C::NT / 256) void grad_gemm_kernel(GradGemmA
         if constexpr (P == 1) {
             at(cur, 1, f1);
             stage(0);
-            multiply(f0, fb);
+            multiply(f0, fb, false);
             convert(w1, fn);
             read_b(cur, 2, w0);
             spread();
             at(cur, 2, f0);
             stage(1);
-            multiply(f1, fn);
+            multiply(f1, fn, false);
             convert(w0, fb);
             read_b(cur, 3, w1);
             spread();
             at(cur, 3, f1);
             stage(2);
-            multiply(f0, fb);
+            multiply(f0, fb, false);
             convert(w1, fn);
             read_b(nxt, 0, w0);
             spread();
             at(nxt, 0, f0);
             stage(3);
-            multiply(f1, fn);
+            multiply(f1, fn, false);
             convert(w0, fb);
             read_b(nxt, 1, w1);
             spread();
@@ -234,21 +268,21 @@ __global__ __launch_bounds__(C::NT, C::NT / 256) void grad_gemm_kernel(GradGemmA
             at(cur, 1, f1);
             read_b(cur, 1, w1);
             stage(0);
-            multiply(f0, fb);
+            multiply(f0, fb, true);
             spread();
             at(cur, 2, f0);
             stage(1);
-            multiply(f1, fb);
+            multiply(f1, fb, false);
             convert(w1, fn);
             spread();
             at(cur, 3, f1);
             stage(2);
-            multiply(f0, fn);
+            multiply(f0, fn, true);
             read_b(nxt, 0, w0);
             spread();
             at(nxt, 0, f0);
             stage(3);
-            multiply(f1, fn);
+            multiply(f1, fn, false);
             convert(w0, fb);
             spread();
         }
@@ -259,6 +293,7 @@ __global__ __launch_bounds__(C::NT, C::NT / 256) void grad_gemm_kernel(GradGemmA
         lds_barrier();
     }
 
+    const float down = grad_scale<P>(max_a, max_b, a.maxima.b != nullptr).down;
 #pragma unroll
     for (int y = 0; y < C::NB; ++y) {
         const int col = wn * C::NB * 32 + y * 32 + l32;
@@ -272,10 +307,10 @@ __global__ __launch_bounds__(C::NT, C::NT / 256) void grad_gemm_kernel(GradGemmA
                 const int64_t at = blockIdx.y * a.slab + (i0 + row) * a.ldc + j0 + col;
                 if constexpr (kBf16) {
                     __bf16* p = static_cast<__bf16*>(a.c) + at;
-                    *p = (__bf16)(kAdd ? (float)*p + acc[x][y][v] : acc[x][y][v]);
+                    *p = (__bf16)(kAdd ? (float)*p + down * acc[x][y][v] : down * acc[x][y][v]);
                 } else {
                     float* p = static_cast<float*>(a.c) + at;
-                    *p = kAdd ? *p + acc[x][y][v] : acc[x][y][v];
+                    *p = kAdd ? *p + down * acc[x][y][v] : down * acc[x][y][v];
                 }
             }
     }

@@ -1,6 +1,6 @@
 """Cross entropy over the int8 vocabulary matrix and its gradients against the fp64 formula.
 
-The bounds (vocabulary_reference.py) count fp32 roundings, and for the gradients the bf16 pieces of
+The bounds (vocabulary_reference.py) count fp32 roundings, and for the gradients the 16-bit pieces of
 d: elementwise, relative to the magnitude of the terms summed.
 """
 import pytest
@@ -179,6 +179,23 @@ def test_negative_scales(torch_cuda):
     _check_backward(ops, dloss, dx, de, False)
 
 
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("sx,se,sd", [(1e-20, 1.0, 1.0), (1.0, 1e-12, 1.0), (1.0, 1.0, 1e25), (1e-3, 1e-3, 1e-25),
+                                      (1e12, 1e-12, 1e-12)])
+def test_scales_of_any_size(torch_cuda, sx, se, sd, bf16):
+    """The pieces' common scale follows the inputs': tiny and huge scales and losses, mixed within a batch."""
+    import torch
+    import vocabulary_reference as ref
+    x_q, s_x, e, s_e, targets = ref.head(70, 600, 64, seed=14)
+    spread = torch.logspace(0, -6, 70, device="cuda")
+    ops = (x_q, s_x * sx * spread, e, s_e * se, targets)
+    loss, lse = _forward(ops)
+    _check_forward(ops, loss, lse)
+    dloss = torch.rand(70, device="cuda") * sd * spread.flip(0)
+    dx, de = _backward(ops, lse, dloss, bf16)
+    _check_backward(ops, dloss, dx, de, bf16)
+
+
 def test_gradients_against_differences(torch_cuda):
     """Along the scales: d loss / d s_x[m] = sum_k dx[m][k] x_q[m][k], and the same for s_e with de;
     central differences of the fp64 loss.  Step h = 1e-5 relative: the differences' own error is h^2 of the
@@ -289,8 +306,9 @@ def test_matrix_past_32_bits(torch_cuda):
     X = x_q.double() * s_x.double()[:, None]
     for rows in (slice(0, 64), slice(V - 64, V), slice(V // 2, V // 2 + 64)):
         w = d[:, rows].t().contiguous() @ X
-        bound = (d[:, rows].abs() * (ref.UB ** 2 + 70 * ref.U) + (d[:, rows].abs() + 1e-12) * (2 * b_lse + 8 * ref.U)[:, None])
-        ref.within(de[rows], w, bound.t().contiguous() @ X.abs() + 1e-38, "de")
+        bound = (d[:, rows].abs() * (2.0 ** -19 + 70 * ref.U) + (d[:, rows].abs() + 1e-12) * (2 * b_lse + 8 * ref.U)[:, None])
+        floor = 2.0 ** -46 * float(s_x.max()) * x_q.double().abs().sum(0)[None, :]
+        ref.within(de[rows], w, bound.t().contiguous() @ X.abs() + floor + 1e-38, "de")
     wx = torch.zeros(M, K, dtype=torch.float64, device="cuda")
     mx = torch.zeros_like(wx)
     for i in range(0, V, 100_000):
@@ -298,4 +316,5 @@ def test_matrix_past_32_bits(torch_cuda):
         wx += d[:, i:i + 100_000].contiguous() @ E
         mx += d[:, i:i + 100_000].abs().contiguous() @ E.abs()
     # sums in fp32 over 1.1 million terms: depth R / 16 steps of a product's 16 terms
-    ref.within(dx, wx, mx * (ref.UB ** 2 + (V / 16 + 64) * ref.U + float(2 * b_lse.max()) + 8 * ref.U), "dx")
+    floor = 2.0 ** -46 * float(s_e.max()) * 127 * V
+    ref.within(dx, wx, mx * (2.0 ** -19 + (V / 16 + 64) * ref.U + float(2 * b_lse.max()) + 8 * ref.U) + floor, "dx")

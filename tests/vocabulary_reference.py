@@ -76,16 +76,21 @@ def gradients(x_q, s_x, e, s_e, targets, dloss):
 
 def gradient_bounds(x_q, s_x, e, s_e, d, p, g, lse, z, bf16):
     """Elementwise absolute bounds of dx and de.  d's own error: p to the exponent's error (two times the
-    forward bound, which holds the logit's and lse's) plus 3 steps of the exponential and products, and 3
-    roundings of d; its pieces 2^-16 (2^-8 for bf16); the sums one rounding a term at the most."""
+    forward bound, which holds the logit's and lse's) plus 3 steps of the exponential and products, and 4
+    roundings of d; the sums one rounding a term at the most.  Its pieces: bf16 and an fp16 remainder 2^-8 2^-11 =
+    2^-19, or fp16 alone 2^-11; and half a step of fp16's smallest numbers, 2^-25, before the values are
+    scaled back from 2^23 (2^15) over at most 4 times the largest possible one: 2^-25 4 / 2^23 = 2^-46 (2^-38) of it."""
     V, M = e.shape[0], x_q.shape[0]
     b_lse, _ = loss_bounds(z, lse, V)
-    err = g.abs()[:, None] * p * (2 * b_lse + 4 * U)[:, None] + d.abs() * 4 * U
-    piece = UB if bf16 else UB * UB
-    aE = e.double().abs() * s_e.double().abs()[:, None]
-    aX = x_q.double().abs() * s_x.double().abs()[:, None]
-    bx = (err + d.abs() * (piece + (V + 64) * U)) @ aE
-    bw = (err + d.abs() * (piece + (M + 64) * U)).t().contiguous() @ aX
+    err = g.abs()[:, None] * p * (2 * b_lse + 4 * U)[:, None] + d.abs() * 5 * U
+    piece, floor = (2.0 ** -11, 2.0 ** -38) if bf16 else (2.0 ** -19, 2.0 ** -46)
+    codes_e, codes_x = e.double().abs(), x_q.double().abs()
+    aE = codes_e * s_e.double().abs()[:, None]
+    aX = codes_x * s_x.double().abs()[:, None]
+    top_x = float(g.abs().max()) * float(s_e.abs().max())
+    top_w = float((g * s_x.double()).abs().max())
+    bx = (err + d.abs() * (piece + (V + 64) * U)) @ aE + floor * top_x * codes_e.sum(0)[None, :]
+    bw = (err + d.abs() * (piece + (M + 64) * U)).t().contiguous() @ aX + floor * top_w * codes_x.sum(0)[None, :]
     return bx, bw
 
 

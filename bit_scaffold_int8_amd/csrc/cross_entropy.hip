@@ -31,7 +31,7 @@ namespace dfssm {
 namespace {
 
 constexpr float kLog2e = 1.44269504088896340736f;
-constexpr float kLn2 = 0.69314718055994530942f;
+constexpr double kLn2 = 0.69314718055994530942;
 
 struct LossArgs {
     const int8_t* x_q;
@@ -134,7 +134,7 @@ __global__ __launch_bounds__(1024) void loss_join_kernel(LossArgs a, const int32
     float s = p.y == 0.0f ? 0.0f : p.y * __builtin_amdgcn_exp2f(p.x - all);
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) s += __shfl_xor(s, d);
-    const float l = (all + __log2f(s)) * kLn2;
+    const float l = (float)(((double)all + (double)__log2f(s)) * kLn2);  // (one rounding, of the result)
 
     const int32_t target = targets[m];
     float out = 0.0f;
@@ -282,17 +282,18 @@ __global__ __launch_bounds__(C::NT, C::kMinWaves) void grad_tile_kernel(GradArgs
         const int64_t m = m0 + (t < trows ? t : trows - 1);
         const int64_t target = a.targets[m];
         const bool counts = t < trows && target >= 0 && target < a.vocab;
-        const float sx2 = a.s_x[m] * kLog2e;
-        const float l2 = counts ? a.lse[m] * kLog2e : __builtin_inff();  // (exp 0 where the token does not count)
+        // (p is formed from z - lse: in base 2 the roundings of lse log2 e and s_x log2 e would be p's largest errors;
+        // 0 where the token does not count)
+        const float sx = a.s_x[m], lse = counts ? a.lse[m] : __builtin_inff();
         const float dloss = counts ? a.dloss[m] : 0.0f;
-        const float dl = dloss * up_x, dlx = dloss * a.s_x[m] * up_w;
+        const float dl = dloss * up_x, dlx = dloss * sx * up_w;
         const int tl = counts ? (int)(target - a.v0 - n0 - wn) : -1;     // the target's row in the wave's range
 #pragma unroll
         for (int b = 0; b < C::WB; ++b) {
             float p[16];
 #pragma unroll
             for (int v = 0; v < 16; ++v)
-                p[v] = __builtin_amdgcn_exp2f(__builtin_fmaf(se[b][v] * (float)acc[b][tb][v], sx2, -l2));
+                p[v] = __builtin_amdgcn_exp2f(__builtin_fmaf(se[b][v] * (float)acc[b][tb][v], sx, -lse) * kLog2e);
             if (__ballot(tl >= b * 32 && tl < b * 32 + 32)) {
 #pragma unroll
                 for (int v = 0; v < 16; ++v)
@@ -364,7 +365,7 @@ struct Plan {
     size_t maxima, gx, gw, dx, bytes;
 };
 
-constexpr int64_t kMaxSlabBytes = (int64_t)512 << 20, kMaxPieceBytes = (int64_t)512 << 20;
+constexpr int64_t kMaxSlabBytes = (int64_t)512 << 20, kMaxPieceBytes = (int64_t)640 << 20;
 
 // About how long a piece takes: its gradient tiles and its products (dx with the slabs it adds), and the launches.
 float piece_cost(int64_t M, int64_t rows, int64_t K, int P, bool want_dx, bool want_de) {
@@ -377,9 +378,9 @@ Plan make_plan(int64_t M, int64_t V, int64_t K, bool bf16, bool want_dx, bool wa
     const int P = bf16 ? 1 : 2;
     Plan p{};
     p.Mp = (M + 255) / 64 * 64;
-    // The longest piece whose d takes at most 512 MB (2048 rows at the least); among pieces up to it, the one that
+    // The longest piece whose d takes at most 640 MB (2048 rows at the least); among pieces up to it, the one that
     // wastes least: pieces of equal length, and pieces whose tiles of de fill whole rounds of the 256 CUs, with
-    // a short last one (4096 tokens x 50280 rows: 6 rounds of 8192 rows and a rest instead of 7 of 7424).
+    // a short last one (4096 tokens x 50280 rows: 3 pieces of 16384 rows, two rounds each, and a rest, instead of 7 of 7424).
     const int64_t per_row = p.Mp * P * 2 * ((want_dx ? 1 : 0) + (want_de ? 1 : 0));
     const int64_t all = ceil_div(V, 256);
     int64_t most = kMaxPieceBytes / per_row / 256;

@@ -4,8 +4,8 @@
 //   backward:  de[v] (+)= scale sum over the t with tokens[t] = v of dout[t]
 //
 // The gradient is a scatter of T rows into V, with rows hit any number of times.  Float atomics
-// would add in an order that changes from run to run, so the tokens are sorted (stable radix sort by 8 bits a
-// pass; equal tokens stay in their order) and each row's sum runs over its tokens in order.  The sorted list
+// would add in an order that changes from run to run, so the tokens are sorted (up to 8192 by counting, more in
+// stable radix passes of 8 bits; equal tokens stay in their order) and each row's sum runs over its tokens in order.  The sorted list
 // is cut into pieces of equal length, so that a token that fills half the batch is summed by many
 // workgroups: a piece writes the rows that lie wholly in it, and the sums of a row that crosses its
 // ends go to the workspace, from where a second kernel joins them in order.
@@ -137,57 +137,46 @@ __device__ __forceinline__ int scan256(int v, int32_t* part) {
 // A token's sort key: tokens outside the vocabulary sort behind all others.
 __device__ __forceinline__ uint32_t token_key(int32_t id, uint32_t V) { return id >= 0 && (uint32_t)id < V ? (uint32_t)id : V; }
 
-// Few tokens (1024 R at the most): every pass in one workgroup.
-constexpr int kOneWaves = 16;
+// Few tokens: a token's place is the number of tokens with a smaller key and of earlier ones with the same.
+// A group places 64 tokens, one a lane; its 16 waves share the keys, which are uniform and come as scalar loads,
+// two vector instructions a key (4096 tokens 9.9 us; radix passes by one workgroup took 12.8).  The key is the id as an
+// unsigned number: ids outside the vocabulary come behind all others, in any order.
+constexpr int kRankMost = 8192, kRankWaves = 16;
 
-template <int R>
-__global__ __launch_bounds__(kOneWaves * 64) void sort_one_kernel(const int32_t* __restrict__ tokens, int T, uint32_t V,
-                                                                  int passes, uint32_t* __restrict__ keys,
-                                                                  int32_t* __restrict__ order) {
-    __shared__ SortShared<kOneWaves> sh;
-    __shared__ uint32_t skey[kOneWaves * R * 64];
-    __shared__ int32_t sidx[kOneWaves * R * 64];
-    __shared__ int32_t part[4];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    uint32_t key[R];
-    int32_t idx[R];
-    bool live[R];
-    int digit[R], rank[R];
-    const int i0 = wave * R * 64 + lane;
+__global__ __launch_bounds__(kRankWaves * 64) void sort_rank_kernel(const uint32_t* __restrict__ tokens, int T,
+                                                                    uint32_t* __restrict__ keys,
+                                                                    int32_t* __restrict__ order) {
+    __shared__ int32_t part[kRankWaves][64];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    const int b0 = (int)blockIdx.x * 64, b1 = b0 + 64 < T ? b0 + 64 : T, t = b0 + lane;
+    const uint32_t key = tokens[t < T ? t : T - 1];
+    // (a multiple of 64: the group's own tokens are one wave's, and loads are aligned)
+    const int share = (T + kRankWaves * 64 - 1) / (kRankWaves * 64) * 64;
+    const int begin = wave * share, end = begin + share < T ? begin + share : T;
+    int place = 0;
+    // earlier tokens count where their key is the same, too
+    const int e0 = end < b0 ? end : b0;
+#pragma unroll 32
+    for (int j = begin; j < e0; ++j) place += tokens[j] <= key;
+    if (begin <= b0 && b0 < end) {  // the group's own tokens: the lanes hold them
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-        const int i = i0 + r * 64;
-        live[r] = i < T;
-        idx[r] = i;
-        key[r] = live[r] ? token_key(tokens[i], V) : 0u;
-    }
-    for (int p = 0; p < passes; ++p) {
-        block_ranks<kOneWaves, R>(key, live, 8 * p, sh, digit, rank);
-        const int start = scan256(threadIdx.x < 256 ? sh.total[threadIdx.x] : 0, part);
-        if (threadIdx.x < 256) sh.start[threadIdx.x] = start;
-        __syncthreads();
-#pragma unroll
-        for (int r = 0; r < R; ++r)
-            if (live[r]) {
-                const int at = sh.start[digit[r]] + rank[r];
-                skey[at] = key[r];
-                sidx[at] = idx[r];
-            }
-        __syncthreads();
-#pragma unroll
-        for (int r = 0; r < R; ++r)
-            if (live[r]) {
-                key[r] = skey[i0 + r * 64];
-                idx[r] = sidx[i0 + r * 64];
-            }
-        __syncthreads();
-    }
-#pragma unroll
-    for (int r = 0; r < R; ++r)
-        if (live[r]) {
-            keys[i0 + r * 64] = key[r];
-            order[i0 + r * 64] = idx[r];
+        for (int i = 0; i < 64; ++i) {
+            const uint32_t k = (uint32_t)__builtin_amdgcn_readlane((int)key, i);
+            if (i < b1 - b0) place += i < lane ? k <= key : k < key;
         }
+    }
+#pragma unroll 32
+    for (int j = begin > b1 ? begin : b1; j < end; ++j) place += tokens[j] < key;
+    part[wave][lane] = place;
+    __syncthreads();
+    if (wave == 0 && t < T) {
+        int at = 0;
+#pragma unroll
+        for (int w = 0; w < kRankWaves; ++w) at += part[w][lane];
+        keys[at] = key;
+        order[at] = t;
+    }
 }
 
 // Many tokens, blocks of 512 R items.  A pass is two kernels: how often each digit occurs in each block ...
@@ -458,13 +447,15 @@ struct Plan {
 
 Plan make_plan(int64_t T, int64_t V, int64_t K) {
     Plan p{};
-    // pieces of 32 tokens, longer ones past 32768 tokens (1024 pieces fill the GPU)
-    p.piece = ((T + 1023) / 1024 + 31) / 32 * 32;
+    // pieces of 8 tokens (one batch of loads: 4096 tokens of width 2048 20.3 us against 30.5 in pieces of 32), longer ones
+    // past 8192 tokens, where 1024 pieces fill the GPU and shorter ones only leave more to join (16384 tokens: 104
+    // against 96 us)
+    p.piece = T <= kRankMost ? 8 : ((T + 1023) / 1024 + 31) / 32 * 32;
     p.pieces = (int)((T + p.piece - 1) / p.piece);
-    // sorted by one workgroup, or in blocks of 1024 tokens; of 4096 where so many blocks' counts would take long to
-    // add up (each block reads all)
-    p.sort_block = T <= 4096 ? 4096 : T <= 65536 ? kManyThreads * 2 : kManyThreads * 8;
-    p.sort_blocks = (int)((T + p.sort_block - 1) / p.sort_block);
+    // radix passes in blocks of 1024 tokens; of 4096 where so many blocks' counts would take long to add up
+    // (each block reads all)
+    p.sort_block = T <= 65536 ? kManyThreads * 2 : kManyThreads * 8;
+    p.sort_blocks = T <= kRankMost ? 0 : (int)((T + p.sort_block - 1) / p.sort_block);
     p.passes = 1;
     while (p.passes < 4 && ((uint64_t)V >> (8 * p.passes)) != 0) ++p.passes;  // keys 0 .. V
     size_t at = 0;
@@ -546,9 +537,9 @@ hipError_t launch_embedding_backward(const int32_t* tokens, int64_t T, const voi
     int32_t* order[2] = {reinterpret_cast<int32_t*>(ws + p.order[0]), reinterpret_cast<int32_t*>(ws + p.order[1])};
     int32_t* hist = reinterpret_cast<int32_t*>(ws + p.hist);
     int at = 0;
-    if (p.sort_blocks == 1) {
-        if (T <= 1024) sort_one_kernel<1><<<1, kOneWaves * 64, 0, stream>>>(tokens, (int)T, (uint32_t)V, p.passes, keys[0], order[0]);
-        else sort_one_kernel<4><<<1, kOneWaves * 64, 0, stream>>>(tokens, (int)T, (uint32_t)V, p.passes, keys[0], order[0]);
+    if (p.sort_blocks == 0) {
+        sort_rank_kernel<<<dim3((unsigned)((T + 63) / 64)), kRankWaves * 64, 0, stream>>>(
+            reinterpret_cast<const uint32_t*>(tokens), (int)T, keys[0], order[0]);
     } else {
         const dim3 grid((unsigned)p.sort_blocks);
         for (int i = 0; i < p.passes; ++i) {

@@ -465,6 +465,8 @@ def dfssm_cross_entropy(x_q, s_x, e, s_e, targets, loss, lse, workspace, stream=
 
 def dfssm_cross_entropy_backward_workspace_bytes(M: int, V: int, K: int, dx, de) -> int:
     """For the gradients dx and de (tensors, or None for one that is not wanted)."""
+    if dx is None and de is None:
+        raise ValueError("dfssm_cross_entropy_backward_workspace_bytes: dx or de expected")
     t = _type("dx, de", de if dx is None else dx)
     return int(lib.dfssm_cross_entropy_backward_workspace_bytes(M, V, K, t, dx is not None, de is not None))
 

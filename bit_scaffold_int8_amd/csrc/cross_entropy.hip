@@ -19,7 +19,7 @@
 // int8 product; keeping them would cost 4 M V bytes written and read.
 //
 // What bounds it: forward, the int8 products under the power limit (tile_i8.h); backward, 4096 tokens x 50280 rows x
-// 2048 fp32 in 2.9 ms: the products for dx and de 1.25 and 1.3 ms (grad_gemm.h), the gradient tiles 0.65 ms, of which
+// 2048 fp32 in 3.3 ms: the products for dx and de 1.28 and 1.34 ms (grad_gemm.h), the gradient tiles 0.65 ms, of which
 // about 0.25 are their 8 bytes a logit (1.6 GB), written in bursts between the products.
 #include <math.h>
 
@@ -174,7 +174,8 @@ struct GradArgs {
     int64_t ldgx, ldgw;  // elements
 };
 
-// Partial maxima of what bounds d s_e and d s_x (|p - [v = target]| <= 1): they scale d into fp16's range.
+// Partial maxima of what bounds d s_e and d s_x (|p - [v = target]| <= 1): they scale d into fp16's range.  An infinite
+// factor takes no part: its own gradients are infinite or NaN at any scale, and the others keep theirs.
 __global__ __launch_bounds__(256) void grad_maxima_kernel(const float* __restrict__ s_e, int64_t V,
                                                           const float* __restrict__ s_x,
                                                           const float* __restrict__ dloss,
@@ -187,8 +188,9 @@ __global__ __launch_bounds__(256) void grad_maxima_kernel(const float* __restric
     for (int64_t i = first; i < M; i += step) {
         const int64_t target = targets[i];
         if (target >= 0 && target < V) {
-            d = fmaxf(d, fabsf(dloss[i]));
-            dx = fmaxf(dx, fabsf(dloss[i] * s_x[i]));
+            const float l = fabsf(dloss[i]), lx = fabsf(dloss[i] * s_x[i]);
+            if (l < __builtin_inff()) d = fmaxf(d, l);
+            if (lx < __builtin_inff()) dx = fmaxf(dx, lx);
         }
     }
     e = wave_max(e);
@@ -283,8 +285,8 @@ __global__ __launch_bounds__(C::NT, C::kMinWaves) void grad_tile_kernel(GradArgs
         const int64_t target = a.targets[m];
         const bool counts = t < trows && target >= 0 && target < a.vocab;
         // (p is formed from z - lse: in base 2 the roundings of lse log2 e and s_x log2 e would be p's largest errors;
-        // 0 where the token does not count)
-        const float sx = a.s_x[m], lse = counts ? a.lse[m] : __builtin_inff();
+        // 0 where the token does not count, whatever its scale is)
+        const float sx = counts ? a.s_x[m] : 0.0f, lse = counts ? a.lse[m] : __builtin_inff();
         const float dloss = counts ? a.dloss[m] : 0.0f;
         const float dl = dloss * up_x, dlx = dloss * sx * up_w;
         const int tl = counts ? (int)(target - a.v0 - n0 - wn) : -1;     // the target's row in the wave's range

@@ -458,6 +458,8 @@ typedef enum {
  *   x_q  int8 [M][K], row m at x_q + m*ldx;   s_x fp32 [M]
  *   w    int8 [N][K], row n at w + n*ldw;     s_w fp32 [N]
  *   y    y_type [M][N], row m at element m*ldy, written; elements past N of a row are left
+ * At K = 131072 one of two rows must hold a code other than -128 (the accumulator ends at 2^31 - 1); the
+ * quantizer's codes, -127 to 127, always do.
  * Any alignment of x_q and w, any K; rows whose start and stride are multiples of 16 bytes, with
  * K % 16 == 0, are read fastest.  y needs its element's alignment (16 bytes and a row stride of 16
  * bytes' multiple store fastest).  y must not overlap an input.
@@ -480,8 +482,9 @@ dfssm_status dfssm_int8_gemm(const int8_t* x_q, int64_t ldx, const float* s_x, i
  *   workspace  at least dfssm_cross_entropy_workspace_bytes(M, V, K) bytes, 16-byte aligned; its
  *              contents need no preparation and mean nothing afterwards.  Calls that share one
  *              must not overlap in time; graphs captured with one may be replayed in turn.
- * x_q and e 16-byte aligned.  Scales must be finite.  Requires K % 16 == 0.  Sums are formed in fp32 in a
- * fixed order: equal inputs give equal bits.
+ * x_q and e 16-byte aligned.  Scales must be finite (one of a position that does not count may be anything: only
+ * its own lse shows it).  Requires K % 16 == 0.  Sums are formed in fp32 in a fixed order: equal inputs give
+ * equal bits.  Accumulators are dfssm_int8_gemm's.
  * Errors: DFSSM_ERR_INVALID_ARG for a NULL or misaligned pointer, sizes <= 0 or >= 2^31, K % 16 != 0, a
  * short workspace; DFSSM_ERR_UNSUPPORTED for K > 131072, M > 2^25, V > 2^28 or M * V > 2^38.
  * The size query returns 0 for sizes that the call refuses.
@@ -495,7 +498,7 @@ dfssm_status dfssm_cross_entropy(const int8_t* x_q, const float* s_x, int64_t M,
  * Gradients of dfssm_cross_entropy for the dequantized values x = s_x x_q and E = s_e e (straight
  * through the quantizers):
  *   d[m][v]  = dloss[m] * (exp(z[m][v] - lse[m]) - [v == targets[m]]);  0 for positions that do not
- *              count, whatever dloss holds there
+ *              count, whatever dloss, s_x and lse hold there
  *   dx[m][k] = sum_v d[m][v] * s_e[v] * e[v][k]
  *   de[v][k] = sum_m d[m][v] * s_x[m] * x_q[m][k]     (added to what de holds if accumulate_de)
  *   x_q, s_x, e, s_e, targets as in the forward call, lse [M] from it, dloss fp32 [M] (read)

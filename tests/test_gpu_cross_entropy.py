@@ -133,6 +133,86 @@ def test_positions_that_do_not_count(torch_cuda):
         assert torch.equal(de, base)
 
 
+@pytest.mark.parametrize("bf16", [False, True])
+def test_padding_with_any_scale(torch_cuda, bf16):
+    """Positions that do not count may hold any scale, dloss and lse: the other ones' results do not change by a bit."""
+    import torch
+    import vocabulary_reference as ref
+    for M in (5, 100, 300):
+        x_q, s_x, e, s_e, targets = ref.head(M, 1100, 64, seed=M, ignored=0.3)
+        targets[M // 2:M // 2 + 2] = -100
+        ops = (x_q, s_x, e, s_e, targets)
+        loss, lse = _forward(ops)
+        dloss = torch.rand(M, device="cuda")
+        want_x, want_e = _backward(ops, lse, dloss, bf16)
+        live = (targets >= 0) & (targets < 1100)
+        for junk in (float("nan"), float("inf"), -float("inf"), 3.0e38):
+            s_j, d_j = torch.where(live, s_x, torch.full_like(s_x, junk)), torch.where(live, dloss, torch.full_like(s_x, junk))
+            got = _forward((x_q, s_j, e, s_e, targets))
+            assert torch.equal(got[0], loss) and torch.equal(got[1][live], lse[live])
+            dx, de = _backward((x_q, s_j, e, s_e, targets), got[1], d_j, bf16)
+            assert torch.equal(dx, want_x) and torch.equal(de, want_e)
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+def test_infinite_dloss_of_one_position(torch_cuda, bf16):
+    """It stays that position's: the other tokens' gradients keep their precision."""
+    import torch
+    import vocabulary_reference as ref
+    M = 70
+    ops = ref.head(M, 600, 64, seed=3, ignored=0.0)
+    _, lse = _forward(ops)
+    for bad in (float("inf"), -float("inf"), float("nan")):
+        dloss = torch.rand(M, device="cuda") + 0.1
+        dloss[33] = bad
+        dx, _ = _backward(ops, lse, dloss, bf16, want=(True, False))
+        assert not bool(torch.isfinite(dx[33]).any())
+        rest = torch.arange(M, device="cuda") != 33
+        part = [o[rest].contiguous() if o.shape[0] == M else o for o in ops]
+        _check_backward(part, dloss[rest], dx[rest], None, bf16)
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("M,V,K", [(8200, 20000, 64), (2100, 60001, 256), (4100, 33000, 2048), (8192, 20001, 8192)])
+def test_vocabulary_in_pieces(torch_cuda, M, V, K, bf16):
+    """The vocabulary in several pieces of the workspace, with a slab of dx for each piece and split, or (the last
+    shape, 268 MB a slab) with pieces that add to one; more rows than whole rounds of the largest tiles."""
+    import torch
+    import vocabulary_reference as ref
+    print("cross_entropy pieces", M, V, K, bf16, flush=True)
+    ops = ref.head(M, V, K, seed=K)
+    loss, lse = _forward(ops)
+    _check_forward(ops, loss, lse)
+    dloss = torch.rand(M, device="cuda") / M
+    base = torch.randn(V, K, device="cuda").to(torch.bfloat16 if bf16 else torch.float32) / M
+    dx, de = _backward(ops, lse, dloss, bf16, base=base)
+    _check_backward(ops, dloss, dx, de, bf16, base=base)
+
+
+def test_two_streams_at_once(torch_cuda):
+    """Calls with workspaces of their own on two streams, with nothing between them."""
+    import torch
+    import vocabulary_reference as ref
+    sets = [ref.head(200, 9000, 512, seed=1), ref.head(333, 7000, 256, seed=2)]
+    dloss = [torch.rand(o[0].shape[0], device="cuda") for o in sets]
+    want = []
+    for o, d in zip(sets, dloss):
+        loss, lse = _forward(o)
+        want.append((loss, lse, *_backward(o, lse, d, False)))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    got = [[], []]
+    for _ in range(3):
+        for i, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                loss, lse = _forward(sets[i])
+                got[i].append((loss, lse, *_backward(sets[i], lse, dloss[i], False)))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for g in got[i]:
+            assert all(torch.equal(a, b) for a, b in zip(g, want[i]))
+
+
 def test_zero_tokens_and_zero_rows(torch_cuda):
     """Scales of zero: a token's logits are all 0 (lse = log V), a row's logit is 0; codes under a zero
     scale do not reach the other operand's gradient, but the scale's owner still has one."""

@@ -96,6 +96,24 @@ def test_gradient(torch_cuda, T, V, K, din, dout16, accumulate):
     _check(tokens, dout, 1.5, V, de, dout16, base)
 
 
+@pytest.mark.parametrize("T,V,K", [(8191, 900, 8), (8192, 1 << 15, 12), (8193, 255, 8), (9000, (1 << 24) + 3, 2),
+                                   (65536, 40000, 4), (65537, 256, 4), (8192, 3, 2048)])
+def test_where_the_sort_changes(torch_cuda, T, V, K):
+    """Lengths on both sides of the sort's variants; a vocabulary of four radix passes."""
+    import torch
+    print("embedding_backward sort", T, V, K, flush=True)
+    tokens = torch.randint(-2, V + 2, (T,), device="cuda", dtype=torch.int32)
+    tokens[T // 3:T // 3 + T // 8] = V - 1
+    tokens[::101] = -(1 << 31)
+    tokens[5::103] = (1 << 31) - 1
+    dout = torch.randn(T, K, device="cuda")
+    dout[(tokens < 0) | (tokens >= V)] = float("nan")
+    clean = torch.nan_to_num(dout)
+    for base in (None, torch.randn(V, K, device="cuda")):
+        de = _gradient(tokens, dout, 1.0, V, False, base)
+        _check(tokens, clean, 1.0, V, de, False, base)
+
+
 @pytest.mark.parametrize("T", [1, 31, 32, 33, 64, 4096, 4100, 50000])
 def test_one_token_fills_the_batch(torch_cuda, T):
     """Every position the same id (also the last row, and an id outside the vocabulary)."""

@@ -105,6 +105,20 @@ def test_outputs_past_32_bits(torch_cuda):
     _check(x, sx, w, sw, y, True)
 
 
+@pytest.mark.parametrize("M,N,K,pad", [(5, (1 << 20) + 33, 32, 0), ((1 << 17) + 40, 40, 48, 0), ((1 << 17) + 1, 33, 17, 3)])
+def test_more_rows_than_a_launch_takes(torch_cuda, M, N, K, pad):
+    """Products that go in slices of 2^20 channels and 2^17 tokens."""
+    import torch
+    from bit_scaffold_int8_amd import dfssm
+    print("int8_gemm slices", M, N, K, flush=True)
+    x, sx, w, sw = _inputs(M, N, K, 9)
+    buf = torch.full((M, N + pad), -7.0, device="cuda")
+    y = buf[:, :N]
+    dfssm.dfssm_int8_gemm(x, sx, w, sw, y)
+    _check(x, sx, w, sw, y, False)
+    assert bool((buf[:, N:] == -7.0).all())
+
+
 def test_another_stream_and_a_replayed_graph(torch_cuda):
     import torch
     from bit_scaffold_int8_amd import dfssm

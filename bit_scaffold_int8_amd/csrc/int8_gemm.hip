@@ -8,10 +8,10 @@
 // that lanes write runs of a token's row instead of 16-byte pieces of 32 rows.
 //
 // What bounds it: many tokens, the products under the power limit and, in bursts that nothing overlaps, the stores
-// (2048 x 50280 x 2048: 275 us for fp32, 249 for bf16; the loss over the same logits 235); few tokens, reading w once
+// (2048 x 50280 x 2048: 241 us for bf16; the loss over the same logits 218); few tokens, reading w once
 // (50280 x 2048, 1 to 64 tokens: 17 to 19 us, 5.5 to 6 TB/s); few rows, the latency of K's chunks (1 x 2048 x
 // 4096: 6.1 us, of which 4 do not grow with K).
-// Measured and not kept: stores past the caches (275 against 276 us for 412 MB, 545 against 517 for 824), device-scope
+// Measured and not kept (before the rest of a last round went to small tiles): stores past the caches (275 against 276 us for 412 MB, 545 against 517 for 824), device-scope
 // stores (333), two smaller tiles to a CU so that stores overlap products (310 streamed, 337 not).
 #include <type_traits>
 

@@ -16,9 +16,10 @@
 // loads run two chunks ahead (registers hold the chunk after the one in LDS).  Chunks of 64 k,
 // with three buffers or with two smaller tiles per CU, measured 8 % slower: half-line loads.
 //
-// What bounds it: 2048 tokens x 50280 rows x 2048 run 239 us as logits' statistics (1.8 POPS); without
-// staging 207 us, so most of it is the products under the power limit (the GPU clocks down to 2.0 GHz at 45 %
-// matrix-core occupancy) and each tile's epilogue (about 5 of 33 us), which nothing overlaps.
+// What bounds it: 2048 tokens x 50280 rows x 2048 ran 239 us as logits' statistics in 7 rounds of 256 x 256 tiles (1.8
+// POPS; 218 us since the last round's rest goes to small tiles); without staging 207, so most of it is the products
+// under the power limit (the GPU clocks down to 2.0 GHz at 45 % matrix-core occupancy) and each tile's epilogue (about
+// 5 of 33 us), which nothing overlaps.
 #pragma once
 
 #include "device_common.h"
@@ -26,8 +27,7 @@
 namespace dfssm {
 
 constexpr int kTileChunk = 128;               // k bytes per chunk
-constexpr int kTileDead = 0x40000000;         // a load offset past every tile's resource: reads zero
-constexpr int64_t kTileMaxLd = (int64_t)1 << 22;  // row stride limit: 256 rows stay below kTileDead
+constexpr int kTileDead = 0x40000000;         // a load offset past every tile's resource (row strides end at 2^22): reads zero
 
 // WW x TW waves, each with WB x TB blocks of 32 x 32; KS such groups of waves take every KS-th chunk of K each and
 // add up their sums through LDS (small tiles: they are used where there are few, and K's length is the time).

@@ -22,6 +22,8 @@
 // 5 of 33 us), which nothing overlaps.
 #pragma once
 
+#include <type_traits>
+
 #include "device_common.h"
 
 namespace dfssm {
@@ -87,26 +89,29 @@ struct Stager {
             for (int j = 0; j < P; ++j) row_off[j] = (int)(min(row0 + j * kRowStep, rows - 1) * ld_);
         }
     }
-    // Piece j of a chunk: off = offset(chunk) first.
+    // Piece j of a chunk: off = offset(chunk) first.  kInner: rows of 16 bytes or more, and for store a piece that
+    // its row holds.
     __device__ __forceinline__ int offset(int chunk, int K) const {
         const int k = chunk * kTileChunk + piece * 16;
         if constexpr (kFast) return off0 + (k < K ? k : kTileDead);
         return k;
     }
+    template <bool kInner = false>
     __device__ __forceinline__ void load(int j, int off, int K) {
         if constexpr (kFast) {
             const v4i r = __builtin_amdgcn_raw_buffer_load_b128(rsrc, off + j * (int)(kRowStep * ld), 0, 0);
             v[j] = make_uint4((uint32_t)r.x, (uint32_t)r.y, (uint32_t)r.z, (uint32_t)r.w);
-        } else if (K >= 16) {
+        } else if (kInner || K >= 16) {
             __builtin_memcpy(&v[j], base + (uint32_t)(row_off[j] + min(off, K - 16)), 16);
         } else {
             v[j] = load16_guarded<false>(reinterpret_cast<const uint8_t*>(base) + row_off[j], off, K);
         }
     }
     // off: the offset that piece j was loaded with.
+    template <bool kInner = false>
     __device__ __forceinline__ void store(int j, uint8_t* lds, int off, int K) const {
         uint4 r = v[j];
-        if constexpr (!kFast) {
+        if constexpr (!kFast && !kInner) {
             // only a row's last chunk (and what follows it) holds pieces that leave the row
             if (off - piece * 16 + kTileChunk > K && K >= 16) r = shift_bytes(r, max(off - (K - 16), 0));
         }
@@ -196,22 +201,23 @@ __device__ __forceinline__ bool tile_i8(const int8_t* __restrict__ w, int64_t ld
     // fragments and a quarter of the staging (registers to the other buffer, then the loads that refill
     // them).  A wave issues in order, so a burst of LDS or memory instructions would hold back the
     // products behind it; the pattern spreads them one by one over the products.
-    auto step = [&](int s, int cur, int nxt, int ow, int ot, int held, const Frags& f, Frags* next) {
+    auto step = [&](auto inner, int s, int cur, int nxt, int ow, int ot, int held, const Frags& f, Frags* next) {
+        constexpr bool kInner = decltype(inner)::value;
         if (next) read(cur, s + 1, *next);
 #pragma unroll
         for (int j = 0; j < C::PW; ++j)
             if (j * 4 / C::PW == s) {
-                sw.store(j, lds + nxt, held, K);
-                sw.load(j, ow, K);
+                sw.template store<kInner>(j, lds + nxt, held, K);
+                sw.template load<kInner>(j, ow, K);
             }
 #pragma unroll
         for (int j = 0; j < C::PT; ++j)
             if (j * 4 / C::PT == s) {
-                st.store(j, lds + nxt + kXOff, held, K);
-                st.load(j, ot, K);
+                st.template store<kInner>(j, lds + nxt + kXOff, held, K);
+                st.template load<kInner>(j, ot, K);
             }
         multiply(f);
-        if constexpr (kFast) {
+        if constexpr (kInner) {
 #pragma unroll
             for (int i = 0; i < C::WB * C::TB; ++i) {
                 __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // a product
@@ -223,7 +229,7 @@ __device__ __forceinline__ bool tile_i8(const int8_t* __restrict__ w, int64_t ld
         __builtin_amdgcn_sched_barrier(0);
     };
     Frags f0, f1;
-    for (int c = 0; c < nch; ++c) {
+    auto chunk = [&](auto inner, int c) {
         lds_barrier();
         const int cur = (c & 1) * C::kBufBytes, nxt = C::kBufBytes - cur;
         // (past the last chunk zeros are staged that nothing reads)
@@ -232,10 +238,19 @@ __device__ __forceinline__ bool tile_i8(const int8_t* __restrict__ w, int64_t ld
         const int held = st.offset((c + 1) * C::KS + kg, K);
         read(cur, 0, f0);
         __builtin_amdgcn_sched_barrier(0);
-        step(0, cur, nxt, ow, ot, held, f0, &f1);
-        step(1, cur, nxt, ow, ot, held, f1, &f0);
-        step(2, cur, nxt, ow, ot, held, f0, &f1);
-        step(3, cur, nxt, ow, ot, held, f1, nullptr);
+        step(inner, 0, cur, nxt, ow, ot, held, f0, &f1);
+        step(inner, 1, cur, nxt, ow, ot, held, f1, &f0);
+        step(inner, 2, cur, nxt, ow, ot, held, f0, &f1);
+        step(inner, 3, cur, nxt, ow, ot, held, f1, nullptr);
+    };
+    int c = 0;
+    if constexpr (kFast) {
+        for (; c < nch; ++c) chunk(std::true_type{}, c);
+    } else {
+        // without the shifts' branches while the chunk that the registers hold is inside the rows
+        // (300 rows x 4000 tokens x 8001: 43 us, 54 with them in every chunk)
+        for (const int inside = K / kTileChunk / C::KS - 1; c < inside; ++c) chunk(std::true_type{}, c);
+        for (; c < nch; ++c) chunk(std::false_type{}, c);
     }
     if constexpr (C::KS > 1) {
         int32_t* const sums = reinterpret_cast<int32_t*>(all_lds) + tid;

@@ -461,8 +461,7 @@ typedef enum {
  * At K = 131072 one of two rows must hold a code other than -128 (the accumulator ends at 2^31 - 1); the
  * quantizer's codes, -127 to 127, always do.
  * Any alignment of x_q and w, any K; rows whose start and stride are multiples of 16 bytes, with
- * K % 16 == 0, are read fastest.  y needs its element's alignment (16 bytes and a row stride of 16
- * bytes' multiple store fastest).  y must not overlap an input.
+ * K % 16 == 0, are read fastest.  y needs its element's alignment and must not overlap an input.
  * Errors: DFSSM_ERR_INVALID_ARG for a NULL pointer, sizes <= 0 or >= 2^31, ldx or ldw < K, ldy < N,
  * a type that is none, misaligned scales or y; DFSSM_ERR_UNSUPPORTED for K > 131072, ldx or ldw >
  * 2^22, ldy >= 2^40, or more than 2^30 blocks of 32 x 32 outputs.

@@ -341,6 +341,7 @@ __global__ __launch_bounds__(256) void slab_sum_kernel(const float* __restrict__
                                                        void* __restrict__ out) {
     for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4; i < n; i += (int64_t)gridDim.x * 1024) {
         v4f s = *reinterpret_cast<const v4f*>(slabs + i);
+#pragma unroll 8
         for (int k = 1; k < splits; ++k) s += *reinterpret_cast<const v4f*>(slabs + k * n + i);
         if constexpr (kBf16) {
             *reinterpret_cast<uint2*>(static_cast<uint16_t*>(out) + i) =

@@ -23,8 +23,9 @@ __global__ __launch_bounds__(256) void lookup_scaled_kernel(const int32_t* __res
                                                             const int8_t* __restrict__ e,
                                                             const float* __restrict__ s_e, int64_t V, int64_t K,
                                                             float scale, void* __restrict__ out, int64_t ldo) {
-    const int64_t k = ((int64_t)blockIdx.y * 256 + threadIdx.x) * VEC;
+    int64_t k = ((int64_t)blockIdx.y * 256 + threadIdx.x) * VEC;
     if (k >= K) return;
+    k = k + VEC <= K ? k : K - VEC;  // (a row's last vector may overlap the one before: both write the same)
     const int64_t t0 = (int64_t)blockIdx.x * kLookTokens;
     int64_t id[kLookTokens];
     float s[kLookTokens];
@@ -36,7 +37,7 @@ __global__ __launch_bounds__(256) void lookup_scaled_kernel(const int32_t* __res
         const bool in = id[j] >= 0 && id[j] < V;
         const int64_t row = in ? id[j] : 0;
         s[j] = in ? scale * s_e[row] : 0.0f;
-        __builtin_memcpy(c[j], __builtin_assume_aligned(e + row * K + k, VEC), VEC);
+        __builtin_memcpy(c[j], e + row * K + k, VEC);
         if (!in)
 #pragma unroll
             for (int i = 0; i < VEC; ++i) c[j][i] = 0;
@@ -49,12 +50,12 @@ __global__ __launch_bounds__(256) void lookup_scaled_kernel(const int32_t* __res
             uint16_t o[VEC];
 #pragma unroll
             for (int i = 0; i < VEC; ++i) o[i] = (uint16_t)bf16_bits(s[j] * (float)c[j][i]);
-            __builtin_memcpy(__builtin_assume_aligned(static_cast<uint16_t*>(out) + at, VEC * 2), o, VEC * 2);
+            __builtin_memcpy(static_cast<uint16_t*>(out) + at, o, VEC * 2);
         } else {
             float o[VEC];
 #pragma unroll
             for (int i = 0; i < VEC; ++i) o[i] = s[j] * (float)c[j][i];
-            __builtin_memcpy(__builtin_assume_aligned(static_cast<float*>(out) + at, VEC * 4), o, VEC * 4);
+            __builtin_memcpy(static_cast<float*>(out) + at, o, VEC * 4);
         }
     }
 }
@@ -273,17 +274,18 @@ struct SumArgs {
     float* tail;            // [pieces][K]: its part of a row that begins in it and goes on behind it
     int64_t piece;          // sorted tokens per piece
     int pieces, col_blocks;
+    int fill_rows;          // per workgroup that writes zeros: 8 or kFillRows
 };
 
 template <bool kBf16, int VEC>
 __device__ __forceinline__ void load_vec(const void* base, int64_t at, float (&v)[VEC]) {
     if constexpr (kBf16) {
         uint16_t b[VEC];
-        __builtin_memcpy(b, __builtin_assume_aligned(static_cast<const uint16_t*>(base) + at, VEC * 2), VEC * 2);
+        __builtin_memcpy(b, static_cast<const uint16_t*>(base) + at, VEC * 2);
 #pragma unroll
         for (int i = 0; i < VEC; ++i) v[i] = __uint_as_float((uint32_t)b[i] << 16);
     } else {
-        __builtin_memcpy(v, __builtin_assume_aligned(static_cast<const float*>(base) + at, VEC * 4), VEC * 4);
+        __builtin_memcpy(v, static_cast<const float*>(base) + at, VEC * 4);
     }
 }
 
@@ -293,9 +295,9 @@ __device__ __forceinline__ void store_vec(void* base, int64_t at, const float (&
         uint16_t b[VEC];
 #pragma unroll
         for (int i = 0; i < VEC; ++i) b[i] = (uint16_t)bf16_bits(v[i]);
-        __builtin_memcpy(__builtin_assume_aligned(static_cast<uint16_t*>(base) + at, VEC * 2), b, VEC * 2);
+        __builtin_memcpy(static_cast<uint16_t*>(base) + at, b, VEC * 2);
     } else {
-        __builtin_memcpy(__builtin_assume_aligned(static_cast<float*>(base) + at, VEC * 4), v, VEC * 4);
+        __builtin_memcpy(static_cast<float*>(base) + at, v, VEC * 4);
     }
 }
 
@@ -314,14 +316,23 @@ __device__ __forceinline__ void store_zeros(void* base, int64_t at) {
     }
 }
 
+// skip: elements of the vector that the thread before writes.
 template <bool kOutBf16, bool kAdd, int VEC>
-__device__ __forceinline__ void write_row(const SumArgs& a, uint32_t row, int64_t k, const float (&sum)[VEC]) {
+__device__ __forceinline__ void write_row(const SumArgs& a, uint32_t row, int64_t k, int skip, const float (&sum)[VEC]) {
     float o[VEC];
     const int64_t at = (int64_t)row * a.K + k;
     if constexpr (kAdd) {
         load_vec<kOutBf16, VEC>(a.de, at, o);
 #pragma unroll
         for (int i = 0; i < VEC; ++i) o[i] += a.scale * sum[i];
+        if (skip) {  // (added once)
+#pragma unroll
+            for (int i = 1; i < VEC; ++i) {
+                const float one[1] = {o[i]};
+                if (i >= skip) store_vec<kOutBf16, 1>(a.de, at + i, one);
+            }
+            return;
+        }
     } else {
 #pragma unroll
         for (int i = 0; i < VEC; ++i) o[i] = a.scale * sum[i];
@@ -329,7 +340,18 @@ __device__ __forceinline__ void write_row(const SumArgs& a, uint32_t row, int64_
     store_vec<kOutBf16, VEC>(a.de, at, o);
 }
 
-constexpr int kFillRows = 32;  // rows per workgroup that fills the rows without tokens
+// A row's vectors may start anywhere in memory; its last one is moved back to end with the row and overlaps the one
+// before by the returned number of elements, which both compute alike (16384 tokens of width 2049 125 us, element by
+// element 161; width 2048 114).
+template <int VEC>
+__device__ __forceinline__ int row_vector(int64_t& k, int64_t K) {
+    const int64_t over = k + VEC - K;
+    if (over <= 0) return 0;
+    k -= over;
+    return (int)over;
+}
+
+constexpr int kFillRows = 32;  // rows at most per workgroup that fills the rows without tokens
 
 // Workgroups [0, pieces * col_blocks) sum pieces; the ones behind them (none when adding to de) write zeros
 // to the rows that no token names.
@@ -340,34 +362,59 @@ __global__ __launch_bounds__(256) void piece_sum_kernel(SumArgs a) {
         if constexpr (!kAdd) {
             static_assert(kFillRows * 8 == 256, "8 lanes search a row");
             __shared__ int32_t named[kFillRows];
-            const int64_t r0 = (int64_t)((int)blockIdx.x - nsum) * kFillRows;
-            // the first sorted token >= row, 8 probes a step
-            const int j = threadIdx.x & 7, group = threadIdx.x & 56;
-            const uint32_t row = (uint32_t)(r0 + (threadIdx.x >> 3));
-            int lo = 0, hi = (int)a.T;
-            while (__any(lo < hi)) {
-                const int len = hi - lo, p = lo + (int)((int64_t)len * (j + 1) / 9);
-                const bool less = len > 0 && a.keys[p] < row;
-                const int n = __popcll((__ballot(less) >> group) & 255);  // the probes below the row: the first n
-                const int below = lo + (int)((int64_t)len * n / 9), above = lo + (int)((int64_t)len * (n + 1) / 9);
-                if (len > 0) {
-                    if (n < 8) hi = above;
-                    if (n > 0) lo = below + 1;
+            const int64_t r0 = (int64_t)((int)blockIdx.x - nsum) * a.fill_rows;
+            const int rows = (int)(a.V - r0 < a.fill_rows ? a.V - r0 : a.fill_rows);
+            if (threadIdx.x < (unsigned)a.fill_rows * 8) {  // (whole waves: 8 rows each)
+                // the first sorted token >= row, 8 probes a step
+                const int j = threadIdx.x & 7, group = threadIdx.x & 56;
+                const uint32_t row = (uint32_t)(r0 + (threadIdx.x >> 3));
+                int lo = 0, hi = (int)a.T;
+                while (__any(lo < hi)) {
+                    const int len = hi - lo, p = lo + (int)((int64_t)len * (j + 1) / 9);
+                    const bool less = len > 0 && a.keys[p] < row;
+                    const int n = __popcll((__ballot(less) >> group) & 255);  // the probes below the row: the first n
+                    const int below = lo + (int)((int64_t)len * n / 9), above = lo + (int)((int64_t)len * (n + 1) / 9);
+                    if (len > 0) {
+                        if (n < 8) hi = above;
+                        if (n > 0) lo = below + 1;
+                    }
+                }
+                if (j == 0) named[threadIdx.x >> 3] = lo < a.T && a.keys[lo] == row;
+            }
+            __syncthreads();
+            if (a.K % VEC == 0 && a.K >= 256 * VEC) {
+                for (int r = 0; r < rows; ++r)
+                    if (!named[r])
+                        for (int64_t k = threadIdx.x * VEC; k < a.K; k += 256 * VEC)
+                            store_zeros<kOutBf16, VEC, kStream>(a.de, (r0 + r) * a.K + k);
+            } else {
+                // the group's rows as one run of vectors, which rows need not start with: rows of odd width still take
+                // whole aligned lines, and narrow rows all the threads
+                const uint32_t K = (uint32_t)a.K, n = (uint32_t)rows * K;
+                const float per = 1.0f / (float)K;
+#pragma unroll 4
+                for (uint32_t i = threadIdx.x * VEC; i < n; i += 256 * VEC) {
+                    uint32_t r = (uint32_t)((float)i * per);  // (i < 2^22: off by one at the most)
+                    r = r * K > i ? r - 1 : (r + 1) * K <= i ? r + 1 : r;
+                    const uint32_t next = (r + 1) * K;        // K >= VEC: the vector reaches at most one row more
+                    if (i + VEC <= n && !named[r] && (i + VEC <= next || !named[r + 1])) {
+                        store_zeros<kOutBf16, VEC, kStream>(a.de, r0 * a.K + i);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < VEC; ++j)
+                            if (i + j < n && !named[i + j < next ? r : r + 1])
+                                store_zeros<kOutBf16, 1, false>(a.de, r0 * a.K + i + j);
+                    }
                 }
             }
-            if (j == 0) named[threadIdx.x >> 3] = lo < a.T && a.keys[lo] == row;
-            __syncthreads();
-            for (int r = 0; r < kFillRows && r0 + r < a.V; ++r)
-                if (!named[r])
-                    for (int64_t k = threadIdx.x * VEC; k < a.K; k += 256 * VEC)
-                        store_zeros<kOutBf16, VEC, kStream>(a.de, (r0 + r) * a.K + k);
         }
         return;
     }
     const int piece = (int)blockIdx.x / a.col_blocks, cb = (int)blockIdx.x - piece * a.col_blocks;
-    const int64_t k = ((int64_t)cb * 256 + threadIdx.x) * VEC;
+    int64_t k = ((int64_t)cb * 256 + threadIdx.x) * VEC;
     const int64_t p0 = piece * a.piece, p1 = p0 + a.piece < a.T ? p0 + a.piece : a.T;
     if (k >= a.K) return;
+    const int skip = row_vector<VEC>(k, a.K);
     const bool from_before = p0 > 0 && a.keys[p0 - 1] == a.keys[p0];
     const bool goes_on = p1 < a.T && a.keys[p1] == a.keys[p1 - 1];
     float sum[VEC] = {};
@@ -393,7 +440,7 @@ __global__ __launch_bounds__(256) void piece_sum_kernel(SumArgs a) {
                 if (key[j] < a.V) {
                     if (first && from_before) store_vec<false, VEC>(a.head, piece * a.K + k, sum);
                     else if (last && goes_on) store_vec<false, VEC>(a.tail, piece * a.K + k, sum);
-                    else write_row<kOutBf16, kAdd, VEC>(a, key[j], k, sum);
+                    else write_row<kOutBf16, kAdd, VEC>(a, key[j], k, skip, sum);
                 }
                 first = false;
 #pragma unroll
@@ -407,9 +454,10 @@ __global__ __launch_bounds__(256) void piece_sum_kernel(SumArgs a) {
 template <bool kOutBf16, bool kAdd, int VEC>
 __global__ __launch_bounds__(256) void piece_join_kernel(SumArgs a) {
     const int piece = (int)blockIdx.x / a.col_blocks, cb = (int)blockIdx.x - piece * a.col_blocks;
-    const int64_t k = ((int64_t)cb * 256 + threadIdx.x) * VEC;
+    int64_t k = ((int64_t)cb * 256 + threadIdx.x) * VEC;
     const int64_t p0 = piece * a.piece, p1 = p0 + a.piece;
     if (k >= a.K || p1 >= a.T) return;
+    const int skip = row_vector<VEC>(k, a.K);
     const uint32_t row = a.keys[p1 - 1];
     if (row >= a.V || a.keys[p1] != row) return;                    // nothing goes on
     if (p0 > 0 && a.keys[p0] == row && a.keys[p0 - 1] == row) return;  // it began before this piece
@@ -435,7 +483,7 @@ __global__ __launch_bounds__(256) void piece_join_kernel(SumArgs a) {
                 for (int i = 0; i < VEC; ++i) sum[i] += v[j][i];
         if (n < U) break;
     }
-    write_row<kOutBf16, kAdd, VEC>(a, row, k, sum);
+    write_row<kOutBf16, kAdd, VEC>(a, row, k, skip, sum);
 }
 
 // How a backward call's workspace lies.
@@ -478,10 +526,12 @@ Plan make_plan(int64_t T, int64_t V, int64_t K) {
 template <bool kInBf16, bool kOutBf16, bool kAdd, int VEC>
 hipError_t launch_sums(SumArgs a, hipStream_t stream) {
     a.col_blocks = (int)((a.K + 256 * VEC - 1) / (256 * VEC));
-    const int64_t fills = kAdd ? 0 : ((int64_t)a.V + kFillRows - 1) / kFillRows;
+    // (8 where 32 would leave the GPU unfilled: 200 tokens x 1500 rows of width 3000 13 us against 19)
+    a.fill_rows = a.V >= 32768 ? kFillRows : 8;
+    const int64_t fills = kAdd ? 0 : ((int64_t)a.V + a.fill_rows - 1) / a.fill_rows;
     const dim3 grid((unsigned)((int64_t)a.pieces * a.col_blocks + fills));
     constexpr bool kMayStream = !kAdd && VEC == 4;
-    if (kMayStream && (int64_t)a.V * a.K * (kOutBf16 ? 2 : 4) > (int64_t)160 << 20)
+    if (kMayStream && ((uintptr_t)a.de & 15u) == 0 && (int64_t)a.V * a.K * (kOutBf16 ? 2 : 4) > (int64_t)160 << 20)
         piece_sum_kernel<kInBf16, kOutBf16, kAdd, VEC, kMayStream><<<grid, 256, 0, stream>>>(a);
     else
         piece_sum_kernel<kInBf16, kOutBf16, kAdd, VEC, false><<<grid, 256, 0, stream>>>(a);
@@ -497,13 +547,11 @@ hipError_t launch_sums_t(const SumArgs& a, bool add, bool vec, hipStream_t strea
     return vec ? launch_sums<kInBf16, kOutBf16, false, 4>(a, stream) : launch_sums<kInBf16, kOutBf16, false, 1>(a, stream);
 }
 
-bool aligned(const void* p, uintptr_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
-
 template <bool kBf16>
 hipError_t launch_lookup_t(const int32_t* tokens, int64_t T, const int8_t* e, const float* s_e, int64_t V, int64_t K,
                            float scale, void* out, int64_t ldo, hipStream_t stream) {
     constexpr int VEC = kBf16 ? 8 : 4;  // 16 bytes of output a thread
-    const bool vec = K % VEC == 0 && ldo % VEC == 0 && aligned(e, VEC) && aligned(out, 16);
+    const bool vec = K >= VEC;
     const int64_t per = 256 * (vec ? VEC : 1);
     constexpr int64_t kSlice = (int64_t)1 << 24;  // tokens per launch: its threads stay below 2^32
     for (int64_t t0 = 0; t0 < T; t0 += kSlice) {
@@ -556,8 +604,8 @@ hipError_t launch_embedding_backward(const int32_t* tokens, int64_t T, const voi
     }
     if (hipError_t err = hipGetLastError()) return err;
     const SumArgs a{keys[at], order[at], T, dout, ldd, (uint32_t)V, K, scale, de,
-                    reinterpret_cast<float*>(ws + p.head), reinterpret_cast<float*>(ws + p.tail), p.piece, p.pieces, 0};
-    const bool vec = K % 4 == 0 && ldd % 4 == 0 && aligned(dout, dout_bf16 ? 8 : 16) && aligned(de, de_bf16 ? 8 : 16);
+                    reinterpret_cast<float*>(ws + p.head), reinterpret_cast<float*>(ws + p.tail), p.piece, p.pieces, 0, 0};
+    const bool vec = K >= 4;
     if (dout_bf16) return de_bf16 ? launch_sums_t<true, true>(a, accumulate, vec, stream) : launch_sums_t<true, false>(a, accumulate, vec, stream);
     return de_bf16 ? launch_sums_t<false, true>(a, accumulate, vec, stream) : launch_sums_t<false, false>(a, accumulate, vec, stream);
 }

@@ -542,8 +542,8 @@ dfssm_status dfssm_embedding_lookup_scaled(const int32_t* tokens, int64_t T, con
  * to what de holds, and rows that no token names are left untouched.  So the tied matrix's gradient is
  * dfssm_cross_entropy_backward into de, then this call with accumulate 1.
  *   tokens int32 [T]; ids outside [0, V) take no part
- *   dout dout_type [T][K], row t at element t*ldd;  de de_type [V][K] (16 bytes' alignment and K % 4 ==
- *   0 are fastest)
+ *   dout dout_type [T][K], row t at element t*ldd;  de de_type [V][K] (rows of a multiple of 16
+ *   bytes, aligned to them, are fastest)
  *   workspace  at least dfssm_embedding_backward_workspace_bytes(T, V, K) bytes, 16-byte aligned,
  *              under dfssm_cross_entropy's rules
  * The tokens are sorted; a row's sum runs over its tokens in order, in fp32: equal inputs give

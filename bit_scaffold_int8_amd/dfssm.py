@@ -406,7 +406,7 @@ def _run_on(name, tensors, stream, *args) -> None:
         stream = torch._C._cuda_getCurrentRawStream(dev)
     elif not isinstance(stream, int):
         stream = stream.cuda_stream
-    if dev == torch.cuda.current_device():
+    if dev == torch._C._cuda_getDevice():
         _call(name, *args, stream)
         return
     with torch.cuda.device(dev):

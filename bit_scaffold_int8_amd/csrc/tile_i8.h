@@ -278,8 +278,8 @@ __device__ __forceinline__ bool tile_i8(const int8_t* __restrict__ w, int64_t ld
 
 // ---- which tile a shape takes (host)
 
-enum TileKind { kTile256, kTile256x192, kTile128, kTile128x64, kTile128x32, kTile64x64, kTile64x32, kTile32x32, kTileKinds };
-constexpr int kTileKindsNoSplit = kTile128x64 + 1;  // the first ones: 64 tokens or more, K not split
+enum TileKind { kTile256, kTile256x192, kTile128, kTile128x64, kTile64x64, kTile128x32, kTile64x32, kTile32x32, kTileKinds };
+constexpr int kTileKinds64 = kTile64x64 + 1;  // the first ones: 64 tokens or more
 
 struct TileShape {
     int rows, tokens;
@@ -289,14 +289,13 @@ struct TileShape {
 // Measured on 512 to 50280 rows x 1 to 2048 tokens, K 512 to 8192, large ones in long runs under the power limit.
 // Large tiles reread least and win when they fill the GPU (50280 rows x 1500 tokens, K 2048, in this order:
 // 183, 199, 207, 235 us; x 300 tokens, of which the second wastes least: 59, 53, 60, 62); small ones win when they do
-// not (2048 rows x 1 token, K 4096: 39 us for the first, then 17, 12, 11, 9.5, 7.2, 6.1 from the third on), or when
+// not (2048 rows x 1 token, K 4096: 39 us for the first, then 17, 12, 9.5, 11, 7.2, 6.1 from the third on), or when
 // the large ones' last round would be nearly empty (8512 rows x 300 tokens: 26, 22, 13, 13 us).
 inline const TileShape& tile_shape(int kind) {
     static const TileShape t[kTileKinds] = {
         {256, 256, 7.0f, 24.0f, 34.0f}, {256, 192, 6.5f, 21.0f, 30.0f}, {128, 128, 4.1f, 10.7f, 11.5f},
-        {128, 64, 3.3f, 7.9f, 7.8f},
-        {128, 32, 2.9f, 6.8f, 4.0f},    {64, 64, 3.4f, 6.3f, 3.4f},    {64, 32, 3.6f, 5.4f, 2.35f},
-        {32, 32, 3.95f, 5.0f, 4.0f}};
+        {128, 64, 3.3f, 7.9f, 7.8f},    {64, 64, 3.4f, 6.3f, 3.4f},     {128, 32, 2.9f, 6.8f, 4.0f},
+        {64, 32, 3.6f, 5.4f, 2.35f},    {32, 32, 3.95f, 5.0f, 4.0f}};
     return t[kind];
 }
 

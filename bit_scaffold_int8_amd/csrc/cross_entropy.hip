@@ -356,9 +356,13 @@ __global__ __launch_bounds__(256) void slab_sum_kernel(const float* __restrict__
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // The tiles of the gradient kernel for a piece's rows: of those with 64 tokens or more, so that the padded
-// tokens of d s_x fill whole chunks of the product (64 tokens) and are all written.  (The smallest splits K: 25 tokens x
-// 11898 rows x 2480 9.8 us, 13.4 by the next one.)
-TileSplit grad_tiles(int64_t M, int64_t rows, int64_t K) { return split_rows(rows, M, K, kTile256, kTileKinds64); }
+// tokens of d s_x fill whole chunks of the product (64 tokens) and are all written.  The smallest splits K
+// and only serves a round of the 256 CUs (25 tokens x 11898 rows x 2480 9.8 us, 13.4 by the next one; 4096 x 1128 x 2048,
+// in 4 1/2 rounds 41 us, 35 by 256 x 192).
+TileSplit grad_tiles(int64_t M, int64_t rows, int64_t K) {
+    const int64_t smallest = ((M + 63) / 64) * ((rows + 63) / 64);
+    return split_rows(rows, M, K, kTile256, smallest <= 256 ? kTileKinds64 : kTile64x64);
+}
 
 // How a backward call is cut and where its workspace lies; the size query and the call agree on it.
 struct Plan {

@@ -243,8 +243,8 @@ __device__ __forceinline__ void store_block(const uint8_t* blk, int ld_blk, uint
     }
 }
 
-// What lies past the vocabulary or the tokens inside the padded buffers is finite and meets zero codes
-// (or is not read) in the products.  Both forms of d go through LDS, so that memory is written in whole
+// What lies past the vocabulary or the tokens inside the padded buffers is zero: the products read it against zero
+// codes, and an infinite one would make them NaN.  Both forms of d go through LDS, so that memory is written in whole
 // rows of a block (64 P bytes): written from the registers, d s_x would go out in 2-byte stores.
 template <class C, int P>
 __global__ __launch_bounds__(C::NT, C::kMinWaves) void grad_tile_kernel(GradArgs a) {
@@ -296,6 +296,11 @@ __global__ __launch_bounds__(C::NT, C::kMinWaves) void grad_tile_kernel(GradArgs
 #pragma unroll
             for (int v = 0; v < 16; ++v)
                 p[v] = __builtin_amdgcn_exp2f(__builtin_fmaf(se[b][v] * (float)acc[b][tb][v], sx, -lse) * kLog2e);
+            if (wrows < C::BW) {  // rows that do not exist: their exp(0 - lse) has no bound
+#pragma unroll
+                for (int v = 0; v < 16; ++v)
+                    if (wn + b * 32 + 8 * (v >> 2) + 4 * g + (v & 3) >= wrows) p[v] = 0.0f;
+            }
             if (__ballot(tl >= b * 32 && tl < b * 32 + 32)) {
 #pragma unroll
                 for (int v = 0; v < 16; ++v)

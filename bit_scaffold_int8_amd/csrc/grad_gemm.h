@@ -43,7 +43,7 @@ __device__ __forceinline__ GradScale grad_scale(float a, float b, bool with_b) {
 }
 
 // One row of A holds, for each block of 32 r, the block's 32 first pieces and then (P = 2) its 32
-// second pieces: 64 P bytes.  Row strides are multiples of 128 bytes, R is padded with finite values to them.
+// second pieces: 64 P bytes.  Row strides are multiples of 128 bytes, R is padded with zeros to them.
 struct GradGemmArgs {
     const uint8_t* a;      // [>= I rows][lda bytes]
     int64_t lda;           // bytes; 256 rows stay below 2^30

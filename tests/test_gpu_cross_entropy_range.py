@@ -1,0 +1,53 @@
+"""The cross entropy's gradients where the logits' range is unusual, against the fp64 formula with the bounds of
+vocabulary_reference.py."""
+import pytest
+
+from test_gpu_cross_entropy import _backward, _check_backward, _check_forward, _forward
+from test_gpu_parity import torch_cuda  # noqa: F401  (fixture)
+
+pytestmark = pytest.mark.gpu
+
+LEVELS = (-1.0, -2.0, -3.0, -5.0, -10.0, -30.0, -100.0)
+
+
+def _negative(M, V, K, seed, ignored=0.1):
+    """Operands whose logits are all negative (positive x_q, negative e); each token's scale puts its lse on one of
+    LEVELS."""
+    import torch
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(seed)
+    x_q = torch.randint(1, 128, (M, K), generator=gen, device="cuda").to(torch.int8)
+    e = -torch.randint(1, 128, (V, K), generator=gen, device="cuda").to(torch.int8)
+    s_e = 0.01 * (0.5 + torch.rand(V, generator=gen, device="cuda"))
+    targets = torch.randint(0, V, (M,), generator=gen, device="cuda", dtype=torch.int32)
+    z = (x_q.double() @ e.double().t().contiguous()) * s_e.double()
+    level = torch.tensor(LEVELS, device="cuda", dtype=torch.float64)[torch.arange(M, device="cuda") % len(LEVELS)]
+    # lse falls from log V to below every level as the scale grows
+    lo, hi = torch.zeros(M, device="cuda", dtype=torch.float64), 150.0 / z.abs().amin(1)
+    for _ in range(40):
+        mid = (lo + hi) / 2
+        above = torch.logsumexp(z * mid[:, None], 1) > level
+        lo, hi = torch.where(above, mid, lo), torch.where(above, hi, mid)
+    targets[torch.rand(M, generator=gen, device="cuda") < ignored] = -100
+    return x_q, hi.float(), e, s_e, targets
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("M,V,K", [(1, 1, 16), (7, 1, 64), (7, 31, 64), (7, 32, 64), (14, 33, 48), (7, 63, 64), (21, 96, 32),
+                                   (5, 1000, 64), (70, 1001, 64), (300, 1000, 128), (40, 1024, 64), (35, 1056, 64),
+                                   (300, 1056, 48), (7, 50280, 64), (300, 50280, 128), (1100, 6001, 64),
+                                   (8200, 20001, 64)])
+def test_logits_negative_throughout(torch_cuda, M, V, K, bf16):
+    """A vocabulary's last tile has rows that do not exist; with lse below zero exp(0 - lse) is above 1 for them, and
+    must not reach dx (the last shape: several pieces of the vocabulary, a ragged one last)."""
+    import torch
+    print("negative logits", M, V, K, bf16, flush=True)
+    ops = _negative(M, V, K, seed=M + V)
+    loss, lse = _forward(ops)
+    _check_forward(ops, loss, lse)
+    assert bool((lse < -0.9).all())
+    dloss = (torch.rand(M, device="cuda") + 0.5) / M
+    dx, de = _backward(ops, lse, dloss, bf16)
+    _check_backward(ops, dloss, dx, de, bf16)
+    alone, _ = _backward(ops, lse, dloss, bf16, want=(True, False))
+    _check_backward(ops, dloss, alone, None, bf16)

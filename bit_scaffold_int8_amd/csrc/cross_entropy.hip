@@ -168,41 +168,39 @@ struct GradArgs {
     const int32_t* targets;
     const float* lse;
     const float* dloss;
-    const float* maxima; // [3][kMaximaBlocks]: of |s_e|, |dloss|, |dloss s_x| (tokens that count)
+    const float* maxima; // [2][kMaximaBlocks]: of |s_e|, |dloss s_x| (tokens that count)
     uint16_t* gx;        // [tokens][Vp P]: d s_e, or NULL
     uint16_t* gw;        // [Vp][Mp P]: d s_x, or NULL
     int64_t ldgx, ldgw;  // elements
 };
 
-// Partial maxima of what bounds d s_e and d s_x (|p - [v = target]| <= 1): they scale d into fp16's range.  An infinite
-// factor takes no part: its own gradients are infinite or NaN at any scale, and the others keep theirs.
+// Partial maxima of what bounds d s_e (with the token's dloss) and d s_x (|p - [v = target]| <= 1): they scale d into
+// fp16's range.  An infinite dloss s_x takes no part: its own gradients are infinite or NaN at any scale, and the others
+// keep theirs.
 __global__ __launch_bounds__(256) void grad_maxima_kernel(const float* __restrict__ s_e, int64_t V,
                                                           const float* __restrict__ s_x,
                                                           const float* __restrict__ dloss,
                                                           const int32_t* __restrict__ targets, int64_t M,
                                                           float* __restrict__ maxima) {
-    __shared__ float part[3][4];
+    __shared__ float part[2][4];
     const int64_t first = (int64_t)blockIdx.x * 256 + threadIdx.x, step = (int64_t)kMaximaBlocks * 256;
-    float e = 0.0f, d = 0.0f, dx = 0.0f;
+    float e = 0.0f, dx = 0.0f;
     for (int64_t i = first; i < V; i += step) e = fmaxf(e, fabsf(s_e[i]));
     for (int64_t i = first; i < M; i += step) {
         const int64_t target = targets[i];
         if (target >= 0 && target < V) {
-            const float l = fabsf(dloss[i]), lx = fabsf(dloss[i] * s_x[i]);
-            if (l < __builtin_inff()) d = fmaxf(d, l);
+            const float lx = fabsf(dloss[i] * s_x[i]);
             if (lx < __builtin_inff()) dx = fmaxf(dx, lx);
         }
     }
     e = wave_max(e);
-    d = wave_max(d);
     dx = wave_max(dx);
     if ((threadIdx.x & 63) == 0) {
         part[0][threadIdx.x >> 6] = e;
-        part[1][threadIdx.x >> 6] = d;
-        part[2][threadIdx.x >> 6] = dx;
+        part[1][threadIdx.x >> 6] = dx;
     }
     __syncthreads();
-    if (threadIdx.x < 3) {
+    if (threadIdx.x < 2) {
         const float* p = part[threadIdx.x];
         maxima[threadIdx.x * kMaximaBlocks + blockIdx.x] = fmaxf(fmaxf(p[0], p[1]), fmaxf(p[2], p[3]));
     }
@@ -257,11 +255,11 @@ __global__ __launch_bounds__(C::NT, C::kMinWaves) void grad_tile_kernel(GradArgs
     const int wrows = (int)(a.V - n0 < C::BW ? a.V - n0 : C::BW);
     const int trows = (int)(a.M - m0 < C::BT ? a.M - m0 : C::BT);
     const int lane = threadIdx.x & (kWave - 1);
-    const float max_e = a.maxima[lane], max_d = a.maxima[kMaximaBlocks + lane], max_dx = a.maxima[2 * kMaximaBlocks + lane];
+    const float max_e = a.maxima[lane], max_dx = a.maxima[kMaximaBlocks + lane];
     v16i acc[C::WB][C::TB];
     const bool holds = tile_i8<C, true>(a.e + n0 * a.K, a.K, wrows, a.x_q + m0 * a.K, a.K, trows, a.K, lds, acc);
 
-    const float up_x = grad_scale<P>(max_d, max_e, true).up, up_w = grad_scale<P>(max_dx, 0.0f, false).up;
+    const int above_e = above_exponent(wave_max(max_e)), up_w = grad_exponent<P>(above_exponent(wave_max(max_dx)), kNoRow);
     const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x / kWave));
     const int ww = wave % C::WW, tw = wave / C::WW;
     const int l32 = lane & 31, g = lane >> 5;
@@ -288,7 +286,8 @@ __global__ __launch_bounds__(C::NT, C::kMinWaves) void grad_tile_kernel(GradArgs
         // 0 where the token does not count, whatever its scale is)
         const float sx = counts ? a.s_x[m] : 0.0f, lse = counts ? a.lse[m] : __builtin_inff();
         const float dloss = counts ? a.dloss[m] : 0.0f;
-        const float dl = dloss * up_x, dlx = dloss * sx * up_w;
+        const float dl = __builtin_amdgcn_ldexpf(dloss, grad_exponent<P>(above_e, dloss));
+        const float dlx = __builtin_amdgcn_ldexpf(dloss * sx, up_w);
         const int tl = counts ? (int)(target - a.v0 - n0 - wn) : -1;     // the target's row in the wave's range
 #pragma unroll
         for (int b = 0; b < C::WB; ++b) {
@@ -420,7 +419,7 @@ Plan make_plan(int64_t M, int64_t V, int64_t K, bool bf16, bool want_dx, bool wa
         at += (b + 255) / 256 * 256;
         return was;
     };
-    p.maxima = take(3 * kMaximaBlocks * sizeof(float));
+    p.maxima = take(2 * kMaximaBlocks * sizeof(float));
     if (want_dx) {
         // Each piece has slabs of its own, summed at the end: adding to a slab at the end of every piece's
         // product costs more (all workgroups read and write at once, and nothing else runs).  Not past 512 MB.
@@ -524,7 +523,6 @@ hipError_t launch_cross_entropy_backward(const int8_t* x_q, const float* s_x, in
     const int P = bf16 ? 1 : 2;
     uint8_t* const ws = static_cast<uint8_t*>(workspace);
     float* const maxima = reinterpret_cast<float*>(ws + p.maxima);
-    const float *max_e = maxima, *max_d = maxima + kMaximaBlocks, *max_dx = maxima + 2 * kMaximaBlocks;
     grad_maxima_kernel<<<kMaximaBlocks, 256, 0, stream>>>(s_e, V, s_x, dloss, targets, M, maxima);
     if (hipError_t err = hipGetLastError()) return err;
     for (int64_t v0 = 0; v0 < V; v0 += p.piece) {
@@ -535,12 +533,12 @@ hipError_t launch_cross_entropy_backward(const int8_t* x_q, const float* s_x, in
         if (hipError_t err = P == 1 ? launch_grad_tiles<1>(g, stream) : launch_grad_tiles<2>(g, stream)) return err;
         if (dx) {
             float* const slab = reinterpret_cast<float*>(ws + p.dx) + (p.add ? 0 : v0 / p.piece * p.splits * M * K);
-            const GradGemmArgs a{ws + p.gx, p.piece * P * 2, g.e, K, M, K, rows, {max_d, max_e}, p.slabs ? slab : dx, K, M * K,
+            const GradGemmArgs a{ws + p.gx, p.piece * P * 2, g.e, K, M, K, rows, {maxima, dloss}, p.slabs ? slab : dx, K, M * K,
                                  grad_shape(M, K, rows, P, p.splits, p.splits).wide_rows, p.splits, p.add && v0 > 0, false};
             if (hipError_t err = launch_grad_gemm(a, P, stream)) return err;
         }
         if (de) {
-            const GradGemmArgs a{ws + p.gw, p.Mp * P * 2, x_q, K, rows, K, M, {max_dx, nullptr},
+            const GradGemmArgs a{ws + p.gw, p.Mp * P * 2, x_q, K, rows, K, M, {maxima + kMaximaBlocks, nullptr},
                                  static_cast<uint8_t*>(de) + v0 * K * (bf16 ? 2 : 4), K, 0,
                                  grad_shape(rows, K, M, P, 1, 1).wide_rows, 1, accumulate, bf16};
             if (hipError_t err = launch_grad_gemm(a, P, stream)) return err;

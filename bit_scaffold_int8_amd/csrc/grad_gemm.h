@@ -7,8 +7,9 @@
 //   two pieces (P = 2): the value rounded to bf16 and the remainder rounded to fp16.  The remainder is at most 2^-8 of
 //     the value and keeps 11 bits: relative error 2^-19.  (Two bf16 pieces reach 2^-17.)
 //   one piece (P = 1): the value rounded to fp16, 2^-11.  (bf16: 2^-8.)
-// fp16 ends at 2^-24, so k puts the largest possible value just inside its range (GradScale): what is smaller
-// than 2^-29 of that loses bits, at 2^-40 all of fp16's; the bf16 piece keeps its 8 at any size.
+// fp16 ends at 2^-24, so k puts the largest possible value just inside its range (grad_exponent): what is smaller
+// than 2^-29 of that loses bits, at 2^-40 all of fp16's; the bf16 piece keeps its 8 at any size.  Where a row of A has
+// a factor of its own, k is the row's: rows of any size keep their bits.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -18,29 +19,24 @@
 
 namespace dfssm {
 
-// The largest sizes of the values' factors, as kMaximaBlocks partial maxima each: what scales A.
+// What bounds A's values and so scales them: a common factor's partial maxima, and a factor for each row.
 constexpr int kMaximaBlocks = 64;  // one a lane
-struct GradMaxima {
-    const float* a;
-    const float* b;  // or NULL: the factor 1
+struct GradFactors {
+    const float* maxima;  // [kMaximaBlocks]
+    const float* rows;    // [I] (then C is fp32), or NULL: the factor 1
 };
 
-// v < 2^exponent for any finite v >= 0.
+// v < 2^exponent for any finite v.
 __device__ __forceinline__ int above_exponent(float v) { return (int)(__float_as_uint(v) >> 23 & 255u) - 126; }
 
-// 2^k for values below the product of the maxima: at most 2^23 with two pieces (the remainder then stays below 2^15)
-// and 2^15 with one.  k is kept where both 2^k and a factor times 2^k are fp32 numbers.
-struct GradScale {
-    float up, down;  // 2^k, 2^-k
-};
+// k for values below the product of a common factor < 2^common and a row's factor: 2^k times them is at most 2^23 with two
+// pieces (the remainder then stays below 2^15) and 2^15 with one.  The row's factor times 2^k is an fp32 number.
 template <int P>
-__device__ __forceinline__ GradScale grad_scale(float a, float b, bool with_b) {
-    const int ea = above_exponent(wave_max(a)), eb = with_b ? above_exponent(wave_max(b)) : 0;
-    int k = (P == 2 ? 23 : 15) - ea - eb;
-    const int most = 120 - (ea > 0 ? ea : 0);
-    k = k > most ? most : k < -120 ? -120 : k;
-    return GradScale{__uint_as_float((uint32_t)(k + 127) << 23), __uint_as_float((uint32_t)(127 - k) << 23)};
+__device__ __forceinline__ int grad_exponent(int common, float row) {
+    const int k = (P == 2 ? 23 : 15) - common, most = 120;
+    return (k < most ? k : most) - above_exponent(row);
 }
+constexpr float kNoRow = 0.5f;  // a row's factor of 1: below 2^0
 
 // One row of A holds, for each block of 32 r, the block's 32 first pieces and then (P = 2) its 32
 // second pieces: 64 P bytes.  Row strides are multiples of 128 bytes, R is padded with zeros to them.
@@ -50,7 +46,7 @@ struct GradGemmArgs {
     const int8_t* b;       // [R][ldb], 16-byte aligned rows
     int64_t ldb;
     int64_t I, J, R;       // J % 16 == 0
-    GradMaxima maxima;     // A's scale
+    GradFactors factors;   // A's scale
     void* c;               // fp32 or bf16 [I][ldc]
     int64_t ldc;
     int64_t slab;          // elements between the outputs of two splits of R (fp32)

@@ -10,6 +10,8 @@
 // products; the large bf16 product of the library reaches 1.41 on this GPU), at 2.0 GHz and 58 % of the matrix cores' cycles.
 // On the way: 214 us with the loads sunk to a chunk's end and LDS conflicts, 203 with both mended, 197 with the
 // staging spread between the products, 187 with the third LDS buffer.
+#include <type_traits>
+
 #include "device_common.h"
 #include "grad_gemm.h"
 
@@ -51,7 +53,8 @@ __device__ __forceinline__ void codes4_fp16(int w, uint32_t& h0, uint32_t& h1) {
     h1 = __builtin_bit_cast(uint32_t, __builtin_bit_cast(v2h, perm(0x64646464u, u, 0x04030402u)) - off);
 }
 
-template <class C, int P, bool kBf16, bool kAdd>
+// kRows: A's rows have factors of their own.
+template <class C, int P, bool kBf16, bool kAdd, bool kRows>
 __global__ __launch_bounds__(C::NT, C::NT / 256) void grad_gemm_kernel(GradGemmArgs a, int nti, int ntj,
                                                                       int chunks_per_split) {
     constexpr int kR = 64 / P;              // r per chunk: 128 bytes of an A row
@@ -80,7 +83,7 @@ __global__ __launch_bounds__(C::NT, C::NT / 256) void grad_gemm_kernel(GradGemmA
     const int nchunks = (int)((a.R + kR - 1) / kR);
     const int c0 = blockIdx.y * chunks_per_split;
     const int c1 = c0 + chunks_per_split < nchunks ? c0 + chunks_per_split : nchunks;
-    const float max_a = a.maxima.a[lane], max_b = a.maxima.b ? a.maxima.b[lane] : 0.0f;
+    const float maximum = a.factors.maxima[lane];
 
     const __amdgpu_buffer_rsrc_t ar = make_rsrc(a.a + i0 * a.lda, (uint32_t)((rows - 1) * a.lda + (int64_t)nchunks * 128));
     const int arow = tid >> 3, apiece = tid & 7;
@@ -293,7 +296,14 @@ __global__ __launch_bounds__(C::NT, C::NT / 256) void grad_gemm_kernel(GradGemmA
         lds_barrier();
     }
 
-    const float down = grad_scale<P>(max_a, max_b, a.maxima.b != nullptr).down;
+    const int common = above_exponent(wave_max(maximum));
+    const int down = -grad_exponent<P>(common, kNoRow);
+    int* const row_down = reinterpret_cast<int*>(lds);
+    if constexpr (kRows) {  // (the loop's last barrier freed the buffers)
+        for (int r = tid; r < C::BM; r += C::NT)
+            row_down[r] = r < rows ? -grad_exponent<P>(common, a.factors.rows[i0 + r]) : 0;
+        lds_barrier();
+    }
 #pragma unroll
     for (int y = 0; y < C::NB; ++y) {
         const int col = wn * C::NB * 32 + y * 32 + l32;
@@ -305,12 +315,13 @@ __global__ __launch_bounds__(C::NT, C::NT / 256) void grad_gemm_kernel(GradGemmA
                 const int row = wm * C::MB * 32 + x * 32 + 8 * (v >> 2) + 4 * g + (v & 3);
                 if (row >= rows) continue;
                 const int64_t at = blockIdx.y * a.slab + (i0 + row) * a.ldc + j0 + col;
+                const float value = __builtin_amdgcn_ldexpf(acc[x][y][v], kRows ? row_down[row] : down);
                 if constexpr (kBf16) {
                     __bf16* p = static_cast<__bf16*>(a.c) + at;
-                    *p = (__bf16)(kAdd ? (float)*p + down * acc[x][y][v] : down * acc[x][y][v]);
+                    *p = (__bf16)(kAdd ? (float)*p + value : value);
                 } else {
                     float* p = static_cast<float*>(a.c) + at;
-                    *p = kAdd ? *p + down * acc[x][y][v] : down * acc[x][y][v];
+                    *p = kAdd ? *p + value : value;
                 }
             }
     }
@@ -326,12 +337,21 @@ hipError_t launch_c(const GradGemmArgs& a, hipStream_t stream) {
     const int64_t nchunks = (a.R + kR - 1) / kR;
     const int per = (int)((nchunks + a.splits - 1) / a.splits);
     const dim3 grid((unsigned)(nti * ntj), (unsigned)a.splits);
-    if (a.bf16_out) {
-        if (a.accumulate) grad_gemm_kernel<C, P, true, true><<<grid, C::NT, 0, stream>>>(a, nti, ntj, per);
-        else grad_gemm_kernel<C, P, true, false><<<grid, C::NT, 0, stream>>>(a, nti, ntj, per);
+    auto run = [&](auto bf16, auto add, auto has_rows) {
+        grad_gemm_kernel<C, P, bf16.value, add.value, has_rows.value><<<grid, C::NT, 0, stream>>>(a, nti, ntj, per);
+    };
+    constexpr std::true_type yes{};
+    constexpr std::false_type no{};
+    if (a.factors.rows) {  // dx, in fp32 slabs
+        if (a.bf16_out) return hipErrorInvalidValue;
+        if (a.accumulate) run(no, yes, yes);
+        else run(no, no, yes);
+    } else if (a.bf16_out) {
+        if (a.accumulate) run(yes, yes, no);
+        else run(yes, no, no);
     } else {
-        if (a.accumulate) grad_gemm_kernel<C, P, false, true><<<grid, C::NT, 0, stream>>>(a, nti, ntj, per);
-        else grad_gemm_kernel<C, P, false, false><<<grid, C::NT, 0, stream>>>(a, nti, ntj, per);
+        if (a.accumulate) run(no, yes, no);
+        else run(no, no, no);
     }
     return hipGetLastError();
 }
@@ -382,6 +402,7 @@ hipError_t launch_grad_gemm(const GradGemmArgs& a, int pieces, hipStream_t strea
     if (a.wide_rows == a.I) return hipSuccess;
     part.I = a.I - a.wide_rows;
     part.a = a.a + a.wide_rows * a.lda;
+    if (a.factors.rows) part.factors.rows = a.factors.rows + a.wide_rows;
     part.c = static_cast<uint8_t*>(a.c) + a.wide_rows * a.ldc * (a.bf16_out ? 2 : 4);
     return pieces == 1 ? launch_c<Short, 1>(part, stream) : launch_c<Short, 2>(part, stream);
 }

@@ -505,10 +505,11 @@ dfssm_status dfssm_cross_entropy(const int8_t* x_q, const float* s_x, int64_t M,
  *       16-byte aligned, written (every row), overlapping nothing
  *   workspace  at least dfssm_cross_entropy_backward_workspace_bytes(M, V, K, grad_type, dx != NULL,
  *              de != NULL) bytes, 16-byte aligned, under the forward call's rules
- * d s_e and d s_x enter the two products in 16-bit pieces, scaled by a power of two that puts the largest
- * possible one, max |dloss| max |s_e| and max |dloss s_x|, inside fp16's range: for DFSSM_F32 gradients
- * rounded to bf16 and the remainder to fp16 (together within 2^-19 of the value; below 2^-29 of the
- * largest possible one the remainder loses bits, to 2^-8 at 2^-40 and below), for DFSSM_BF16 as fp16
+ * d s_e and d s_x enter the two products in 16-bit pieces, scaled by powers of two that put the largest
+ * possible one inside fp16's range: for dx the token's own |dloss| max |s_e|, so that a token's gradient has the same
+ * relative precision whatever the others' dloss are; for de, whose rows sum over the tokens, max |dloss s_x|.  For
+ * DFSSM_F32 gradients d is rounded to bf16 and the remainder to fp16 (together within 2^-19 of the value; below 2^-29
+ * of the largest possible one the remainder loses bits, to 2^-8 at 2^-40 and below), for DFSSM_BF16 to fp16
  * (2^-11; below 2^-29 of the largest bits are lost, below 2^-40 the value counts as zero).  The codes are exact, and
  * sums run in fp32 in a fixed order.
  * Errors: as the forward call's; DFSSM_ERR_INVALID_ARG also for accumulate_de other than 0 and 1 or a

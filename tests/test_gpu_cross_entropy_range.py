@@ -51,3 +51,28 @@ def test_logits_negative_throughout(torch_cuda, M, V, K, bf16):
     _check_backward(ops, dloss, dx, de, bf16)
     alone, _ = _backward(ops, lse, dloss, bf16, want=(True, False))
     _check_backward(ops, dloss, alone, None, bf16)
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("M,V,K", [(5, 300, 64), (70, 600, 64), (300, 5000, 128), (600, 2100, 528)])
+def test_losses_of_any_spread(torch_cuda, M, V, K, bf16):
+    """A token's dx is as exact as with the same dloss everywhere, whatever the other tokens' dloss are: it is
+    linear in the token's own, so the formula and its bounds for ones are scaled by it."""
+    import torch
+    import vocabulary_reference as ref
+    print("losses of any spread", M, V, K, bf16, flush=True)
+    ops = ref.head(M, V, K, seed=M + K, ignored=0.0)
+    _, lse = _forward(ops)
+    ones = torch.ones(M, device="cuda")
+    want_x, _, d, p, g, l64, z = ref.gradients(*ops, ones)
+    bx, _ = ref.gradient_bounds(*ops[:4], d, p, g, l64, z, bf16)
+    spread = torch.linspace(0, -60, M, device="cuda").exp2() * (1 + torch.rand(M, device="cuda"))
+    for huge in (1.0, 1e30, -1e30):
+        dloss = spread.clone()
+        dloss[M // 2] *= huge
+        dx, _ = _backward(ops, lse, dloss, bf16, want=(True, False))
+        w = want_x * dloss.double()[:, None]
+        ref.within(dx, w, ref.rounded(bx * dloss.double().abs()[:, None], w, bf16), "dx")
+    base = torch.randn(V, K, device="cuda").to(torch.bfloat16 if bf16 else torch.float32)
+    dx, de = _backward(ops, lse, spread, bf16, base=base)
+    _check_backward(ops, spread, dx, de, bf16, base=base)

@@ -83,7 +83,7 @@ __global__ __launch_bounds__(C::NT, C::kMinWaves) void loss_tile_kernel(LossArgs
                 if (wrows < C::BW && wn + b * 32 + 8 * (v >> 2) + 4 * g + (v & 3) >= wrows) z[b][v] = neg;
                 top = fmaxf(top, z[b][v]);
             }
-        const float base = top == neg ? 0.0f : top;  // (no row of the wave's range exists)
+        const float base = top == neg ? 0.0f : top;  // (no row of the wave's range exists, or all are -infinity)
         float sum = 0.0f;
 #pragma unroll
         for (int b = 0; b < C::WB; ++b)
@@ -100,9 +100,10 @@ __global__ __launch_bounds__(C::NT, C::kMinWaves) void loss_tile_kernel(LossArgs
         float top = neg;
 #pragma unroll
         for (int w = 0; w < C::WW; ++w) top = fmaxf(top, red[w * C::BT + t].x);
+        const float base = top == neg ? 0.0f : top;  // (every logit of the tile may be -infinity)
         float sum = 0.0f;
 #pragma unroll
-        for (int w = 0; w < C::WW; ++w) sum += red[w * C::BT + t].y * __builtin_amdgcn_exp2f(red[w * C::BT + t].x - top);
+        for (int w = 0; w < C::WW; ++w) sum += red[w * C::BT + t].y * __builtin_amdgcn_exp2f(red[w * C::BT + t].x - base);
         a.part[(int64_t)pos.w * a.M + m0 + t] = make_float2(top, sum);
     }
 }
@@ -120,8 +121,8 @@ __global__ __launch_bounds__(1024) void loss_join_kernel(LossArgs a, const int32
     if (m0 + (lane & 15) < a.M)
         for (int w = wave * 4 + (lane >> 4); w < a.ntw; w += 64) {
             const float2 p = a.part[(int64_t)w * a.M + m0 + (lane & 15)];
-            const float t = fmaxf(top, p.x);
-            sum = sum * __builtin_amdgcn_exp2f(top - t) + p.y * __builtin_amdgcn_exp2f(p.x - t);
+            const float t = fmaxf(top, p.x), base = t == neg ? 0.0f : t;
+            sum = sum * __builtin_amdgcn_exp2f(top - base) + p.y * __builtin_amdgcn_exp2f(p.x - base);
             top = t;
         }
     pairs[wave][lane] = make_float2(top, sum);
@@ -283,8 +284,9 @@ __global__ __launch_bounds__(C::NT, C::kMinWaves) void grad_tile_kernel(GradArgs
         const int64_t target = a.targets[m];
         const bool counts = t < trows && target >= 0 && target < a.vocab;
         // (p is formed from z - lse: in base 2 the roundings of lse log2 e and s_x log2 e would be p's largest errors;
-        // 0 where the token does not count, whatever its scale is)
-        const float sx = counts ? a.s_x[m] : 0.0f, lse = counts ? a.lse[m] : __builtin_inff();
+        // 0 where the token does not count, whatever its scale and its logits are: the mask takes out a NaN, too)
+        const float sx = counts ? a.s_x[m] : 0.0f, lse = counts ? a.lse[m] : 0.0f;
+        const uint32_t keep = counts ? 0xFFFFFFFFu : 0u;
         const float dloss = counts ? a.dloss[m] : 0.0f;
         const float dl = __builtin_amdgcn_ldexpf(dloss, grad_exponent<P>(above_e, dloss));
         const float dlx = __builtin_amdgcn_ldexpf(dloss * sx, up_w);
@@ -294,7 +296,8 @@ __global__ __launch_bounds__(C::NT, C::kMinWaves) void grad_tile_kernel(GradArgs
             float p[16];
 #pragma unroll
             for (int v = 0; v < 16; ++v)
-                p[v] = __builtin_amdgcn_exp2f(__builtin_fmaf(se[b][v] * (float)acc[b][tb][v], sx, -lse) * kLog2e);
+                p[v] = __uint_as_float(keep & __float_as_uint(__builtin_amdgcn_exp2f(
+                    __builtin_fmaf(se[b][v] * (float)acc[b][tb][v], sx, -lse) * kLog2e)));
             if (wrows < C::BW) {  // rows that do not exist: their exp(0 - lse) has no bound
 #pragma unroll
                 for (int v = 0; v < 16; ++v)

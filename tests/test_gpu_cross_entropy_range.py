@@ -76,3 +76,37 @@ def test_losses_of_any_spread(torch_cuda, M, V, K, bf16):
     base = torch.randn(V, K, device="cuda").to(torch.bfloat16 if bf16 else torch.float32)
     dx, de = _backward(ops, lse, spread, bf16, base=base)
     _check_backward(ops, spread, dx, de, bf16, base=base)
+
+
+@pytest.mark.parametrize("M,V,K", [(3, 700, 32), (40, 1000, 64), (300, 1500, 64), (600, 50280, 64)])
+def test_rows_whose_logits_are_minus_infinity(torch_cuda, M, V, K):
+    """Finite scales whose product is not: rows that such logits take out (whole tiles of them, first and last) leave
+    the others' lse, loss and de as they are without them; their own de is zero."""
+    import torch
+    import vocabulary_reference as ref
+    print("minus infinity", M, V, K, flush=True)
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(M)
+    x_q, s_x, e, s_e, targets = ref.head(M, V, K, seed=M)
+    x_q = torch.where(x_q == 0, torch.ones_like(x_q), x_q.abs())
+    out = torch.zeros(V, dtype=torch.bool, device="cuda")
+    out[:512] = True
+    out[V - 100:V - 40] = True
+    e[out], s_e[out] = -100, 3.0e38
+    s_x = s_x.clamp_min(1e-3)
+    keep = (~out).nonzero()[:, 0]
+    targets = torch.where(targets >= 0, keep[torch.randint(0, len(keep), (M,), generator=gen, device="cuda")].to(torch.int32), targets)
+    ops = (x_q, s_x, e, s_e, targets)
+    new = torch.full((V,), -100, dtype=torch.int32, device="cuda")
+    new[keep] = torch.arange(len(keep), dtype=torch.int32, device="cuda")
+    part = (x_q, s_x, e[keep].contiguous(), s_e[keep].contiguous(),
+            torch.where(targets >= 0, new[targets.clamp_min(0).long()], targets))
+    loss, lse = _forward(ops)
+    _check_forward(part, loss, lse)
+    dloss = torch.rand(M, generator=gen, device="cuda")
+    _, de = _backward(ops, lse, dloss, False, want=(False, True))
+    assert bool((de[out] == 0).all())
+    _check_backward(part, dloss, None, de[keep], False)
+    e[:], s_e[:] = -100, 3.0e38  # nothing is left
+    loss, lse = _forward((x_q, s_x, e, s_e, targets))
+    assert bool((lse == -float("inf")).all())

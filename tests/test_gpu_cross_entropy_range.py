@@ -110,3 +110,24 @@ def test_rows_whose_logits_are_minus_infinity(torch_cuda, M, V, K):
     e[:], s_e[:] = -100, 3.0e38  # nothing is left
     loss, lse = _forward((x_q, s_x, e, s_e, targets))
     assert bool((lse == -float("inf")).all())
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("M,V,K", [(5, 1000, 256), (70, 600, 272), (300, 5000, 256), (2100, 60001, 512), (8200, 20000, 512),
+                                   (4100, 33000, 512), (8192, 20001, 8192)])
+def test_pieces_hold_their_bits(torch_cuda, M, V, K, bf16):
+    """Both pieces of d reach both gradients, over many rows, tokens, pieces of the vocabulary and slabs."""
+    import torch
+    import gradient_pieces as gp
+    import vocabulary_reference as ref
+    print("pieces' bits", M, V, K, bf16, flush=True)
+    ops, lse, dloss, row = gp.operands(M, V, K, M + V, "cuda")
+    base = torch.randn(V, K, device="cuda").to(torch.bfloat16 if bf16 else torch.float32)
+    want_x, want_e, size_x, size_e, n = gp.gradients(ops, dloss, row)
+    bx, be = gp.bounds(size_x, size_e, n, bf16)
+    dx, de = _backward(ops, lse, dloss, bf16)
+    ref.within(dx, want_x, ref.rounded(bx, want_x, bf16), "dx")
+    ref.within(de, want_e, ref.rounded(be, want_e, bf16), "de")
+    _, de = _backward(ops, lse, dloss, bf16, want=(False, True), base=base)
+    want_e = want_e + base.double()
+    ref.within(de, want_e, ref.rounded(be, want_e, bf16), "de added")

@@ -382,6 +382,7 @@ struct Plan {
 };
 
 constexpr int64_t kMaxSlabBytes = (int64_t)512 << 20, kMaxPieceBytes = (int64_t)640 << 20;
+constexpr int64_t kMaxSlabs = 256;  // (64 splits of four pieces)
 
 // About how long a piece takes: its gradient tiles and its products (dx with the slabs it adds), and the launches.
 float piece_cost(int64_t M, int64_t rows, int64_t K, int P, bool want_dx, bool want_de) {
@@ -425,9 +426,10 @@ Plan make_plan(int64_t M, int64_t V, int64_t K, bool bf16, bool want_dx, bool wa
     p.maxima = take(2 * kMaximaBlocks * sizeof(float));
     if (want_dx) {
         // Each piece has slabs of its own, summed at the end: adding to a slab at the end of every piece's
-        // product costs more (all workgroups read and write at once, and nothing else runs).  Not past 512 MB.
+        // product costs more (all workgroups read and write at once, and nothing else runs).  Not past 512 MB or 256 slabs.
         const int64_t pieces = ceil_div(V, p.piece), slab = M * K * 4;
-        const int64_t room = kMaxSlabBytes / (slab * pieces);
+        const int64_t most_slabs = kMaxSlabBytes / slab < kMaxSlabs ? kMaxSlabBytes / slab : kMaxSlabs;
+        const int64_t room = most_slabs / pieces;
         p.add = pieces > 1 && room < 1;
         p.splits = grad_shape(M, K, p.piece < V ? p.piece : V, P, 1, (int)(p.add || room < 1 ? 1 : room > 64 ? 64 : room)).splits;
         p.slabs = (int)(p.add ? p.splits : pieces * p.splits);
@@ -436,7 +438,15 @@ Plan make_plan(int64_t M, int64_t V, int64_t K, bool bf16, bool want_dx, bool wa
         p.dx = take((size_t)(p.slabs * slab));
     }
     if (want_de) p.gw = take((size_t)(p.piece * p.Mp * P * 2));
-    p.bytes = at;
+    // The workspace is what the limits above allow, not what this plan takes (at most that): plans of shorter batches may
+    // take more, and a size that never falls as M, V or K grows serves them all.
+    int64_t d = kMaxPieceBytes > 8 * 256 * per_row ? kMaxPieceBytes : 8 * 256 * per_row, slabs = 0;
+    if (d > all * 256 * per_row) d = all * 256 * per_row;
+    if (want_dx) {
+        const int64_t slab = M * K * 4, few = slab * kMaxSlabs < kMaxSlabBytes ? slab * kMaxSlabs : kMaxSlabBytes;
+        slabs = slab > few ? slab : few;
+    }
+    p.bytes = (size_t)(2 * kMaximaBlocks * sizeof(float) + d + (slabs + 255) / 256 * 256);
     return p;
 }
 
@@ -487,17 +497,29 @@ int64_t row_tiles(const TileSplit& s, int64_t V) {
     return main_row_tiles(s) + (s.main < V ? ceil_div(V - s.main, tile_shape(s.tail).rows) : 0);
 }
 
+// The tiles' pairs that the forward pass has room for: all that tiles of 128 rows or more write, and 2^20, so that few
+// tokens may take smaller ones.  It grows with M and V: a longer batch's workspace serves a shorter one.
+int64_t most_pairs(int64_t M, int64_t V) { return M * ceil_div(V, 128) + ((int64_t)1 << 20); }
+
+// The forward pass's tiles.  (Past that room, of few shapes and at most 8 % by the cost: 320 tokens x 430248 rows x 32 with
+// 64 rows a tile.)
+TileSplit loss_tiles(int64_t M, int64_t V, int64_t K) {
+    const TileSplit s = split_rows(V, M, K);
+    return row_tiles(s, V) * M <= most_pairs(M, V) ? s : split_rows(V, M, K, kTile256, kTileKinds128);
+}
+
 }  // namespace
 
 size_t cross_entropy_workspace_bytes(int64_t M, int64_t V, int64_t K) {
-    return (size_t)(row_tiles(split_rows(V, M, K), V) * M) * sizeof(float2);
+    (void)K;
+    return (size_t)most_pairs(M, V) * sizeof(float2);
 }
 
 hipError_t launch_cross_entropy(const int8_t* x_q, const float* s_x, int64_t M, int64_t V, int64_t K, const int8_t* e,
                                 const float* s_e, const int32_t* targets, float* loss, float* lse, void* workspace,
                                 hipStream_t stream) {
     LossArgs a{x_q, s_x, M, V, (int)K, 0, 0, e, s_e, static_cast<float2*>(workspace)};
-    const TileSplit split = split_rows(V, M, K);
+    const TileSplit split = loss_tiles(M, V, K);
     a.V = split.main;
     if (hipError_t err = launch_loss_kind(a, split.kind, stream)) return err;
     if (split.main < V) {

@@ -516,9 +516,12 @@ Plan make_plan(int64_t T, int64_t V, int64_t K) {
         p.keys[i] = take(T * 4);
         p.order[i] = take(T * 4);
     }
-    p.hist = take((int64_t)p.sort_blocks * 256 * 4);
-    p.head = take(p.pieces * K * 4);
-    p.tail = take(p.pieces * K * 4);
+    // Room that no shorter batch's plan needs more of: its pieces, 8 tokens each up to 1024 of them, and its blocks, at
+    // most 64 up to 65536 tokens.
+    const int64_t rows = T < kRankMost ? (T + 7) / 8 : 1024;
+    p.hist = take((int64_t)(T > 65536 && p.sort_blocks < 64 ? 64 : p.sort_blocks) * 256 * 4);
+    p.head = take(rows * K * 4);
+    p.tail = take(rows * K * 4);
     p.bytes = at;
     return p;
 }

@@ -280,6 +280,7 @@ __device__ __forceinline__ bool tile_i8(const int8_t* __restrict__ w, int64_t ld
 
 enum TileKind { kTile256, kTile256x192, kTile128, kTile128x64, kTile64x64, kTile128x32, kTile64x32, kTile32x32, kTileKinds };
 constexpr int kTileKinds64 = kTile64x64 + 1;  // the first ones: 64 tokens or more
+constexpr int kTileKinds128 = kTile128x64 + 1;  // 128 rows or more
 
 struct TileShape {
     int rows, tokens;

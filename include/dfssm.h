@@ -486,7 +486,8 @@ dfssm_status dfssm_int8_gemm(const int8_t* x_q, int64_t ldx, const float* s_x, i
  * equal bits.  Accumulators are dfssm_int8_gemm's.
  * Errors: DFSSM_ERR_INVALID_ARG for a NULL or misaligned pointer, sizes <= 0 or >= 2^31, K % 16 != 0, a
  * short workspace; DFSSM_ERR_UNSUPPORTED for K > 131072, M > 2^25, V > 2^28 or M * V > 2^38.
- * The size query returns 0 for sizes that the call refuses.
+ * The size query returns 0 for sizes that the call refuses, and never falls as M, V or K grows: a workspace
+ * for the longest batch serves every shorter one.
  */
 size_t dfssm_cross_entropy_workspace_bytes(int64_t M, int64_t V, int64_t K);
 dfssm_status dfssm_cross_entropy(const int8_t* x_q, const float* s_x, int64_t M, int64_t V, int64_t K,
@@ -504,7 +505,8 @@ dfssm_status dfssm_cross_entropy(const int8_t* x_q, const float* s_x, int64_t M,
  *   dx  grad_type [M][K], or NULL;  de  grad_type [V][K], or NULL (a frozen matrix); not both NULL;
  *       16-byte aligned, written (every row), overlapping nothing
  *   workspace  at least dfssm_cross_entropy_backward_workspace_bytes(M, V, K, grad_type, dx != NULL,
- *              de != NULL) bytes, 16-byte aligned, under the forward call's rules
+ *              de != NULL) bytes, 16-byte aligned, under the forward call's rules (at most 1.2 GB for M <= 40000
+ *              and M K <= 2^27; a workspace for both gradients serves one, and one for fp32 serves bf16)
  * d s_e and d s_x enter the two products in 16-bit pieces, scaled by powers of two that put the largest
  * possible one inside fp16's range: for dx the token's own |dloss| max |s_e|, so that a token's gradient has the same
  * relative precision whatever the others' dloss are; for de, whose rows sum over the tokens, max |dloss s_x|.  For
@@ -551,7 +553,8 @@ dfssm_status dfssm_embedding_lookup_scaled(const int32_t* tokens, int64_t T, con
  * equal bits.
  * Errors: DFSSM_ERR_INVALID_ARG for a NULL or misaligned pointer, sizes <= 0 or >= 2^31, ldd < K, a type
  * that is none, accumulate other than 0 and 1, a short workspace; DFSSM_ERR_UNSUPPORTED for T > 2^24,
- * V > 2^28, K > 131072 or ldd >= 2^31.  The size query returns 0 for sizes that the call refuses.
+ * V > 2^28, K > 131072 or ldd >= 2^31.  The size query returns 0 for sizes that the call refuses, and never falls
+ * as T, V or K grows.
  */
 size_t dfssm_embedding_backward_workspace_bytes(int64_t T, int64_t V, int64_t K);
 dfssm_status dfssm_embedding_backward(const int32_t* tokens, int64_t T, const void* dout, int64_t ldd,

@@ -15,11 +15,12 @@
 // from them d, twice: d s_e with the vocabulary contiguous (for dx) and d s_x with the tokens contiguous
 // (for de), in 16-bit pieces (grad_gemm.h); two products with the codes then give the piece's rows of de
 // and its share of dx.  The gradient's type sets the pieces: fp32 takes two (relative error at most
-// 2^-19 of each d), bf16 one (2^-11, an eighth of the final rounding).  Recomputing the logits costs one
+// 2^-19 of each d: below the summation's where sums are long, above it where they are short, de of 64 tokens 6.6e-7 against
+// 64 bits), bf16 one (2^-11, an eighth of the final rounding).  Recomputing the logits costs one
 // int8 product; keeping them would cost 4 M V bytes written and read.
 //
 // What bounds it: forward, the int8 products under the power limit (tile_i8.h); backward, 4096 tokens x 50280 rows x
-// 2048 fp32 in 3.3 ms: the products for dx and de 1.28 and 1.34 ms (grad_gemm.h), the gradient tiles 0.65 ms, of which
+// 2048 fp32 in 3.3 ms: the products for dx and de 1.28 and 1.34 ms (grad_gemm.h), the gradient tiles 0.67 ms, of which
 // about 0.25 are their 8 bytes a logit (1.6 GB), written in bursts between the products.
 #include <math.h>
 

@@ -9,8 +9,9 @@
 //
 // What bounds it: many tokens, the products under the power limit and, in bursts that nothing overlaps, the stores
 // (2048 x 50280 x 2048: 241 us for bf16; the loss over the same logits 218); few tokens, reading w once
-// (50280 x 2048, 1 to 64 tokens: 17 to 19 us, 5.5 to 6 TB/s); few rows, the latency of K's chunks (1 x 2048 x
-// 4096: 6.1 us, of which 4 do not grow with K).
+// (50280 x 2048, 1 to 64 tokens: 17 to 19 us, 5.5 to 6 TB/s); few rows, the latency of K's chunks in a workgroup, and
+// CUs without one (1 x 2048 x 4096: 6.1 us, 64 workgroups).  For up to 16 tokens it is faster than the head's GEMV
+// (int8_head.hip; 50280 x 2048 20.9 against 24.5 us in a graph over uncached copies, 8512 x 2048 7.4 against 16.2).
 // Measured and not kept (before the rest of a last round went to small tiles): stores past the caches (275 against 276 us for 412 MB, 545 against 517 for 824), device-scope
 // stores (333), two smaller tiles to a CU so that stores overlap products (310 streamed, 337 not).
 #include <type_traits>

@@ -460,6 +460,7 @@ typedef enum {
  *   y    y_type [M][N], row m at element m*ldy, written; elements past N of a row are left
  * At K = 131072 one of two rows must hold a code other than -128 (the accumulator ends at 2^31 - 1); the
  * quantizer's codes, -127 to 127, always do.
+ * Where dfssm_int8_rowscale_gemm takes the shape both give the same bits, and this call is the faster.
  * Any alignment of x_q and w, any K; rows whose start and stride are multiples of 16 bytes, with
  * K % 16 == 0, are read fastest.  y needs its element's alignment and must not overlap an input.
  * Errors: DFSSM_ERR_INVALID_ARG for a NULL pointer, sizes <= 0 or >= 2^31, ldx or ldw < K, ldy < N,
@@ -482,7 +483,7 @@ dfssm_status dfssm_int8_gemm(const int8_t* x_q, int64_t ldx, const float* s_x, i
  *              contents need no preparation and mean nothing afterwards.  Calls that share one
  *              must not overlap in time; graphs captured with one may be replayed in turn.
  * x_q and e 16-byte aligned.  Scales must be finite (one of a position that does not count may be anything: only
- * its own lse shows it).  Requires K % 16 == 0.  Sums are formed in fp32 in a fixed order: equal inputs give
+ * its own lse shows it); a row whose logit they take to -infinity has probability 0.  Requires K % 16 == 0.  Sums are formed in fp32 in a fixed order: equal inputs give
  * equal bits.  Accumulators are dfssm_int8_gemm's.
  * Errors: DFSSM_ERR_INVALID_ARG for a NULL or misaligned pointer, sizes <= 0 or >= 2^31, K % 16 != 0, a
  * short workspace; DFSSM_ERR_UNSUPPORTED for K > 131072, M > 2^25, V > 2^28 or M * V > 2^38.
@@ -549,8 +550,9 @@ dfssm_status dfssm_embedding_lookup_scaled(const int32_t* tokens, int64_t T, con
  *   bytes, aligned to them, are fastest)
  *   workspace  at least dfssm_embedding_backward_workspace_bytes(T, V, K) bytes, 16-byte aligned,
  *              under dfssm_cross_entropy's rules
- * The tokens are sorted; a row's sum runs over its tokens in order, in fp32: equal inputs give
- * equal bits.
+ * The tokens are sorted and cut into pieces of equal length; a row's sum runs over its tokens in order within each piece,
+ * then over the pieces, in fp32: equal inputs give equal bits.  Added to a DFSSM_BF16 de the sum is rounded once more (a
+ * tied matrix's bf16 gradient is rounded by both calls, an fp32 one by neither to fewer bits).
  * Errors: DFSSM_ERR_INVALID_ARG for a NULL or misaligned pointer, sizes <= 0 or >= 2^31, ldd < K, a type
  * that is none, accumulate other than 0 and 1, a short workspace; DFSSM_ERR_UNSUPPORTED for T > 2^24,
  * V > 2^28, K > 131072 or ldd >= 2^31.  The size query returns 0 for sizes that the call refuses, and never falls

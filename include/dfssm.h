@@ -483,8 +483,8 @@ dfssm_status dfssm_int8_gemm(const int8_t* x_q, int64_t ldx, const float* s_x, i
  *              contents need no preparation and mean nothing afterwards.  Calls that share one
  *              must not overlap in time; graphs captured with one may be replayed in turn.
  * x_q and e 16-byte aligned.  Scales must be finite (one of a position that does not count may be anything: only
- * its own lse shows it); a row whose logit they take to -infinity has probability 0.  Requires K % 16 == 0.  Sums are formed in fp32 in a fixed order: equal inputs give
- * equal bits.  Accumulators are dfssm_int8_gemm's.
+ * its own lse shows it); a row whose logit they take to -infinity has probability 0.  Requires K % 16 == 0.
+ * Sums are formed in fp32 in a fixed order: equal inputs give equal bits.  Accumulators are dfssm_int8_gemm's.
  * Errors: DFSSM_ERR_INVALID_ARG for a NULL or misaligned pointer, sizes <= 0 or >= 2^31, K % 16 != 0, a
  * short workspace; DFSSM_ERR_UNSUPPORTED for K > 131072, M > 2^25, V > 2^28 or M * V > 2^38.
  * The size query returns 0 for sizes that the call refuses, and never falls as M, V or K grows: a workspace

@@ -197,7 +197,7 @@ def _prepare_scan(case, st, gen):
         st["dsin"] = torch.empty_like(st["sin"])
     if own:
         from bit_scaffold_int8_amd import dfssm
-        n = dfssm.dfssm_mamba2_scan_workspace_bytes(T, S, H, HEADDIM, N)
+        n = dfssm.dfssm_mamba2_scan_workspace_bytes(T, S, H, HEADDIM, N, G)
         if case["train"]:
             n = max(n, dfssm.dfssm_mamba2_scan_backward_workspace_bytes(T, S, H, HEADDIM, N, G))
         st["ws"] = torch.empty(n, dtype=torch.uint8, device="cuda")

@@ -7,6 +7,10 @@
 #include <hip/hip_runtime.h>
 #include <stdlib.h>
 
+#include <initializer_list>
+
+#include "scan.h"
+
 namespace dfssm {
 hipError_t launch_quantize_act(const float* x, int64_t M, int64_t K, int8_t* x_q, float* s_x,
                                hipStream_t stream);
@@ -75,6 +79,17 @@ size_t embedding_backward_workspace_bytes(int64_t T, int64_t V, int64_t K);
 hipError_t launch_embedding_backward(const int32_t* tokens, int64_t T, const void* dout, int64_t ldd, bool dout_bf16,
                                      int64_t V, int64_t K, float scale, void* de, bool de_bf16, bool accumulate,
                                      void* workspace, hipStream_t stream);
+hipError_t launch_mamba2_conv(const Sequences& seq, const void* u, int64_t ldu, bool bf16_in, int ch, const float* w,
+                              const float* b, const float* win, float* wout, void* out, int64_t ldo, bool bf16_out,
+                              hipStream_t stream);
+size_t mamba2_conv_backward_workspace_bytes(int64_t T, int64_t ch);
+hipError_t launch_mamba2_conv_backward(const Sequences& seq, const void* u, int64_t ldu, bool bf16_in, int ch, const float* w,
+                                       const float* b, const float* win, const void* dout, int64_t ldd, bool bf16_out,
+                                       const float* dwout, void* du, int64_t lddu, float* dw, float* db, float* dwin,
+                                       void* workspace, hipStream_t stream);
+size_t mamba2_scan_workspace_bytes(int64_t T, int64_t S, int64_t H, int64_t N, int64_t G);
+hipError_t launch_mamba2_scan(ScanArgs a, bool bf16, int N, const float* state_in, float* state_out, void* y, int64_t ldy,
+                              void* workspace, hipStream_t stream);
 }  // namespace dfssm
 
 #include "decode_args.h"
@@ -326,6 +341,75 @@ dfssm_status density_checks(int64_t rows, int64_t d_state) {
     if (rows <= 0 || d_state <= 0) return DFSSM_ERR_INVALID_ARG;
     if (!dfssm::density_field_supported(d_state)) return DFSSM_ERR_UNSUPPORTED;
     if (rows >= ((int64_t)1 << 40) / d_state) return DFSSM_ERR_INVALID_ARG;
+    return DFSSM_OK;
+}
+
+// ---- packed sequences
+constexpr int64_t kMaxTokens = (int64_t)1 << 20, kMaxChannels = (int64_t)1 << 20, kMaxLd = (int64_t)1 << 31;
+
+bool overlapping(const void* a, int64_t na, const void* b, int64_t nb) {
+    const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
+    return a && b && x < y + (uintptr_t)nb && y < x + (uintptr_t)na;
+}
+
+dfssm_status sequence_sizes(int64_t T, int64_t S, bool offsets) {
+    if (T <= 0 || S <= 0 || T >= kMaxRows || S >= kMaxRows || (!offsets && T % S != 0)) return DFSSM_ERR_INVALID_ARG;
+    if (T > kMaxTokens || S > kMaxBatch) return DFSSM_ERR_UNSUPPORTED;
+    return DFSSM_OK;
+}
+
+dfssm_status conv_sizes(int64_t T, int64_t S, int64_t ch, bool offsets) {
+    if (ch <= 0 || ch >= kMaxRows) return DFSSM_ERR_INVALID_ARG;
+    if (dfssm_status st = sequence_sizes(T, S, offsets)) return st;
+    return ch > kMaxChannels ? DFSSM_ERR_UNSUPPORTED : DFSSM_OK;
+}
+
+// A matrix's stride: what is shorter than a row is wrong, 2^31 and more is refused.
+dfssm_status stride_ok(int64_t ld, int64_t row) {
+    return ld < row ? DFSSM_ERR_INVALID_ARG : ld >= kMaxLd ? DFSSM_ERR_UNSUPPORTED : DFSSM_OK;
+}
+
+dfssm::Sequences sequences(const int32_t* cu, int64_t T, int64_t S) { return {cu, (int)T, (int)S, (int)(T / S)}; }
+
+dfssm_status scan_sizes(int64_t T, int64_t S, int64_t H, int64_t P, int64_t N, int64_t G, bool offsets) {
+    if (H <= 0 || P <= 0 || N <= 0 || G <= 0 || H >= kMaxRows || P >= kMaxRows || N >= kMaxRows || H % G != 0)
+        return DFSSM_ERR_INVALID_ARG;
+    if (dfssm_status st = sequence_sizes(T, S, offsets)) return st;
+    if (P != dfssm::kP || (N != 64 && N != 128) || H > 1024 || S * H > ((int64_t)1 << 21) ||
+        (T / dfssm::kChunk + S) * (H + 4 * G) > ((int64_t)1 << 25))
+        return DFSSM_ERR_UNSUPPORTED;
+    return DFSSM_OK;
+}
+
+// Rows that are read in pieces of 16 bytes.
+dfssm_status wide_rows(const void* p, int64_t ld, int64_t row, int32_t type) {
+    if (!aligned16(p) || ld % (type == DFSSM_BF16 ? 8 : 4) != 0) return DFSSM_ERR_INVALID_ARG;
+    return stride_ok(ld, row);
+}
+
+dfssm_status scan_operands(const dfssm_mamba2_scan_operands* op, dfssm::ScanArgs& a) {
+    if (!op || !op->x || !op->B || !op->C || !op->dt || !op->A_log || !op->D || !op->dt_bias) return DFSSM_ERR_INVALID_ARG;
+    if (!type_ok(op->type)) return DFSSM_ERR_INVALID_ARG;
+    const int64_t bc = op->ngroups * op->d_state;
+    const bool sized = op->nheads > 0 && op->nheads < kMaxRows && op->ngroups > 0 && op->ngroups < kMaxRows && op->d_state > 0 &&
+                       op->d_state < kMaxRows;
+    if (!sized) return DFSSM_ERR_INVALID_ARG;
+    if (!aligned16(op->state_in) || !aligned4(op->dt) || !aligned4(op->A_log) || !aligned4(op->D) ||
+        !aligned4(op->dt_bias) || !aligned4(op->cu_seqlens))
+        return DFSSM_ERR_INVALID_ARG;
+    // (what is wrong comes before what is not supported)
+    dfssm_status worst = scan_sizes(op->T, op->S, op->nheads, op->headdim, op->d_state, op->ngroups, op->cu_seqlens != nullptr);
+    for (dfssm_status st : {wide_rows(op->x, op->ldx, op->nheads * dfssm::kP, op->type), wide_rows(op->B, op->ldb, bc, op->type),
+                            wide_rows(op->C, op->ldc, bc, op->type), stride_ok(op->lddt, op->nheads)})
+        if (worst != DFSSM_ERR_INVALID_ARG && st != DFSSM_OK) worst = st;
+    if (worst != DFSSM_OK) return worst;
+    a = dfssm::ScanArgs{};
+    a.seq = sequences(op->cu_seqlens, op->T, op->S);
+    a.H = (int)op->nheads;
+    a.G = (int)op->ngroups;
+    a.x = op->x, a.B = op->B, a.C = op->C, a.dt = op->dt;
+    a.ldx = op->ldx, a.lddt = op->lddt, a.ldb = op->ldb, a.ldc = op->ldc;
+    a.A_log = op->A_log, a.D = op->D, a.dt_bias = op->dt_bias;
     return DFSSM_OK;
 }
 
@@ -653,6 +737,73 @@ dfssm_status dfssm_embedding_backward(const int32_t* tokens, int64_t T, const vo
     if (workspace_bytes < dfssm::embedding_backward_workspace_bytes(T, V, K)) return DFSSM_ERR_INVALID_ARG;
     return dfssm::launch_embedding_backward(tokens, T, dout, ldd, dout_type == DFSSM_BF16, V, K, scale, de,
                                             de_type == DFSSM_BF16, accumulate != 0, workspace, stream) == hipSuccess
+               ? DFSSM_OK
+               : DFSSM_ERR_HIP;
+}
+
+dfssm_status dfssm_mamba2_conv(const void* xbc, int64_t ldx, int32_t in_type, int64_t T, int64_t S, int64_t ch,
+                               const int32_t* cu_seqlens, const float* conv_w, const float* conv_b,
+                               const float* window_in, float* window_out, void* out, int64_t ldo, int32_t out_type,
+                               hipStream_t stream) {
+    if (!xbc || !conv_w || !conv_b || !out || !type_ok(in_type) || !type_ok(out_type)) return DFSSM_ERR_INVALID_ARG;
+    if (!aligned_type(xbc, in_type) || !aligned_type(out, out_type) || !aligned16(conv_w) || !aligned4(conv_b) ||
+        !aligned16(window_in) || !aligned16(window_out) || !aligned4(cu_seqlens) || ldx < ch || ldo < ch)
+        return DFSSM_ERR_INVALID_ARG;
+    if (dfssm_status st = conv_sizes(T, S, ch, cu_seqlens != nullptr)) return st;
+    if (overlapping(window_in, S * ch * 16, window_out, S * ch * 16)) return DFSSM_ERR_INVALID_ARG;
+    if (ldx >= kMaxLd || ldo >= kMaxLd) return DFSSM_ERR_UNSUPPORTED;
+    return dfssm::launch_mamba2_conv(sequences(cu_seqlens, T, S), xbc, ldx, in_type == DFSSM_BF16, (int)ch, conv_w, conv_b,
+                                     window_in, window_out, out, ldo, out_type == DFSSM_BF16, stream) == hipSuccess
+               ? DFSSM_OK
+               : DFSSM_ERR_HIP;
+}
+
+size_t dfssm_mamba2_conv_backward_workspace_bytes(int64_t T, int64_t S, int64_t ch) {
+    return conv_sizes(T, S, ch, true) == DFSSM_OK ? dfssm::mamba2_conv_backward_workspace_bytes(T, ch) : 0;
+}
+
+dfssm_status dfssm_mamba2_conv_backward(const void* xbc, int64_t ldx, int32_t in_type, int64_t T, int64_t S, int64_t ch,
+                                        const int32_t* cu_seqlens, const float* conv_w, const float* conv_b,
+                                        const float* window_in, const void* dout, int64_t ldd, int32_t out_type,
+                                        const float* dwindow_out, void* dxbc, int64_t lddx, float* dconv_w,
+                                        float* dconv_b, float* dwindow_in, void* workspace, size_t workspace_bytes,
+                                        hipStream_t stream) {
+    if (!xbc || !conv_w || !conv_b || !dout || !dxbc || !type_ok(in_type) || !type_ok(out_type)) return DFSSM_ERR_INVALID_ARG;
+    if ((dconv_w == nullptr) != (dconv_b == nullptr) || (dconv_w && !workspace)) return DFSSM_ERR_INVALID_ARG;
+    if (!aligned_type(xbc, in_type) || !aligned_type(dxbc, in_type) || !aligned_type(dout, out_type) || !aligned16(conv_w) ||
+        !aligned4(conv_b) || !aligned16(window_in) || !aligned16(dwindow_out) || !aligned16(dwindow_in) ||
+        !aligned16(dconv_w) || !aligned4(dconv_b) || !aligned16(workspace) || !aligned4(cu_seqlens) || ldx < ch || ldd < ch || lddx < ch)
+        return DFSSM_ERR_INVALID_ARG;
+    if (dfssm_status st = conv_sizes(T, S, ch, cu_seqlens != nullptr)) return st;
+    if (overlapping(dwindow_in, S * ch * 16, dwindow_out, S * ch * 16) || overlapping(dwindow_in, S * ch * 16, window_in, S * ch * 16))
+        return DFSSM_ERR_INVALID_ARG;
+    if (dconv_w && workspace_bytes < dfssm::mamba2_conv_backward_workspace_bytes(T, ch)) return DFSSM_ERR_INVALID_ARG;
+    if (ldx >= kMaxLd || ldd >= kMaxLd || lddx >= kMaxLd) return DFSSM_ERR_UNSUPPORTED;
+    return dfssm::launch_mamba2_conv_backward(sequences(cu_seqlens, T, S), xbc, ldx, in_type == DFSSM_BF16, (int)ch, conv_w,
+                                              conv_b, window_in, dout, ldd, out_type == DFSSM_BF16, dwindow_out, dxbc, lddx,
+                                              dconv_w, dconv_b, dwindow_in, workspace, stream) == hipSuccess
+               ? DFSSM_OK
+               : DFSSM_ERR_HIP;
+}
+
+size_t dfssm_mamba2_scan_workspace_bytes(int64_t T, int64_t S, int64_t nheads, int64_t headdim, int64_t d_state,
+                                         int64_t ngroups) {
+    if (scan_sizes(T, S, nheads, headdim, d_state, ngroups, true) != DFSSM_OK) return 0;
+    return dfssm::mamba2_scan_workspace_bytes(T, S, nheads, d_state, ngroups);
+}
+
+dfssm_status dfssm_mamba2_scan(const dfssm_mamba2_scan_operands* op, void* y, int64_t ldy, float* state_out,
+                               void* workspace, size_t workspace_bytes, hipStream_t stream) {
+    dfssm::ScanArgs a;
+    if (!y || !workspace || !aligned16(workspace) || !aligned16(state_out)) return DFSSM_ERR_INVALID_ARG;
+    if (dfssm_status st = scan_operands(op, a)) return st;
+    if (dfssm_status st = wide_rows(y, ldy, op->nheads * dfssm::kP, op->type)) return st;
+    const int64_t states = op->S * op->nheads * dfssm::kP * op->d_state * 4;
+    if (state_out != op->state_in && overlapping(state_out, states, op->state_in, states)) return DFSSM_ERR_INVALID_ARG;
+    if (workspace_bytes < dfssm::mamba2_scan_workspace_bytes(op->T, op->S, op->nheads, op->d_state, op->ngroups))
+        return DFSSM_ERR_INVALID_ARG;
+    return dfssm::launch_mamba2_scan(a, op->type == DFSSM_BF16, (int)op->d_state, op->state_in, state_out, y, ldy, workspace,
+                                     stream) == hipSuccess
                ? DFSSM_OK
                : DFSSM_ERR_HIP;
 }

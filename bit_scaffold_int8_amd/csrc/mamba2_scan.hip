@@ -1,0 +1,625 @@
+// mamba2_scan.hip -- the Mamba-2 scan over packed sequences (gfx950): a linear attention whose state decays by
+// a factor for each head and token.
+//
+//   h_t = e^{a_t} h_{t-1} + dt_t x_t B_t^T,   y_t = h_t C_t + D x_t,   a_t = -dt_t exp(A_log)
+//
+// Two forms.  Short sequences (single tokens above all) go token by token through the recurrence, like the decode step: the
+// states, 32 KB a head, are read and written once and everything else is small.  Longer ones go in chunks of 64 tokens, in
+// which the recurrence is a product of matrices (cs: the decays' running sum within the chunk):
+//
+//   y_t = sum_{s <= t} e^{cs_t - cs_s} (C_t . B_s) dt_s x_s  +  e^{cs_t} h_start C_t  +  D x_t
+//   h_end = e^{cs_end} h_start + sum_s e^{cs_end - cs_s} dt_s x_s B_s^T
+//
+//  * prepare: for each chunk, what its heads share: the products C . B of a group, B and C as bf16 pieces in the order in
+//    which the matrix instructions take them (scan.h), and the decays of each head.
+//  * sweep: a wave owns 32 channels of a head and walks over the chunks of a segment with their state, 32 x N fp32
+//    values, in registers as the matrix instructions' accumulators.  These are at the same time operands of h C: the state
+//    goes through no memory between chunks.  The two heads of a workgroup share the pieces of B and C in LDS.
+//  * One sequence has too few heads to fill the GPU, so it is cut into segments of several chunks: a first sweep
+//    finds what each segment adds to the state, a small kernel joins them in order, the second sweep starts from the joined ones.
+#include <math.h>
+
+#include "scan.h"
+
+namespace dfssm {
+
+namespace {
+
+constexpr double kLog2eD = 1.4426950408889634074;
+constexpr int kSweepThreads = 256;
+
+__device__ __forceinline__ int4 chunk_of(const ScanArgs& a, int c) {
+    if (a.chunks) return a.chunks[c];
+    const int per = (a.seq.L + kChunk - 1) / kChunk, s = c / per, i = c - s * per;
+    const int left = a.seq.L - i * kChunk;
+    return make_int4(s * a.seq.L + i * kChunk, left < kChunk ? left : kChunk, s, 0);
+}
+
+// w: 1 the sequence's first segment, 2 its last
+__device__ __forceinline__ int4 segment_of(const ScanArgs& a, int g) {
+    if (a.segments) return a.segments[g];
+    const int chunks = (a.seq.L + kChunk - 1) / kChunk, per = (chunks + a.per_segment - 1) / a.per_segment;
+    const int s = g / per, i = g - s * per, left = chunks - i * a.per_segment;
+    return make_int4(s * chunks + i * a.per_segment, left < a.per_segment ? left : a.per_segment, s,
+                     (i == 0 ? 1 : 0) | (i == per - 1 ? 2 : 0));
+}
+
+// ---------------------------------------------------------------- the tables of packed sequences
+
+// Chunks and segments of every sequence, one after another (a sequence without tokens has one empty chunk: its state passes
+// through).  One workgroup: a running sum over the sequences, then each table entry finds its sequence by bisection.
+__global__ __launch_bounds__(1024) void scan_tables_kernel(ScanArgs a, int* __restrict__ first_chunk) {
+    __shared__ int2 sums[1024];
+    __shared__ int2 base;
+    const int tid = threadIdx.x, S = a.seq.S;
+    if (tid == 0) base = make_int2(0, 0);
+    __syncthreads();
+    for (int s0 = 0; s0 < S; s0 += 1024) {
+        const int s = s0 + tid;
+        int2 n = make_int2(0, 0);
+        if (s < S) {
+            const Span p = span_of(a.seq, s);
+            n.x = p.end > p.begin ? (p.end - p.begin + kChunk - 1) / kChunk : 1;
+            n.y = (n.x + a.per_segment - 1) / a.per_segment;
+        }
+        sums[tid] = n;
+        __syncthreads();
+        for (int d = 1; d < 1024; d <<= 1) {
+            const int2 o = tid >= d ? sums[tid - d] : make_int2(0, 0);
+            __syncthreads();
+            sums[tid].x += o.x;
+            sums[tid].y += o.y;
+            __syncthreads();
+        }
+        if (s < S) {
+            // (bad offsets may claim more chunks than there is room for: those past it do not exist)
+            const int c = base.x + sums[tid].x - n.x, g = base.y + sums[tid].y - n.y;
+            first_chunk[s] = c < a.nchunks ? c : a.nchunks;
+            a.first_segment[s] = g < a.nsegments ? g : a.nsegments;
+        }
+        __syncthreads();
+        if (tid == 0) {
+            base.x = base.x + sums[1023].x < a.nchunks ? base.x + sums[1023].x : a.nchunks;
+            base.y = base.y + sums[1023].y < a.nsegments ? base.y + sums[1023].y : a.nsegments;
+        }
+        __syncthreads();
+    }
+    if (tid == 0) {
+        first_chunk[S] = base.x;
+        a.first_segment[S] = base.y;
+    }
+    __syncthreads();
+    auto owner = [&](const int* first, int i) {  // the last sequence that starts at entry i or before it
+        int lo = 0, hi = S - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (first[mid] <= i) lo = mid;
+            else hi = mid - 1;
+        }
+        return lo;
+    };
+    for (int i = tid; i < a.nchunks; i += 1024) {
+        int4 v = make_int4(0, 0, -1, 0);
+        if (i < first_chunk[S]) {
+            const int s = owner(first_chunk, i);
+            const Span p = span_of(a.seq, s);
+            const int at = p.begin + (i - first_chunk[s]) * kChunk, left = p.end - at;
+            v = make_int4(at, left < 0 ? 0 : left < kChunk ? left : kChunk, s, 0);
+        }
+        a.chunks[i] = v;
+    }
+    for (int i = tid; i < a.nsegments; i += 1024) {
+        int4 v = make_int4(0, 0, -1, 0);
+        if (i < a.first_segment[S]) {
+            const int s = owner(a.first_segment, i), n = i - a.first_segment[s];
+            const int c = first_chunk[s] + n * a.per_segment, left = first_chunk[s + 1] - c;
+            v = make_int4(c, left < 0 ? 0 : left < a.per_segment ? left : a.per_segment, s,
+                          (n == 0 ? 1 : 0) | (i + 1 == a.first_segment[s + 1] ? 2 : 0));
+        }
+        a.segments[i] = v;
+    }
+}
+
+// ---------------------------------------------------------------- prepare
+
+// The decays of one head over a chunk, a token a lane.
+__device__ void head_arrays(const ScanArgs& a, const int4& ch, int c, int h) {
+    const int lane = threadIdx.x & 63;
+    float dt = 0.0f;
+    if (lane < ch.y) dt = scan_softplus(a.dt[(int64_t)(ch.x + lane) * a.lddt + h] + a.dt_bias[h]);
+    // A factor below 2^-4096 is zero, and so is every product of decays that has it: cut there, the sums stay finite.
+    double cs = -(double)dt * (double)expf(a.A_log[h]) * kLog2eD;
+    cs = cs < -4096.0 ? -4096.0 : cs;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const double o = __shfl_up(cs, d);
+        if (lane >= d) cs += o;
+    }
+    const double end = __shfl(cs, 63);
+    float* const out = a.heads + ((int64_t)c * a.H + h) * kHeadArrays * kChunk + lane;
+    const float hi = (float)cs;
+    out[kCsHi * kChunk] = hi;
+    out[kCsLo * kChunk] = (float)(cs - (double)hi);
+    out[kStep * kChunk] = dt;
+    out[kWeight * kChunk] = dt * __builtin_amdgcn_exp2f((float)(end - cs));
+    out[kDecay * kChunk] = __builtin_amdgcn_exp2f(hi);
+}
+
+// Workgroups (chunk, y): y below G the group's products and pieces, behind them the decays of four heads each.
+template <bool kBf16, int kN, bool kBackward>
+__global__ __launch_bounds__(256) void prepare_kernel(ScanArgs a) {
+    constexpr int kPieces = kBf16 ? 1 : 3, kLd = kN + 4, kTiles = kN / 16, kSteps = kN / 32;
+    using Block = GroupBlock<kN, kPieces>;
+    __shared__ __attribute__((aligned(16))) float rows[2][kChunk * kLd];
+    const int c = blockIdx.x;
+    const int4 ch = chunk_of(a, c);
+    if (ch.z < 0 || ch.y <= 0) return;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    if ((int)blockIdx.y >= a.G) {
+        const int h = ((int)blockIdx.y - a.G) * 4 + wave;
+        if (h < a.H) head_arrays(a, ch, c, h);
+        return;
+    }
+    const int g = blockIdx.y;
+    using E = Elem<kBf16>;
+    for (int i = tid; i < 2 * kChunk * (kN / 4); i += 256) {
+        const int which = i / (kChunk * (kN / 4)), r = i / (kN / 4) % kChunk, k = i % (kN / 4) * 4;
+        const int64_t at = (int64_t)(ch.x + (r < ch.y ? r : 0)) * (which ? a.ldc : a.ldb) + g * kN + k;
+        v4f v = E::load4(static_cast<const typename E::type*>(which ? a.C : a.B) + at);
+        if (r >= ch.y) v = v4f{0.0f, 0.0f, 0.0f, 0.0f};   // (whatever lies behind the sequence takes no part)
+        *reinterpret_cast<v4f*>(&rows[which][r * kLd + k]) = v;
+    }
+    __syncthreads();
+    uint8_t* const out = a.groups + ((int64_t)c * a.G + g) * (kBackward ? Block::backward : Block::forward);
+    const int r = lane & 15, q = lane >> 4;
+    // eight values of a token's row / across the tokens
+    auto along = [&](int which, int tile, int step) {
+        const float* p = &rows[which][(tile * 16 + r) * kLd + step * 32 + 4 * q];
+        const v4f lo = *reinterpret_cast<const v4f*>(p), hi = *reinterpret_cast<const v4f*>(p + 16);
+        const float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+        return split<kPieces>(v);
+    };
+    auto across = [&](int which, int tile, int step) {
+        float v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = rows[which][(step * 32 + place(q, j)) * kLd + tile * 16 + r];
+        return split<kPieces>(v);
+    };
+    // products: forward rows s, columns t (s <= t); backward rows t, columns s
+    constexpr int kRowSide = kBackward ? 1 : 0;
+    int n = 0;
+    for (int rt = 0; rt < 4; ++rt)
+        for (int ct = 0; ct < 4; ++ct) {
+            if (kBackward ? ct > rt : ct < rt) continue;
+            if ((n++ & 3) != wave) continue;
+            v4f acc = {0.0f, 0.0f, 0.0f, 0.0f};
+            for (int k = 0; k < kSteps; ++k) acc = mma(along(kRowSide, rt, k), along(1 - kRowSide, ct, k), acc);
+            *reinterpret_cast<v4f*>(out + ((rt * 4 + ct) * 64 + lane) * 16) = acc;
+        }
+    for (int i = wave; i < 4 * kSteps; i += 4)
+        store_pieces(out + Block::kRows + (i * 64 + lane) * 16, Block::kPlane, along(1 - kRowSide, i / kSteps, i % kSteps));
+    for (int i = wave; i < kTiles * 2; i += 4) {
+        store_pieces(out + Block::kAcross + (i * 64 + lane) * 16, Block::kPlane, across(0, i / 2, i % 2));
+        if constexpr (kBackward)
+            store_pieces(out + Block::kCross + (i * 64 + lane) * 16, Block::kPlane, across(1, i / 2, i % 2));
+    }
+}
+
+// ---------------------------------------------------------------- the sweep
+
+// A set of pieces from memory to LDS.
+template <int kBytes>
+__device__ __forceinline__ void stage(const uint8_t* from, uint8_t* lds) {
+    constexpr int kEach = kBytes / (kSweepThreads * 16);
+    static_assert(kEach * kSweepThreads * 16 == kBytes, "whole pieces of 16 bytes a thread");
+    v4i v[kEach];
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) v[i] = *reinterpret_cast<const v4i*>(from + (i * kSweepThreads + threadIdx.x) * 16);
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) *reinterpret_cast<v4i*>(lds + (i * kSweepThreads + threadIdx.x) * 16) = v[i];
+}
+
+__device__ __forceinline__ void unpack(float (&f)[8], v4f lo, v4f hi) {
+    f[0] = lo.x, f[1] = lo.y, f[2] = lo.z, f[3] = lo.w, f[4] = hi.x, f[5] = hi.y, f[6] = hi.z, f[7] = hi.w;
+}
+
+template <bool kBf16, int kN, int kMode>
+__global__ __launch_bounds__(kSweepThreads, 2) void sweep_kernel(SweepArgs s) {
+    // pieces of the data; of the state and of the chunk's own products where y is bf16: two leave an error of 2^-17, far
+    // below its rounding; of what goes into the state, which is fp32 whatever the data: three
+    constexpr int kData = kBf16 ? 1 : 3, kOut = kBf16 ? 2 : 3, kIn = 3;
+    constexpr int kTiles = kN / 16, kSteps = kN / 32;
+    using Block = GroupBlock<kN, kData>;
+    using E = Elem<kBf16>;
+    __shared__ __attribute__((aligned(16))) uint8_t lds[Block::kSet];
+    const ScanArgs& a = s.a;
+    const int per_group = a.H / a.G, pairs = (per_group + 1) / 2;
+    const int seg = blockIdx.x / (a.G * pairs), rest = blockIdx.x % (a.G * pairs);
+    const int g = rest / pairs, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    const int in_group = rest % pairs * 2 + (wave >> 1), half = wave & 1;
+    const bool live = in_group < per_group;      // (an odd group's last pair is one head)
+    const int head = g * per_group + (live ? in_group : 0);
+    const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
+    const int4 sg = segment_of(a, seg);
+    if (sg.z < 0) return;
+    const int p0 = half * 32 + r;                // the lane's channel of the first of two tiles
+
+    v4f h[kTiles][2];
+    const int64_t mine = ((int64_t)sg.z * a.H + head) * kP * kN;
+    v4f* const slot = s.segment_states ? reinterpret_cast<v4f*>(s.segment_states) +
+                                             (((int64_t)seg * a.H + head) * 2 + half) * kTiles * 2 * 64 + lane : nullptr;
+#pragma unroll
+    for (int n = 0; n < kTiles; ++n)
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+            h[n][p] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+            if constexpr (kMode != kLocal) {
+                if (slot) h[n][p] = slot[(n * 2 + p) * 64];
+                else if (s.start) h[n][p] = *reinterpret_cast<const v4f*>(s.start + mine + (p0 + p * 16) * kN + n * 16 + 4 * q);
+            }
+        }
+    float through = 1.0f;  // the segment's decay
+    const float skip = kMode == kOutput ? a.D[head] : 0.0f;
+
+    for (int i = 0; i < sg.y; ++i) {
+        const int c = s.reverse ? sg.x + sg.y - 1 - i : sg.x + i;
+        const int4 ch = chunk_of(a, c);
+        if (ch.y <= 0) continue;
+        const uint8_t* const block = a.groups + ((int64_t)c * a.G + g) * s.group_bytes;
+        const float* const arrays = a.heads + ((int64_t)c * a.H + head) * kHeadArrays * kChunk;
+        if (kMode == kStarts && live) {
+            float* const out = s.starts + ((int64_t)c * a.H + head) * kP * kN;
+#pragma unroll
+            for (int n = 0; n < kTiles; ++n)
+#pragma unroll
+                for (int p = 0; p < 2; ++p) *reinterpret_cast<v4f*>(out + (p0 + p * 16) * kN + n * 16 + 4 * q) = h[n][p];
+        }
+        // the chunk's rows of v, places of the sums along its tokens; zero behind the sequence
+        float v[2][2][8];
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int row = k * 32 + place(q, j), there = row < ch.y ? row : 0;
+                const auto* at = static_cast<const typename E::type*>(s.v) + (int64_t)(ch.x + there) * s.ldv + head * kP + p0;
+#pragma unroll
+                for (int p = 0; p < 2; ++p) {
+                    const float x = E::load(at + p * 16);
+                    v[k][p][j] = row < ch.y ? x : 0.0f;
+                }
+            }
+        if constexpr (kMode == kOutput) {
+            stage<Block::kSet>(block + Block::kRows, lds);
+            __syncthreads();
+            if (live) {
+                v4f y[4][2];
+#pragma unroll
+                for (int t = 0; t < 4; ++t) y[t][0] = y[t][1] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int k = 0; k < kSteps; ++k) {
+                    Pieces<kOut> state[2];
+#pragma unroll
+                    for (int p = 0; p < 2; ++p) {
+                        float f[8];
+                        unpack(f, h[2 * k][p], h[2 * k + 1][p]);
+                        state[p] = split<kOut>(f);
+                    }
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) {
+                        const Pieces<kData> cr = load_pieces<kData>(lds + ((t * kSteps + k) * 64 + lane) * 16, Block::kPlane);
+                        y[t][0] = mma(cr, state[0], y[t][0]);
+                        y[t][1] = mma(cr, state[1], y[t][1]);
+                    }
+                }
+#pragma unroll
+                for (int t = 0; t < 4; ++t) {
+                    const v4f e = *reinterpret_cast<const v4f*>(arrays + kDecay * kChunk + t * 16 + 4 * q);
+                    y[t][0] *= e;
+                    y[t][1] *= e;
+                }
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {   // 32 tokens s
+                    Pieces<kData> x[2];
+                    x[0] = split<kData>(v[k][0]);
+                    x[1] = split<kData>(v[k][1]);
+                    float hi[8], lo[8], step[8];
+                    const float* const from = arrays + k * 32 + 4 * q;
+                    unpack(hi, *reinterpret_cast<const v4f*>(from), *reinterpret_cast<const v4f*>(from + 16));
+                    unpack(lo, *reinterpret_cast<const v4f*>(from + kCsLo * kChunk), *reinterpret_cast<const v4f*>(from + kCsLo * kChunk + 16));
+                    unpack(step, *reinterpret_cast<const v4f*>(from + kStep * kChunk), *reinterpret_cast<const v4f*>(from + kStep * kChunk + 16));
+#pragma unroll
+                    for (int t = 2 * k; t < 4; ++t) {
+                        const float thi = arrays[t * 16 + r], tlo = arrays[kCsLo * kChunk + t * 16 + r];
+                        float w[8];
+                        const uint8_t* const products = block + ((2 * k * 4 + t) * 64 + lane) * 16;
+                        const v4f g0 = *reinterpret_cast<const v4f*>(products);
+                        const v4f g1 = t > 2 * k ? *reinterpret_cast<const v4f*>(products + 4 * 64 * 16) : v4f{0.0f, 0.0f, 0.0f, 0.0f};
+                        unpack(w, g0, g1);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            const int row = k * 32 + place(q, j);
+                            const float f = step[j] * __builtin_amdgcn_exp2f((thi - hi[j]) + (tlo - lo[j]));
+                            w[j] = t * 16 + r >= row ? w[j] * f : 0.0f;
+                        }
+                        const Pieces<kOut> wp = split<kOut>(w);
+                        y[t][0] = mma(wp, x[0], y[t][0]);
+                        y[t][1] = mma(wp, x[1], y[t][1]);
+                    }
+                }
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int row = t * 16 + 4 * q + j;
+                        auto* at = static_cast<typename E::type*>(s.y) + (int64_t)(ch.x + row) * s.ldy + head * kP + p0;
+                        if (row < ch.y) {
+#pragma unroll
+                            for (int p = 0; p < 2; ++p)
+                                E::store(at + p * 16, fmaf(skip, v[t >> 1][p][(t & 1) * 4 + j], y[t][p][j]));
+                        }
+                    }
+            }
+            __syncthreads();
+        }
+        stage<Block::kSet>(block + s.key, lds);
+        __syncthreads();
+        if (live) {
+            const float last = arrays[kDecay * kChunk + kChunk - 1];
+            through *= last;
+#pragma unroll
+            for (int n = 0; n < kTiles; ++n) {
+                h[n][0] *= last;
+                h[n][1] *= last;
+            }
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const float* const from = arrays + (s.reverse ? kDecay : kWeight) * kChunk + k * 32 + 4 * q;
+                float w[8];
+                unpack(w, *reinterpret_cast<const v4f*>(from), *reinterpret_cast<const v4f*>(from + 16));
+                Pieces<kIn> in[2];
+#pragma unroll
+                for (int p = 0; p < 2; ++p) {
+                    float f[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) f[j] = v[k][p][j] * w[j];
+                    in[p] = split<kIn>(f);
+                }
+#pragma unroll
+                for (int n = 0; n < kTiles; ++n) {
+                    const Pieces<kData> key = load_pieces<kData>(lds + ((n * 2 + k) * 64 + lane) * 16, Block::kPlane);
+                    h[n][0] = mma(key, in[0], h[n][0]);
+                    h[n][1] = mma(key, in[1], h[n][1]);
+                }
+            }
+        }
+        __syncthreads();
+    }
+    if (!live) return;
+    if constexpr (kMode == kLocal) {
+#pragma unroll
+        for (int n = 0; n < kTiles; ++n)
+#pragma unroll
+            for (int p = 0; p < 2; ++p) slot[(n * 2 + p) * 64] = h[n][p];
+        if (half == 0 && lane == 0) s.segment_decay[(int64_t)seg * a.H + head] = through;
+    } else if (s.end && (sg.w & (s.reverse ? 1 : 2))) {
+#pragma unroll
+        for (int n = 0; n < kTiles; ++n)
+#pragma unroll
+            for (int p = 0; p < 2; ++p)
+                *reinterpret_cast<v4f*>(s.end + mine + (p0 + p * 16) * kN + n * 16 + 4 * q) = h[n][p];
+    }
+}
+
+// The state at the start of every segment of a sequence, in place of what the segments add.
+template <int kN>
+__global__ __launch_bounds__(256) void join_segments_kernel(SweepArgs s) {
+    constexpr int kTiles = kN / 16, kEach = kP * kN / 4;   // v4f of a head
+    const int sequence = blockIdx.x / s.a.H, head = blockIdx.x % s.a.H;
+    const int i = blockIdx.y * 256 + threadIdx.x;
+    const int lane = i & 63, p = i / 64 % 2, n = i / 128 % kTiles, half = i / (128 * kTiles);
+    const int per = (s.a.seq.L + kChunk - 1) / kChunk;
+    const int each = s.a.segments ? 0 : (per + s.a.per_segment - 1) / s.a.per_segment;
+    const int first = s.a.segments ? s.a.first_segment[sequence] : sequence * each;
+    const int count = (s.a.segments ? s.a.first_segment[sequence + 1] : first + each) - first;
+    v4f h = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (s.start)
+        h = *reinterpret_cast<const v4f*>(s.start + (((int64_t)sequence * s.a.H + head) * kP + half * 32 + p * 16 + (lane & 15)) * kN +
+                                          n * 16 + 4 * (lane >> 4));
+    v4f* const states = reinterpret_cast<v4f*>(s.segment_states);
+#pragma unroll 4
+    for (int k = 0; k < count; ++k) {
+        const int64_t at = (int64_t)(s.reverse ? first + count - 1 - k : first + k) * s.a.H + head;
+        const v4f add = states[at * kEach + i];
+        const float decay = s.segment_decay[at];
+        states[at * kEach + i] = h;
+        h = h * decay + add;
+    }
+}
+
+// ---------------------------------------------------------------- the recurrence, token by token
+
+// As in the decode step, 16 channels of a head to a workgroup and 16 threads to a channel: each state value is read
+// and written once by one thread.  The next token's operands are loaded while this one's are used.
+template <bool kBf16, int kN>
+__global__ __launch_bounds__(256) void recurrent_kernel(SweepArgs s) {
+    constexpr int kV = kN / 16, kV4 = kV / 4;
+    using E = Elem<kBf16>;
+    using T = typename E::type;
+    const ScanArgs& a = s.a;
+    const int head = blockIdx.x / 4, p = blockIdx.x % 4 * 16 + threadIdx.x / 16, q = threadIdx.x % 16;
+    const int sequence = blockIdx.y, g = head / (a.H / a.G);
+    const Span span = span_of(a.seq, sequence);
+    const int64_t at = (((int64_t)sequence * a.H + head) * kP + p) * kN + kV * q;
+    v4f h[kV4], b[kV4], c[kV4];
+#pragma unroll
+    for (int i = 0; i < kV4; ++i) h[i] = s.start ? *reinterpret_cast<const v4f*>(s.start + at + 4 * i) : v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    float x = 0.0f, raw = 0.0f;
+    auto fetch = [&](int t) {
+        x = E::load(static_cast<const T*>(s.v) + t * s.ldv + head * kP + p);
+        raw = a.dt[t * a.lddt + head];
+#pragma unroll
+        for (int i = 0; i < kV4; ++i) {
+            b[i] = E::load4(static_cast<const T*>(a.B) + t * a.ldb + g * kN + kV * q + 4 * i);
+            c[i] = E::load4(static_cast<const T*>(a.C) + t * a.ldc + g * kN + kV * q + 4 * i);
+        }
+    };
+    const float rate = expf(a.A_log[head]), bias = a.dt_bias[head], skip = a.D[head];
+    if (span.begin < span.end) fetch(span.begin);
+    for (int t = span.begin; t < span.end; ++t) {
+        const float dt = scan_softplus(raw + bias), decay = expf(-dt * rate), dtx = dt * x, own = skip * x;
+        float y = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kV4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                h[i][j] = fmaf(h[i][j], decay, dtx * b[i][j]);
+                y = fmaf(h[i][j], c[i][j], y);
+            }
+        if (t + 1 < span.end) fetch(t + 1);
+        y += dpp_f<kDppXor1>(y);
+        y += dpp_f<kDppXor2>(y);
+        y += dpp_f<kDppHalfMirror>(y);
+        y += dpp_f<kDppMirror>(y);
+        if (q == 0) E::store(static_cast<T*>(s.y) + t * s.ldy + head * kP + p, own + y);
+    }
+    if (s.end)
+#pragma unroll
+        for (int i = 0; i < kV4; ++i) *reinterpret_cast<v4f*>(s.end + at + 4 * i) = h[i];
+}
+
+template <class F>
+hipError_t with_kind(bool bf16, int N, F f) {
+    if (N == 128) return bf16 ? f(std::true_type(), std::integral_constant<int, 128>()) : f(std::false_type(), std::integral_constant<int, 128>());
+    return bf16 ? f(std::true_type(), std::integral_constant<int, 64>()) : f(std::false_type(), std::integral_constant<int, 64>());
+}
+
+}  // namespace
+
+hipError_t launch_scan_prepare(const ScanArgs& a, bool bf16, int N, bool backward, hipStream_t stream) {
+    if (a.chunks) {
+        scan_tables_kernel<<<1, 1024, 0, stream>>>(a, a.first_segment + a.seq.S + 1);
+        if (hipError_t err = hipGetLastError()) return err;
+    }
+    return with_kind(bf16, N, [&](auto b, auto n) {
+        const dim3 grid((unsigned)a.nchunks, (unsigned)(a.G + (a.H + 3) / 4));
+        if (backward) prepare_kernel<b.value, n.value, true><<<grid, 256, 0, stream>>>(a);
+        else prepare_kernel<b.value, n.value, false><<<grid, 256, 0, stream>>>(a);
+        return hipGetLastError();
+    });
+}
+
+hipError_t launch_sweep(const SweepArgs& s, const ScanPlan& plan, bool bf16, int N, SweepMode mode, hipStream_t stream) {
+    const dim3 grid((unsigned)(plan.nsegments * s.a.G * ((s.a.H / s.a.G + 1) / 2)));
+    return with_kind(bf16, N, [&](auto b, auto n) {
+        if (plan.segmented) {
+            sweep_kernel<b.value, n.value, kLocal><<<grid, kSweepThreads, 0, stream>>>(s);
+            if (hipError_t err = hipGetLastError()) return err;
+            join_segments_kernel<n.value><<<dim3((unsigned)(s.a.seq.S * s.a.H), kP * n.value / 1024), 256, 0, stream>>>(s);
+            if (hipError_t err = hipGetLastError()) return err;
+        }
+        if (mode == kStarts) sweep_kernel<b.value, n.value, kStarts><<<grid, kSweepThreads, 0, stream>>>(s);
+        else sweep_kernel<b.value, n.value, kOutput><<<grid, kSweepThreads, 0, stream>>>(s);
+        return hipGetLastError();
+    });
+}
+
+// ---------------------------------------------------------------- the host's side
+
+// Sequences of up to this many tokens on average go token by token.
+constexpr int kRecurrentTokens = 8;
+
+bool scan_recurrent(const Sequences& seq) { return seq.T <= (int64_t)kRecurrentTokens * seq.S; }
+
+// Enough workgroups for two on each CU: what one segment a sequence does not give, more segments do, at the price of a
+// second sweep without outputs.
+constexpr int kSweepGroups = 512;
+constexpr int64_t kMaxSegmentHeads = 4 * kSweepGroups;   // room for the segments' states, in heads
+
+ScanPlan scan_plan(const Sequences& seq, int H, int G) {
+    ScanPlan p{};
+    const int64_t pairs = (int64_t)G * ((H / G + 1) / 2);
+    const int64_t each = (seq.L + kChunk - 1) / kChunk;    // chunks of a sequence, without offsets
+    p.nchunks = (int)(seq.cu ? seq.T / kChunk + seq.S : seq.S * each);
+    const int64_t all = p.nchunks * pairs;
+    int64_t per = seq.S * pairs >= kSweepGroups ? p.nchunks : (all + kSweepGroups - 1) / kSweepGroups;
+    if (per < 1) per = 1;
+    auto segments = [&](int64_t n) { return seq.cu ? p.nchunks / n + seq.S : seq.S * ((each + n - 1) / n); };
+    while (per < p.nchunks && segments(per) * H > kMaxSegmentHeads) per *= 2;
+    if (per > p.nchunks) per = p.nchunks;
+    p.segmented = seq.cu ? per < p.nchunks : per < each;
+    if (!p.segmented) per = p.nchunks;
+    p.per_segment = (int)per;
+    p.nsegments = (int)(p.segmented ? segments(per) : seq.S);
+    return p;
+}
+
+int scan_group_bytes(bool bf16, int N, bool backward) {
+    int bytes = 0;
+    (void)with_kind(bf16, N, [&](auto b, auto n) {
+        using Block = GroupBlock<n.value, b.value ? 1 : 3>;
+        bytes = backward ? Block::backward : Block::forward;
+        return hipSuccess;
+    });
+    return bytes;
+}
+
+// The workspace's parts that the forward and the backward pass share, for every number of tokens and sequences up to the
+// given ones: bounds of each part, none of which falls as a size grows.
+size_t scan_workspace(ScanArgs& a, SweepArgs& s, uint8_t* ws, int64_t T, int64_t S, int64_t H, int64_t G, int N, int group_bytes) {
+    size_t at = 0;
+    auto take = [&](int64_t bytes) {
+        uint8_t* const p = ws + at;
+        at += (size_t)(bytes + 255) / 256 * 256;
+        return p;
+    };
+    const int64_t chunks = T / kChunk + S;
+    a.chunks = reinterpret_cast<int4*>(take(chunks * 16));
+    a.segments = reinterpret_cast<int4*>(take((chunks + S) * 16));
+    a.first_segment = reinterpret_cast<int*>(take((S + 1) * 8));
+    a.groups = take(chunks * G * group_bytes);
+    a.heads = reinterpret_cast<float*>(take(chunks * H * kHeadArrays * kChunk * 4));
+    s.segment_states = reinterpret_cast<float*>(take(kMaxSegmentHeads * kP * N * 4));
+    s.segment_decay = reinterpret_cast<float*>(take(kMaxSegmentHeads * 4));
+    return at;
+}
+
+size_t mamba2_scan_workspace_bytes(int64_t T, int64_t S, int64_t H, int64_t N, int64_t G) {
+    ScanArgs a{};
+    SweepArgs s{};
+    return scan_workspace(a, s, nullptr, T, S, H, G, (int)N, scan_group_bytes(false, (int)N, false));
+}
+
+hipError_t launch_mamba2_scan(ScanArgs a, bool bf16, int N, const float* state_in, float* state_out, void* y, int64_t ldy,
+                              void* workspace, hipStream_t stream) {
+    SweepArgs s{};
+    s.v = a.x;
+    s.ldv = a.ldx;
+    s.start = state_in;
+    s.end = state_out;
+    s.y = y;
+    s.ldy = ldy;
+    if (scan_recurrent(a.seq)) {
+        s.a = a;
+        return with_kind(bf16, N, [&](auto b, auto n) {
+            recurrent_kernel<b.value, n.value><<<dim3((unsigned)(a.H * 4), (unsigned)a.seq.S), 256, 0, stream>>>(s);
+            return hipGetLastError();
+        });
+    }
+    const ScanPlan plan = scan_plan(a.seq, a.H, a.G);
+    s.group_bytes = scan_group_bytes(bf16, N, false);
+    scan_workspace(a, s, static_cast<uint8_t*>(workspace), a.seq.T, a.seq.S, a.H, a.G, N, s.group_bytes);
+    if (!a.seq.cu) a.chunks = a.segments = nullptr;
+    if (!plan.segmented) s.segment_states = nullptr;
+    a.nchunks = plan.nchunks;
+    a.nsegments = plan.nsegments;
+    a.per_segment = plan.per_segment;
+    s.a = a;
+    (void)with_kind(bf16, N, [&](auto b, auto n) {
+        s.key = GroupBlock<n.value, b.value ? 1 : 3>::kAcross;
+        return hipSuccess;
+    });
+    if (hipError_t err = launch_scan_prepare(a, bf16, N, false, stream)) return err;
+    return launch_sweep(s, plan, bf16, N, kOutput, stream);
+}
+
+}  // namespace dfssm

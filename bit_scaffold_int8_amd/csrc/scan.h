@@ -1,0 +1,146 @@
+// scan.h -- what the Mamba-2 scan and its gradients share (gfx950), private to the library: how sequences are cut
+// into chunks and segments, the layouts of the workspace, and matrix products of fp32 values on the bf16 matrix cores.
+//
+// Products: the 16x16x32 bf16 instruction takes, from lane (r = lane % 16, q = lane / 16), eight values of row
+// (or column) r.  Which of the 32 summed places they are is free as long as both operands agree; here
+//   place(q, j) = 4 q + j % 4 + 16 (j / 4)
+// Its result holds column r, rows 4 q + v: so two results stacked by rows are an operand of the next product as
+// they stand, and an operand's values lie in two groups of four neighbours.
+//
+// An fp32 value enters as bf16 pieces x = p0 + p1 + p2 (each the rounding of what is left; after three the rest is below
+// 2^-24 of x), and a product of two such takes the six products of pieces down to 2^-16: what it leaves out is of
+// the size of fp32's own rounding.  A bf16 value is its own only piece.  Against the fp32 matrix
+// instructions (1/16 of the rate) that is 2.7 times the rate for fp32 data and 5.3 times or more for bf16 data.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <type_traits>
+
+#include "sequences.h"
+
+namespace dfssm {
+
+typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
+typedef __bf16 v4bf __attribute__((ext_vector_type(4)));
+
+constexpr int kChunk = 64;     // tokens of a chunk
+constexpr int kP = 64;         // channels of a head
+constexpr int kHeadArrays = 5; // per chunk and head, 64 values each:
+enum { kCsHi, kCsLo, kStep, kWeight, kDecay };
+//   cs = log2 of the decay from the chunk's start through token t, as hi + lo (summed in fp64: differences of
+//   close ones keep fp32's precision however far the sum has come);  step = dt;  weight = dt 2^(cs_end - cs);  decay = 2^cs
+
+struct ScanArgs {
+    Sequences seq;
+    int H, G;
+    const void *x, *B, *C;
+    const float* dt;
+    int64_t ldx, lddt, ldb, ldc;
+    const float *A_log, *D, *dt_bias;
+    // workspace
+    int4* chunks;     // [chunk]: first row, rows, sequence (-1: no such chunk), -
+    int4* segments;   // [segment]: first chunk, chunks, sequence (-1: none), number within the sequence
+    int* first_segment;  // [S + 1]
+    int nchunks, nsegments, per_segment;  // bounds of the numbers, chunks of a segment
+    uint8_t* groups;  // [chunk][G] blocks of group_bytes
+    float* heads;     // [chunk][H][kHeadArrays][kChunk]
+};
+
+// A group's block for one chunk: products C_t . B_s (fp32, results of 16 x 16), then three sets of pieces, each
+// [piece][16-row tile][32-place step][lane][8]:
+//   rows   rows of C (forward) or of B (backward) along the state
+//   across  B, across the tokens (rows of it: state places)
+//   cross   C, across the tokens (backward)
+template <int kN, int kPieces>
+struct GroupBlock {
+    static constexpr int kG = kChunk * kChunk * 4, kPlane = kChunk * kN * 2, kSet = kPieces * kPlane;
+    static constexpr int kRows = kG, kAcross = kRows + kSet, kCross = kAcross + kSet;
+    static constexpr int forward = kCross, backward = kCross + kSet;
+};
+
+template <int kPieces>
+struct Pieces {
+    v8bf p[kPieces];
+};
+
+template <int kPieces>
+__device__ __forceinline__ Pieces<kPieces> split(const float (&x)[8]) {
+    Pieces<kPieces> out;
+    float r[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) r[j] = x[j];
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const __bf16 b = (__bf16)r[j];
+            out.p[i][j] = b;
+            if (i + 1 < kPieces) r[j] -= (float)b;
+        }
+    return out;
+}
+
+// acc += a b: the products of pieces whose numbers add up to at most 2, the small ones first.
+template <int kA, int kB>
+__device__ __forceinline__ v4f mma(const Pieces<kA>& a, const Pieces<kB>& b, v4f acc) {
+#pragma unroll
+    for (int sum = 2; sum >= 0; --sum)
+#pragma unroll
+        for (int i = 0; i < kA; ++i)
+            if (sum - i >= 0 && sum - i < kB)
+                acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.p[i], b.p[sum - i], acc, 0, 0, 0);
+    return acc;
+}
+
+// Pieces stored [piece][...][lane][8]; `plane` bytes from piece to piece.
+template <int kPieces>
+__device__ __forceinline__ Pieces<kPieces> load_pieces(const uint8_t* at, int plane) {
+    Pieces<kPieces> out;
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) out.p[i] = *reinterpret_cast<const v8bf*>(at + i * plane);
+    return out;
+}
+template <int kPieces>
+__device__ __forceinline__ void store_pieces(uint8_t* at, int plane, const Pieces<kPieces>& v) {
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) *reinterpret_cast<v8bf*>(at + i * plane) = v.p[i];
+}
+
+__device__ __forceinline__ int place(int q, int j) { return 4 * q + (j & 3) + 16 * (j >> 2); }
+
+// softplus with the identity above 20, as the decode step has it
+__device__ __forceinline__ float scan_softplus(float v) { return v > 20.0f ? v : log1pf(expf(v)); }
+
+// The gradient's own side of the launches.
+struct ScanPlan {
+    int nchunks, nsegments, per_segment;
+    bool segmented;   // some sequence may have more than one segment
+};
+
+hipError_t launch_scan_prepare(const ScanArgs& a, bool bf16, int N, bool backward, hipStream_t stream);
+
+// One sweep over the chunks of every segment with the state in registers:
+//   state <- 2^cs_end state + sum_t weight_t v_t k_t^T
+// kLocal keeps what a segment adds to a state of zero, and its decay; kStarts stores the state at the start of each
+// chunk; kOutput computes y.  Backwards (reverse) v is dy, k is C, and the weight is the decay from the chunk's start.
+enum SweepMode { kLocal, kStarts, kOutput };
+struct SweepArgs {
+    ScanArgs a;
+    const void* v;       // x, or dy
+    int64_t ldv;
+    int key;             // offset of the key's set in a group's block
+    int group_bytes;
+    bool reverse;
+    const float* start;  // [S][H][64][N]: the caller's states, or NULL: zeros
+    float* end;          // the same, or NULL
+    float* segment_states;  // [segment][H][64][N] in the registers' order, when the sequences are segmented; or NULL
+    float* segment_decay;   // [segment][H]
+    float* starts;       // [chunk][H][64][N]   (kStarts)
+    void* y;             // (kOutput)
+    int64_t ldy;
+};
+hipError_t launch_sweep(const SweepArgs& s, const ScanPlan& plan, bool bf16, int N, SweepMode mode, hipStream_t stream);
+
+}  // namespace dfssm

@@ -1,0 +1,71 @@
+// sequences.h -- packed sequences for the Mamba-2 operators over many tokens (gfx950), private to the library.
+//
+// S sequences lie one after another in T rows: sequence s in rows [cu[s], cu[s + 1]), or, without
+// offsets, S sequences of T / S rows each.  Offsets live in device memory, so the host cannot check them; every reader
+// cuts them to [0, T], which keeps bad ones inside the buffers (what they compute is then unspecified).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "device_common.h"
+
+namespace dfssm {
+
+struct Sequences {
+    const int32_t* cu;  // [S + 1], or NULL
+    int T, S, L;        // L: the common length without offsets
+};
+
+struct Span {
+    int begin, end;
+};
+
+__device__ __forceinline__ Span span_of(const Sequences& q, int s) {
+    if (!q.cu) return {s * q.L, (s + 1) * q.L};
+    int b = q.cu[s], e = q.cu[s + 1];
+    b = b < 0 ? 0 : b > q.T ? q.T : b;
+    e = e < b ? b : e > q.T ? q.T : e;
+    return {b, e};
+}
+
+// The last sequence that starts at row t or before it (rows before the first one: sequence 0, whose span excludes them).
+__device__ __forceinline__ int sequence_at(const Sequences& q, int t) {
+    if (!q.cu) return t / q.L;
+    int lo = 0, hi = q.S - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (q.cu[mid] <= t) lo = mid;
+        else hi = mid - 1;
+    }
+    return lo;
+}
+
+// Elements of either type as fp32, one or four at a time.
+template <bool kBf16>
+struct Elem;
+template <>
+struct Elem<false> {
+    using type = float;
+    static __device__ __forceinline__ float load(const float* p) { return *p; }
+    static __device__ __forceinline__ v4f load4(const float* p) { return *reinterpret_cast<const v4f*>(p); }
+    static __device__ __forceinline__ void store(float* p, float v) { *p = v; }
+    static __device__ __forceinline__ void store4(float* p, v4f v) { *reinterpret_cast<v4f*>(p) = v; }
+};
+template <>
+struct Elem<true> {
+    using type = uint16_t;
+    static __device__ __forceinline__ float load(const uint16_t* p) { return __uint_as_float((uint32_t)*p << 16); }
+    static __device__ __forceinline__ v4f load4(const uint16_t* p) {
+        const uint2 v = *reinterpret_cast<const uint2*>(p);
+        return {__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xFFFF0000u), __uint_as_float(v.y << 16),
+                __uint_as_float(v.y & 0xFFFF0000u)};
+    }
+    static __device__ __forceinline__ void store(uint16_t* p, float v) { *p = (uint16_t)bf16_bits(v); }
+    static __device__ __forceinline__ void store4(uint16_t* p, v4f v) {
+        *reinterpret_cast<uint2*>(p) =
+            make_uint2(bf16_bits(v.x) | (bf16_bits(v.y) << 16), bf16_bits(v.z) | (bf16_bits(v.w) << 16));
+    }
+};
+
+}  // namespace dfssm

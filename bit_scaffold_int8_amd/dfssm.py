@@ -30,7 +30,9 @@ EXPORTED = ("dfssm_status_string", "dfssm_version", "dfssm_quantize_act", "dfssm
             "dfssm_density_field_decode", "dfssm_density_field_requantize", "dfssm_int8_gemm",
             "dfssm_cross_entropy_workspace_bytes", "dfssm_cross_entropy",
             "dfssm_cross_entropy_backward_workspace_bytes", "dfssm_cross_entropy_backward",
-            "dfssm_embedding_lookup_scaled", "dfssm_embedding_backward_workspace_bytes", "dfssm_embedding_backward")
+            "dfssm_embedding_lookup_scaled", "dfssm_embedding_backward_workspace_bytes", "dfssm_embedding_backward",
+            "dfssm_mamba2_conv", "dfssm_mamba2_conv_backward_workspace_bytes", "dfssm_mamba2_conv_backward",
+            "dfssm_mamba2_scan_workspace_bytes", "dfssm_mamba2_scan")
 
 # dfssm_type: the element type of a result or a gradient
 DFSSM_F32 = 0
@@ -48,6 +50,16 @@ DECODE_WEIGHT_FIELDS = ("in_w_bits", "in_s_w", "in_w_a", "in_s_a", "in_w_b", "in
 
 class DecodeLayerWeights(ctypes.Structure):
     _fields_ = [(name, ctypes.c_void_p) for name in DECODE_WEIGHT_FIELDS]
+
+
+# dfssm_mamba2_scan_operands: pointers, then sizes, then the type
+SCAN_POINTERS = ("x", "B", "C", "dt", "A_log", "D", "dt_bias", "state_in", "cu_seqlens")
+SCAN_SIZES = ("ldx", "ldb", "ldc", "lddt", "T", "S", "nheads", "headdim", "d_state", "ngroups")
+
+
+class ScanOperands(ctypes.Structure):
+    _fields_ = ([(name, ctypes.c_void_p) for name in SCAN_POINTERS] + [(name, ctypes.c_int64) for name in SCAN_SIZES]
+                + [("type", ctypes.c_int32)])
 
 
 class DfssmError(RuntimeError):
@@ -108,10 +120,16 @@ def _load():
         "dfssm_embedding_lookup_scaled": [P, i64, P, P, i64, i64, ctypes.c_float, P, i64, i32, P],
         "dfssm_embedding_backward": [P, i64, P, i64, i32, i64, i64, ctypes.c_float, P, i32, i32, P, ctypes.c_size_t,
                                      P],
+        "dfssm_mamba2_conv": [P, i64, i32, i64, i64, i64, P, P, P, P, P, P, i64, i32, P],
+        "dfssm_mamba2_conv_backward": [P, i64, i32, i64, i64, i64, P, P, P, P, P, i64, i32, P, P, i64, P, P, P, P,
+                                       ctypes.c_size_t, P],
+        "dfssm_mamba2_scan": [P, P, i64, P, P, ctypes.c_size_t, P],
     }
     for name, argtypes in (("dfssm_cross_entropy_workspace_bytes", [i64, i64, i64]),
                            ("dfssm_cross_entropy_backward_workspace_bytes", [i64, i64, i64, i32, i32, i32]),
-                           ("dfssm_embedding_backward_workspace_bytes", [i64, i64, i64])):
+                           ("dfssm_embedding_backward_workspace_bytes", [i64, i64, i64]),
+                           ("dfssm_mamba2_conv_backward_workspace_bytes", [i64, i64, i64]),
+                           ("dfssm_mamba2_scan_workspace_bytes", [i64] * 6)):
         getattr(lib, name).argtypes = argtypes
         getattr(lib, name).restype = ctypes.c_size_t
     for name, argtypes in sigs.items():
@@ -525,3 +543,132 @@ def dfssm_embedding_backward(tokens, dout, scale, de, workspace, accumulate: boo
     _run_on("dfssm_embedding_backward", (tokens, dout, de, workspace), stream, tokens.data_ptr(), T, dout.data_ptr(),
             ldd, _type("dout", dout), V, K, float(scale), de.data_ptr(), _type("de", de), int(bool(accumulate)),
             workspace.data_ptr(), _bytes(workspace))
+
+
+# ---- the Mamba-2 operators over packed sequences.  cu_seqlens: int32 offsets [S + 1] on the same device, or None for
+# sequences of equal length (their number is that of the states or windows, or `sequences`).
+
+def _sequences(name, T, cu_seqlens, states, sequences) -> int:
+    """The number of sequences, agreed on by everything that tells it."""
+    import torch
+    told = [t.shape[0] for t in states if t is not None]
+    if cu_seqlens is not None:
+        if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
+            raise ValueError(f"{name}: cu_seqlens: S + 1 offsets expected, got shape {tuple(cu_seqlens.shape)}")
+        _dense("cu_seqlens", cu_seqlens, cu_seqlens.shape, torch.int32)
+        told.append(cu_seqlens.numel() - 1)
+    if sequences is not None:
+        told.append(int(sequences))
+    S = told[0] if told else 1
+    if any(n != S for n in told):
+        raise ValueError(f"{name}: the numbers of sequences differ: {told}")
+    if cu_seqlens is None and (S <= 0 or T % S != 0):
+        raise ValueError(f"{name}: {T} rows are not {S} sequences of equal length")
+    return S
+
+
+def _optional(what, t, shape):
+    import torch
+    if t is not None:
+        _dense(what, t, shape, torch.float32)
+
+
+def _present(*tensors):
+    return [t for t in tensors if t is not None]
+
+
+def _conv_operands(name, xbc, conv_w, conv_b, windows, cu_seqlens, sequences) -> tuple:
+    import torch
+    T, ch = _matrix("xbc", xbc)
+    ldx = _rows("xbc", xbc, (T, ch))
+    _dense("conv_w", conv_w, (ch, 4), torch.float32)
+    _dense("conv_b", conv_b, (ch,), torch.float32)
+    S = _sequences(name, T, cu_seqlens, windows.values(), sequences)
+    for what, t in windows.items():
+        _optional(what, t, (S, ch, 4))
+    return ldx, _type("xbc", xbc), T, S, ch
+
+
+def dfssm_mamba2_conv(xbc, conv_w, conv_b, window_in, window_out, out, cu_seqlens=None, sequences=None, stream=None) -> None:
+    """out [T, ch] = silu of the causal convolution of xbc [T, ch] (each fp32 or bf16, rows may be strided) with
+    conv_w [ch, 4], conv_b [ch]; window_in / window_out fp32 [S, ch, 4] or None (zeros / not wanted)."""
+    ldx, tx, T, S, ch = _conv_operands("dfssm_mamba2_conv", xbc, conv_w, conv_b,
+                                       {"window_in": window_in, "window_out": window_out}, cu_seqlens, sequences)
+    ldo = _rows("out", out, (T, ch))
+    _run_on("dfssm_mamba2_conv", _present(xbc, conv_w, conv_b, out, window_in, window_out, cu_seqlens), stream,
+            xbc.data_ptr(), ldx, tx, T, S, ch, _ptr(cu_seqlens), conv_w.data_ptr(), conv_b.data_ptr(), _ptr(window_in),
+            _ptr(window_out), out.data_ptr(), ldo, _type("out", out))
+
+
+def dfssm_mamba2_conv_backward_workspace_bytes(T: int, S: int, ch: int) -> int:
+    return int(lib.dfssm_mamba2_conv_backward_workspace_bytes(T, S, ch))
+
+
+def dfssm_mamba2_conv_backward(xbc, conv_w, conv_b, window_in, dout, dwindow_out, dxbc, dconv_w, dconv_b, dwindow_in,
+                               workspace, cu_seqlens=None, sequences=None, stream=None) -> None:
+    """dxbc [T, ch] (xbc's type), dconv_w, dconv_b (both None: frozen) and dwindow_in (or None) from the forward call's
+    operands, dout [T, ch] and dwindow_out (or None: zeros); workspace: a tensor of
+    dfssm_mamba2_conv_backward_workspace_bytes(T, S, ch) bytes, or None with frozen weights."""
+    windows = {"window_in": window_in, "dwindow_out": dwindow_out, "dwindow_in": dwindow_in}
+    ldx, tx, T, S, ch = _conv_operands("dfssm_mamba2_conv_backward", xbc, conv_w, conv_b, windows, cu_seqlens, sequences)
+    ldd, lddx = _rows("dout", dout, (T, ch)), _rows("dxbc", dxbc, (T, ch), xbc.dtype)
+    _optional("dconv_w", dconv_w, (ch, 4))
+    _optional("dconv_b", dconv_b, (ch,))
+    _run_on("dfssm_mamba2_conv_backward",
+            _present(xbc, conv_w, conv_b, dout, dxbc, *windows.values(), dconv_w, dconv_b, workspace, cu_seqlens), stream,
+            xbc.data_ptr(), ldx, tx, T, S, ch, _ptr(cu_seqlens), conv_w.data_ptr(), conv_b.data_ptr(), _ptr(window_in),
+            dout.data_ptr(), ldd, _type("dout", dout), _ptr(dwindow_out), dxbc.data_ptr(), lddx, _ptr(dconv_w),
+            _ptr(dconv_b), _ptr(dwindow_in), _ptr(workspace), 0 if workspace is None else _bytes(workspace))
+
+
+def _heads(what, t, T, dtype) -> tuple:
+    """Checks rows of parts [T, A, B] whose parts lie side by side; (stride of a row, A, B)."""
+    if t.dim() != 3 or t.shape[0] != T:
+        raise ValueError(f"{what}: shape ({T}, ., .) expected, got {tuple(t.shape)}")
+    if t.dtype is not dtype:
+        raise ValueError(f"{what}: {dtype} expected, got {t.dtype}")
+    _, A, B = t.shape
+    st, sa, sb = t.stride()
+    if (sb != 1 and B > 1) or (sa != B and A > 1) or (st < A * B and T > 1):
+        raise ValueError(f"{what}: rows must be contiguous and must not overlap, got strides {t.stride()}")
+    return (st if T > 1 else A * B), A, B
+
+
+def _scan_operands(name, x, dt, B, C, A_log, D, dt_bias, state_in, states, cu_seqlens, sequences):
+    """Checks the scan's operands; (dfssm_mamba2_scan_operands, its tensors, the states' shape)."""
+    import torch
+    T = x.shape[0]
+    ldx, H, P = _heads("x", x, T, x.dtype)
+    ldb, G, N = _heads("B", B, T, x.dtype)
+    ldc, *same = _heads("C", C, T, x.dtype)
+    if same != [G, N]:
+        raise ValueError(f"C: shape {tuple(B.shape)} expected, got {tuple(C.shape)}")
+    lddt = _rows("dt", dt, (T, H), torch.float32)
+    for what, t in (("A_log", A_log), ("D", D), ("dt_bias", dt_bias)):
+        _dense(what, t, (H,), torch.float32)
+    S = _sequences(name, T, cu_seqlens, (state_in, *states.values()), sequences)
+    for what, t in (("state_in", state_in), *states.items()):
+        _optional(what, t, (S, H, P, N))
+    op = ScanOperands(x.data_ptr(), B.data_ptr(), C.data_ptr(), dt.data_ptr(), A_log.data_ptr(), D.data_ptr(),
+                      dt_bias.data_ptr(), _ptr(state_in), _ptr(cu_seqlens), ldx, ldb, ldc, lddt, T, S, H, P, N, G,
+                      _type("x", x))
+    return op, _present(x, dt, B, C, A_log, D, dt_bias, state_in, cu_seqlens, *states.values())
+
+
+def dfssm_mamba2_scan_workspace_bytes(T: int, S: int, nheads: int, headdim: int, d_state: int, ngroups: int = 1) -> int:
+    return int(lib.dfssm_mamba2_scan_workspace_bytes(T, S, nheads, headdim, d_state, ngroups))
+
+
+def dfssm_mamba2_scan(x, dt, B, C, A_log, D, dt_bias, state_in, state_out, y, workspace, cu_seqlens=None, sequences=None,
+                      stream=None) -> None:
+    """y [T, H, 64] and state_out of the scan over x [T, H, 64], dt fp32 [T, H] (raw), B, C [T, G, N], A_log, D,
+    dt_bias [H] (x, B, C, y all fp32 or all bf16, rows may be strided); state_in / state_out fp32 [S, H, 64, N] or None
+    (zeros / not wanted), the same tensor for an update in place; workspace: a tensor of
+    dfssm_mamba2_scan_workspace_bytes(T, S, H, 64, N, G) bytes."""
+    op, tensors = _scan_operands("dfssm_mamba2_scan", x, dt, B, C, A_log, D, dt_bias, state_in, {"state_out": state_out},
+                                 cu_seqlens, sequences)
+    ldy, *same = _heads("y", y, op.T, x.dtype)
+    if same != [op.nheads, op.headdim]:
+        raise ValueError(f"y: shape {tuple(x.shape)} expected, got {tuple(y.shape)}")
+    _run_on("dfssm_mamba2_scan", [*tensors, y, workspace], stream, ctypes.addressof(op), y.data_ptr(), ldy,
+            _ptr(state_out), workspace.data_ptr(), _bytes(workspace))

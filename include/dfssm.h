@@ -564,6 +564,99 @@ dfssm_status dfssm_embedding_backward(const int32_t* tokens, int64_t T, const vo
                                       int32_t de_type, int32_t accumulate, void* workspace, size_t workspace_bytes,
                                       hipStream_t stream);
 
+/*
+ * The causal convolution in front of the Mamba-2 scan, for the tokens of S packed sequences (the many-token form of
+ * the decode step's shift register; technical summary, section 2C, Stateful Ops):
+ *   u = the sequence's window, oldest first, then its rows;   pre[t][c] = conv_b[c] + sum_j conv_w[c][j] u[t - 3 + j][c]
+ *   out[t][c] = silu(pre[t][c]) = pre / (1 + exp(-pre))
+ * Sequences: with cu_seqlens (int32 [S + 1] in device memory) sequence s is the rows cu_seqlens[s] up to
+ * cu_seqlens[s + 1], which may be none; rows outside every sequence are neither read nor written.  With NULL all S
+ * have T / S rows.  Offsets must not fall and must lie in [0, T]; the host cannot check that, and what others
+ * give is unspecified (but stays inside the buffers).
+ *   xbc  in_type [T][ch], row t at element t*ldx (a part of in_proj's row)   out  out_type [T][ch], rows ldo apart, written
+ *   conv_w fp32 [ch][4] (16-byte aligned), conv_b fp32 [ch]
+ *   window_in   fp32 [S][ch][4] (16-byte aligned), or NULL for zeros: the layout of dfssm_mamba2_decode_step
+ *   window_out  fp32 [S][ch][4] (16-byte aligned; must not overlap window_in), or NULL: each sequence's last four inputs
+ * Rows whose start and stride are multiples of four elements, with ch % 4 == 0, are fastest.  No output may overlap an input.
+ * Non-finite inputs reach only the outputs whose sums they enter.  One kernel launch.
+ * Errors: DFSSM_ERR_INVALID_ARG for a NULL or misaligned pointer, sizes <= 0 or >= 2^31, T % S != 0 without
+ * offsets, a stride < ch, a type that is none, overlapping windows; DFSSM_ERR_UNSUPPORTED for T > 2^20, S > 65535,
+ * ch > 2^20 or a stride >= 2^31.
+ */
+dfssm_status dfssm_mamba2_conv(const void* xbc, int64_t ldx, int32_t in_type, int64_t T, int64_t S, int64_t ch,
+                               const int32_t* cu_seqlens, const float* conv_w, const float* conv_b,
+                               const float* window_in, float* window_out, void* out, int64_t ldo, int32_t out_type,
+                               hipStream_t stream);
+
+/*
+ * Gradients of dfssm_mamba2_conv (with sig = 1 / (1 + exp(-pre)), pre formed again):
+ *   dpre = dout sig (1 + pre (1 - sig));   dxbc[t][c] = sum_j conv_w[c][j] dpre[t + 3 - j][c]  (+ dwindow_out of the last four)
+ *   dconv_w[c][j] = sum_t dpre[t][c] u[t - 3 + j][c];   dconv_b[c] = sum_t dpre[t][c];   dwindow_in: the window's part of u
+ *   dout  out_type [T][ch] (read), rows ldd apart;   dxbc  in_type [T][ch] (written), rows lddx apart
+ *   dwindow_out  fp32 [S][ch][4], or NULL for zeros;   dwindow_in  the same, written, or NULL (16-byte aligned, not overlapping)
+ *   dconv_w fp32 [ch][4] (16-byte aligned) and dconv_b fp32 [ch], written, or both NULL (frozen)
+ *   workspace  at least dfssm_mamba2_conv_backward_workspace_bytes(T, S, ch) bytes, 16-byte aligned, under
+ *              dfssm_cross_entropy's rules; may be NULL (0 bytes) with frozen weights
+ * Sums run in fp32 in a fixed order.  At most two kernel launches.  Errors as the forward call's, and
+ * DFSSM_ERR_INVALID_ARG for a short workspace or one of dconv_w and dconv_b without the other.
+ */
+size_t dfssm_mamba2_conv_backward_workspace_bytes(int64_t T, int64_t S, int64_t ch);
+dfssm_status dfssm_mamba2_conv_backward(const void* xbc, int64_t ldx, int32_t in_type, int64_t T, int64_t S, int64_t ch,
+                                        const int32_t* cu_seqlens, const float* conv_w, const float* conv_b,
+                                        const float* window_in, const void* dout, int64_t ldd, int32_t out_type,
+                                        const float* dwindow_out, void* dxbc, int64_t lddx, float* dconv_w,
+                                        float* dconv_b, float* dwindow_in, void* workspace, size_t workspace_bytes,
+                                        hipStream_t stream);
+
+/*
+ * The Mamba-2 scan over the tokens of S packed sequences: a linear attention whose state decays by a factor for each
+ * head and token (the recurrence of dfssm_mamba2_decode_step; its published chunked form for many tokens):
+ *   dt = softplus(dt_raw + dt_bias[h]) (identity above 20)
+ *   state[h] <- exp(-dt exp(A_log[h])) state[h] + dt x[t][h] B[t][g]^T
+ *   y[t][h] = state[h] C[t][g] + D[h] x[t][h],   g = h / (nheads / ngroups)
+ *   x   type [T][nheads][64], row t at element t*ldx      B, C  type [T][ngroups][d_state], rows ldb and ldc apart
+ *   dt  fp32 [T][nheads] (raw, as in in_proj's row), rows lddt apart;   A_log, D, dt_bias  fp32 [nheads]
+ *   state_in  fp32 [S][nheads][64][d_state], or NULL for zeros: the layout of dfssm_mamba2_decode_step
+ *   cu_seqlens, T, S: as in dfssm_mamba2_conv; rows outside every sequence are left alone
+ * x, B, C and y start at multiples of 16 bytes and have strides that are multiples of 16 bytes; the states are 16-byte aligned.
+ * Non-finite values and sizes are not checked: rows behind a sequence may hold anything, others must be finite.
+ */
+typedef struct dfssm_mamba2_scan_operands {
+    const void* x;
+    const void* B;
+    const void* C;
+    const float* dt;
+    const float* A_log;
+    const float* D;
+    const float* dt_bias;
+    const float* state_in;
+    const int32_t* cu_seqlens;
+    int64_t ldx, ldb, ldc, lddt;
+    int64_t T, S, nheads, headdim, d_state, ngroups;
+    int32_t type;
+} dfssm_mamba2_scan_operands;
+
+/*
+ *   y          type [T][nheads][64], rows ldy apart, written
+ *   state_out  fp32 [S][nheads][64][d_state], written, or NULL; may be state_in itself (the update in place)
+ *   workspace  at least dfssm_mamba2_scan_workspace_bytes(T, S, nheads, headdim, d_state, ngroups) bytes, 16-byte
+ *              aligned, under dfssm_cross_entropy's rules
+ * Sequences of at most 8 tokens on average go token by token through the recurrence in fp32 (one launch, the workspace
+ * unused); longer ones by chunks of 64 tokens on the matrix cores.  There fp32 operands and the state are taken in
+ * three bf16 pieces (relative error 2^-24 of each), and where y is bf16 the state's and the chunk's weights enter y in two
+ * (2^-17); the state itself is fp32 and formed from three pieces for either type.  A chunk's decays are
+ * differences of sums in fp64.  Sums run in a fixed order: equal inputs give equal bits.
+ * Errors: DFSSM_ERR_INVALID_ARG for a NULL or misaligned pointer, sizes <= 0 or >= 2^31, nheads % ngroups != 0, T % S != 0
+ * without offsets, strides shorter than a row, a type that is none, a short workspace;
+ * DFSSM_ERR_UNSUPPORTED unless headdim == 64, d_state == 64 or 128, nheads <= 1024, T <= 2^20, S <= 65535, S * nheads <= 2^21,
+ * (T / 64 + S) * (nheads + 4 ngroups) <= 2^25 and strides < 2^31.  The size query returns 0 for sizes that the
+ * call refuses, and never falls as one grows.
+ */
+size_t dfssm_mamba2_scan_workspace_bytes(int64_t T, int64_t S, int64_t nheads, int64_t headdim, int64_t d_state,
+                                         int64_t ngroups);
+dfssm_status dfssm_mamba2_scan(const dfssm_mamba2_scan_operands* op, void* y, int64_t ldy, float* state_out,
+                               void* workspace, size_t workspace_bytes, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -90,6 +90,16 @@ hipError_t launch_mamba2_conv_backward(const Sequences& seq, const void* u, int6
 size_t mamba2_scan_workspace_bytes(int64_t T, int64_t S, int64_t H, int64_t N, int64_t G);
 hipError_t launch_mamba2_scan(ScanArgs a, bool bf16, int N, const float* state_in, float* state_out, void* y, int64_t ldy,
                               void* workspace, hipStream_t stream);
+int64_t distillation_max_top();
+hipError_t launch_distillation(const int8_t* x_q, const float* s_x, int64_t M, int64_t V, int64_t K, const int8_t* e,
+                               const float* s_e, const int32_t* ids, const float* top, int64_t k, float temperature,
+                               float* loss, float* lse, float* logp, void* workspace, hipStream_t stream);
+size_t distillation_backward_workspace_bytes(int64_t M, int64_t V, int64_t K, int64_t k, bool bf16, bool want_dx, bool want_de);
+hipError_t launch_distillation_backward(const int8_t* x_q, const float* s_x, int64_t M, int64_t V, int64_t K,
+                                        const int8_t* e, const float* s_e, const int32_t* ids, const float* top, int64_t k,
+                                        float temperature, const float* lse, const float* logp, const float* dloss,
+                                        void* dx, void* de, bool bf16, bool accumulate, void* workspace,
+                                        hipStream_t stream);
 }  // namespace dfssm
 
 #include "decode_args.h"
@@ -318,6 +328,7 @@ constexpr int64_t kMaxBlocks = (int64_t)1 << 30;       // 32 x 32 blocks of one 
 // (a launch holds fewer than 2^32 threads)
 constexpr int64_t kMaxLossTokens = (int64_t)1 << 25, kMaxLossRows = (int64_t)1 << 28;  // of one forward call
 constexpr int64_t kMaxLossLogits = (int64_t)1 << 38;
+constexpr int64_t kMaxTeacherEntries = (int64_t)1 << 28;  // (eight of them take a wave)
 constexpr int64_t kMaxLossGradTokens = (int64_t)1 << 18;  // of one backward call
 constexpr int64_t kMaxGradTokens = (int64_t)1 << 24, kMaxGradRows = (int64_t)1 << 28;  // of one embedding gradient
 
@@ -330,6 +341,14 @@ dfssm_status loss_sizes(int64_t M, int64_t V, int64_t K) {
     if (K > kMaxK || M > kMaxLossTokens || V > kMaxLossRows || M * V > kMaxLossLogits) return DFSSM_ERR_UNSUPPORTED;
     return DFSSM_OK;
 }
+
+dfssm_status distillation_sizes(int64_t M, int64_t V, int64_t K, int64_t top) {
+    if (top <= 0) return DFSSM_ERR_INVALID_ARG;
+    if (dfssm_status st = loss_sizes(M, V, K)) return st;
+    return top > dfssm::distillation_max_top() || M * top > kMaxTeacherEntries ? DFSSM_ERR_UNSUPPORTED : DFSSM_OK;
+}
+
+bool temperature_ok(float t) { return t >= 0x1p-60f && t <= 0x1p60f; }
 
 dfssm_status embedding_sizes(int64_t T, int64_t V, int64_t K) {
     if (T <= 0 || V <= 0 || K <= 0 || T >= kMaxRows || V >= kMaxRows) return DFSSM_ERR_INVALID_ARG;
@@ -701,6 +720,58 @@ dfssm_status dfssm_cross_entropy_backward(const int8_t* x_q, const float* s_x, i
         return DFSSM_ERR_INVALID_ARG;
     return dfssm::launch_cross_entropy_backward(x_q, s_x, M, V, K, e, s_e, targets, lse, dloss, dx, de, bf16,
                                                 accumulate_de != 0, workspace, stream) == hipSuccess
+               ? DFSSM_OK
+               : DFSSM_ERR_HIP;
+}
+
+size_t dfssm_distillation_workspace_bytes(int64_t M, int64_t V, int64_t K, int64_t top) {
+    return distillation_sizes(M, V, K, top) == DFSSM_OK ? dfssm::cross_entropy_workspace_bytes(M, V, K) : 0;
+}
+
+dfssm_status dfssm_distillation(const int8_t* x_q, const float* s_x, int64_t M, int64_t V, int64_t K, const int8_t* e,
+                                const float* s_e, const int32_t* top_ids, const float* top_logits, int64_t top,
+                                float temperature, float* loss, float* lse, float* logp, void* workspace,
+                                size_t workspace_bytes, hipStream_t stream) {
+    if (!x_q || !s_x || !e || !s_e || !top_ids || !top_logits || !loss || !lse || !logp || !workspace) return DFSSM_ERR_INVALID_ARG;
+    if (!temperature_ok(temperature)) return DFSSM_ERR_INVALID_ARG;
+    if (!aligned16(x_q) || !aligned16(e) || !aligned16(workspace) || !aligned4(s_x) || !aligned4(s_e) ||
+        !aligned4(top_ids) || !aligned4(top_logits) || !aligned4(loss) || !aligned4(lse) || !aligned4(logp))
+        return DFSSM_ERR_INVALID_ARG;
+    if (dfssm_status st = distillation_sizes(M, V, K, top)) return st;
+    if (workspace_bytes < dfssm::cross_entropy_workspace_bytes(M, V, K)) return DFSSM_ERR_INVALID_ARG;
+    return dfssm::launch_distillation(x_q, s_x, M, V, K, e, s_e, top_ids, top_logits, top, temperature, loss, lse, logp,
+                                      workspace, stream) == hipSuccess
+               ? DFSSM_OK
+               : DFSSM_ERR_HIP;
+}
+
+size_t dfssm_distillation_backward_workspace_bytes(int64_t M, int64_t V, int64_t K, int64_t top, int32_t grad_type,
+                                                   int32_t want_dx, int32_t want_de) {
+    if (distillation_sizes(M, V, K, top) != DFSSM_OK || M > kMaxLossGradTokens || !type_ok(grad_type) || (!want_dx && !want_de))
+        return 0;
+    return dfssm::distillation_backward_workspace_bytes(M, V, K, top, grad_type == DFSSM_BF16, want_dx != 0, want_de != 0);
+}
+
+dfssm_status dfssm_distillation_backward(const int8_t* x_q, const float* s_x, int64_t M, int64_t V, int64_t K,
+                                         const int8_t* e, const float* s_e, const int32_t* top_ids,
+                                         const float* top_logits, int64_t top, float temperature, const float* lse,
+                                         const float* logp, const float* dloss, void* dx, void* de, int32_t grad_type,
+                                         int32_t accumulate_de, void* workspace, size_t workspace_bytes,
+                                         hipStream_t stream) {
+    if (!x_q || !s_x || !e || !s_e || !top_ids || !top_logits || !lse || !logp || !dloss || (!dx && !de) || !workspace)
+        return DFSSM_ERR_INVALID_ARG;
+    if (!type_ok(grad_type) || (accumulate_de != 0 && accumulate_de != 1) || !temperature_ok(temperature)) return DFSSM_ERR_INVALID_ARG;
+    if (!aligned16(x_q) || !aligned16(e) || !aligned16(workspace) || !aligned16(dx) || !aligned16(de) ||
+        !aligned4(s_x) || !aligned4(s_e) || !aligned4(top_ids) || !aligned4(top_logits) || !aligned4(lse) || !aligned4(logp) ||
+        !aligned4(dloss))
+        return DFSSM_ERR_INVALID_ARG;
+    if (dfssm_status st = distillation_sizes(M, V, K, top)) return st;
+    if (M > kMaxLossGradTokens) return DFSSM_ERR_UNSUPPORTED;
+    const bool bf16 = grad_type == DFSSM_BF16;
+    if (workspace_bytes < dfssm::distillation_backward_workspace_bytes(M, V, K, top, bf16, dx != nullptr, de != nullptr))
+        return DFSSM_ERR_INVALID_ARG;
+    return dfssm::launch_distillation_backward(x_q, s_x, M, V, K, e, s_e, top_ids, top_logits, top, temperature, lse, logp, dloss,
+                                               dx, de, bf16, accumulate_de != 0, workspace, stream) == hipSuccess
                ? DFSSM_OK
                : DFSSM_ERR_HIP;
 }

@@ -19,6 +19,15 @@
 // 64 bits), bf16 one (2^-11, an eighth of the final rounding).  Recomputing the logits costs one
 // int8 product; keeping them would cost 4 M V bytes written and read.
 //
+// Distillation from a teacher's largest logits is the same work with another target: a distribution q over the teacher's
+// rows i_1 .. i_k instead of one row, and logits divided by a temperature T.
+//
+//   q = softmax over j of top_j / T,   loss = sum_j q_j (log q_j - log p_{i_j}),   p = softmax over the vocabulary of z / T
+//   d[m][v] = dloss[m] / T (p[v] - sum of q_j with i_j = v)
+//
+// Forward, the rows' logits are formed by themselves (k dot products a token); backward, the gradient tiles
+// write d with no target, and a small kernel then overwrites the k values a token that have one.
+//
 // What bounds it: forward, the int8 products under the power limit (tile_i8.h); backward, 4096 tokens x 50280 rows x
 // 2048 fp32 in 3.3 ms: the products for dx and de 1.28 and 1.34 ms (grad_gemm.h), the gradient tiles 0.67 ms, of which
 // about 0.25 are their 8 bytes a logit (1.6 GB), written in bursts between the products.
@@ -42,6 +51,7 @@ struct LossArgs {
     const int8_t* e;
     const float* s_e;
     float2* part;   // [ntw][M]: a tile's maximum (of z log2 e) and sum of 2^(z log2 e - maximum)
+    float unit = kLog2e;  // log2 e, over the temperature
 };
 
 // ---------------------------------------------------------------- forward
@@ -74,7 +84,7 @@ __global__ __launch_bounds__(C::NT, C::kMinWaves) void loss_tile_kernel(LossArgs
 #pragma unroll
     for (int tb = 0; tb < C::TB && holds; ++tb) {
         const int t = (tw * C::TB + tb) * 32 + l32;
-        const float sx2 = a.s_x[m0 + (t < trows ? t : trows - 1)] * kLog2e;
+        const float sx2 = a.s_x[m0 + (t < trows ? t : trows - 1)] * a.unit;
         float z[C::WB][16], top = neg;
 #pragma unroll
         for (int b = 0; b < C::WB; ++b)
@@ -109,12 +119,10 @@ __global__ __launch_bounds__(C::NT, C::kMinWaves) void loss_tile_kernel(LossArgs
     }
 }
 
-// Joins the tiles' pairs in tile order and forms the target's logit: 16 tokens to a workgroup of
-// 1024 threads, 64 threads to a token (one wave).
-__global__ __launch_bounds__(1024) void loss_join_kernel(LossArgs a, const int32_t* __restrict__ targets,
-                                                         float* __restrict__ loss, float* __restrict__ lse) {
+// Joins the tiles' pairs in tile order: 16 tokens to a workgroup of 1024 threads, each wave gets its own token's lse
+// (m0 + wave; of no meaning past M).
+__device__ __forceinline__ float join_pairs(const LossArgs& a, float2 (&pairs)[16][64]) {
     // pairs[wave][token]: a wave reads 16 tokens x 4 tiles, consecutive tokens side by side
-    __shared__ float2 pairs[16][64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int64_t m0 = (int64_t)blockIdx.x * 16;
     const float neg = -__builtin_inff();
@@ -128,16 +136,23 @@ __global__ __launch_bounds__(1024) void loss_join_kernel(LossArgs a, const int32
         }
     pairs[wave][lane] = make_float2(top, sum);
     __syncthreads();
-    const int64_t m = m0 + wave;
-    if (m >= a.M) return;
     // lane i holds pair i of the wave's token: waves i / 4, tile classes i % 4
     const float2 p = pairs[lane >> 2][(lane & 3) * 16 + wave];
     const float all = wave_max(p.x);
     float s = p.y == 0.0f ? 0.0f : p.y * __builtin_amdgcn_exp2f(p.x - all);
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) s += __shfl_xor(s, d);
-    const float l = (float)(((double)all + (double)__log2f(s)) * kLn2);  // (one rounding, of the result)
+    return (float)(((double)all + (double)__log2f(s)) * kLn2);  // (one rounding, of the result)
+}
 
+// The joined sums and the target's logit, a wave a token.
+__global__ __launch_bounds__(1024) void loss_join_kernel(LossArgs a, const int32_t* __restrict__ targets,
+                                                         float* __restrict__ loss, float* __restrict__ lse) {
+    __shared__ float2 pairs[16][64];
+    const float l = join_pairs(a, pairs);
+    const int lane = threadIdx.x & 63;
+    const int64_t m = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 6);
+    if (m >= a.M) return;
     const int32_t target = targets[m];
     float out = 0.0f;
     if (target >= 0 && target < a.V) {
@@ -158,6 +173,113 @@ __global__ __launch_bounds__(1024) void loss_join_kernel(LossArgs a, const int32
     }
 }
 
+// ---------------------------------------------------------------- a teacher's largest logits
+struct TeacherArgs {
+    const int32_t* ids;   // [M][k]; outside [0, V): no entry
+    const float* top;     // [M][k]
+    int k;
+    float inv_t;          // 1 / temperature
+};
+constexpr int kMaxTop = 256;    // entries a token: four a lane
+constexpr int kDots = 8;        // dot products a wave forms side by side, so that their loads are in flight together
+
+// z / T of the teacher's rows: logits[m][j].
+__global__ __launch_bounds__(256) void teacher_logits_kernel(LossArgs a, TeacherArgs t, float* __restrict__ logits) {
+    const int lane = threadIdx.x & 63, groups = (t.k + kDots - 1) / kDots;
+    const int64_t unit = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    const int64_t m = unit / groups;
+    const int j0 = (int)(unit - m * groups) * kDots;
+    if (m >= a.M) return;
+    const int8_t* const x = a.x_q + m * a.K;
+    const int8_t* rows[kDots];
+    int id[kDots], dot[kDots] = {};
+#pragma unroll
+    for (int i = 0; i < kDots; ++i) {
+        id[i] = j0 + i < t.k ? t.ids[m * t.k + j0 + i] : -1;
+        if (id[i] < 0 || id[i] >= a.V) id[i] = -1;
+        rows[i] = a.e + (int64_t)(id[i] < 0 ? 0 : id[i]) * a.K;
+    }
+    for (int k = lane * 16; k < a.K; k += 64 * 16) {
+        const v4i xv = *reinterpret_cast<const v4i*>(x + k);
+        v4i ev[kDots];
+#pragma unroll
+        for (int i = 0; i < kDots; ++i) ev[i] = *reinterpret_cast<const v4i*>(rows[i] + k);
+#pragma unroll
+        for (int i = 0; i < kDots; ++i)
+#pragma unroll
+            for (int w = 0; w < 4; ++w) dot[i] = __builtin_amdgcn_sdot4(xv[w], ev[i][w], dot[i], false);
+    }
+    const float sx = a.s_x[m];
+#pragma unroll
+    for (int i = 0; i < kDots; ++i) {
+        const int all = wave_sum(dot[i]);
+        if (lane == 0 && j0 + i < t.k)
+            logits[m * t.k + j0 + i] = id[i] < 0 ? 0.0f : sx * (a.s_e[id[i]] * (float)all) * t.inv_t;
+    }
+}
+
+// A token's teacher, lane i with entries i, i + 64, ..: its probabilities (0 where there is no entry) and their logarithms.
+struct Teacher {
+    int id[kMaxTop / 64];
+    float q[kMaxTop / 64], logq[kMaxTop / 64];
+    bool counts;   // some entry has a probability
+    __device__ __forceinline__ Teacher(const TeacherArgs& t, int64_t m, int64_t V) {
+        const int lane = threadIdx.x & 63;
+        const float neg = -__builtin_inff();
+        float best = neg, sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kMaxTop / 64; ++i) {
+            const int j = i * 64 + lane;
+            id[i] = j < t.k ? t.ids[m * t.k + j] : -1;
+            if (id[i] < 0 || id[i] >= V) id[i] = -1;
+            q[i] = id[i] < 0 ? neg : t.top[m * t.k + j];   // (what stands where there is no entry is not looked at)
+            best = fmaxf(best, q[i]);
+        }
+        best = wave_max(best);
+        counts = best != neg;
+#pragma unroll
+        for (int i = 0; i < kMaxTop / 64; ++i) {
+            logq[i] = counts ? (q[i] - best) * t.inv_t : neg;
+            q[i] = __builtin_amdgcn_exp2f(logq[i] * kLog2e);
+            sum += q[i];
+        }
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) sum += __shfl_xor(sum, d);
+        const float log_sum = counts ? logf(sum) : 0.0f, over = counts ? 1.0f / sum : 0.0f;
+#pragma unroll
+        for (int i = 0; i < kMaxTop / 64; ++i) {
+            q[i] *= over;
+            logq[i] -= log_sum;
+        }
+    }
+};
+
+// The joined sums, and the loss from them and the teacher's rows' logits, which become log p.
+__global__ __launch_bounds__(1024) void distillation_join_kernel(LossArgs a, TeacherArgs t, float* __restrict__ loss,
+                                                                 float* __restrict__ lse, float* __restrict__ logp) {
+    __shared__ float2 pairs[16][64];
+    const float l = join_pairs(a, pairs);
+    const int lane = threadIdx.x & 63;
+    const int64_t m = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 6);
+    if (m >= a.M) return;
+    const Teacher teacher(t, m, a.V);
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kMaxTop / 64; ++i) {
+        const int j = i * 64 + lane;
+        if (teacher.id[i] < 0) continue;
+        const float lp = logp[m * t.k + j] - l;
+        logp[m * t.k + j] = lp;
+        if (teacher.q[i] > 0.0f) sum = fmaf(teacher.q[i], teacher.logq[i] - lp, sum);  // (0 log 0 = 0)
+    }
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) sum += __shfl_xor(sum, d);
+    if (lane == 0) {
+        lse[m] = l;
+        loss[m] = sum;
+    }
+}
+
 // ---------------------------------------------------------------- backward
 struct GradArgs {
     const int8_t* x_q;
@@ -174,6 +296,8 @@ struct GradArgs {
     uint16_t* gx;        // [tokens][Vp P]: d s_e, or NULL
     uint16_t* gw;        // [Vp][Mp P]: d s_x, or NULL
     int64_t ldgx, ldgw;  // elements
+    float inv_t = 1.0f;     // 1 / temperature: of the logits (dloss has it already)
+    bool one_target = true; // targets name a row; else they only say which tokens count
 };
 
 // Partial maxima of what bounds d s_e (with the token's dloss) and d s_x (|p - [v = target]| <= 1): they scale d into
@@ -286,12 +410,12 @@ __global__ __launch_bounds__(C::NT, C::kMinWaves) void grad_tile_kernel(GradArgs
         const bool counts = t < trows && target >= 0 && target < a.vocab;
         // (p is formed from z - lse: in base 2 the roundings of lse log2 e and s_x log2 e would be p's largest errors;
         // 0 where the token does not count, whatever its scale and its logits are: the mask takes out a NaN, too)
-        const float sx = counts ? a.s_x[m] : 0.0f, lse = counts ? a.lse[m] : 0.0f;
+        const float scale = counts ? a.s_x[m] : 0.0f, sx = scale * a.inv_t, lse = counts ? a.lse[m] : 0.0f;
         const uint32_t keep = counts ? 0xFFFFFFFFu : 0u;
         const float dloss = counts ? a.dloss[m] : 0.0f;
         const float dl = __builtin_amdgcn_ldexpf(dloss, grad_exponent<P>(above_e, dloss));
-        const float dlx = __builtin_amdgcn_ldexpf(dloss * sx, up_w);
-        const int tl = counts ? (int)(target - a.v0 - n0 - wn) : -1;     // the target's row in the wave's range
+        const float dlx = __builtin_amdgcn_ldexpf(dloss * scale, up_w);
+        const int tl = counts && a.one_target ? (int)(target - a.v0 - n0 - wn) : -1;     // the target's row in the wave's range
 #pragma unroll
         for (int b = 0; b < C::WB; ++b) {
             float p[16];
@@ -341,6 +465,64 @@ __global__ __launch_bounds__(C::NT, C::kMinWaves) void grad_tile_kernel(GradArgs
             wave_lds_order();
         }
     }
+}
+
+// What the gradient of a distillation needs of each token, a wave a token: d_j = p - q for its entries (all q of the same
+// row together, so that every entry of a row holds the row's value), dloss / T, and whether it counts (0) or not (-1).
+__global__ __launch_bounds__(256) void teacher_gradient_kernel(TeacherArgs t, int64_t M, int64_t V, const float* __restrict__ logp,
+                                                               const float* __restrict__ dloss, float* __restrict__ d,
+                                                               float* __restrict__ dl, int32_t* __restrict__ counts) {
+    __shared__ float qs[4][kMaxTop];
+    __shared__ int ids[4][kMaxTop];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t m = (int64_t)blockIdx.x * 4 + wave;
+    if (m >= M) return;
+    const Teacher teacher(t, m, V);
+#pragma unroll
+    for (int i = 0; i < kMaxTop / 64; ++i) {
+        qs[wave][i * 64 + lane] = teacher.q[i];
+        ids[wave][i * 64 + lane] = teacher.id[i];
+    }
+    wave_lds_order();
+    float q[kMaxTop / 64] = {};
+    for (int j = 0; j < t.k; ++j) {
+        const int id = ids[wave][j];
+        const float qj = qs[wave][j];
+#pragma unroll
+        for (int i = 0; i < kMaxTop / 64; ++i) q[i] += id == teacher.id[i] ? qj : 0.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < kMaxTop / 64; ++i)
+        if (teacher.id[i] >= 0) d[m * t.k + i * 64 + lane] = __builtin_amdgcn_exp2f(logp[m * t.k + i * 64 + lane] * kLog2e) - q[i];
+    if (lane == 0) {
+        dl[m] = teacher.counts ? dloss[m] * t.inv_t : 0.0f;
+        counts[m] = teacher.counts ? 0 : -1;
+    }
+}
+
+// The pieces of the entries' d inside a piece of the vocabulary, over what the tiles have written there; a thread an entry.
+template <int P>
+__global__ __launch_bounds__(256) void teacher_scatter_kernel(GradArgs a, const int32_t* __restrict__ ids, int k,
+                                                              const float* __restrict__ d) {
+    const int lane = threadIdx.x & 63;
+    const int above_e = above_exponent(wave_max(a.maxima[lane]));
+    const int up_w = grad_exponent<P>(above_exponent(wave_max(a.maxima[kMaximaBlocks + lane])), kNoRow);
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= a.M * k) return;
+    const int64_t m = i / k, row = ids[i] - a.v0;   // (ids outside the vocabulary lie in no piece)
+    if (ids[i] < 0 || row < 0 || row >= a.V || a.targets[m] < 0) return;
+    const float dloss = a.dloss[m];
+    auto put = [&](uint16_t* at, float v) {
+        const float x[4] = {v, 0.0f, 0.0f, 0.0f};
+        uint2 first, second;
+        split4<P>(x, first, second);
+        at[0] = (uint16_t)first.x;
+        if constexpr (P == 2) at[32] = (uint16_t)second.x;
+    };
+    if (a.gx)
+        put(a.gx + m * a.ldgx + row / 32 * 32 * P + row % 32,
+            d[i] * __builtin_amdgcn_ldexpf(dloss, grad_exponent<P>(above_e, dloss)) * a.s_e[row]);
+    if (a.gw) put(a.gw + row * a.ldgw + m / 32 * 32 * P + m % 32, d[i] * __builtin_amdgcn_ldexpf(dloss * a.s_x[m], up_w));
 }
 
 // dx = the sum of its slabs (one for each piece and split), rounded to its type.  Unrolled: with few tokens there are few
@@ -516,10 +698,13 @@ size_t cross_entropy_workspace_bytes(int64_t M, int64_t V, int64_t K) {
     return (size_t)most_pairs(M, V) * sizeof(float2);
 }
 
-hipError_t launch_cross_entropy(const int8_t* x_q, const float* s_x, int64_t M, int64_t V, int64_t K, const int8_t* e,
-                                const float* s_e, const int32_t* targets, float* loss, float* lse, void* workspace,
-                                hipStream_t stream) {
-    LossArgs a{x_q, s_x, M, V, (int)K, 0, 0, e, s_e, static_cast<float2*>(workspace)};
+namespace {
+
+// The pairs of all tiles; a.V rows, a.ntw of their tiles on return.
+hipError_t launch_loss_tiles(LossArgs& a, hipStream_t stream) {
+    const int64_t M = a.M, V = a.V, K = a.K;
+    const int8_t* const e = a.e;
+    const float* const s_e = a.s_e;
     const TileSplit split = loss_tiles(M, V, K);
     a.V = split.main;
     if (hipError_t err = launch_loss_kind(a, split.kind, stream)) return err;
@@ -533,6 +718,16 @@ hipError_t launch_cross_entropy(const int8_t* x_q, const float* s_x, int64_t M, 
     }
     a.V = V;
     a.ntw = (int)row_tiles(split, V);
+    return hipSuccess;
+}
+
+}  // namespace
+
+hipError_t launch_cross_entropy(const int8_t* x_q, const float* s_x, int64_t M, int64_t V, int64_t K, const int8_t* e,
+                                const float* s_e, const int32_t* targets, float* loss, float* lse, void* workspace,
+                                hipStream_t stream) {
+    LossArgs a{x_q, s_x, M, V, (int)K, 0, 0, e, s_e, static_cast<float2*>(workspace)};
+    if (hipError_t err = launch_loss_tiles(a, stream)) return err;
     loss_join_kernel<<<dim3((unsigned)ceil_div(M, 16)), 1024, 0, stream>>>(a, targets, loss, lse);
     return hipGetLastError();
 }
@@ -541,10 +736,18 @@ size_t cross_entropy_backward_workspace_bytes(int64_t M, int64_t V, int64_t K, b
     return make_plan(M, V, K, bf16, want_dx, want_de).bytes;
 }
 
-hipError_t launch_cross_entropy_backward(const int8_t* x_q, const float* s_x, int64_t M, int64_t V, int64_t K,
-                                         const int8_t* e, const float* s_e, const int32_t* targets, const float* lse,
-                                         const float* dloss, void* dx, void* de, bool bf16, bool accumulate,
-                                         void* workspace, hipStream_t stream) {
+namespace {
+
+// A teacher's entries and their d, where the targets are distributions.
+struct TeacherGradient {
+    const TeacherArgs* args;
+    const float* d;
+};
+
+hipError_t launch_gradients(const int8_t* x_q, const float* s_x, int64_t M, int64_t V, int64_t K, const int8_t* e,
+                            const float* s_e, const int32_t* targets, const float* lse, const float* dloss, void* dx,
+                            void* de, bool bf16, bool accumulate, const TeacherGradient& teacher, void* workspace,
+                            hipStream_t stream) {
     const Plan p = make_plan(M, V, K, bf16, dx != nullptr, de != nullptr);
     const int P = bf16 ? 1 : 2;
     uint8_t* const ws = static_cast<uint8_t*>(workspace);
@@ -556,7 +759,17 @@ hipError_t launch_cross_entropy_backward(const int8_t* x_q, const float* s_x, in
         GradArgs g{x_q, s_x, M, rows, v0, V, (int)K, 0, 0, e + v0 * K, s_e + v0, targets, lse, dloss, maxima,
                    dx ? reinterpret_cast<uint16_t*>(ws + p.gx) : nullptr,
                    de ? reinterpret_cast<uint16_t*>(ws + p.gw) : nullptr, p.piece * P, p.Mp * P};
+        if (teacher.args) {
+            g.inv_t = teacher.args->inv_t;
+            g.one_target = false;
+        }
         if (hipError_t err = P == 1 ? launch_grad_tiles<1>(g, stream) : launch_grad_tiles<2>(g, stream)) return err;
+        if (teacher.args) {
+            const dim3 grid((unsigned)ceil_div(M * teacher.args->k, 256));
+            if (P == 1) teacher_scatter_kernel<1><<<grid, 256, 0, stream>>>(g, teacher.args->ids, teacher.args->k, teacher.d);
+            else teacher_scatter_kernel<2><<<grid, 256, 0, stream>>>(g, teacher.args->ids, teacher.args->k, teacher.d);
+            if (hipError_t err = hipGetLastError()) return err;
+        }
         if (dx) {
             float* const slab = reinterpret_cast<float*>(ws + p.dx) + (p.add ? 0 : v0 / p.piece * p.splits * M * K);
             const GradGemmArgs a{ws + p.gx, p.piece * P * 2, g.e, K, M, K, rows, {maxima, dloss}, p.slabs ? slab : dx, K, M * K,
@@ -580,6 +793,66 @@ hipError_t launch_cross_entropy_backward(const int8_t* x_q, const float* s_x, in
         return hipGetLastError();
     }
     return hipSuccess;
+}
+
+}  // namespace
+
+hipError_t launch_cross_entropy_backward(const int8_t* x_q, const float* s_x, int64_t M, int64_t V, int64_t K,
+                                         const int8_t* e, const float* s_e, const int32_t* targets, const float* lse,
+                                         const float* dloss, void* dx, void* de, bool bf16, bool accumulate,
+                                         void* workspace, hipStream_t stream) {
+    return launch_gradients(x_q, s_x, M, V, K, e, s_e, targets, lse, dloss, dx, de, bf16, accumulate, {nullptr, nullptr},
+                            workspace, stream);
+}
+
+int64_t distillation_max_top() { return kMaxTop; }
+
+hipError_t launch_distillation(const int8_t* x_q, const float* s_x, int64_t M, int64_t V, int64_t K, const int8_t* e,
+                               const float* s_e, const int32_t* ids, const float* top, int64_t k, float temperature,
+                               float* loss, float* lse, float* logp, void* workspace, hipStream_t stream) {
+    const TeacherArgs t{ids, top, (int)k, 1.0f / temperature};
+    LossArgs a{x_q, s_x, M, V, (int)K, 0, 0, e, s_e, static_cast<float2*>(workspace), kLog2e * t.inv_t};
+    if (hipError_t err = launch_loss_tiles(a, stream)) return err;
+    teacher_logits_kernel<<<dim3((unsigned)ceil_div(M * ceil_div(k, kDots), 4)), 256, 0, stream>>>(a, t, logp);
+    if (hipError_t err = hipGetLastError()) return err;
+    distillation_join_kernel<<<dim3((unsigned)ceil_div(M, 16)), 1024, 0, stream>>>(a, t, loss, lse, logp);
+    return hipGetLastError();
+}
+
+namespace {
+
+// The entries' d, dloss / T and the marks of the tokens that count, in front of the cross entropy's workspace.
+struct TeacherParts {
+    size_t d, dl, counts, rest;
+    TeacherParts(int64_t M, int64_t k) {
+        auto up = [](int64_t n) { return (size_t)((n * 4 + 255) / 256 * 256); };
+        d = 0;
+        dl = up(M * k);
+        counts = dl + up(M);
+        rest = counts + up(M);
+    }
+};
+
+}  // namespace
+
+size_t distillation_backward_workspace_bytes(int64_t M, int64_t V, int64_t K, int64_t k, bool bf16, bool want_dx, bool want_de) {
+    return TeacherParts(M, k).rest + cross_entropy_backward_workspace_bytes(M, V, K, bf16, want_dx, want_de);
+}
+
+hipError_t launch_distillation_backward(const int8_t* x_q, const float* s_x, int64_t M, int64_t V, int64_t K,
+                                        const int8_t* e, const float* s_e, const int32_t* ids, const float* top, int64_t k,
+                                        float temperature, const float* lse, const float* logp, const float* dloss,
+                                        void* dx, void* de, bool bf16, bool accumulate, void* workspace,
+                                        hipStream_t stream) {
+    const TeacherParts parts(M, k);
+    uint8_t* const ws = static_cast<uint8_t*>(workspace);
+    float* const d = reinterpret_cast<float*>(ws + parts.d);
+    float* const dl = reinterpret_cast<float*>(ws + parts.dl);
+    int32_t* const counts = reinterpret_cast<int32_t*>(ws + parts.counts);
+    const TeacherArgs t{ids, top, (int)k, 1.0f / temperature};
+    teacher_gradient_kernel<<<dim3((unsigned)ceil_div(M, 4)), 256, 0, stream>>>(t, M, V, logp, dloss, d, dl, counts);
+    if (hipError_t err = hipGetLastError()) return err;
+    return launch_gradients(x_q, s_x, M, V, K, e, s_e, counts, lse, dl, dx, de, bf16, accumulate, {&t, d}, ws + parts.rest, stream);
 }
 
 }  // namespace dfssm

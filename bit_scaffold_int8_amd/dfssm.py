@@ -31,6 +31,8 @@ EXPORTED = ("dfssm_status_string", "dfssm_version", "dfssm_quantize_act", "dfssm
             "dfssm_cross_entropy_workspace_bytes", "dfssm_cross_entropy",
             "dfssm_cross_entropy_backward_workspace_bytes", "dfssm_cross_entropy_backward",
             "dfssm_embedding_lookup_scaled", "dfssm_embedding_backward_workspace_bytes", "dfssm_embedding_backward",
+            "dfssm_distillation_workspace_bytes", "dfssm_distillation",
+            "dfssm_distillation_backward_workspace_bytes", "dfssm_distillation_backward",
             "dfssm_mamba2_conv", "dfssm_mamba2_conv_backward_workspace_bytes", "dfssm_mamba2_conv_backward",
             "dfssm_mamba2_scan_workspace_bytes", "dfssm_mamba2_scan")
 
@@ -120,6 +122,9 @@ def _load():
         "dfssm_embedding_lookup_scaled": [P, i64, P, P, i64, i64, ctypes.c_float, P, i64, i32, P],
         "dfssm_embedding_backward": [P, i64, P, i64, i32, i64, i64, ctypes.c_float, P, i32, i32, P, ctypes.c_size_t,
                                      P],
+        "dfssm_distillation": [P, P, i64, i64, i64, P, P, P, P, i64, ctypes.c_float, P, P, P, P, ctypes.c_size_t, P],
+        "dfssm_distillation_backward": [P, P, i64, i64, i64, P, P, P, P, i64, ctypes.c_float, P, P, P, P, P, i32, i32, P,
+                                        ctypes.c_size_t, P],
         "dfssm_mamba2_conv": [P, i64, i32, i64, i64, i64, P, P, P, P, P, P, i64, i32, P],
         "dfssm_mamba2_conv_backward": [P, i64, i32, i64, i64, i64, P, P, P, P, P, i64, i32, P, P, i64, P, P, P, P,
                                        ctypes.c_size_t, P],
@@ -128,6 +133,8 @@ def _load():
     for name, argtypes in (("dfssm_cross_entropy_workspace_bytes", [i64, i64, i64]),
                            ("dfssm_cross_entropy_backward_workspace_bytes", [i64, i64, i64, i32, i32, i32]),
                            ("dfssm_embedding_backward_workspace_bytes", [i64, i64, i64]),
+                           ("dfssm_distillation_workspace_bytes", [i64] * 4),
+                           ("dfssm_distillation_backward_workspace_bytes", [i64] * 4 + [i32] * 3),
                            ("dfssm_mamba2_conv_backward_workspace_bytes", [i64, i64, i64]),
                            ("dfssm_mamba2_scan_workspace_bytes", [i64] * 6)):
         getattr(lib, name).argtypes = argtypes
@@ -451,7 +458,7 @@ def dfssm_int8_gemm(x_q, s_x, w, s_w, y, stream=None) -> None:
             w.data_ptr(), ldw, s_w.data_ptr(), y.data_ptr(), ldy, _type("y", y))
 
 
-def _head(x_q, s_x, e, s_e, targets) -> tuple:
+def _head(x_q, s_x, e, s_e, targets=None) -> tuple:
     """Checks the head's operands; (M, V, K)."""
     import torch
     M, K = _matrix("x_q", x_q)
@@ -460,7 +467,8 @@ def _head(x_q, s_x, e, s_e, targets) -> tuple:
     _dense("s_x", s_x, (M,), torch.float32)
     _dense("e", e, (V, K), torch.int8)
     _dense("s_e", s_e, (V,), torch.float32)
-    _dense("targets", targets, (M,), torch.int32)
+    if targets is not None:
+        _dense("targets", targets, (M,), torch.int32)
     return M, V, K
 
 
@@ -510,6 +518,68 @@ def dfssm_cross_entropy_backward(x_q, s_x, e, s_e, targets, lse, dloss, dx, de, 
             x_q.data_ptr(), s_x.data_ptr(), M, V, K, e.data_ptr(), s_e.data_ptr(), targets.data_ptr(),
             lse.data_ptr(), dloss.data_ptr(), _ptr(dx), _ptr(de), t, int(bool(accumulate)), workspace.data_ptr(),
             _bytes(workspace))
+
+
+def _teacher(x_q, s_x, e, s_e, top_ids, top_logits) -> tuple:
+    """Checks the head's and the teacher's operands; (M, V, K, top)."""
+    import torch
+    M, V, K = _head(x_q, s_x, e, s_e)
+    top = _matrix("top_ids", top_ids)[1]
+    _dense("top_ids", top_ids, (M, top), torch.int32)
+    _dense("top_logits", top_logits, (M, top), torch.float32)
+    return M, V, K, top
+
+
+def dfssm_distillation_workspace_bytes(M: int, V: int, K: int, top: int) -> int:
+    return int(lib.dfssm_distillation_workspace_bytes(M, V, K, top))
+
+
+def dfssm_distillation(x_q, s_x, e, s_e, top_ids, top_logits, temperature, loss, lse, logp, workspace, stream=None) -> None:
+    """loss, lse fp32 [M] and logp fp32 [M, top]: the divergence of the head's distribution (x_q int8 [M, K], s_x [M],
+    e int8 [V, K], s_e [V]) from a teacher's, given by its largest logits (top_ids int32, top_logits fp32, both
+    [M, top]; ids outside [0, V): no entry) at a temperature; workspace: a tensor of
+    dfssm_distillation_workspace_bytes(M, V, K, top) bytes."""
+    import torch
+    M, V, K, top = _teacher(x_q, s_x, e, s_e, top_ids, top_logits)
+    _dense("loss", loss, (M,), torch.float32)
+    _dense("lse", lse, (M,), torch.float32)
+    _dense("logp", logp, (M, top), torch.float32)
+    _run_on("dfssm_distillation", (x_q, s_x, e, s_e, top_ids, top_logits, loss, lse, logp, workspace), stream,
+            x_q.data_ptr(), s_x.data_ptr(), M, V, K, e.data_ptr(), s_e.data_ptr(), top_ids.data_ptr(),
+            top_logits.data_ptr(), top, float(temperature), loss.data_ptr(), lse.data_ptr(), logp.data_ptr(),
+            workspace.data_ptr(), _bytes(workspace))
+
+
+def dfssm_distillation_backward_workspace_bytes(M: int, V: int, K: int, top: int, dx, de) -> int:
+    """For the gradients dx and de (tensors, or None for one that is not wanted)."""
+    if dx is None and de is None:
+        raise ValueError("dfssm_distillation_backward_workspace_bytes: dx or de expected")
+    t = _type("dx, de", de if dx is None else dx)
+    return int(lib.dfssm_distillation_backward_workspace_bytes(M, V, K, top, t, dx is not None, de is not None))
+
+
+def dfssm_distillation_backward(x_q, s_x, e, s_e, top_ids, top_logits, temperature, lse, logp, dloss, dx, de, workspace,
+                                accumulate: bool = False, stream=None) -> None:
+    """dx [M, K] and de [V, K] (both fp32 or both bf16; None for one that is not wanted) from the forward call's
+    operands, its lse and logp, and dloss fp32 [M]; accumulate adds to de.  workspace: a tensor of
+    dfssm_distillation_backward_workspace_bytes(M, V, K, top, dx, de) bytes."""
+    import torch
+    M, V, K, top = _teacher(x_q, s_x, e, s_e, top_ids, top_logits)
+    _dense("lse", lse, (M,), torch.float32)
+    _dense("logp", logp, (M, top), torch.float32)
+    _dense("dloss", dloss, (M,), torch.float32)
+    outs = [t for t in (dx, de) if t is not None]
+    if not outs:
+        raise ValueError("dfssm_distillation_backward: dx or de expected")
+    t = _type("dx, de", outs[0])
+    if dx is not None:
+        _dense("dx", dx, (M, K), outs[0].dtype)
+    if de is not None:
+        _dense("de", de, (V, K), outs[0].dtype)
+    _run_on("dfssm_distillation_backward", (x_q, s_x, e, s_e, top_ids, top_logits, lse, logp, dloss, workspace, *outs),
+            stream, x_q.data_ptr(), s_x.data_ptr(), M, V, K, e.data_ptr(), s_e.data_ptr(), top_ids.data_ptr(),
+            top_logits.data_ptr(), top, float(temperature), lse.data_ptr(), logp.data_ptr(), dloss.data_ptr(), _ptr(dx),
+            _ptr(de), t, int(bool(accumulate)), workspace.data_ptr(), _bytes(workspace))
 
 
 def dfssm_embedding_lookup_scaled(tokens, e, s_e, scale, out, stream=None) -> None:

@@ -527,6 +527,44 @@ dfssm_status dfssm_cross_entropy_backward(const int8_t* x_q, const float* s_x, i
                                           hipStream_t stream);
 
 /*
+ * Distillation from a teacher's largest logits through the int8 LM head, without the M x V logits in memory: the
+ * Kullback-Leibler divergence of the head's distribution from the teacher's at a temperature T.  With z as in dfssm_cross_entropy,
+ * and the entries j of token m whose id lies in [0, V):
+ *   p = softmax over the vocabulary of z[m] / T,   q = softmax over the entries of top_logits[m] / T
+ *   loss[m] = sum_j q_j (log q_j - log p[top_ids[m][j]]);   lse[m] = log sum_v exp(z[m][v] / T);   logp[m][j] = log p[top_ids[m][j]]
+ *   x_q, s_x, e, s_e as in dfssm_cross_entropy
+ *   top_ids int32 [M][top], top_logits fp32 [M][top] (read): an id outside [0, V) is no entry (a padded row; its logit may be anything, its
+ *             logp is 0); a logit of -infinity has q = 0; a token of no entry, or of such logits only, does not count: its
+ *             loss is 0.  Order does not matter, and an id may stand twice (its entries are those of the sum above).
+ *   loss, lse fp32 [M], logp fp32 [M][top] (written)
+ *   temperature  T, finite and above 0: at least 2^-60
+ *   workspace  at least dfssm_distillation_workspace_bytes(M, V, K, top) bytes, under dfssm_cross_entropy's rules
+ * Errors: as dfssm_cross_entropy; DFSSM_ERR_INVALID_ARG for top <= 0 or a temperature out of range, DFSSM_ERR_UNSUPPORTED for
+ * top > 256 or M * top > 2^28.
+ */
+size_t dfssm_distillation_workspace_bytes(int64_t M, int64_t V, int64_t K, int64_t top);
+dfssm_status dfssm_distillation(const int8_t* x_q, const float* s_x, int64_t M, int64_t V, int64_t K, const int8_t* e,
+                                const float* s_e, const int32_t* top_ids, const float* top_logits, int64_t top,
+                                float temperature, float* loss, float* lse, float* logp, void* workspace,
+                                size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * Gradients of dfssm_distillation for the dequantized values, as dfssm_cross_entropy_backward has them, with
+ *   d[m][v] = dloss[m] / T (p[v] - sum of the q_j with top_ids[m][j] == v);  0 for tokens that do not count
+ *   lse [M] and logp [M][top] from the forward call, dloss fp32 [M] (read)
+ *   dx, de, grad_type, accumulate_de, the precision of d and the workspace's rules: as there
+ * Errors: as the forward call's and dfssm_cross_entropy_backward's.
+ */
+size_t dfssm_distillation_backward_workspace_bytes(int64_t M, int64_t V, int64_t K, int64_t top, int32_t grad_type,
+                                                   int32_t want_dx, int32_t want_de);
+dfssm_status dfssm_distillation_backward(const int8_t* x_q, const float* s_x, int64_t M, int64_t V, int64_t K,
+                                         const int8_t* e, const float* s_e, const int32_t* top_ids,
+                                         const float* top_logits, int64_t top, float temperature, const float* lse,
+                                         const float* logp, const float* dloss, void* dx, void* de, int32_t grad_type,
+                                         int32_t accumulate_de, void* workspace, size_t workspace_bytes,
+                                         hipStream_t stream);
+
+/*
  * dfssm_embedding_lookup with a factor, a row stride and an fp32 or bf16 result:
  *   out[t][k] = (scale * s_e[id]) * E[id][k], id = tokens[t]   (fp32, then rounded to out_type);
  *   zeros for an id outside [0, V)

@@ -15,7 +15,7 @@ PROBE_SOURCES = ["probe_mfma.hip"]
 SOURCES = ["api.hip", "quantize.hip", "lora_down.hip", "gemv.hip", "gemm_mfma.hip", "gemm_prefill.hip",
            "int8_head.hip", "mamba2_step.hip", "decode_layers.hip",
            "density_field.hip", "int8_gemm.hip", "cross_entropy.hip", "grad_gemm.hip", "embedding.hip",
-           "mamba2_conv.hip", "mamba2_scan.hip"]
+           "mamba2_conv.hip", "mamba2_scan.hip", "mamba2_scan_backward.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [

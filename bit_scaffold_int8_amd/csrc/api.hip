@@ -100,6 +100,11 @@ hipError_t launch_distillation_backward(const int8_t* x_q, const float* s_x, int
                                         float temperature, const float* lse, const float* logp, const float* dloss,
                                         void* dx, void* de, bool bf16, bool accumulate, void* workspace,
                                         hipStream_t stream);
+size_t mamba2_scan_backward_workspace_bytes(int64_t T, int64_t S, int64_t H, int64_t N, int64_t G);
+hipError_t launch_mamba2_scan_backward(ScanArgs a, bool bf16, int N, const float* state_in, const void* dy, int64_t lddy,
+                                       const float* dstate_out, void* dx, int64_t lddx, float* ddt, int64_t ldddt, void* dB,
+                                       int64_t lddb, void* dC, int64_t lddc, float* dA_log, float* dD, float* ddt_bias,
+                                       float* dstate_in, void* workspace, hipStream_t stream);
 }  // namespace dfssm
 
 #include "decode_args.h"
@@ -875,6 +880,43 @@ dfssm_status dfssm_mamba2_scan(const dfssm_mamba2_scan_operands* op, void* y, in
         return DFSSM_ERR_INVALID_ARG;
     return dfssm::launch_mamba2_scan(a, op->type == DFSSM_BF16, (int)op->d_state, op->state_in, state_out, y, ldy, workspace,
                                      stream) == hipSuccess
+               ? DFSSM_OK
+               : DFSSM_ERR_HIP;
+}
+
+size_t dfssm_mamba2_scan_backward_workspace_bytes(int64_t T, int64_t S, int64_t nheads, int64_t headdim,
+                                                  int64_t d_state, int64_t ngroups) {
+    if (scan_sizes(T, S, nheads, headdim, d_state, ngroups, true) != DFSSM_OK) return 0;
+    return dfssm::mamba2_scan_backward_workspace_bytes(T, S, nheads, d_state, ngroups);
+}
+
+dfssm_status dfssm_mamba2_scan_backward(const dfssm_mamba2_scan_operands* op, const dfssm_mamba2_scan_gradients* grad,
+                                        void* workspace, size_t workspace_bytes, hipStream_t stream) {
+    dfssm::ScanArgs a;
+    if (!grad || !grad->dy || !grad->dx || !grad->dB || !grad->dC || !grad->ddt || !grad->dA_log || !grad->dD || !grad->ddt_bias ||
+        !workspace)
+        return DFSSM_ERR_INVALID_ARG;
+    if (!aligned16(workspace) || !aligned16(grad->dstate_out) || !aligned16(grad->dstate_in) || !aligned4(grad->ddt) ||
+        !aligned4(grad->dA_log) || !aligned4(grad->dD) || !aligned4(grad->ddt_bias))
+        return DFSSM_ERR_INVALID_ARG;
+    if (dfssm_status st = scan_operands(op, a)) return st;
+    const int64_t row = op->nheads * dfssm::kP, bc = op->ngroups * op->d_state;
+    dfssm_status worst = DFSSM_OK;
+    for (dfssm_status st : {wide_rows(grad->dy, grad->lddy, row, op->type), wide_rows(grad->dx, grad->lddx, row, op->type),
+                            wide_rows(grad->dB, grad->lddb, bc, op->type), wide_rows(grad->dC, grad->lddc, bc, op->type),
+                            stride_ok(grad->ldddt, op->nheads)})
+        if (worst != DFSSM_ERR_INVALID_ARG && st != DFSSM_OK) worst = st;
+    if (worst != DFSSM_OK) return worst;
+    const int64_t states = op->S * op->nheads * dfssm::kP * op->d_state * 4;
+    if ((grad->dstate_in != grad->dstate_out && overlapping(grad->dstate_in, states, grad->dstate_out, states)) ||
+        overlapping(grad->dstate_in, states, op->state_in, states))
+        return DFSSM_ERR_INVALID_ARG;
+    if (workspace_bytes < dfssm::mamba2_scan_backward_workspace_bytes(op->T, op->S, op->nheads, op->d_state, op->ngroups))
+        return DFSSM_ERR_INVALID_ARG;
+    return dfssm::launch_mamba2_scan_backward(a, op->type == DFSSM_BF16, (int)op->d_state, op->state_in, grad->dy, grad->lddy,
+                                              grad->dstate_out, grad->dx, grad->lddx, grad->ddt, grad->ldddt, grad->dB, grad->lddb,
+                                              grad->dC, grad->lddc, grad->dA_log, grad->dD, grad->ddt_bias, grad->dstate_in,
+                                              workspace, stream) == hipSuccess
                ? DFSSM_OK
                : DFSSM_ERR_HIP;
 }

@@ -1,0 +1,514 @@
+// mamba2_scan_backward.hip -- gradients of the Mamba-2 scan (gfx950).  With dh the gradient of the state,
+//
+//   dh_t = e^{a_{t+1}} dh_{t+1} + dy_t C_t^T,   dx_t = dt_t dh_t B_t + D dy_t,
+//   dB_t = sum over heads dt_t dh_t^T x_t,   dC_t = sum over heads h_t^T dy_t,
+//   ddt_t = x_t . (dh_t B_t) - exp(A_log) da_t,   da_t = e^{a_t} <dh_t, h_{t-1}>
+//
+// By chunks, as forward (scan.h, mamba2_scan.hip): one sweep forwards stores the state h at the start of every
+// chunk, one backwards the gradient g at every chunk's end (the same kernel with x -> dy, B -> C), and then all chunks are
+// independent.  In one, with L[t][s] = e^{cs_t - cs_s} for s <= t, M[t][s] = dy_t . x_s and K[t][s] = C_t . B_s:
+//
+//   dx_s = dt_s (sum_t K L dy_t + e^{cs_end - cs_s} g B_s) + D dy_s
+//   dC_t = sum over heads (sum_s M L dt_s B_s + e^{cs_t} h^T dy_t)
+//   dB_s = sum over heads (sum_t M L dt_s C_t + dt_s e^{cs_end - cs_s} g^T x_s)
+//   E[t][s] = M K L:  x_s . (dh_s B_s) = sum_t E[t][s] + e^{cs_end - cs_s} <g, x_s B_s^T>, and da_t adds up what crosses from
+//   before t to t or behind it: pairs s < t <= t' of E dt_s, h to t' >= t, s < t to g, and h to g.
+//
+// A workgroup takes a chunk and some heads of a group one after another; dC and dB, sums over heads, stay in its registers,
+// and of the products M L dt B only the sum over the heads of M L dt is formed, and multiplied once.  The shares of several
+// workgroups are joined in order.
+#include <math.h>
+
+#include "scan.h"
+
+namespace dfssm {
+
+size_t scan_workspace(ScanArgs& a, SweepArgs& s, uint8_t* ws, int64_t T, int64_t S, int64_t H, int64_t G, int N, int group_bytes);
+int scan_group_bytes(bool bf16, int N, bool backward);
+ScanPlan scan_plan(const Sequences& seq, int H, int G);
+
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kGradGroups = 512;   // workgroups wanted of the gradient kernel: two for each CU
+constexpr int kMaxSlabs = 2 * kGradGroups;
+constexpr int kSums = 4;           // floats per chunk and head: sums of da a, dy . x, ddt (and one that pads)
+
+struct ScanGradArgs {
+    ScanArgs a;
+    const void* dy;
+    int64_t lddy;
+    const float *starts, *ends;    // [chunk][H][64][N]: h at the chunk's start, its gradient at the chunk's end
+    void *dx, *dB, *dC;
+    int64_t lddx, lddb, lddc;
+    float* ddt;
+    int64_t ldddt;
+    float* sums;                   // [chunk][H][kSums]
+    float* slabs;                  // [slice][chunk][G][2][64][N]: shares of dB and dC
+    int slices, per_slice, group_bytes;
+};
+
+template <bool kBf16, int kN>
+struct GradLds {
+    static constexpr int kData = kBf16 ? 1 : 3, kOut = kBf16 ? 2 : 3, kPlane = kChunk * kP * 2;
+    static constexpr int kDy = 0, kX = kDy + kData * kPlane, kW = kX + kData * kPlane, kRows = kW + kOut * kPlane;
+    static constexpr int kPart = kRows + kData * kChunk * kN * 2;       // floats
+    static constexpr int kRowSum = 0, kColSum = 4 * kChunk, kDiag = 6 * kChunk, kDot = 7 * kChunk, kU = 8 * kChunk,
+                         kV = kU + kN / 16 * kChunk, kPass = kV + kN / 16 * kChunk;
+    static constexpr int bytes = kPart + (kPass + 8) * 4;
+    static constexpr int kLdSum = kChunk + 4;                           // the heads' sum of M L dt, over dy, x and W
+    static_assert(kChunk * kLdSum * 4 <= kRows, "it fits");
+};
+
+__device__ __forceinline__ float row_sum(float v) {   // over the 16 lanes of a row
+    v += dpp_f<kDppXor1>(v);
+    v += dpp_f<kDppXor2>(v);
+    v += dpp_f<kDppHalfMirror>(v);
+    v += dpp_f<kDppMirror>(v);
+    return v;
+}
+
+template <bool kBf16, int kN>
+__global__ __launch_bounds__(kThreads, 2) void scan_grad_kernel(ScanGradArgs s) {
+    using Lds = GradLds<kBf16, kN>;
+    using Block = GroupBlock<kN, Lds::kData>;
+    using E = Elem<kBf16>;
+    using T = typename E::type;
+    constexpr int kData = Lds::kData, kOut = Lds::kOut, kFull = 3, kPlane = Lds::kPlane;
+    // a wave's part of dB and dC: one tile of 16 state places, kTT tiles of tokens
+    constexpr int kTiles = kN / 16, kParts = 8 / kTiles, kTT = 4 / kParts, kSteps = kN / 32;
+    __shared__ __attribute__((aligned(16))) uint8_t lds[Lds::bytes];
+    float* const part = reinterpret_cast<float*>(lds + Lds::kPart);
+    const ScanArgs& a = s.a;
+    const int slice = blockIdx.y % s.slices, g = blockIdx.y / s.slices, c = blockIdx.x;
+    const int per_group = a.H / a.G, first = slice * s.per_slice;
+    const int last = first + s.per_slice < per_group ? first + s.per_slice : per_group;
+    int4 ch;
+    if (a.chunks) {
+        ch = a.chunks[c];
+    } else {
+        const int per = (a.seq.L + kChunk - 1) / kChunk, i = c % per, left = a.seq.L - i * kChunk;
+        ch = make_int4(c / per * a.seq.L + i * kChunk, left < kChunk ? left : kChunk, c / per, 0);
+    }
+    if (ch.z < 0 || ch.y <= 0) return;
+    const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, q = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const uint8_t* const block = a.groups + ((int64_t)c * a.G + g) * s.group_bytes;
+
+    // what stays for all heads: B's rows in LDS; K's tiles of this wave, and B and C at the places of its part of dB and dC
+    for (int i = tid; i < Block::kSet / 16; i += kThreads)
+        *reinterpret_cast<v4i*>(lds + Lds::kRows + i * 16) = *reinterpret_cast<const v4i*>(block + Block::kRows + i * 16);
+    for (int i = tid; i < kOut * kPlane / 16; i += kThreads)    // (tiles above the diagonal stay zero)
+        *reinterpret_cast<v4i*>(lds + Lds::kW + i * 16) = v4i{0, 0, 0, 0};
+    const int st = wave & 3, half = wave >> 2;        // M's tiles: columns st, rows st + half and st + half + 2
+    v4f products[2], sum_w[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int tt = st + half + 2 * i;
+        products[i] = sum_w[i] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+        if (tt < 4) products[i] = *reinterpret_cast<const v4f*>(block + ((tt * 4 + st) * 64 + lane) * 16);
+    }
+    const int nt = wave % kTiles, t0 = wave / kTiles * kTT;
+    v4f b_at[kTT], c_at[kTT], acc_b[kTT], acc_c[kTT];
+#pragma unroll
+    for (int t = 0; t < kTT; ++t) {
+        acc_b[t] = acc_c[t] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+            const int row = (t0 + t) * 16 + 4 * q + v, there = row < ch.y ? row : 0;
+            const float bv = E::load(static_cast<const T*>(a.B) + (int64_t)(ch.x + there) * a.ldb + g * kN + nt * 16 + r);
+            const float cv = E::load(static_cast<const T*>(a.C) + (int64_t)(ch.x + there) * a.ldc + g * kN + nt * 16 + r);
+            b_at[t][v] = row < ch.y ? bv : 0.0f;
+            c_at[t][v] = row < ch.y ? cv : 0.0f;
+        }
+    }
+    const int pt = wave & 3, sh = wave >> 2;          // dx's tiles: channels pt, tokens 2 sh and 2 sh + 1
+
+    for (int k = first; k < last; ++k) {
+        const int head = g * per_group + k;
+        const float* const arrays = a.heads + ((int64_t)c * a.H + head) * kHeadArrays * kChunk;
+        const float* const h = s.starts + ((int64_t)c * a.H + head) * kP * kN;
+        const float* const dh = s.ends + ((int64_t)c * a.H + head) * kP * kN;
+        {   // dy and x as pieces along the channels: each wave one tile of rows and one step
+            const int row = (wave >> 1) * 16 + r, there = row < ch.y ? row : 0, p = head * kP + (wave & 1) * 32 + 4 * q;
+            const T* const from_dy = static_cast<const T*>(s.dy) + (int64_t)(ch.x + there) * s.lddy + p;
+            const T* const from_x = static_cast<const T*>(a.x) + (int64_t)(ch.x + there) * a.ldx + p;
+            const v4f y0 = E::load4(from_dy), y1 = E::load4(from_dy + 16), x0 = E::load4(from_x), x1 = E::load4(from_x + 16);
+            float y[8], x[8];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                y[j] = row < ch.y ? y0[j] : 0.0f;
+                y[j + 4] = row < ch.y ? y1[j] : 0.0f;
+                x[j] = row < ch.y ? x0[j] : 0.0f;
+                x[j + 4] = row < ch.y ? x1[j] : 0.0f;
+            }
+            store_pieces(lds + Lds::kDy + (wave * 64 + lane) * 16, kPlane, split<kData>(y));
+            store_pieces(lds + Lds::kX + (wave * 64 + lane) * 16, kPlane, split<kData>(x));
+        }
+        // the states at this wave's places, across the channels
+        float h_at[2][8], dh_at[2][8];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                h_at[i][j] = h[(i * 32 + place(q, j)) * kN + nt * 16 + r];
+                dh_at[i][j] = dh[(i * 32 + place(q, j)) * kN + nt * 16 + r];
+            }
+        __syncthreads();
+        {   // M, K L, E: columns s along the lanes
+            const float s_hi = arrays[st * 16 + r], s_lo = arrays[kCsLo * kChunk + st * 16 + r], s_dt = arrays[kStep * kChunk + st * 16 + r];
+            float column = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int tt = st + half + 2 * i;
+                if (tt >= 4) continue;
+                v4f m = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    m = mma(load_pieces<kData>(lds + Lds::kDy + ((tt * 2 + j) * 64 + lane) * 16, kPlane),
+                            load_pieces<kData>(lds + Lds::kX + ((st * 2 + j) * 64 + lane) * 16, kPlane), m);
+                const v4f hi = *reinterpret_cast<const v4f*>(arrays + tt * 16 + 4 * q);
+                const v4f lo = *reinterpret_cast<const v4f*>(arrays + kCsLo * kChunk + tt * 16 + 4 * q);
+                float kl[8];
+                v4f rows;
+#pragma unroll
+                for (int v = 0; v < 4; ++v) {
+                    const bool on = tt > st || 4 * q + v >= r, strict = tt > st || 4 * q + v > r;
+                    const float f = on ? __builtin_amdgcn_exp2f((hi[v] - s_hi) + (lo[v] - s_lo)) : 0.0f;
+                    kl[v] = products[i][v] * f;
+                    kl[v + 4] = 0.0f;
+                    const float e = m[v] * kl[v];
+                    sum_w[i][v] = fmaf(m[v] * f, s_dt, sum_w[i][v]);
+                    column += strict ? e : 0.0f;
+                    rows[v] = row_sum(strict ? e * s_dt : 0.0f);
+                    if (tt == st && 4 * q + v == r) {
+                        part[Lds::kDiag + st * 16 + r] = e;
+                        part[Lds::kDot + st * 16 + r] = m[v];
+                    }
+                }
+                const Pieces<kOut> w = split<kOut>(kl);
+#pragma unroll
+                for (int n = 0; n < kOut; ++n)
+                    *reinterpret_cast<v4bf*>(lds + Lds::kW + n * kPlane + ((st * 2 + (tt >> 1)) * 64 + lane) * 16 + (tt & 1) * 8) =
+                        __builtin_shufflevector(w.p[n], w.p[n], 0, 1, 2, 3);
+                if (r == 0) *reinterpret_cast<v4f*>(part + Lds::kRowSum + st * kChunk + tt * 16 + 4 * q) = rows;
+            }
+            column += __shfl_xor(column, 16);
+            column += __shfl_xor(column, 32);
+            if (q == 0) part[Lds::kColSum + half * kChunk + st * 16 + r] = column;
+        }
+        {   // dC and dB through the states
+            const Pieces<kFull> hp[2] = {split<kFull>(h_at[0]), split<kFull>(h_at[1])};
+            const Pieces<kFull> dhp[2] = {split<kFull>(dh_at[0]), split<kFull>(dh_at[1])};
+#pragma unroll
+            for (int t = 0; t < kTT; ++t) {
+                v4f u = {0.0f, 0.0f, 0.0f, 0.0f}, w = u;
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    u = mma(load_pieces<kData>(lds + Lds::kDy + (((t0 + t) * 2 + j) * 64 + lane) * 16, kPlane), hp[j], u);
+                    w = mma(load_pieces<kData>(lds + Lds::kX + (((t0 + t) * 2 + j) * 64 + lane) * 16, kPlane), dhp[j], w);
+                }
+                acc_c[t] += u * *reinterpret_cast<const v4f*>(arrays + kDecay * kChunk + (t0 + t) * 16 + 4 * q);
+                acc_b[t] += w * *reinterpret_cast<const v4f*>(arrays + kWeight * kChunk + (t0 + t) * 16 + 4 * q);
+                v4f us, ws;
+#pragma unroll
+                for (int v = 0; v < 4; ++v) {
+                    us[v] = row_sum(u[v] * c_at[t][v]);
+                    ws[v] = row_sum(w[v] * b_at[t][v]);
+                }
+                if (r == 0) {
+                    *reinterpret_cast<v4f*>(part + Lds::kU + nt * kChunk + (t0 + t) * 16 + 4 * q) = us;
+                    *reinterpret_cast<v4f*>(part + Lds::kV + nt * kChunk + (t0 + t) * 16 + 4 * q) = ws;
+                }
+            }
+            float pass = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) pass = fmaf(h_at[i][j], dh_at[i][j], pass);
+            pass = row_sum(pass);
+            pass += __shfl_xor(pass, 16);
+            pass += __shfl_xor(pass, 32);
+            if (lane == 0) part[Lds::kPass + wave] = t0 == 0 ? pass : 0.0f;
+        }
+        __syncthreads();
+        {   // dx
+            float dy[2][8];
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const int row = i * 32 + place(q, j), there = row < ch.y ? row : 0;
+                    const float v = E::load(static_cast<const T*>(s.dy) + (int64_t)(ch.x + there) * s.lddy + head * kP + pt * 16 + r);
+                    dy[i][j] = row < ch.y ? v : 0.0f;
+                }
+            v4f inter[2], intra[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) inter[i] = intra[i] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int n = 0; n < kSteps; ++n) {
+                const float* const from = dh + (pt * 16 + r) * kN + n * 32 + 4 * q;
+                const v4f lo = *reinterpret_cast<const v4f*>(from), hi = *reinterpret_cast<const v4f*>(from + 16);
+                const float f[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+                const Pieces<kOut> state = split<kOut>(f);
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    inter[i] = mma(load_pieces<kData>(lds + Lds::kRows + (((2 * sh + i) * kSteps + n) * 64 + lane) * 16, Block::kPlane),
+                                   state, inter[i]);
+            }
+            const Pieces<kData> rows[2] = {split<kData>(dy[0]), split<kData>(dy[1])};
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    if (j >= sh)     // (tokens t from the tile's own on)
+                        intra[i] = mma(load_pieces<kOut>(lds + Lds::kW + (((2 * sh + i) * 2 + j) * 64 + lane) * 16, kPlane), rows[j], intra[i]);
+            const float skip = a.D[head];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int tile = 2 * sh + i;
+                const v4f dt = *reinterpret_cast<const v4f*>(arrays + kStep * kChunk + tile * 16 + 4 * q);
+                const v4f weight = *reinterpret_cast<const v4f*>(arrays + kWeight * kChunk + tile * 16 + 4 * q);
+#pragma unroll
+                for (int v = 0; v < 4; ++v) {
+                    const int row = tile * 16 + 4 * q + v;
+                    const float own = sh == 0 ? dy[0][i * 4 + v] : dy[1][i * 4 + v];
+                    if (row < ch.y)
+                        E::store(static_cast<T*>(s.dx) + (int64_t)(ch.x + row) * s.lddx + head * kP + pt * 16 + r,
+                                 fmaf(skip, own, fmaf(dt[v], intra[i][v], weight[v] * inter[i][v])));
+                }
+            }
+        }
+        if (wave == (k & 7)) {   // ddt and the parameters' sums, a token a lane
+            const float hi = arrays[lane], lo = arrays[kCsLo * kChunk + lane], dt = arrays[kStep * kChunk + lane];
+            const float end_hi = arrays[kChunk - 1], end_lo = arrays[kCsLo * kChunk + kChunk - 1];
+            float rows = 0.0f, u = 0.0f, v = 0.0f, pass = 0.0f;
+            for (int i = 0; i <= lane >> 4; ++i) rows += part[Lds::kRowSum + i * kChunk + lane];
+#pragma unroll
+            for (int i = 0; i < kTiles; ++i) {
+                u += part[Lds::kU + i * kChunk + lane];
+                v += part[Lds::kV + i * kChunk + lane];
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) pass += part[Lds::kPass + i];
+            const float columns = part[Lds::kColSum + lane] + part[Lds::kColSum + kChunk + lane];
+            u *= arrays[kDecay * kChunk + lane];
+            v *= __builtin_amdgcn_exp2f((end_hi - hi) + (end_lo - lo));
+            pass *= arrays[kDecay * kChunk + kChunk - 1];
+            const float z = columns + part[Lds::kDiag + lane] + v;    // x . (dh B)
+            // from t on: rows of E and u, less the columns from t on (pairs that lie behind t whole); before t: v
+            double from = (double)rows + (double)u - (double)(dt * columns), before = (double)(dt * v);
+            const double own = before;
+#pragma unroll
+            for (int d = 1; d < 64; d <<= 1) {
+                const double o = __shfl_down(from, d), p = __shfl_up(before, d);
+                if (lane + d < 64) from += o;
+                if (lane >= d) before += p;
+            }
+            const float da = (float)(from + (before - own) + (double)pass);
+            const float rate = expf(a.A_log[head]);
+            float raw = 0.0f, ddt = 0.0f;
+            if (lane < ch.y) {
+                raw = a.dt[(int64_t)(ch.x + lane) * a.lddt + head] + a.dt_bias[head];
+                ddt = (z - rate * da) * (raw > 20.0f ? 1.0f : 1.0f / (1.0f + expf(-raw)));
+                s.ddt[(int64_t)(ch.x + lane) * s.ldddt + head] = ddt;
+            }
+            float sum_a = -rate * dt * da, sum_d = part[Lds::kDot + lane], sum_t = ddt;
+#pragma unroll
+            for (int d = 1; d < 64; d <<= 1) {
+                sum_a += __shfl_xor(sum_a, d);
+                sum_d += __shfl_xor(sum_d, d);
+                sum_t += __shfl_xor(sum_t, d);
+            }
+            if (lane == 0)
+                *reinterpret_cast<v4f*>(s.sums + ((int64_t)c * a.H + head) * kSums) = v4f{sum_a, sum_d, sum_t, 0.0f};
+        }
+    }
+
+    // dC += W B and dB += W^T C with W the heads' sum of M L dt
+    __syncthreads();
+    float* const w = reinterpret_cast<float*>(lds);
+    for (int i = tid; i < kChunk * Lds::kLdSum; i += kThreads) w[i] = 0.0f;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int tt = st + half + 2 * i;
+        if (tt >= 4) continue;
+#pragma unroll
+        for (int v = 0; v < 4; ++v) w[(tt * 16 + 4 * q + v) * Lds::kLdSum + st * 16 + r] = sum_w[i][v];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const Pieces<kData> across = load_pieces<kData>(block + Block::kAcross + ((nt * 2 + j) * 64 + lane) * 16, Block::kPlane);
+        const Pieces<kData> cross = load_pieces<kData>(block + Block::kCross + ((nt * 2 + j) * 64 + lane) * 16, Block::kPlane);
+#pragma unroll
+        for (int t = 0; t < kTT; ++t) {
+            const float* const from = w + ((t0 + t) * 16 + r) * Lds::kLdSum + j * 32 + 4 * q;
+            const v4f lo = *reinterpret_cast<const v4f*>(from), hi = *reinterpret_cast<const v4f*>(from + 16);
+            const float f[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+            acc_c[t] = mma(split<kOut>(f), across, acc_c[t]);
+            float e[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) e[i] = w[(j * 32 + place(q, i)) * Lds::kLdSum + (t0 + t) * 16 + r];
+            acc_b[t] = mma(split<kOut>(e), cross, acc_b[t]);
+        }
+    }
+    float* const slab = s.slabs ? s.slabs + ((((int64_t)slice * a.nchunks + c) * a.G + g) * 2) * kChunk * kN : nullptr;
+#pragma unroll
+    for (int t = 0; t < kTT; ++t)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+            const int row = (t0 + t) * 16 + 4 * q + v;
+            if (row >= ch.y) continue;
+            if (slab) {
+                slab[row * kN + nt * 16 + r] = acc_b[t][v];
+                slab[(kChunk + row) * kN + nt * 16 + r] = acc_c[t][v];
+            } else {
+                E::store(static_cast<T*>(s.dB) + (int64_t)(ch.x + row) * s.lddb + g * kN + nt * 16 + r, acc_b[t][v]);
+                E::store(static_cast<T*>(s.dC) + (int64_t)(ch.x + row) * s.lddc + g * kN + nt * 16 + r, acc_c[t][v]);
+            }
+        }
+}
+
+// dB and dC: the slices' shares in their order; workgroups (chunk, group).
+template <bool kBf16, int kN>
+__global__ __launch_bounds__(256) void join_slabs_kernel(ScanGradArgs s) {
+    using E = Elem<kBf16>;
+    using T = typename E::type;
+    const ScanArgs& a = s.a;
+    const int c = blockIdx.x, g = blockIdx.y;
+    int4 ch;
+    if (a.chunks) {
+        ch = a.chunks[c];
+    } else {
+        const int per = (a.seq.L + kChunk - 1) / kChunk, i = c % per, left = a.seq.L - i * kChunk;
+        ch = make_int4(c / per * a.seq.L + i * kChunk, left < kChunk ? left : kChunk, c / per, 0);
+    }
+    if (ch.z < 0) return;
+    const int64_t step = (int64_t)a.nchunks * a.G * 2 * kChunk * kN;
+    for (int i = threadIdx.x; i < 2 * kChunk * kN / 4; i += 256) {
+        const int which = i / (kChunk * kN / 4), row = i / (kN / 4) % kChunk, n = i % (kN / 4) * 4;
+        if (row >= ch.y) continue;
+        const float* const from = s.slabs + (((int64_t)c * a.G + g) * 2 + which) * kChunk * kN + row * kN + n;
+        v4f v = *reinterpret_cast<const v4f*>(from);
+#pragma unroll 4
+        for (int k = 1; k < s.slices; ++k) v += *reinterpret_cast<const v4f*>(from + k * step);
+        if (which == 0) E::store4(static_cast<T*>(s.dB) + (int64_t)(ch.x + row) * s.lddb + g * kN + n, v);
+        else E::store4(static_cast<T*>(s.dC) + (int64_t)(ch.x + row) * s.lddc + g * kN + n, v);
+    }
+}
+
+// The parameters' gradients of a head: the chunks' sums, each thread every 256th, then the threads in a tree.
+__global__ __launch_bounds__(256) void join_sums_kernel(ScanArgs a, const float* __restrict__ sums, float* __restrict__ dA_log,
+                                                        float* __restrict__ dD, float* __restrict__ ddt_bias) {
+    __shared__ v4f part[256];
+    const int head = blockIdx.x, tid = threadIdx.x;
+    v4f v = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int c = tid; c < a.nchunks; c += 256) {
+        if (a.chunks) {   // (the table's unused entries and empty chunks have no sums)
+            const int4 ch = a.chunks[c];
+            if (ch.z < 0 || ch.y <= 0) continue;
+        }
+        v += *reinterpret_cast<const v4f*>(sums + ((int64_t)c * a.H + head) * kSums);
+    }
+    part[tid] = v;
+    __syncthreads();
+    for (int d = 128; d > 0; d >>= 1) {
+        if (tid < d) part[tid] += part[tid + d];
+        __syncthreads();
+    }
+    if (tid == 0) {
+        dA_log[head] = part[0].x;
+        dD[head] = part[0].y;
+        ddt_bias[head] = part[0].z;
+    }
+}
+
+template <class F>
+hipError_t with_kind(bool bf16, int N, F f) {
+    if (N == 128) return bf16 ? f(std::true_type(), std::integral_constant<int, 128>()) : f(std::false_type(), std::integral_constant<int, 128>());
+    return bf16 ? f(std::true_type(), std::integral_constant<int, 64>()) : f(std::false_type(), std::integral_constant<int, 64>());
+}
+
+struct GradParts {
+    float *starts, *ends, *sums, *slabs;
+    size_t bytes;
+};
+
+GradParts grad_parts(ScanArgs& a, SweepArgs& s, uint8_t* ws, int64_t T, int64_t S, int64_t H, int64_t G, int N, int group_bytes) {
+    GradParts p{};
+    size_t at = scan_workspace(a, s, ws, T, S, H, G, N, group_bytes);
+    auto take = [&](int64_t bytes) {
+        float* const q = reinterpret_cast<float*>(ws + at);
+        at += (size_t)(bytes + 255) / 256 * 256;
+        return q;
+    };
+    const int64_t chunks = T / kChunk + S;
+    p.starts = take(chunks * H * kP * N * 4);
+    p.ends = take(chunks * H * kP * N * 4);
+    p.sums = take(chunks * H * kSums * 4);
+    p.slabs = take((int64_t)kMaxSlabs * 2 * kChunk * N * 4);
+    p.bytes = at;
+    return p;
+}
+
+}  // namespace
+
+size_t mamba2_scan_backward_workspace_bytes(int64_t T, int64_t S, int64_t H, int64_t N, int64_t G) {
+    ScanArgs a{};
+    SweepArgs s{};
+    return grad_parts(a, s, nullptr, T, S, H, G, (int)N, scan_group_bytes(false, (int)N, true)).bytes;
+}
+
+hipError_t launch_mamba2_scan_backward(ScanArgs a, bool bf16, int N, const float* state_in, const void* dy, int64_t lddy,
+                                       const float* dstate_out, void* dx, int64_t lddx, float* ddt, int64_t ldddt, void* dB,
+                                       int64_t lddb, void* dC, int64_t lddc, float* dA_log, float* dD, float* ddt_bias,
+                                       float* dstate_in, void* workspace, hipStream_t stream) {
+    const ScanPlan plan = scan_plan(a.seq, a.H, a.G);
+    SweepArgs s{};
+    s.group_bytes = scan_group_bytes(bf16, N, true);
+    const GradParts parts = grad_parts(a, s, static_cast<uint8_t*>(workspace), a.seq.T, a.seq.S, a.H, a.G, N, s.group_bytes);
+    if (!a.seq.cu) a.chunks = a.segments = nullptr;
+    if (!plan.segmented) s.segment_states = nullptr;
+    a.nchunks = plan.nchunks;
+    a.nsegments = plan.nsegments;
+    a.per_segment = plan.per_segment;
+    if (hipError_t err = launch_scan_prepare(a, bf16, N, true, stream)) return err;
+    return with_kind(bf16, N, [&](auto b, auto n) {
+        using Block = GroupBlock<n.value, b.value ? 1 : 3>;
+        s.a = a;
+        s.v = a.x;
+        s.ldv = a.ldx;
+        s.key = Block::kAcross;
+        s.start = state_in;
+        s.starts = parts.starts;
+        if (hipError_t err = launch_sweep(s, plan, bf16, N, kStarts, stream)) return err;
+        s.v = dy;
+        s.ldv = lddy;
+        s.key = Block::kCross;
+        s.reverse = true;
+        s.start = dstate_out;
+        s.end = dstate_in;
+        s.starts = parts.ends;
+        if (hipError_t err = launch_sweep(s, plan, bf16, N, kStarts, stream)) return err;
+        ScanGradArgs g{a, dy, lddy, parts.starts, parts.ends, dx, dB, dC, lddx, lddb, lddc, ddt, ldddt, parts.sums, nullptr, 1, 0,
+                       s.group_bytes};
+        const int per_group = a.H / a.G;
+        const int64_t units = (int64_t)a.nchunks * a.G;
+        const int64_t wanted = units >= kGradGroups ? 1 : (kGradGroups + units - 1) / units;
+        g.per_slice = (int)((per_group + wanted - 1) / wanted);
+        g.slices = (per_group + g.per_slice - 1) / g.per_slice;
+        if (g.slices > 1) g.slabs = parts.slabs;
+        scan_grad_kernel<b.value, n.value><<<dim3((unsigned)a.nchunks, (unsigned)(a.G * g.slices)), kThreads, 0, stream>>>(g);
+        if (hipError_t err = hipGetLastError()) return err;
+        if (g.slices > 1) {
+            join_slabs_kernel<b.value, n.value><<<dim3((unsigned)a.nchunks, (unsigned)a.G), 256, 0, stream>>>(g);
+            if (hipError_t err = hipGetLastError()) return err;
+        }
+        join_sums_kernel<<<dim3((unsigned)a.H), 256, 0, stream>>>(a, parts.sums, dA_log, dD, ddt_bias);
+        return hipGetLastError();
+    });
+}
+
+}  // namespace dfssm

@@ -34,7 +34,8 @@ EXPORTED = ("dfssm_status_string", "dfssm_version", "dfssm_quantize_act", "dfssm
             "dfssm_distillation_workspace_bytes", "dfssm_distillation",
             "dfssm_distillation_backward_workspace_bytes", "dfssm_distillation_backward",
             "dfssm_mamba2_conv", "dfssm_mamba2_conv_backward_workspace_bytes", "dfssm_mamba2_conv_backward",
-            "dfssm_mamba2_scan_workspace_bytes", "dfssm_mamba2_scan")
+            "dfssm_mamba2_scan_workspace_bytes", "dfssm_mamba2_scan", "dfssm_mamba2_scan_backward_workspace_bytes",
+            "dfssm_mamba2_scan_backward")
 
 # dfssm_type: the element type of a result or a gradient
 DFSSM_F32 = 0
@@ -62,6 +63,16 @@ SCAN_SIZES = ("ldx", "ldb", "ldc", "lddt", "T", "S", "nheads", "headdim", "d_sta
 class ScanOperands(ctypes.Structure):
     _fields_ = ([(name, ctypes.c_void_p) for name in SCAN_POINTERS] + [(name, ctypes.c_int64) for name in SCAN_SIZES]
                 + [("type", ctypes.c_int32)])
+
+
+# dfssm_mamba2_scan_gradients
+SCAN_GRADIENTS = ("dy", "dstate_out", "dx", "dB", "dC", "ddt", "dA_log", "dD", "ddt_bias", "dstate_in")
+SCAN_GRADIENT_SIZES = ("lddy", "lddx", "lddb", "lddc", "ldddt")
+
+
+class ScanGradients(ctypes.Structure):
+    _fields_ = ([(name, ctypes.c_void_p) for name in SCAN_GRADIENTS]
+                + [(name, ctypes.c_int64) for name in SCAN_GRADIENT_SIZES])
 
 
 class DfssmError(RuntimeError):
@@ -129,6 +140,7 @@ def _load():
         "dfssm_mamba2_conv_backward": [P, i64, i32, i64, i64, i64, P, P, P, P, P, i64, i32, P, P, i64, P, P, P, P,
                                        ctypes.c_size_t, P],
         "dfssm_mamba2_scan": [P, P, i64, P, P, ctypes.c_size_t, P],
+        "dfssm_mamba2_scan_backward": [P, P, P, ctypes.c_size_t, P],
     }
     for name, argtypes in (("dfssm_cross_entropy_workspace_bytes", [i64, i64, i64]),
                            ("dfssm_cross_entropy_backward_workspace_bytes", [i64, i64, i64, i32, i32, i32]),
@@ -136,7 +148,8 @@ def _load():
                            ("dfssm_distillation_workspace_bytes", [i64] * 4),
                            ("dfssm_distillation_backward_workspace_bytes", [i64] * 4 + [i32] * 3),
                            ("dfssm_mamba2_conv_backward_workspace_bytes", [i64, i64, i64]),
-                           ("dfssm_mamba2_scan_workspace_bytes", [i64] * 6)):
+                           ("dfssm_mamba2_scan_workspace_bytes", [i64] * 6),
+                           ("dfssm_mamba2_scan_backward_workspace_bytes", [i64] * 6)):
         getattr(lib, name).argtypes = argtypes
         getattr(lib, name).restype = ctypes.c_size_t
     for name, argtypes in sigs.items():
@@ -742,3 +755,32 @@ def dfssm_mamba2_scan(x, dt, B, C, A_log, D, dt_bias, state_in, state_out, y, wo
         raise ValueError(f"y: shape {tuple(x.shape)} expected, got {tuple(y.shape)}")
     _run_on("dfssm_mamba2_scan", [*tensors, y, workspace], stream, ctypes.addressof(op), y.data_ptr(), ldy,
             _ptr(state_out), workspace.data_ptr(), _bytes(workspace))
+
+
+def dfssm_mamba2_scan_backward_workspace_bytes(T: int, S: int, nheads: int, headdim: int, d_state: int,
+                                               ngroups: int = 1) -> int:
+    return int(lib.dfssm_mamba2_scan_backward_workspace_bytes(T, S, nheads, headdim, d_state, ngroups))
+
+
+def dfssm_mamba2_scan_backward(x, dt, B, C, A_log, D, dt_bias, state_in, dy, dstate_out, dx, ddt, dB, dC, dA_log, dD, ddt_bias,
+                               dstate_in, workspace, cu_seqlens=None, sequences=None, stream=None) -> None:
+    """The gradients of dfssm_mamba2_scan from its operands, dy [T, H, 64] and dstate_out (fp32 [S, H, 64, N] or None:
+    zeros): dx, dB, dC (their operands' type and shape), ddt fp32 [T, H], dA_log, dD, ddt_bias fp32 [H], dstate_in (fp32, or
+    None: not wanted; dstate_out itself: in place); workspace: a tensor of
+    dfssm_mamba2_scan_backward_workspace_bytes(T, S, H, 64, N, G) bytes."""
+    import torch
+    op, tensors = _scan_operands("dfssm_mamba2_scan_backward", x, dt, B, C, A_log, D, dt_bias, state_in,
+                                 {"dstate_out": dstate_out, "dstate_in": dstate_in}, cu_seqlens, sequences)
+    strides = {}
+    for what, t, like in (("dy", dy, x), ("dx", dx, x), ("dB", dB, B), ("dC", dC, C)):
+        strides[what], *same = _heads(what, t, op.T, x.dtype)
+        if same != list(like.shape[1:]):
+            raise ValueError(f"{what}: shape {tuple(like.shape)} expected, got {tuple(t.shape)}")
+    ldddt = _rows("ddt", ddt, (op.T, op.nheads), torch.float32)
+    for what, t in (("dA_log", dA_log), ("dD", dD), ("ddt_bias", ddt_bias)):
+        _dense(what, t, (op.nheads,), torch.float32)
+    grad = ScanGradients(dy.data_ptr(), _ptr(dstate_out), dx.data_ptr(), dB.data_ptr(), dC.data_ptr(), ddt.data_ptr(),
+                         dA_log.data_ptr(), dD.data_ptr(), ddt_bias.data_ptr(), _ptr(dstate_in), strides["dy"], strides["dx"],
+                         strides["dB"], strides["dC"], ldddt)
+    _run_on("dfssm_mamba2_scan_backward", [*tensors, dy, dx, dB, dC, ddt, dA_log, dD, ddt_bias, workspace], stream,
+            ctypes.addressof(op), ctypes.addressof(grad), workspace.data_ptr(), _bytes(workspace))

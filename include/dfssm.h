@@ -695,6 +695,45 @@ size_t dfssm_mamba2_scan_workspace_bytes(int64_t T, int64_t S, int64_t nheads, i
 dfssm_status dfssm_mamba2_scan(const dfssm_mamba2_scan_operands* op, void* y, int64_t ldy, float* state_out,
                                void* workspace, size_t workspace_bytes, hipStream_t stream);
 
+/*
+ * Gradients of dfssm_mamba2_scan; with dstate the gradient of the state, running backwards from dstate_out:
+ *   dstate[h] += dy[t][h] C[t][g]^T;   dx[t][h] = dt dstate[h] B[t][g] + D[h] dy[t][h]
+ *   dB[t][g] = sum over the group's heads of dt dstate[h]^T x[t][h];   dC[t][g] = sum over them of state[h]^T dy[t][h]
+ *   da = exp(-dt exp(A_log[h])) <dstate[h], state before t>;   dstate[h] <- exp(-dt exp(A_log[h])) dstate[h]
+ *   ddt[t][h] = (x . (dstate[h] B) - exp(A_log[h]) da) sigmoid(dt_raw + dt_bias[h])  (factor 1 above 20: of the raw dt)
+ *   dA_log[h] = -sum_t dt exp(A_log[h]) da;   dD[h] = sum_t x . dy;   ddt_bias[h] = sum_t ddt;   dstate_in: dstate at the start
+ *   dy          type [T][nheads][64] (read), rows lddy apart;   dstate_out  fp32 [S][nheads][64][d_state], or NULL for zeros
+ *   dx, dB, dC  of x's, B's and C's type and shape, rows lddx, lddb and lddc apart, written
+ *   ddt fp32 [T][nheads], rows ldddt apart, written;   dA_log, dD, ddt_bias  fp32 [nheads], written
+ *   dstate_in   fp32 [S][nheads][64][d_state], written, or NULL; may be dstate_out itself
+ *   workspace   at least dfssm_mamba2_scan_backward_workspace_bytes(...) bytes, 16-byte aligned, under
+ *               dfssm_cross_entropy's rules: the state and its gradient once for every 64 tokens, 2 nheads * 256 d_state bytes
+ * The alignment and the strides' rules are the forward call's (dy, dx, dB and dC like x).  No output may overlap an input
+ * or another output but as said.
+ * The chunked form for every length.  The products take fp32 operands, the states and their gradients in three bf16 pieces
+ * (2^-24 of each), and where dx, dB and dC are bf16 what enters only these in two (2^-17); ddt and the parameters'
+ * gradients are formed from three for either type.  Sums run in a fixed order.
+ * Errors: as the forward call's.
+ */
+typedef struct dfssm_mamba2_scan_gradients {
+    const void* dy;
+    const float* dstate_out;
+    void* dx;
+    void* dB;
+    void* dC;
+    float* ddt;
+    float* dA_log;
+    float* dD;
+    float* ddt_bias;
+    float* dstate_in;
+    int64_t lddy, lddx, lddb, lddc, ldddt;
+} dfssm_mamba2_scan_gradients;
+
+size_t dfssm_mamba2_scan_backward_workspace_bytes(int64_t T, int64_t S, int64_t nheads, int64_t headdim,
+                                                  int64_t d_state, int64_t ngroups);
+dfssm_status dfssm_mamba2_scan_backward(const dfssm_mamba2_scan_operands* op, const dfssm_mamba2_scan_gradients* grad,
+                                        void* workspace, size_t workspace_bytes, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

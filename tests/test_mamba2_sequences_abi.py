@@ -96,13 +96,40 @@ def test_scan_rejects(kw, want):
     assert _scan(**kw) == want
 
 
+def _scan_backward(ws=A, n=BIG, null=False, no_gradients=False, **kw):
+    import ctypes
+    from bit_scaffold_int8_amd import dfssm
+    g = dict(dy=A, dstate_out=A, dx=A, dB=A, dC=A, ddt=A, dA_log=A, dD=A, ddt_bias_=A, dstate_in=1 << 40, lddy=256, lddx=256,
+             lddb=128, lddc=128, ldddt=4)
+    g.update({k: v for k, v in kw.items() if k in g})
+    op = _operands(**{k: v for k, v in kw.items() if k not in g and k != "ldy"})
+    names = [n if n != "ddt_bias" else "ddt_bias_" for n in dfssm.SCAN_GRADIENTS + dfssm.SCAN_GRADIENT_SIZES]
+    grad = dfssm.ScanGradients(*[g[n] for n in names])
+    return _raw("dfssm_mamba2_scan_backward", None if null else ctypes.addressof(op),
+                None if no_gradients else ctypes.addressof(grad), ws, n, None)
+
+
+@pytest.mark.parametrize("kw,want", _SCAN + [
+    (dict(no_gradients=True), 1), (dict(dy=None), 1), (dict(dx=None), 1), (dict(dB=None), 1), (dict(dC=None), 1), (dict(ddt=None), 1),
+    (dict(dA_log=None), 1), (dict(dD=None), 1), (dict(ddt_bias_=None), 1), (dict(dy=A + 8), 1), (dict(dx=A + 4), 1),
+    (dict(dB=A + 8), 1), (dict(dC=A + 8), 1), (dict(ddt=A + 2), 1), (dict(dA_log=A + 1), 1), (dict(dD=A + 2), 1),
+    (dict(ddt_bias_=A + 2), 1), (dict(dstate_out=A + 8), 1), (dict(dstate_in=A + 16), 1), (dict(dstate_in=A), 1),
+    (dict(lddy=252), 1), (dict(lddx=258), 1), (dict(lddb=64), 1), (dict(lddc=130), 1), (dict(ldddt=3), 1), (dict(lddy=1 << 31), 2),
+    (dict(ldddt=1 << 31), 2),
+])
+def test_scan_backward_rejects(kw, want):
+    assert _scan_backward(**kw) == want
+
+
 def test_workspace_queries():
     from bit_scaffold_int8_amd import dfssm
     q = dfssm.dfssm_mamba2_scan_workspace_bytes
     assert q(0, 1, 1, 64, 128) == 0 and q(8, 1, 1, 32, 128) == 0 and q(8, 1, 4, 64, 128, 3) == 0
     assert dfssm.dfssm_mamba2_conv_backward_workspace_bytes(0, 1, 4) == 0
     base = (2048, 8, 64, 64, 64, 1)
+    b = dfssm.dfssm_mamba2_scan_backward_workspace_bytes
+    assert b(0, 1, 1, 64, 128) == 0 and b(*base) > q(*base)
     for i, more in ((0, 2049), (1, 9), (2, 65), (4, 128), (5, 2)):
         bigger = list(base)
         bigger[i] = more
-        assert q(*bigger) >= q(*base) > 0
+        assert q(*bigger) >= q(*base) > 0 and b(*bigger) >= b(*base)

@@ -173,9 +173,9 @@ __global__ __launch_bounds__(256) void prepare_kernel(ScanArgs a) {
     uint8_t* const out = a.groups + ((int64_t)c * a.G + g) * (kBackward ? Block::backward : Block::forward);
     const int r = lane & 15, q = lane >> 4;
     // eight values of a token's row / across the tokens
-    auto along = [&](int which, int tile, int step) {
+    auto along = [&](int which, int tile, int step, float sign = 1.0f) {
         const float* p = &rows[which][(tile * 16 + r) * kLd + step * 32 + 4 * q];
-        const v4f lo = *reinterpret_cast<const v4f*>(p), hi = *reinterpret_cast<const v4f*>(p + 16);
+        const v4f lo = sign * *reinterpret_cast<const v4f*>(p), hi = sign * *reinterpret_cast<const v4f*>(p + 16);
         const float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
         return split<kPieces>(v);
     };
@@ -192,9 +192,12 @@ __global__ __launch_bounds__(256) void prepare_kernel(ScanArgs a) {
         for (int ct = 0; ct < 4; ++ct) {
             if (kBackward ? ct > rt : ct < rt) continue;
             if ((n++ & 3) != wave) continue;
-            v4f acc = {0.0f, 0.0f, 0.0f, 0.0f};
-            for (int k = 0; k < kSteps; ++k) acc = mma(along(kRowSide, rt, k), along(1 - kRowSide, ct, k), acc);
-            *reinterpret_cast<v4f*>(out + ((rt * 4 + ct) * 64 + lane) * 16) = acc;
+            v4f acc[2] = {};
+            for (int k = 0; k < kSteps; k += 2) {
+                acc[0] = mma(along(kRowSide, rt, k), along(1 - kRowSide, ct, k), acc[0]);
+                acc[1] = mma(along(kRowSide, rt, k + 1, -1.0f), along(1 - kRowSide, ct, k + 1), acc[1]);
+            }
+            *reinterpret_cast<v4f*>(out + ((rt * 4 + ct) * 64 + lane) * 16) = opposite(acc);
         }
     for (int i = wave; i < 4 * kSteps; i += 4)
         store_pieces(out + Block::kRows + (i * 64 + lane) * 16, Block::kPlane, along(1 - kRowSide, i / kSteps, i % kSteps));
@@ -366,29 +369,37 @@ __global__ __launch_bounds__(kSweepThreads, 2) void sweep_kernel(SweepArgs s) {
         if (live) {
             const float last = arrays[kDecay * kChunk + kChunk - 1];
             through *= last;
-#pragma unroll
-            for (int n = 0; n < kTiles; ++n) {
-                h[n][0] *= last;
-                h[n][1] *= last;
-            }
+            // (the later half's weights are smaller in fast heads, and so are its errors: what is left changes its sign
+            // from chunk to chunk)
+            const float sign = c & 1 ? -1.0f : 1.0f;
+            Pieces<kIn> in[2][2];
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 const float* const from = arrays + (s.reverse ? kDecay : kWeight) * kChunk + k * 32 + 4 * q;
                 float w[8];
                 unpack(w, *reinterpret_cast<const v4f*>(from), *reinterpret_cast<const v4f*>(from + 16));
-                Pieces<kIn> in[2];
 #pragma unroll
                 for (int p = 0; p < 2; ++p) {
                     float f[8];
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) f[j] = v[k][p][j] * w[j];
-                    in[p] = split<kIn>(f);
+                    for (int j = 0; j < 8; ++j) f[j] = v[k][p][j] * (k ? -sign : sign) * w[j];
+                    in[k][p] = split<kIn>(f);
+                }
+            }
+#pragma unroll
+            for (int n = 0; n < kTiles; ++n) {
+                v4f add[2][2];
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const Pieces<kData> key = load_pieces<kData>(lds + ((n * 2 + k) * 64 + lane) * 16, Block::kPlane);
+                    add[0][k] = mma(key, in[k][0], v4f{0.0f, 0.0f, 0.0f, 0.0f});
+                    add[1][k] = mma(key, in[k][1], v4f{0.0f, 0.0f, 0.0f, 0.0f});
                 }
 #pragma unroll
-                for (int n = 0; n < kTiles; ++n) {
-                    const Pieces<kData> key = load_pieces<kData>(lds + ((n * 2 + k) * 64 + lane) * 16, Block::kPlane);
-                    h[n][0] = mma(key, in[0], h[n][0]);
-                    h[n][1] = mma(key, in[1], h[n][1]);
+                for (int p = 0; p < 2; ++p) {
+                    const v4f sum = opposite(add[p]);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) h[n][p][j] = fmaf(h[n][p][j], last, sign * sum[j]);
                 }
             }
         }

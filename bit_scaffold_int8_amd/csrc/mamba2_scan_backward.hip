@@ -53,9 +53,9 @@ struct GradLds {
     static constexpr int kData = kBf16 ? 1 : 3, kOut = kBf16 ? 2 : 3, kPlane = kChunk * kP * 2;
     static constexpr int kDy = 0, kX = kDy + kData * kPlane, kW = kX + kData * kPlane, kRows = kW + kOut * kPlane;
     static constexpr int kPart = kRows + kData * kChunk * kN * 2;       // floats
-    static constexpr int kRowSum = 0, kColSum = 4 * kChunk, kDiag = 6 * kChunk, kDot = 7 * kChunk, kU = 8 * kChunk,
-                         kV = kU + kN / 16 * kChunk, kPass = kV + kN / 16 * kChunk;
-    static constexpr int bytes = kPart + (kPass + 8) * 4;
+    static constexpr int kRowSum = 0, kColSum = 8 * kChunk, kDiag = 12 * kChunk, kDot = 13 * kChunk, kU = 14 * kChunk,
+                         kV = kU + kN / 16 * kChunk, kPass = kV + kN / 16 * kChunk;   // (the first two hold doubles)
+    static constexpr int bytes = kPart + (kPass + 16) * 4;
     static constexpr int kLdSum = kChunk + 4;                           // the heads' sum of M L dt, over dy, x and W
     static_assert(kChunk * kLdSum * 4 <= kRows, "it fits");
 };
@@ -65,6 +65,23 @@ __device__ __forceinline__ float row_sum(float v) {   // over the 16 lanes of a 
     v += dpp_f<kDppXor2>(v);
     v += dpp_f<kDppHalfMirror>(v);
     v += dpp_f<kDppMirror>(v);
+    return v;
+}
+
+// The same in fp64.  E's sums are: what da takes of them is the small difference of what all of a chunk's pairs add up to, and
+// its error is the same for many tokens, so that it stays in the sums over the tokens (dA_log of 2048 tokens against 64 bits:
+// 1.0e-6 with sums in fp32).
+template <int kCtrl>
+__device__ __forceinline__ double dpp_d(double v) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    return __builtin_bit_cast(double, (uint64_t)(uint32_t)dpp_i<kCtrl>((int)(uint32_t)(u >> 32)) << 32 |
+                                          (uint32_t)dpp_i<kCtrl>((int)(uint32_t)u));
+}
+__device__ __forceinline__ double row_sum(double v) {
+    v += dpp_d<kDppXor1>(v);
+    v += dpp_d<kDppXor2>(v);
+    v += dpp_d<kDppHalfMirror>(v);
+    v += dpp_d<kDppMirror>(v);
     return v;
 }
 
@@ -79,6 +96,9 @@ __global__ __launch_bounds__(kThreads, 2) void scan_grad_kernel(ScanGradArgs s) 
     constexpr int kTiles = kN / 16, kParts = 8 / kTiles, kTT = 4 / kParts, kSteps = kN / 32;
     __shared__ __attribute__((aligned(16))) uint8_t lds[Lds::bytes];
     float* const part = reinterpret_cast<float*>(lds + Lds::kPart);
+    double* const row_sums = reinterpret_cast<double*>(part + Lds::kRowSum);
+    double* const column_sums = reinterpret_cast<double*>(part + Lds::kColSum);
+    double* const passes = reinterpret_cast<double*>(part + Lds::kPass);
     const ScanArgs& a = s.a;
     const int slice = blockIdx.y % s.slices, g = blockIdx.y / s.slices, c = blockIdx.x;
     const int per_group = a.H / a.G, first = slice * s.per_slice;
@@ -139,8 +159,8 @@ __global__ __launch_bounds__(kThreads, 2) void scan_grad_kernel(ScanGradArgs s) 
             for (int j = 0; j < 4; ++j) {
                 y[j] = row < ch.y ? y0[j] : 0.0f;
                 y[j + 4] = row < ch.y ? y1[j] : 0.0f;
-                x[j] = row < ch.y ? x0[j] : 0.0f;
-                x[j + 4] = row < ch.y ? x1[j] : 0.0f;
+                x[j] = row < ch.y ? wave & 1 ? -x0[j] : x0[j] : 0.0f;   // (the second half negated: opposite())
+                x[j + 4] = row < ch.y ? wave & 1 ? -x1[j] : x1[j] : 0.0f;
             }
             store_pieces(lds + Lds::kDy + (wave * 64 + lane) * 16, kPlane, split<kData>(y));
             store_pieces(lds + Lds::kX + (wave * 64 + lane) * 16, kPlane, split<kData>(x));
@@ -151,26 +171,28 @@ __global__ __launch_bounds__(kThreads, 2) void scan_grad_kernel(ScanGradArgs s) 
         for (int i = 0; i < 2; ++i)
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                h_at[i][j] = h[(i * 32 + place(q, j)) * kN + nt * 16 + r];
+                const float v = h[(i * 32 + place(q, j)) * kN + nt * 16 + r];
+                h_at[i][j] = i ? -v : v;
                 dh_at[i][j] = dh[(i * 32 + place(q, j)) * kN + nt * 16 + r];
             }
         __syncthreads();
         {   // M, K L, E: columns s along the lanes
             const float s_hi = arrays[st * 16 + r], s_lo = arrays[kCsLo * kChunk + st * 16 + r], s_dt = arrays[kStep * kChunk + st * 16 + r];
-            float column = 0.0f;
+            double column = 0.0;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int tt = st + half + 2 * i;
                 if (tt >= 4) continue;
-                v4f m = {0.0f, 0.0f, 0.0f, 0.0f};
+                v4f both[2];
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
-                    m = mma(load_pieces<kData>(lds + Lds::kDy + ((tt * 2 + j) * 64 + lane) * 16, kPlane),
-                            load_pieces<kData>(lds + Lds::kX + ((st * 2 + j) * 64 + lane) * 16, kPlane), m);
+                    both[j] = mma(load_pieces<kData>(lds + Lds::kDy + ((tt * 2 + j) * 64 + lane) * 16, kPlane),
+                                  load_pieces<kData>(lds + Lds::kX + ((st * 2 + j) * 64 + lane) * 16, kPlane), v4f{0.0f, 0.0f, 0.0f, 0.0f});
+                const v4f m = opposite(both);
                 const v4f hi = *reinterpret_cast<const v4f*>(arrays + tt * 16 + 4 * q);
                 const v4f lo = *reinterpret_cast<const v4f*>(arrays + kCsLo * kChunk + tt * 16 + 4 * q);
                 float kl[8];
-                v4f rows;
+                double rows[4];
 #pragma unroll
                 for (int v = 0; v < 4; ++v) {
                     const bool on = tt > st || 4 * q + v >= r, strict = tt > st || 4 * q + v > r;
@@ -179,8 +201,8 @@ __global__ __launch_bounds__(kThreads, 2) void scan_grad_kernel(ScanGradArgs s) 
                     kl[v + 4] = 0.0f;
                     const float e = m[v] * kl[v];
                     sum_w[i][v] = fmaf(m[v] * f, s_dt, sum_w[i][v]);
-                    column += strict ? e : 0.0f;
-                    rows[v] = row_sum(strict ? e * s_dt : 0.0f);
+                    column += strict ? (double)e : 0.0;
+                    rows[v] = row_sum(strict ? (double)e * (double)s_dt : 0.0);
                     if (tt == st && 4 * q + v == r) {
                         part[Lds::kDiag + st * 16 + r] = e;
                         part[Lds::kDot + st * 16 + r] = m[v];
@@ -191,23 +213,27 @@ __global__ __launch_bounds__(kThreads, 2) void scan_grad_kernel(ScanGradArgs s) 
                 for (int n = 0; n < kOut; ++n)
                     *reinterpret_cast<v4bf*>(lds + Lds::kW + n * kPlane + ((st * 2 + (tt >> 1)) * 64 + lane) * 16 + (tt & 1) * 8) =
                         __builtin_shufflevector(w.p[n], w.p[n], 0, 1, 2, 3);
-                if (r == 0) *reinterpret_cast<v4f*>(part + Lds::kRowSum + st * kChunk + tt * 16 + 4 * q) = rows;
+                if (r == 0)
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) row_sums[st * kChunk + tt * 16 + 4 * q + v] = rows[v];
             }
             column += __shfl_xor(column, 16);
             column += __shfl_xor(column, 32);
-            if (q == 0) part[Lds::kColSum + half * kChunk + st * 16 + r] = column;
+            if (q == 0) column_sums[half * kChunk + st * 16 + r] = column;
         }
         {   // dC and dB through the states
             const Pieces<kFull> hp[2] = {split<kFull>(h_at[0]), split<kFull>(h_at[1])};
             const Pieces<kFull> dhp[2] = {split<kFull>(dh_at[0]), split<kFull>(dh_at[1])};
 #pragma unroll
             for (int t = 0; t < kTT; ++t) {
-                v4f u = {0.0f, 0.0f, 0.0f, 0.0f}, w = u;
+                v4f us_[2], ws_[2];
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    u = mma(load_pieces<kData>(lds + Lds::kDy + (((t0 + t) * 2 + j) * 64 + lane) * 16, kPlane), hp[j], u);
-                    w = mma(load_pieces<kData>(lds + Lds::kX + (((t0 + t) * 2 + j) * 64 + lane) * 16, kPlane), dhp[j], w);
+                    const v4f zero = {0.0f, 0.0f, 0.0f, 0.0f};
+                    us_[j] = mma(load_pieces<kData>(lds + Lds::kDy + (((t0 + t) * 2 + j) * 64 + lane) * 16, kPlane), hp[j], zero);
+                    ws_[j] = mma(load_pieces<kData>(lds + Lds::kX + (((t0 + t) * 2 + j) * 64 + lane) * 16, kPlane), dhp[j], zero);
                 }
+                const v4f u = opposite(us_), w = opposite(ws_);
                 acc_c[t] += u * *reinterpret_cast<const v4f*>(arrays + kDecay * kChunk + (t0 + t) * 16 + 4 * q);
                 acc_b[t] += w * *reinterpret_cast<const v4f*>(arrays + kWeight * kChunk + (t0 + t) * 16 + 4 * q);
                 v4f us, ws;
@@ -221,15 +247,15 @@ __global__ __launch_bounds__(kThreads, 2) void scan_grad_kernel(ScanGradArgs s) 
                     *reinterpret_cast<v4f*>(part + Lds::kV + nt * kChunk + (t0 + t) * 16 + 4 * q) = ws;
                 }
             }
-            float pass = 0.0f;
+            double pass = 0.0;
 #pragma unroll
             for (int i = 0; i < 2; ++i)
 #pragma unroll
-                for (int j = 0; j < 8; ++j) pass = fmaf(h_at[i][j], dh_at[i][j], pass);
+                for (int j = 0; j < 8; ++j) pass += (double)(i ? -h_at[i][j] : h_at[i][j]) * (double)dh_at[i][j];
             pass = row_sum(pass);
             pass += __shfl_xor(pass, 16);
             pass += __shfl_xor(pass, 32);
-            if (lane == 0) part[Lds::kPass + wave] = t0 == 0 ? pass : 0.0f;
+            if (lane == 0) passes[wave] = t0 == 0 ? pass : 0.0;
         }
         __syncthreads();
         {   // dx
@@ -282,22 +308,24 @@ __global__ __launch_bounds__(kThreads, 2) void scan_grad_kernel(ScanGradArgs s) 
         if (wave == (k & 7)) {   // ddt and the parameters' sums, a token a lane
             const float hi = arrays[lane], lo = arrays[kCsLo * kChunk + lane], dt = arrays[kStep * kChunk + lane];
             const float end_hi = arrays[kChunk - 1], end_lo = arrays[kCsLo * kChunk + kChunk - 1];
-            float rows = 0.0f, u = 0.0f, v = 0.0f, pass = 0.0f;
-            for (int i = 0; i <= lane >> 4; ++i) rows += part[Lds::kRowSum + i * kChunk + lane];
+            double rows = 0.0;
+            float u = 0.0f, v = 0.0f;
+            double pass = 0.0;
+            for (int i = 0; i <= lane >> 4; ++i) rows += row_sums[i * kChunk + lane];
 #pragma unroll
             for (int i = 0; i < kTiles; ++i) {
                 u += part[Lds::kU + i * kChunk + lane];
                 v += part[Lds::kV + i * kChunk + lane];
             }
 #pragma unroll
-            for (int i = 0; i < 8; ++i) pass += part[Lds::kPass + i];
-            const float columns = part[Lds::kColSum + lane] + part[Lds::kColSum + kChunk + lane];
+            for (int i = 0; i < 8; ++i) pass += passes[i];
+            const double columns = column_sums[lane] + column_sums[kChunk + lane];
             u *= arrays[kDecay * kChunk + lane];
             v *= __builtin_amdgcn_exp2f((end_hi - hi) + (end_lo - lo));
             pass *= arrays[kDecay * kChunk + kChunk - 1];
-            const float z = columns + part[Lds::kDiag + lane] + v;    // x . (dh B)
+            const float z = (float)columns + part[Lds::kDiag + lane] + v;    // x . (dh B)
             // from t on: rows of E and u, less the columns from t on (pairs that lie behind t whole); before t: v
-            double from = (double)rows + (double)u - (double)(dt * columns), before = (double)(dt * v);
+            double from = rows + (double)u - (double)dt * columns, before = (double)dt * (double)v;
             const double own = before;
 #pragma unroll
             for (int d = 1; d < 64; d <<= 1) {
@@ -305,7 +333,7 @@ __global__ __launch_bounds__(kThreads, 2) void scan_grad_kernel(ScanGradArgs s) 
                 if (lane + d < 64) from += o;
                 if (lane >= d) before += p;
             }
-            const float da = (float)(from + (before - own) + (double)pass);
+            const float da = (float)(from + (before - own) + pass);
             const float rate = expf(a.A_log[head]);
             float raw = 0.0f, ddt = 0.0f;
             if (lane < ch.y) {

@@ -405,10 +405,10 @@ dfssm_status scan_sizes(int64_t T, int64_t S, int64_t H, int64_t P, int64_t N, i
     return DFSSM_OK;
 }
 
-// Rows that are read in pieces of 16 bytes.
+// Rows that are read in pieces of 16 bytes; 64 of them stay below 2^31 bytes.
 dfssm_status wide_rows(const void* p, int64_t ld, int64_t row, int32_t type) {
-    if (!aligned16(p) || ld % (type == DFSSM_BF16 ? 8 : 4) != 0) return DFSSM_ERR_INVALID_ARG;
-    return stride_ok(ld, row);
+    if (!aligned16(p) || ld % (type == DFSSM_BF16 ? 8 : 4) != 0 || ld < row) return DFSSM_ERR_INVALID_ARG;
+    return ld > kMaxStride ? DFSSM_ERR_UNSUPPORTED : DFSSM_OK;
 }
 
 dfssm_status scan_operands(const dfssm_mamba2_scan_operands* op, dfssm::ScanArgs& a) {

@@ -233,7 +233,7 @@ __global__ __launch_bounds__(kSweepThreads, 2) void sweep_kernel(SweepArgs s) {
     constexpr int kData = kBf16 ? 1 : 3, kOut = kBf16 ? 2 : 3, kIn = 3;
     constexpr int kTiles = kN / 16, kSteps = kN / 32;
     using Block = GroupBlock<kN, kData>;
-    using E = Elem<kBf16>;
+    constexpr int kSize = RowBuffer<kBf16>::kSize;
     __shared__ __attribute__((aligned(16))) uint8_t lds[Block::kSet];
     const ScanArgs& a = s.a;
     const int per_group = a.H / a.G, pairs = (per_group + 1) / 2;
@@ -279,18 +279,14 @@ __global__ __launch_bounds__(kSweepThreads, 2) void sweep_kernel(SweepArgs s) {
         }
         // the chunk's rows of v, places of the sums along its tokens; zero behind the sequence
         float v[2][2][8];
+        const RowBuffer<kBf16> rows(s.v, ch.x, s.ldv, ch.y, head * kP + half * 32, 32);
+        const int own = opaque(4 * q * (int)s.ldv + r) * kSize;
 #pragma unroll
         for (int k = 0; k < 2; ++k)
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int row = k * 32 + place(q, j), there = row < ch.y ? row : 0;
-                const auto* at = static_cast<const typename E::type*>(s.v) + (int64_t)(ch.x + there) * s.ldv + head * kP + p0;
+            for (int j = 0; j < 8; ++j)
 #pragma unroll
-                for (int p = 0; p < 2; ++p) {
-                    const float x = E::load(at + p * 16);
-                    v[k][p][j] = row < ch.y ? x : 0.0f;
-                }
-            }
+                for (int p = 0; p < 2; ++p) v[k][p][j] = rows.load(own + (k * 32 + place(0, j)) * (int)s.ldv * kSize + p * 16 * kSize);
         if constexpr (kMode == kOutput) {
             stage<Block::kSet>(block + Block::kRows, lds);
             __syncthreads();
@@ -349,17 +345,16 @@ __global__ __launch_bounds__(kSweepThreads, 2) void sweep_kernel(SweepArgs s) {
                         y[t][1] = mma(wp, x[1], y[t][1]);
                     }
                 }
+                const RowBuffer<kBf16> out(s.y, ch.x, s.ldy, ch.y, head * kP + half * 32, 32);
+                const int to = opaque(4 * q * (int)s.ldy + r) * kSize;
 #pragma unroll
                 for (int t = 0; t < 4; ++t)
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        const int row = t * 16 + 4 * q + j;
-                        auto* at = static_cast<typename E::type*>(s.y) + (int64_t)(ch.x + row) * s.ldy + head * kP + p0;
-                        if (row < ch.y) {
 #pragma unroll
-                            for (int p = 0; p < 2; ++p)
-                                E::store(at + p * 16, fmaf(skip, v[t >> 1][p][(t & 1) * 4 + j], y[t][p][j]));
-                        }
+                        for (int p = 0; p < 2; ++p)
+                            out.store(fmaf(skip, v[t >> 1][p][(t & 1) * 4 + j], y[t][p][j]),
+                                      to + (t * 16 + j) * (int)s.ldy * kSize + p * 16 * kSize);
                     }
             }
             __syncthreads();

@@ -91,6 +91,7 @@ __global__ __launch_bounds__(kThreads, 2) void scan_grad_kernel(ScanGradArgs s) 
     using Block = GroupBlock<kN, Lds::kData>;
     using E = Elem<kBf16>;
     using T = typename E::type;
+    constexpr int kSize = RowBuffer<kBf16>::kSize;
     constexpr int kData = Lds::kData, kOut = Lds::kOut, kFull = 3, kPlane = Lds::kPlane;
     // a wave's part of dB and dC: one tile of 16 state places, kTT tiles of tokens
     constexpr int kTiles = kN / 16, kParts = 8 / kTiles, kTT = 4 / kParts, kSteps = kN / 32;
@@ -115,7 +116,7 @@ __global__ __launch_bounds__(kThreads, 2) void scan_grad_kernel(ScanGradArgs s) 
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const uint8_t* const block = a.groups + ((int64_t)c * a.G + g) * s.group_bytes;
 
-    // what stays for all heads: B's rows in LDS; K's tiles of this wave, and B and C at the places of its part of dB and dC
+    // what stays for all heads: B's rows in LDS, and K's tiles of this wave
     for (int i = tid; i < Block::kSet / 16; i += kThreads)
         *reinterpret_cast<v4i*>(lds + Lds::kRows + i * 16) = *reinterpret_cast<const v4i*>(block + Block::kRows + i * 16);
     for (int i = tid; i < kOut * kPlane / 16; i += kThreads)    // (tiles above the diagonal stay zero)
@@ -129,19 +130,10 @@ __global__ __launch_bounds__(kThreads, 2) void scan_grad_kernel(ScanGradArgs s) 
         if (tt < 4) products[i] = *reinterpret_cast<const v4f*>(block + ((tt * 4 + st) * 64 + lane) * 16);
     }
     const int nt = wave % kTiles, t0 = wave / kTiles * kTT;
-    v4f b_at[kTT], c_at[kTT], acc_b[kTT], acc_c[kTT];
+    const RowBuffer<kBf16> b_rows(a.B, ch.x, a.ldb, ch.y, g * kN + nt * 16, 16), c_rows(a.C, ch.x, a.ldc, ch.y, g * kN + nt * 16, 16);
+    v4f acc_b[kTT], acc_c[kTT];
 #pragma unroll
-    for (int t = 0; t < kTT; ++t) {
-        acc_b[t] = acc_c[t] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int v = 0; v < 4; ++v) {
-            const int row = (t0 + t) * 16 + 4 * q + v, there = row < ch.y ? row : 0;
-            const float bv = E::load(static_cast<const T*>(a.B) + (int64_t)(ch.x + there) * a.ldb + g * kN + nt * 16 + r);
-            const float cv = E::load(static_cast<const T*>(a.C) + (int64_t)(ch.x + there) * a.ldc + g * kN + nt * 16 + r);
-            b_at[t][v] = row < ch.y ? bv : 0.0f;
-            c_at[t][v] = row < ch.y ? cv : 0.0f;
-        }
-    }
+    for (int t = 0; t < kTT; ++t) acc_b[t] = acc_c[t] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
     const int pt = wave & 3, sh = wave >> 2;          // dx's tiles: channels pt, tokens 2 sh and 2 sh + 1
 
     for (int k = first; k < last; ++k) {
@@ -150,30 +142,32 @@ __global__ __launch_bounds__(kThreads, 2) void scan_grad_kernel(ScanGradArgs s) 
         const float* const h = s.starts + ((int64_t)c * a.H + head) * kP * kN;
         const float* const dh = s.ends + ((int64_t)c * a.H + head) * kP * kN;
         {   // dy and x as pieces along the channels: each wave one tile of rows and one step
-            const int row = (wave >> 1) * 16 + r, there = row < ch.y ? row : 0, p = head * kP + (wave & 1) * 32 + 4 * q;
-            const T* const from_dy = static_cast<const T*>(s.dy) + (int64_t)(ch.x + there) * s.lddy + p;
-            const T* const from_x = static_cast<const T*>(a.x) + (int64_t)(ch.x + there) * a.ldx + p;
-            const v4f y0 = E::load4(from_dy), y1 = E::load4(from_dy + 16), x0 = E::load4(from_x), x1 = E::load4(from_x + 16);
+            const int p = head * kP + (wave & 1) * 32, row = opaque((wave >> 1) * 16 + r);
+            const RowBuffer<kBf16> dy_rows(s.dy, ch.x, s.lddy, ch.y, p, 32), x_rows(a.x, ch.x, a.ldx, ch.y, p, 32);
+            const int from_dy = (row * (int)s.lddy + 4 * q) * kSize, from_x = (row * (int)a.ldx + 4 * q) * kSize;
+            const v4f y0 = dy_rows.load4(from_dy), y1 = dy_rows.load4(from_dy + 16 * kSize);
+            const v4f x0 = x_rows.load4(from_x), x1 = x_rows.load4(from_x + 16 * kSize);
             float y[8], x[8];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                y[j] = row < ch.y ? y0[j] : 0.0f;
-                y[j + 4] = row < ch.y ? y1[j] : 0.0f;
-                x[j] = row < ch.y ? wave & 1 ? -x0[j] : x0[j] : 0.0f;   // (the second half negated: opposite())
-                x[j + 4] = row < ch.y ? wave & 1 ? -x1[j] : x1[j] : 0.0f;
+                y[j] = y0[j];
+                y[j + 4] = y1[j];
+                x[j] = wave & 1 ? -x0[j] : x0[j];   // (the second half negated: opposite())
+                x[j + 4] = wave & 1 ? -x1[j] : x1[j];
             }
             store_pieces(lds + Lds::kDy + (wave * 64 + lane) * 16, kPlane, split<kData>(y));
             store_pieces(lds + Lds::kX + (wave * 64 + lane) * 16, kPlane, split<kData>(x));
         }
         // the states at this wave's places, across the channels
         float h_at[2][8], dh_at[2][8];
+        const int from_h = opaque(4 * q * kN + nt * 16 + r);
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const float v = h[(i * 32 + place(q, j)) * kN + nt * 16 + r];
+                const float v = h[from_h + (i * 32 + place(0, j)) * kN];
                 h_at[i][j] = i ? -v : v;
-                dh_at[i][j] = dh[(i * 32 + place(q, j)) * kN + nt * 16 + r];
+                dh_at[i][j] = dh[from_h + (i * 32 + place(0, j)) * kN];
             }
         __syncthreads();
         {   // M, K L, E: columns s along the lanes
@@ -216,12 +210,15 @@ __global__ __launch_bounds__(kThreads, 2) void scan_grad_kernel(ScanGradArgs s) 
                 if (r == 0)
 #pragma unroll
                     for (int v = 0; v < 4; ++v) row_sums[st * kChunk + tt * 16 + 4 * q + v] = rows[v];
+                __builtin_amdgcn_sched_barrier(0);
             }
             column += __shfl_xor(column, 16);
             column += __shfl_xor(column, 32);
             if (q == 0) column_sums[half * kChunk + st * 16 + r] = column;
         }
+        __builtin_amdgcn_sched_barrier(0);
         {   // dC and dB through the states
+            const int from_c = opaque(4 * q * (int)a.ldc + r) * kSize, from_b = opaque(4 * q * (int)a.ldb + r) * kSize;
             const Pieces<kFull> hp[2] = {split<kFull>(h_at[0]), split<kFull>(h_at[1])};
             const Pieces<kFull> dhp[2] = {split<kFull>(dh_at[0]), split<kFull>(dh_at[1])};
 #pragma unroll
@@ -239,13 +236,14 @@ __global__ __launch_bounds__(kThreads, 2) void scan_grad_kernel(ScanGradArgs s) 
                 v4f us, ws;
 #pragma unroll
                 for (int v = 0; v < 4; ++v) {
-                    us[v] = row_sum(u[v] * c_at[t][v]);
-                    ws[v] = row_sum(w[v] * b_at[t][v]);
+                    us[v] = row_sum(u[v] * c_rows.load(from_c + ((t0 + t) * 16 + v) * (int)a.ldc * kSize));
+                    ws[v] = row_sum(w[v] * b_rows.load(from_b + ((t0 + t) * 16 + v) * (int)a.ldb * kSize));
                 }
                 if (r == 0) {
                     *reinterpret_cast<v4f*>(part + Lds::kU + nt * kChunk + (t0 + t) * 16 + 4 * q) = us;
                     *reinterpret_cast<v4f*>(part + Lds::kV + nt * kChunk + (t0 + t) * 16 + 4 * q) = ws;
                 }
+                __builtin_amdgcn_sched_barrier(0);
             }
             double pass = 0.0;
 #pragma unroll
@@ -259,21 +257,20 @@ __global__ __launch_bounds__(kThreads, 2) void scan_grad_kernel(ScanGradArgs s) 
         }
         __syncthreads();
         {   // dx
+            const RowBuffer<kBf16> dy_rows(s.dy, ch.x, s.lddy, ch.y, head * kP + pt * 16, 16);
+            const int from_dy = opaque(4 * q * (int)s.lddy + r) * kSize;
+            const int from_dh = opaque((pt * 16 + r) * kN + 4 * q);
             float dy[2][8];
 #pragma unroll
             for (int i = 0; i < 2; ++i)
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const int row = i * 32 + place(q, j), there = row < ch.y ? row : 0;
-                    const float v = E::load(static_cast<const T*>(s.dy) + (int64_t)(ch.x + there) * s.lddy + head * kP + pt * 16 + r);
-                    dy[i][j] = row < ch.y ? v : 0.0f;
-                }
+                for (int j = 0; j < 8; ++j) dy[i][j] = dy_rows.load(from_dy + (i * 32 + place(0, j)) * (int)s.lddy * kSize);
             v4f inter[2], intra[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) inter[i] = intra[i] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
             for (int n = 0; n < kSteps; ++n) {
-                const float* const from = dh + (pt * 16 + r) * kN + n * 32 + 4 * q;
+                const float* const from = dh + from_dh + n * 32;
                 const v4f lo = *reinterpret_cast<const v4f*>(from), hi = *reinterpret_cast<const v4f*>(from + 16);
                 const float f[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
                 const Pieces<kOut> state = split<kOut>(f);
@@ -281,6 +278,7 @@ __global__ __launch_bounds__(kThreads, 2) void scan_grad_kernel(ScanGradArgs s) 
                 for (int i = 0; i < 2; ++i)
                     inter[i] = mma(load_pieces<kData>(lds + Lds::kRows + (((2 * sh + i) * kSteps + n) * 64 + lane) * 16, Block::kPlane),
                                    state, inter[i]);
+                __builtin_amdgcn_sched_barrier(0);
             }
             const Pieces<kData> rows[2] = {split<kData>(dy[0]), split<kData>(dy[1])};
 #pragma unroll
@@ -290,6 +288,8 @@ __global__ __launch_bounds__(kThreads, 2) void scan_grad_kernel(ScanGradArgs s) 
                     if (j >= sh)     // (tokens t from the tile's own on)
                         intra[i] = mma(load_pieces<kOut>(lds + Lds::kW + (((2 * sh + i) * 2 + j) * 64 + lane) * 16, kPlane), rows[j], intra[i]);
             const float skip = a.D[head];
+            const RowBuffer<kBf16> dx_rows(s.dx, ch.x, s.lddx, ch.y, head * kP + pt * 16, 16);
+            const int to = opaque(4 * q * (int)s.lddx + r) * kSize;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int tile = 2 * sh + i;
@@ -297,14 +297,13 @@ __global__ __launch_bounds__(kThreads, 2) void scan_grad_kernel(ScanGradArgs s) 
                 const v4f weight = *reinterpret_cast<const v4f*>(arrays + kWeight * kChunk + tile * 16 + 4 * q);
 #pragma unroll
                 for (int v = 0; v < 4; ++v) {
-                    const int row = tile * 16 + 4 * q + v;
                     const float own = sh == 0 ? dy[0][i * 4 + v] : dy[1][i * 4 + v];
-                    if (row < ch.y)
-                        E::store(static_cast<T*>(s.dx) + (int64_t)(ch.x + row) * s.lddx + head * kP + pt * 16 + r,
-                                 fmaf(skip, own, fmaf(dt[v], intra[i][v], weight[v] * inter[i][v])));
+                    dx_rows.store(fmaf(skip, own, fmaf(dt[v], intra[i][v], weight[v] * inter[i][v])),
+                                  to + (tile * 16 + v) * (int)s.lddx * kSize);
                 }
             }
         }
+        __builtin_amdgcn_sched_barrier(0);
         if (wave == (k & 7)) {   // ddt and the parameters' sums, a token a lane
             const float hi = arrays[lane], lo = arrays[kCsLo * kChunk + lane], dt = arrays[kStep * kChunk + lane];
             const float end_hi = arrays[kChunk - 1], end_lo = arrays[kCsLo * kChunk + kChunk - 1];

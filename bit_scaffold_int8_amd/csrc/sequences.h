@@ -68,4 +68,39 @@ struct Elem<true> {
     }
 };
 
+// A chunk's rows of a matrix, from column `col` on, as a buffer: what lies past the last row's `width` elements reads as zero and
+// is not written, so rows behind a sequence need no branch, and offsets are 32 bits (row strides of up to 2^22 elements).
+template <bool kBf16>
+struct RowBuffer {
+    __amdgpu_buffer_rsrc_t rsrc;
+    static constexpr int kSize = kBf16 ? 2 : 4;
+    __device__ __forceinline__ RowBuffer(const void* base, int64_t first, int64_t ld, int rows, int col, int width)
+        : rsrc(make_rsrc(static_cast<const uint8_t*>(base) + (first * ld + col) * kSize,
+                         (uint32_t)(((rows - 1) * (uint32_t)ld + (uint32_t)width) * kSize))) {}
+    __device__ __forceinline__ float load(int bytes) const {
+        if constexpr (kBf16) return __uint_as_float((uint32_t)(uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rsrc, bytes, 0, 0) << 16);
+        else return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rsrc, bytes, 0, 0));
+    }
+    __device__ __forceinline__ v4f load4(int bytes) const {
+        if constexpr (kBf16) {
+            const auto v = __builtin_amdgcn_raw_buffer_load_b64(rsrc, bytes, 0, 0);
+            return {__uint_as_float(v[0] << 16), __uint_as_float(v[0] & 0xFFFF0000u), __uint_as_float(v[1] << 16),
+                    __uint_as_float(v[1] & 0xFFFF0000u)};
+        } else {
+            return __builtin_bit_cast(v4f, __builtin_amdgcn_raw_buffer_load_b128(rsrc, bytes, 0, 0));
+        }
+    }
+    __device__ __forceinline__ void store(float v, int bytes) const {
+        if constexpr (kBf16) __builtin_amdgcn_raw_buffer_store_b16((uint16_t)bf16_bits(v), rsrc, bytes, 0, 0);
+        else __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v), rsrc, bytes, 0, 0);
+    }
+};
+
+// A lane's offset that the optimizer takes as new: what is computed from it is not kept in registers from one turn of a loop
+// to the next (an empty asm statement emits no instruction).
+__device__ __forceinline__ int opaque(int v) {
+    asm volatile("" : "+v"(v));
+    return v;
+}
+
 }  // namespace dfssm

@@ -687,7 +687,7 @@ typedef struct dfssm_mamba2_scan_operands {
  * Errors: DFSSM_ERR_INVALID_ARG for a NULL or misaligned pointer, sizes <= 0 or >= 2^31, nheads % ngroups != 0, T % S != 0
  * without offsets, strides shorter than a row, a type that is none, a short workspace;
  * DFSSM_ERR_UNSUPPORTED unless headdim == 64, d_state == 64 or 128, nheads <= 1024, T <= 2^20, S <= 65535, S * nheads <= 2^21,
- * (T / 64 + S) * (nheads + 4 ngroups) <= 2^25 and strides < 2^31.  The size query returns 0 for sizes that the
+ * (T / 64 + S) * (nheads + 4 ngroups) <= 2^25, strides <= 2^22 and lddt < 2^31.  The size query returns 0 for sizes that the
  * call refuses, and never falls as one grows.
  */
 size_t dfssm_mamba2_scan_workspace_bytes(int64_t T, int64_t S, int64_t nheads, int64_t headdim, int64_t d_state,

@@ -26,22 +26,15 @@ namespace dfssm {
 namespace {
 
 constexpr double kLog2eD = 1.4426950408889634074;
-constexpr int kSweepThreads = 256;
-
-__device__ __forceinline__ int4 chunk_of(const ScanArgs& a, int c) {
-    if (a.chunks) return a.chunks[c];
-    const int per = (a.seq.L + kChunk - 1) / kChunk, s = c / per, i = c - s * per;
-    const int left = a.seq.L - i * kChunk;
-    return make_int4(s * a.seq.L + i * kChunk, left < kChunk ? left : kChunk, s, 0);
-}
+constexpr int kSweepWaves = 8, kSweepThreads = kSweepWaves * 64, kSweepHeads = kSweepWaves / 2;
 
 // w: 1 the sequence's first segment, 2 its last
 __device__ __forceinline__ int4 segment_of(const ScanArgs& a, int g) {
-    if (a.segments) return a.segments[g];
+    if (a.segments) return uniform(a.segments[g]);
     const int chunks = (a.seq.L + kChunk - 1) / kChunk, per = (chunks + a.per_segment - 1) / a.per_segment;
     const int s = g / per, i = g - s * per, left = chunks - i * a.per_segment;
-    return make_int4(s * chunks + i * a.per_segment, left < a.per_segment ? left : a.per_segment, s,
-                     (i == 0 ? 1 : 0) | (i == per - 1 ? 2 : 0));
+    return uniform(make_int4(s * chunks + i * a.per_segment, left < a.per_segment ? left : a.per_segment, s,
+                             (i == 0 ? 1 : 0) | (i == per - 1 ? 2 : 0)));
 }
 
 // ---------------------------------------------------------------- the tables of packed sequences
@@ -143,6 +136,9 @@ __device__ void head_arrays(const ScanArgs& a, const int4& ch, int c, int h) {
     out[kStep * kChunk] = dt;
     out[kWeight * kChunk] = dt * __builtin_amdgcn_exp2f((float)(end - cs));
     out[kDecay * kChunk] = __builtin_amdgcn_exp2f(hi);
+    const double before = __shfl(cs, lane < 16 ? 0 : (lane & 48) - 1), behind = __shfl(cs, lane | 15);
+    out[kEnter * kChunk] = __builtin_amdgcn_exp2f((float)(cs - (lane < 16 ? 0.0 : before)));
+    out[kLeave * kChunk] = dt * __builtin_amdgcn_exp2f((float)(behind - cs));
 }
 
 // Workgroups (chunk, y): y below G the group's products and pieces, behind them the decays of four heads each.
@@ -210,45 +206,75 @@ __global__ __launch_bounds__(256) void prepare_kernel(ScanArgs a) {
 
 // ---------------------------------------------------------------- the sweep
 
-// A set of pieces from memory to LDS.
+// A part of what the heads share on its way from memory through registers to LDS: loaded while something else is worked on,
+// written when that is done.  (Loads straight to LDS would cost no registers, but the compiler lets no later read of LDS
+// pass one.)  Past the buffer it is zero.
 template <int kBytes>
-__device__ __forceinline__ void stage(const uint8_t* from, uint8_t* lds) {
-    constexpr int kEach = kBytes / (kSweepThreads * 16);
-    static_assert(kEach * kSweepThreads * 16 == kBytes, "whole pieces of 16 bytes a thread");
+struct Staged {
+    static constexpr int kEach = (kBytes + kSweepThreads * 16 - 1) / (kSweepThreads * 16);
     v4i v[kEach];
+    __device__ __forceinline__ void load(const void* from, uint32_t bytes) {
+        const __amdgpu_buffer_rsrc_t rsrc = make_rsrc(from, bytes);
 #pragma unroll
-    for (int i = 0; i < kEach; ++i) v[i] = *reinterpret_cast<const v4i*>(from + (i * kSweepThreads + threadIdx.x) * 16);
+        for (int i = 0; i < kEach; ++i)
+            v[i] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(rsrc, (i * kSweepThreads + (int)threadIdx.x) * 16, 0, 0));
+    }
+    __device__ __forceinline__ void store(uint8_t* lds) const {
 #pragma unroll
-    for (int i = 0; i < kEach; ++i) *reinterpret_cast<v4i*>(lds + (i * kSweepThreads + threadIdx.x) * 16) = v[i];
-}
+        for (int i = 0; i < kEach; ++i)
+            if (kBytes % (kSweepThreads * 16) == 0 || (i * kSweepThreads + (int)threadIdx.x) * 16 < kBytes)
+                *reinterpret_cast<v4i*>(lds + (i * kSweepThreads + threadIdx.x) * 16) = v[i];
+    }
+};
 
 __device__ __forceinline__ void unpack(float (&f)[8], v4f lo, v4f hi) {
     f[0] = lo.x, f[1] = lo.y, f[2] = lo.z, f[3] = lo.w, f[4] = hi.x, f[5] = hi.y, f[6] = hi.z, f[7] = hi.w;
 }
+__device__ __forceinline__ v4f at4(const float* p) { return *reinterpret_cast<const v4f*>(p); }
 
+// A workgroup: four heads of a group, a wave 32 channels of one.  A lane's two tiles of 16 channels hold the even and the
+// odd ones, so that it reads and writes quads.  What the heads share of a chunk comes to LDS in two parts, each loaded
+// while the other is worked on: products and C (for y), then B across the tokens (for the state); without y, B's
+// part of the next chunk.
 template <bool kBf16, int kN, int kMode>
 __global__ __launch_bounds__(kSweepThreads, 2) void sweep_kernel(SweepArgs s) {
     // pieces of the data; of the state and of the chunk's own products where y is bf16: two leave an error of 2^-17, far
     // below its rounding; of what goes into the state, which is fp32 whatever the data: three
-    constexpr int kData = kBf16 ? 1 : 3, kOut = kBf16 ? 2 : 3, kIn = 3;
-    constexpr int kTiles = kN / 16, kSteps = kN / 32;
+    constexpr int kData = kBf16 ? 1 : 3, kOut = kBf16 ? 2 : 3, kInto = 3;
+    constexpr int kTiles = kN / 16, kSteps = kN / 32, kSize = RowBuffer<kBf16>::kSize;
     using Block = GroupBlock<kN, kData>;
-    constexpr int kSize = RowBuffer<kBf16>::kSize;
-    __shared__ __attribute__((aligned(16))) uint8_t lds[Block::kSet];
+    constexpr bool kY = kMode == kOutput;
+    constexpr int kFirst = Block::kG + Block::kSet, kArrays = kSweepHeads * kHeadArrays * kChunk * 4;
+    static_assert(Block::kRows == Block::kG, "the products and C's rows lie side by side");
+    __shared__ __attribute__((aligned(16))) uint8_t first_lds[kY ? kFirst : Block::kSet];
+    __shared__ __attribute__((aligned(16))) uint8_t key_lds[Block::kSet];
+    __shared__ __attribute__((aligned(16))) uint8_t head_lds[2][kArrays];
     const ScanArgs& a = s.a;
-    const int per_group = a.H / a.G, pairs = (per_group + 1) / 2;
-    const int seg = blockIdx.x / (a.G * pairs), rest = blockIdx.x % (a.G * pairs);
-    const int g = rest / pairs, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-    const int in_group = rest % pairs * 2 + (wave >> 1), half = wave & 1;
-    const bool live = in_group < per_group;      // (an odd group's last pair is one head)
-    const int head = g * per_group + (live ? in_group : 0);
+    const int per_group = a.H / a.G, quads = (per_group + kSweepHeads - 1) / kSweepHeads;
+    const int seg = blockIdx.x / (a.G * quads), rest = blockIdx.x % (a.G * quads);
+    const int g = rest / quads, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    const int head0 = rest % quads * kSweepHeads, in_group = head0 + (wave >> 1), half = wave & 1;
+    const bool live = in_group < per_group;      // (the last heads of a group may not fill a workgroup)
+    const int head = g * per_group + (live ? in_group : head0);
+    const uint32_t array_bytes = (uint32_t)((per_group - head0 < kSweepHeads ? per_group - head0 : kSweepHeads) * kHeadArrays * kChunk * 4);
     const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
     const int4 sg = segment_of(a, seg);
     if (sg.z < 0) return;
-    const int p0 = half * 32 + r;                // the lane's channel of the first of two tiles
+    const int p0 = half * 32 + 2 * r;            // the lane's first channel
 
+    auto chunk_at = [&](int i) { return s.reverse ? sg.x + sg.y - 1 - i : sg.x + i; };
+    auto block_of = [&](int c) { return a.groups + ((int64_t)c * a.G + g) * s.group_bytes; };
+    Staged<kArrays> next_arrays;
+    Staged<kFirst> next_first;
+    Staged<Block::kSet> next_key;
+    auto load_arrays = [&](int i) {
+        next_arrays.load(a.heads + ((int64_t)chunk_at(i) * a.H + g * per_group + head0) * kHeadArrays * kChunk, array_bytes);
+    };
+
+    // The state as sigma h.  The matrix instructions round down; with sigma changing from chunk to chunk their errors do, too.
     v4f h[kTiles][2];
     const int64_t mine = ((int64_t)sg.z * a.H + head) * kP * kN;
+    float sigma = sg.x & 1 ? -1.0f : 1.0f;
     v4f* const slot = s.segment_states ? reinterpret_cast<v4f*>(s.segment_states) +
                                              (((int64_t)seg * a.H + head) * 2 + half) * kTiles * 2 * 64 + lane : nullptr;
 #pragma unroll
@@ -257,162 +283,193 @@ __global__ __launch_bounds__(kSweepThreads, 2) void sweep_kernel(SweepArgs s) {
         for (int p = 0; p < 2; ++p) {
             h[n][p] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
             if constexpr (kMode != kLocal) {
-                if (slot) h[n][p] = slot[(n * 2 + p) * 64];
-                else if (s.start) h[n][p] = *reinterpret_cast<const v4f*>(s.start + mine + (p0 + p * 16) * kN + n * 16 + 4 * q);
+                if (slot) h[n][p] = sigma * slot[(n * 2 + p) * 64];
+                else if (s.start) h[n][p] = sigma * at4(s.start + mine + (p0 + p) * kN + n * 16 + 4 * q);
             }
         }
     float through = 1.0f;  // the segment's decay
-    const float skip = kMode == kOutput ? a.D[head] : 0.0f;
+    const float skip = kY ? a.D[head] : 0.0f;
+    const int count = chunk_of(a, sg.x).y > 0 ? sg.y : 0;   // (a sequence without tokens has one empty chunk)
 
-    for (int i = 0; i < sg.y; ++i) {
-        const int c = s.reverse ? sg.x + sg.y - 1 - i : sg.x + i;
-        const int4 ch = chunk_of(a, c);
-        if (ch.y <= 0) continue;
-        const uint8_t* const block = a.groups + ((int64_t)c * a.G + g) * s.group_bytes;
-        const float* const arrays = a.heads + ((int64_t)c * a.H + head) * kHeadArrays * kChunk;
-        if (kMode == kStarts && live) {
-            float* const out = s.starts + ((int64_t)c * a.H + head) * kP * kN;
-#pragma unroll
-            for (int n = 0; n < kTiles; ++n)
-#pragma unroll
-                for (int p = 0; p < 2; ++p) *reinterpret_cast<v4f*>(out + (p0 + p * 16) * kN + n * 16 + 4 * q) = h[n][p];
-        }
-        // the chunk's rows of v, places of the sums along its tokens; zero behind the sequence
-        float v[2][2][8];
+    float v[2][2][8];
+    auto load_v = [&](int i) {   // the chunk's rows of v, places of the sums along its tokens; zero behind the sequence
+        const int4 ch = chunk_of(a, chunk_at(i));
         const RowBuffer<kBf16> rows(s.v, ch.x, s.ldv, ch.y, head * kP + half * 32, 32);
-        const int own = opaque(4 * q * (int)s.ldv + r) * kSize;
+        const int own = opaque(4 * q * (int)s.ldv + 2 * r) * kSize;
 #pragma unroll
         for (int k = 0; k < 2; ++k)
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-#pragma unroll
-                for (int p = 0; p < 2; ++p) v[k][p][j] = rows.load(own + (k * 32 + place(0, j)) * (int)s.ldv * kSize + p * 16 * kSize);
-        if constexpr (kMode == kOutput) {
-            stage<Block::kSet>(block + Block::kRows, lds);
-            __syncthreads();
-            if (live) {
-                v4f y[4][2];
-#pragma unroll
-                for (int t = 0; t < 4; ++t) y[t][0] = y[t][1] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                for (int k = 0; k < kSteps; ++k) {
-                    Pieces<kOut> state[2];
-#pragma unroll
-                    for (int p = 0; p < 2; ++p) {
-                        float f[8];
-                        unpack(f, h[2 * k][p], h[2 * k + 1][p]);
-                        state[p] = split<kOut>(f);
-                    }
-#pragma unroll
-                    for (int t = 0; t < 4; ++t) {
-                        const Pieces<kData> cr = load_pieces<kData>(lds + ((t * kSteps + k) * 64 + lane) * 16, Block::kPlane);
-                        y[t][0] = mma(cr, state[0], y[t][0]);
-                        y[t][1] = mma(cr, state[1], y[t][1]);
-                    }
-                }
-#pragma unroll
-                for (int t = 0; t < 4; ++t) {
-                    const v4f e = *reinterpret_cast<const v4f*>(arrays + kDecay * kChunk + t * 16 + 4 * q);
-                    y[t][0] *= e;
-                    y[t][1] *= e;
-                }
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {   // 32 tokens s
-                    Pieces<kData> x[2];
-                    x[0] = split<kData>(v[k][0]);
-                    x[1] = split<kData>(v[k][1]);
-                    float hi[8], lo[8], step[8];
-                    const float* const from = arrays + k * 32 + 4 * q;
-                    unpack(hi, *reinterpret_cast<const v4f*>(from), *reinterpret_cast<const v4f*>(from + 16));
-                    unpack(lo, *reinterpret_cast<const v4f*>(from + kCsLo * kChunk), *reinterpret_cast<const v4f*>(from + kCsLo * kChunk + 16));
-                    unpack(step, *reinterpret_cast<const v4f*>(from + kStep * kChunk), *reinterpret_cast<const v4f*>(from + kStep * kChunk + 16));
-#pragma unroll
-                    for (int t = 2 * k; t < 4; ++t) {
-                        const float thi = arrays[t * 16 + r], tlo = arrays[kCsLo * kChunk + t * 16 + r];
-                        float w[8];
-                        const uint8_t* const products = block + ((2 * k * 4 + t) * 64 + lane) * 16;
-                        const v4f g0 = *reinterpret_cast<const v4f*>(products);
-                        const v4f g1 = t > 2 * k ? *reinterpret_cast<const v4f*>(products + 4 * 64 * 16) : v4f{0.0f, 0.0f, 0.0f, 0.0f};
-                        unpack(w, g0, g1);
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            const int row = k * 32 + place(q, j);
-                            const float f = step[j] * __builtin_amdgcn_exp2f((thi - hi[j]) + (tlo - lo[j]));
-                            w[j] = t * 16 + r >= row ? w[j] * f : 0.0f;
-                        }
-                        const Pieces<kOut> wp = split<kOut>(w);
-                        y[t][0] = mma(wp, x[0], y[t][0]);
-                        y[t][1] = mma(wp, x[1], y[t][1]);
-                    }
-                }
-                const RowBuffer<kBf16> out(s.y, ch.x, s.ldy, ch.y, head * kP + half * 32, 32);
-                const int to = opaque(4 * q * (int)s.ldy + r) * kSize;
-#pragma unroll
-                for (int t = 0; t < 4; ++t)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-#pragma unroll
-                        for (int p = 0; p < 2; ++p)
-                            out.store(fmaf(skip, v[t >> 1][p][(t & 1) * 4 + j], y[t][p][j]),
-                                      to + (t * 16 + j) * (int)s.ldy * kSize + p * 16 * kSize);
-                    }
+            for (int j = 0; j < 8; ++j) {
+                const float2 pair = rows.load2(own + (k * 32 + place(0, j)) * (int)s.ldv * kSize);
+                v[k][0][j] = pair.x;
+                v[k][1][j] = pair.y;
             }
-            __syncthreads();
-        }
-        stage<Block::kSet>(block + s.key, lds);
-        __syncthreads();
-        if (live) {
-            const float last = arrays[kDecay * kChunk + kChunk - 1];
-            through *= last;
-            // (the later half's weights are smaller in fast heads, and so are its errors: what is left changes its sign
-            // from chunk to chunk)
-            const float sign = c & 1 ? -1.0f : 1.0f;
-            Pieces<kIn> in[2][2];
+    };
+    if (count > 0) {
+        load_arrays(0);
+        if constexpr (kY) next_first.load(block_of(sg.x), kFirst);
+        else next_key.load(block_of(chunk_at(0)) + s.key, Block::kSet);
+        if constexpr (!kY) load_v(0);
+    }
+    for (int i = 0; i < count; ++i) {
+        const int c = chunk_at(i);
+        const float* const arrays = reinterpret_cast<const float*>(head_lds[i & 1]) + (live ? wave >> 1 : 0) * kHeadArrays * kChunk;
+        next_arrays.store(head_lds[i & 1]);
+        if constexpr (kY) next_first.store(first_lds);
+        else next_key.store(i & 1 ? first_lds : key_lds);
+        lds_barrier();
+        if constexpr (kY) {
+            load_v(i);
+            if constexpr (kBf16) next_key.load(block_of(c) + s.key, Block::kSet);
+            __builtin_amdgcn_sched_barrier(0);   // (or the loads would sink to where they are used)
+            v4f y[4][2];
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const float* const from = arrays + (s.reverse ? kDecay : kWeight) * kChunk + k * 32 + 4 * q;
-                float w[8];
-                unpack(w, *reinterpret_cast<const v4f*>(from), *reinterpret_cast<const v4f*>(from + 16));
+            for (int t = 0; t < 4; ++t) y[t][0] = y[t][1] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+            const uint8_t* const rows = first_lds + Block::kRows + lane * 16;
+#pragma unroll
+            for (int k = 0; k < kSteps; ++k) {
+                Pieces<kOut> state[2];
 #pragma unroll
                 for (int p = 0; p < 2; ++p) {
                     float f[8];
+                    unpack(f, h[2 * k][p], h[2 * k + 1][p]);
+                    state[p] = split<kOut>(f);
+                }
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) f[j] = v[k][p][j] * (k ? -sign : sign) * w[j];
-                    in[k][p] = split<kIn>(f);
+                for (int t = 0; t < 4; ++t) {
+                    const Pieces<kData> cr = load_pieces<kData>(rows + (t * kSteps + k) * 1024, Block::kPlane);
+                    y[t][0] = mma(cr, state[0], y[t][0]);
+                    y[t][1] = mma(cr, state[1], y[t][1]);
                 }
             }
 #pragma unroll
-            for (int n = 0; n < kTiles; ++n) {
-                v4f add[2][2];
+            for (int t = 0; t < 4; ++t) {
+                const v4f e = sigma * at4(arrays + kDecay * kChunk + t * 16 + 4 * q);
+                y[t][0] *= e;
+                y[t][1] *= e;
+            }
+            float enter[4], between[4];     // between[t]: the decay of tile t as a whole
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const Pieces<kData> key = load_pieces<kData>(lds + ((n * 2 + k) * 64 + lane) * 16, Block::kPlane);
-                    add[0][k] = mma(key, in[k][0], v4f{0.0f, 0.0f, 0.0f, 0.0f});
-                    add[1][k] = mma(key, in[k][1], v4f{0.0f, 0.0f, 0.0f, 0.0f});
+            for (int t = 0; t < 4; ++t) {
+                enter[t] = arrays[kEnter * kChunk + t * 16 + r];
+                between[t] = arrays[kEnter * kChunk + t * 16 + 15];
+            }
+            const uint8_t* const products = first_lds + lane * 16;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {   // 32 tokens s, two tiles
+                Pieces<kData> x[2];
+                x[0] = split<kData>(v[k][0]);
+                x[1] = split<kData>(v[k][1]);
+                const v4f leave[2] = {at4(arrays + kLeave * kChunk + k * 32 + 4 * q), at4(arrays + kLeave * kChunk + k * 32 + 16 + 4 * q)};
+#pragma unroll
+                for (int t = 2 * k; t < 4; ++t) {
+                    float w[8];
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        const int st = 2 * k + u;   // the tile of s
+                        v4f part = {0.0f, 0.0f, 0.0f, 0.0f};
+                        if (st < t) {
+                            float f = enter[t];
+#pragma unroll
+                            for (int m = 0; m < 4; ++m)
+                                if (m > st && m < t) f *= between[m];
+                            part = *reinterpret_cast<const v4f*>(products + (st * 4 + t) * 1024) * (leave[u] * f);
+                        } else if (st == t) {
+                            const float hi = arrays[t * 16 + r], lo = arrays[kCsLo * kChunk + t * 16 + r];
+                            const v4f his = at4(arrays + t * 16 + 4 * q), los = at4(arrays + kCsLo * kChunk + t * 16 + 4 * q);
+                            const v4f step = at4(arrays + kStep * kChunk + t * 16 + 4 * q);
+                            const v4f product = *reinterpret_cast<const v4f*>(products + (t * 4 + t) * 1024);
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                part[j] = product[j] * (step[j] * decay_between(hi - his[j], lo - los[j], r >= 4 * q + j));
+                        }
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) w[u * 4 + j] = part[j];
+                    }
+                    const Pieces<kOut> wp = split<kOut>(w);
+                    y[t][0] = mma(wp, x[0], y[t][0]);
+                    y[t][1] = mma(wp, x[1], y[t][1]);
                 }
+            }
+            if constexpr (!kBf16) {   // (three pieces are too many registers to hold meanwhile)
+                __builtin_amdgcn_sched_barrier(0);
+                next_key.load(block_of(c) + s.key, Block::kSet);
+            }
+            if (live) {
+                const int4 ch = chunk_of(a, c);
+                const RowBuffer<kBf16> out(s.y, ch.x, s.ldy, ch.y, head * kP + half * 32, 32);
+                const int to = opaque(4 * q * (int)s.ldy + 2 * r) * kSize;
 #pragma unroll
-                for (int p = 0; p < 2; ++p) {
-                    const v4f sum = opposite(add[p]);
+                for (int t = 0; t < 4; ++t)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) h[n][p][j] = fmaf(h[n][p][j], last, sign * sum[j]);
-                }
+                    for (int j = 0; j < 4; ++j)
+                        out.store2(fmaf(skip, v[t >> 1][0][(t & 1) * 4 + j], y[t][0][j]),
+                                   fmaf(skip, v[t >> 1][1][(t & 1) * 4 + j], y[t][1][j]), to + (t * 16 + j) * (int)s.ldy * kSize);
+            }
+            next_key.store(key_lds);
+            lds_barrier();
+            if (i + 1 < count) {
+                load_arrays(i + 1);
+                next_first.load(block_of(chunk_at(i + 1)), kFirst);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        } else {
+            if (i + 1 < count) {
+                load_arrays(i + 1);
+                next_key.load(block_of(chunk_at(i + 1)) + s.key, Block::kSet);
+            }
+            if (kMode == kStarts && live) {
+                float* const out = s.starts + ((int64_t)c * a.H + head) * kP * kN + opaque(p0 * kN + 4 * q);
+#pragma unroll
+                for (int n = 0; n < kTiles; ++n)
+#pragma unroll
+                    for (int p = 0; p < 2; ++p) *reinterpret_cast<v4f*>(out + p * kN + n * 16) = sigma * h[n][p];
             }
         }
-        __syncthreads();
+        const float last = arrays[kDecay * kChunk + kChunk - 1];
+        through *= last;
+        Pieces<kInto> in[2][2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const float* const from = arrays + (s.reverse ? kDecay : kWeight) * kChunk + k * 32 + 4 * q;
+            float w[8];
+            unpack(w, -sigma * at4(from), -sigma * at4(from + 16));
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+                float f[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) f[j] = v[k][p][j] * w[j];
+                in[k][p] = split<kInto>(f);
+            }
+        }
+        if (!kY && i + 1 < count) load_v(i + 1);
+        __builtin_amdgcn_sched_barrier(0);
+        const uint8_t* const keys = (!kY && (i & 1) ? first_lds : key_lds) + lane * 16;
+#pragma unroll
+        for (int n = 0; n < kTiles; ++n) {
+            const Pieces<kData> key0 = load_pieces<kData>(keys + n * 2048, Block::kPlane);
+            const Pieces<kData> key1 = load_pieces<kData>(keys + n * 2048 + 1024, Block::kPlane);
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+                const v4f add = mma(key1, in[1][p], mma(key0, in[0][p], v4f{0.0f, 0.0f, 0.0f, 0.0f}));
+#pragma unroll
+                for (int j = 0; j < 4; ++j) h[n][p][j] = fmaf(h[n][p][j], -last, add[j]);
+            }
+        }
+        sigma = -sigma;
     }
     if (!live) return;
     if constexpr (kMode == kLocal) {
 #pragma unroll
         for (int n = 0; n < kTiles; ++n)
 #pragma unroll
-            for (int p = 0; p < 2; ++p) slot[(n * 2 + p) * 64] = h[n][p];
+            for (int p = 0; p < 2; ++p) slot[(n * 2 + p) * 64] = sigma * h[n][p];
         if (half == 0 && lane == 0) s.segment_decay[(int64_t)seg * a.H + head] = through;
     } else if (s.end && (sg.w & (s.reverse ? 1 : 2))) {
 #pragma unroll
         for (int n = 0; n < kTiles; ++n)
 #pragma unroll
-            for (int p = 0; p < 2; ++p)
-                *reinterpret_cast<v4f*>(s.end + mine + (p0 + p * 16) * kN + n * 16 + 4 * q) = h[n][p];
+            for (int p = 0; p < 2; ++p) *reinterpret_cast<v4f*>(s.end + mine + (p0 + p) * kN + n * 16 + 4 * q) = sigma * h[n][p];
     }
 }
 
@@ -429,7 +486,7 @@ __global__ __launch_bounds__(256) void join_segments_kernel(SweepArgs s) {
     const int count = (s.a.segments ? s.a.first_segment[sequence + 1] : first + each) - first;
     v4f h = {0.0f, 0.0f, 0.0f, 0.0f};
     if (s.start)
-        h = *reinterpret_cast<const v4f*>(s.start + (((int64_t)sequence * s.a.H + head) * kP + half * 32 + p * 16 + (lane & 15)) * kN +
+        h = *reinterpret_cast<const v4f*>(s.start + (((int64_t)sequence * s.a.H + head) * kP + half * 32 + 2 * (lane & 15) + p) * kN +
                                           n * 16 + 4 * (lane >> 4));
     v4f* const states = reinterpret_cast<v4f*>(s.segment_states);
 #pragma unroll 4
@@ -515,7 +572,7 @@ hipError_t launch_scan_prepare(const ScanArgs& a, bool bf16, int N, bool backwar
 }
 
 hipError_t launch_sweep(const SweepArgs& s, const ScanPlan& plan, bool bf16, int N, SweepMode mode, hipStream_t stream) {
-    const dim3 grid((unsigned)(plan.nsegments * s.a.G * ((s.a.H / s.a.G + 1) / 2)));
+    const dim3 grid((unsigned)(plan.nsegments * s.a.G * ((s.a.H / s.a.G + kSweepHeads - 1) / kSweepHeads)));
     return with_kind(bf16, N, [&](auto b, auto n) {
         if (plan.segmented) {
             sweep_kernel<b.value, n.value, kLocal><<<grid, kSweepThreads, 0, stream>>>(s);
@@ -536,18 +593,18 @@ constexpr int kRecurrentTokens = 8;
 
 bool scan_recurrent(const Sequences& seq) { return seq.T <= (int64_t)kRecurrentTokens * seq.S; }
 
-// Enough workgroups for two on each CU: what one segment a sequence does not give, more segments do, at the price of a
+// Enough workgroups for one on each CU: what one segment a sequence does not give, more segments do, at the price of a
 // second sweep without outputs.
-constexpr int kSweepGroups = 512;
-constexpr int64_t kMaxSegmentHeads = 4 * kSweepGroups;   // room for the segments' states, in heads
+constexpr int kSweepGroups = 256;
+constexpr int64_t kMaxSegmentHeads = 8 * kSweepGroups;   // room for the segments' states, in heads
 
 ScanPlan scan_plan(const Sequences& seq, int H, int G) {
     ScanPlan p{};
-    const int64_t pairs = (int64_t)G * ((H / G + 1) / 2);
+    const int64_t quads = (int64_t)G * ((H / G + kSweepHeads - 1) / kSweepHeads);
     const int64_t each = (seq.L + kChunk - 1) / kChunk;    // chunks of a sequence, without offsets
     p.nchunks = (int)(seq.cu ? seq.T / kChunk + seq.S : seq.S * each);
-    const int64_t all = p.nchunks * pairs;
-    int64_t per = seq.S * pairs >= kSweepGroups ? p.nchunks : (all + kSweepGroups - 1) / kSweepGroups;
+    const int64_t all = p.nchunks * quads;
+    int64_t per = seq.S * quads >= kSweepGroups ? p.nchunks : (all + kSweepGroups - 1) / kSweepGroups;
     if (per < 1) per = 1;
     auto segments = [&](int64_t n) { return seq.cu ? p.nchunks / n + seq.S : seq.S * ((each + n - 1) / n); };
     while (per < p.nchunks && segments(per) * H > kMaxSegmentHeads) per *= 2;

@@ -104,13 +104,7 @@ __global__ __launch_bounds__(kThreads, 2) void scan_grad_kernel(ScanGradArgs s) 
     const int slice = blockIdx.y % s.slices, g = blockIdx.y / s.slices, c = blockIdx.x;
     const int per_group = a.H / a.G, first = slice * s.per_slice;
     const int last = first + s.per_slice < per_group ? first + s.per_slice : per_group;
-    int4 ch;
-    if (a.chunks) {
-        ch = a.chunks[c];
-    } else {
-        const int per = (a.seq.L + kChunk - 1) / kChunk, i = c % per, left = a.seq.L - i * kChunk;
-        ch = make_int4(c / per * a.seq.L + i * kChunk, left < kChunk ? left : kChunk, c / per, 0);
-    }
+    const int4 ch = chunk_of(a, c);
     if (ch.z < 0 || ch.y <= 0) return;
     const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, q = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -171,7 +165,7 @@ __global__ __launch_bounds__(kThreads, 2) void scan_grad_kernel(ScanGradArgs s) 
             }
         __syncthreads();
         {   // M, K L, E: columns s along the lanes
-            const float s_hi = arrays[st * 16 + r], s_lo = arrays[kCsLo * kChunk + st * 16 + r], s_dt = arrays[kStep * kChunk + st * 16 + r];
+            const float s_dt = arrays[kStep * kChunk + st * 16 + r];
             double column = 0.0;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
@@ -183,18 +177,29 @@ __global__ __launch_bounds__(kThreads, 2) void scan_grad_kernel(ScanGradArgs s) 
                     both[j] = mma(load_pieces<kData>(lds + Lds::kDy + ((tt * 2 + j) * 64 + lane) * 16, kPlane),
                                   load_pieces<kData>(lds + Lds::kX + ((st * 2 + j) * 64 + lane) * 16, kPlane), v4f{0.0f, 0.0f, 0.0f, 0.0f});
                 const v4f m = opposite(both);
-                const v4f hi = *reinterpret_cast<const v4f*>(arrays + tt * 16 + 4 * q);
-                const v4f lo = *reinterpret_cast<const v4f*>(arrays + kCsLo * kChunk + tt * 16 + 4 * q);
+                v4f f;     // L
+                if (tt == st) {
+                    const v4f hi = *reinterpret_cast<const v4f*>(arrays + tt * 16 + 4 * q);
+                    const v4f lo = *reinterpret_cast<const v4f*>(arrays + kCsLo * kChunk + tt * 16 + 4 * q);
+                    const float s_hi = arrays[st * 16 + r], s_lo = arrays[kCsLo * kChunk + st * 16 + r];
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) f[v] = decay_between(hi[v] - s_hi, lo[v] - s_lo, 4 * q + v >= r);
+                } else {
+                    // behind s in its tile (leave has dt as a factor, which may be zero: from the sums), the tiles between, before t in its own
+                    const float end_hi = arrays[st * 16 + 15], end_lo = arrays[kCsLo * kChunk + st * 16 + 15];
+                    float behind = decay_between(end_hi - arrays[st * 16 + r], end_lo - arrays[kCsLo * kChunk + st * 16 + r], true);
+                    for (int n = st + 1; n < tt; ++n) behind *= arrays[kEnter * kChunk + n * 16 + 15];
+                    f = behind * *reinterpret_cast<const v4f*>(arrays + kEnter * kChunk + tt * 16 + 4 * q);
+                }
                 float kl[8];
                 double rows[4];
 #pragma unroll
                 for (int v = 0; v < 4; ++v) {
-                    const bool on = tt > st || 4 * q + v >= r, strict = tt > st || 4 * q + v > r;
-                    const float f = on ? __builtin_amdgcn_exp2f((hi[v] - s_hi) + (lo[v] - s_lo)) : 0.0f;
-                    kl[v] = products[i][v] * f;
+                    const bool strict = tt > st || 4 * q + v > r;
+                    kl[v] = products[i][v] * f[v];
                     kl[v + 4] = 0.0f;
                     const float e = m[v] * kl[v];
-                    sum_w[i][v] = fmaf(m[v] * f, s_dt, sum_w[i][v]);
+                    sum_w[i][v] = fmaf(m[v] * f[v], s_dt, sum_w[i][v]);
                     column += strict ? (double)e : 0.0;
                     rows[v] = row_sum(strict ? (double)e * (double)s_dt : 0.0);
                     if (tt == st && 4 * q + v == r) {
@@ -405,13 +410,7 @@ __global__ __launch_bounds__(256) void join_slabs_kernel(ScanGradArgs s) {
     using T = typename E::type;
     const ScanArgs& a = s.a;
     const int c = blockIdx.x, g = blockIdx.y;
-    int4 ch;
-    if (a.chunks) {
-        ch = a.chunks[c];
-    } else {
-        const int per = (a.seq.L + kChunk - 1) / kChunk, i = c % per, left = a.seq.L - i * kChunk;
-        ch = make_int4(c / per * a.seq.L + i * kChunk, left < kChunk ? left : kChunk, c / per, 0);
-    }
+    const int4 ch = chunk_of(a, c);
     if (ch.z < 0) return;
     const int64_t step = (int64_t)a.nchunks * a.G * 2 * kChunk * kN;
     for (int i = threadIdx.x; i < 2 * kChunk * kN / 4; i += 256) {

@@ -27,10 +27,13 @@ typedef __bf16 v4bf __attribute__((ext_vector_type(4)));
 
 constexpr int kChunk = 64;     // tokens of a chunk
 constexpr int kP = 64;         // channels of a head
-constexpr int kHeadArrays = 5; // per chunk and head, 64 values each:
-enum { kCsHi, kCsLo, kStep, kWeight, kDecay };
+constexpr int kHeadArrays = 7; // per chunk and head, 64 values each:
+enum { kCsHi, kCsLo, kStep, kWeight, kDecay, kEnter, kLeave };
 //   cs = log2 of the decay from the chunk's start through token t, as hi + lo (summed in fp64: differences of
-//   close ones keep fp32's precision however far the sum has come);  step = dt;  weight = dt 2^(cs_end - cs);  decay = 2^cs
+//   close ones keep fp32's precision however far the sum has come);  step = dt;  weight = dt 2^(cs_end - cs);  decay = 2^cs;
+//   enter = the decay from the start of the token's tile of 16 through it;  leave = dt times the decay behind it to its tile's end.
+// The decay between tokens of different tiles is the product of a leave, the tiles in between (their last enter) and an
+// enter: all of them at most 1, so that none can overflow, and one product where a difference and an exponential would be.
 
 struct ScanArgs {
     Sequences seq;
@@ -47,6 +50,25 @@ struct ScanArgs {
     uint8_t* groups;  // [chunk][G] blocks of group_bytes
     float* heads;     // [chunk][H][kHeadArrays][kChunk]
 };
+
+// A table's entry in scalar registers (it is the same for the whole wave, which the compiler cannot see of a load: buffers made from
+// it would be loops over the lanes).
+__device__ __forceinline__ int4 uniform(int4 v) {
+    return make_int4(__builtin_amdgcn_readfirstlane(v.x), __builtin_amdgcn_readfirstlane(v.y),
+                     __builtin_amdgcn_readfirstlane(v.z), __builtin_amdgcn_readfirstlane(v.w));
+}
+
+__device__ __forceinline__ int4 chunk_of(const ScanArgs& a, int c) {
+    if (a.chunks) return uniform(a.chunks[c]);
+    const int per = (a.seq.L + kChunk - 1) / kChunk, s = c / per, i = c - s * per;
+    const int left = a.seq.L - i * kChunk;
+    return uniform(make_int4(s * a.seq.L + i * kChunk, left < kChunk ? left : kChunk, s, 0));
+}
+
+// 2^(hi + lo), or 0 (without a branch: the exponential of a difference that is far below its range).
+__device__ __forceinline__ float decay_between(float hi, float lo, bool on) {
+    return __builtin_amdgcn_exp2f(on ? hi + lo : -1e30f);
+}
 
 // A group's block for one chunk: products C_t . B_s (fp32, results of 16 x 16), then three sets of pieces, each
 // [piece][16-row tile][32-place step][lane][8]:

@@ -90,6 +90,24 @@ struct RowBuffer {
             return __builtin_bit_cast(v4f, __builtin_amdgcn_raw_buffer_load_b128(rsrc, bytes, 0, 0));
         }
     }
+    // two neighbours (an even place)
+    __device__ __forceinline__ float2 load2(int bytes) const {
+        if constexpr (kBf16) {
+            const uint32_t v = __builtin_amdgcn_raw_buffer_load_b32(rsrc, bytes, 0, 0);
+            return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
+        } else {
+            const auto v = __builtin_amdgcn_raw_buffer_load_b64(rsrc, bytes, 0, 0);
+            return make_float2(__uint_as_float(v[0]), __uint_as_float(v[1]));
+        }
+    }
+    __device__ __forceinline__ void store2(float x, float y, int bytes) const {
+        if constexpr (kBf16) {
+            __builtin_amdgcn_raw_buffer_store_b32(bf16_bits(x) | (bf16_bits(y) << 16), rsrc, bytes, 0, 0);
+        } else {
+            typedef uint32_t v2u __attribute__((ext_vector_type(2)));
+            __builtin_amdgcn_raw_buffer_store_b64(v2u{__float_as_uint(x), __float_as_uint(y)}, rsrc, bytes, 0, 0);
+        }
+    }
     __device__ __forceinline__ void store(float v, int bytes) const {
         if constexpr (kBf16) __builtin_amdgcn_raw_buffer_store_b16((uint16_t)bf16_bits(v), rsrc, bytes, 0, 0);
         else __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v), rsrc, bytes, 0, 0);

@@ -30,7 +30,7 @@ ScanPlan scan_plan(const Sequences& seq, int H, int G);
 namespace {
 
 constexpr int kThreads = 512;
-constexpr int kGradGroups = 512;   // workgroups wanted of the gradient kernel: two for each CU
+constexpr int kGradGroups = 256;   // workgroups wanted of the gradient kernel: one for each CU
 constexpr int kMaxSlabs = 2 * kGradGroups;
 constexpr int kSums = 4;           // floats per chunk and head: sums of da a, dy . x, ddt (and one that pads)
 
@@ -52,10 +52,11 @@ template <bool kBf16, int kN>
 struct GradLds {
     static constexpr int kData = kBf16 ? 1 : 3, kOut = kBf16 ? 2 : 3, kPlane = kChunk * kP * 2;
     static constexpr int kDy = 0, kX = kDy + kData * kPlane, kW = kX + kData * kPlane, kRows = kW + kOut * kPlane;
-    static constexpr int kPart = kRows + kData * kChunk * kN * 2;       // floats
+    static constexpr int kK = kRows + kData * kChunk * kN * 2, kPart = kK + kChunk * kChunk * 4;   // (the latter: floats)
     static constexpr int kRowSum = 0, kColSum = 8 * kChunk, kDiag = 12 * kChunk, kDot = 13 * kChunk, kU = 14 * kChunk,
-                         kV = kU + kN / 16 * kChunk, kPass = kV + kN / 16 * kChunk;   // (the first two hold doubles)
-    static constexpr int bytes = kPart + (kPass + 16) * 4;
+                         kV = kU + kN / 16 * kChunk, kPass = kV + 4 * kChunk;   // (the first two and the last hold doubles)
+    static constexpr int kArrays = kPass + 16;                                  // the head's decays
+    static constexpr int kParts = kArrays + kHeadArrays * kChunk, bytes = kPart + 2 * kParts * 4;   // (this turn's head and the one before)
     static constexpr int kLdSum = kChunk + 4;                           // the heads' sum of M L dt, over dy, x and W
     static_assert(kChunk * kLdSum * 4 <= kRows, "it fits");
 };
@@ -96,10 +97,6 @@ __global__ __launch_bounds__(kThreads, 2) void scan_grad_kernel(ScanGradArgs s) 
     // a wave's part of dB and dC: one tile of 16 state places, kTT tiles of tokens
     constexpr int kTiles = kN / 16, kParts = 8 / kTiles, kTT = 4 / kParts, kSteps = kN / 32;
     __shared__ __attribute__((aligned(16))) uint8_t lds[Lds::bytes];
-    float* const part = reinterpret_cast<float*>(lds + Lds::kPart);
-    double* const row_sums = reinterpret_cast<double*>(part + Lds::kRowSum);
-    double* const column_sums = reinterpret_cast<double*>(part + Lds::kColSum);
-    double* const passes = reinterpret_cast<double*>(part + Lds::kPass);
     const ScanArgs& a = s.a;
     const int slice = blockIdx.y % s.slices, g = blockIdx.y / s.slices, c = blockIdx.x;
     const int per_group = a.H / a.G, first = slice * s.per_slice;
@@ -110,60 +107,166 @@ __global__ __launch_bounds__(kThreads, 2) void scan_grad_kernel(ScanGradArgs s) 
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const uint8_t* const block = a.groups + ((int64_t)c * a.G + g) * s.group_bytes;
 
-    // what stays for all heads: B's rows in LDS, and K's tiles of this wave
+    // what stays for all heads: B's rows and K in LDS, and C at the places of this wave's part of dC
     for (int i = tid; i < Block::kSet / 16; i += kThreads)
         *reinterpret_cast<v4i*>(lds + Lds::kRows + i * 16) = *reinterpret_cast<const v4i*>(block + Block::kRows + i * 16);
+    for (int i = tid; i < kChunk * kChunk / 4; i += kThreads)
+        *reinterpret_cast<v4i*>(lds + Lds::kK + i * 16) = *reinterpret_cast<const v4i*>(block + i * 16);
     for (int i = tid; i < kOut * kPlane / 16; i += kThreads)    // (tiles above the diagonal stay zero)
         *reinterpret_cast<v4i*>(lds + Lds::kW + i * 16) = v4i{0, 0, 0, 0};
     const int st = wave & 3, half = wave >> 2;        // M's tiles: columns st, rows st + half and st + half + 2
-    v4f products[2], sum_w[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int tt = st + half + 2 * i;
-        products[i] = sum_w[i] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-        if (tt < 4) products[i] = *reinterpret_cast<const v4f*>(block + ((tt * 4 + st) * 64 + lane) * 16);
-    }
+    v4f sum_w[2] = {};
     const int nt = wave % kTiles, t0 = wave / kTiles * kTT;
-    const RowBuffer<kBf16> b_rows(a.B, ch.x, a.ldb, ch.y, g * kN + nt * 16, 16), c_rows(a.C, ch.x, a.ldc, ch.y, g * kN + nt * 16, 16);
-    v4f acc_b[kTT], acc_c[kTT];
+    const RowBuffer<kBf16> c_rows(a.C, ch.x, a.ldc, ch.y, g * kN + nt * 16, 16);
+    v4f c_at[kTT], acc_b[kTT], acc_c[kTT];
 #pragma unroll
-    for (int t = 0; t < kTT; ++t) acc_b[t] = acc_c[t] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int t = 0; t < kTT; ++t) {
+        acc_b[t] = acc_c[t] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int v = 0; v < 4; ++v) c_at[t][v] = c_rows.load((((t0 + t) * 16 + 4 * q + v) * (int)a.ldc + r) * kSize);
+    }
     const int pt = wave & 3, sh = wave >> 2;          // dx's tiles: channels pt, tokens 2 sh and 2 sh + 1
 
-    for (int k = first; k < last; ++k) {
-        const int head = g * per_group + k;
-        const float* const arrays = a.heads + ((int64_t)c * a.H + head) * kHeadArrays * kChunk;
-        const float* const h = s.starts + ((int64_t)c * a.H + head) * kP * kN;
-        const float* const dh = s.ends + ((int64_t)c * a.H + head) * kP * kN;
-        {   // dy and x as pieces along the channels: each wave one tile of rows and one step
-            const int p = head * kP + (wave & 1) * 32, row = opaque((wave >> 1) * 16 + r);
-            const RowBuffer<kBf16> dy_rows(s.dy, ch.x, s.lddy, ch.y, p, 32), x_rows(a.x, ch.x, a.ldx, ch.y, p, 32);
-            const int from_dy = (row * (int)s.lddy + 4 * q) * kSize, from_x = (row * (int)a.ldx + 4 * q) * kSize;
-            const v4f y0 = dy_rows.load4(from_dy), y1 = dy_rows.load4(from_dy + 16 * kSize);
-            const v4f x0 = x_rows.load4(from_x), x1 = x_rows.load4(from_x + 16 * kSize);
-            float y[8], x[8];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                y[j] = y0[j];
-                y[j + 4] = y1[j];
-                x[j] = wave & 1 ? -x0[j] : x0[j];   // (the second half negated: opposite())
-                x[j + 4] = wave & 1 ? -x1[j] : x1[j];
-            }
-            store_pieces(lds + Lds::kDy + (wave * 64 + lane) * 16, kPlane, split<kData>(y));
-            store_pieces(lds + Lds::kX + (wave * 64 + lane) * 16, kPlane, split<kData>(x));
-        }
-        // the states at this wave's places, across the channels
-        float h_at[2][8], dh_at[2][8];
-        const int from_h = opaque(4 * q * kN + nt * 16 + r);
+    // What a turn needs of a head's rows and states is loaded in the turn before, as soon as the registers that hold it are free.
+    v4f y0, y1, x0, x1;
+    float decays = 0.0f;
+    static_assert(kHeadArrays * kChunk <= kThreads, "one value a thread");
+    auto load_rows = [&](int k, int r, int q) {   // dy and x along the channels: each wave one tile of rows and half of the channels
+        const int p = (g * per_group + k) * kP + (wave & 1) * 32, row = (wave >> 1) * 16 + r;
+        const RowBuffer<kBf16> dy_rows(s.dy, ch.x, s.lddy, ch.y, p, 32), x_rows(a.x, ch.x, a.ldx, ch.y, p, 32);
+        const int from_dy = (row * (int)s.lddy + 4 * q) * kSize, from_x = (row * (int)a.ldx + 4 * q) * kSize;
+        y0 = dy_rows.load4(from_dy), y1 = dy_rows.load4(from_dy + 16 * kSize);
+        x0 = x_rows.load4(from_x), x1 = x_rows.load4(from_x + 16 * kSize);
+        if (tid < kHeadArrays * kChunk) decays = a.heads[((int64_t)c * a.H + g * per_group + k) * kHeadArrays * kChunk + tid];
+    };
+    float h_at[2][8], dh_at[2][8];
+    auto load_states = [&](int k, int from) { // the states at this wave's places, across the channels
+        const int64_t at = ((int64_t)c * a.H + g * per_group + k) * kP * kN;
+        const RowBuffer<false> h(s.starts, 0, 0, 1, at, kP * kN), dh(s.ends, 0, 0, 1, at, kP * kN);
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const float v = h[from_h + (i * 32 + place(0, j)) * kN];
-                h_at[i][j] = i ? -v : v;
-                dh_at[i][j] = dh[from_h + (i * 32 + place(0, j)) * kN];
+                h_at[i][j] = h.load(from + (i * 32 + place(0, j)) * kN * 4);
+                dh_at[i][j] = dh.load(from + (i * 32 + place(0, j)) * kN * 4);
             }
+    };
+    // ddt of a head and its share of the parameters' sums, a token a lane: by one wave in the turn after the head's own, from
+    // what the turn has left in LDS
+    auto finish = [&](int k, int lane) {
+        const int head = g * per_group + k;
+        const float* const part = reinterpret_cast<const float*>(lds + Lds::kPart) + (k & 1) * Lds::kParts;
+        const float* const arrays = part + Lds::kArrays;
+        const double* const row_sums = reinterpret_cast<const double*>(part + Lds::kRowSum);
+        const double* const column_sums = reinterpret_cast<const double*>(part + Lds::kColSum);
+        const double* const passes = reinterpret_cast<const double*>(part + Lds::kPass);
+        const float hi = arrays[lane], lo = arrays[kCsLo * kChunk + lane], dt = arrays[kStep * kChunk + lane];
+        const float end_hi = arrays[kChunk - 1], end_lo = arrays[kCsLo * kChunk + kChunk - 1];
+        double rows = 0.0;
+        float u = 0.0f, v = 0.0f;
+        double pass = 0.0;
+        for (int i = 0; i <= lane >> 4; ++i) rows += row_sums[i * kChunk + lane];
+#pragma unroll
+        for (int i = 0; i < kTiles; ++i) u += part[Lds::kU + i * kChunk + lane];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v += part[Lds::kV + i * kChunk + lane];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) pass += passes[i];
+        const double columns = column_sums[lane] + column_sums[kChunk + lane];
+        u *= arrays[kDecay * kChunk + lane];
+        v *= __builtin_amdgcn_exp2f((end_hi - hi) + (end_lo - lo));
+        pass *= arrays[kDecay * kChunk + kChunk - 1];
+        const float z = (float)columns + part[Lds::kDiag + lane] + v;    // x . (dh B)
+        // from t on: rows of E and u, less the columns from t on (pairs that lie behind t whole); before t: v
+        double from = rows + (double)u - (double)dt * columns, before = (double)dt * (double)v;
+        const double own = before;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const double o = __shfl_down(from, d), p = __shfl_up(before, d);
+            if (lane + d < 64) from += o;
+            if (lane >= d) before += p;
+        }
+        const float da = (float)(from + (before - own) + pass);
+        const float rate = expf(a.A_log[head]);
+        float raw = 0.0f, ddt = 0.0f;
+        if (lane < ch.y) {
+            raw = a.dt[(int64_t)(ch.x + lane) * a.lddt + head] + a.dt_bias[head];
+            ddt = (z - rate * da) * (raw > 20.0f ? 1.0f : 1.0f / (1.0f + expf(-raw)));
+            s.ddt[(int64_t)(ch.x + lane) * s.ldddt + head] = ddt;
+        }
+        float sum_a = -rate * dt * da, sum_d = part[Lds::kDot + lane], sum_t = ddt;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            sum_a += __shfl_xor(sum_a, d);
+            sum_d += __shfl_xor(sum_d, d);
+            sum_t += __shfl_xor(sum_t, d);
+        }
+        if (lane == 0)
+            *reinterpret_cast<v4f*>(s.sums + ((int64_t)c * a.H + head) * kSums) = v4f{sum_a, sum_d, sum_t, 0.0f};
+    };
+    load_rows(first, r, q);
+    for (int k = first; k < last; ++k) {
+        // (what depends on the lane is formed anew in each turn: kept over the turns it would fill the registers)
+        const int lane = opaque(tid & 63), r = lane & 15, q = lane >> 4;
+        const int head = g * per_group + k;
+        float* const part = reinterpret_cast<float*>(lds + Lds::kPart) + (k & 1) * Lds::kParts;
+        float* const arrays = part + Lds::kArrays;
+        if (tid < kHeadArrays * kChunk) arrays[tid] = decays;
+        double* const row_sums = reinterpret_cast<double*>(part + Lds::kRowSum);
+        double* const column_sums = reinterpret_cast<double*>(part + Lds::kColSum);
+        double* const passes = reinterpret_cast<double*>(part + Lds::kPass);
+        {   // (x's second half negated: opposite())
+            const float sign = wave & 1 ? -1.0f : 1.0f;
+            const float y[8] = {y0.x, y0.y, y0.z, y0.w, y1.x, y1.y, y1.z, y1.w};
+            const float x[8] = {sign * x0.x, sign * x0.y, sign * x0.z, sign * x0.w, sign * x1.x, sign * x1.y, sign * x1.z, sign * x1.w};
+            store_pieces(lds + Lds::kDy + (wave * 64 + lane) * 16, kPlane, split<kData>(y));
+            store_pieces(lds + Lds::kX + (wave * 64 + lane) * 16, kPlane, split<kData>(x));
+        }
+        load_states(k, (4 * q * kN + nt * 16 + r) * 4);
+        double pass = 0.0;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                pass += (double)h_at[i][j] * (double)dh_at[i][j];
+                if (i) h_at[i][j] = -h_at[i][j];
+            }
+        const Pieces<kFull> hp[2] = {split<kFull>(h_at[0]), split<kFull>(h_at[1])};
+        const Pieces<kFull> dhp[2] = {split<kFull>(dh_at[0]), split<kFull>(dh_at[1])};
         __syncthreads();
+        if (k > first && wave == ((k - 1) & 7)) finish(k - 1, lane);
+        __builtin_amdgcn_sched_barrier(0);
+        {   // dC and dB through the states
+#pragma unroll
+            for (int t = 0; t < kTT; ++t) {
+                v4f us_[2], ws_[2];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const v4f zero = {0.0f, 0.0f, 0.0f, 0.0f};
+                    us_[j] = mma(load_pieces<kData>(lds + Lds::kDy + (((t0 + t) * 2 + j) * 64 + lane) * 16, kPlane), hp[j], zero);
+                    ws_[j] = mma(load_pieces<kData>(lds + Lds::kX + (((t0 + t) * 2 + j) * 64 + lane) * 16, kPlane), dhp[j], zero);
+                }
+                const v4f u = opposite(us_), w = opposite(ws_);
+                acc_c[t] += u * *reinterpret_cast<const v4f*>(arrays + kDecay * kChunk + (t0 + t) * 16 + 4 * q);
+                acc_b[t] += w * *reinterpret_cast<const v4f*>(arrays + kWeight * kChunk + (t0 + t) * 16 + 4 * q);
+                v4f us;
+#pragma unroll
+                for (int v = 0; v < 4; ++v) us[v] = row_sum(u[v] * c_at[t][v]);
+                if (r == 0) *reinterpret_cast<v4f*>(part + Lds::kU + nt * kChunk + (t0 + t) * 16 + 4 * q) = us;
+            }
+            pass = row_sum(pass);
+            pass += __shfl_xor(pass, 16);
+            pass += __shfl_xor(pass, 32);
+            if (lane == 0) passes[wave] = t0 == 0 ? pass : 0.0;
+        }
+        // for dx: the state's gradient along the state
+        v4f dh_rows[2 * kSteps];
+        {
+            const RowBuffer<false> dh(s.ends, 0, 0, 1, ((int64_t)c * a.H + head) * kP * kN, kP * kN);
+#pragma unroll
+            for (int n = 0; n < 2 * kSteps; ++n) dh_rows[n] = dh.load4(((pt * 16 + r) * kN + 4 * q + n * 16) * 4);
+        }
+        __builtin_amdgcn_sched_barrier(0);
         {   // M, K L, E: columns s along the lanes
             const float s_dt = arrays[kStep * kChunk + st * 16 + r];
             double column = 0.0;
@@ -191,12 +294,13 @@ __global__ __launch_bounds__(kThreads, 2) void scan_grad_kernel(ScanGradArgs s) 
                     for (int n = st + 1; n < tt; ++n) behind *= arrays[kEnter * kChunk + n * 16 + 15];
                     f = behind * *reinterpret_cast<const v4f*>(arrays + kEnter * kChunk + tt * 16 + 4 * q);
                 }
+                const v4f product = *reinterpret_cast<const v4f*>(lds + Lds::kK + ((tt * 4 + st) * 64 + lane) * 16);
                 float kl[8];
                 double rows[4];
 #pragma unroll
                 for (int v = 0; v < 4; ++v) {
                     const bool strict = tt > st || 4 * q + v > r;
-                    kl[v] = products[i][v] * f[v];
+                    kl[v] = product[v] * f[v];
                     kl[v + 4] = 0.0f;
                     const float e = m[v] * kl[v];
                     sum_w[i][v] = fmaf(m[v] * f[v], s_dt, sum_w[i][v]);
@@ -215,76 +319,42 @@ __global__ __launch_bounds__(kThreads, 2) void scan_grad_kernel(ScanGradArgs s) 
                 if (r == 0)
 #pragma unroll
                     for (int v = 0; v < 4; ++v) row_sums[st * kChunk + tt * 16 + 4 * q + v] = rows[v];
-                __builtin_amdgcn_sched_barrier(0);
             }
             column += __shfl_xor(column, 16);
             column += __shfl_xor(column, 32);
             if (q == 0) column_sums[half * kChunk + st * 16 + r] = column;
         }
-        __builtin_amdgcn_sched_barrier(0);
-        {   // dC and dB through the states
-            const int from_c = opaque(4 * q * (int)a.ldc + r) * kSize, from_b = opaque(4 * q * (int)a.ldb + r) * kSize;
-            const Pieces<kFull> hp[2] = {split<kFull>(h_at[0]), split<kFull>(h_at[1])};
-            const Pieces<kFull> dhp[2] = {split<kFull>(dh_at[0]), split<kFull>(dh_at[1])};
-#pragma unroll
-            for (int t = 0; t < kTT; ++t) {
-                v4f us_[2], ws_[2];
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const v4f zero = {0.0f, 0.0f, 0.0f, 0.0f};
-                    us_[j] = mma(load_pieces<kData>(lds + Lds::kDy + (((t0 + t) * 2 + j) * 64 + lane) * 16, kPlane), hp[j], zero);
-                    ws_[j] = mma(load_pieces<kData>(lds + Lds::kX + (((t0 + t) * 2 + j) * 64 + lane) * 16, kPlane), dhp[j], zero);
-                }
-                const v4f u = opposite(us_), w = opposite(ws_);
-                acc_c[t] += u * *reinterpret_cast<const v4f*>(arrays + kDecay * kChunk + (t0 + t) * 16 + 4 * q);
-                acc_b[t] += w * *reinterpret_cast<const v4f*>(arrays + kWeight * kChunk + (t0 + t) * 16 + 4 * q);
-                v4f us, ws;
-#pragma unroll
-                for (int v = 0; v < 4; ++v) {
-                    us[v] = row_sum(u[v] * c_rows.load(from_c + ((t0 + t) * 16 + v) * (int)a.ldc * kSize));
-                    ws[v] = row_sum(w[v] * b_rows.load(from_b + ((t0 + t) * 16 + v) * (int)a.ldb * kSize));
-                }
-                if (r == 0) {
-                    *reinterpret_cast<v4f*>(part + Lds::kU + nt * kChunk + (t0 + t) * 16 + 4 * q) = us;
-                    *reinterpret_cast<v4f*>(part + Lds::kV + nt * kChunk + (t0 + t) * 16 + 4 * q) = ws;
-                }
-                __builtin_amdgcn_sched_barrier(0);
-            }
-            double pass = 0.0;
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-#pragma unroll
-                for (int j = 0; j < 8; ++j) pass += (double)(i ? -h_at[i][j] : h_at[i][j]) * (double)dh_at[i][j];
-            pass = row_sum(pass);
-            pass += __shfl_xor(pass, 16);
-            pass += __shfl_xor(pass, 32);
-            if (lane == 0) passes[wave] = t0 == 0 ? pass : 0.0;
-        }
         __syncthreads();
-        {   // dx
-            const RowBuffer<kBf16> dy_rows(s.dy, ch.x, s.lddy, ch.y, head * kP + pt * 16, 16);
-            const int from_dy = opaque(4 * q * (int)s.lddy + r) * kSize;
-            const int from_dh = opaque((pt * 16 + r) * kN + 4 * q);
-            float dy[2][8];
+        float dy[2][8], x_at[2][4];     // dy across the tokens, and x where dx lies
+        {
+            const RowBuffer<kBf16> dy_rows(s.dy, ch.x, s.lddy, ch.y, head * kP + pt * 16, 16), x_rows(a.x, ch.x, a.ldx, ch.y, head * kP + pt * 16, 16);
+            const int from_dy = (4 * q * (int)s.lddy + r) * kSize, from_x = ((sh * 32 + 4 * q) * (int)a.ldx + r) * kSize;
 #pragma unroll
             for (int i = 0; i < 2; ++i)
 #pragma unroll
                 for (int j = 0; j < 8; ++j) dy[i][j] = dy_rows.load(from_dy + (i * 32 + place(0, j)) * (int)s.lddy * kSize);
-            v4f inter[2], intra[2];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) inter[i] = intra[i] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int v = 0; v < 4; ++v) x_at[i][v] = x_rows.load(from_x + (i * 16 + v) * (int)a.ldx * kSize);
+        }
+        load_rows(k + 1 < last ? k + 1 : k, r, q);
+        __builtin_amdgcn_sched_barrier(0);
+        {   // dx
+            v4f halves[2][2] = {}, intra[2] = {};
 #pragma unroll
             for (int n = 0; n < kSteps; ++n) {
-                const float* const from = dh + from_dh + n * 32;
-                const v4f lo = *reinterpret_cast<const v4f*>(from), hi = *reinterpret_cast<const v4f*>(from + 16);
-                const float f[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-                const Pieces<kOut> state = split<kOut>(f);
+                const v4f lo = dh_rows[2 * n], hi = dh_rows[2 * n + 1];
+                const float sign = n & 1 ? -1.0f : 1.0f;
+                const float f[8] = {sign * lo.x, sign * lo.y, sign * lo.z, sign * lo.w, sign * hi.x, sign * hi.y, sign * hi.z, sign * hi.w};
+                const Pieces<kFull> state = split<kFull>(f);   // (ddt takes of it, too)
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
-                    inter[i] = mma(load_pieces<kData>(lds + Lds::kRows + (((2 * sh + i) * kSteps + n) * 64 + lane) * 16, Block::kPlane),
-                                   state, inter[i]);
-                __builtin_amdgcn_sched_barrier(0);
+                    halves[i][n & 1] = mma(load_pieces<kData>(lds + Lds::kRows + (((2 * sh + i) * kSteps + n) * 64 + lane) * 16, Block::kPlane),
+                                           state, halves[i][n & 1]);
             }
+
+            __builtin_amdgcn_sched_barrier(0);
             const Pieces<kData> rows[2] = {split<kData>(dy[0]), split<kData>(dy[1])};
 #pragma unroll
             for (int i = 0; i < 2; ++i)
@@ -294,68 +364,28 @@ __global__ __launch_bounds__(kThreads, 2) void scan_grad_kernel(ScanGradArgs s) 
                         intra[i] = mma(load_pieces<kOut>(lds + Lds::kW + (((2 * sh + i) * 2 + j) * 64 + lane) * 16, kPlane), rows[j], intra[i]);
             const float skip = a.D[head];
             const RowBuffer<kBf16> dx_rows(s.dx, ch.x, s.lddx, ch.y, head * kP + pt * 16, 16);
-            const int to = opaque(4 * q * (int)s.lddx + r) * kSize;
+            const int to = (4 * q * (int)s.lddx + r) * kSize;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int tile = 2 * sh + i;
                 const v4f dt = *reinterpret_cast<const v4f*>(arrays + kStep * kChunk + tile * 16 + 4 * q);
                 const v4f weight = *reinterpret_cast<const v4f*>(arrays + kWeight * kChunk + tile * 16 + 4 * q);
+                const v4f inter = opposite(halves[i]);
+                v4f along;     // x . (g B)
 #pragma unroll
                 for (int v = 0; v < 4; ++v) {
+                    along[v] = row_sum(x_at[i][v] * inter[v]);
                     const float own = sh == 0 ? dy[0][i * 4 + v] : dy[1][i * 4 + v];
-                    dx_rows.store(fmaf(skip, own, fmaf(dt[v], intra[i][v], weight[v] * inter[i][v])),
+                    dx_rows.store(fmaf(skip, own, fmaf(dt[v], intra[i][v], weight[v] * inter[v])),
                                   to + (tile * 16 + v) * (int)s.lddx * kSize);
                 }
+                if (r == 0) *reinterpret_cast<v4f*>(part + Lds::kV + pt * kChunk + tile * 16 + 4 * q) = along;
             }
         }
         __builtin_amdgcn_sched_barrier(0);
-        if (wave == (k & 7)) {   // ddt and the parameters' sums, a token a lane
-            const float hi = arrays[lane], lo = arrays[kCsLo * kChunk + lane], dt = arrays[kStep * kChunk + lane];
-            const float end_hi = arrays[kChunk - 1], end_lo = arrays[kCsLo * kChunk + kChunk - 1];
-            double rows = 0.0;
-            float u = 0.0f, v = 0.0f;
-            double pass = 0.0;
-            for (int i = 0; i <= lane >> 4; ++i) rows += row_sums[i * kChunk + lane];
-#pragma unroll
-            for (int i = 0; i < kTiles; ++i) {
-                u += part[Lds::kU + i * kChunk + lane];
-                v += part[Lds::kV + i * kChunk + lane];
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) pass += passes[i];
-            const double columns = column_sums[lane] + column_sums[kChunk + lane];
-            u *= arrays[kDecay * kChunk + lane];
-            v *= __builtin_amdgcn_exp2f((end_hi - hi) + (end_lo - lo));
-            pass *= arrays[kDecay * kChunk + kChunk - 1];
-            const float z = (float)columns + part[Lds::kDiag + lane] + v;    // x . (dh B)
-            // from t on: rows of E and u, less the columns from t on (pairs that lie behind t whole); before t: v
-            double from = rows + (double)u - (double)dt * columns, before = (double)dt * (double)v;
-            const double own = before;
-#pragma unroll
-            for (int d = 1; d < 64; d <<= 1) {
-                const double o = __shfl_down(from, d), p = __shfl_up(before, d);
-                if (lane + d < 64) from += o;
-                if (lane >= d) before += p;
-            }
-            const float da = (float)(from + (before - own) + pass);
-            const float rate = expf(a.A_log[head]);
-            float raw = 0.0f, ddt = 0.0f;
-            if (lane < ch.y) {
-                raw = a.dt[(int64_t)(ch.x + lane) * a.lddt + head] + a.dt_bias[head];
-                ddt = (z - rate * da) * (raw > 20.0f ? 1.0f : 1.0f / (1.0f + expf(-raw)));
-                s.ddt[(int64_t)(ch.x + lane) * s.ldddt + head] = ddt;
-            }
-            float sum_a = -rate * dt * da, sum_d = part[Lds::kDot + lane], sum_t = ddt;
-#pragma unroll
-            for (int d = 1; d < 64; d <<= 1) {
-                sum_a += __shfl_xor(sum_a, d);
-                sum_d += __shfl_xor(sum_d, d);
-                sum_t += __shfl_xor(sum_t, d);
-            }
-            if (lane == 0)
-                *reinterpret_cast<v4f*>(s.sums + ((int64_t)c * a.H + head) * kSums) = v4f{sum_a, sum_d, sum_t, 0.0f};
-        }
     }
+    __syncthreads();
+    if (wave == ((last - 1) & 7)) finish(last - 1, lane);
 
     // dC += W B and dB += W^T C with W the heads' sum of M L dt
     __syncthreads();
@@ -403,7 +433,7 @@ __global__ __launch_bounds__(kThreads, 2) void scan_grad_kernel(ScanGradArgs s) 
         }
 }
 
-// dB and dC: the slices' shares in their order; workgroups (chunk, group).
+// dB and dC: the slices' shares in their order; workgroups (chunk, group, a part of the rows).
 template <bool kBf16, int kN>
 __global__ __launch_bounds__(256) void join_slabs_kernel(ScanGradArgs s) {
     using E = Elem<kBf16>;
@@ -413,16 +443,15 @@ __global__ __launch_bounds__(256) void join_slabs_kernel(ScanGradArgs s) {
     const int4 ch = chunk_of(a, c);
     if (ch.z < 0) return;
     const int64_t step = (int64_t)a.nchunks * a.G * 2 * kChunk * kN;
-    for (int i = threadIdx.x; i < 2 * kChunk * kN / 4; i += 256) {
-        const int which = i / (kChunk * kN / 4), row = i / (kN / 4) % kChunk, n = i % (kN / 4) * 4;
-        if (row >= ch.y) continue;
-        const float* const from = s.slabs + (((int64_t)c * a.G + g) * 2 + which) * kChunk * kN + row * kN + n;
-        v4f v = *reinterpret_cast<const v4f*>(from);
+    const int i = blockIdx.z * 256 + threadIdx.x;
+    const int which = i / (kChunk * kN / 4), row = i / (kN / 4) % kChunk, n = i % (kN / 4) * 4;
+    if (row >= ch.y) return;
+    const float* const from = s.slabs + (((int64_t)c * a.G + g) * 2 + which) * kChunk * kN + row * kN + n;
+    v4f v = *reinterpret_cast<const v4f*>(from);
 #pragma unroll 4
-        for (int k = 1; k < s.slices; ++k) v += *reinterpret_cast<const v4f*>(from + k * step);
-        if (which == 0) E::store4(static_cast<T*>(s.dB) + (int64_t)(ch.x + row) * s.lddb + g * kN + n, v);
-        else E::store4(static_cast<T*>(s.dC) + (int64_t)(ch.x + row) * s.lddc + g * kN + n, v);
-    }
+    for (int k = 1; k < s.slices; ++k) v += *reinterpret_cast<const v4f*>(from + k * step);
+    if (which == 0) E::store4(static_cast<T*>(s.dB) + (int64_t)(ch.x + row) * s.lddb + g * kN + n, v);
+    else E::store4(static_cast<T*>(s.dC) + (int64_t)(ch.x + row) * s.lddc + g * kN + n, v);
 }
 
 // The parameters' gradients of a head: the chunks' sums, each thread every 256th, then the threads in a tree.
@@ -529,7 +558,7 @@ hipError_t launch_mamba2_scan_backward(ScanArgs a, bool bf16, int N, const float
         scan_grad_kernel<b.value, n.value><<<dim3((unsigned)a.nchunks, (unsigned)(a.G * g.slices)), kThreads, 0, stream>>>(g);
         if (hipError_t err = hipGetLastError()) return err;
         if (g.slices > 1) {
-            join_slabs_kernel<b.value, n.value><<<dim3((unsigned)a.nchunks, (unsigned)a.G), 256, 0, stream>>>(g);
+            join_slabs_kernel<b.value, n.value><<<dim3((unsigned)a.nchunks, (unsigned)a.G, kChunk * n.value / 512), 256, 0, stream>>>(g);
             if (hipError_t err = hipGetLastError()) return err;
         }
         join_sums_kernel<<<dim3((unsigned)a.H), 256, 0, stream>>>(a, parts.sums, dA_log, dD, ddt_bias);

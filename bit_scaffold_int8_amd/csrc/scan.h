@@ -87,20 +87,30 @@ struct Pieces {
     v8bf p[kPieces];
 };
 
+// (Two values at a time by their bits: written element by element, each piece is converted once to be kept and once more
+// to be taken off.)
 template <int kPieces>
 __device__ __forceinline__ Pieces<kPieces> split(const float (&x)[8]) {
+    typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
+    typedef float v2f __attribute__((ext_vector_type(2)));
+    typedef uint32_t v4u __attribute__((ext_vector_type(4)));
     Pieces<kPieces> out;
     float r[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) r[j] = x[j];
 #pragma unroll
-    for (int i = 0; i < kPieces; ++i)
+    for (int i = 0; i < kPieces; ++i) {
+        v4u bits;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const __bf16 b = (__bf16)r[j];
-            out.p[i][j] = b;
-            if (i + 1 < kPieces) r[j] -= (float)b;
+        for (int j = 0; j < 4; ++j) {
+            bits[j] = __builtin_bit_cast(uint32_t, __builtin_convertvector((v2f{r[2 * j], r[2 * j + 1]}), v2bf));
+            if (i + 1 < kPieces) {
+                r[2 * j] -= __uint_as_float(bits[j] << 16);
+                r[2 * j + 1] -= __uint_as_float(bits[j] & 0xFFFF0000u);
+            }
         }
+        out.p[i] = __builtin_bit_cast(v8bf, bits);
+    }
     return out;
 }
 

@@ -74,7 +74,7 @@ template <bool kBf16>
 struct RowBuffer {
     __amdgpu_buffer_rsrc_t rsrc;
     static constexpr int kSize = kBf16 ? 2 : 4;
-    __device__ __forceinline__ RowBuffer(const void* base, int64_t first, int64_t ld, int rows, int col, int width)
+    __device__ __forceinline__ RowBuffer(const void* base, int64_t first, int64_t ld, int rows, int64_t col, int width)
         : rsrc(make_rsrc(static_cast<const uint8_t*>(base) + (first * ld + col) * kSize,
                          (uint32_t)(((rows - 1) * (uint32_t)ld + (uint32_t)width) * kSize))) {}
     __device__ __forceinline__ float load(int bytes) const {

@@ -292,6 +292,7 @@ __global__ __launch_bounds__(kSweepThreads, 2) void sweep_kernel(SweepArgs s) {
     const int count = chunk_of(a, sg.x).y > 0 ? sg.y : 0;   // (a sequence without tokens has one empty chunk)
 
     float v[2][2][8];
+    typename RowBuffer<kBf16>::Pair raw[2][8];
     auto load_v = [&](int i) {   // the chunk's rows of v, places of the sums along its tokens; zero behind the sequence
         const int4 ch = chunk_of(a, chunk_at(i));
         const RowBuffer<kBf16> rows(s.v, ch.x, s.ldv, ch.y, head * kP + half * 32, 32);
@@ -299,10 +300,15 @@ __global__ __launch_bounds__(kSweepThreads, 2) void sweep_kernel(SweepArgs s) {
 #pragma unroll
         for (int k = 0; k < 2; ++k)
 #pragma unroll
+            for (int j = 0; j < 8; ++j) raw[k][j] = rows.load2(own + (k * 32 + place(0, j)) * (int)s.ldv * kSize);
+    };
+    auto take_v = [&]() {
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const float2 pair = rows.load2(own + (k * 32 + place(0, j)) * (int)s.ldv * kSize);
-                v[k][0][j] = pair.x;
-                v[k][1][j] = pair.y;
+                v[k][0][j] = RowBuffer<kBf16>::first(raw[k][j]);
+                v[k][1][j] = RowBuffer<kBf16>::second(raw[k][j]);
             }
     };
     if (count > 0) {
@@ -322,6 +328,7 @@ __global__ __launch_bounds__(kSweepThreads, 2) void sweep_kernel(SweepArgs s) {
             load_v(i);
             if constexpr (kBf16) next_key.load(block_of(c) + s.key, Block::kSet);
             __builtin_amdgcn_sched_barrier(0);   // (or the loads would sink to where they are used)
+            take_v();
             v4f y[4][2];
 #pragma unroll
             for (int t = 0; t < 4; ++t) y[t][0] = y[t][1] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
@@ -342,6 +349,7 @@ __global__ __launch_bounds__(kSweepThreads, 2) void sweep_kernel(SweepArgs s) {
                     y[t][1] = mma(cr, state[1], y[t][1]);
                 }
             }
+            read_ahead<kData, 2 * products_of(kData, kOut), 4 * kSteps, 2>();
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
                 const v4f e = sigma * at4(arrays + kDecay * kChunk + t * 16 + 4 * q);
@@ -414,10 +422,13 @@ __global__ __launch_bounds__(kSweepThreads, 2) void sweep_kernel(SweepArgs s) {
             }
             __builtin_amdgcn_sched_barrier(0);
         } else {
-            if (i + 1 < count) {
+            take_v();
+            if (i + 1 < count) {   // (before the stores: a wait for loads waits for the stores before them)
                 load_arrays(i + 1);
                 next_key.load(block_of(chunk_at(i + 1)) + s.key, Block::kSet);
+                load_v(i + 1);
             }
+            __builtin_amdgcn_sched_barrier(0);
             if (kMode == kStarts && live) {
                 float* const out = s.starts + ((int64_t)c * a.H + head) * kP * kN + opaque(p0 * kN + 4 * q);
 #pragma unroll
@@ -442,20 +453,23 @@ __global__ __launch_bounds__(kSweepThreads, 2) void sweep_kernel(SweepArgs s) {
                 in[k][p] = split<kInto>(f);
             }
         }
-        if (!kY && i + 1 < count) load_v(i + 1);
         __builtin_amdgcn_sched_barrier(0);
         const uint8_t* const keys = (!kY && (i & 1) ? first_lds : key_lds) + lane * 16;
 #pragma unroll
         for (int n = 0; n < kTiles; ++n) {
             const Pieces<kData> key0 = load_pieces<kData>(keys + n * 2048, Block::kPlane);
             const Pieces<kData> key1 = load_pieces<kData>(keys + n * 2048 + 1024, Block::kPlane);
+            v4f add[2];
+#pragma unroll
+            for (int p = 0; p < 2; ++p) add[p] = mma(key0, in[0][p], v4f{0.0f, 0.0f, 0.0f, 0.0f});
 #pragma unroll
             for (int p = 0; p < 2; ++p) {
-                const v4f add = mma(key1, in[1][p], mma(key0, in[0][p], v4f{0.0f, 0.0f, 0.0f, 0.0f}));
+                add[p] = mma(key1, in[1][p], add[p]);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) h[n][p][j] = fmaf(h[n][p][j], -last, add[j]);
+                for (int j = 0; j < 4; ++j) h[n][p][j] = fmaf(h[n][p][j], -last, add[p][j]);
             }
         }
+        read_ahead<kData, 2 * products_of(kData, kInto), 2 * kTiles, 2>();
         sigma = -sigma;
     }
     if (!live) return;

@@ -8,6 +8,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "device_common.h"
 
 namespace dfssm {
@@ -90,15 +92,19 @@ struct RowBuffer {
             return __builtin_bit_cast(v4f, __builtin_amdgcn_raw_buffer_load_b128(rsrc, bytes, 0, 0));
         }
     }
-    // two neighbours (an even place)
-    __device__ __forceinline__ float2 load2(int bytes) const {
-        if constexpr (kBf16) {
-            const uint32_t v = __builtin_amdgcn_raw_buffer_load_b32(rsrc, bytes, 0, 0);
-            return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
-        } else {
-            const auto v = __builtin_amdgcn_raw_buffer_load_b64(rsrc, bytes, 0, 0);
-            return make_float2(__uint_as_float(v[0]), __uint_as_float(v[1]));
-        }
+    // two neighbours (an even place), as they lie in memory
+    using Pair = std::conditional_t<kBf16, uint32_t, uint64_t>;
+    __device__ __forceinline__ Pair load2(int bytes) const {
+        if constexpr (kBf16) return __builtin_amdgcn_raw_buffer_load_b32(rsrc, bytes, 0, 0);
+        else return __builtin_bit_cast(uint64_t, __builtin_amdgcn_raw_buffer_load_b64(rsrc, bytes, 0, 0));
+    }
+    static __device__ __forceinline__ float first(Pair v) {
+        if constexpr (kBf16) return __uint_as_float(v << 16);
+        else return __uint_as_float((uint32_t)v);
+    }
+    static __device__ __forceinline__ float second(Pair v) {
+        if constexpr (kBf16) return __uint_as_float(v & 0xFFFF0000u);
+        else return __uint_as_float((uint32_t)(v >> 32));
     }
     __device__ __forceinline__ void store2(float x, float y, int bytes) const {
         if constexpr (kBf16) {

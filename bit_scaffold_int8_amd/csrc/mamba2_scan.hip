@@ -141,24 +141,29 @@ __device__ void head_arrays(const ScanArgs& a, const int4& ch, int c, int h) {
     out[kLeave * kChunk] = dt * __builtin_amdgcn_exp2f((float)(behind - cs));
 }
 
-// Workgroups (chunk, y): y below G the group's products and pieces, behind them the decays of four heads each.
+// Workgroups (chunk, y): y below G a group's products and its pieces along the state, below 2 G those across the tokens, behind
+// them the decays of 16 heads each.
+constexpr int kPrepareWaves = 8, kPrepareHeads = 2 * kPrepareWaves;
 template <bool kBf16, int kN, bool kBackward>
-__global__ __launch_bounds__(256) void prepare_kernel(ScanArgs a) {
-    constexpr int kPieces = kBf16 ? 1 : 3, kLd = kN + 4, kTiles = kN / 16, kSteps = kN / 32;
+__global__ __launch_bounds__(kPrepareWaves * 64) void prepare_kernel(ScanArgs a) {
+    constexpr int kPieces = kBf16 ? 1 : 3, kLd = kN + 4, kTiles = kN / 16, kSteps = kN / 32, kThreads = kPrepareWaves * 64;
     using Block = GroupBlock<kN, kPieces>;
     __shared__ __attribute__((aligned(16))) float rows[2][kChunk * kLd];
     const int c = blockIdx.x;
     const int4 ch = chunk_of(a, c);
     if (ch.z < 0 || ch.y <= 0) return;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    if ((int)blockIdx.y >= a.G) {
-        const int h = ((int)blockIdx.y - a.G) * 4 + wave;
-        if (h < a.H) head_arrays(a, ch, c, h);
+    if ((int)blockIdx.y >= 2 * a.G) {
+        for (int h = ((int)blockIdx.y - 2 * a.G) * kPrepareHeads + wave, n = 0; n < 2; ++n, h += kPrepareWaves)
+            if (h < a.H) head_arrays(a, ch, c, h);
         return;
     }
-    const int g = blockIdx.y;
+    const bool is_across = (int)blockIdx.y >= a.G;
+    const int g = is_across ? blockIdx.y - a.G : blockIdx.y;
     using E = Elem<kBf16>;
-    for (int i = tid; i < 2 * kChunk * (kN / 4); i += 256) {
+    const int matrices = is_across && !kBackward ? 1 : 2;     // (forward, B alone is wanted across the tokens)
+#pragma unroll 4
+    for (int i = tid; i < matrices * kChunk * (kN / 4); i += kThreads) {
         const int which = i / (kChunk * (kN / 4)), r = i / (kN / 4) % kChunk, k = i % (kN / 4) * 4;
         const int64_t at = (int64_t)(ch.x + (r < ch.y ? r : 0)) * (which ? a.ldc : a.ldb) + g * kN + k;
         v4f v = E::load4(static_cast<const typename E::type*>(which ? a.C : a.B) + at);
@@ -181,13 +186,21 @@ __global__ __launch_bounds__(256) void prepare_kernel(ScanArgs a) {
         for (int j = 0; j < 8; ++j) v[j] = rows[which][(step * 32 + place(q, j)) * kLd + tile * 16 + r];
         return split<kPieces>(v);
     };
+    if (is_across) {
+        for (int i = wave; i < kTiles * 2; i += kPrepareWaves) {
+            store_pieces(out + Block::kAcross + (i * 64 + lane) * 16, Block::kPlane, across(0, i / 2, i % 2));
+            if constexpr (kBackward)
+                store_pieces(out + Block::kCross + (i * 64 + lane) * 16, Block::kPlane, across(1, i / 2, i % 2));
+        }
+        return;
+    }
     // products: forward rows s, columns t (s <= t); backward rows t, columns s
     constexpr int kRowSide = kBackward ? 1 : 0;
     int n = 0;
     for (int rt = 0; rt < 4; ++rt)
         for (int ct = 0; ct < 4; ++ct) {
             if (kBackward ? ct > rt : ct < rt) continue;
-            if ((n++ & 3) != wave) continue;
+            if (n++ % kPrepareWaves != wave) continue;
             v4f acc[2] = {};
             for (int k = 0; k < kSteps; k += 2) {
                 acc[0] = mma(along(kRowSide, rt, k), along(1 - kRowSide, ct, k), acc[0]);
@@ -195,13 +208,8 @@ __global__ __launch_bounds__(256) void prepare_kernel(ScanArgs a) {
             }
             *reinterpret_cast<v4f*>(out + ((rt * 4 + ct) * 64 + lane) * 16) = opposite(acc);
         }
-    for (int i = wave; i < 4 * kSteps; i += 4)
+    for (int i = wave; i < 4 * kSteps; i += kPrepareWaves)
         store_pieces(out + Block::kRows + (i * 64 + lane) * 16, Block::kPlane, along(1 - kRowSide, i / kSteps, i % kSteps));
-    for (int i = wave; i < kTiles * 2; i += 4) {
-        store_pieces(out + Block::kAcross + (i * 64 + lane) * 16, Block::kPlane, across(0, i / 2, i % 2));
-        if constexpr (kBackward)
-            store_pieces(out + Block::kCross + (i * 64 + lane) * 16, Block::kPlane, across(1, i / 2, i % 2));
-    }
 }
 
 // ---------------------------------------------------------------- the sweep
@@ -578,9 +586,9 @@ hipError_t launch_scan_prepare(const ScanArgs& a, bool bf16, int N, bool backwar
         if (hipError_t err = hipGetLastError()) return err;
     }
     return with_kind(bf16, N, [&](auto b, auto n) {
-        const dim3 grid((unsigned)a.nchunks, (unsigned)(a.G + (a.H + 3) / 4));
-        if (backward) prepare_kernel<b.value, n.value, true><<<grid, 256, 0, stream>>>(a);
-        else prepare_kernel<b.value, n.value, false><<<grid, 256, 0, stream>>>(a);
+        const dim3 grid((unsigned)a.nchunks, (unsigned)(2 * a.G + (a.H + kPrepareHeads - 1) / kPrepareHeads));
+        if (backward) prepare_kernel<b.value, n.value, true><<<grid, kPrepareWaves * 64, 0, stream>>>(a);
+        else prepare_kernel<b.value, n.value, false><<<grid, kPrepareWaves * 64, 0, stream>>>(a);
         return hipGetLastError();
     });
 }

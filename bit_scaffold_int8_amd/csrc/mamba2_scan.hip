@@ -326,7 +326,7 @@ __global__ __launch_bounds__(kSweepThreads, 2) void sweep_kernel(SweepArgs s) {
         if constexpr (!kY) load_v(0);
     }
     for (int i = 0; i < count; ++i) {
-        const int c = chunk_at(i);
+        const int c = chunk_at(i), following = i + 1 < count ? i + 1 : i;   // (the last chunk's loads are idle ones: no branch)
         const float* const arrays = reinterpret_cast<const float*>(head_lds[i & 1]) + (live ? wave >> 1 : 0) * kHeadArrays * kChunk;
         next_arrays.store(head_lds[i & 1]);
         if constexpr (kY) next_first.store(first_lds);
@@ -335,8 +335,6 @@ __global__ __launch_bounds__(kSweepThreads, 2) void sweep_kernel(SweepArgs s) {
         if constexpr (kY) {
             load_v(i);
             if constexpr (kBf16) next_key.load(block_of(c) + s.key, Block::kSet);
-            __builtin_amdgcn_sched_barrier(0);   // (or the loads would sink to where they are used)
-            take_v();
             v4f y[4][2];
 #pragma unroll
             for (int t = 0; t < 4; ++t) y[t][0] = y[t][1] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
@@ -357,13 +355,14 @@ __global__ __launch_bounds__(kSweepThreads, 2) void sweep_kernel(SweepArgs s) {
                     y[t][1] = mma(cr, state[1], y[t][1]);
                 }
             }
-            read_ahead<kData, 2 * products_of(kData, kOut), 4 * kSteps, 2>();
+            read_ahead<kData, 2 * products_of(kData, kOut), 4 * kSteps, 2, 16 + (kBf16 ? Staged<Block::kSet>::kEach : 0)>();
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
                 const v4f e = sigma * at4(arrays + kDecay * kChunk + t * 16 + 4 * q);
                 y[t][0] *= e;
                 y[t][1] *= e;
             }
+            take_v();
             float enter[4], between[4];     // between[t]: the decay of tile t as a whole
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
@@ -424,25 +423,23 @@ __global__ __launch_bounds__(kSweepThreads, 2) void sweep_kernel(SweepArgs s) {
             }
             next_key.store(key_lds);
             lds_barrier();
-            if (i + 1 < count) {
-                load_arrays(i + 1);
-                next_first.load(block_of(chunk_at(i + 1)), kFirst);
-            }
-            __builtin_amdgcn_sched_barrier(0);
+            load_arrays(following);
+            next_first.load(block_of(chunk_at(following)), kFirst);
         } else {
             take_v();
-            if (i + 1 < count) {   // (before the stores: a wait for loads waits for the stores before them)
-                load_arrays(i + 1);
-                next_key.load(block_of(chunk_at(i + 1)) + s.key, Block::kSet);
-                load_v(i + 1);
-            }
-            __builtin_amdgcn_sched_barrier(0);
-            if (kMode == kStarts && live) {
-                float* const out = s.starts + ((int64_t)c * a.H + head) * kP * kN + opaque(p0 * kN + 4 * q);
+            // (before the stores: a wait for loads waits for the stores before them)
+            load_arrays(following);
+            next_key.load(block_of(chunk_at(following)) + s.key, Block::kSet);
+            load_v(following);
+            if constexpr (kMode == kStarts) {
+                const __amdgpu_buffer_rsrc_t out =
+                    make_rsrc(s.starts + ((int64_t)c * a.H + head) * kP * kN, live ? kP * kN * 4 : 0);
+                const int to = opaque(p0 * kN + 4 * q) * 4;
 #pragma unroll
                 for (int n = 0; n < kTiles; ++n)
 #pragma unroll
-                    for (int p = 0; p < 2; ++p) *reinterpret_cast<v4f*>(out + p * kN + n * 16) = sigma * h[n][p];
+                    for (int p = 0; p < 2; ++p)
+                        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4u, sigma * h[n][p]), out, to + (p * kN + n * 16) * 4, 0, 0);
             }
         }
         const float last = arrays[kDecay * kChunk + kChunk - 1];
@@ -461,7 +458,6 @@ __global__ __launch_bounds__(kSweepThreads, 2) void sweep_kernel(SweepArgs s) {
                 in[k][p] = split<kInto>(f);
             }
         }
-        __builtin_amdgcn_sched_barrier(0);
         const uint8_t* const keys = (!kY && (i & 1) ? first_lds : key_lds) + lane * 16;
 #pragma unroll
         for (int n = 0; n < kTiles; ++n) {
@@ -477,7 +473,7 @@ __global__ __launch_bounds__(kSweepThreads, 2) void sweep_kernel(SweepArgs s) {
                 for (int j = 0; j < 4; ++j) h[n][p][j] = fmaf(h[n][p][j], -last, add[p][j]);
             }
         }
-        read_ahead<kData, 2 * products_of(kData, kInto), 2 * kTiles, 2>();
+        read_ahead<kData, 2 * products_of(kData, kInto), 2 * kTiles, 2, kY ? 1 + Staged<kFirst>::kEach : 17 + Staged<Block::kSet>::kEach>();
         sigma = -sigma;
     }
     if (!live) return;

@@ -24,6 +24,7 @@ namespace dfssm {
 
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 typedef __bf16 v4bf __attribute__((ext_vector_type(4)));
+typedef uint32_t v4u __attribute__((ext_vector_type(4)));
 
 constexpr int kChunk = 64;     // tokens of a chunk
 constexpr int kP = 64;         // channels of a head
@@ -93,7 +94,6 @@ template <int kPieces>
 __device__ __forceinline__ Pieces<kPieces> split(const float (&x)[8]) {
     typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
     typedef float v2f __attribute__((ext_vector_type(2)));
-    typedef uint32_t v4u __attribute__((ext_vector_type(4)));
     Pieces<kPieces> out;
     float r[8];
 #pragma unroll
@@ -136,13 +136,15 @@ constexpr int products_of(int a, int b) {
 // The order of a stretch of steps that each read fragments from LDS and multiply them: the reads of the next kAhead
 // steps go out before a step's products (left alone, the compiler reads a step's fragments right before its products, and with two waves
 // a SIMD the latency is most of the time: 16384 tokens' sweep 148 us, with this order 121).
-template <int kReads, int kProducts, int kCount, int kAhead>
+// kLoads loads from memory go out with the first steps, one each: all at once they hold up what comes behind them.
+template <int kReads, int kProducts, int kCount, int kAhead, int kLoads>
 __device__ __forceinline__ void read_ahead() {
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) __builtin_amdgcn_sched_group_barrier(0x100, kReads, 0);   // LDS reads
 #pragma unroll
     for (int i = 0; i < kCount; ++i) {
         __builtin_amdgcn_sched_group_barrier(0x008, kProducts, 0);                             // matrix instructions
+        if (i < kLoads) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);                     // loads
         if (i + kAhead < kCount) __builtin_amdgcn_sched_group_barrier(0x100, kReads, 0);
     }
     __builtin_amdgcn_sched_barrier(0);

@@ -254,8 +254,11 @@ __global__ __launch_bounds__(kSweepThreads, 2) void sweep_kernel(SweepArgs s) {
     constexpr bool kY = kMode == kOutput;
     constexpr int kFirst = Block::kG + Block::kSet, kArrays = kSweepHeads * kHeadArrays * kChunk * 4;
     static_assert(Block::kRows == Block::kG, "the products and C's rows lie side by side");
-    __shared__ __attribute__((aligned(16))) uint8_t first_lds[kY ? kFirst : Block::kSet];
-    __shared__ __attribute__((aligned(16))) uint8_t key_lds[Block::kSet];
+    // y's two parts twice where there is room (bf16), so that a chunk needs one barrier and the waves drift apart: one's matrix
+    // instructions run beside another's vector ones
+    constexpr bool kTwice = kY && kBf16;
+    __shared__ __attribute__((aligned(16))) uint8_t first_lds_[kY ? (kTwice ? 2 : 1) * kFirst : Block::kSet];
+    __shared__ __attribute__((aligned(16))) uint8_t key_lds_[(kTwice ? 2 : 1) * Block::kSet];
     __shared__ __attribute__((aligned(16))) uint8_t head_lds[2][kArrays];
     const ScanArgs& a = s.a;
     const int per_group = a.H / a.G, quads = (per_group + kSweepHeads - 1) / kSweepHeads;
@@ -322,19 +325,20 @@ __global__ __launch_bounds__(kSweepThreads, 2) void sweep_kernel(SweepArgs s) {
     if (count > 0) {
         load_arrays(0);
         if constexpr (kY) next_first.load(block_of(sg.x), kFirst);
-        else next_key.load(block_of(chunk_at(0)) + s.key, Block::kSet);
+        if constexpr (!kY || kTwice) next_key.load(block_of(chunk_at(0)) + s.key, Block::kSet);
         if constexpr (!kY) load_v(0);
     }
     for (int i = 0; i < count; ++i) {
         const int c = chunk_at(i), following = i + 1 < count ? i + 1 : i;   // (the last chunk's loads are idle ones: no branch)
         const float* const arrays = reinterpret_cast<const float*>(head_lds[i & 1]) + (live ? wave >> 1 : 0) * kHeadArrays * kChunk;
+        uint8_t* const first_lds = first_lds_ + (kTwice ? (i & 1) * kFirst : 0);
+        uint8_t* const key_lds = !kY && (i & 1) ? first_lds_ : key_lds_ + (kTwice ? (i & 1) * Block::kSet : 0);
         next_arrays.store(head_lds[i & 1]);
         if constexpr (kY) next_first.store(first_lds);
-        else next_key.store(i & 1 ? first_lds : key_lds);
+        if constexpr (!kY || kTwice) next_key.store(key_lds);
         lds_barrier();
         if constexpr (kY) {
             load_v(i);
-            if constexpr (kBf16) next_key.load(block_of(c) + s.key, Block::kSet);
             v4f y[4][2];
 #pragma unroll
             for (int t = 0; t < 4; ++t) y[t][0] = y[t][1] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
@@ -355,7 +359,7 @@ __global__ __launch_bounds__(kSweepThreads, 2) void sweep_kernel(SweepArgs s) {
                     y[t][1] = mma(cr, state[1], y[t][1]);
                 }
             }
-            read_ahead<kData, 2 * products_of(kData, kOut), 4 * kSteps, 2, 16 + (kBf16 ? Staged<Block::kSet>::kEach : 0)>();
+            read_ahead<kData, 2 * products_of(kData, kOut), 4 * kSteps, 2, 16>();
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
                 const v4f e = sigma * at4(arrays + kDecay * kChunk + t * 16 + 4 * q);
@@ -406,7 +410,7 @@ __global__ __launch_bounds__(kSweepThreads, 2) void sweep_kernel(SweepArgs s) {
                     y[t][1] = mma(wp, x[1], y[t][1]);
                 }
             }
-            if constexpr (!kBf16) {   // (three pieces are too many registers to hold meanwhile)
+            if constexpr (!kTwice) {   // (three pieces are too many registers to hold before)
                 __builtin_amdgcn_sched_barrier(0);
                 next_key.load(block_of(c) + s.key, Block::kSet);
             }
@@ -421,10 +425,13 @@ __global__ __launch_bounds__(kSweepThreads, 2) void sweep_kernel(SweepArgs s) {
                         out.store2(fmaf(skip, v[t >> 1][0][(t & 1) * 4 + j], y[t][0][j]),
                                    fmaf(skip, v[t >> 1][1][(t & 1) * 4 + j], y[t][1][j]), to + (t * 16 + j) * (int)s.ldy * kSize);
             }
-            next_key.store(key_lds);
-            lds_barrier();
+            if constexpr (!kTwice) {
+                next_key.store(key_lds);
+                lds_barrier();
+            }
             load_arrays(following);
             next_first.load(block_of(chunk_at(following)), kFirst);
+            if constexpr (kTwice) next_key.load(block_of(chunk_at(following)) + s.key, Block::kSet);
         } else {
             take_v();
             // (before the stores: a wait for loads waits for the stores before them)
@@ -458,7 +465,7 @@ __global__ __launch_bounds__(kSweepThreads, 2) void sweep_kernel(SweepArgs s) {
                 in[k][p] = split<kInto>(f);
             }
         }
-        const uint8_t* const keys = (!kY && (i & 1) ? first_lds : key_lds) + lane * 16;
+        const uint8_t* const keys = key_lds + lane * 16;
 #pragma unroll
         for (int n = 0; n < kTiles; ++n) {
             const Pieces<kData> key0 = load_pieces<kData>(keys + n * 2048, Block::kPlane);
@@ -473,7 +480,7 @@ __global__ __launch_bounds__(kSweepThreads, 2) void sweep_kernel(SweepArgs s) {
                 for (int j = 0; j < 4; ++j) h[n][p][j] = fmaf(h[n][p][j], -last, add[p][j]);
             }
         }
-        read_ahead<kData, 2 * products_of(kData, kInto), 2 * kTiles, 2, kY ? 1 + Staged<kFirst>::kEach : 17 + Staged<Block::kSet>::kEach>();
+        read_ahead<kData, 2 * products_of(kData, kInto), 2 * kTiles, 2, (kY ? Staged<kFirst>::kEach : 16) + 1 + (!kY || kTwice ? Staged<Block::kSet>::kEach : 0)>();
         sigma = -sigma;
     }
     if (!live) return;

@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libdfssm.so")
@@ -633,6 +634,16 @@ def dfssm_embedding_backward(tokens, dout, scale, de, workspace, accumulate: boo
 
 def _sequences(name, T, cu_seqlens, states, sequences) -> int:
     """The number of sequences, agreed on by everything that tells it."""
+    if cu_seqlens is None and sequences is None:   # (the common case, without the list)
+        S = 0
+        for t in states:
+            if t is not None:
+                if S not in (0, t.shape[0]):
+                    raise ValueError(f"{name}: the numbers of sequences differ: {S}, {t.shape[0]}")
+                S = t.shape[0]
+        if T % (S or 1):
+            raise ValueError(f"{name}: {T} rows are not {S} sequences of equal length")
+        return S or 1
     import torch
     told = [t.shape[0] for t in states if t is not None]
     if cu_seqlens is not None:
@@ -706,36 +717,51 @@ def dfssm_mamba2_conv_backward(xbc, conv_w, conv_b, window_in, dout, dwindow_out
 
 def _heads(what, t, T, dtype) -> tuple:
     """Checks rows of parts [T, A, B] whose parts lie side by side; (stride of a row, A, B)."""
-    if t.dim() != 3 or t.shape[0] != T:
-        raise ValueError(f"{what}: shape ({T}, ., .) expected, got {tuple(t.shape)}")
+    shape = t.shape
+    if len(shape) != 3 or shape[0] != T:
+        raise ValueError(f"{what}: shape ({T}, ., .) expected, got {tuple(shape)}")
     if t.dtype is not dtype:
         raise ValueError(f"{what}: {dtype} expected, got {t.dtype}")
-    _, A, B = t.shape
+    _, A, B = shape
     st, sa, sb = t.stride()
     if (sb != 1 and B > 1) or (sa != B and A > 1) or (st < A * B and T > 1):
         raise ValueError(f"{what}: rows must be contiguous and must not overlap, got strides {t.stride()}")
     return (st if T > 1 else A * B), A, B
 
 
+# dfssm_mamba2_scan_operands and dfssm_mamba2_scan_gradients as bytes (packed faster than a ctypes structure is made)
+_pack_operands = struct.Struct(f"{len(SCAN_POINTERS)}Q{len(SCAN_SIZES)}qi4x").pack
+_pack_gradients = struct.Struct(f"{len(SCAN_GRADIENTS)}Q{len(SCAN_GRADIENT_SIZES)}q").pack
+
+
 def _scan_operands(name, x, dt, B, C, A_log, D, dt_bias, state_in, states, cu_seqlens, sequences):
-    """Checks the scan's operands; (dfssm_mamba2_scan_operands, its tensors, the states' shape)."""
+    """Checks the scan's operands; (dfssm_mamba2_scan_operands, its tensors, T, H, P, G, N)."""
     import torch
-    T = x.shape[0]
+    T = x.shape[0] if x.dim() else 0
     ldx, H, P = _heads("x", x, T, x.dtype)
     ldb, G, N = _heads("B", B, T, x.dtype)
-    ldc, *same = _heads("C", C, T, x.dtype)
-    if same != [G, N]:
+    ldc, Gc, Nc = _heads("C", C, T, x.dtype)
+    if Gc != G or Nc != N:
         raise ValueError(f"C: shape {tuple(B.shape)} expected, got {tuple(C.shape)}")
     lddt = _rows("dt", dt, (T, H), torch.float32)
-    for what, t in (("A_log", A_log), ("D", D), ("dt_bias", dt_bias)):
-        _dense(what, t, (H,), torch.float32)
-    S = _sequences(name, T, cu_seqlens, (state_in, *states.values()), sequences)
-    for what, t in (("state_in", state_in), *states.items()):
-        _optional(what, t, (S, H, P, N))
-    op = ScanOperands(x.data_ptr(), B.data_ptr(), C.data_ptr(), dt.data_ptr(), A_log.data_ptr(), D.data_ptr(),
-                      dt_bias.data_ptr(), _ptr(state_in), _ptr(cu_seqlens), ldx, ldb, ldc, lddt, T, S, H, P, N, G,
-                      _type("x", x))
-    return op, _present(x, dt, B, C, A_log, D, dt_bias, state_in, cu_seqlens, *states.values())
+    f32, row = torch.float32, (H,)
+    _dense("A_log", A_log, row, f32)
+    _dense("D", D, row, f32)
+    _dense("dt_bias", dt_bias, row, f32)
+    S = _sequences(name, T, cu_seqlens, (state_in, *states), sequences)
+    tensors = [x, dt, B, C, A_log, D, dt_bias]
+    state = (S, H, P, N)
+    for t in (state_in, *states):
+        if t is not None:
+            _dense("state", t, state, f32)
+            tensors.append(t)
+    if cu_seqlens is not None:
+        tensors.append(cu_seqlens)
+    op = _pack_operands(x.data_ptr(), B.data_ptr(), C.data_ptr(), dt.data_ptr(), A_log.data_ptr(), D.data_ptr(),
+                        dt_bias.data_ptr(), 0 if state_in is None else state_in.data_ptr(),
+                        0 if cu_seqlens is None else cu_seqlens.data_ptr(), ldx, ldb, ldc, lddt, T, S, H, P, N, G,
+                        _type("x", x))
+    return op, tensors, T, H, P, G, N
 
 
 def dfssm_mamba2_scan_workspace_bytes(T: int, S: int, nheads: int, headdim: int, d_state: int, ngroups: int = 1) -> int:
@@ -748,13 +774,14 @@ def dfssm_mamba2_scan(x, dt, B, C, A_log, D, dt_bias, state_in, state_out, y, wo
     dt_bias [H] (x, B, C, y all fp32 or all bf16, rows may be strided); state_in / state_out fp32 [S, H, 64, N] or None
     (zeros / not wanted), the same tensor for an update in place; workspace: a tensor of
     dfssm_mamba2_scan_workspace_bytes(T, S, H, 64, N, G) bytes."""
-    op, tensors = _scan_operands("dfssm_mamba2_scan", x, dt, B, C, A_log, D, dt_bias, state_in, {"state_out": state_out},
-                                 cu_seqlens, sequences)
-    ldy, *same = _heads("y", y, op.T, x.dtype)
-    if same != [op.nheads, op.headdim]:
+    op, tensors, T, H, P, _, _ = _scan_operands("dfssm_mamba2_scan", x, dt, B, C, A_log, D, dt_bias, state_in,
+                                                (state_out,), cu_seqlens, sequences)
+    ldy, Hy, Py = _heads("y", y, T, x.dtype)
+    if Hy != H or Py != P:
         raise ValueError(f"y: shape {tuple(x.shape)} expected, got {tuple(y.shape)}")
-    _run_on("dfssm_mamba2_scan", [*tensors, y, workspace], stream, ctypes.addressof(op), y.data_ptr(), ldy,
-            _ptr(state_out), workspace.data_ptr(), _bytes(workspace))
+    tensors += (y, workspace)
+    _run_on("dfssm_mamba2_scan", tensors, stream, op, y.data_ptr(), ldy, _ptr(state_out), workspace.data_ptr(),
+            _bytes(workspace))
 
 
 def dfssm_mamba2_scan_backward_workspace_bytes(T: int, S: int, nheads: int, headdim: int, d_state: int,
@@ -769,18 +796,18 @@ def dfssm_mamba2_scan_backward(x, dt, B, C, A_log, D, dt_bias, state_in, dy, dst
     None: not wanted; dstate_out itself: in place); workspace: a tensor of
     dfssm_mamba2_scan_backward_workspace_bytes(T, S, H, 64, N, G) bytes."""
     import torch
-    op, tensors = _scan_operands("dfssm_mamba2_scan_backward", x, dt, B, C, A_log, D, dt_bias, state_in,
-                                 {"dstate_out": dstate_out, "dstate_in": dstate_in}, cu_seqlens, sequences)
+    op, tensors, T, H, _, _, _ = _scan_operands("dfssm_mamba2_scan_backward", x, dt, B, C, A_log, D, dt_bias, state_in,
+                                                (dstate_out, dstate_in), cu_seqlens, sequences)
     strides = {}
     for what, t, like in (("dy", dy, x), ("dx", dx, x), ("dB", dB, B), ("dC", dC, C)):
-        strides[what], *same = _heads(what, t, op.T, x.dtype)
+        strides[what], *same = _heads(what, t, T, x.dtype)
         if same != list(like.shape[1:]):
             raise ValueError(f"{what}: shape {tuple(like.shape)} expected, got {tuple(t.shape)}")
-    ldddt = _rows("ddt", ddt, (op.T, op.nheads), torch.float32)
+    ldddt = _rows("ddt", ddt, (T, H), torch.float32)
     for what, t in (("dA_log", dA_log), ("dD", dD), ("ddt_bias", ddt_bias)):
-        _dense(what, t, (op.nheads,), torch.float32)
-    grad = ScanGradients(dy.data_ptr(), _ptr(dstate_out), dx.data_ptr(), dB.data_ptr(), dC.data_ptr(), ddt.data_ptr(),
-                         dA_log.data_ptr(), dD.data_ptr(), ddt_bias.data_ptr(), _ptr(dstate_in), strides["dy"], strides["dx"],
-                         strides["dB"], strides["dC"], ldddt)
+        _dense(what, t, (H,), torch.float32)
+    grad = _pack_gradients(dy.data_ptr(), _ptr(dstate_out) or 0, dx.data_ptr(), dB.data_ptr(), dC.data_ptr(), ddt.data_ptr(),
+                           dA_log.data_ptr(), dD.data_ptr(), ddt_bias.data_ptr(), _ptr(dstate_in) or 0, strides["dy"],
+                           strides["dx"], strides["dB"], strides["dC"], ldddt)
     _run_on("dfssm_mamba2_scan_backward", [*tensors, dy, dx, dB, dC, ddt, dA_log, dD, ddt_bias, workspace], stream,
-            ctypes.addressof(op), ctypes.addressof(grad), workspace.data_ptr(), _bytes(workspace))
+            op, grad, workspace.data_ptr(), _bytes(workspace))

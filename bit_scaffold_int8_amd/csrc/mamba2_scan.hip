@@ -106,7 +106,8 @@ __global__ __launch_bounds__(1024) void scan_tables_kernel(ScanArgs a, int* __re
         if (i < a.first_segment[S]) {
             const int s = owner(a.first_segment, i), n = i - a.first_segment[s];
             const int c = first_chunk[s] + n * a.per_segment, left = first_chunk[s + 1] - c;
-            v = make_int4(c, left < 0 ? 0 : left < a.per_segment ? left : a.per_segment, s,
+            // (no chunks are left only where bad offsets claimed more than there is room for)
+            v = make_int4(c, left < a.per_segment ? left : a.per_segment, left > 0 ? s : -1,
                           (n == 0 ? 1 : 0) | (i + 1 == a.first_segment[s + 1] ? 2 : 0));
         }
         a.segments[i] = v;
@@ -527,7 +528,8 @@ __global__ __launch_bounds__(256) void join_segments_kernel(SweepArgs s) {
 // ---------------------------------------------------------------- the recurrence, token by token
 
 // As in the decode step, 16 channels of a head to a workgroup and 16 threads to a channel: each state value is read
-// and written once by one thread.  The next token's operands are loaded while this one's are used.
+// and written once by one thread.  A wave forms the steps and decays of 64 tokens at once, a token a lane; four tokens' rows are
+// in flight together.
 template <bool kBf16, int kN>
 __global__ __launch_bounds__(256) void recurrent_kernel(SweepArgs s) {
     constexpr int kV = kN / 16, kV4 = kV / 4;
@@ -535,40 +537,58 @@ __global__ __launch_bounds__(256) void recurrent_kernel(SweepArgs s) {
     using T = typename E::type;
     const ScanArgs& a = s.a;
     const int head = blockIdx.x / 4, p = blockIdx.x % 4 * 16 + threadIdx.x / 16, q = threadIdx.x % 16;
-    const int sequence = blockIdx.y, g = head / (a.H / a.G);
+    const int sequence = blockIdx.y, g = head / (a.H / a.G), lane = threadIdx.x & 63;
     const Span span = span_of(a.seq, sequence);
     const int64_t at = (((int64_t)sequence * a.H + head) * kP + p) * kN + kV * q;
-    v4f h[kV4], b[kV4], c[kV4];
+    v4f h[kV4];
 #pragma unroll
     for (int i = 0; i < kV4; ++i) h[i] = s.start ? *reinterpret_cast<const v4f*>(s.start + at + 4 * i) : v4f{0.0f, 0.0f, 0.0f, 0.0f};
-    float x = 0.0f, raw = 0.0f;
-    auto fetch = [&](int t) {
-        x = E::load(static_cast<const T*>(s.v) + t * s.ldv + head * kP + p);
-        raw = a.dt[t * a.lddt + head];
+    struct Row {
+        float x;
+        v4f b[kV4], c[kV4];
+    };
+    auto fetch = [&](Row& row, int t) {
+        row.x = E::load(static_cast<const T*>(s.v) + t * s.ldv + head * kP + p);
 #pragma unroll
         for (int i = 0; i < kV4; ++i) {
-            b[i] = E::load4(static_cast<const T*>(a.B) + t * a.ldb + g * kN + kV * q + 4 * i);
-            c[i] = E::load4(static_cast<const T*>(a.C) + t * a.ldc + g * kN + kV * q + 4 * i);
+            row.b[i] = E::load4(static_cast<const T*>(a.B) + t * a.ldb + g * kN + kV * q + 4 * i);
+            row.c[i] = E::load4(static_cast<const T*>(a.C) + t * a.ldc + g * kN + kV * q + 4 * i);
         }
     };
     const float rate = expf(a.A_log[head]), bias = a.dt_bias[head], skip = a.D[head];
-    if (span.begin < span.end) fetch(span.begin);
-    for (int t = span.begin; t < span.end; ++t) {
-        const float dt = scan_softplus(raw + bias), decay = expf(-dt * rate), dtx = dt * x, own = skip * x;
+    auto step = [&](const Row& row, int t, float dt, float decay) {
+        const float dtx = dt * row.x;
         float y = 0.0f;
 #pragma unroll
         for (int i = 0; i < kV4; ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                h[i][j] = fmaf(h[i][j], decay, dtx * b[i][j]);
-                y = fmaf(h[i][j], c[i][j], y);
+                h[i][j] = fmaf(h[i][j], decay, dtx * row.b[i][j]);
+                y = fmaf(h[i][j], row.c[i][j], y);
             }
-        if (t + 1 < span.end) fetch(t + 1);
         y += dpp_f<kDppXor1>(y);
         y += dpp_f<kDppXor2>(y);
         y += dpp_f<kDppHalfMirror>(y);
         y += dpp_f<kDppMirror>(y);
-        if (q == 0) E::store(static_cast<T*>(s.y) + t * s.ldy + head * kP + p, own + y);
+        if (q == 0) E::store(static_cast<T*>(s.y) + t * s.ldy + head * kP + p, fmaf(skip, row.x, y));
+    };
+    for (int t0 = span.begin; t0 < span.end; t0 += 64) {
+        const int mine = t0 + lane < span.end ? t0 + lane : span.end - 1, stop = t0 + 64 < span.end ? t0 + 64 : span.end;
+        const float dts = scan_softplus(a.dt[mine * a.lddt + head] + bias), decays = expf(-dts * rate);
+        auto of = [&](float v, int t) { return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), t - t0)); };
+        int t = t0;
+        for (; t + 4 <= stop; t += 4) {
+            Row rows[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) fetch(rows[j], t + j);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) step(rows[j], t + j, of(dts, t + j), of(decays, t + j));
+        }
+        for (; t < stop; ++t) {
+            Row row;
+            fetch(row, t);
+            step(row, t, of(dts, t), of(decays, t));
+        }
     }
     if (s.end)
 #pragma unroll
@@ -613,10 +633,15 @@ hipError_t launch_sweep(const SweepArgs& s, const ScanPlan& plan, bool bf16, int
 
 // ---------------------------------------------------------------- the host's side
 
-// Sequences of up to this many tokens on average go token by token.
-constexpr int kRecurrentTokens = 8;
-
-bool scan_recurrent(const Sequences& seq) { return seq.T <= (int64_t)kRecurrentTokens * seq.S; }
+// Whether the sequences go token by token: by their average length and, in units of 64, the number of heads of all of them.
+// Measured in us, d_state 128 (token by token 2, 8, 16, 32, 64 tokens | chunks up to 64 tokens):
+//   1 x 64 heads, fp32  4.2, 5.6, 7.7, 11.7, 20.0 | 27;   bf16  4.2, 5.5, 7.4, 11.3, 19.1 | 21
+//   8 x 64 heads, fp32  10, 17, 26, 45, 79 | 31;   bf16  10, 14, 21, 35, 60 | 25
+//   64 x 64 heads, fp32  57, 116, 178, 303, 582 | 115 to 136;   bf16  49, 80, 128, 214, 382 | 88 to 98
+bool scan_recurrent(const Sequences& seq, int H) {
+    const float units = (float)seq.S * (float)H / 64.0f, tokens = (float)seq.T / (float)seq.S;
+    return tokens * (0.15f + 0.13f * units) <= 18.0f + units;
+}
 
 // Enough workgroups for one on each CU: what one segment a sequence does not give, more segments do, at the price of a
 // second sweep without outputs.
@@ -686,7 +711,7 @@ hipError_t launch_mamba2_scan(ScanArgs a, bool bf16, int N, const float* state_i
     s.end = state_out;
     s.y = y;
     s.ldy = ldy;
-    if (scan_recurrent(a.seq)) {
+    if (scan_recurrent(a.seq, a.H)) {
         s.a = a;
         return with_kind(bf16, N, [&](auto b, auto n) {
             recurrent_kernel<b.value, n.value><<<dim3((unsigned)(a.H * 4), (unsigned)a.seq.S), 256, 0, stream>>>(s);

@@ -679,8 +679,8 @@ typedef struct dfssm_mamba2_scan_operands {
  *   state_out  fp32 [S][nheads][64][d_state], written, or NULL; may be state_in itself (the update in place)
  *   workspace  at least dfssm_mamba2_scan_workspace_bytes(T, S, nheads, headdim, d_state, ngroups) bytes, 16-byte
  *              aligned, under dfssm_cross_entropy's rules
- * Sequences of at most 8 tokens on average go token by token through the recurrence in fp32 (one launch, the workspace
- * unused); longer ones by chunks of 64 tokens on the matrix cores.  There fp32 operands and the state are taken in
+ * Short sequences go token by token through the recurrence in fp32 (one launch, the workspace unused): of 64 heads, one of up
+ * to 68 tokens, 8 of 22 on average, 64 of 9; longer ones by chunks of 64 tokens on the matrix cores.  There fp32 operands and the state are taken in
  * three bf16 pieces (relative error 2^-24 of each), and where y is bf16 the state's and the chunk's weights enter y in two
  * (2^-17); the state itself is fp32 and formed from three pieces for either type.  A chunk's decays are
  * differences of sums in fp64.  Sums run in a fixed order: equal inputs give equal bits.

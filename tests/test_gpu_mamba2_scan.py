@@ -109,6 +109,11 @@ SHAPES = [
     ([0, 200, 0], 2, 64, 2, True, 0, 3),
     ([0, 0], 2, 128, 1, True, 5, 0),
     ([2, 0, 7, 3], 6, 128, 3, True, 4, 2),
+    # (from here on by chunks, as 130, 130 and 300 above; the others token by token)
+    ([128], 2, 128, 1, False, 0, 0),
+    ([193, 193, 193], 9, 64, 1, False, 0, 0),
+    ([1, 0, 63, 64, 65, 129, 640, 200], 3, 128, 1, True, 7, 0),
+    ([0, 500, 0], 2, 64, 2, True, 0, 3),
 ]
 
 
@@ -127,6 +132,29 @@ def test_scan_from_zeros_and_in_place(lens):
     y, state = run(o, lens, where, torch.float32, False, state=False)
     check(o, lens, where, inside, torch.float32, y, state, with_state=False)
     y, state = run(o, lens, where, torch.float32, False, in_place=True)
+    check(o, lens, where, inside, torch.float32, y, state)
+
+
+@pytest.mark.parametrize("lens", [[40], [200]])
+@pytest.mark.parametrize("kind", ["forgets", "keeps", "steps above 20", "mixed"])
+def test_scan_extreme_decays(lens, kind):
+    """Decays of nothing and of everything, and steps where softplus is the identity: finite, and within the bounds.  (An
+    exponent of 2^12 and more errs by more than the bounds' 16, but its term is zero on both sides.)"""
+    o, where, inside = make(lens, 4, 128, seed=9)
+    T = lens[0]
+    if kind == "forgets":
+        o["dt"] += 8.0
+        o["A_log"] += 6.0
+    elif kind == "keeps":
+        o["dt"] -= 40.0
+    elif kind == "steps above 20":
+        o["dt"] = 19.5 + torch.arange(T * 4).reshape(T, 4) % 7 * 0.25 - o["dt_bias"]
+        o["A_log"] -= 8.0
+    else:
+        o["dt"][::3] += 30.0
+        o["dt"][1::3] -= 30.0
+    y, state = run(o, lens, where, torch.float32, False)
+    assert bool(torch.isfinite(y).all()) and bool(torch.isfinite(state).all())
     check(o, lens, where, inside, torch.float32, y, state)
 
 

@@ -54,8 +54,8 @@ struct GradLds {
     static constexpr int kDy = 0, kX = kDy + kData * kPlane, kW = kX + kData * kPlane, kRows = kW + kOut * kPlane;
     static constexpr int kK = kRows + kData * kChunk * kN * 2, kPart = kK + kChunk * kChunk * 4;   // (the latter: floats)
     static constexpr int kRowSum = 0, kColSum = 8 * kChunk, kDiag = 12 * kChunk, kDot = 13 * kChunk, kU = 14 * kChunk,
-                         kV = kU + kN / 16 * kChunk, kPass = kV + 4 * kChunk;   // (the first two and the last hold doubles)
-    static constexpr int kArrays = kPass + 16;                                  // the head's decays
+                         kV = kU + kN / 16 * kChunk, kPass = kV + 4 * kChunk;   // (the first two hold doubles)
+    static constexpr int kArrays = kPass + 32;                                  // the head's decays
     static constexpr int kParts = kArrays + kHeadArrays * kChunk, bytes = kPart + 2 * kParts * 4;   // (this turn's head and the one before)
     static constexpr int kLdSum = kChunk + 4;                           // the heads' sum of M L dt, over dy, x and W
     static_assert(kChunk * kLdSum * 4 <= kRows, "it fits");
@@ -159,7 +159,6 @@ __global__ __launch_bounds__(kThreads, 2) void scan_grad_kernel(ScanGradArgs s) 
         const float* const arrays = part + Lds::kArrays;
         const double* const row_sums = reinterpret_cast<const double*>(part + Lds::kRowSum);
         const double* const column_sums = reinterpret_cast<const double*>(part + Lds::kColSum);
-        const double* const passes = reinterpret_cast<const double*>(part + Lds::kPass);
         const float hi = arrays[lane], lo = arrays[kCsLo * kChunk + lane], dt = arrays[kStep * kChunk + lane];
         const float end_hi = arrays[kChunk - 1], end_lo = arrays[kCsLo * kChunk + kChunk - 1];
         double rows = 0.0;
@@ -171,7 +170,7 @@ __global__ __launch_bounds__(kThreads, 2) void scan_grad_kernel(ScanGradArgs s) 
 #pragma unroll
         for (int i = 0; i < 4; ++i) v += part[Lds::kV + i * kChunk + lane];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) pass += passes[i];
+        for (int i = 0; i < 32; ++i) pass += (double)part[Lds::kPass + i];
         const double columns = column_sums[lane] + column_sums[kChunk + lane];
         u *= arrays[kDecay * kChunk + lane];
         v *= __builtin_amdgcn_exp2f((end_hi - hi) + (end_lo - lo));
@@ -214,7 +213,6 @@ __global__ __launch_bounds__(kThreads, 2) void scan_grad_kernel(ScanGradArgs s) 
         if (tid < kHeadArrays * kChunk) arrays[tid] = decays;
         double* const row_sums = reinterpret_cast<double*>(part + Lds::kRowSum);
         double* const column_sums = reinterpret_cast<double*>(part + Lds::kColSum);
-        double* const passes = reinterpret_cast<double*>(part + Lds::kPass);
         {   // (x's second half negated: opposite())
             const float sign = wave & 1 ? -1.0f : 1.0f;
             const float y[8] = {y0.x, y0.y, y0.z, y0.w, y1.x, y1.y, y1.z, y1.w};
@@ -223,12 +221,12 @@ __global__ __launch_bounds__(kThreads, 2) void scan_grad_kernel(ScanGradArgs s) 
             store_pieces(lds + Lds::kX + (wave * 64 + lane) * 16, kPlane, split<kData>(x));
         }
         load_states(k, (4 * q * kN + nt * 16 + r) * 4);
-        double pass = 0.0;
+        float pass = 0.0f;
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                pass += (double)h_at[i][j] * (double)dh_at[i][j];
+                pass = fmaf(h_at[i][j], dh_at[i][j], pass);
                 if (i) h_at[i][j] = -h_at[i][j];
             }
         const Pieces<kFull> hp[2] = {split<kFull>(h_at[0]), split<kFull>(h_at[1])};
@@ -237,6 +235,7 @@ __global__ __launch_bounds__(kThreads, 2) void scan_grad_kernel(ScanGradArgs s) 
         if (k > first && wave == ((k - 1) & 7)) finish(k - 1, lane);
         __builtin_amdgcn_sched_barrier(0);
         {   // dC and dB through the states
+            v4f us[kTT];     // C . (h^T dy), the wave's places
 #pragma unroll
             for (int t = 0; t < kTT; ++t) {
                 v4f us_[2], ws_[2];
@@ -249,15 +248,16 @@ __global__ __launch_bounds__(kThreads, 2) void scan_grad_kernel(ScanGradArgs s) 
                 const v4f u = opposite(us_), w = opposite(ws_);
                 acc_c[t] += u * *reinterpret_cast<const v4f*>(arrays + kDecay * kChunk + (t0 + t) * 16 + 4 * q);
                 acc_b[t] += w * *reinterpret_cast<const v4f*>(arrays + kWeight * kChunk + (t0 + t) * 16 + 4 * q);
-                v4f us;
 #pragma unroll
-                for (int v = 0; v < 4; ++v) us[v] = row_sum(u[v] * c_at[t][v]);
-                if (r == 0) *reinterpret_cast<v4f*>(part + Lds::kU + nt * kChunk + (t0 + t) * 16 + 4 * q) = us;
+                for (int v = 0; v < 4; ++v) us[t][v] = row_sum(u[v] * c_at[t][v]);
             }
             pass = row_sum(pass);
-            pass += __shfl_xor(pass, 16);
-            pass += __shfl_xor(pass, 32);
-            if (lane == 0) passes[wave] = t0 == 0 ? pass : 0.0;
+            
+            if (r == 0) {
+#pragma unroll
+                for (int t = 0; t < kTT; ++t) *reinterpret_cast<v4f*>(part + Lds::kU + nt * kChunk + (t0 + t) * 16 + 4 * q) = us[t];
+                part[Lds::kPass + wave * 4 + q] = t0 == 0 ? pass : 0.0f;
+            }
         }
         // for dx: the state's gradient along the state
         v4f dh_rows[2 * kSteps];
@@ -295,7 +295,7 @@ __global__ __launch_bounds__(kThreads, 2) void scan_grad_kernel(ScanGradArgs s) 
                     f = behind * *reinterpret_cast<const v4f*>(arrays + kEnter * kChunk + tt * 16 + 4 * q);
                 }
                 const v4f product = *reinterpret_cast<const v4f*>(lds + Lds::kK + ((tt * 4 + st) * 64 + lane) * 16);
-                float kl[8];
+                float kl[8], on_e = 0.0f, on_m = 0.0f;    // (on the diagonal)
                 double rows[4];
 #pragma unroll
                 for (int v = 0; v < 4; ++v) {
@@ -306,10 +306,12 @@ __global__ __launch_bounds__(kThreads, 2) void scan_grad_kernel(ScanGradArgs s) 
                     sum_w[i][v] = fmaf(m[v] * f[v], s_dt, sum_w[i][v]);
                     column += strict ? (double)e : 0.0;
                     rows[v] = row_sum(strict ? (double)e * (double)s_dt : 0.0);
-                    if (tt == st && 4 * q + v == r) {
-                        part[Lds::kDiag + st * 16 + r] = e;
-                        part[Lds::kDot + st * 16 + r] = m[v];
-                    }
+                    on_e = r == 4 * q + v ? e : on_e;
+                    on_m = r == 4 * q + v ? m[v] : on_m;
+                }
+                if (tt == st && q == r >> 2) {
+                    part[Lds::kDiag + st * 16 + r] = on_e;
+                    part[Lds::kDot + st * 16 + r] = on_m;
                 }
                 const Pieces<kOut> w = split<kOut>(kl);
 #pragma unroll
@@ -353,7 +355,6 @@ __global__ __launch_bounds__(kThreads, 2) void scan_grad_kernel(ScanGradArgs s) 
                     halves[i][n & 1] = mma(load_pieces<kData>(lds + Lds::kRows + (((2 * sh + i) * kSteps + n) * 64 + lane) * 16, Block::kPlane),
                                            state, halves[i][n & 1]);
             }
-
             __builtin_amdgcn_sched_barrier(0);
             const Pieces<kData> rows[2] = {split<kData>(dy[0]), split<kData>(dy[1])};
 #pragma unroll
@@ -365,22 +366,25 @@ __global__ __launch_bounds__(kThreads, 2) void scan_grad_kernel(ScanGradArgs s) 
             const float skip = a.D[head];
             const RowBuffer<kBf16> dx_rows(s.dx, ch.x, s.lddx, ch.y, head * kP + pt * 16, 16);
             const int to = (4 * q * (int)s.lddx + r) * kSize;
+            v4f along[2];          // x . (g B)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int tile = 2 * sh + i;
                 const v4f dt = *reinterpret_cast<const v4f*>(arrays + kStep * kChunk + tile * 16 + 4 * q);
                 const v4f weight = *reinterpret_cast<const v4f*>(arrays + kWeight * kChunk + tile * 16 + 4 * q);
                 const v4f inter = opposite(halves[i]);
-                v4f along;     // x . (g B)
 #pragma unroll
                 for (int v = 0; v < 4; ++v) {
-                    along[v] = row_sum(x_at[i][v] * inter[v]);
+                    along[i][v] = row_sum(x_at[i][v] * inter[v]);
                     const float own = sh == 0 ? dy[0][i * 4 + v] : dy[1][i * 4 + v];
                     dx_rows.store(fmaf(skip, own, fmaf(dt[v], intra[i][v], weight[v] * inter[v])),
                                   to + (tile * 16 + v) * (int)s.lddx * kSize);
                 }
-                if (r == 0) *reinterpret_cast<v4f*>(part + Lds::kV + pt * kChunk + tile * 16 + 4 * q) = along;
             }
+            if (r == 0)
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    *reinterpret_cast<v4f*>(part + Lds::kV + pt * kChunk + (2 * sh + i) * 16 + 4 * q) = along[i];
         }
         __builtin_amdgcn_sched_barrier(0);
     }

@@ -26,7 +26,6 @@ namespace dfssm {
 namespace {
 
 constexpr double kLog2eD = 1.4426950408889634074;
-constexpr int kSweepWaves = 8, kSweepThreads = kSweepWaves * 64, kSweepHeads = kSweepWaves / 2;
 
 // w: 1 the sequence's first segment, 2 its last
 __device__ __forceinline__ int4 segment_of(const ScanArgs& a, int g) {
@@ -218,21 +217,21 @@ __global__ __launch_bounds__(kPrepareWaves * 64) void prepare_kernel(ScanArgs a)
 // A part of what the heads share on its way from memory through registers to LDS: loaded while something else is worked on,
 // written when that is done.  (Loads straight to LDS would cost no registers, but the compiler lets no later read of LDS
 // pass one.)  Past the buffer it is zero.
-template <int kBytes>
+template <int kBytes, int kThreads>
 struct Staged {
-    static constexpr int kEach = (kBytes + kSweepThreads * 16 - 1) / (kSweepThreads * 16);
+    static constexpr int kEach = (kBytes + kThreads * 16 - 1) / (kThreads * 16);
     v4i v[kEach];
     __device__ __forceinline__ void load(const void* from, uint32_t bytes) {
         const __amdgpu_buffer_rsrc_t rsrc = make_rsrc(from, bytes);
 #pragma unroll
         for (int i = 0; i < kEach; ++i)
-            v[i] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(rsrc, (i * kSweepThreads + (int)threadIdx.x) * 16, 0, 0));
+            v[i] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(rsrc, (i * kThreads + (int)threadIdx.x) * 16, 0, 0));
     }
     __device__ __forceinline__ void store(uint8_t* lds) const {
 #pragma unroll
         for (int i = 0; i < kEach; ++i)
-            if (kBytes % (kSweepThreads * 16) == 0 || (i * kSweepThreads + (int)threadIdx.x) * 16 < kBytes)
-                *reinterpret_cast<v4i*>(lds + (i * kSweepThreads + threadIdx.x) * 16) = v[i];
+            if (kBytes % (kThreads * 16) == 0 || (i * kThreads + (int)threadIdx.x) * 16 < kBytes)
+                *reinterpret_cast<v4i*>(lds + (i * kThreads + threadIdx.x) * 16) = v[i];
     }
 };
 
@@ -241,12 +240,14 @@ __device__ __forceinline__ void unpack(float (&f)[8], v4f lo, v4f hi) {
 }
 __device__ __forceinline__ v4f at4(const float* p) { return *reinterpret_cast<const v4f*>(p); }
 
-// A workgroup: four heads of a group, a wave 32 channels of one.  A lane's two tiles of 16 channels hold the even and the
+// A workgroup: four heads of a group (or two: the host's rule), a wave 32 channels of one.  A lane's two tiles of 16 channels hold the even and the
 // odd ones, so that it reads and writes quads.  What the heads share of a chunk comes to LDS in two parts, each loaded
 // while the other is worked on: products and C (for y), then B across the tokens (for the state); without y, B's
 // part of the next chunk.
-template <bool kBf16, int kN, int kMode>
-__global__ __launch_bounds__(kSweepThreads, 2) void sweep_kernel(SweepArgs s) {
+// (The bound: two waves to a SIMD; what lets only one workgroup of four waves on a CU has one.)
+template <bool kBf16, int kN, int kMode, int kWaves>
+__global__ __launch_bounds__(kWaves * 64, kWaves == 4 && (kMode == kOutput || !kBf16) ? 1 : 2) void sweep_kernel(SweepArgs s) {
+    constexpr int kSweepThreads = kWaves * 64, kSweepHeads = kWaves / 2;
     // pieces of the data; of the state and of the chunk's own products where y is bf16: two leave an error of 2^-17, far
     // below its rounding; of what goes into the state, which is fp32 whatever the data: three
     constexpr int kData = kBf16 ? 1 : 3, kOut = kBf16 ? 2 : 3, kInto = 3;
@@ -276,9 +277,9 @@ __global__ __launch_bounds__(kSweepThreads, 2) void sweep_kernel(SweepArgs s) {
 
     auto chunk_at = [&](int i) { return s.reverse ? sg.x + sg.y - 1 - i : sg.x + i; };
     auto block_of = [&](int c) { return a.groups + ((int64_t)c * a.G + g) * s.group_bytes; };
-    Staged<kArrays> next_arrays;
-    Staged<kFirst> next_first;
-    Staged<Block::kSet> next_key;
+    Staged<kArrays, kSweepThreads> next_arrays;
+    Staged<kFirst, kSweepThreads> next_first;
+    Staged<Block::kSet, kSweepThreads> next_key;
     auto load_arrays = [&](int i) {
         next_arrays.load(a.heads + ((int64_t)chunk_at(i) * a.H + g * per_group + head0) * kHeadArrays * kChunk, array_bytes);
     };
@@ -481,7 +482,7 @@ __global__ __launch_bounds__(kSweepThreads, 2) void sweep_kernel(SweepArgs s) {
                 for (int j = 0; j < 4; ++j) h[n][p][j] = fmaf(h[n][p][j], -last, add[p][j]);
             }
         }
-        read_ahead<kData, 2 * products_of(kData, kInto), 2 * kTiles, 2, (kY ? Staged<kFirst>::kEach : 16) + 1 + (!kY || kTwice ? Staged<Block::kSet>::kEach : 0)>();
+        read_ahead<kData, 2 * products_of(kData, kInto), 2 * kTiles, 2, (kY ? Staged<kFirst, kSweepThreads>::kEach : 16) + 1 + (!kY || kTwice ? Staged<Block::kSet, kSweepThreads>::kEach : 0)>();
         sigma = -sigma;
     }
     if (!live) return;
@@ -617,17 +618,21 @@ hipError_t launch_scan_prepare(const ScanArgs& a, bool bf16, int N, bool backwar
 }
 
 hipError_t launch_sweep(const SweepArgs& s, const ScanPlan& plan, bool bf16, int N, SweepMode mode, hipStream_t stream) {
-    const dim3 grid((unsigned)(plan.nsegments * s.a.G * ((s.a.H / s.a.G + kSweepHeads - 1) / kSweepHeads)));
-    return with_kind(bf16, N, [&](auto b, auto n) {
-        if (plan.segmented) {
-            sweep_kernel<b.value, n.value, kLocal><<<grid, kSweepThreads, 0, stream>>>(s);
+    auto sweep = [&](auto b, auto n, auto w) {
+        constexpr int kHeads = w.value / 2, kThreads = w.value * 64;
+        const dim3 grid((unsigned)(plan.nsegments * s.a.G * ((s.a.H / s.a.G + kHeads - 1) / kHeads)));
+        if constexpr (w.value == 8) if (plan.segmented) {    // (workgroups of two heads are taken where nothing is cut)
+            sweep_kernel<b.value, n.value, kLocal, w.value><<<grid, kThreads, 0, stream>>>(s);
             if (hipError_t err = hipGetLastError()) return err;
             join_segments_kernel<n.value><<<dim3((unsigned)(s.a.seq.S * s.a.H), kP * n.value / 1024), 256, 0, stream>>>(s);
             if (hipError_t err = hipGetLastError()) return err;
         }
-        if (mode == kStarts) sweep_kernel<b.value, n.value, kStarts><<<grid, kSweepThreads, 0, stream>>>(s);
-        else sweep_kernel<b.value, n.value, kOutput><<<grid, kSweepThreads, 0, stream>>>(s);
+        if (mode == kStarts) sweep_kernel<b.value, n.value, kStarts, w.value><<<grid, kThreads, 0, stream>>>(s);
+        else sweep_kernel<b.value, n.value, kOutput, w.value><<<grid, kThreads, 0, stream>>>(s);
         return hipGetLastError();
+    };
+    return with_kind(bf16, N, [&](auto b, auto n) {
+        return plan.waves == 4 ? sweep(b, n, std::integral_constant<int, 4>()) : sweep(b, n, std::integral_constant<int, 8>());
     });
 }
 
@@ -644,18 +649,21 @@ bool scan_recurrent(const Sequences& seq, int H) {
 }
 
 // Enough workgroups for one on each CU: what one segment a sequence does not give, more segments do, at the price of a
-// second sweep without outputs.
+// second sweep without outputs.  Where workgroups of two heads fill three quarters of the CUs without it, they are taken instead
+// (8 x 2048 tokens, bf16: states 159 us a sweep, 221 by segments and four heads; one sequence of 16384 tokens, cut into segments
+// anyway: 285 us, 221 with four heads; 2048 fp32 78 and 75).
 constexpr int kSweepGroups = 256;
 constexpr int64_t kMaxSegmentHeads = 8 * kSweepGroups;   // room for the segments' states, in heads
 
 ScanPlan scan_plan(const Sequences& seq, int H, int G) {
     ScanPlan p{};
-    const int64_t quads = (int64_t)G * ((H / G + kSweepHeads - 1) / kSweepHeads);
     const int64_t each = (seq.L + kChunk - 1) / kChunk;    // chunks of a sequence, without offsets
     p.nchunks = (int)(seq.cu ? seq.T / kChunk + seq.S : seq.S * each);
-    const int64_t all = p.nchunks * quads;
-    int64_t per = seq.S * quads >= kSweepGroups ? p.nchunks : (all + kSweepGroups - 1) / kSweepGroups;
-    if (per < 1) per = 1;
+    auto units = [&](int heads) { return (int64_t)G * ((H / G + heads - 1) / heads); };
+    const bool pairs = seq.S * units(4) < kSweepGroups && seq.S * units(2) * 4 >= kSweepGroups * 3;
+    p.waves = pairs ? 4 : 8;
+    int64_t per = p.nchunks;
+    if (!pairs && seq.S * units(4) < kSweepGroups) per = (p.nchunks * units(4) + kSweepGroups - 1) / kSweepGroups;
     auto segments = [&](int64_t n) { return seq.cu ? p.nchunks / n + seq.S : seq.S * ((each + n - 1) / n); };
     while (per < p.nchunks && segments(per) * H > kMaxSegmentHeads) per *= 2;
     if (per > p.nchunks) per = p.nchunks;

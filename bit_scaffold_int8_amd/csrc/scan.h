@@ -174,9 +174,10 @@ __device__ __forceinline__ int place(int q, int j) { return 4 * q + (j & 3) + 16
 // softplus with the identity above 20, as the decode step has it
 __device__ __forceinline__ float scan_softplus(float v) { return v > 20.0f ? v : log1pf(expf(v)); }
 
-// The gradient's own side of the launches.
+// How sequences are cut: bounds of the tables, and a sweep's workgroups.
 struct ScanPlan {
     int nchunks, nsegments, per_segment;
+    int waves;        // of a sweep's workgroup: two for each head
     bool segmented;   // some sequence may have more than one segment
 };
 

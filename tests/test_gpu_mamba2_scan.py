@@ -158,9 +158,11 @@ def test_scan_extreme_decays(lens, kind):
     check(o, lens, where, inside, torch.float32, y, state)
 
 
-def test_scan_many_sequences_one_segment_each():
-    """Enough sequences and heads that none is cut into segments."""
-    lens = [0, 70, 1, 40] * 66
-    o, where, inside = make(lens, 4, 64, dtype=torch.bfloat16, seed=6)
-    y, state = run(o, lens, where, torch.bfloat16, True)
-    check(o, lens, where, inside, torch.bfloat16, y, state)
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("times", [30, 66])
+def test_scan_many_sequences_one_segment_each(times, dtype):
+    """Enough sequences and heads that none is cut into segments, with two and with four heads to a workgroup."""
+    lens = [0, 70, 1, 40] * times
+    o, where, inside = make(lens, 4, 64, dtype=dtype, seed=6)
+    y, state = run(o, lens, where, dtype, True)
+    check(o, lens, where, inside, dtype, y, state)

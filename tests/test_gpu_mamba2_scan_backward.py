@@ -171,13 +171,15 @@ def test_gradients_without_states_and_in_place(lens):
     check(o, dy, dstate, lens, where, inside, torch.float32, out)
 
 
-def test_gradients_many_sequences():
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("times", [30, 66])
+def test_gradients_many_sequences(times, dtype):
     """Enough sequences that none is cut into segments and no head's share needs joining."""
-    lens = [0, 70, 1, 9] * 66
-    shape = (lens, 4, 64, 1, True, 3, 0)
-    o, where, inside, dy, dstate = operands(shape, torch.bfloat16)
-    out = run(o, dy, dstate, lens, where, torch.bfloat16, True)
-    check(o, dy, dstate, lens, where, inside, torch.bfloat16, out)
+    lens = [0, 70, 1, 9] * times
+    shape = (lens, 4, 128 if times == 30 else 64, 1, True, 3, 0)
+    o, where, inside, dy, dstate = operands(shape, dtype)
+    out = run(o, dy, dstate, lens, where, dtype, True)
+    check(o, dy, dstate, lens, where, inside, dtype, out)
 
 
 def test_gradients_against_differences():

@@ -369,7 +369,7 @@ dfssm_status density_checks(int64_t rows, int64_t d_state) {
 }
 
 // ---- packed sequences
-constexpr int64_t kMaxTokens = (int64_t)1 << 20, kMaxChannels = (int64_t)1 << 20, kMaxLd = (int64_t)1 << 31;
+constexpr int64_t kMaxTokens = (int64_t)1 << 20, kMaxChannels = (int64_t)1 << 18, kMaxLd = (int64_t)1 << 31;
 
 bool overlapping(const void* a, int64_t na, const void* b, int64_t nb) {
     const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
@@ -385,7 +385,7 @@ dfssm_status sequence_sizes(int64_t T, int64_t S, bool offsets) {
 dfssm_status conv_sizes(int64_t T, int64_t S, int64_t ch, bool offsets) {
     if (ch <= 0 || ch >= kMaxRows) return DFSSM_ERR_INVALID_ARG;
     if (dfssm_status st = sequence_sizes(T, S, offsets)) return st;
-    return ch > kMaxChannels ? DFSSM_ERR_UNSUPPORTED : DFSSM_OK;
+    return ch > kMaxChannels || T * ch > ((int64_t)1 << 34) ? DFSSM_ERR_UNSUPPORTED : DFSSM_OK;
 }
 
 // A matrix's stride: what is shorter than a row is wrong, 2^31 and more is refused.
@@ -400,7 +400,8 @@ dfssm_status scan_sizes(int64_t T, int64_t S, int64_t H, int64_t P, int64_t N, i
         return DFSSM_ERR_INVALID_ARG;
     if (dfssm_status st = sequence_sizes(T, S, offsets)) return st;
     if (P != dfssm::kP || (N != 64 && N != 128) || H > 1024 || S * H > ((int64_t)1 << 21) ||
-        (T / dfssm::kChunk + S) * (H + 4 * G) > ((int64_t)1 << 25))
+        (T / dfssm::kChunk + S) * (H + 4 * G) > ((int64_t)1 << 25) ||
+        (T / dfssm::kChunk + S) * G > ((int64_t)1 << 21))    // (1024 threads and more a chunk and group: below 2^32 in a launch)
         return DFSSM_ERR_UNSUPPORTED;
     return DFSSM_OK;
 }

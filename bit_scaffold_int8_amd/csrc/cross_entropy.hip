@@ -183,7 +183,8 @@ struct TeacherArgs {
 constexpr int kMaxTop = 256;    // entries a token: four a lane
 constexpr int kDots = 8;        // dot products a wave forms side by side, so that their loads are in flight together
 
-// z / T of the teacher's rows: logits[m][j].
+// z / T of the teacher's rows: logits[m][j].  Rows of E at random, 2 KB each, mostly from the caches (4096 tokens of 128
+// entries, K 2048: 1.07 GB in 95 us, 11 TB/s; 300 tokens of 20 6 us).
 __global__ __launch_bounds__(256) void teacher_logits_kernel(LossArgs a, TeacherArgs t, float* __restrict__ logits) {
     const int lane = threadIdx.x & 63, groups = (t.k + kDots - 1) / kDots;
     const int64_t unit = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
@@ -500,7 +501,9 @@ __global__ __launch_bounds__(256) void teacher_gradient_kernel(TeacherArgs t, in
     }
 }
 
-// The pieces of the entries' d inside a piece of the vocabulary, over what the tiles have written there; a thread an entry.
+// The pieces of the entries' d inside a piece of the vocabulary, over what the tiles have written there; a thread an entry.  (Looked
+// up inside the tiles instead, every tile would search every token's entries.  4096 tokens of 128 entries: 15 us a piece of
+// the vocabulary, four of them, against 2.5 ms of products: stores of 2 bytes at random.)
 template <int P>
 __global__ __launch_bounds__(256) void teacher_scatter_kernel(GradArgs a, const int32_t* __restrict__ ids, int k,
                                                               const float* __restrict__ d) {

@@ -23,7 +23,9 @@ namespace dfssm {
 namespace {
 
 constexpr int kWaves = 4;       // runs a workgroup walks, one a wave
-constexpr int kRun = 8, kGradRun = 32;   // rows of a run: 2048 x 4352 fp32 15.8 us, 18.2 with 16 (fewer waves), 24 with 32
+// Rows of a run: 2048 x 4352 fp32 15.8 us, 18.2 with 16 (fewer waves), 24 with 32 (before sigmoid() below: 14.4 now, 4.95 TB/s of
+// the 71 MB it cannot do without, which is what bounds it).  Backward a run costs six rows more: 32.
+constexpr int kRun = 8, kGradRun = 32;
 
 struct ConvArgs {
     Sequences seq;
@@ -140,6 +142,7 @@ __global__ __launch_bounds__(kWaves * 64) void conv_kernel(ConvArgs a) {
     const int stop = t + kRun < a.seq.T ? t + kRun : a.seq.T;
     for (int s = sequence_at(a.seq, t); s < a.seq.S && t < stop; ++s) {
         const Span p = span_of(a.seq, s);
+        if (p.begin >= stop) break;
         if (t < p.begin) t = p.begin;
         const int end = p.end < stop ? p.end : stop;
         if (t >= end) continue;
@@ -216,6 +219,7 @@ __global__ __launch_bounds__(kWaves * 64) void conv_grad_kernel(ConvGradArgs a) 
     const int stop = t + kGradRun < f.seq.T ? t + kGradRun : f.seq.T;
     for (int s = sequence_at(f.seq, t); s < f.seq.S && t < stop; ++s) {
         const Span p = span_of(f.seq, s);
+        if (p.begin >= stop) break;
         if (t < p.begin) t = p.begin;
         const int end = p.end < stop ? p.end : stop;
         if (t >= end) continue;

@@ -17,6 +17,12 @@
 // A workgroup takes a chunk and some heads of a group one after another; dC and dB, sums over heads, stay in its registers,
 // and of the products M L dt B only the sum over the heads of M L dt is formed, and multiplied once.  The shares of several
 // workgroups are joined in order.
+//
+// Measured, 64 heads of 64 channels, d_state 128, in us (prepare, sweep forwards, sweep backwards, gradients, joins):
+//   2048 tokens fp32   11, 69, 66 (each with its segments), 128, 10;   8 x 2048 tokens bf16   21, 159, 159, 683, 5
+// The gradient kernel has one workgroup a CU (its LDS and registers are full: two waves to a SIMD), and a head of a chunk takes it
+// 23 thousand cycles, of which the issue of its vector and matrix instructions is 13: the rest is waiting at its two
+// barriers, for the states from memory (64 KB a head and chunk, half of what it reads) and for LDS.
 #include <math.h>
 
 #include "scan.h"
@@ -252,7 +258,6 @@ __global__ __launch_bounds__(kThreads, 2) void scan_grad_kernel(ScanGradArgs s) 
                 for (int v = 0; v < 4; ++v) us[t][v] = row_sum(u[v] * c_at[t][v]);
             }
             pass = row_sum(pass);
-            
             if (r == 0) {
 #pragma unroll
                 for (int t = 0; t < kTT; ++t) *reinterpret_cast<v4f*>(part + Lds::kU + nt * kChunk + (t0 + t) * 16 + 4 * q) = us[t];

@@ -134,9 +134,9 @@ constexpr int products_of(int a, int b) {
 }
 
 // The order of a stretch of steps that each read fragments from LDS and multiply them: the reads of the next kAhead
-// steps go out before a step's products (left alone, the compiler reads a step's fragments right before its products, and with two waves
-// a SIMD the latency is most of the time: 16384 tokens' sweep 148 us, with this order 121).
-// kLoads loads from memory go out with the first steps, one each: all at once they hold up what comes behind them.
+// steps go out before a step's products.  Left alone, the compiler reads a step's fragments right before its products (a sweep for
+// the states of 16384 tokens bf16 175 us, with this order 164; one for y gains nothing).
+// kLoads loads from memory go out with the first steps, one each: all at once they hold up what comes behind them (139).
 template <int kReads, int kProducts, int kCount, int kAhead, int kLoads>
 __device__ __forceinline__ void read_ahead() {
 #pragma unroll

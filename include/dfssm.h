@@ -619,7 +619,7 @@ dfssm_status dfssm_embedding_backward(const int32_t* tokens, int64_t T, const vo
  * Non-finite inputs reach only the outputs whose sums they enter.  One kernel launch.
  * Errors: DFSSM_ERR_INVALID_ARG for a NULL or misaligned pointer, sizes <= 0 or >= 2^31, T % S != 0 without
  * offsets, a stride < ch, a type that is none, overlapping windows; DFSSM_ERR_UNSUPPORTED for T > 2^20, S > 65535,
- * ch > 2^20 or a stride >= 2^31.
+ * ch > 2^18, T * ch > 2^34 or a stride >= 2^31.
  */
 dfssm_status dfssm_mamba2_conv(const void* xbc, int64_t ldx, int32_t in_type, int64_t T, int64_t S, int64_t ch,
                                const int32_t* cu_seqlens, const float* conv_w, const float* conv_b,
@@ -687,8 +687,8 @@ typedef struct dfssm_mamba2_scan_operands {
  * Errors: DFSSM_ERR_INVALID_ARG for a NULL or misaligned pointer, sizes <= 0 or >= 2^31, nheads % ngroups != 0, T % S != 0
  * without offsets, strides shorter than a row, a type that is none, a short workspace;
  * DFSSM_ERR_UNSUPPORTED unless headdim == 64, d_state == 64 or 128, nheads <= 1024, T <= 2^20, S <= 65535, S * nheads <= 2^21,
- * (T / 64 + S) * (nheads + 4 ngroups) <= 2^25, strides <= 2^22 and lddt < 2^31.  The size query returns 0 for sizes that the
- * call refuses, and never falls as one grows.
+ * (T / 64 + S) * (nheads + 4 ngroups) <= 2^25, (T / 64 + S) * ngroups <= 2^21, strides <= 2^22 and lddt < 2^31.  The size
+ * query returns 0 for sizes that the call refuses, and never falls as one grows.
  */
 size_t dfssm_mamba2_scan_workspace_bytes(int64_t T, int64_t S, int64_t nheads, int64_t headdim, int64_t d_state,
                                          int64_t ngroups);

@@ -32,7 +32,8 @@ _CONV = [
     (dict(T=1 << 31, S=1), 1), (dict(S=1 << 31, cu=A), 1), (dict(T=13), 1), (dict(ti=2), 1), (dict(to=-1), 1),
     (dict(ldx=63), 1), (dict(x=A + 2), 1), (dict(x=A + 1, ti=1), 1), (dict(w=A + 8), 1), (dict(b=A + 2), 1),
     (dict(win=A + 8), 1), (dict(cu=A + 2), 1), (dict(T=(1 << 20) + 4, S=4), 2), (dict(S=65536, T=65536), 2),
-    (dict(ch=(1 << 20) + 1, ldx=1 << 21, ldo=1 << 21, ldd=1 << 21, lddx=1 << 21), 2), (dict(ldx=1 << 31), 2),
+    (dict(ch=(1 << 18) + 1, ldx=1 << 21, ldo=1 << 21, ldd=1 << 21, lddx=1 << 21), 2), (dict(ldx=1 << 31), 2),
+    (dict(T=(1 << 17) + 1, S=1, ch=1 << 17, ldx=1 << 21, ldo=1 << 21, ldd=1 << 21, lddx=1 << 21), 2),   # (a launch of 2^32 threads)
 ]
 
 
@@ -84,6 +85,9 @@ _SCAN = [
     (dict(nheads=1025, ngroups=1, ldx=65600, ldy=65600, lddt=1025, lddy=65600, lddx=65600, ldddt=1025), 2),
     (dict(T=(1 << 20) + 4, S=4), 2), (dict(T=65536, S=65536), 2), (dict(lddt=1 << 31), 2), (dict(ldx=1 << 31), 2),
     (dict(T=65535, S=65535, nheads=64, ldx=4096, ldy=4096, lddt=64, lddy=4096, lddx=4096, ldddt=64), 2),
+    # a launch of 2^32 threads: 4096 chunks and a sequence of 1024 groups
+    (dict(T=4096 * 64, S=1, nheads=1024, ngroups=1024, d_state=64, ldx=65536, ldb=65536, ldc=65536, ldy=65536, lddt=1024,
+          lddy=65536, lddx=65536, lddb=65536, lddc=65536, ldddt=1024), 2),
 ]
 
 

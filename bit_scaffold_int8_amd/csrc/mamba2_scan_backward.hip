@@ -19,10 +19,10 @@
 // workgroups are joined in order.
 //
 // Measured, 64 heads of 64 channels, d_state 128, in us (prepare, sweep forwards, sweep backwards, gradients, joins):
-//   2048 tokens fp32   11, 69, 66 (each with its segments), 128, 10;   8 x 2048 tokens bf16   21, 159, 159, 683, 5
-// The gradient kernel has one workgroup a CU (its LDS and registers are full: two waves to a SIMD), and a head of a chunk takes it
-// 23 thousand cycles, of which the issue of its vector and matrix instructions is 13: the rest is waiting at its two
-// barriers, for the states from memory (64 KB a head and chunk, half of what it reads) and for LDS.
+//   2048 tokens fp32   11, 69, 66 (each with its segments), 111, 10;   8 x 2048 tokens bf16   21, 160, 160, 637, 5
+// The gradient kernel has one workgroup a CU (its registers are full: two waves to a SIMD), and a head of a chunk takes it
+// 22 thousand cycles, of which the issue of its vector and matrix instructions is 12: the rest is waiting at its two
+// barriers, for the states (64 KB a head and chunk; from the cache it would take 5 % less) and for LDS.
 #include <math.h>
 
 #include "scan.h"
@@ -67,11 +67,17 @@ struct GradLds {
     static_assert(kChunk * kLdSum * 4 <= kRows, "it fits");
 };
 
+// Another lane's value where every lane has a source: without a value to keep for others, no register need be cleared first.
+template <int kCtrl>
+__device__ __forceinline__ int lane_of(int v) { return __builtin_amdgcn_update_dpp(0, v, kCtrl, 0xF, 0xF, true); }
+template <int kCtrl>
+__device__ __forceinline__ float lane_of(float v) { return __int_as_float(lane_of<kCtrl>(__float_as_int(v))); }
+
 __device__ __forceinline__ float row_sum(float v) {   // over the 16 lanes of a row
-    v += dpp_f<kDppXor1>(v);
-    v += dpp_f<kDppXor2>(v);
-    v += dpp_f<kDppHalfMirror>(v);
-    v += dpp_f<kDppMirror>(v);
+    v += lane_of<kDppXor1>(v);
+    v += lane_of<kDppXor2>(v);
+    v += lane_of<kDppHalfMirror>(v);
+    v += lane_of<kDppMirror>(v);
     return v;
 }
 
@@ -79,16 +85,16 @@ __device__ __forceinline__ float row_sum(float v) {   // over the 16 lanes of a 
 // its error is the same for many tokens, so that it stays in the sums over the tokens (dA_log of 2048 tokens against 64 bits:
 // 1.0e-6 with sums in fp32).
 template <int kCtrl>
-__device__ __forceinline__ double dpp_d(double v) {
+__device__ __forceinline__ double lane_of(double v) {
     const uint64_t u = __builtin_bit_cast(uint64_t, v);
-    return __builtin_bit_cast(double, (uint64_t)(uint32_t)dpp_i<kCtrl>((int)(uint32_t)(u >> 32)) << 32 |
-                                          (uint32_t)dpp_i<kCtrl>((int)(uint32_t)u));
+    return __builtin_bit_cast(double, (uint64_t)(uint32_t)lane_of<kCtrl>((int)(uint32_t)(u >> 32)) << 32 |
+                                          (uint32_t)lane_of<kCtrl>((int)(uint32_t)u));
 }
 __device__ __forceinline__ double row_sum(double v) {
-    v += dpp_d<kDppXor1>(v);
-    v += dpp_d<kDppXor2>(v);
-    v += dpp_d<kDppHalfMirror>(v);
-    v += dpp_d<kDppMirror>(v);
+    v += lane_of<kDppXor1>(v);
+    v += lane_of<kDppXor2>(v);
+    v += lane_of<kDppHalfMirror>(v);
+    v += lane_of<kDppMirror>(v);
     return v;
 }
 
@@ -120,7 +126,11 @@ __global__ __launch_bounds__(kThreads, 2) void scan_grad_kernel(ScanGradArgs s) 
         *reinterpret_cast<v4i*>(lds + Lds::kK + i * 16) = *reinterpret_cast<const v4i*>(block + i * 16);
     for (int i = tid; i < kOut * kPlane / 16; i += kThreads)    // (tiles above the diagonal stay zero)
         *reinterpret_cast<v4i*>(lds + Lds::kW + i * 16) = v4i{0, 0, 0, 0};
-    const int st = wave & 3, half = wave >> 2;        // M's tiles: columns st, rows st + half and st + half + 2
+    // M's tiles: columns st, rows st + half and st + half + 2 (up to 3).  Waves w and w + 4 are on one SIMD: the ten tiles are dealt so
+    // that none has more than three, and wave 4, which has none, finishes the head before (dealt in order, four to one SIMD and one to
+    // another, and each wave in turn to finish: 8 x 2048 tokens bf16 617 us, 599 now, at best).
+    const int late = wave & 3, st = wave < 4 ? wave >> 1 : 3 - ((late ^ late >> 1) & 1), half = wave < 4 ? wave & 1 : 1 - (late & 1);
+    constexpr int kIdle = 4;
     v4f sum_w[2] = {};
     const int nt = wave % kTiles, t0 = wave / kTiles * kTT;
     const RowBuffer<kBf16> c_rows(a.C, ch.x, a.ldc, ch.y, g * kN + nt * 16, 16);
@@ -133,22 +143,33 @@ __global__ __launch_bounds__(kThreads, 2) void scan_grad_kernel(ScanGradArgs s) 
     }
     const int pt = wave & 3, sh = wave >> 2;          // dx's tiles: channels pt, tokens 2 sh and 2 sh + 1
 
+    // The kernel's arguments, read again where a turn needs them: kept over the turns they would fill the scalar registers
+    // and be moved to and from vector ones, 200 instructions a turn (2048 tokens fp32 122 us).
+    auto arguments = [] {
+        auto p = (const __attribute__((address_space(4))) ScanGradArgs*)__builtin_amdgcn_kernarg_segment_ptr();
+        asm volatile("" : "+s"(p));
+        return p;
+    };
+
     // What a turn needs of a head's rows and states is loaded in the turn before, as soon as the registers that hold it are free.
     v4f y0, y1, x0, x1;
     float decays = 0.0f;
     static_assert(kHeadArrays * kChunk <= kThreads, "one value a thread");
     auto load_rows = [&](int k, int r, int q) {   // dy and x along the channels: each wave one tile of rows and half of the channels
+        const auto now = arguments();
+        const int lddy = (int)now->lddy, ldx = (int)now->a.ldx;
         const int p = (g * per_group + k) * kP + (wave & 1) * 32, row = (wave >> 1) * 16 + r;
-        const RowBuffer<kBf16> dy_rows(s.dy, ch.x, s.lddy, ch.y, p, 32), x_rows(a.x, ch.x, a.ldx, ch.y, p, 32);
-        const int from_dy = (row * (int)s.lddy + 4 * q) * kSize, from_x = (row * (int)a.ldx + 4 * q) * kSize;
+        const RowBuffer<kBf16> dy_rows(now->dy, ch.x, lddy, ch.y, p, 32), x_rows(now->a.x, ch.x, ldx, ch.y, p, 32);
+        const int from_dy = (row * lddy + 4 * q) * kSize, from_x = (row * ldx + 4 * q) * kSize;
         y0 = dy_rows.load4(from_dy), y1 = dy_rows.load4(from_dy + 16 * kSize);
         x0 = x_rows.load4(from_x), x1 = x_rows.load4(from_x + 16 * kSize);
-        if (tid < kHeadArrays * kChunk) decays = a.heads[((int64_t)c * a.H + g * per_group + k) * kHeadArrays * kChunk + tid];
+        if (tid < kHeadArrays * kChunk) decays = now->a.heads[((int64_t)c * now->a.H + g * per_group + k) * kHeadArrays * kChunk + tid];
     };
     float h_at[2][8], dh_at[2][8];
     auto load_states = [&](int k, int from) { // the states at this wave's places, across the channels
-        const int64_t at = ((int64_t)c * a.H + g * per_group + k) * kP * kN;
-        const RowBuffer<false> h(s.starts, 0, 0, 1, at, kP * kN), dh(s.ends, 0, 0, 1, at, kP * kN);
+        const auto now = arguments();
+        const int64_t at = ((int64_t)c * now->a.H + g * per_group + k) * kP * kN;
+        const RowBuffer<false> h(now->starts, 0, 0, 1, at, kP * kN), dh(now->ends, 0, 0, 1, at, kP * kN);
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -160,6 +181,7 @@ __global__ __launch_bounds__(kThreads, 2) void scan_grad_kernel(ScanGradArgs s) 
     // ddt of a head and its share of the parameters' sums, a token a lane: by one wave in the turn after the head's own, from
     // what the turn has left in LDS
     auto finish = [&](int k, int lane) {
+        const auto now = arguments();
         const int head = g * per_group + k;
         const float* const part = reinterpret_cast<const float*>(lds + Lds::kPart) + (k & 1) * Lds::kParts;
         const float* const arrays = part + Lds::kArrays;
@@ -192,12 +214,12 @@ __global__ __launch_bounds__(kThreads, 2) void scan_grad_kernel(ScanGradArgs s) 
             if (lane >= d) before += p;
         }
         const float da = (float)(from + (before - own) + pass);
-        const float rate = expf(a.A_log[head]);
+        const float rate = expf(now->a.A_log[head]);
         float raw = 0.0f, ddt = 0.0f;
         if (lane < ch.y) {
-            raw = a.dt[(int64_t)(ch.x + lane) * a.lddt + head] + a.dt_bias[head];
+            raw = now->a.dt[(int64_t)(ch.x + lane) * now->a.lddt + head] + now->a.dt_bias[head];
             ddt = (z - rate * da) * (raw > 20.0f ? 1.0f : 1.0f / (1.0f + expf(-raw)));
-            s.ddt[(int64_t)(ch.x + lane) * s.ldddt + head] = ddt;
+            now->ddt[(int64_t)(ch.x + lane) * now->ldddt + head] = ddt;
         }
         float sum_a = -rate * dt * da, sum_d = part[Lds::kDot + lane], sum_t = ddt;
 #pragma unroll
@@ -207,7 +229,7 @@ __global__ __launch_bounds__(kThreads, 2) void scan_grad_kernel(ScanGradArgs s) 
             sum_t += __shfl_xor(sum_t, d);
         }
         if (lane == 0)
-            *reinterpret_cast<v4f*>(s.sums + ((int64_t)c * a.H + head) * kSums) = v4f{sum_a, sum_d, sum_t, 0.0f};
+            *reinterpret_cast<v4f*>(now->sums + ((int64_t)c * now->a.H + head) * kSums) = v4f{sum_a, sum_d, sum_t, 0.0f};
     };
     load_rows(first, r, q);
     for (int k = first; k < last; ++k) {
@@ -238,7 +260,7 @@ __global__ __launch_bounds__(kThreads, 2) void scan_grad_kernel(ScanGradArgs s) 
         const Pieces<kFull> hp[2] = {split<kFull>(h_at[0]), split<kFull>(h_at[1])};
         const Pieces<kFull> dhp[2] = {split<kFull>(dh_at[0]), split<kFull>(dh_at[1])};
         __syncthreads();
-        if (k > first && wave == ((k - 1) & 7)) finish(k - 1, lane);
+        if (k > first && wave == kIdle) finish(k - 1, lane);
         __builtin_amdgcn_sched_barrier(0);
         {   // dC and dB through the states
             v4f us[kTT];     // C . (h^T dy), the wave's places
@@ -267,7 +289,8 @@ __global__ __launch_bounds__(kThreads, 2) void scan_grad_kernel(ScanGradArgs s) 
         // for dx: the state's gradient along the state
         v4f dh_rows[2 * kSteps];
         {
-            const RowBuffer<false> dh(s.ends, 0, 0, 1, ((int64_t)c * a.H + head) * kP * kN, kP * kN);
+            const auto now = arguments();
+            const RowBuffer<false> dh(now->ends, 0, 0, 1, ((int64_t)c * now->a.H + head) * kP * kN, kP * kN);
 #pragma unroll
             for (int n = 0; n < 2 * kSteps; ++n) dh_rows[n] = dh.load4(((pt * 16 + r) * kN + 4 * q + n * 16) * 4);
         }
@@ -334,16 +357,18 @@ __global__ __launch_bounds__(kThreads, 2) void scan_grad_kernel(ScanGradArgs s) 
         __syncthreads();
         float dy[2][8], x_at[2][4];     // dy across the tokens, and x where dx lies
         {
-            const RowBuffer<kBf16> dy_rows(s.dy, ch.x, s.lddy, ch.y, head * kP + pt * 16, 16), x_rows(a.x, ch.x, a.ldx, ch.y, head * kP + pt * 16, 16);
-            const int from_dy = (4 * q * (int)s.lddy + r) * kSize, from_x = ((sh * 32 + 4 * q) * (int)a.ldx + r) * kSize;
+            const auto now = arguments();
+            const int lddy = (int)now->lddy, ldx = (int)now->a.ldx, p = head * kP + pt * 16;
+            const RowBuffer<kBf16> dy_rows(now->dy, ch.x, lddy, ch.y, p, 16), x_rows(now->a.x, ch.x, ldx, ch.y, p, 16);
+            const int from_dy = (4 * q * lddy + r) * kSize, from_x = ((sh * 32 + 4 * q) * ldx + r) * kSize;
 #pragma unroll
             for (int i = 0; i < 2; ++i)
 #pragma unroll
-                for (int j = 0; j < 8; ++j) dy[i][j] = dy_rows.load(from_dy + (i * 32 + place(0, j)) * (int)s.lddy * kSize);
+                for (int j = 0; j < 8; ++j) dy[i][j] = dy_rows.load(from_dy + (i * 32 + place(0, j)) * lddy * kSize);
 #pragma unroll
             for (int i = 0; i < 2; ++i)
 #pragma unroll
-                for (int v = 0; v < 4; ++v) x_at[i][v] = x_rows.load(from_x + (i * 16 + v) * (int)a.ldx * kSize);
+                for (int v = 0; v < 4; ++v) x_at[i][v] = x_rows.load(from_x + (i * 16 + v) * ldx * kSize);
         }
         load_rows(k + 1 < last ? k + 1 : k, r, q);
         __builtin_amdgcn_sched_barrier(0);
@@ -368,9 +393,11 @@ __global__ __launch_bounds__(kThreads, 2) void scan_grad_kernel(ScanGradArgs s) 
                 for (int j = 0; j < 2; ++j)
                     if (j >= sh)     // (tokens t from the tile's own on)
                         intra[i] = mma(load_pieces<kOut>(lds + Lds::kW + (((2 * sh + i) * 2 + j) * 64 + lane) * 16, kPlane), rows[j], intra[i]);
-            const float skip = a.D[head];
-            const RowBuffer<kBf16> dx_rows(s.dx, ch.x, s.lddx, ch.y, head * kP + pt * 16, 16);
-            const int to = (4 * q * (int)s.lddx + r) * kSize;
+            const auto now = arguments();
+            const float skip = now->a.D[head];
+            const int lddx = (int)now->lddx;
+            const RowBuffer<kBf16> dx_rows(now->dx, ch.x, lddx, ch.y, head * kP + pt * 16, 16);
+            const int to = (4 * q * lddx + r) * kSize;
             v4f along[2];          // x . (g B)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
@@ -383,7 +410,7 @@ __global__ __launch_bounds__(kThreads, 2) void scan_grad_kernel(ScanGradArgs s) 
                     along[i][v] = row_sum(x_at[i][v] * inter[v]);
                     const float own = sh == 0 ? dy[0][i * 4 + v] : dy[1][i * 4 + v];
                     dx_rows.store(fmaf(skip, own, fmaf(dt[v], intra[i][v], weight[v] * inter[v])),
-                                  to + (tile * 16 + v) * (int)s.lddx * kSize);
+                                  to + (tile * 16 + v) * lddx * kSize);
                 }
             }
             if (r == 0)
@@ -394,7 +421,7 @@ __global__ __launch_bounds__(kThreads, 2) void scan_grad_kernel(ScanGradArgs s) 
         __builtin_amdgcn_sched_barrier(0);
     }
     __syncthreads();
-    if (wave == ((last - 1) & 7)) finish(last - 1, lane);
+    if (wave == kIdle) finish(last - 1, lane);
 
     // dC += W B and dB += W^T C with W the heads' sum of M L dt
     __syncthreads();

@@ -210,3 +210,37 @@ def test_gradient_against_differences():
         slope, mine = float((up - down) / (2 * h)), float((got.double() * way).sum())
         scale = float((got.double() * way).abs().sum())
         assert abs(slope - mine) <= 2.0 ** -14 * scale
+
+
+def test_captured_and_replayed():
+    """Both directions in a graph, replayed on other operands with eager calls in between: the bits of the eager calls."""
+    from bit_scaffold_int8_amd import dfssm
+    M, V, K, k, T = 40, 700, 64, 20, 1.5
+    batches = [(ref.head(M, V, K, seed=s)[:4], *teacher(M, V, k, seed=s)) for s in (11, 12, 13)]
+    x_q, s_x, e, s_e = (t.clone() for t in batches[0][0])
+    ids, top = batches[0][1].clone(), batches[0][2].clone()
+    dloss = torch.rand(M, device="cuda")
+    loss, lse = torch.empty(M, device="cuda"), torch.empty(M, device="cuda")
+    logp, dx, de = torch.empty(M, k, device="cuda"), torch.empty(M, K, device="cuda"), torch.empty(V, K, device="cuda")
+    n = max(dfssm.dfssm_distillation_workspace_bytes(M, V, K, k), dfssm.dfssm_distillation_backward_workspace_bytes(M, V, K, k, dx, de))
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    ones = torch.ones(1000, device="cuda")
+
+    def step():
+        dfssm.dfssm_distillation(x_q, s_x, e, s_e, ids, top, T, loss, lse, logp, ws)
+        dfssm.dfssm_distillation_backward(x_q, s_x, e, s_e, ids, top, T, lse, logp, dloss, dx, de, ws)
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for ops, i, t in batches + batches[:1]:
+        for to, source in zip((x_q, s_x, e, s_e, ids, top), (*ops, i, t)):
+            to.copy_(source)
+        graph.replay()
+        got = [v.clone() for v in (loss, lse, logp, dx, de)]
+        assert float((ones * 2).sum()) == 2000.0
+        want = forward(ops, i, t, T)
+        want += backward(ops, i, t, T, want[1], want[2], dloss, False)
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)

@@ -108,6 +108,7 @@ SHAPES = [
     ([1, 0, 63, 64, 65, 129], 3, 128, 1, True, 7, 0),
     ([0, 200, 0], 2, 64, 2, True, 0, 3),
     ([0, 0], 2, 128, 1, True, 5, 0),
+    ([90, 3], 40, 64, 40, True, 2, 0),      # a head to a group, more heads than a launch's part of the decays holds
     ([2, 0, 7, 3], 6, 128, 3, True, 4, 2),
     # (from here on by chunks, as 130, 130 and 300 above; the others token by token)
     ([128], 2, 128, 1, False, 0, 0),
@@ -135,13 +136,11 @@ def test_scan_from_zeros_and_in_place(lens):
     check(o, lens, where, inside, torch.float32, y, state)
 
 
-@pytest.mark.parametrize("lens", [[40], [200]])
-@pytest.mark.parametrize("kind", ["forgets", "keeps", "steps above 20", "mixed"])
-def test_scan_extreme_decays(lens, kind):
-    """Decays of nothing and of everything, and steps where softplus is the identity: finite, and within the bounds.  (An
-    exponent of 2^12 and more errs by more than the bounds' 16, but its term is zero on both sides.)"""
-    o, where, inside = make(lens, 4, 128, seed=9)
-    T = lens[0]
+EXTREMES = ["forgets", "keeps", "steps above 20", "mixed"]
+
+
+def extreme(o, kind):
+    T = o["dt"].shape[0]
     if kind == "forgets":
         o["dt"] += 8.0
         o["A_log"] += 6.0
@@ -153,6 +152,15 @@ def test_scan_extreme_decays(lens, kind):
     else:
         o["dt"][::3] += 30.0
         o["dt"][1::3] -= 30.0
+
+
+@pytest.mark.parametrize("lens", [[40], [200]])
+@pytest.mark.parametrize("kind", EXTREMES)
+def test_scan_extreme_decays(lens, kind):
+    """Decays of nothing and of everything, and steps where softplus is the identity: finite, and within the bounds.  (An
+    exponent of 2^12 and more errs by more than the bounds' 16, but its term is zero on both sides.)"""
+    o, where, inside = make(lens, 4, 128, seed=9)
+    extreme(o, kind)
     y, state = run(o, lens, where, torch.float32, False)
     assert bool(torch.isfinite(y).all()) and bool(torch.isfinite(state).all())
     check(o, lens, where, inside, torch.float32, y, state)

@@ -11,7 +11,7 @@ import pytest
 import torch
 
 import sequences_reference as ref
-from test_gpu_mamba2_scan import make, packed
+from test_gpu_mamba2_scan import EXTREMES, extreme, make, packed
 
 pytestmark = pytest.mark.gpu
 
@@ -124,7 +124,14 @@ def check(o, dy, dstate, lens, where, inside, dtype, out, with_state=True):
         assert bool((err <= bound).all()), (k, float((err / bound).max()))
         if dtype is torch.float32 or k not in ("x", "B", "C"):
             rms = lambda t: float(t.pow(2).mean().sqrt())  # noqa: E731
-            assert rms(err) <= 2.0 ** -19 * rms(m), (k, rms(err) / rms(m))
+            # Every term of the state's gradient has the first token's decay e^-c, c = step exp(A_log), as a factor, and c's error
+            # is the same in all of them: the exponential's and the rounding of the product, 2^-24 of c each, make c 2^-23.  For c up to
+            # 16 that is 2^-19 and below; past it, it is what the terms' roundings do not average out.
+            c = 16.0
+            if k == "state" and bool(inside.any()):
+                steps = torch.nn.functional.softplus(a["dt"] + a["dt_bias"], threshold=20) * torch.exp(a["A_log"])
+                c = max(c, float(torch.stack([steps[b].min() for b, e in where if e > b]).min()))
+            assert rms(err) <= c * 2.0 ** -23 * rms(m), (k, rms(err) / rms(m), c)
 
 
 SHAPES = [
@@ -140,6 +147,7 @@ SHAPES = [
     ([0, 150, 0], 2, 64, 2, True, 0, 3),
     ([0, 0], 2, 128, 1, True, 5, 0),
     ([2, 0, 7, 3], 6, 128, 3, True, 4, 2),
+    ([90, 3], 40, 64, 40, True, 2, 0),
 ]
 
 
@@ -168,6 +176,17 @@ def test_gradients_without_states_and_in_place(lens):
     out = run(o, dy, dstate, lens, where, torch.float32, False, state=False)
     check(o, dy, dstate, lens, where, inside, torch.float32, out, with_state=False)
     out = run(o, dy, dstate, lens, where, torch.float32, False, in_place=True)
+    check(o, dy, dstate, lens, where, inside, torch.float32, out)
+
+
+@pytest.mark.parametrize("lens", [[40], [200]])
+@pytest.mark.parametrize("kind", EXTREMES)
+def test_gradients_extreme_decays(lens, kind):
+    """As forward: decays of nothing and of everything, steps where softplus is the identity."""
+    o, where, inside, dy, dstate = operands((lens, 4, 128, 1, False, 0, 0), torch.float32)
+    extreme(o, kind)
+    out = run(o, dy, dstate, lens, where, torch.float32, False)
+    assert all(bool(torch.isfinite(v).all()) for v in out.values())
     check(o, dy, dstate, lens, where, inside, torch.float32, out)
 
 

@@ -143,7 +143,7 @@ __global__ __launch_bounds__(kThreads, 2) void scan_grad_kernel(ScanGradArgs s) 
     }
     const int pt = wave & 3, sh = wave >> 2;          // dx's tiles: channels pt, tokens 2 sh and 2 sh + 1
 
-    // The kernel's arguments, read again where a turn needs them: kept over the turns they would fill the scalar registers
+    // The kernel's arguments (one struct, at the segment's start), read again where a turn needs them: kept over the turns they would fill the scalar registers
     // and be moved to and from vector ones, 200 instructions a turn (2048 tokens fp32 122 us).
     auto arguments = [] {
         auto p = (const __attribute__((address_space(4))) ScanGradArgs*)__builtin_amdgcn_kernarg_segment_ptr();

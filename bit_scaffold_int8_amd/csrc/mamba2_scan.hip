@@ -24,7 +24,8 @@
 // The sweeps are bound by the issue of their instructions.  For y of bf16 data a wave issues 184 matrix instructions a chunk (16
 // cycles of a SIMD each) and about 1030 vector ones (to split the state and the chunk's weights into pieces, above all), and
 // with two waves to a SIMD the two kinds hardly overlap; fp32 data take 3 pieces and twice the matrix instructions, and
-// there the segments' states, 64 KB a head and segment written and read, cost as much as the chunks.
+// there the segments' states, 64 KB a head and segment written and read, cost as much as the chunks.  The sweeps that store the
+// states of every chunk are bound by that: 8 x 2048 tokens bf16 146 us at best, 4.6 TB/s.
 // (At 16384 tokens the whole is 285 MB and 215 us: a quarter of the memory's rate.)
 #include <math.h>
 

@@ -452,7 +452,7 @@ const char* dfssm_status_string(dfssm_status status) {
     return "DFSSM_ERR_UNKNOWN";
 }
 
-int32_t dfssm_version(void) { return 401; }
+int32_t dfssm_version(void) { return 402; }
 
 dfssm_status dfssm_prefill_plan(int64_t M, int64_t N, int64_t K, int64_t batch, int32_t* main_cfg,
                                 int32_t* tail_cfg, int64_t* n_split) {

@@ -220,14 +220,17 @@ __global__ __launch_bounds__(256) void teacher_logits_kernel(LossArgs a, Teacher
 }
 
 // A token's teacher, lane i with entries i, i + 64, ..: its probabilities (0 where there is no entry) and their logarithms.
+// A NaN or +infinity among its entries makes all of them NaN, as the softmax of them is: a teacher that overflowed shows in the
+// loss.  (fmaxf passes a NaN over, so whether a token counts is not told by the maximum.)
 struct Teacher {
     int id[kMaxTop / 64];
     float q[kMaxTop / 64], logq[kMaxTop / 64];
-    bool counts;   // some entry has a probability
+    bool counts;   // some entry's logit is not -infinity
     __device__ __forceinline__ Teacher(const TeacherArgs& t, int64_t m, int64_t V) {
         const int lane = threadIdx.x & 63;
         const float neg = -__builtin_inff();
         float best = neg, sum = 0.0f;
+        bool some = false;
 #pragma unroll
         for (int i = 0; i < kMaxTop / 64; ++i) {
             const int j = i * 64 + lane;
@@ -235,9 +238,10 @@ struct Teacher {
             if (id[i] < 0 || id[i] >= V) id[i] = -1;
             q[i] = id[i] < 0 ? neg : t.top[m * t.k + j];   // (what stands where there is no entry is not looked at)
             best = fmaxf(best, q[i]);
+            some |= q[i] != neg;
         }
         best = wave_max(best);
-        counts = best != neg;
+        counts = __ballot(some) != 0;
 #pragma unroll
         for (int i = 0; i < kMaxTop / 64; ++i) {
             logq[i] = counts ? (q[i] - best) * t.inv_t : neg;
@@ -271,7 +275,7 @@ __global__ __launch_bounds__(1024) void distillation_join_kernel(LossArgs a, Tea
         if (teacher.id[i] < 0) continue;
         const float lp = logp[m * t.k + j] - l;
         logp[m * t.k + j] = lp;
-        if (teacher.q[i] > 0.0f) sum = fmaf(teacher.q[i], teacher.logq[i] - lp, sum);  // (0 log 0 = 0)
+        if (!(teacher.q[i] == 0.0f)) sum = fmaf(teacher.q[i], teacher.logq[i] - lp, sum);  // (0 log 0 = 0; a NaN is no zero)
     }
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) sum += __shfl_xor(sum, d);

@@ -535,7 +535,9 @@ dfssm_status dfssm_cross_entropy_backward(const int8_t* x_q, const float* s_x, i
  *   x_q, s_x, e, s_e as in dfssm_cross_entropy
  *   top_ids int32 [M][top], top_logits fp32 [M][top] (read): an id outside [0, V) is no entry (a padded row; its logit may be anything, its
  *             logp is 0); a logit of -infinity has q = 0; a token of no entry, or of such logits only, does not count: its
- *             loss is 0.  Order does not matter, and an id may stand twice (its entries are those of the sum above).
+ *             loss is 0.  Order does not matter, and an id may stand twice (its entries are those of the sum above).  A NaN or
+ *             +infinity among a token's entries makes its loss NaN, and in the backward call its row of dx and the rows of
+ *             de that its entries name; nothing else.
  *   loss, lse fp32 [M], logp fp32 [M][top] (written)
  *   temperature  T, finite and above 0: at least 2^-60
  *   workspace  at least dfssm_distillation_workspace_bytes(M, V, K, top) bytes, under dfssm_cross_entropy's rules

@@ -53,12 +53,16 @@ struct ConvGradArgs {
 
 // 1 / (1 + exp(-v)) to about two steps of fp32: the exponential in base 2 with the rounding of v log2 e made up for, and the
 // hardware's reciprocal (expf and a correctly rounded division take three times the instructions, which then bound the
-// kernel: 4158 x 4352 fp32 to bf16 27 us).  The exponent ends at 126: there the result is below 2^-125.
+// kernel: 4158 x 4352 fp32 to bf16 27 us).  The argument is cut before anything is formed of it, so that the exponential and the
+// correction stay finite: above 126 the result is 1; below -87 it is 0 (in truth below 2^-125, where the reciprocal ends), so
+// that the product with any v, and the slope's, vanishes as it should.
 __device__ __forceinline__ float sigmoid(float v) {
-    constexpr float kLog2e = 1.44269504088896340736f, kLog2eRest = 1.92596299e-8f, kLn2 = 0.693147180559945f;
-    const float t = -v * kLog2e, rest = fmaf(-v, kLog2e, -t) - v * kLog2eRest;
-    const float e = __builtin_amdgcn_exp2f(fminf(t, 126.0f));
-    return __builtin_amdgcn_rcpf(fmaf(e, rest * kLn2, e) + 1.0f);
+    constexpr float kLog2e = 1.44269504088896340736f, kLog2eRest = 1.92596299e-8f, kLn2 = 0.693147180559945f, kLeast = -87.0f;
+    const float c = fminf(fmaxf(v, kLeast), 126.0f);   // (a NaN comes back with the product or the slope)
+    const float t = -c * kLog2e, rest = fmaf(-c, kLog2e, -t) - c * kLog2eRest;
+    const float e = __builtin_amdgcn_exp2f(t);
+    const float s = __builtin_amdgcn_rcpf(fmaf(e, rest * kLn2, e) + 1.0f);
+    return v < kLeast ? 0.0f : s;
 }
 
 // kVec channels' values of a row.

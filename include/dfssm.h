@@ -539,7 +539,9 @@ dfssm_status dfssm_cross_entropy_backward(const int8_t* x_q, const float* s_x, i
  *             +infinity among a token's entries makes its loss NaN, and in the backward call its row of dx and the rows of
  *             de that its entries name; nothing else.
  *   loss, lse fp32 [M], logp fp32 [M][top] (written)
- *   temperature  T, finite and above 0: at least 2^-60
+ *   temperature  T, from 2^-60 up to 2^60.  z / T and lse are fp32: their difference, p's logarithm, errs by up to about
+ *             2^-20 of their size, which the loss has as its own error and p, in the gradients, as a relative one (T so small
+ *             that z / T passes 2^16 leaves p few bits or none)
  *   workspace  at least dfssm_distillation_workspace_bytes(M, V, K, top) bytes, under dfssm_cross_entropy's rules
  * Errors: as dfssm_cross_entropy; DFSSM_ERR_INVALID_ARG for top <= 0 or a temperature out of range, DFSSM_ERR_UNSUPPORTED for
  * top > 256 or M * top > 2^28.
@@ -659,7 +661,8 @@ dfssm_status dfssm_mamba2_conv_backward(const void* xbc, int64_t ldx, int32_t in
  *   state_in  fp32 [S][nheads][64][d_state], or NULL for zeros: the layout of dfssm_mamba2_decode_step
  *   cu_seqlens, T, S: as in dfssm_mamba2_conv; rows outside every sequence are left alone
  * x, B, C and y start at multiples of 16 bytes and have strides that are multiples of 16 bytes; the states are 16-byte aligned.
- * Non-finite values and sizes are not checked: rows behind a sequence may hold anything, others must be finite.
+ * Non-finite values are not checked: rows behind a sequence may hold anything, others must be finite (by chunks a NaN or an
+ * infinity reaches earlier tokens of its chunk, too).
  */
 typedef struct dfssm_mamba2_scan_operands {
     const void* x;
@@ -677,12 +680,14 @@ typedef struct dfssm_mamba2_scan_operands {
 } dfssm_mamba2_scan_operands;
 
 /*
- *   y          type [T][nheads][64], rows ldy apart, written
+ *   y          type [T][nheads][64], rows ldy apart, written; overlaps no input
  *   state_out  fp32 [S][nheads][64][d_state], written, or NULL; may be state_in itself (the update in place)
  *   workspace  at least dfssm_mamba2_scan_workspace_bytes(T, S, nheads, headdim, d_state, ngroups) bytes, 16-byte
  *              aligned, under dfssm_cross_entropy's rules
  * Short sequences go token by token through the recurrence in fp32 (one launch, the workspace unused): of 64 heads, one of up
- * to 68 tokens, 8 of 22 on average, 64 of 9; longer ones by chunks of 64 tokens on the matrix cores.  There fp32 operands and the state are taken in
+ * to 67 tokens, 8 of 21, 64 of 9; longer ones by chunks of 64 tokens on the matrix cores.  Lengths lie in device memory: the host
+ * goes by T / S, so one form serves all sequences of a call, and a long one among many short ones takes longer than in a call of
+ * its own (a token at a time, or its chunks one after another).  There fp32 operands and the state are taken in
  * three bf16 pieces (relative error 2^-24 of each), and where y is bf16 the state's and the chunk's weights enter y in two
  * (2^-17); the state itself is fp32 and formed from three pieces for either type.  A chunk's decays are
  * differences of sums in fp64.  Sums run in a fixed order: equal inputs give equal bits.

@@ -664,7 +664,7 @@ bool scan_recurrent(const Sequences& seq, int H) {
 // (8 x 2048 tokens, bf16: states 159 us a sweep, 221 by segments and four heads; one sequence of 16384 tokens, cut into segments
 // anyway: 285 us, 221 with four heads; 2048 fp32 78 and 75).
 constexpr int kSweepGroups = 256;
-constexpr int64_t kMaxSegmentHeads = 8 * kSweepGroups;   // room for the segments' states, in heads
+constexpr int64_t kMaxSegmentHeads = 8 * kSweepGroups;   // the most heads that have segments' states: 67 MB at d_state 128
 
 ScanPlan scan_plan(const Sequences& seq, int H, int G) {
     ScanPlan p{};
@@ -710,8 +710,10 @@ size_t scan_workspace(ScanArgs& a, SweepArgs& s, uint8_t* ws, int64_t T, int64_t
     a.first_segment = reinterpret_cast<int*>(take((S + 1) * 8));
     a.groups = take(chunks * G * group_bytes);
     a.heads = reinterpret_cast<float*>(take(chunks * H * kHeadArrays * kChunk * 4));
-    s.segment_states = reinterpret_cast<float*>(take(kMaxSegmentHeads * kP * N * 4));
-    s.segment_decay = reinterpret_cast<float*>(take(kMaxSegmentHeads * 4));
+    // (at most a segment a chunk and one more a sequence)
+    const int64_t heads = (chunks + S) * H < kMaxSegmentHeads ? (chunks + S) * H : kMaxSegmentHeads;
+    s.segment_states = reinterpret_cast<float*>(take(heads * kP * N * 4));
+    s.segment_decay = reinterpret_cast<float*>(take(heads * 4));
     return at;
 }
 

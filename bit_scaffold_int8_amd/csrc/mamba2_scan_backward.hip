@@ -539,7 +539,9 @@ GradParts grad_parts(ScanArgs& a, SweepArgs& s, uint8_t* ws, int64_t T, int64_t 
     p.starts = take(chunks * H * kP * N * 4);
     p.ends = take(chunks * H * kP * N * 4);
     p.sums = take(chunks * H * kSums * 4);
-    p.slabs = take((int64_t)kMaxSlabs * 2 * kChunk * N * 4);
+    // (a group's slices are no more than its heads)
+    const int64_t slabs = chunks * H < kMaxSlabs ? chunks * H : kMaxSlabs;
+    p.slabs = take(slabs * 2 * kChunk * N * 4);
     p.bytes = at;
     return p;
 }

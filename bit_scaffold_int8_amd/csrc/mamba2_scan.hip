@@ -607,12 +607,6 @@ __global__ __launch_bounds__(256) void recurrent_kernel(SweepArgs s) {
         for (int i = 0; i < kV4; ++i) *reinterpret_cast<v4f*>(s.end + at + 4 * i) = h[i];
 }
 
-template <class F>
-hipError_t with_kind(bool bf16, int N, F f) {
-    if (N == 128) return bf16 ? f(std::true_type(), std::integral_constant<int, 128>()) : f(std::false_type(), std::integral_constant<int, 128>());
-    return bf16 ? f(std::true_type(), std::integral_constant<int, 64>()) : f(std::false_type(), std::integral_constant<int, 64>());
-}
-
 }  // namespace
 
 hipError_t launch_scan_prepare(const ScanArgs& a, bool bf16, int N, bool backward, hipStream_t stream) {

@@ -29,10 +29,6 @@
 
 namespace dfssm {
 
-size_t scan_workspace(ScanArgs& a, SweepArgs& s, uint8_t* ws, int64_t T, int64_t S, int64_t H, int64_t G, int N, int group_bytes);
-int scan_group_bytes(bool bf16, int N, bool backward);
-ScanPlan scan_plan(const Sequences& seq, int H, int G);
-
 namespace {
 
 constexpr int kThreads = 512;
@@ -514,12 +510,6 @@ __global__ __launch_bounds__(256) void join_sums_kernel(ScanArgs a, const float*
         dD[head] = part[0].y;
         ddt_bias[head] = part[0].z;
     }
-}
-
-template <class F>
-hipError_t with_kind(bool bf16, int N, F f) {
-    if (N == 128) return bf16 ? f(std::true_type(), std::integral_constant<int, 128>()) : f(std::false_type(), std::integral_constant<int, 128>());
-    return bf16 ? f(std::true_type(), std::integral_constant<int, 64>()) : f(std::false_type(), std::integral_constant<int, 64>());
 }
 
 struct GradParts {

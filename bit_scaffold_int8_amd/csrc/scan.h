@@ -205,4 +205,16 @@ struct SweepArgs {
 };
 hipError_t launch_sweep(const SweepArgs& s, const ScanPlan& plan, bool bf16, int N, SweepMode mode, hipStream_t stream);
 
+// f for the type of the data and d_state (64 or 128), as constants.
+template <class F>
+hipError_t with_kind(bool bf16, int N, F f) {
+    if (N == 128) return bf16 ? f(std::true_type(), std::integral_constant<int, 128>()) : f(std::false_type(), std::integral_constant<int, 128>());
+    return bf16 ? f(std::true_type(), std::integral_constant<int, 64>()) : f(std::false_type(), std::integral_constant<int, 64>());
+}
+
+// The host's side of the forward pass that the backward pass shares (mamba2_scan.hip).
+ScanPlan scan_plan(const Sequences& seq, int H, int G);
+int scan_group_bytes(bool bf16, int N, bool backward);
+size_t scan_workspace(ScanArgs& a, SweepArgs& s, uint8_t* ws, int64_t T, int64_t S, int64_t H, int64_t G, int N, int group_bytes);
+
 }  // namespace dfssm

@@ -91,6 +91,7 @@ size_t mamba2_scan_workspace_bytes(int64_t T, int64_t S, int64_t H, int64_t N, i
 hipError_t launch_mamba2_scan(ScanArgs a, bool bf16, int N, const float* state_in, float* state_out, void* y, int64_t ldy,
                               void* workspace, hipStream_t stream);
 int64_t distillation_max_top();
+size_t distillation_workspace_bytes(int64_t M, int64_t V, int64_t K);
 hipError_t launch_distillation(const int8_t* x_q, const float* s_x, int64_t M, int64_t V, int64_t K, const int8_t* e,
                                const float* s_e, const int32_t* ids, const float* top, int64_t k, float temperature,
                                float* loss, float* lse, float* logp, void* workspace, hipStream_t stream);
@@ -731,7 +732,7 @@ dfssm_status dfssm_cross_entropy_backward(const int8_t* x_q, const float* s_x, i
 }
 
 size_t dfssm_distillation_workspace_bytes(int64_t M, int64_t V, int64_t K, int64_t top) {
-    return distillation_sizes(M, V, K, top) == DFSSM_OK ? dfssm::cross_entropy_workspace_bytes(M, V, K) : 0;
+    return distillation_sizes(M, V, K, top) == DFSSM_OK ? dfssm::distillation_workspace_bytes(M, V, K) : 0;
 }
 
 dfssm_status dfssm_distillation(const int8_t* x_q, const float* s_x, int64_t M, int64_t V, int64_t K, const int8_t* e,
@@ -744,7 +745,7 @@ dfssm_status dfssm_distillation(const int8_t* x_q, const float* s_x, int64_t M, 
         !aligned4(top_ids) || !aligned4(top_logits) || !aligned4(loss) || !aligned4(lse) || !aligned4(logp))
         return DFSSM_ERR_INVALID_ARG;
     if (dfssm_status st = distillation_sizes(M, V, K, top)) return st;
-    if (workspace_bytes < dfssm::cross_entropy_workspace_bytes(M, V, K)) return DFSSM_ERR_INVALID_ARG;
+    if (workspace_bytes < dfssm::distillation_workspace_bytes(M, V, K)) return DFSSM_ERR_INVALID_ARG;
     return dfssm::launch_distillation(x_q, s_x, M, V, K, e, s_e, top_ids, top_logits, top, temperature, loss, lse, logp,
                                       workspace, stream) == hipSuccess
                ? DFSSM_OK

@@ -28,6 +28,13 @@
 // Forward, the rows' logits are formed by themselves (k dot products a token); backward, the gradient tiles
 // write d with no target, and a small kernel then overwrites the k values a token that have one.
 //
+// p = exp(z / T - lse) has lse's absolute error as a relative one, the same for all of a token's rows: 32 bits of an lse of 30
+// leave it 1e-6, and the rounding of the logits that the sums are formed of as much again.  (561 tokens, V 2992, lse up to 22: dx was
+// 1.7e-6 from 64 bits, where fp32 with p normalized by its own sum has 1.05e-6; now 0.47e-6.)  So the tiles also add up what the logits
+// lose when they are rounded (in first order), and the lse with it goes into logp, which ends at 32 bits of a value near 0 where
+// the student knows one of the teacher's choices.  Backward takes it from there: lse = z_j / T - logp_j for the j of the
+// largest logp.  Both directions scale by the same 32-bit s_x log2 e / T.
+//
 // What bounds it: forward, the int8 products under the power limit (tile_i8.h); backward, 4096 tokens x 50280 rows x
 // 2048 fp32 in 3.3 ms: the products for dx and de 1.28 and 1.34 ms (grad_gemm.h), the gradient tiles 0.67 ms, of which
 // about 0.25 are their 8 bytes a logit (1.6 GB), written in bursts between the products.
@@ -52,10 +59,12 @@ struct LossArgs {
     const float* s_e;
     float2* part;   // [ntw][M]: a tile's maximum (of z log2 e) and sum of 2^(z log2 e - maximum)
     float unit = kLog2e;  // log2 e, over the temperature
+    float* missed = nullptr;  // (distillation) [ntw][M]: what the sum lacks for the logits as they are before their rounding
 };
 
 // ---------------------------------------------------------------- forward
-template <class C>
+// kMissed: the distillation's.
+template <class C, bool kMissed>
 __global__ __launch_bounds__(C::NT, C::kMinWaves) void loss_tile_kernel(LossArgs a) {
     __shared__ __attribute__((aligned(16))) uint8_t lds[C::kLdsBytes];
     const TilePos pos = tile_pos(blockIdx.x, a.ntw, a.ntt);
@@ -80,31 +89,43 @@ __global__ __launch_bounds__(C::NT, C::kMinWaves) void loss_tile_kernel(LossArgs
         }
     lds_barrier();
     float2* const red = reinterpret_cast<float2*>(lds);  // [WW][BT]
+    float* const red_missed = reinterpret_cast<float*>(red + C::WW * C::BT);
     const float neg = -__builtin_inff();
 #pragma unroll
     for (int tb = 0; tb < C::TB && holds; ++tb) {
         const int t = (tw * C::TB + tb) * 32 + l32;
         const float sx2 = a.s_x[m0 + (t < trows ? t : trows - 1)] * a.unit;
-        float z[C::WB][16], top = neg;
+        float z[C::WB][16], rest[C::WB][16], top = neg;
 #pragma unroll
         for (int b = 0; b < C::WB; ++b)
 #pragma unroll
             for (int v = 0; v < 16; ++v) {
-                z[b][v] = sx2 * (se[b][v] * (float)acc[b][tb][v]);
+                const float unscaled = se[b][v] * (float)acc[b][tb][v];
+                z[b][v] = sx2 * unscaled;
+                if constexpr (kMissed) rest[b][v] = fmaf(unscaled, sx2, -z[b][v]);
                 if (wrows < C::BW && wn + b * 32 + 8 * (v >> 2) + 4 * g + (v & 3) >= wrows) z[b][v] = neg;
                 top = fmaxf(top, z[b][v]);
             }
         const float base = top == neg ? 0.0f : top;  // (no row of the wave's range exists, or all are -infinity)
-        float sum = 0.0f;
+        float sum = 0.0f, missed = 0.0f;
 #pragma unroll
         for (int b = 0; b < C::WB; ++b)
 #pragma unroll
-            for (int v = 0; v < 16; ++v) sum += __builtin_amdgcn_exp2f(z[b][v] - base);
+            for (int v = 0; v < 16; ++v) {
+                const float e = __builtin_amdgcn_exp2f(z[b][v] - base);
+                sum += e;
+                if constexpr (kMissed) missed = fmaf(e, rest[b][v], missed);
+            }
+        // (an infinite logit leaves 0 inf: its lane does without)
+        if constexpr (kMissed) missed = fabsf(missed) <= sum ? missed * (float)kLn2 : 0.0f;
         // the two halves of the wave hold the same tokens
-        const float otop = __shfl_xor(top, 32), osum = __shfl_xor(sum, 32);
+        const float otop = __shfl_xor(top, 32), osum = __shfl_xor(sum, 32), omissed = kMissed ? __shfl_xor(missed, 32) : 0.0f;
         const float both = fmaxf(top, otop), b2 = both == neg ? 0.0f : both;
         sum = g == 0 ? sum * __builtin_amdgcn_exp2f(top - b2) + osum * __builtin_amdgcn_exp2f(otop - b2) : 0.0f;
         if (g == 0) red[ww * C::BT + t] = make_float2(both, sum);
+        if constexpr (kMissed)
+            if (g == 0)
+                red_missed[ww * C::BT + t] = missed * __builtin_amdgcn_exp2f(top - b2) + omissed * __builtin_amdgcn_exp2f(otop - b2);
     }
     lds_barrier();
     for (int t = threadIdx.x; t < trows; t += C::NT) {
@@ -116,40 +137,64 @@ __global__ __launch_bounds__(C::NT, C::kMinWaves) void loss_tile_kernel(LossArgs
 #pragma unroll
         for (int w = 0; w < C::WW; ++w) sum += red[w * C::BT + t].y * __builtin_amdgcn_exp2f(red[w * C::BT + t].x - base);
         a.part[(int64_t)pos.w * a.M + m0 + t] = make_float2(top, sum);
+        if constexpr (kMissed) {
+            float missed = 0.0f;
+#pragma unroll
+            for (int w = 0; w < C::WW; ++w) missed += red_missed[w * C::BT + t] * __builtin_amdgcn_exp2f(red[w * C::BT + t].x - base);
+            a.missed[(int64_t)pos.w * a.M + m0 + t] = missed;
+        }
     }
 }
 
-// Joins the tiles' pairs in tile order: 16 tokens to a workgroup of 1024 threads, each wave gets its own token's lse
-// (m0 + wave; of no meaning past M).
-__device__ __forceinline__ float join_pairs(const LossArgs& a, float2 (&pairs)[16][64]) {
-    // pairs[wave][token]: a wave reads 16 tokens x 4 tiles, consecutive tokens side by side
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t m0 = (int64_t)blockIdx.x * 16;
-    const float neg = -__builtin_inff();
-    float top = neg, sum = 0.0f;
-    if (m0 + (lane & 15) < a.M)
-        for (int w = wave * 4 + (lane >> 4); w < a.ntw; w += 64) {
-            const float2 p = a.part[(int64_t)w * a.M + m0 + (lane & 15)];
-            const float t = fmaxf(top, p.x), base = t == neg ? 0.0f : t;
-            sum = sum * __builtin_amdgcn_exp2f(top - base) + p.y * __builtin_amdgcn_exp2f(p.x - base);
-            top = t;
-        }
-    pairs[wave][lane] = make_float2(top, sum);
-    __syncthreads();
-    // lane i holds pair i of the wave's token: waves i / 4, tile classes i % 4
-    const float2 p = pairs[lane >> 2][(lane & 3) * 16 + wave];
-    const float all = wave_max(p.x);
-    float s = p.y == 0.0f ? 0.0f : p.y * __builtin_amdgcn_exp2f(p.x - all);
+// Joins the tiles' pairs in tile order: 16 tokens to a workgroup of 1024 threads, each wave gets its own token's (m0 + wave; of no
+// meaning past M): the maximum, the sum and what the sum misses.
+template <bool kMissed>
+struct Joined {
+    float all, sum, missed;
+    __device__ __forceinline__ Joined(const LossArgs& a, float2 (&pairs)[16][64], float (*rests)[64]) {
+        // pairs[wave][token]: a wave reads 16 tokens x 4 tiles, consecutive tokens side by side
+        const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+        const int64_t m0 = (int64_t)blockIdx.x * 16;
+        const float neg = -__builtin_inff();
+        float top = neg, part = 0.0f, rest = 0.0f;
+        if (m0 + (lane & 15) < a.M)
+            for (int w = wave * 4 + (lane >> 4); w < a.ntw; w += 64) {
+                const float2 p = a.part[(int64_t)w * a.M + m0 + (lane & 15)];
+                const float t = fmaxf(top, p.x), base = t == neg ? 0.0f : t;
+                const float was = __builtin_amdgcn_exp2f(top - base), now = __builtin_amdgcn_exp2f(p.x - base);
+                part = part * was + p.y * now;
+                if constexpr (kMissed) rest = rest * was + a.missed[(int64_t)w * a.M + m0 + (lane & 15)] * now;
+                top = t;
+            }
+        pairs[wave][lane] = make_float2(top, part);
+        if constexpr (kMissed) rests[wave][lane] = rest;
+        __syncthreads();
+        // lane i holds pair i of the wave's token: waves i / 4, tile classes i % 4
+        const float2 p = pairs[lane >> 2][(lane & 3) * 16 + wave];
+        all = wave_max(p.x);
+        const float f = __builtin_amdgcn_exp2f(p.x - all);
+        sum = p.y == 0.0f ? 0.0f : p.y * f;
+        missed = kMissed && p.y != 0.0f ? rests[lane >> 2][(lane & 3) * 16 + wave] * f : 0.0f;
 #pragma unroll
-    for (int d = 1; d < 64; d <<= 1) s += __shfl_xor(s, d);
-    return (float)(((double)all + (double)__log2f(s)) * kLn2);  // (one rounding, of the result)
-}
+        for (int d = 1; d < 64; d <<= 1) {
+            sum += __shfl_xor(sum, d);
+            if constexpr (kMissed) missed += __shfl_xor(missed, d);
+        }
+    }
+    __device__ __forceinline__ float lse() const { return (float)(((double)all + (double)__log2f(sum)) * kLn2); }  // (one rounding, of the result)
+    // to more than 32 bits, in base 2: the sum's exponent apart, so that the logarithm is of a number between 1/2 and 1
+    __device__ __forceinline__ double lse2() const {
+        int exponent;
+        const float mantissa = frexpf(sum, &exponent);
+        return (double)all + (double)exponent + (double)(__log2f(mantissa) + missed / sum * kLog2e);
+    }
+};
 
 // The joined sums and the target's logit, a wave a token.
 __global__ __launch_bounds__(1024) void loss_join_kernel(LossArgs a, const int32_t* __restrict__ targets,
                                                          float* __restrict__ loss, float* __restrict__ lse) {
     __shared__ float2 pairs[16][64];
-    const float l = join_pairs(a, pairs);
+    const float l = Joined<false>(a, pairs, nullptr).lse();
     const int lane = threadIdx.x & 63;
     const int64_t m = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 6);
     if (m >= a.M) return;
@@ -178,13 +223,13 @@ struct TeacherArgs {
     const int32_t* ids;   // [M][k]; outside [0, V): no entry
     const float* top;     // [M][k]
     int k;
-    float inv_t;          // 1 / temperature
+    float inv_t, unit;    // 1 / temperature, log2 e / temperature
 };
 constexpr int kMaxTop = 256;    // entries a token: four a lane
 constexpr int kDots = 8;        // dot products a wave forms side by side, so that their loads are in flight together
 
-// z / T of the teacher's rows: logits[m][j].  Rows of E at random, 2 KB each, mostly from the caches (4096 tokens of 128
-// entries, K 2048: 1.07 GB in 95 us, 11 TB/s; 300 tokens of 20 6 us).
+// The logits of the teacher's rows as the tiles have them, but for s_x / T: logits[m][j].  Rows of E at random, 2 KB each, mostly from
+// the caches (4096 tokens of 128 entries, K 2048: 1.07 GB in 95 us, 11 TB/s; 300 tokens of 20 6 us).
 __global__ __launch_bounds__(256) void teacher_logits_kernel(LossArgs a, TeacherArgs t, float* __restrict__ logits) {
     const int lane = threadIdx.x & 63, groups = (t.k + kDots - 1) / kDots;
     const int64_t unit = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
@@ -210,12 +255,10 @@ __global__ __launch_bounds__(256) void teacher_logits_kernel(LossArgs a, Teacher
 #pragma unroll
             for (int w = 0; w < 4; ++w) dot[i] = __builtin_amdgcn_sdot4(xv[w], ev[i][w], dot[i], false);
     }
-    const float sx = a.s_x[m];
 #pragma unroll
     for (int i = 0; i < kDots; ++i) {
         const int all = wave_sum(dot[i]);
-        if (lane == 0 && j0 + i < t.k)
-            logits[m * t.k + j0 + i] = id[i] < 0 ? 0.0f : sx * (a.s_e[id[i]] * (float)all) * t.inv_t;
+        if (lane == 0 && j0 + i < t.k) logits[m * t.k + j0 + i] = id[i] < 0 ? 0.0f : a.s_e[id[i]] * (float)all;
     }
 }
 
@@ -263,24 +306,26 @@ struct Teacher {
 __global__ __launch_bounds__(1024) void distillation_join_kernel(LossArgs a, TeacherArgs t, float* __restrict__ loss,
                                                                  float* __restrict__ lse, float* __restrict__ logp) {
     __shared__ float2 pairs[16][64];
-    const float l = join_pairs(a, pairs);
+    __shared__ float rests[16][64];
+    const Joined<true> joined(a, pairs, rests);
     const int lane = threadIdx.x & 63;
     const int64_t m = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 6);
     if (m >= a.M) return;
     const Teacher teacher(t, m, a.V);
+    const double l2 = joined.lse2(), sx2 = (double)(a.s_x[m] * t.unit);
     float sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < kMaxTop / 64; ++i) {
         const int j = i * 64 + lane;
         if (teacher.id[i] < 0) continue;
-        const float lp = logp[m * t.k + j] - l;
+        const float lp = (float)(((double)logp[m * t.k + j] * sx2 - l2) * kLn2);
         logp[m * t.k + j] = lp;
         if (!(teacher.q[i] == 0.0f)) sum = fmaf(teacher.q[i], teacher.logq[i] - lp, sum);  // (0 log 0 = 0; a NaN is no zero)
     }
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) sum += __shfl_xor(sum, d);
     if (lane == 0) {
-        lse[m] = l;
+        lse[m] = joined.lse();
         loss[m] = sum;
     }
 }
@@ -301,8 +346,9 @@ struct GradArgs {
     uint16_t* gx;        // [tokens][Vp P]: d s_e, or NULL
     uint16_t* gw;        // [Vp][Mp P]: d s_x, or NULL
     int64_t ldgx, ldgw;  // elements
-    float inv_t = 1.0f;     // 1 / temperature: of the logits (dloss has it already)
-    bool one_target = true; // targets name a row; else they only say which tokens count
+    // (distillation: targets only say which tokens count, dloss has 1 / T, lse is in base 2, and p takes a factor of its own)
+    const float* fine = nullptr;
+    float unit = 0.0f;      // log2 e / T
 };
 
 // Partial maxima of what bounds d s_e (with the token's dloss) and d s_x (|p - [v = target]| <= 1): they scale d into
@@ -375,7 +421,8 @@ __device__ __forceinline__ void store_block(const uint8_t* blk, int ld_blk, uint
 // What lies past the vocabulary or the tokens inside the padded buffers is zero: the products read it against zero
 // codes, and an infinite one would make them NaN.  Both forms of d go through LDS, so that memory is written in whole
 // rows of a block (64 P bytes): written from the registers, d s_x would go out in 2-byte stores.
-template <class C, int P>
+// kTeacher: the distillation's.
+template <class C, int P, bool kTeacher>
 __global__ __launch_bounds__(C::NT, C::kMinWaves) void grad_tile_kernel(GradArgs a) {
     constexpr int kLd = 64 * P + 16;            // a block row in LDS
     constexpr int kBlk = 2 * 32 * kLd;          // a wave's two blocks
@@ -415,25 +462,29 @@ __global__ __launch_bounds__(C::NT, C::kMinWaves) void grad_tile_kernel(GradArgs
         const bool counts = t < trows && target >= 0 && target < a.vocab;
         // (p is formed from z - lse: in base 2 the roundings of lse log2 e and s_x log2 e would be p's largest errors;
         // 0 where the token does not count, whatever its scale and its logits are: the mask takes out a NaN, too)
-        const float scale = counts ? a.s_x[m] : 0.0f, sx = scale * a.inv_t, lse = counts ? a.lse[m] : 0.0f;
+        // (a teacher's: in base 2 with the forward pass's scale, and what lse's rounding leaves out as a factor of p)
+        const float scale = counts ? a.s_x[m] : 0.0f, lse = counts ? a.lse[m] : 0.0f, sx2 = scale * a.unit;
+        const float fine = kTeacher && counts ? a.fine[m] : 1.0f;
         const uint32_t keep = counts ? 0xFFFFFFFFu : 0u;
         const float dloss = counts ? a.dloss[m] : 0.0f;
-        const float dl = __builtin_amdgcn_ldexpf(dloss, grad_exponent<P>(above_e, dloss));
-        const float dlx = __builtin_amdgcn_ldexpf(dloss * scale, up_w);
-        const int tl = counts && a.one_target ? (int)(target - a.v0 - n0 - wn) : -1;     // the target's row in the wave's range
+        const float dl = __builtin_amdgcn_ldexpf(dloss, grad_exponent<P>(above_e, dloss)) * fine;
+        const float dlx = __builtin_amdgcn_ldexpf(dloss * scale, up_w) * fine;
+        const int tl = counts && !kTeacher ? (int)(target - a.v0 - n0 - wn) : -1;     // the target's row in the wave's range
 #pragma unroll
         for (int b = 0; b < C::WB; ++b) {
             float p[16];
 #pragma unroll
-            for (int v = 0; v < 16; ++v)
-                p[v] = __uint_as_float(keep & __float_as_uint(__builtin_amdgcn_exp2f(
-                    __builtin_fmaf(se[b][v] * (float)acc[b][tb][v], sx, -lse) * kLog2e)));
+            for (int v = 0; v < 16; ++v) {
+                const float unscaled = se[b][v] * (float)acc[b][tb][v];
+                const float exponent = kTeacher ? fmaf(unscaled, sx2, -lse) : fmaf(unscaled, scale, -lse) * kLog2e;
+                p[v] = __uint_as_float(keep & __float_as_uint(__builtin_amdgcn_exp2f(exponent)));
+            }
             if (wrows < C::BW) {  // rows that do not exist: their exp(0 - lse) has no bound
 #pragma unroll
                 for (int v = 0; v < 16; ++v)
                     if (wn + b * 32 + 8 * (v >> 2) + 4 * g + (v & 3) >= wrows) p[v] = 0.0f;
             }
-            if (__ballot(tl >= b * 32 && tl < b * 32 + 32)) {
+            if (!kTeacher && __ballot(tl >= b * 32 && tl < b * 32 + 32)) {
 #pragma unroll
                 for (int v = 0; v < 16; ++v)
                     if (tl == b * 32 + 8 * (v >> 2) + 4 * g + (v & 3)) p[v] -= 1.0f;
@@ -473,16 +524,21 @@ __global__ __launch_bounds__(C::NT, C::kMinWaves) void grad_tile_kernel(GradArgs
 }
 
 // What the gradient of a distillation needs of each token, a wave a token: d_j = p - q for its entries (all q of the same
-// row together, so that every entry of a row holds the row's value), dloss / T, and whether it counts (0) or not (-1).
-__global__ __launch_bounds__(256) void teacher_gradient_kernel(TeacherArgs t, int64_t M, int64_t V, const float* __restrict__ logp,
-                                                               const float* __restrict__ dloss, float* __restrict__ d,
-                                                               float* __restrict__ dl, int32_t* __restrict__ counts) {
+// row together, so that every entry of a row holds the row's value), dloss / T, whether it counts (0) or not (-1), and lse in base 2:
+// rounded, and 2 to the power of what that leaves out.
+struct TokenParts {
+    float *d, *dl, *lse2, *fine;   // [M][k], [M] each
+    int32_t* counts;
+};
+__global__ __launch_bounds__(256) void teacher_gradient_kernel(LossArgs a, TeacherArgs t, const float* __restrict__ lse,
+                                                               const float* __restrict__ logp, const float* __restrict__ dloss,
+                                                               TokenParts out) {
     __shared__ float qs[4][kMaxTop];
     __shared__ int ids[4][kMaxTop];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int64_t m = (int64_t)blockIdx.x * 4 + wave;
-    if (m >= M) return;
-    const Teacher teacher(t, m, V);
+    if (m >= a.M) return;
+    const Teacher teacher(t, m, a.V);
 #pragma unroll
     for (int i = 0; i < kMaxTop / 64; ++i) {
         qs[wave][i * 64 + lane] = teacher.q[i];
@@ -496,12 +552,37 @@ __global__ __launch_bounds__(256) void teacher_gradient_kernel(TeacherArgs t, in
 #pragma unroll
         for (int i = 0; i < kMaxTop / 64; ++i) q[i] += id == teacher.id[i] ? qj : 0.0f;
     }
+    float nearest = -__builtin_inff();   // the lane's largest logp, and its row
+    int row = -1;
 #pragma unroll
     for (int i = 0; i < kMaxTop / 64; ++i)
-        if (teacher.id[i] >= 0) d[m * t.k + i * 64 + lane] = __builtin_amdgcn_exp2f(logp[m * t.k + i * 64 + lane] * kLog2e) - q[i];
+        if (teacher.id[i] >= 0) {
+            const float lp = logp[m * t.k + i * 64 + lane];
+            out.d[m * t.k + i * 64 + lane] = __builtin_amdgcn_exp2f(lp * kLog2e) - q[i];
+            if (lp > nearest) nearest = lp, row = teacher.id[i];
+        }
+    // lse again from that entry, where its logp is nearer than lse (which, formed of rounded logits, errs by twice its own
+    // rounding and more: rms 0.86e-6 where the rounding alone is 0.30e-6, lse up to 22)
+    const float top = wave_max(nearest);
+    const uint64_t who = __ballot(nearest == top && row >= 0);
+    double l2 = (double)lse[m] / kLn2;
+    if (who && fabsf(top) < 2.0f * fabsf(lse[m])) {
+        row = __builtin_amdgcn_readlane(row, __builtin_ctzll(who));
+        const int8_t *x = a.x_q + m * a.K, *e = a.e + (int64_t)row * a.K;
+        int32_t dot = 0;
+        for (int k = lane * 16; k < a.K; k += 64 * 16) {
+            const v4i xv = *reinterpret_cast<const v4i*>(x + k), ev = *reinterpret_cast<const v4i*>(e + k);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) dot = __builtin_amdgcn_sdot4(xv[j], ev[j], dot, false);
+        }
+        l2 = (double)(a.s_e[row] * (float)wave_sum(dot)) * (double)(a.s_x[m] * t.unit) - (double)top / kLn2;
+    }
     if (lane == 0) {
-        dl[m] = teacher.counts ? dloss[m] * t.inv_t : 0.0f;
-        counts[m] = teacher.counts ? 0 : -1;
+        const float lse2 = (float)l2;
+        out.lse2[m] = lse2;
+        out.fine[m] = fabsf(lse2) < __builtin_inff() ? __builtin_amdgcn_exp2f((float)((double)lse2 - l2)) : 1.0f;
+        out.dl[m] = teacher.counts ? dloss[m] * t.inv_t : 0.0f;
+        out.counts[m] = teacher.counts ? 0 : -1;
     }
 }
 
@@ -640,14 +721,14 @@ Plan make_plan(int64_t M, int64_t V, int64_t K, bool bf16, bool want_dx, bool wa
     return p;
 }
 
-template <int P>
+template <int P, bool kTeacher>
 hipError_t launch_grad_kind(GradArgs a, int kind, hipStream_t stream) {
     return with_tile(kind, [&](auto tile) {
         using C = decltype(tile);
         if constexpr (C::BT >= 64) {
             a.ntt = (int)ceil_div(a.M, C::BT);
             a.ntw = (int)ceil_div(a.V, C::BW);
-            grad_tile_kernel<C, P><<<dim3((unsigned)(a.ntw * a.ntt)), C::NT, 0, stream>>>(a);
+            grad_tile_kernel<C, P, kTeacher><<<dim3((unsigned)(a.ntw * a.ntt)), C::NT, 0, stream>>>(a);
             return hipGetLastError();
         } else {
             return hipErrorInvalidValue;
@@ -655,12 +736,12 @@ hipError_t launch_grad_kind(GradArgs a, int kind, hipStream_t stream) {
     });
 }
 
-template <int P>
+template <int P, bool kTeacher>
 hipError_t launch_grad_tiles(const GradArgs& a, hipStream_t stream) {
     const TileSplit split = grad_tiles(a.M, a.V, a.K);
     GradArgs part = a;
     part.V = split.main;
-    if (hipError_t err = launch_grad_kind<P>(part, split.kind, stream)) return err;
+    if (hipError_t err = launch_grad_kind<P, kTeacher>(part, split.kind, stream)) return err;
     if (split.main == a.V) return hipSuccess;
     part.V = a.V - split.main;
     part.v0 = a.v0 + split.main;
@@ -668,7 +749,7 @@ hipError_t launch_grad_tiles(const GradArgs& a, hipStream_t stream) {
     part.s_e = a.s_e + split.main;
     if (a.gx) part.gx = a.gx + split.main * P;
     if (a.gw) part.gw = a.gw + split.main * a.ldgw;
-    return launch_grad_kind<P>(part, split.tail, stream);
+    return launch_grad_kind<P, kTeacher>(part, split.tail, stream);
 }
 
 hipError_t launch_loss_kind(LossArgs a, int kind, hipStream_t stream) {
@@ -676,7 +757,9 @@ hipError_t launch_loss_kind(LossArgs a, int kind, hipStream_t stream) {
         using C = decltype(tile);
         a.ntw = (int)ceil_div(a.V, C::BW);
         a.ntt = (int)ceil_div(a.M, C::BT);
-        loss_tile_kernel<C><<<dim3((unsigned)((int64_t)a.ntw * a.ntt)), C::NT, 0, stream>>>(a);
+        const dim3 grid((unsigned)((int64_t)a.ntw * a.ntt));
+        if (a.missed) loss_tile_kernel<C, true><<<grid, C::NT, 0, stream>>>(a);
+        else loss_tile_kernel<C, false><<<grid, C::NT, 0, stream>>>(a);
         return hipGetLastError();
     });
 }
@@ -721,6 +804,7 @@ hipError_t launch_loss_tiles(LossArgs& a, hipStream_t stream) {
         rest.e = e + split.main * K;
         rest.s_e = s_e + split.main;
         rest.part = a.part + main_row_tiles(split) * M;
+        if (a.missed) rest.missed = a.missed + main_row_tiles(split) * M;
         if (hipError_t err = launch_loss_kind(rest, split.tail, stream)) return err;
     }
     a.V = V;
@@ -748,7 +832,7 @@ namespace {
 // A teacher's entries and their d, where the targets are distributions.
 struct TeacherGradient {
     const TeacherArgs* args;
-    const float* d;
+    const float *d, *fine;
 };
 
 hipError_t launch_gradients(const int8_t* x_q, const float* s_x, int64_t M, int64_t V, int64_t K, const int8_t* e,
@@ -766,12 +850,12 @@ hipError_t launch_gradients(const int8_t* x_q, const float* s_x, int64_t M, int6
         GradArgs g{x_q, s_x, M, rows, v0, V, (int)K, 0, 0, e + v0 * K, s_e + v0, targets, lse, dloss, maxima,
                    dx ? reinterpret_cast<uint16_t*>(ws + p.gx) : nullptr,
                    de ? reinterpret_cast<uint16_t*>(ws + p.gw) : nullptr, p.piece * P, p.Mp * P};
-        if (teacher.args) {
-            g.inv_t = teacher.args->inv_t;
-            g.one_target = false;
-        }
-        if (hipError_t err = P == 1 ? launch_grad_tiles<1>(g, stream) : launch_grad_tiles<2>(g, stream)) return err;
-        if (teacher.args) {
+        if (!teacher.args) {
+            if (hipError_t err = P == 1 ? launch_grad_tiles<1, false>(g, stream) : launch_grad_tiles<2, false>(g, stream)) return err;
+        } else {
+            g.fine = teacher.fine;
+            g.unit = teacher.args->unit;
+            if (hipError_t err = P == 1 ? launch_grad_tiles<1, true>(g, stream) : launch_grad_tiles<2, true>(g, stream)) return err;
             const dim3 grid((unsigned)ceil_div(M * teacher.args->k, 256));
             if (P == 1) teacher_scatter_kernel<1><<<grid, 256, 0, stream>>>(g, teacher.args->ids, teacher.args->k, teacher.d);
             else teacher_scatter_kernel<2><<<grid, 256, 0, stream>>>(g, teacher.args->ids, teacher.args->k, teacher.d);
@@ -808,17 +892,30 @@ hipError_t launch_cross_entropy_backward(const int8_t* x_q, const float* s_x, in
                                          const int8_t* e, const float* s_e, const int32_t* targets, const float* lse,
                                          const float* dloss, void* dx, void* de, bool bf16, bool accumulate,
                                          void* workspace, hipStream_t stream) {
-    return launch_gradients(x_q, s_x, M, V, K, e, s_e, targets, lse, dloss, dx, de, bf16, accumulate, {nullptr, nullptr},
+    return launch_gradients(x_q, s_x, M, V, K, e, s_e, targets, lse, dloss, dx, de, bf16, accumulate, {nullptr, nullptr, nullptr},
                             workspace, stream);
 }
 
 int64_t distillation_max_top() { return kMaxTop; }
 
+namespace {
+
+TeacherArgs teacher_args(const int32_t* ids, const float* top, int64_t k, float temperature) {
+    return {ids, top, (int)k, 1.0f / temperature, (float)(1.0 / kLn2 / (double)temperature)};
+}
+
+}  // namespace
+
+size_t distillation_workspace_bytes(int64_t M, int64_t V, int64_t K) {
+    return cross_entropy_workspace_bytes(M, V, K) / sizeof(float2) * (sizeof(float2) + sizeof(float));
+}
+
 hipError_t launch_distillation(const int8_t* x_q, const float* s_x, int64_t M, int64_t V, int64_t K, const int8_t* e,
                                const float* s_e, const int32_t* ids, const float* top, int64_t k, float temperature,
                                float* loss, float* lse, float* logp, void* workspace, hipStream_t stream) {
-    const TeacherArgs t{ids, top, (int)k, 1.0f / temperature};
-    LossArgs a{x_q, s_x, M, V, (int)K, 0, 0, e, s_e, static_cast<float2*>(workspace), kLog2e * t.inv_t};
+    const TeacherArgs t = teacher_args(ids, top, k, temperature);
+    float2* const part = static_cast<float2*>(workspace);
+    LossArgs a{x_q, s_x, M, V, (int)K, 0, 0, e, s_e, part, t.unit, reinterpret_cast<float*>(part + most_pairs(M, V))};
     if (hipError_t err = launch_loss_tiles(a, stream)) return err;
     teacher_logits_kernel<<<dim3((unsigned)ceil_div(M * ceil_div(k, kDots), 4)), 256, 0, stream>>>(a, t, logp);
     if (hipError_t err = hipGetLastError()) return err;
@@ -828,14 +925,16 @@ hipError_t launch_distillation(const int8_t* x_q, const float* s_x, int64_t M, i
 
 namespace {
 
-// The entries' d, dloss / T and the marks of the tokens that count, in front of the cross entropy's workspace.
+// The entries' d and what the tokens have, in front of the cross entropy's workspace.
 struct TeacherParts {
-    size_t d, dl, counts, rest;
+    size_t d, dl, lse2, fine, counts, rest;
     TeacherParts(int64_t M, int64_t k) {
         auto up = [](int64_t n) { return (size_t)((n * 4 + 255) / 256 * 256); };
         d = 0;
         dl = up(M * k);
-        counts = dl + up(M);
+        lse2 = dl + up(M);
+        fine = lse2 + up(M);
+        counts = fine + up(M);
         rest = counts + up(M);
     }
 };
@@ -853,13 +952,14 @@ hipError_t launch_distillation_backward(const int8_t* x_q, const float* s_x, int
                                         hipStream_t stream) {
     const TeacherParts parts(M, k);
     uint8_t* const ws = static_cast<uint8_t*>(workspace);
-    float* const d = reinterpret_cast<float*>(ws + parts.d);
-    float* const dl = reinterpret_cast<float*>(ws + parts.dl);
-    int32_t* const counts = reinterpret_cast<int32_t*>(ws + parts.counts);
-    const TeacherArgs t{ids, top, (int)k, 1.0f / temperature};
-    teacher_gradient_kernel<<<dim3((unsigned)ceil_div(M, 4)), 256, 0, stream>>>(t, M, V, logp, dloss, d, dl, counts);
+    auto floats = [&](size_t at) { return reinterpret_cast<float*>(ws + at); };
+    const TokenParts out{floats(parts.d), floats(parts.dl), floats(parts.lse2), floats(parts.fine), reinterpret_cast<int32_t*>(ws + parts.counts)};
+    const TeacherArgs t = teacher_args(ids, top, k, temperature);
+    const LossArgs a{x_q, s_x, M, V, (int)K, 0, 0, e, s_e, nullptr};
+    teacher_gradient_kernel<<<dim3((unsigned)ceil_div(M, 4)), 256, 0, stream>>>(a, t, lse, logp, dloss, out);
     if (hipError_t err = hipGetLastError()) return err;
-    return launch_gradients(x_q, s_x, M, V, K, e, s_e, counts, lse, dl, dx, de, bf16, accumulate, {&t, d}, ws + parts.rest, stream);
+    return launch_gradients(x_q, s_x, M, V, K, e, s_e, out.counts, out.lse2, out.dl, dx, de, bf16, accumulate, {&t, out.d, out.fine},
+                            ws + parts.rest, stream);
 }
 
 }  // namespace dfssm

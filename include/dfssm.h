@@ -539,9 +539,9 @@ dfssm_status dfssm_cross_entropy_backward(const int8_t* x_q, const float* s_x, i
  *             +infinity among a token's entries makes its loss NaN, and in the backward call its row of dx and the rows of
  *             de that its entries name; nothing else.
  *   loss, lse fp32 [M], logp fp32 [M][top] (written)
- *   temperature  T, from 2^-60 up to 2^60.  z / T and lse are fp32: their difference, p's logarithm, errs by up to about
- *             2^-20 of their size, which the loss has as its own error and p, in the gradients, as a relative one (T so small
- *             that z / T passes 2^16 leaves p few bits or none)
+ *   temperature  T, from 2^-60 up to 2^60.  z / T is formed in fp32: p of a row errs by up to about 2^-23 |z / T| of itself,
+ *             the loss by as much itself (T so small that z / T passes 2^20 leaves p no bits); lse by up to 2^-21 of the largest
+ *             |z / T|, logp of a row by its own rounding and its logit's
  *   workspace  at least dfssm_distillation_workspace_bytes(M, V, K, top) bytes, under dfssm_cross_entropy's rules
  * Errors: as dfssm_cross_entropy; DFSSM_ERR_INVALID_ARG for top <= 0 or a temperature out of range, DFSSM_ERR_UNSUPPORTED for
  * top > 256 or M * top > 2^28.
@@ -555,7 +555,8 @@ dfssm_status dfssm_distillation(const int8_t* x_q, const float* s_x, int64_t M, 
 /*
  * Gradients of dfssm_distillation for the dequantized values, as dfssm_cross_entropy_backward has them, with
  *   d[m][v] = dloss[m] / T (p[v] - sum of the q_j with top_ids[m][j] == v);  0 for tokens that do not count
- *   lse [M] and logp [M][top] from the forward call, dloss fp32 [M] (read)
+ *   lse [M] and logp [M][top] from the forward call with the same operands, dloss fp32 [M] (read).  The entry whose logp is nearest 0
+ *             gives a token's lse to more than lse's 32 bits: what the token's p add up to errs by 2^-24 of that logp or less
  *   dx, de, grad_type, accumulate_de, the precision of d and the workspace's rules: as there
  * Errors: as the forward call's and dfssm_cross_entropy_backward's.
  */

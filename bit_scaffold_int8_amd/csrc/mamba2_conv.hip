@@ -23,7 +23,7 @@ namespace dfssm {
 namespace {
 
 constexpr int kWaves = 4;       // runs a workgroup walks, one a wave
-// Rows of a run: 2048 x 4352 fp32 15.8 us, 18.2 with 16 (fewer waves), 24 with 32 (before sigmoid() below: 14.4 now, 4.95 TB/s of
+// Rows of a run: 2048 x 4352 fp32 15.8 us, 18.2 with 16 (fewer waves), 24 with 32 (before sigmoid() below: 14.6 now, 4.9 TB/s of
 // the 71 MB it cannot do without, which is what bounds it).  Backward a run costs six rows more: 32.
 constexpr int kRun = 8, kGradRun = 32;
 

@@ -18,15 +18,15 @@
 //  * One sequence has too few heads to fill the GPU, so it is cut into segments of several chunks: a first sweep
 //    finds what each segment adds to the state, a small kernel joins them in order, the second sweep starts from the joined ones.
 //
-// Measured, 64 heads of 64 channels, d_state 128, in us (prepare, first sweep, join, second sweep):
-//   2048 tokens fp32   9.3, 22, 11.4, 42;   16384 tokens bf16   19, 65, 12, 146
-//   five packed sequences of 0 to 2500 tokens, 4101 in all, bf16   8.7 (and 4.9 for the tables), 25, 13, 53
+// Measured, 64 heads of 64 channels, d_state 128, in us, means of 12 launches (prepare, first sweep, join, second sweep):
+//   2048 tokens fp32   9.2, 22, 11.5, 42;   16384 tokens bf16   19, 68, 12, 155 (at best 138)
+//   five packed sequences of 0 to 2500 tokens, 4101 in all, bf16   8.7 (and 5.1 for the tables), 25, 13, 53
 // The sweeps are bound by the issue of their instructions.  For y of bf16 data a wave issues 184 matrix instructions a chunk (16
-// cycles of a SIMD each) and about 1030 vector ones (to split the state and the chunk's weights into pieces, above all), and
-// with two waves to a SIMD the two kinds hardly overlap; fp32 data take 3 pieces and twice the matrix instructions, and
-// there the segments' states, 64 KB a head and segment written and read, cost as much as the chunks.  The sweeps that store the
-// states of every chunk are bound by that: 8 x 2048 tokens bf16 146 us at best, 4.6 TB/s.
-// (At 16384 tokens the whole is 285 MB and 215 us: a quarter of the memory's rate.)
+// cycles of a SIMD each) and 1040 vector ones (to split the state and the chunk's weights into pieces, above all): 34 and 48 % of
+// the SIMDs' busy cycles (counters), and with two waves to a SIMD the two kinds hardly overlap.  fp32 data take 3 pieces, 456 and 1500
+// instructions (38 and 31 %), and there the segments' states, 64 KB a head and segment written and read, cost as much as the
+// chunks.  The sweeps that store the states of every chunk are bound by that: 8 x 2048 tokens bf16 160 us, 4.2 TB/s (145 at best).
+// (At 16384 tokens the whole is 285 MB and 225 us: a quarter of the memory's rate.)
 #include <math.h>
 
 #include "scan.h"
@@ -643,7 +643,10 @@ hipError_t launch_sweep(const SweepArgs& s, const ScanPlan& plan, bool bf16, int
 
 // ---------------------------------------------------------------- the host's side
 
-// Whether the sequences go token by token: by their average length and, in units of 64, the number of heads of all of them.
+// Whether the sequences go token by token: by their average length and, in units of 64, the number of heads of all of them.  (Lengths
+// that offsets give lie in device memory.  Where one is far above the average it costs what its form costs it, 64 heads, bf16:
+// among 63 single tokens a prompt of 500, token by token, 240 us, where the two alone take 44 and 46; among 255 one of 1800
+// 947, alone 196 and 62.)
 // Measured in us, d_state 128 (token by token 2, 8, 16, 32, 64 tokens | chunks up to 64 tokens):
 //   1 x 64 heads, fp32  4.2, 5.6, 7.7, 11.7, 20.0 | 27;   bf16  4.2, 5.5, 7.4, 11.3, 19.1 | 21
 //   8 x 64 heads, fp32  10, 17, 26, 45, 79 | 31;   bf16  10, 14, 21, 35, 60 | 25
@@ -654,8 +657,10 @@ bool scan_recurrent(const Sequences& seq, int H) {
 }
 
 // Enough workgroups for one on each CU: what one segment a sequence does not give, more segments do, at the price of a
-// second sweep without outputs.  Where workgroups of two heads fill three quarters of the CUs without it, they are taken instead
-// (8 x 2048 tokens, bf16: states 159 us a sweep, 221 by segments and four heads; one sequence of 16384 tokens, cut into segments
+// second sweep without outputs.  It goes by the number of sequences, as if all were of one length: a long one among many that would fill
+// the CUs is not cut, and its chunks go one after another (64 heads, bf16: 16384 tokens in one sequence 289 us in a row of calls,
+// 16000 and five of 64 1.18 ms, with 15 or 31 of 64 1.7 ms; with gradients 1.30, 3.8 and 5.7 ms).  Where workgroups of two heads fill three quarters of the CUs without it, they are taken instead
+// (8 x 2048 tokens, bf16: states 160 us a sweep, 221 by segments and four heads; one sequence of 16384 tokens, cut into segments
 // anyway: 285 us, 221 with four heads; 2048 fp32 78 and 75).
 constexpr int kSweepGroups = 256;
 constexpr int64_t kMaxSegmentHeads = 8 * kSweepGroups;   // the most heads that have segments' states: 67 MB at d_state 128

@@ -18,11 +18,11 @@
 // and of the products M L dt B only the sum over the heads of M L dt is formed, and multiplied once.  The shares of several
 // workgroups are joined in order.
 //
-// Measured, 64 heads of 64 channels, d_state 128, in us (prepare, sweep forwards, sweep backwards, gradients, joins):
-//   2048 tokens fp32   11, 69, 66 (each with its segments), 111, 10;   8 x 2048 tokens bf16   21, 160, 160, 637, 5
+// Measured, 64 heads of 64 channels, d_state 128, in us, means of 12 launches (prepare, sweep forwards, sweep backwards, gradients, joins):
+//   2048 tokens fp32   11, 72, 72 (each with its segments), 111 (at best 109), 10.5;   8 x 2048 tokens bf16   22, 161, 161, 641 (598), 5
 // The gradient kernel has one workgroup a CU (its registers are full: two waves to a SIMD), and a head of a chunk takes it
-// 22 thousand cycles, of which the issue of its vector and matrix instructions is 12: the rest is waiting at its two
-// barriers, for the states (64 KB a head and chunk; from the cache it would take 5 % less) and for LDS.
+// 20 thousand cycles, of which the issue of its vector and matrix instructions (bf16 1120 and 81 a wave) is 11.5: the rest is waiting at
+// its two barriers, for the states (64 KB a head and chunk; from the cache it would take 5 % less) and for LDS.
 #include <math.h>
 
 #include "scan.h"

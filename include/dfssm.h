@@ -540,7 +540,7 @@ dfssm_status dfssm_cross_entropy_backward(const int8_t* x_q, const float* s_x, i
  *             de that its entries name; nothing else.
  *   loss, lse fp32 [M], logp fp32 [M][top] (written)
  *   temperature  T, from 2^-60 up to 2^60.  z / T is formed in fp32: p of a row errs by up to about 2^-23 |z / T| of itself,
- *             the loss by as much itself (T so small that z / T passes 2^20 leaves p no bits); lse by up to 2^-21 of the largest
+ *             the loss by as much itself (where T is so small that z / T passes 2^20 gradients are unspecified); lse by up to 2^-21 of the largest
  *             |z / T|, logp of a row by its own rounding and its logit's
  *   workspace  at least dfssm_distillation_workspace_bytes(M, V, K, top) bytes, under dfssm_cross_entropy's rules
  * Errors: as dfssm_cross_entropy; DFSSM_ERR_INVALID_ARG for top <= 0 or a temperature out of range, DFSSM_ERR_UNSUPPORTED for
